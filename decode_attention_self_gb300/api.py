@@ -24,7 +24,7 @@ DR_OK, DR_ERR_INVALID_ARG, DR_ERR_UNSUPPORTED, DR_ERR_CUDA = 0, 1, 2, 3
 DR_KV_CONTIGUOUS, DR_KV_PAGED = 0, 1
 DR_BF16, DR_F32 = 0, 1
 DR_KV_BF16, DR_KV_FP8_E4M3 = 0, 1
-DR_ERRF_SEQ_LEN, DR_ERRF_BLOCK_ID, DR_ERRF_POS, DR_ERRF_TOKEN, DR_ERRF_TIMEOUT = 1, 2, 4, 8, 16
+DR_ERRF_SEQ_LEN, DR_ERRF_BLOCK_ID, DR_ERRF_POS, DR_ERRF_TOKEN, DR_ERRF_TIMEOUT, DR_ERRF_ROW_START = 1, 2, 4, 8, 16, 32
 DR_SAMPLE_ADVANCE = 1
 
 if not os.path.exists(LIB_PATH):
@@ -39,7 +39,13 @@ class dr_kv_cache(ctypes.Structure):
                 ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
 
 
+class dr_score_opts(ctypes.Structure):
+    _fields_ = [("causal", ctypes.c_int32), ("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p),
+                ("prefix_len", ctypes.c_void_p), ("first_key", ctypes.c_void_p)]
+
+
 _vp, _i, _f = ctypes.c_void_p, ctypes.c_int, ctypes.c_float
+_i64, _sz = ctypes.c_int64, ctypes.c_size_t
 _lib.dr_kv_append.argtypes = [ctypes.POINTER(dr_kv_cache), _vp, _vp, _vp, _i, _i, _i, _vp, _vp]
 _lib.dr_decode_self_attn.argtypes = [_vp, ctypes.POINTER(dr_kv_cache), _vp, _i, _i, _i, _i, _f, _vp, _i, _vp, _vp]
 _lib.dr_decode_cross_attn.argtypes = [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _f, _vp, _i, _vp, _vp]
@@ -51,13 +57,20 @@ _lib.dr_lm_head.argtypes = [_vp, _vp, _i, _i, _i, _i, _i, _vp, _vp, _vp]
 _lib.dr_lm_head_stall_test.argtypes = [_vp, _vp, _i, _i, _i, _i, _i, _vp, _vp, _i, _vp]
 _lib.dr_decode_self_attn_stall_test.argtypes = [_vp, ctypes.POINTER(dr_kv_cache), _vp, _i, _i, _i, _i, _f, _vp, _i, _vp,
                                                 _i, _vp]
+_lib.dr_rope_table.argtypes = [_vp, _i, _i, ctypes.c_double, _vp]
+_lib.dr_rope_append.argtypes = [ctypes.POINTER(dr_kv_cache), _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp,
+                                _vp, _i, _i, _i, _i, _i, _i, _i, _i, _vp, _vp]
+_lib.dr_prompt_attn.argtypes = [_vp, _i64, ctypes.POINTER(dr_kv_cache), _vp, _vp, ctypes.POINTER(dr_score_opts), _i, _i,
+                                _i, _i, _i, _i, _f, _vp, _i, _vp, _sz, _vp, _vp]
+_lib.dr_prompt_attn_workspace.argtypes = [_i, _i, _i, _i, _i, _i]
+_lib.dr_prompt_attn_workspace.restype = _sz
 _lib.dr_plan_splits.argtypes = [_i, _i, _i, _i, _i]
 _lib.dr_plan_splits.restype = _i
 _lib.dr_status_string.argtypes = [_i]
 _lib.dr_status_string.restype = ctypes.c_char_p
 for _fn in ("dr_kv_append", "dr_decode_self_attn", "dr_decode_cross_attn", "dr_decode_layer",
             "dr_sample_topk_delayed", "dr_embed_tokens", "dr_lm_head", "dr_lm_head_stall_test",
-            "dr_decode_self_attn_stall_test"):
+            "dr_decode_self_attn_stall_test", "dr_rope_table", "dr_rope_append", "dr_prompt_attn"):
     getattr(_lib, _fn).restype = _i
 
 
@@ -271,6 +284,133 @@ def dr_lm_head_stall_test(hidden: torch.Tensor, W: torch.Tensor, C: int, logits:
                                       ldv, _ptr(logits, torch.float32, "logits"),
                                       _ptr(err_flag, torch.int32, "err_flag"), int(stall_slab), _stream(stream)))
     return logits
+
+
+def _token_rows(t: torch.Tensor | None, dtype: torch.dtype, name: str):
+    """(pointer, elements between tokens) of a [T, heads, D] tensor whose tokens are dense but may lie apart."""
+    if t is None:
+        return None, 0
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError(f"{name} must be [T, heads, D] with contiguous heads")
+    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2])
+
+
+def _same_device(**tensors):
+    """Every given tensor lies on the current device, whose stream the call is enqueued on."""
+    dev = torch.cuda.current_device()
+    for name, t in tensors.items():
+        if t is not None and (not t.is_cuda or t.device.index != dev):
+            raise ValueError(f"{name} must be on the current CUDA device {dev}, is on {t.device}")
+
+
+def _sized(t: torch.Tensor | None, shape: tuple, name: str):
+    if t is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, has {tuple(t.shape)}")
+
+
+def _cache_rows(cache: KVCache, B: int, Hkv: int, D: int, name: str = "cache"):
+    """The cache's tensors agree with B rows of Hkv heads."""
+    if cache.k.dim() != 4 or cache.v.shape != cache.k.shape or cache.k.shape[1] != Hkv or cache.k.shape[3] != D:
+        raise ValueError(f"{name}.k and {name}.v must be [.., {Hkv}, .., {D}]")
+    rows = cache.block_table.shape[0] if cache.paged else cache.k.shape[0]
+    if rows < B:
+        raise ValueError(f"{name} holds {rows} rows, the call has {B}")
+
+
+def dr_rope_table(table: torch.Tensor, base: float = 10000.0, stream=None) -> torch.Tensor:
+    """Fill table [max_pos, rot_dim] float32 with cos (first half) and sin of p * base^(-2i / rot_dim)."""
+    _same_device(table=table)
+    _check("dr_rope_table", _lib.dr_rope_table(_ptr(table, torch.float32, "table"), table.shape[0], table.shape[1],
+                                               float(base), _stream(stream)))
+    return table
+
+
+def dr_rope_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, row_start: torch.Tensor, start_pos: torch.Tensor,
+                   q: torch.Tensor | None = None, q_out: torch.Tensor | None = None,
+                   table: torch.Tensor | None = None, interleaved: bool = False,
+                   pos_offset: torch.Tensor | None = None, err_flag: torch.Tensor | None = None, stream=None) -> None:
+    """Rotate q [T,Hq,D] (into q_out) and k [T,Hkv,D] by position and append k, v of ragged tokens to the cache.
+
+    Row b's tokens row_start[b] .. row_start[b+1]-1 go to slots start_pos[b], start_pos[b]+1, ...; q, k, v and q_out
+    may be slices of a fused projection (dense heads, any token stride that is a multiple of 8).
+    """
+    T, Hkv, D = k.shape
+    B = start_pos.shape[0]
+    Hq = Hkv if q is None else q.shape[1]
+    _same_device(cache_k=cache.k, cache_v=cache.v, block_table=cache.block_table, k=k, v=v, row_start=row_start,
+                 start_pos=start_pos, q=q, q_out=q_out, table=table, pos_offset=pos_offset, err_flag=err_flag)
+    _cache_rows(cache, B, Hkv, D)
+    _sized(v, (T, Hkv, D), "v")
+    _sized(q, (T, Hq, D), "q")
+    _sized(q_out, (T, Hq, D), "q_out")
+    _sized(row_start, (B + 1,), "row_start")
+    _sized(pos_offset, (B,), "pos_offset")
+    qp, qs = _token_rows(q, torch.bfloat16, "q")
+    kp, ks = _token_rows(k, torch.bfloat16, "k")
+    vp, vs = _token_rows(v, torch.bfloat16, "v")
+    op, os_ = _token_rows(q_out, torch.bfloat16, "q_out")
+    c = cache.as_c()
+    _check("dr_rope_append",
+           _lib.dr_rope_append(ctypes.byref(c), qp, qs, kp, ks, vp, vs, op, os_,
+                               _ptr(row_start, torch.int32, "row_start"), _ptr(start_pos, torch.int32, "start_pos"),
+                               _ptr(pos_offset, torch.int32, "pos_offset"), _ptr(table, torch.float32, "table"),
+                               0 if table is None else table.shape[0], 0 if table is None else table.shape[1],
+                               int(bool(interleaved)), T, B, Hq, Hkv, D, _ptr(err_flag, torch.int32, "err_flag"),
+                               _stream(stream)))
+
+
+def _score_opts(causal: bool, softcap: float, slopes, prefix_len, first_key) -> dr_score_opts:
+    return dr_score_opts(int(bool(causal)), float(softcap), _ptr(slopes, torch.float32, "slopes"),
+                         _ptr(prefix_len, torch.int32, "prefix_len"), _ptr(first_key, torch.int32, "first_key"))
+
+
+def _sms() -> int:
+    return torch.cuda.get_device_properties(torch.cuda.current_device()).multi_processor_count
+
+
+def _out_dtype(out: torch.Tensor) -> int:
+    if out.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"out must be torch.bfloat16 or torch.float32, got {out.dtype}")
+    return DR_F32 if out.dtype == torch.float32 else DR_BF16
+
+
+def dr_prompt_attn_workspace(T: int, B: int, Hq: int, Hkv: int, max_len: int, num_sms: int | None = None) -> int:
+    """Bytes of workspace dr_prompt_attn wants (0: none), for the current device unless num_sms is given."""
+    return int(_lib.dr_prompt_attn_workspace(T, B, Hq, Hkv, max_len, _sms() if num_sms is None else num_sms))
+
+
+def dr_prompt_attn(q: torch.Tensor, cache: KVCache, row_start: torch.Tensor, kv_len: torch.Tensor, out: torch.Tensor,
+                   causal: bool = True, softcap: float = 0.0, slopes: torch.Tensor | None = None,
+                   prefix_len: torch.Tensor | None = None, first_key: torch.Tensor | None = None,
+                   max_len_hint: int = 0, scale: float = 0.0, workspace: torch.Tensor | None = None,
+                   err_flag: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Attention of ragged tokens q [T,Hq,D]: row b's tokens are the last of its kv_len[b] keys in the cache."""
+    T, Hq, D = q.shape
+    B, Hkv = kv_len.shape[0], cache.k.shape[1]
+    _same_device(q=q, cache_k=cache.k, cache_v=cache.v, block_table=cache.block_table, row_start=row_start,
+                 kv_len=kv_len, out=out, slopes=slopes, prefix_len=prefix_len, first_key=first_key,
+                 workspace=workspace, err_flag=err_flag)
+    _cache_rows(cache, B, Hkv, D)
+    _sized(out, (T, Hq, D), "out")
+    _sized(row_start, (B + 1,), "row_start")
+    _sized(slopes, (Hq,), "slopes")
+    _sized(prefix_len, (B,), "prefix_len")
+    _sized(first_key, (T,), "first_key")
+    qp, qs = _token_rows(q, torch.bfloat16, "q")
+    c = cache.as_c()
+    o = _score_opts(causal, softcap, slopes, prefix_len, first_key)
+    _check("dr_prompt_attn",
+           _lib.dr_prompt_attn(qp, qs, ctypes.byref(c), _ptr(row_start, torch.int32, "row_start"),
+                               _ptr(kv_len, torch.int32, "kv_len"), ctypes.byref(o), T, B, Hq, Hkv, D,
+                               int(max_len_hint), float(scale), _ptr(out, None, "out"), _out_dtype(out),
+                               _ptr(workspace, torch.uint8, "workspace"),
+                               0 if workspace is None else workspace.numel(), _ptr(err_flag, torch.int32, "err_flag"),
+                               _stream(stream)))
+    return out
 
 
 def loaded_library_path() -> str:

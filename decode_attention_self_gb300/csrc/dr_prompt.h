@@ -1,0 +1,61 @@
+// Internal declarations of the prompt-side operators (rotated append, prompt attention, shared-prefix attention).
+// Launch helpers take validated arguments; dr_prompt_api.cu owns all argument checking.
+#pragma once
+
+#include "dr_internal.h"
+
+namespace dr {
+
+struct RopeAppendParams {
+    void *k_cache, *v_cache;            // bf16 or e4m3 cache
+    const int32_t *block_table;         // paged only
+    int32_t cap, max_blocks, num_blocks, kv_fp8;
+    float k_scale, v_scale;
+    const uint16_t *q, *k, *v;          // [T][heads][64] bf16, tokens *_stride elements apart; q may be null
+    uint16_t *q_out;
+    int64_t q_stride, k_stride, v_stride, q_out_stride;
+    const int32_t *row_start;           // [B+1]
+    const int32_t *start_pos;           // [B]
+    const int32_t *pos_offset;          // [B] or null
+    const float *rope;                  // [rope_len][rot] cos then sin, or null
+    int32_t rope_len, rot, interleaved;
+    int32_t T, B, Hq, Hkv;
+    int32_t *err;
+};
+
+cudaError_t launch_rope_append(const RopeAppendParams &p, bool paged, cudaStream_t stream);
+cudaError_t launch_rope_table(float *table, int max_pos, int rot, double base, cudaStream_t stream);
+
+// One attention call over a cache of Hkv heads by queries of Hq = g * Hkv heads.
+struct PromptParams {
+    const uint16_t *q;                  // [T][Hq][64] bf16, tokens q_stride elements apart
+    int64_t q_stride;
+    const void *k, *v;                  // cache, as dr_kv_cache
+    const int32_t *table;
+    int32_t cap, max_blocks, num_blocks;
+    float sscale;                       // scores in log2 units: raw * sscale (scale * log2 e * k_scale)
+    float out_scale;                    // v_scale of an e4m3 cache, else 1
+    float cap_c1, cap_c2;               // score cap: c1 - 2 c1 / (2^(raw c2) + 1); c1 = 0: no cap
+    const float *slopes;                // [Hq] or null: s -= slope * |pos - key|
+    const int32_t *row_start;           // [B+1]; null: one query per row, token b = row b
+    const int32_t *kv_len;              // [B]; null: no keys (a row's state is its prefix part alone)
+    const int32_t *prefix_len;          // [B] or null: keys every query of a row sees, causal or not
+    const int32_t *first_key;           // [T] or null: keys before it are hidden from query t
+    int32_t causal;
+    int32_t T, B, Hq, Hkv, g;
+    void *out;                          // [T][Hq][64]
+    int32_t out_f32;
+    int32_t *err;
+    // token kernel: items per row, and the most tokens a row may have to be taken by it (more: the tile kernel's)
+    int32_t tokens_per_row, few_max;
+    // softmax states of key ranges attended before: [nparts][rows = T*Hq] (m, l) and [nparts][rows][64]; null: none
+    float2 *part_ml;
+    float *part_acc;
+    int32_t nparts;
+};
+
+// Query rows one token at a time (memory bound: single tokens of a batch).
+cudaError_t launch_attn_tokens(const PromptParams &p, bool paged, bool fp8, int splits, cudaStream_t stream);
+int plan_token_splits(long long items, int Hkv, int g, int max_len, bool fp8, int sms);
+
+}  // namespace dr

@@ -1,0 +1,195 @@
+// extern "C" boundary of the prompt-side operators: argument checks, plans and launches.  As in dr_api.cu, nothing
+// here allocates device memory or synchronises with the host.
+#include <math.h>
+
+#include "dr_prompt.h"
+
+namespace {
+
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Validates a cache description; on success stores the keys a row can hold in *cap.
+dr_status check_cache(const dr_kv_cache *c, int *cap) {
+    if (!c || !c->k || !c->v || !aligned16(c->k) || !aligned16(c->v)) return DR_ERR_INVALID_ARG;
+    if (c->kv_dtype != DR_KV_BF16 && c->kv_dtype != DR_KV_FP8_E4M3) return DR_ERR_INVALID_ARG;
+    if (c->kv_dtype == DR_KV_FP8_E4M3 &&
+        (!(c->k_scale > 0.f) || !(c->v_scale > 0.f) || isinf(c->k_scale) || isinf(c->v_scale)))
+        return DR_ERR_INVALID_ARG;
+    if (c->layout == DR_KV_CONTIGUOUS) {
+        if (c->max_len < 1) return DR_ERR_INVALID_ARG;
+        *cap = c->max_len;
+        return DR_OK;
+    }
+    if (c->layout != DR_KV_PAGED) return DR_ERR_INVALID_ARG;
+    if (!c->block_table || c->num_blocks < 1 || c->max_blocks_per_seq < 1) return DR_ERR_INVALID_ARG;
+    if (c->block_size != dr::kBlockKeys) return DR_ERR_UNSUPPORTED;
+    if ((long long)c->max_blocks_per_seq * c->block_size > 0x7FFFFFFFLL) return DR_ERR_INVALID_ARG;
+    *cap = c->max_blocks_per_seq * c->block_size;
+    return DR_OK;
+}
+
+// Ragged tokens T in B rows, Hq query heads on Hkv key/value heads.
+dr_status check_sizes(int T, int B, int Hq, int Hkv, int D) {
+    if (T < 1 || B < 1 || B > 65535 || Hq < 1 || Hkv < 1 || Hq > 4096 || Hq % Hkv != 0) return DR_ERR_INVALID_ARG;
+    if ((long long)T * Hq > 0x7FFFFFFFLL) return DR_ERR_INVALID_ARG;
+    if (D != dr::kHeadDim || Hq / Hkv > 128) return DR_ERR_UNSUPPORTED;
+    return DR_OK;
+}
+
+// A token stride in elements: whole tokens, 16-byte steps.
+bool bad_stride(int64_t stride, int heads) { return stride < (int64_t)heads * dr::kHeadDim || stride % 8 != 0; }
+
+dr_status from_cuda(cudaError_t e) { return e == cudaSuccess ? DR_OK : DR_ERR_CUDA; }
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+void fill_cache(dr::PromptParams &p, const dr_kv_cache *c, int cap) {
+    const bool paged = c->layout == DR_KV_PAGED, fp8 = c->kv_dtype == DR_KV_FP8_E4M3;
+    p.k = c->k;
+    p.v = c->v;
+    p.table = paged ? c->block_table : nullptr;
+    p.cap = cap;
+    p.max_blocks = paged ? c->max_blocks_per_seq : 0;
+    p.num_blocks = paged ? c->num_blocks : 0;
+    p.out_scale = fp8 ? c->v_scale : 1.f;
+}
+
+void fill_scores(dr::PromptParams &p, const dr_kv_cache *c, float scale, const dr_score_opts *o) {
+    const float s = (scale > 0.f ? scale : 1.0f / sqrtf((float)dr::kHeadDim)) *
+                    (c && c->kv_dtype == DR_KV_FP8_E4M3 ? c->k_scale : 1.f);
+    p.sscale = s * kLog2e;
+    p.slopes = o ? o->slopes : nullptr;
+    p.cap_c1 = o ? o->softcap * kLog2e : 0.f;
+    p.cap_c2 = o && o->softcap > 0.f ? 2.0f * kLog2e * s / o->softcap : 0.f;
+}
+
+// A cap so small that 2 log2(e) scale / cap overflows is refused with the other bad numbers.
+dr_status check_scores(float scale, const dr_score_opts *o) {
+    if (!(scale == scale) || isinf(scale)) return DR_ERR_INVALID_ARG;
+    if (!o) return DR_OK;
+    if (!(o->softcap >= 0.f) || o->softcap > 1e30f || (o->softcap > 0.f && o->softcap < 1e-6f)) return DR_ERR_INVALID_ARG;
+    if (o->causal != 0 && o->causal != 1) return DR_ERR_INVALID_ARG;
+    return DR_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+dr_status dr_rope_table(float *table, int max_pos, int rot_dim, double base, void *stream) {
+    if (!table || !aligned16(table) || max_pos < 1 || !(base > 0.0) || isinf(base)) return DR_ERR_INVALID_ARG;
+    if (rot_dim < 16 || rot_dim > dr::kHeadDim || rot_dim % 16 != 0) return DR_ERR_UNSUPPORTED;
+    return from_cuda(dr::launch_rope_table(table, max_pos, rot_dim, base, static_cast<cudaStream_t>(stream)));
+}
+
+dr_status dr_rope_append(const dr_kv_cache *cache, const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                         const void *v, int64_t v_stride, void *q_out, int64_t q_out_stride, const int32_t *row_start,
+                         const int32_t *start_pos, const int32_t *pos_offset, const float *rope_table, int rope_len,
+                         int rot_dim, int interleaved, int T, int B, int Hq, int Hkv, int D, int32_t *err_flag,
+                         void *stream) {
+    dr_status st = check_sizes(T, B, Hq, Hkv, D);
+    if (st != DR_OK) return st;
+    int cap = 0;
+    st = check_cache(cache, &cap);
+    if (st != DR_OK) return st;
+    if (!k || !v || !row_start || !start_pos || !aligned16(k) || !aligned16(v)) return DR_ERR_INVALID_ARG;
+    if (bad_stride(k_stride, Hkv) || bad_stride(v_stride, Hkv)) return DR_ERR_INVALID_ARG;
+    if ((q == nullptr) != (q_out == nullptr)) return DR_ERR_INVALID_ARG;
+    if (q && (!aligned16(q) || !aligned16(q_out) || bad_stride(q_stride, Hq) || bad_stride(q_out_stride, Hq)))
+        return DR_ERR_INVALID_ARG;
+    if (interleaved != 0 && interleaved != 1) return DR_ERR_INVALID_ARG;
+    if (rope_table) {
+        if (!aligned16(rope_table) || rope_len < 1) return DR_ERR_INVALID_ARG;
+        if (rot_dim < 16 || rot_dim > D || rot_dim % 16 != 0) return DR_ERR_UNSUPPORTED;
+    }
+    dr::RopeAppendParams p = {};
+    p.k_cache = cache->k;
+    p.v_cache = cache->v;
+    p.block_table = cache->block_table;
+    p.cap = cap;
+    p.max_blocks = cache->max_blocks_per_seq;
+    p.num_blocks = cache->num_blocks;
+    p.kv_fp8 = cache->kv_dtype == DR_KV_FP8_E4M3;
+    p.k_scale = cache->k_scale;
+    p.v_scale = cache->v_scale;
+    p.q = static_cast<const uint16_t *>(q);
+    p.k = static_cast<const uint16_t *>(k);
+    p.v = static_cast<const uint16_t *>(v);
+    p.q_out = static_cast<uint16_t *>(q_out);
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.q_out_stride = q_out_stride;
+    p.row_start = row_start;
+    p.start_pos = start_pos;
+    p.pos_offset = pos_offset;
+    p.rope = rope_table;
+    p.rope_len = rope_len;
+    p.rot = rope_table ? rot_dim : 0;
+    p.interleaved = interleaved;
+    p.T = T;
+    p.B = B;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.err = err_flag;
+    return from_cuda(
+        dr::launch_rope_append(p, cache->layout == DR_KV_PAGED, static_cast<cudaStream_t>(stream)));
+}
+
+dr_status dr_prompt_attn(const void *q, int64_t q_stride, const dr_kv_cache *cache, const int32_t *row_start,
+                         const int32_t *kv_len, const dr_score_opts *opts, int T, int B, int Hq, int Hkv, int D,
+                         int max_len_hint, float scale, void *out, dr_dtype out_dtype, void *ws, size_t ws_bytes,
+                         int32_t *err_flag, void *stream) {
+    dr_status st = check_sizes(T, B, Hq, Hkv, D);
+    if (st != DR_OK) return st;
+    int cap = 0;
+    st = check_cache(cache, &cap);
+    if (st != DR_OK) return st;
+    st = check_scores(scale, opts);
+    if (st != DR_OK) return st;
+    if (!q || !row_start || !kv_len || !out || !aligned16(q) || !aligned16(out) || bad_stride(q_stride, Hq))
+        return DR_ERR_INVALID_ARG;
+    if (out_dtype != DR_BF16 && out_dtype != DR_F32) return DR_ERR_INVALID_ARG;
+    if (!aligned16(ws)) return DR_ERR_INVALID_ARG;
+    if (opts && opts->prefix_len && !opts->causal) return DR_ERR_INVALID_ARG;
+    dr::PromptParams p = {};
+    p.q = static_cast<const uint16_t *>(q);
+    p.q_stride = q_stride;
+    fill_cache(p, cache, cap);
+    fill_scores(p, cache, scale, opts);
+    p.row_start = row_start;
+    p.kv_len = kv_len;
+    p.causal = opts ? opts->causal : 1;
+    p.prefix_len = opts ? opts->prefix_len : nullptr;
+    p.first_key = opts ? opts->first_key : nullptr;
+    p.T = T;
+    p.B = B;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.g = Hq / Hkv;
+    p.out = out;
+    p.out_f32 = out_dtype == DR_F32;
+    p.err = err_flag;
+    const int sms = dr::current_device_sms();
+    if (sms <= 0) return DR_ERR_CUDA;
+    const bool paged = cache->layout == DR_KV_PAGED, fp8 = cache->kv_dtype == DR_KV_FP8_E4M3;
+    const int len = max_len_hint > 0 && max_len_hint < cap ? max_len_hint : cap;
+    (void)ws_bytes;
+    p.tokens_per_row = (T + B - 1) / B;
+    p.few_max = 0x7FFFFFFF;
+    const long long items = (long long)B * p.tokens_per_row;
+    return from_cuda(dr::launch_attn_tokens(p, paged, fp8, dr::plan_token_splits(items, Hkv, p.g, len, fp8, sms),
+                                            static_cast<cudaStream_t>(stream)));
+}
+
+size_t dr_prompt_attn_workspace(int T, int B, int Hq, int Hkv, int max_len, int num_sms) {
+    (void)T;
+    (void)B;
+    (void)Hq;
+    (void)Hkv;
+    (void)max_len;
+    (void)num_sms;
+    return 0;
+}
+
+}  // extern "C"

@@ -17,6 +17,12 @@
  * decoder's two ends around them are dr_lm_head (the merged codebook heads
  * on the newest position, writing the logits the sampler reads) and
  * dr_embed_tokens (the merged embedding lookup of the drawn tokens).
+ * Around the step, on the same caches and with grouped heads:
+ *   dr_rope_append          rotate q and k by position and append the keys and
+ *                           values of ragged new tokens (prompts, or one per row);
+ *   dr_prompt_attn          attention of ragged query tokens over the cache, with
+ *                           a score cap, a distance bias and causal, prefix and
+ *                           document masks.
  *
  * Conventions shared by every call
  *   - Every pointer argument except `stream` is a DEVICE pointer owned by the
@@ -36,7 +42,10 @@
  *     is non-NULL, ORs a DR_ERRF_* bit into *err_flag (a device int32 the
  *     caller zeroes and reads back when it chooses).
  *   - Head dimension D must be 64 (DR_ERR_UNSUPPORTED otherwise); keys and
- *     values have as many heads H as the query (plain multi-head attention).
+ *     values have as many heads H as the query (plain multi-head attention),
+ *     except in the calls that take Hq and Hkv: there Hq is a multiple of Hkv
+ *     (at most 128 times), and query head h uses key/value head h / (Hq/Hkv);
+ *     such a call's cache is described with Hkv in the place of H.
  *   - Calls on the same stream are ordered; the library holds no state
  *     between calls, so calls on different streams may overlap as long as
  *     they do not write the same buffers.
@@ -78,6 +87,7 @@ typedef enum dr_kv_dtype {
 #define DR_ERRF_POS 4      /* an append position outside [0, capacity) or on an unmapped block; row skipped */
 #define DR_ERRF_TOKEN 8    /* a token outside [0, V) in dr_embed_tokens; that codebook's row was skipped */
 #define DR_ERRF_TIMEOUT 16 /* a bounded on-chip wait gave up (never expected); that CTA's results were not written */
+#define DR_ERRF_ROW_START 32 /* row_start does not rise from 0 to at most T; rows were cut to [0, T) */
 
 /* Sampler flags. */
 #define DR_SAMPLE_ADVANCE 1 /* after drawing, step[b] += 1 for every row b */
@@ -332,6 +342,101 @@ dr_status dr_lm_head_stall_test(const void *hidden, const void *W, int B, int K,
 dr_status dr_decode_self_attn_stall_test(const void *q, const dr_kv_cache *cache, const int32_t *seq_len, int B, int H,
                                         int D, int max_seq_len_hint, float scale, void *out, dr_dtype out_dtype,
                                         int32_t *err_flag, int stall_row, void *stream);
+
+/*
+ * dr_rope_table -- cos and sin of every position and frequency, the table
+ * that dr_rope_append reads (made once, kept by the caller):
+ *   table[p][i]             = cos(p * base^(-2i / rot_dim)),  i in [0, rot_dim/2)
+ *   table[p][rot_dim/2 + i] = sin(p * base^(-2i / rot_dim))
+ * Angles and functions are computed in 64 bits and rounded once to fp32.
+ *   table : [max_pos][rot_dim] float32 (device, 16-byte aligned, written)
+ *   rot_dim : 16, 32, 48 or 64 (DR_ERR_UNSUPPORTED otherwise);  base > 0
+ */
+dr_status dr_rope_table(float *table, int max_pos, int rot_dim, double base, void *stream);
+
+/*
+ * dr_rope_append -- rotate the queries and keys of ragged new tokens by their
+ * positions and append the keys and values to the cache, in one pass.
+ *
+ * Row b's tokens are t = row_start[b] .. row_start[b+1]-1; token
+ * row_start[b] + i goes to cache slot start_pos[b] + i of row b and is
+ * rotated for position start_pos[b] + i (+ pos_offset[b]):
+ *   (x1, x2) -> (x1 cos - x2 sin, x2 cos + x1 sin)
+ * on the pairs (i, i + rot_dim/2), or (2i, 2i+1) when interleaved, i in
+ * [0, rot_dim/2) of every head; dimensions from rot_dim on and all of v pass
+ * through.  Products and sum are rounded apart in fp32; the result is rounded
+ * once: to bf16, or to the e4m3 code of fl32(x / scale) as in dr_kv_append.
+ * Tokens from row_start[B] on are left as they are (q_out and cache).
+ *
+ *   cache    : see dr_kv_cache, with Hkv heads; B rows
+ *   q        : nullable [T][Hq][D] bf16 (device, 16-byte aligned), tokens q_stride elements apart (a multiple
+ *              of 8, at least Hq*D: a slice of a fused projection's output will do)
+ *   k, v     : [T][Hkv][D] bf16 likewise, k_stride and v_stride
+ *   q_out    : rotated queries, [T][Hq][D] bf16 likewise; null exactly when q is; may be q itself with the same
+ *              stride, else it overlaps no input
+ *   row_start: [B+1] int32 (device), rising from 0 to at most T (DR_ERRF_ROW_START otherwise); rows may be empty
+ *   start_pos: [B] int32 (device), cache slot of each row's first new token.  DR_ERRF_POS and no key or value is
+ *              written where a slot is outside [0, capacity) or its block outside the pool
+ *   pos_offset : nullable [B] int32 (device), added to the slot for the rotation (keys before the row's own
+ *              cache, such as a shared prefix)
+ *   rope_table : [rope_len][rot_dim] float32 as dr_rope_table makes it (device, 16-byte aligned); null: no
+ *              rotation.  A position outside [0, rope_len): DR_ERRF_POS, the token is left out altogether
+ *   interleaved: 0 or 1
+ * Two rows may not write the same slot of the same block.
+ */
+dr_status dr_rope_append(const dr_kv_cache *cache, const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                         const void *v, int64_t v_stride, void *q_out, int64_t q_out_stride, const int32_t *row_start,
+                         const int32_t *start_pos, const int32_t *pos_offset, const float *rope_table, int rope_len,
+                         int rot_dim, int interleaved, int T, int B, int Hq, int Hkv, int D, int32_t *err_flag,
+                         void *stream);
+
+/* How dr_prompt_attn scores and masks keys (read on the host during the call; the arrays are device pointers). */
+typedef struct dr_score_opts {
+    int32_t causal;            /* 1: the query at position p sees keys up to p; 0: all keys of its row */
+    float softcap;             /* > 0 (1e-6 .. 1e30): s -> softcap * tanh(s / softcap); 0: none */
+    const float *slopes;       /* nullable [Hq] float32: s -> s - slopes[h] * |p - j| (after the cap) */
+    const int32_t *prefix_len; /* nullable [B], causal only: keys j < prefix_len[b] are seen by all queries of row b */
+    const int32_t *first_key;  /* nullable [T]: query t sees no key before first_key[t] (packed documents, windows) */
+} dr_score_opts;
+
+/*
+ * dr_prompt_attn -- attention of ragged query tokens (prompts, chunks of
+ * prompts, or one token per row) over the cache that already holds their keys.
+ *
+ * Row b's queries are t = row_start[b] .. row_start[b+1]-1, n of them; they
+ * are the last n of the row's kv_len[b] keys: query row_start[b] + i stands at
+ * position p = kv_len[b] - n + i.  For query head h and its key/value head:
+ *   s_j = scale * (q . K_j), capped, biased (dr_score_opts)
+ *   out[t][h] = sum_j softmax(s)_j V_j over the keys j in [lo, hi),
+ *   lo = max(0, first_key[t]), hi = min(kv_len[b], max(p + 1, prefix_len[b])) when causal, else kv_len[b].
+ * A query that sees no key outputs zeros.  Scores, softmax statistics and sums
+ * are fp32; the weights are rounded for the product with V to bf16 (e4m3
+ * caches: to f16, which also holds the codes and, scaled by a power of two per
+ * head, q).  Keys at or past kv_len and keys that no query of the call may see
+ * do not reach the result whatever they hold.
+ *
+ *   q        : [T][Hq][D] bf16 (device, 16-byte aligned), tokens q_stride elements apart (multiple of 8, >= Hq*D)
+ *   cache    : see dr_kv_cache, with Hkv heads; B rows
+ *   row_start: [B+1] int32 (device), rising from 0 to at most T (DR_ERRF_ROW_START otherwise); rows may be empty;
+ *              outputs of tokens from row_start[B] on are left as they are
+ *   kv_len   : [B] int32 (device), keys per row, its new tokens' included: n <= kv_len[b] <= capacity (clamped to
+ *              [0, capacity] and flagged DR_ERRF_SEQ_LEN otherwise)
+ *   opts     : nullable (causal, nothing else)
+ *   max_len_hint : an upper bound the caller knows for kv_len (<= 0: the capacity); tunes the work split only
+ *   scale    : <= 0 selects 1/sqrt(D)
+ *   out      : [T][Hq][D] in out_dtype (device, 16-byte aligned)
+ *   ws       : nullable workspace (device, 16-byte aligned) of ws_bytes; with at least
+ *              dr_prompt_attn_workspace bytes few queries over many keys are spread over the GPU.  Its contents
+ *              mean nothing before and after the call; calls that may overlap need one each
+ *   err_flag : nullable device int32 (DR_ERRF_ROW_START, DR_ERRF_SEQ_LEN, DR_ERRF_BLOCK_ID, DR_ERRF_TIMEOUT)
+ */
+dr_status dr_prompt_attn(const void *q, int64_t q_stride, const dr_kv_cache *cache, const int32_t *row_start,
+                         const int32_t *kv_len, const dr_score_opts *opts, int T, int B, int Hq, int Hkv, int D,
+                         int max_len_hint, float scale, void *out, dr_dtype out_dtype, void *ws, size_t ws_bytes,
+                         int32_t *err_flag, void *stream);
+
+/* Host-only: workspace bytes dr_prompt_attn wants for such a call on a GPU with num_sms SMs (0: none needed). */
+size_t dr_prompt_attn_workspace(int T, int B, int Hq, int Hkv, int max_len, int num_sms);
 
 /*
  * dr_plan_splits -- host-only query: how many CTAs (one thread-block
