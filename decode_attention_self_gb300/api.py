@@ -64,13 +64,19 @@ _lib.dr_prompt_attn.argtypes = [_vp, _i64, ctypes.POINTER(dr_kv_cache), _vp, _vp
                                 _i, _i, _i, _i, _f, _vp, _i, _vp, _sz, _vp, _vp]
 _lib.dr_prompt_attn_workspace.argtypes = [_i, _i, _i, _i, _i, _i]
 _lib.dr_prompt_attn_workspace.restype = _sz
+_lib.dr_shared_prefix_attn.argtypes = [_vp, _i64, ctypes.POINTER(dr_kv_cache), _vp, ctypes.POINTER(dr_kv_cache), _vp,
+                                       ctypes.POINTER(dr_score_opts), _i, _i, _i, _i, _i, _i, _f, _vp, _i, _vp, _sz, _vp,
+                                       _vp]
+_lib.dr_shared_prefix_attn_workspace.argtypes = [_i, _i, _i, _i, _i]
+_lib.dr_shared_prefix_attn_workspace.restype = _sz
 _lib.dr_plan_splits.argtypes = [_i, _i, _i, _i, _i]
 _lib.dr_plan_splits.restype = _i
 _lib.dr_status_string.argtypes = [_i]
 _lib.dr_status_string.restype = ctypes.c_char_p
 for _fn in ("dr_kv_append", "dr_decode_self_attn", "dr_decode_cross_attn", "dr_decode_layer",
             "dr_sample_topk_delayed", "dr_embed_tokens", "dr_lm_head", "dr_lm_head_stall_test",
-            "dr_decode_self_attn_stall_test", "dr_rope_table", "dr_rope_append", "dr_prompt_attn"):
+            "dr_decode_self_attn_stall_test", "dr_rope_table", "dr_rope_append", "dr_prompt_attn",
+            "dr_shared_prefix_attn"):
     getattr(_lib, _fn).restype = _i
 
 
@@ -410,6 +416,45 @@ def dr_prompt_attn(q: torch.Tensor, cache: KVCache, row_start: torch.Tensor, kv_
                                _ptr(workspace, torch.uint8, "workspace"),
                                0 if workspace is None else workspace.numel(), _ptr(err_flag, torch.int32, "err_flag"),
                                _stream(stream)))
+    return out
+
+
+def dr_shared_prefix_attn_workspace(B: int, Hq: int, Hkv: int, max_prefix: int, num_sms: int | None = None) -> int:
+    """Bytes of workspace dr_shared_prefix_attn needs for prefixes of up to max_prefix keys."""
+    return int(_lib.dr_shared_prefix_attn_workspace(B, Hq, Hkv, max_prefix, _sms() if num_sms is None else num_sms))
+
+
+def dr_shared_prefix_attn(q: torch.Tensor, prefix: KVCache, prefix_len: torch.Tensor, out: torch.Tensor,
+                          workspace: torch.Tensor, cache: KVCache | None = None, seq_len: torch.Tensor | None = None,
+                          softcap: float = 0.0, slopes: torch.Tensor | None = None, max_prefix_hint: int = 0,
+                          max_seq_len_hint: int = 0, scale: float = 0.0, err_flag: torch.Tensor | None = None,
+                          stream=None) -> torch.Tensor:
+    """One query per row, q [B,Hq,D], over the one-row cache `prefix` that all rows share and the row's own keys."""
+    B, Hq, D = q.shape
+    Hkv = prefix.k.shape[1]
+    if (cache is None) != (seq_len is None):
+        raise ValueError("cache and seq_len go together")
+    _same_device(q=q, prefix_k=prefix.k, prefix_v=prefix.v, prefix_block_table=prefix.block_table,
+                 prefix_len=prefix_len, out=out, workspace=workspace, seq_len=seq_len, slopes=slopes, err_flag=err_flag)
+    _cache_rows(prefix, 1, Hkv, D, "prefix")
+    if cache is not None:
+        _same_device(cache_k=cache.k, cache_v=cache.v, block_table=cache.block_table)
+        _cache_rows(cache, B, Hkv, D)
+    _sized(out, (B, Hq, D), "out")
+    _sized(prefix_len, (1,), "prefix_len")
+    _sized(seq_len, (B,), "seq_len")
+    _sized(slopes, (Hq,), "slopes")
+    qp, qs = _token_rows(q, torch.bfloat16, "q")
+    pc = prefix.as_c()
+    c = None if cache is None else cache.as_c()
+    o = _score_opts(False, softcap, slopes, None, None)
+    _check("dr_shared_prefix_attn",
+           _lib.dr_shared_prefix_attn(qp, qs, ctypes.byref(pc), _ptr(prefix_len, torch.int32, "prefix_len"),
+                                      None if c is None else ctypes.byref(c), _ptr(seq_len, torch.int32, "seq_len"),
+                                      ctypes.byref(o), B, Hq, Hkv, D, int(max_prefix_hint), int(max_seq_len_hint),
+                                      float(scale), _ptr(out, None, "out"), _out_dtype(out),
+                                      _ptr(workspace, torch.uint8, "workspace"), workspace.numel(),
+                                      _ptr(err_flag, torch.int32, "err_flag"), _stream(stream)))
     return out
 
 

@@ -1,0 +1,817 @@
+// Attention of many query rows over a cache on the 5th-generation tensor cores: prompts, chunks of prompts, and the
+// prefix that all rows of a batch share.
+//
+//   S = Q K^T (128 query rows x 128 keys, D = 64),  P = 2^(S' - m),  O = O 2^(m_old - m) + P V,  l = l 2^(..) + sum P
+//
+// The g query heads of a kv head and consecutive tokens fill a tile's rows together (row = token * g + head), so one
+// pass over the keys serves them all.  A CTA holds one tile per softmax warpgroup (kWG of them) and walks its keys
+// 128 at a time:
+//   producer warp     TMA loads of K and V tiles (a paged tile is eight 16-key boxes, lane i fetching block i; blocks
+//                     outside the pool and past the last visible key come from an out-of-range coordinate: zeros)
+//   MMA warp          S = Q K^T into tensor memory, one tile ahead of the softmax; O += P V with P read from tensor
+//                     memory and V as the MN-major operand
+//   softmax warps     one thread per query row: S to registers, mask, running maximum, weights, P back to tensor
+//                     memory; S is free for the next product as soon as it is in registers
+//   helper warps      bf16: in tiles that some row does not see whole, values that are not finite become 0 (0 times
+//                     infinity would reach rows that do not see them); rows that do see them get them back at the end.
+//                     e4m3: codes to f16 (exact) on the way from the TMA's buffer to the MMA's
+// The running maximum moves only when a score passes it by 2^8 (log2 units): O is rescaled rarely.  Sums and states are
+// fp32; weights are rounded once, to bf16 (e4m3: f16), for the product with V.
+//
+// Every wait is bounded (about 2 s): DR_ERRF_TIMEOUT, the CTA writes nothing, drains its copies and frees its tensor
+// memory.
+#include "dr_prompt.h"
+#include "dr_rows.cuh"
+#include "dr_score.cuh"
+#include "dr_tc.cuh"
+
+namespace dr {
+namespace {
+
+using namespace tc;
+
+constexpr int kD = kHeadDim;
+constexpr int kRows = 128;   // query rows per tile (MMA M) and keys per tile (MMA N of S, K of O)
+constexpr int kKeys = 128;
+constexpr float kSlack = 8.0f;
+constexpr int kBitsRing = 8;
+constexpr int kMaxStages = 4;
+constexpr uint32_t kTileBytes = kKeys * kD * 2;   // a K, V or Q tile of 16-bit elements: 16 KB
+
+template <int kWG, bool kFp8>
+struct Config {
+    static constexpr int kHelperWarps = 2;
+    static constexpr int kThreads = 128 * kWG + 128;
+    static constexpr int kCtasPerSm = kWG == 1 ? 2 : 1;
+    static constexpr int kTma = kFp8 ? 2 : (kWG == 1 ? 3 : 4);   // stages that TMA fills (bf16: the MMA reads them)
+    static constexpr int kMma = kFp8 ? 2 : kTma;                 // stages that the MMA reads
+    static constexpr uint32_t kTmaBytes = kKeys * kD * (kFp8 ? 1 : 2);
+    static constexpr uint32_t kQ = 0, kK = kWG * kTileBytes, kV = kK + kMma * kTileBytes,
+                              kRawK = kV + kMma * kTileBytes, kRawV = kRawK + (kFp8 ? kTma * kTmaBytes : 0),
+                              kEnd = kRawV + (kFp8 ? kTma * kTmaBytes : 0);
+    // Registers: softmax threads hold a row of 128 scores; the rest needs few.  The shares add up to the launch's.
+    static constexpr int kLaunchRegs = kWG == 1 ? 128 : 168;
+    static constexpr int kSoftmaxRegs = kWG == 1 ? 184 : 208;
+    static constexpr int kOtherRegs = kWG == 1 ? 72 : 88;
+    static_assert(128 * kWG * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "register split");
+    // tensor memory columns: per warpgroup S (128), O (64), P (64, two weights per column)
+    static constexpr uint32_t kTmemCols = 256 * kWG;
+};
+
+struct Control {   // at Config::kEnd of the dynamic shared memory
+    uint64_t k_full[kMaxStages], k_empty[kMaxStages], v_full[kMaxStages], v_empty[kMaxStages];
+    uint64_t k_ready[kMaxStages], v_ready[kMaxStages], kc_empty[kMaxStages], vc_empty[kMaxStages];
+    uint64_t s_full[2], s_free[2], p_full[2], o_done[2];
+    uint32_t tmem;
+    int gave_up, nonfinite;
+    int bits[kBitsRing];                 // per tile: which of its eight 16-key blocks are there
+    int b, qt, s0, n, L, prefix;         // the CTA's row and tile
+    int lo_min[2], hi_max[2];            // keys that some row of the warpgroup sees
+    int lo_max, hi_min;                  // keys that every row of the CTA sees
+};
+
+struct TileParams {
+    PromptParams p;
+    int32_t splits;
+};
+
+// Physical byte of 16-byte chunk c of 128-byte row r under the 128-byte swizzle (tile base 1024-byte aligned).
+__device__ __forceinline__ uint32_t swz(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
+
+__device__ __forceinline__ bool nonfinite16(uint32_t w, uint32_t exp_mask) {
+    return (w & exp_mask) == exp_mask || ((w >> 16) & exp_mask) == exp_mask;
+}
+
+// Keys [lo, hi) that query i of a row of n queries and L keys sees, and its position.
+__device__ __forceinline__ void visible(const PromptParams &p, int t, int i, int n, int L, int prefix, int &lo, int &hi,
+                                        int &pos) {
+    if (p.row_start) {
+        pos = L - n + i;
+        lo = p.first_key ? max(0, __ldg(p.first_key + t)) : 0;
+        hi = p.causal ? min(L, max(pos + 1, prefix)) : L;
+    } else {   // shared prefix: every query stands behind it
+        pos = L + (p.own_len ? max(0, __ldg(p.own_len + t)) : 0) - 1;
+        lo = 0;
+        hi = L;
+    }
+    if (lo >= hi) lo = hi = 0;
+}
+
+template <int kWG, bool kFp8, bool kPaged>
+__global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>::kCtasPerSm)
+    attn_tiles_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                      const TileParams tp) {
+    using C = Config<kWG, kFp8>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    Control &ctl = *reinterpret_cast<Control *>(smem + C::kEnd);
+    const PromptParams &p = tp.p;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int kProducer = 4 * kWG, kMmaWarp = kProducer + 1, kHelper = kProducer + 2;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kMaxStages; ++i) {
+            mbar_init(&ctl.k_full[i], 1);
+            mbar_init(&ctl.v_full[i], 1);
+            mbar_init(&ctl.k_empty[i], kFp8 ? C::kHelperWarps : 1);
+            mbar_init(&ctl.v_empty[i], kFp8 ? C::kHelperWarps : 1);
+            mbar_init(&ctl.k_ready[i], C::kHelperWarps);
+            mbar_init(&ctl.v_ready[i], C::kHelperWarps);
+            mbar_init(&ctl.kc_empty[i], 1);
+            mbar_init(&ctl.vc_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&ctl.s_full[i], 1);
+            mbar_init(&ctl.s_free[i], 4);
+            mbar_init(&ctl.p_full[i], 4);
+            mbar_init(&ctl.o_done[i], 1);
+            ctl.lo_min[i] = 0x7FFFFFFF;
+            ctl.hi_max[i] = 0;
+        }
+        ctl.lo_max = 0;
+        ctl.hi_min = 0x7FFFFFFF;
+        ctl.gave_up = (smem_u32(smem) & 1023u) != 0;   // never: the swizzled tiles need 1024-byte alignment
+        ctl.nonfinite = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_k)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_v)) : "memory");
+    }
+    pdl_wait();
+    pdl_trigger();
+
+    // Which tile of which row: tiles of the rows in turn, a row's last (longest, when causal) tile first
+    const int split = (int)blockIdx.x % tp.splits;
+    const int rows_per_cta = kRows * kWG;
+    if (warp == 0) {
+        int want = (int)blockIdx.x / tp.splits;
+        int b = -1, s0 = 0, n = 0;
+        if (!p.row_start) {
+            const int tiles = (int)(((long long)p.T * p.g + rows_per_cta - 1) / rows_per_cta);
+            if (want < tiles) b = 0;
+            n = p.T;
+        } else {
+            const bool checks = blockIdx.x == 0 && blockIdx.y == 0;   // this CTA looks every row over
+            for (int base = 0; base < p.B && (b < 0 || checks); base += 32) {
+                int a = 0, e = 0;
+                if (base + lane < p.B) {
+                    a = __ldg(p.row_start + base + lane);
+                    e = __ldg(p.row_start + base + lane + 1);
+                    if (checks && (a < 0 || e < a || e > p.T || (base + lane == 0 && a != 0)))
+                        flag_error(p.err, DR_ERRF_ROW_START);
+                    a = min(max(a, 0), p.T);
+                    e = min(max(e, a), p.T);
+                }
+                if (b >= 0) continue;
+                const int len = e - a;
+                const int tiles = len > p.few_max ? (int)(((long long)len * p.g + rows_per_cta - 1) / rows_per_cta) : 0;
+                int sum = tiles;
+#pragma unroll
+                for (int off = 1; off < 32; off <<= 1) {
+                    const int o = __shfl_up_sync(0xFFFFFFFFu, sum, off);
+                    if (lane >= off) sum += o;
+                }
+                const unsigned m = __ballot_sync(0xFFFFFFFFu, sum > want);
+                if (m) {
+                    const int src = __ffs(m) - 1;
+                    b = base + src;
+                    s0 = __shfl_sync(0xFFFFFFFFu, a, src);
+                    n = __shfl_sync(0xFFFFFFFFu, len, src);
+                    const int before = __shfl_sync(0xFFFFFFFFu, sum - tiles, src), mine = __shfl_sync(0xFFFFFFFFu, tiles, src);
+                    want = mine - 1 - (want - before);
+                } else {
+                    want -= __shfl_sync(0xFFFFFFFFu, sum, 31);
+                }
+            }
+        }
+        if (lane == 0) {
+            int L = 0, prefix = 0;
+            if (b >= 0) {
+                L = __ldg(p.kv_len + b);
+                const int min_len = p.row_start ? n : 0;
+                if (L < min_len || L > p.cap) {
+                    flag_error(p.err, DR_ERRF_SEQ_LEN);
+                    L = min(max(L, 0), p.cap);
+                }
+                prefix = p.prefix_len ? __ldg(p.prefix_len + b) : 0;
+            }
+            ctl.b = b;
+            ctl.qt = want;
+            ctl.s0 = s0;
+            ctl.n = n;
+            ctl.L = L;
+            ctl.prefix = prefix;
+        }
+    }
+    __syncthreads();
+    if (ctl.b < 0 || ctl.gave_up) {   // past the last tile
+        if (ctl.gave_up && threadIdx.x == 0) flag_error(p.err, DR_ERRF_TIMEOUT);
+        return;
+    }
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ctl.tmem)),
+                     "r"(C::kTmemCols));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        fence_before();
+    }
+    const int b = ctl.b, L = ctl.L, n = ctl.n, hk = blockIdx.y;
+
+    // Query rows: each softmax thread loads its own into the swizzled tile
+    const int wg = warp >> 2, row = threadIdx.x & 127;
+    int lo = 0, hi = 0, pos = 0, token = 0, head = 0;
+    bool valid = false;
+    float qfac = 1.0f;
+    if (warp < kProducer) {
+        const long long flat = (long long)ctl.qt * rows_per_cta + wg * kRows + row;
+        valid = flat < (long long)n * p.g;
+        uint8_t *qs = smem + C::kQ + wg * kTileBytes;
+        if (valid) {
+            const int i = (int)(flat / p.g);
+            token = ctl.s0 + i;
+            head = hk * p.g + (int)(flat - (long long)i * p.g);
+            visible(p, token, i, n, L, ctl.prefix, lo, hi, pos);
+            const uint16_t *src = p.q + (size_t)token * p.q_stride + (size_t)head * kD;
+            uint4 w[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) w[c] = ld_ro16(src + 8 * c);
+            if (kFp8) {
+                float big = 0.f;
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    float x[8];
+                    unpack8(w[c], x);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) big = fmaxf(big, fabsf(x[j]));
+                }
+                const float up = pow2_normaliser(big);
+                qfac = 1.0f / up;
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    float x[8];
+                    unpack8(w[c], x);
+                    w[c] = make_uint4(pack_f16(x[0] * up, x[1] * up), pack_f16(x[2] * up, x[3] * up),
+                                      pack_f16(x[4] * up, x[5] * up), pack_f16(x[6] * up, x[7] * up));
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4 *>(qs + swz(row, c)) = w[c];
+        } else {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4 *>(qs + swz(row, c)) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async();
+        const bool sees = hi > lo;
+        const int a0 = __reduce_min_sync(0xFFFFFFFFu, sees ? lo : 0x7FFFFFFF);
+        const int a1 = __reduce_max_sync(0xFFFFFFFFu, hi);
+        const int b0 = __reduce_max_sync(0xFFFFFFFFu, lo);
+        const int b1 = __reduce_min_sync(0xFFFFFFFFu, sees ? hi : 0x7FFFFFFF);
+        if (lane == 0) {
+            atomicMin(&ctl.lo_min[wg], a0);
+            atomicMax(&ctl.hi_max[wg], a1);
+            atomicMax(&ctl.lo_max, b0);
+            atomicMin(&ctl.hi_min, b1);
+        }
+    }
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = ctl.tmem;
+
+    // Key tiles: tile i covers keys [kbase + 128 i, + 128); this split's run, and each warpgroup's part of it
+    int ulo = 0x7FFFFFFF, uhi = 0;
+#pragma unroll
+    for (int w = 0; w < kWG; ++w) {
+        ulo = min(ulo, ctl.lo_min[w]);
+        uhi = max(uhi, ctl.hi_max[w]);
+    }
+    if (ulo >= uhi) ulo = uhi = 0;
+    const int kbase = ulo & ~(kBlockKeys - 1);
+    const int all = (uhi - kbase + kKeys - 1) / kKeys;
+    const int per = (all + tp.splits - 1) / tp.splits;
+    const int t_lo = min(split * per, all), t_hi = min(t_lo + per, all);
+    int jb[kWG], je[kWG], cb = t_hi, ce = t_lo;
+#pragma unroll
+    for (int w = 0; w < kWG; ++w) {
+        jb[w] = je[w] = t_lo;
+        if (ctl.lo_min[w] < ctl.hi_max[w]) {
+            jb[w] = max(t_lo, (ctl.lo_min[w] - kbase) / kKeys);
+            je[w] = max(jb[w], min(t_hi, (ctl.hi_max[w] - kbase + kKeys - 1) / kKeys));
+        }
+        if (je[w] > jb[w]) {
+            cb = min(cb, jb[w]);
+            ce = max(ce, je[w]);
+        }
+    }
+    const int clo = ctl.lo_max, chi = ctl.hi_min;
+    volatile int *gave_up = &ctl.gave_up;
+
+    if (warp >= kProducer) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
+        if (warp == kProducer) {
+            const int kv_row = kPaged ? 0 : b * p.Hkv + hk;
+            // lane i < 8: block i of the tile; z of a missing block is out of range
+            auto block_z = [&](int j, bool &there) -> int {
+                const int key = kbase + j * kKeys + lane * kBlockKeys;
+                int blk = -1;
+                if (lane < 8 && key < uhi) {
+                    blk = __ldg(p.table + (size_t)b * p.max_blocks + key / kBlockKeys);
+                    if ((unsigned)blk >= (unsigned)p.num_blocks) {
+                        flag_error(p.err, DR_ERRF_BLOCK_ID);
+                        blk = -1;
+                    }
+                }
+                there = blk >= 0;
+                return blk >= 0 ? blk * p.Hkv + hk : p.num_blocks * p.Hkv;
+            };
+            bool there = true;
+            int z = 0;
+            if (kPaged && cb < ce) z = block_z(cb, there);
+            for (int j = cb, i = 0, s = 0, round = 0; j < ce; ++j, ++i) {
+                if (round > 0 && !__all_sync(0xFFFFFFFFu, mbar_wait(&ctl.k_empty[s], (round - 1) & 1, gave_up))) break;
+                const unsigned bits = kPaged ? __ballot_sync(0xFFFFFFFFu, there) & 0xFFu : 0xFFu;
+                uint8_t *kd = smem + (kFp8 ? C::kRawK + s * C::kTmaBytes : C::kK + s * kTileBytes);
+                uint8_t *vd = smem + (kFp8 ? C::kRawV + s * C::kTmaBytes : C::kV + s * kTileBytes);
+                if (lane == 0) {
+                    ctl.bits[i % kBitsRing] = (int)bits;
+                    mbar_expect_tx(&ctl.k_full[s], C::kTmaBytes);
+                }
+                __syncwarp();
+                if (kPaged) {
+                    if (lane < 8) tma_load_3d(smem_u32(kd + lane * (C::kTmaBytes / 8)), &map_k, 0, 0, z, &ctl.k_full[s]);
+                } else if (lane == 0) {
+                    tma_load_3d(smem_u32(kd), &map_k, 0, kbase + j * kKeys, kv_row, &ctl.k_full[s]);
+                }
+                if (round > 0 && !__all_sync(0xFFFFFFFFu, mbar_wait(&ctl.v_empty[s], (round - 1) & 1, gave_up))) break;
+                if (lane == 0) mbar_expect_tx(&ctl.v_full[s], C::kTmaBytes);
+                __syncwarp();
+                if (kPaged) {
+                    if (lane < 8) tma_load_3d(smem_u32(vd + lane * (C::kTmaBytes / 8)), &map_v, 0, 0, z, &ctl.v_full[s]);
+                    if (j + 1 < ce) z = block_z(j + 1, there);
+                } else if (lane == 0) {
+                    tma_load_3d(smem_u32(vd), &map_v, 0, kbase + j * kKeys, kv_row, &ctl.v_full[s]);
+                }
+                if (++s == C::kTma) {
+                    s = 0;
+                    ++round;
+                }
+            }
+        } else if (warp == kMmaWarp) {
+            if (lane == 0) {
+                constexpr uint32_t id_s = instr_desc(kRows, kKeys, kFp8, false);
+                constexpr uint32_t id_o = instr_desc(kRows, kD, kFp8, true);
+                uint64_t *k_in = kFp8 ? ctl.k_ready : ctl.k_full, *k_out = kFp8 ? ctl.kc_empty : ctl.k_empty;
+                uint64_t *v_out = kFp8 ? ctl.vc_empty : ctl.v_empty;
+                bool ok = true;
+                // step j: S of tile j, then O of tile j - 1
+                int s = 0, round = 0, sp = 0, roundp = 0;
+                for (int j = cb; j <= ce && cb < ce && ok; ++j) {
+                    if (j < ce) ok = mbar_wait(&k_in[s], round & 1, gave_up);
+#pragma unroll
+                    for (int w = 0; w < kWG; ++w) {
+                        if (ok && j < ce && j >= jb[w] && j < je[w]) {
+                            if (j > jb[w]) ok = mbar_wait(&ctl.s_free[w], (j - jb[w] - 1) & 1, gave_up);
+                            if (ok) {
+                                fence_after();
+                                const uint32_t qa = smem_u32(smem + C::kQ + w * kTileBytes);
+                                const uint32_t ka = smem_u32(smem + C::kK + s * kTileBytes);
+#pragma unroll
+                                for (int k = 0; k < kD / 16; ++k)
+                                    mma_ss(tmem + 256 * w, smem_desc(qa + 32 * k), smem_desc(ka + 32 * k), id_s, k != 0);
+                                commit(&ctl.s_full[w]);
+                            }
+                        }
+                        // (the last stages are not used again: no arrival is left under way when the CTA ends)
+                        if (w == kWG - 1 && ok && j + C::kMma < ce) commit(&k_out[s]);
+                        const int i = j - 1;
+                        if (ok && i >= cb && w == 0) ok = mbar_wait(&ctl.v_ready[sp], roundp & 1, gave_up);
+                        if (ok && i >= jb[w] && i < je[w]) {
+                            ok = mbar_wait(&ctl.p_full[w], (i - jb[w]) & 1, gave_up);
+                            if (ok) {
+                                fence_after();
+                                const uint32_t va = smem_u32(smem + C::kV + sp * kTileBytes);
+#pragma unroll
+                                for (int k = 0; k < kKeys / 16; ++k)
+                                    mma_ts(tmem + 256 * w + 128, tmem + 256 * w + 192 + 8 * k, smem_desc(va + 2048 * k),
+                                           id_o, i > jb[w] || k != 0);
+                                commit(&ctl.o_done[w]);
+                            }
+                        }
+                        if (w == kWG - 1 && ok && i >= cb && i + C::kMma < ce) commit(&v_out[sp]);
+                    }
+                    if (j > cb && ++sp == C::kMma) {
+                        sp = 0;
+                        ++roundp;
+                    }
+                    if (++s == C::kMma) {
+                        s = 0;
+                        ++round;
+                    }
+                }
+            }
+        } else {
+            const int ht = (warp - kHelper) * 32 + lane;
+            constexpr int kHt = C::kHelperWarps * 32;
+            bool ok = true;
+            int s = 0, round = 0, sc = 0, roundc = 0;
+            for (int j = cb, i = 0; j < ce && ok; ++j, ++i) {
+                const int key0 = kbase + j * kKeys;
+                if constexpr (kFp8) {
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv) {
+                        ok = mbar_wait(kv ? &ctl.v_full[s] : &ctl.k_full[s], round & 1, gave_up);
+                        if (ok && roundc > 0)
+                            ok = mbar_wait(kv ? &ctl.vc_empty[sc] : &ctl.kc_empty[sc], (roundc - 1) & 1, gave_up);
+                        ok = __all_sync(0xFFFFFFFFu, ok);
+                        if (!ok) break;
+                        const int bits = ctl.bits[i % kBitsRing];
+                        const bool mixed = key0 < clo || key0 + kKeys > chi || bits != 0xFF;
+                        const uint8_t *raw = smem + (kv ? C::kRawV : C::kRawK) + s * C::kTmaBytes;
+                        uint8_t *dst = smem + (kv ? C::kV : C::kK) + sc * kTileBytes;
+                        bool bad = false;
+                        for (int x = ht; x < kKeys * 4; x += kHt) {
+                            const int r = x >> 2, c = x & 3;
+                            uint4 w = *reinterpret_cast<const uint4 *>(raw + r * 64 + c * 16);
+                            if (kv && mixed) {   // NaN codes (0x7F, 0xFF) of values
+                                uint32_t *ws = &w.x;
+#pragma unroll
+                                for (int y = 0; y < 4; ++y)
+#pragma unroll
+                                    for (int z = 0; z < 4; ++z)
+                                        if (((ws[y] >> (8 * z)) & 0x7F) == 0x7F) {
+                                            ws[y] &= ~(0xFFu << (8 * z));
+                                            bad = bad || (key0 + r >= ulo && key0 + r < uhi);
+                                        }
+                            }
+                            uint32_t h[8];
+                            const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) {
+                                const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(in[y] & 0xFFFFu), __NV_E4M3);
+                                const __half2_raw e = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(in[y] >> 16), __NV_E4M3);
+                                h[2 * y] = (uint32_t)a.x | ((uint32_t)a.y << 16);
+                                h[2 * y + 1] = (uint32_t)e.x | ((uint32_t)e.y << 16);
+                            }
+                            *reinterpret_cast<uint4 *>(dst + swz(r, 2 * c)) = make_uint4(h[0], h[1], h[2], h[3]);
+                            *reinterpret_cast<uint4 *>(dst + swz(r, 2 * c + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
+                        }
+                        if (bad) ctl.nonfinite = 1;
+                        fence_proxy_async();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(kv ? &ctl.v_empty[s] : &ctl.k_empty[s]);
+                            mbar_arrive(kv ? &ctl.v_ready[sc] : &ctl.k_ready[sc]);
+                        }
+                    }
+                    if (++sc == C::kMma) {
+                        sc = 0;
+                        ++roundc;
+                    }
+                } else {
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl.v_full[s], round & 1, gave_up));
+                    if (!ok) break;
+                    const bool mixed = key0 < clo || key0 + kKeys > chi;
+                    if (mixed) {
+                        uint8_t *vt = smem + C::kV + s * kTileBytes;
+                        bool bad = false;
+                        for (int x = ht; x < kKeys * 8; x += kHt) {
+                            uint4 w = *reinterpret_cast<const uint4 *>(vt + x * 16);
+                            if (nonfinite16(w.x, 0x7F80u) || nonfinite16(w.y, 0x7F80u) || nonfinite16(w.z, 0x7F80u) ||
+                                nonfinite16(w.w, 0x7F80u)) {
+                                uint32_t *ws = &w.x;
+#pragma unroll
+                                for (int y = 0; y < 4; ++y) {
+                                    if ((ws[y] & 0x7F80u) == 0x7F80u) ws[y] &= 0xFFFF0000u;
+                                    if ((ws[y] & 0x7F800000u) == 0x7F800000u) ws[y] &= 0x0000FFFFu;
+                                }
+                                *reinterpret_cast<uint4 *>(vt + x * 16) = w;
+                                const int key = key0 + (x >> 3);
+                                bad = bad || (key >= ulo && key < uhi);
+                            }
+                        }
+                        if (bad) ctl.nonfinite = 1;
+                        fence_proxy_async();
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ctl.v_ready[s]);
+                }
+                if (++s == C::kTma) {
+                    s = 0;
+                    ++round;
+                }
+            }
+        }
+        __syncwarp();
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
+        int j0 = jb[0], j1 = je[0];
+        if (kWG == 2 && wg == 1) {
+            j0 = jb[kWG - 1];
+            j1 = je[kWG - 1];
+        }
+        const uint32_t ts = tmem + 256 * wg + ((uint32_t)((warp & 3) * 32) << 16), to = ts + 128, tpw = ts + 192;
+        float m = -INFINITY, mref = 0.f, l = 0.f;
+        const float scale = p.sscale * qfac, c2 = p.cap_c2 * qfac;
+        const bool capped = p.cap_c1 != 0.f, biased = p.slopes != nullptr;
+        const float slope = biased && valid ? __ldg(p.slopes + head) * 1.4426950408889634f : 0.f;
+        const float mul = capped || biased ? 1.0f : scale;
+        bool ok = true;
+        for (int j = j0; j < j1; ++j) {
+            const int k = j - j0, key0 = kbase + j * kKeys;
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl.s_full[wg], k & 1, gave_up));
+            if (!ok) break;
+            fence_after();
+            float s[kKeys];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) ld32(ts + 32 * c, s + 32 * c);
+            wait_ld();
+#pragma unroll
+            for (int c = 0; c < 4; ++c) pin32(s + 32 * c);
+            fence_before();
+            const int bits = ctl.bits[(j - cb) % kBitsRing];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl.s_free[wg]);
+
+            if (capped) {
+#pragma unroll
+                for (int c = 0; c < kKeys; ++c) s[c] = capped_score(s[c], p.cap_c1, c2);
+            } else if (biased) {
+#pragma unroll
+                for (int c = 0; c < kKeys; ++c) s[c] *= scale;
+            }
+            if (biased) {
+                const float d0 = (float)(pos - key0);
+#pragma unroll
+                for (int c = 0; c < kKeys; ++c) s[c] = fmaf(-slope, fabsf(d0 - (float)c), s[c]);
+            }
+            const bool whole = key0 >= lo && key0 + kKeys <= hi && bits == 0xFF;
+            if (__any_sync(0xFFFFFFFFu, !whole)) {
+                const int a = lo - key0, e = hi - key0;
+#pragma unroll
+                for (int c = 0; c < kKeys; ++c)
+                    if (c < a || c >= e || !((bits >> (c / kBlockKeys)) & 1)) s[c] = -INFINITY;
+            }
+            float mx0 = s[0], mx1 = s[1], mx2 = s[2], mx3 = s[3];
+#pragma unroll
+            for (int c = 4; c < kKeys; c += 4) {
+                mx0 = fmaxf(mx0, s[c]);
+                mx1 = fmaxf(mx1, s[c + 1]);
+                mx2 = fmaxf(mx2, s[c + 2]);
+                mx3 = fmaxf(mx3, s[c + 3]);
+            }
+            const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * mul;
+            float corr = 1.0f;
+            if (mx > m + kSlack) {   // also the first visible key (m = -inf)
+                corr = fast_exp2(m - mx);
+                m = mref = mx;
+                l *= corr;
+            }
+            float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+            const float2 mul2 = make_float2(mul, mul), off2 = make_float2(-mref, -mref);
+            uint32_t pk[kKeys / 2];
+#pragma unroll
+            for (int c = 0; c < kKeys; c += 4) {
+                float2 x = __ffma2_rn(make_float2(s[c], s[c + 1]), mul2, off2);
+                float2 y = __ffma2_rn(make_float2(s[c + 2], s[c + 3]), mul2, off2);
+                x.x = fast_exp2(x.x);
+                x.y = fast_exp2(x.y);
+                y.x = fast_exp2(y.x);
+                y.y = fast_exp2(y.y);
+                sum0 = __fadd2_rn(sum0, x);
+                sum1 = __fadd2_rn(sum1, y);
+                pk[c / 2] = kFp8 ? pack_f16(x.x, x.y) : pack_bf16(x.x, x.y);
+                pk[c / 2 + 1] = kFp8 ? pack_f16(y.x, y.y) : pack_bf16(y.x, y.y);
+            }
+            l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
+            if (k > 0) {
+                // P and O are the previous tile's until its product is done
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl.o_done[wg], (k - 1) & 1, gave_up));
+                if (!ok) break;
+                fence_after();
+                if (__any_sync(0xFFFFFFFFu, corr != 1.0f)) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float o[32];
+                        ld32(to + 32 * h, o);
+                        wait_ld();
+                        pin32(o);
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) o[c] *= corr;
+                        st32(to + 32 * h, o);
+                    }
+                }
+            }
+            st32(tpw, pk);
+            st32(tpw + 32, pk + 32);
+            wait_st();
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl.p_full[wg]);
+        }
+
+        float o[kD];
+        if (ok && j1 > j0) {
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl.o_done[wg], (j1 - j0 - 1) & 1, gave_up));
+            fence_after();
+            ld32(to, o);
+            ld32(to + 32, o + 32);
+            wait_ld();
+            pin32(o);
+            pin32(o + 32);
+        } else {
+#pragma unroll
+            for (int c = 0; c < kD; ++c) o[c] = 0.f;
+        }
+        if (ok && valid) {
+            if (*(volatile int *)&ctl.nonfinite) {
+                // Values that are not finite were left out of tiles that some row does not see whole: add those that
+                // this row sees (a positive weight times such a value is such a value)
+                for (int j = j0; j < j1; ++j) {
+                    const int key0 = kbase + j * kKeys;
+                    for (int key = max(lo, key0); key < min(hi, key0 + kKeys); ++key) {
+                        size_t at;
+                        if (kPaged) {
+                            const int blk = __ldg(p.table + (size_t)b * p.max_blocks + key / kBlockKeys);
+                            if ((unsigned)blk >= (unsigned)p.num_blocks) continue;
+                            at = (((size_t)blk * p.Hkv + hk) * kBlockKeys + key % kBlockKeys) * kD;
+                        } else {
+                            at = (((size_t)b * p.Hkv + hk) * (size_t)p.cap + key) * kD;
+                        }
+                        if constexpr (kFp8) {
+                            const uint8_t *v = static_cast<const uint8_t *>(p.v) + at;
+#pragma unroll
+                            for (int c = 0; c < kD; ++c)
+                                if ((v[c] & 0x7F) == 0x7F) o[c] = __int_as_float(0x7FC00000);
+                        } else {
+                            const uint16_t *v = static_cast<const uint16_t *>(p.v) + at;
+#pragma unroll
+                            for (int c = 0; c < kD; ++c)
+                                if ((v[c] & 0x7F80) == 0x7F80) o[c] += __uint_as_float((uint32_t)v[c] << 16);
+                        }
+                    }
+                }
+            }
+            const size_t orow = (size_t)token * p.Hq + head;
+            if (p.part_ml) {
+                const size_t at = (size_t)split * ((size_t)p.T * p.Hq) + orow;
+                p.part_ml[at] = make_float2(m, l);
+                float4 *dst = reinterpret_cast<float4 *>(p.part_acc + at * kD);
+#pragma unroll
+                for (int c = 0; c < kD / 4; ++c)
+                    dst[c] = make_float4(o[4 * c] * p.out_scale, o[4 * c + 1] * p.out_scale, o[4 * c + 2] * p.out_scale,
+                                         o[4 * c + 3] * p.out_scale);
+            } else {
+                const float inv = l == 0.f ? 0.f : p.out_scale / l;
+                const bool none = l == 0.f;
+#pragma unroll
+                for (int c = 0; c < kD; ++c) o[c] = none ? 0.f : o[c] * inv;
+                if (p.out_f32) {
+                    float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(p.out) + orow * kD);
+#pragma unroll
+                    for (int c = 0; c < kD / 4; ++c)
+                        dst[c] = make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+                } else {
+                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + orow * kD);
+#pragma unroll
+                    for (int c = 0; c < kD / 8; ++c)
+                        dst[c] = make_uint4(pack_bf16(o[8 * c], o[8 * c + 1]), pack_bf16(o[8 * c + 2], o[8 * c + 3]),
+                                            pack_bf16(o[8 * c + 4], o[8 * c + 5]), pack_bf16(o[8 * c + 6], o[8 * c + 7]));
+                }
+            }
+        }
+        __syncwarp();
+    }
+    fence_before();
+    __syncthreads();
+    if (*gave_up) {
+        // A wait ran out (never expected): flag it, and let the copies in flight land before the memory is given up
+        if (threadIdx.x == 0) flag_error(p.err, DR_ERRF_TIMEOUT);
+        if (warp == kProducer) {
+            const long long t0 = clock64();
+            while (clock64() - t0 < (1LL << 20)) {
+            }
+        }
+        __syncthreads();
+    }
+    if (warp == kMmaWarp) {
+        fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kTmemCols));
+    }
+}
+
+// out[t][h] from the states of the splits, in split order.  One warp per token: lanes 0-15 and 16-31 take a head each,
+// four dimensions per lane.
+__global__ void __launch_bounds__(256) attn_join_kernel(const PromptParams p) {
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31;
+    const long long tl = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (tl >= p.T) return;
+    const int t = (int)tl;
+    int s0, s1;
+    if (find_row(p.row_start, p.B, p.T, t, lane, s0, s1, nullptr) < 0 || s1 - s0 <= p.few_max) return;
+    const size_t rows = (size_t)p.T * p.Hq;
+    for (int h = lane >> 4; h < p.Hq; h += 2) {
+        const size_t row = (size_t)t * p.Hq + h;
+        float M = -INFINITY;
+        for (int x = 0; x < p.nparts; ++x) M = fmaxf(M, p.part_ml[x * rows + row].x);
+        float l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int x = 0; x < p.nparts; ++x) {
+            const float2 ml = p.part_ml[x * rows + row];
+            if (ml.x == -INFINITY) continue;
+            const float w = exp2f(ml.x - M);
+            const float4 a = reinterpret_cast<const float4 *>(p.part_acc + (x * rows + row) * kD)[lane & 15];
+            l += w * ml.y;
+            o.x += w * a.x;
+            o.y += w * a.y;
+            o.z += w * a.z;
+            o.w += w * a.w;
+        }
+        const float inv = l == 0.f ? 0.f : 1.0f / l;
+        o = l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+        if (p.out_f32)
+            reinterpret_cast<float4 *>(static_cast<float *>(p.out) + row * kD)[lane & 15] = o;
+        else
+            reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + row * kD)[lane & 15] =
+                make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
+    }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        cudaDriverEntryPointQueryResult q;
+        void *ptr = nullptr;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) !=
+                cudaSuccess || q != cudaDriverEntryPointSuccess)
+            ptr = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+    }();
+    return fn;
+}
+
+// Cache as [rows][keys][64] (paged: rows = blocks x heads of 16 keys), box [1][box keys][64].  bf16 tiles land with the
+// 128-byte swizzle that the MMA reads; e4m3 codes land plainly (the helper warps swizzle what they convert).
+bool encode_cache(CUtensorMap *map, const void *ptr, long long rows, int keys, int box_keys, bool fp8) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t e = fp8 ? 1 : 2;
+    const cuuint64_t dims[3] = {(cuuint64_t)kD, (cuuint64_t)keys, (cuuint64_t)rows};
+    const cuuint64_t strides[2] = {kD * e, kD * e * (cuuint64_t)keys};
+    const cuuint32_t box[3] = {(cuuint32_t)kD, (cuuint32_t)box_keys, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return enc(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims,
+               strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               fp8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int kWG, bool kFp8, bool kPaged>
+cudaError_t launch_variant(const PromptParams &p, int splits, cudaStream_t stream) {
+    using C = Config<kWG, kFp8>;
+    auto kern = attn_tiles_kernel<kWG, kFp8, kPaged>;
+    constexpr size_t smem = C::kEnd + sizeof(Control);
+    static_assert(smem <= (kWG == 1 ? 113 * 1024 : 227 * 1024), "shared memory");
+    cudaFuncAttributes fa;
+    cudaError_t e = cudaFuncGetAttributes(&fa, kern);
+    if (e != cudaSuccess) return e;
+    // the register split draws on what the launch gives: fewer would leave a warpgroup waiting
+    if (fa.numRegs * C::kThreads < 128 * kWG * C::kSoftmaxRegs + 128 * C::kOtherRegs) return cudaErrorInvalidConfiguration;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    CUtensorMap mk, mv;
+    const long long rows = (long long)(kPaged ? p.num_blocks : (p.row_start ? p.B : 1)) * p.Hkv;
+    const int keys = kPaged ? kBlockKeys : p.cap, box = kPaged ? kBlockKeys : kKeys;
+    if (rows >= 0x7FFFFFFFLL) return cudaErrorInvalidValue;
+    if (!encode_cache(&mk, p.k, rows, keys, box, kFp8) || !encode_cache(&mv, p.v, rows, keys, box, kFp8))
+        return cudaErrorInvalidValue;
+    const long long rpc = kRows * kWG;
+    // every row may end in a part of a tile; no row has more tiles than tokens
+    const long long per_row = p.row_start ? p.B : 1;
+    long long tiles = ((long long)p.T * p.g + per_row * (rpc - 1)) / rpc;
+    const long long by_tokens = ((long long)p.T * ((p.g + rpc - 1) / rpc));
+    if (tiles > by_tokens) tiles = by_tokens;
+    TileParams tp;
+    tp.p = p;
+    tp.splits = splits;
+    return launch_kernel(kern, dim3((unsigned)(tiles * splits), (unsigned)p.Hkv), dim3(C::kThreads), smem, stream, 1u, mk,
+                         mv, tp);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_tiles(const PromptParams &p, bool paged, bool fp8, int splits, cudaStream_t stream) {
+    if (fp8) return paged ? launch_variant<1, true, true>(p, splits, stream) : launch_variant<1, true, false>(p, splits, stream);
+    return paged ? launch_variant<1, false, true>(p, splits, stream) : launch_variant<1, false, false>(p, splits, stream);
+}
+
+// CTAs that share a tile's keys: while the tiles alone leave SMs (of two CTAs each) idle, with 256 keys each at least.
+int plan_tile_splits(long long tiles, int Hkv, int max_len, int sms) {
+    long long s = 2LL * sms / (tiles * Hkv);
+    const long long by_keys = max_len / 256;
+    if (s > by_keys) s = by_keys;
+    if (s > 64) s = 64;
+    return s < 1 ? 1 : (int)s;
+}
+
+cudaError_t launch_attn_join(const PromptParams &p, cudaStream_t stream) {
+    return launch_kernel(attn_join_kernel, dim3((unsigned)((p.T + 7) / 8)), dim3(256), 0, stream, 1u, p);
+}
+
+}  // namespace dr

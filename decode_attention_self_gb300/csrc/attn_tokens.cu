@@ -392,6 +392,7 @@ __global__ void __launch_bounds__(kThreads) attn_tokens_kernel(const PromptParam
                 o *= p.out_scale;
                 for (int x = 0; x < p.nparts; ++x) {
                     const float2 ml = p.part_ml[x * rows + row];
+                    if (ml.x == -INFINITY) continue;   // an empty share
                     const float wt = exp2f(ml.x - M);
                     ls += wt * ml.y;
                     o += wt * p.part_acc[(x * rows + row) * kD + d];

@@ -48,6 +48,8 @@ struct PromptParams {
     int32_t *err;
     // token kernel: items per row, and the most tokens a row may have to be taken by it (more: the tile kernel's)
     int32_t tokens_per_row, few_max;
+    // tile kernel: queries of a shared prefix stand own_len[t] keys past its end (null: at their row's last keys)
+    const int32_t *own_len;
     // softmax states of key ranges attended before: [nparts][rows = T*Hq] (m, l) and [nparts][rows][64]; null: none
     float2 *part_ml;
     float *part_acc;
@@ -56,6 +58,12 @@ struct PromptParams {
 
 // Query rows one token at a time (memory bound: single tokens of a batch).
 cudaError_t launch_attn_tokens(const PromptParams &p, bool paged, bool fp8, int splits, cudaStream_t stream);
+// Query rows 128 at a time on the tensor cores.  splits CTAs share a tile's keys; with part_ml set every CTA leaves its
+// softmax state there (nparts = splits), else splits is 1 and the outputs are written.
+cudaError_t launch_attn_tiles(const PromptParams &p, bool paged, bool fp8, int splits, cudaStream_t stream);
+// Joins the states that the tile kernel's splits left (rows of more than few_max tokens).
+cudaError_t launch_attn_join(const PromptParams &p, cudaStream_t stream);
+int plan_tile_splits(long long tiles, int Hkv, int max_len, int sms);
 int plan_token_splits(long long items, int Hkv, int g, int max_len, bool fp8, int sms);
 
 }  // namespace dr

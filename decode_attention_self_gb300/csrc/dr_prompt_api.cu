@@ -72,6 +72,20 @@ dr_status check_scores(float scale, const dr_score_opts *o) {
     return DR_OK;
 }
 
+// Query tiles of the tile kernel that T tokens of g heads fill, at least.
+long long tiles_of(int T, int g) { return ((long long)T * g + 127) / 128; }
+
+// Softmax states of `splits` key ranges: (m, l) and 64 sums per (token, head).
+size_t states_bytes(int splits, int T, int Hq) {
+    return (size_t)splits * T * Hq * (dr::kHeadDim + 2) * sizeof(float);
+}
+// The sums first: they keep the workspace's 16-byte alignment.
+void set_states(dr::PromptParams &p, void *ws, int splits) {
+    p.part_acc = static_cast<float *>(ws);
+    p.part_ml = reinterpret_cast<float2 *>(p.part_acc + (size_t)splits * p.T * p.Hq * dr::kHeadDim);
+    p.nparts = splits;
+}
+
 }  // namespace
 
 extern "C" {
@@ -174,22 +188,99 @@ dr_status dr_prompt_attn(const void *q, int64_t q_stride, const dr_kv_cache *cac
     if (sms <= 0) return DR_ERR_CUDA;
     const bool paged = cache->layout == DR_KV_PAGED, fp8 = cache->kv_dtype == DR_KV_FP8_E4M3;
     const int len = max_len_hint > 0 && max_len_hint < cap ? max_len_hint : cap;
-    (void)ws_bytes;
-    p.tokens_per_row = (T + B - 1) / B;
-    p.few_max = 0x7FFFFFFF;
-    const long long items = (long long)B * p.tokens_per_row;
-    return from_cuda(dr::launch_attn_tokens(p, paged, fp8, dr::plan_token_splits(items, Hkv, p.g, len, fp8, sms),
-                                            static_cast<cudaStream_t>(stream)));
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    // Rows of one token go to the token kernel, longer ones to the tile kernel (it reads a row's keys once for all
+    // its tokens).  The host knows only T and B: one launch when that settles it, else both.
+    p.tokens_per_row = 1;
+    p.few_max = 1;
+    const bool few = B > 1 || T == 1, many = T > B;
+    if (!many) p.few_max = 0x7FFFFFFF;
+    if (few) {
+        const cudaError_t e =
+            dr::launch_attn_tokens(p, paged, fp8, dr::plan_token_splits(B, Hkv, p.g, len, fp8, sms), cs);
+        if (e != cudaSuccess || !many) return from_cuda(e);
+    } else {
+        p.few_max = 0;
+    }
+    int splits = dr::plan_tile_splits(tiles_of(T, p.g), Hkv, len, sms);
+    if (splits > 1 && (!ws || ws_bytes < states_bytes(splits, T, Hq))) splits = 1;
+    if (splits > 1) set_states(p, ws, splits);
+    const cudaError_t e = dr::launch_attn_tiles(p, paged, fp8, splits, cs);
+    if (e != cudaSuccess || splits == 1) return from_cuda(e);
+    return from_cuda(dr::launch_attn_join(p, cs));
 }
 
 size_t dr_prompt_attn_workspace(int T, int B, int Hq, int Hkv, int max_len, int num_sms) {
-    (void)T;
-    (void)B;
-    (void)Hq;
-    (void)Hkv;
-    (void)max_len;
-    (void)num_sms;
-    return 0;
+    if (T < 1 || B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || max_len < 1 || num_sms < 1) return 0;
+    if (T <= B) return 0;
+    const int splits = dr::plan_tile_splits(tiles_of(T, Hq / Hkv), Hkv, max_len, num_sms);
+    return splits > 1 ? states_bytes(splits, T, Hq) : 0;
+}
+
+dr_status dr_shared_prefix_attn(const void *q, int64_t q_stride, const dr_kv_cache *prefix, const int32_t *prefix_len,
+                                const dr_kv_cache *cache, const int32_t *seq_len, const dr_score_opts *opts, int B,
+                                int Hq, int Hkv, int D, int max_prefix_hint, int max_seq_len_hint, float scale,
+                                void *out, dr_dtype out_dtype, void *ws, size_t ws_bytes, int32_t *err_flag,
+                                void *stream) {
+    dr_status st = check_sizes(B, B, Hq, Hkv, D);
+    if (st != DR_OK) return st;
+    int pcap = 0, cap = 0;
+    st = check_cache(prefix, &pcap);
+    if (st != DR_OK) return st;
+    if ((cache == nullptr) != (seq_len == nullptr)) return DR_ERR_INVALID_ARG;
+    if (cache) {
+        st = check_cache(cache, &cap);
+        if (st != DR_OK) return st;
+    }
+    st = check_scores(scale, opts);
+    if (st != DR_OK) return st;
+    if (opts && (opts->prefix_len || opts->first_key)) return DR_ERR_INVALID_ARG;
+    if (!q || !prefix_len || !out || !aligned16(q) || !aligned16(out) || bad_stride(q_stride, Hq))
+        return DR_ERR_INVALID_ARG;
+    if (out_dtype != DR_BF16 && out_dtype != DR_F32) return DR_ERR_INVALID_ARG;
+    const int sms = dr::current_device_sms();
+    if (!ws || !aligned16(ws) || ws_bytes < states_bytes(1, B, Hq)) return DR_ERR_INVALID_ARG;
+    if (sms <= 0) return DR_ERR_CUDA;
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+
+    dr::PromptParams p = {};
+    p.q = static_cast<const uint16_t *>(q);
+    p.q_stride = q_stride;
+    fill_cache(p, prefix, pcap);
+    fill_scores(p, prefix, scale, opts);
+    p.kv_len = prefix_len;
+    p.own_len = seq_len;
+    p.T = B;
+    p.B = B;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.g = Hq / Hkv;
+    p.out = out;
+    p.out_f32 = out_dtype == DR_F32;
+    p.err = err_flag;
+    const int plen = max_prefix_hint > 0 && max_prefix_hint < pcap ? max_prefix_hint : pcap;
+    int splits = dr::plan_tile_splits(tiles_of(B, p.g), Hkv, plen, sms);
+    while (splits > 1 && ws_bytes < states_bytes(splits, B, Hq)) --splits;
+    set_states(p, ws, splits);
+    const cudaError_t e = dr::launch_attn_tiles(p, prefix->layout == DR_KV_PAGED,
+                                                prefix->kv_dtype == DR_KV_FP8_E4M3, splits, cs);
+    if (e != cudaSuccess) return DR_ERR_CUDA;
+
+    const dr_kv_cache *own = cache ? cache : prefix;   // no own keys: the token kernel only joins
+    fill_cache(p, own, cache ? cap : pcap);
+    fill_scores(p, own, scale, opts);
+    p.kv_len = seq_len;
+    p.own_len = nullptr;
+    p.tokens_per_row = 1;
+    p.few_max = 0x7FFFFFFF;
+    const bool paged = own->layout == DR_KV_PAGED, fp8 = own->kv_dtype == DR_KV_FP8_E4M3;
+    const int len = !cache ? 1 : max_seq_len_hint > 0 && max_seq_len_hint < cap ? max_seq_len_hint : cap;
+    return from_cuda(dr::launch_attn_tokens(p, paged, fp8, dr::plan_token_splits(B, Hkv, p.g, len, fp8, sms), cs));
+}
+
+size_t dr_shared_prefix_attn_workspace(int B, int Hq, int Hkv, int max_prefix, int num_sms) {
+    if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || max_prefix < 1 || num_sms < 1) return 0;
+    return states_bytes(dr::plan_tile_splits(tiles_of(B, Hq / Hkv), Hkv, max_prefix, num_sms), B, Hq);
 }
 
 }  // extern "C"

@@ -22,7 +22,9 @@
  *                           values of ragged new tokens (prompts, or one per row);
  *   dr_prompt_attn          attention of ragged query tokens over the cache, with
  *                           a score cap, a distance bias and causal, prefix and
- *                           document masks.
+ *                           document masks;
+ *   dr_shared_prefix_attn   single-query attention of a batch whose rows share a
+ *                           long prefix, which is read once for all of them.
  *
  * Conventions shared by every call
  *   - Every pointer argument except `stream` is a DEVICE pointer owned by the
@@ -437,6 +439,40 @@ dr_status dr_prompt_attn(const void *q, int64_t q_stride, const dr_kv_cache *cac
 
 /* Host-only: workspace bytes dr_prompt_attn wants for such a call on a GPU with num_sms SMs (0: none needed). */
 size_t dr_prompt_attn_workspace(int T, int B, int Hq, int Hkv, int max_len, int num_sms);
+
+/*
+ * dr_shared_prefix_attn -- single-query attention of B rows whose first keys
+ * are the same: row b attends the prefix's prefix_len[0] keys, then its own
+ * seq_len[b] keys.
+ *   s_j = scale * (q[b,h] . K_j), capped and biased as in dr_prompt_attn (row b's query stands at position
+ *         prefix_len[0] + seq_len[b] - 1; own key j at prefix_len[0] + j)
+ *   out[b][h] = sum_j softmax(s)_j V_j over both
+ * The prefix is read once per 128 query rows (all rows' heads on its key/value
+ * head together), not once per row; the softmax states of the two parts are
+ * merged in fp32.  Rounding as in dr_prompt_attn.  A row with no key at all
+ * outputs zeros.  For several prefixes, one call per group of rows.
+ *
+ *   q        : [B][Hq][D] bf16 (device, 16-byte aligned), rows q_stride elements apart (multiple of 8, >= Hq*D)
+ *   prefix   : cache of one row (row 0) with Hkv heads; paged: its blocks may lie in the same pool as cache's
+ *   prefix_len : [1] int32 (device), 0 <= prefix_len[0] <= the prefix's capacity (else clamped, DR_ERRF_SEQ_LEN)
+ *   cache, seq_len : the rows' own keys, B rows with Hkv heads, and [B] int32 (device), 0 <= seq_len[b] <= capacity
+ *              (else clamped, DR_ERRF_SEQ_LEN); both null: rows have no own keys (a description that a batch shares)
+ *   opts     : nullable; softcap and slopes are used, prefix_len and first_key must be null
+ *   max_prefix_hint, max_seq_len_hint : upper bounds the caller knows (<= 0: the capacities); tune the split only
+ *   out      : [B][Hq][D] in out_dtype (device, 16-byte aligned)
+ *   ws       : workspace (device, 16-byte aligned) of ws_bytes, at least dr_shared_prefix_attn_workspace with
+ *              max_prefix = 1 (DR_ERR_INVALID_ARG below); as much as it asks for the real bound spreads a prefix over
+ *              the GPU.  Its contents mean nothing before and after the call; calls that may overlap need one each
+ *   err_flag : nullable device int32 (DR_ERRF_SEQ_LEN, DR_ERRF_BLOCK_ID, DR_ERRF_TIMEOUT)
+ */
+dr_status dr_shared_prefix_attn(const void *q, int64_t q_stride, const dr_kv_cache *prefix, const int32_t *prefix_len,
+                                const dr_kv_cache *cache, const int32_t *seq_len, const dr_score_opts *opts, int B,
+                                int Hq, int Hkv, int D, int max_prefix_hint, int max_seq_len_hint, float scale,
+                                void *out, dr_dtype out_dtype, void *ws, size_t ws_bytes, int32_t *err_flag,
+                                void *stream);
+
+/* Host-only: workspace bytes of dr_shared_prefix_attn for prefixes of up to max_prefix keys on num_sms SMs. */
+size_t dr_shared_prefix_attn_workspace(int B, int Hq, int Hkv, int max_prefix, int num_sms);
 
 /*
  * dr_plan_splits -- host-only query: how many CTAs (one thread-block

@@ -94,3 +94,43 @@ def test_prompt_attn_refusals(lib, bad, status):
 @pytest.mark.parametrize("cache,status", BAD_CACHES)
 def test_prompt_attn_refuses_bad_caches(lib, cache, status):
     assert prompt(lib, cache=cache) == status
+
+
+def shared(lib, prefix=None, own=None, seq=FAKE, opts=None, q=FAKE, qs=1024, pl=FAKE, B=2, Hq=16, Hkv=16, D=64, scale=0.0,
+           out=FAKE, od=0, ws=FAKE, ws_bytes=1 << 30):
+    pc = Cache(**(prefix or GOOD))
+    oc = None if own == "none" else ctypes.byref(Cache(**(own or GOOD)))
+    o = None if opts is None else ctypes.byref(Opts(**opts))
+    return lib.dr_shared_prefix_attn(vp(q), ctypes.c_int64(qs), ctypes.byref(pc), vp(pl), oc, vp(seq), o, B, Hq, Hkv, D, 0,
+                                     0, ctypes.c_float(scale), vp(out), od, vp(ws), ctypes.c_size_t(ws_bytes), None, None)
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(B=0), 1), (dict(Hkv=3), 1), (dict(D=128), 2), (dict(q=None), 1), (dict(pl=None), 1), (dict(out=None), 1),
+    (dict(seq=None), 1), (dict(own="none"), 1), (dict(ws=None), 1), (dict(ws=FAKE + 8), 1),
+    (dict(ws_bytes=2 * 16 * 66 * 4 - 1), 1), (dict(opts=dict(first_key=FAKE)), 1), (dict(opts=dict(causal=1, prefix_len=FAKE)), 1),
+    (dict(od=3), 1), (dict(qs=8), 1), (dict(scale=float("nan")), 1), (dict(out=FAKE + 4), 1),
+])
+def test_shared_prefix_refusals(lib, bad, status):
+    assert shared(lib, **bad) == status
+
+
+@pytest.mark.parametrize("cache,status", BAD_CACHES)
+def test_shared_prefix_refuses_bad_caches(lib, cache, status):
+    assert shared(lib, prefix=cache) == status
+    assert shared(lib, own=cache) == status
+
+
+def test_workspace_sizes(lib):
+    lib.dr_prompt_attn_workspace.restype = lib.dr_shared_prefix_attn_workspace.restype = ctypes.c_size_t
+    prompt_ws, shared_ws = lib.dr_prompt_attn_workspace, lib.dr_shared_prefix_attn_workspace
+    assert prompt_ws(1, 1, 16, 16, 4096, 152) == 0            # single tokens take none
+    assert prompt_ws(128, 128, 16, 16, 4096, 152) == 0
+    assert prompt_ws(1 << 20, 4, 16, 16, 1 << 18, 152) == 0   # enough tiles to fill the GPU
+    assert prompt_ws(64, 1, 16, 16, 255, 152) == 0            # too few keys to share out
+    assert prompt_ws(64, 1, 16, 16, 65536, 152) == 19 * 64 * 16 * 66 * 4
+    assert shared_ws(128, 16, 16, 1, 152) == 128 * 16 * 66 * 4
+    assert shared_ws(128, 16, 16, 65536, 152) == 19 * 128 * 16 * 66 * 4
+    for bad in ((0, 1, 16, 16, 9, 152), (4, 1, 16, 5, 9, 152), (4, 1, 16, 16, 0, 152), (4, 1, 16, 16, 9, 0)):
+        assert prompt_ws(*bad) == 0
+    assert shared_ws(0, 16, 16, 9, 152) == 0 and shared_ws(4, 16, 5, 9, 152) == 0
