@@ -46,6 +46,7 @@ class dr_score_opts(ctypes.Structure):
 
 _vp, _i, _f = ctypes.c_void_p, ctypes.c_int, ctypes.c_float
 _i64, _sz = ctypes.c_int64, ctypes.c_size_t
+_byref = ctypes.byref
 _lib.dr_kv_append.argtypes = [ctypes.POINTER(dr_kv_cache), _vp, _vp, _vp, _i, _i, _i, _vp, _vp]
 _lib.dr_decode_self_attn.argtypes = [_vp, ctypes.POINTER(dr_kv_cache), _vp, _i, _i, _i, _i, _f, _vp, _i, _vp, _vp]
 _lib.dr_decode_cross_attn.argtypes = [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _f, _vp, _i, _vp, _vp]
@@ -292,46 +293,99 @@ def dr_lm_head_stall_test(hidden: torch.Tensor, W: torch.Tensor, C: int, logits:
     return logits
 
 
-def _token_rows(t: torch.Tensor | None, dtype: torch.dtype, name: str):
-    """(pointer, elements between tokens) of a [T, heads, D] tensor whose tokens are dense but may lie apart."""
+# The prompt-side calls below check up to fourteen tensors each, and a small call's device work takes a few
+# microseconds, so their checks are written out flat: a tensor that passes costs three attribute reads, and only one
+# that fails is looked at again to say why.
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+_current_device = torch.cuda.current_device
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _refuse(t, dev: int, dtype, shape, name: str):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device.index != dev:
+        raise ValueError(f"{name} must be on the current CUDA device {dev}, is on {t.device}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, has {tuple(t.shape)}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _arg(t, dev: int, dtype, shape, name: str):
+    """Address of a contiguous tensor of this type and shape on device dev; None for None."""
+    if t is None:
+        return None
+    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        _refuse(t, dev, dtype, shape, name)
+    return t.data_ptr()
+
+
+def _rows_arg(t, dev: int, shape, name: str):
+    """(address, elements between tokens) of a bf16 [T, heads, D] tensor whose tokens are dense but may lie apart."""
     if t is None:
         return None, 0
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+    if t.get_device() != dev or t.dtype is not _BF16 or t.shape != shape:
+        _refuse(t, dev, _BF16, shape, name)
+    s0, s1, s2 = t.stride()
+    T, heads, D = shape
+    if s2 != 1 or (s1 != D and heads > 1):
         raise ValueError(f"{name} must be [T, heads, D] with contiguous heads")
-    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2])
+    return t.data_ptr(), (s0 if T > 1 else heads * D)
 
 
-def _same_device(**tensors):
-    """Every given tensor lies on the current device, whose stream the call is enqueued on."""
-    dev = torch.cuda.current_device()
-    for name, t in tensors.items():
-        if t is not None and (not t.is_cuda or t.device.index != dev):
-            raise ValueError(f"{name} must be on the current CUDA device {dev}, is on {t.device}")
-
-
-def _sized(t: torch.Tensor | None, shape: tuple, name: str):
-    if t is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, has {tuple(t.shape)}")
-
-
-def _cache_rows(cache: KVCache, B: int, Hkv: int, D: int, name: str = "cache"):
-    """The cache's tensors agree with B rows of Hkv heads."""
-    if cache.k.dim() != 4 or cache.v.shape != cache.k.shape or cache.k.shape[1] != Hkv or cache.k.shape[3] != D:
-        raise ValueError(f"{name}.k and {name}.v must be [.., {Hkv}, .., {D}]")
-    rows = cache.block_table.shape[0] if cache.paged else cache.k.shape[0]
+def _cache_arg(cache: KVCache, dev: int, B: int, Hkv: int, D: int, name: str) -> dr_kv_cache:
+    """The C description of a cache of at least B rows of Hkv heads, all of it on device dev."""
+    k, v, table = cache.k, cache.v, cache.block_table
+    shape, dt = k.shape, k.dtype
+    if len(shape) != 4 or shape[1] != Hkv or shape[3] != D:
+        raise ValueError(f"{name}.k and {name}.v must be [.., {Hkv}, .., {D}], k is {tuple(shape)}")
+    if dt is not _BF16 and dt is not _U8:
+        raise ValueError(f"{name}.k must be {_BF16}, or {_U8} for e4m3 codes, got {dt}")
+    kp, vp = _arg(k, dev, dt, shape, name + ".k"), _arg(v, dev, dt, shape, name + ".v")
+    fp8 = DR_KV_FP8_E4M3 if dt is _U8 else DR_KV_BF16
+    if table is None:
+        rows = shape[0]
+        c = dr_kv_cache(DR_KV_CONTIGUOUS, shape[2], 0, 0, 0, fp8, kp, vp, None, cache.k_scale, cache.v_scale)
+    else:
+        tshape = table.shape
+        if len(tshape) != 2:
+            raise ValueError(f"{name}.block_table must be [B, max_blocks]")
+        rows = tshape[0]
+        c = dr_kv_cache(DR_KV_PAGED, 0, shape[2], shape[0], tshape[1], fp8, kp, vp,
+                        _arg(table, dev, _I32, tshape, name + ".block_table"), cache.k_scale, cache.v_scale)
     if rows < B:
         raise ValueError(f"{name} holds {rows} rows, the call has {B}")
+    return c
+
+
+def _stream_arg(stream, dev: int):
+    return _raw_stream(dev) if stream is None else stream.cuda_stream
+
+
+def _shape3(t, name: str):
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [T, heads, D]")
+    return t.shape
+
+
+def _out_arg(out, dev: int, shape):
+    """(address, C type) of an output of the queries' shape."""
+    dt = out.dtype
+    if dt is not _BF16 and dt is not _F32:
+        raise ValueError(f"out must be {_BF16} or {_F32}, got {dt}")
+    return _arg(out, dev, dt, shape, "out"), DR_F32 if dt is _F32 else DR_BF16
 
 
 def dr_rope_table(table: torch.Tensor, base: float = 10000.0, stream=None) -> torch.Tensor:
     """Fill table [max_pos, rot_dim] float32 with cos (first half) and sin of p * base^(-2i / rot_dim)."""
-    _same_device(table=table)
-    _check("dr_rope_table", _lib.dr_rope_table(_ptr(table, torch.float32, "table"), table.shape[0], table.shape[1],
-                                               float(base), _stream(stream)))
+    dev = _current_device()
+    if table.dim() != 2:
+        raise ValueError("table must be [max_pos, rot_dim]")
+    n, rot = table.shape
+    _check("dr_rope_table", _lib.dr_rope_table(_arg(table, dev, _F32, table.shape, "table"), n, rot, base,
+                                               _stream_arg(stream, dev)))
     return table
 
 
@@ -344,49 +398,55 @@ def dr_rope_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, row_start: 
     Row b's tokens row_start[b] .. row_start[b+1]-1 go to slots start_pos[b], start_pos[b]+1, ...; q, k, v and q_out
     may be slices of a fused projection (dense heads, any token stride that is a multiple of 8).
     """
-    T, Hkv, D = k.shape
-    B = start_pos.shape[0]
-    Hq = Hkv if q is None else q.shape[1]
-    _same_device(cache_k=cache.k, cache_v=cache.v, block_table=cache.block_table, k=k, v=v, row_start=row_start,
-                 start_pos=start_pos, q=q, q_out=q_out, table=table, pos_offset=pos_offset, err_flag=err_flag)
-    _cache_rows(cache, B, Hkv, D)
-    _sized(v, (T, Hkv, D), "v")
-    _sized(q, (T, Hq, D), "q")
-    _sized(q_out, (T, Hq, D), "q_out")
-    _sized(row_start, (B + 1,), "row_start")
-    _sized(pos_offset, (B,), "pos_offset")
-    qp, qs = _token_rows(q, torch.bfloat16, "q")
-    kp, ks = _token_rows(k, torch.bfloat16, "k")
-    vp, vs = _token_rows(v, torch.bfloat16, "v")
-    op, os_ = _token_rows(q_out, torch.bfloat16, "q_out")
-    c = cache.as_c()
-    _check("dr_rope_append",
-           _lib.dr_rope_append(ctypes.byref(c), qp, qs, kp, ks, vp, vs, op, os_,
-                               _ptr(row_start, torch.int32, "row_start"), _ptr(start_pos, torch.int32, "start_pos"),
-                               _ptr(pos_offset, torch.int32, "pos_offset"), _ptr(table, torch.float32, "table"),
-                               0 if table is None else table.shape[0], 0 if table is None else table.shape[1],
-                               int(bool(interleaved)), T, B, Hq, Hkv, D, _ptr(err_flag, torch.int32, "err_flag"),
-                               _stream(stream)))
+    dev = _current_device()
+    kshape = _shape3(k, "k")
+    T, Hkv, D = kshape
+    B = start_pos.numel()
+    if q is None:
+        Hq, qshape = Hkv, kshape
+    else:
+        qshape = _shape3(q, "q")
+        Hq = qshape[1]
+        if qshape[0] != T or qshape[2] != D:
+            raise ValueError(f"q must have shape ({T}, heads, {D}), has {tuple(qshape)}")
+    c = _cache_arg(cache, dev, B, Hkv, D, "cache")
+    kp, ks = _rows_arg(k, dev, kshape, "k")
+    vp, vs = _rows_arg(v, dev, kshape, "v")
+    qp, qs = _rows_arg(q, dev, qshape, "q")
+    op, os_ = _rows_arg(q_out, dev, qshape, "q_out")
+    if table is None:
+        tp = rope_len = rot = 0
+    else:
+        if table.dim() != 2:
+            raise ValueError("table must be [positions, rot_dim]")
+        rope_len, rot = table.shape
+        tp = _arg(table, dev, _F32, table.shape, "table")
+    st = _lib.dr_rope_append(_byref(c), qp, qs, kp, ks, vp, vs, op, os_, _arg(row_start, dev, _I32, (B + 1,), "row_start"),
+                             _arg(start_pos, dev, _I32, (B,), "start_pos"),
+                             _arg(pos_offset, dev, _I32, (B,), "pos_offset"), tp, rope_len, rot, 1 if interleaved else 0,
+                             T, B, Hq, Hkv, D, _arg(err_flag, dev, _I32, (1,), "err_flag"), _stream_arg(stream, dev))
+    if st:
+        raise DrError("dr_rope_append", st)
 
 
-def _score_opts(causal: bool, softcap: float, slopes, prefix_len, first_key) -> dr_score_opts:
-    return dr_score_opts(int(bool(causal)), float(softcap), _ptr(slopes, torch.float32, "slopes"),
-                         _ptr(prefix_len, torch.int32, "prefix_len"), _ptr(first_key, torch.int32, "first_key"))
+def _score_opts(dev: int, causal: bool, softcap: float, slopes, prefix_len, first_key, T: int, B: int, Hq: int):
+    return dr_score_opts(1 if causal else 0, softcap, _arg(slopes, dev, _F32, (Hq,), "slopes"),
+                         _arg(prefix_len, dev, _I32, (B,), "prefix_len"), _arg(first_key, dev, _I32, (T,), "first_key"))
 
 
 def _sms() -> int:
     return torch.cuda.get_device_properties(torch.cuda.current_device()).multi_processor_count
 
 
-def _out_dtype(out: torch.Tensor) -> int:
-    if out.dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError(f"out must be torch.bfloat16 or torch.float32, got {out.dtype}")
-    return DR_F32 if out.dtype == torch.float32 else DR_BF16
-
-
 def dr_prompt_attn_workspace(T: int, B: int, Hq: int, Hkv: int, max_len: int, num_sms: int | None = None) -> int:
     """Bytes of workspace dr_prompt_attn wants (0: none), for the current device unless num_sms is given."""
     return int(_lib.dr_prompt_attn_workspace(T, B, Hq, Hkv, max_len, _sms() if num_sms is None else num_sms))
+
+
+def _workspace_arg(ws, dev: int):
+    if ws is None:
+        return None, 0
+    return _arg(ws, dev, _U8, ws.shape, "workspace"), ws.numel()
 
 
 def dr_prompt_attn(q: torch.Tensor, cache: KVCache, row_start: torch.Tensor, kv_len: torch.Tensor, out: torch.Tensor,
@@ -395,27 +455,20 @@ def dr_prompt_attn(q: torch.Tensor, cache: KVCache, row_start: torch.Tensor, kv_
                    max_len_hint: int = 0, scale: float = 0.0, workspace: torch.Tensor | None = None,
                    err_flag: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Attention of ragged tokens q [T,Hq,D]: row b's tokens are the last of its kv_len[b] keys in the cache."""
-    T, Hq, D = q.shape
-    B, Hkv = kv_len.shape[0], cache.k.shape[1]
-    _same_device(q=q, cache_k=cache.k, cache_v=cache.v, block_table=cache.block_table, row_start=row_start,
-                 kv_len=kv_len, out=out, slopes=slopes, prefix_len=prefix_len, first_key=first_key,
-                 workspace=workspace, err_flag=err_flag)
-    _cache_rows(cache, B, Hkv, D)
-    _sized(out, (T, Hq, D), "out")
-    _sized(row_start, (B + 1,), "row_start")
-    _sized(slopes, (Hq,), "slopes")
-    _sized(prefix_len, (B,), "prefix_len")
-    _sized(first_key, (T,), "first_key")
-    qp, qs = _token_rows(q, torch.bfloat16, "q")
-    c = cache.as_c()
-    o = _score_opts(causal, softcap, slopes, prefix_len, first_key)
-    _check("dr_prompt_attn",
-           _lib.dr_prompt_attn(qp, qs, ctypes.byref(c), _ptr(row_start, torch.int32, "row_start"),
-                               _ptr(kv_len, torch.int32, "kv_len"), ctypes.byref(o), T, B, Hq, Hkv, D,
-                               int(max_len_hint), float(scale), _ptr(out, None, "out"), _out_dtype(out),
-                               _ptr(workspace, torch.uint8, "workspace"),
-                               0 if workspace is None else workspace.numel(), _ptr(err_flag, torch.int32, "err_flag"),
-                               _stream(stream)))
+    dev = _current_device()
+    qshape = _shape3(q, "q")
+    T, Hq, D = qshape
+    B, Hkv = kv_len.numel(), cache.k.shape[1]
+    c = _cache_arg(cache, dev, B, Hkv, D, "cache")
+    qp, qs = _rows_arg(q, dev, qshape, "q")
+    op, od = _out_arg(out, dev, qshape)
+    o = _score_opts(dev, causal, softcap, slopes, prefix_len, first_key, T, B, Hq)
+    wp, wn = _workspace_arg(workspace, dev)
+    st = _lib.dr_prompt_attn(qp, qs, _byref(c), _arg(row_start, dev, _I32, (B + 1,), "row_start"),
+                             _arg(kv_len, dev, _I32, (B,), "kv_len"), _byref(o), T, B, Hq, Hkv, D, max_len_hint, scale,
+                             op, od, wp, wn, _arg(err_flag, dev, _I32, (1,), "err_flag"), _stream_arg(stream, dev))
+    if st:
+        raise DrError("dr_prompt_attn", st)
     return out
 
 
@@ -430,31 +483,24 @@ def dr_shared_prefix_attn(q: torch.Tensor, prefix: KVCache, prefix_len: torch.Te
                           max_seq_len_hint: int = 0, scale: float = 0.0, err_flag: torch.Tensor | None = None,
                           stream=None) -> torch.Tensor:
     """One query per row, q [B,Hq,D], over the one-row cache `prefix` that all rows share and the row's own keys."""
-    B, Hq, D = q.shape
+    dev = _current_device()
+    qshape = _shape3(q, "q")
+    B, Hq, D = qshape
     Hkv = prefix.k.shape[1]
     if (cache is None) != (seq_len is None):
         raise ValueError("cache and seq_len go together")
-    _same_device(q=q, prefix_k=prefix.k, prefix_v=prefix.v, prefix_block_table=prefix.block_table,
-                 prefix_len=prefix_len, out=out, workspace=workspace, seq_len=seq_len, slopes=slopes, err_flag=err_flag)
-    _cache_rows(prefix, 1, Hkv, D, "prefix")
-    if cache is not None:
-        _same_device(cache_k=cache.k, cache_v=cache.v, block_table=cache.block_table)
-        _cache_rows(cache, B, Hkv, D)
-    _sized(out, (B, Hq, D), "out")
-    _sized(prefix_len, (1,), "prefix_len")
-    _sized(seq_len, (B,), "seq_len")
-    _sized(slopes, (Hq,), "slopes")
-    qp, qs = _token_rows(q, torch.bfloat16, "q")
-    pc = prefix.as_c()
-    c = None if cache is None else cache.as_c()
-    o = _score_opts(False, softcap, slopes, None, None)
-    _check("dr_shared_prefix_attn",
-           _lib.dr_shared_prefix_attn(qp, qs, ctypes.byref(pc), _ptr(prefix_len, torch.int32, "prefix_len"),
-                                      None if c is None else ctypes.byref(c), _ptr(seq_len, torch.int32, "seq_len"),
-                                      ctypes.byref(o), B, Hq, Hkv, D, int(max_prefix_hint), int(max_seq_len_hint),
-                                      float(scale), _ptr(out, None, "out"), _out_dtype(out),
-                                      _ptr(workspace, torch.uint8, "workspace"), workspace.numel(),
-                                      _ptr(err_flag, torch.int32, "err_flag"), _stream(stream)))
+    pc = _cache_arg(prefix, dev, 1, Hkv, D, "prefix")
+    cp = None if cache is None else _byref(_cache_arg(cache, dev, B, Hkv, D, "cache"))
+    qp, qs = _rows_arg(q, dev, qshape, "q")
+    op, od = _out_arg(out, dev, qshape)
+    o = _score_opts(dev, False, softcap, slopes, None, None, B, B, Hq)
+    wp, wn = _workspace_arg(workspace, dev)
+    st = _lib.dr_shared_prefix_attn(qp, qs, _byref(pc), _arg(prefix_len, dev, _I32, (1,), "prefix_len"), cp,
+                                    _arg(seq_len, dev, _I32, (B,), "seq_len"), _byref(o), B, Hq, Hkv, D, max_prefix_hint,
+                                    max_seq_len_hint, scale, op, od, wp, wn,
+                                    _arg(err_flag, dev, _I32, (1,), "err_flag"), _stream_arg(stream, dev))
+    if st:
+        raise DrError("dr_shared_prefix_attn", st)
     return out
 
 

@@ -11,10 +11,12 @@
 //   O^T [64 dims][8 heads] += V^T [64][16] P^T      four instructions per 8 heads
 // The order in which dimensions are summed, and which output row is which dimension, is free, so a lane loads K and V
 // straight from global memory in 16-byte pieces as the fragments that it needs (no shared memory, no transposing
-// loads): lane (r, c) = (lane / 4, lane % 4) holds dims 32i + 8c .. +7 of keys r and r + 8, and dims 8r .. 8r + 7 of
+// loads): lane (r, c) = (lane / 4, lane % 4) holds dims 16c .. 16c + 15 of keys r and r + 8, and dims 8r .. 8r + 7 of
 // keys 2c, 2c + 1, 2c + 8, 2c + 9.  P^T comes from S^T by two 8x8 register transposes.
-// Bound by memory: 4 KB of K and V per 16 keys (bf16) against about 70 warp instructions; even one head in eight
-// columns leaves the matrix instructions mostly idle.
+// Bound by memory: 4 KB of K and V per 16 keys (bf16); even one head in eight columns leaves the matrix instructions
+// mostly idle.  Measured: 128 rows of 512..4096 keys, 16 heads, 178 us (6.7 TB/s); e4m3 115 us (5.2 TB/s, where the
+// conversions count).  A ring of bulk copies in shared memory (4 tiles in flight per warp) was slower at every size:
+// what the loads wait for is the row's chain length - block id - keys, and fewer CTAs per SM hide less of it.
 //
 // e4m3 caches: the codes convert exactly to f16, and the products run in f16 with fp32 sums: q is brought to
 // [0.5, 1) times a power of two per head, which f16 holds exactly down to 2^-15 of the largest element (below that
@@ -55,27 +57,40 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
     return d;
 }
 
-// Two e4m3 codes (low 16 bits of w) -> f16x2, exact.
-__device__ __forceinline__ uint32_t codes2_f16(uint32_t w) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xFFFFu), __NV_E4M3);
-    return (uint32_t)h.x | ((uint32_t)h.y << 16);
+// Four e4m3 codes -> two f16x2, exact.
+__device__ __forceinline__ void codes4_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+}
+
+// 32-byte read-only load of data read once per call: the lanes of a row cover its 128 bytes in one request.
+__device__ __forceinline__ void ld_stream32(const void *p, uint4 &a, uint4 &b) {
+    asm("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+        : "l"(p));
 }
 
 // One 16-key tile as a lane holds it, in the cache's format.
 struct Bf16Tile {
-    uint4 k[4];   // key r: dims 8c.., 32+8c..; key r+8: the same
+    uint4 k[4];   // keys r, r+8: dims 16c ..
     uint4 v[4];   // dims 8r.. of keys 2c, 2c+1, 2c+8, 2c+9
     static constexpr size_t kRowBytes = kD * 2;
     static constexpr bool kF16 = false;
     __device__ __forceinline__ void load_k(int i, const uint8_t *row, int c) {
-        k[2 * i] = ld_stream16(row + 16 * c);
-        k[2 * i + 1] = ld_stream16(row + 64 + 16 * c);
+        ld_stream32(row + 32 * c, k[2 * i], k[2 * i + 1]);
     }
-    __device__ __forceinline__ void load_v(int i, const uint8_t *row, int r) { v[i] = ld_stream16(row + 16 * r); }
+    __device__ __forceinline__ void load_v(int i, const uint8_t *row, int r) {
+        v[i] = ld_stream16(row + 16 * r);
+    }
     __device__ __forceinline__ void zero_k(int i) { k[2 * i] = k[2 * i + 1] = make_uint4(0, 0, 0, 0); }
     __device__ __forceinline__ void zero_v(int i) { v[i] = make_uint4(0, 0, 0, 0); }
-    // word w (0..7): dims pair w of this lane's 16 dims of key r + 8*i
-    __device__ __forceinline__ uint32_t k_word(int i, int w) const { return (&k[2 * i + (w >> 2)].x)[w & 3]; }
+    // words 2 st and 2 st + 1 of this lane's 16 dims (8 pairs) of key r + 8 i
+    __device__ __forceinline__ void k_words(int i, int st, uint32_t &a, uint32_t &b) const {
+        const uint4 &w = k[2 * i + (st >> 1)];
+        a = st & 1 ? w.z : w.x;
+        b = st & 1 ? w.w : w.y;
+    }
     __device__ __forceinline__ void v_words(int i, uint32_t (&o)[4]) const {
         o[0] = v[i].x; o[1] = v[i].y; o[2] = v[i].z; o[3] = v[i].w;
     }
@@ -85,63 +100,87 @@ struct Fp8Tile {
     uint2 v[4];
     static constexpr size_t kRowBytes = kD;
     static constexpr bool kF16 = true;
-    __device__ __forceinline__ void load_k(int i, const uint8_t *row, int c) { k[i] = ld_stream16(row + 16 * c); }
-    __device__ __forceinline__ void load_v(int i, const uint8_t *row, int r) { v[i] = ld_stream8(row + 8 * r); }
+    __device__ __forceinline__ void load_k(int i, const uint8_t *row, int c) {
+        k[i] = ld_stream16(row + 16 * c);
+    }
+    __device__ __forceinline__ void load_v(int i, const uint8_t *row, int r) {
+        v[i] = ld_stream8(row + 8 * r);
+    }
     __device__ __forceinline__ void zero_k(int i) { k[i] = make_uint4(0, 0, 0, 0); }
     __device__ __forceinline__ void zero_v(int i) { v[i] = make_uint2(0, 0); }
-    __device__ __forceinline__ uint32_t k_word(int i, int w) const {
-        const uint32_t x = (&k[i].x)[w >> 1];
-        return codes2_f16((w & 1) ? x >> 16 : x);
+    __device__ __forceinline__ void k_words(int i, int st, uint32_t &a, uint32_t &b) const {
+        codes4_f16(st == 0 ? k[i].x : st == 1 ? k[i].y : st == 2 ? k[i].z : k[i].w, a, b);
     }
     __device__ __forceinline__ void v_words(int i, uint32_t (&o)[4]) const {
-        o[0] = codes2_f16(v[i].x); o[1] = codes2_f16(v[i].x >> 16);
-        o[2] = codes2_f16(v[i].y); o[3] = codes2_f16(v[i].y >> 16);
+        codes4_f16(v[i].x, o[0], o[1]);
+        codes4_f16(v[i].y, o[2], o[3]);
     }
 };
 
+// 16-key tiles of one pass of a warp, and CTAs per SM.  With groups of up to 8 heads two tiles per pass give the chain
+// scores - maximum - weights - sums two independent halves: 128 rows of 512..4096 bf16 keys, 16 heads, 186 -> 178 us
+// against one tile at 5 CTAs per SM (rows of 1..256 keys lose: 17.3 -> 20.3 us); three CTAs or five (spills) are slower.
+// Groups of 16 heads take one tile: two would spill.
+template <typename Tile, int kN>
+constexpr int tiles_per_pass() { return kN == 2 ? 1 : 2; }
+template <typename Tile, int kN>
+constexpr int ctas_per_sm() { return kN == 2 ? 3 : Tile::kF16 ? 5 : 4; }
+constexpr int kMaxSplits = 8;   // CTAs per token and kv head: one portable cluster
 constexpr float kSlack = 8.0f;   // the reference of the weights moves when a score passes it by 2^8
 
-// kN: groups of 8 query heads of one kv head.
-template <typename Tile, bool kPaged, int kN>
-__global__ void __launch_bounds__(kThreads) attn_tokens_kernel(const PromptParams p, int splits) {
+// kN: groups of 8 query heads of one kv head; kPlain: no cap, no bias.
+template <typename Tile, bool kPaged, int kN, bool kPlain>
+__global__ void __launch_bounds__(kThreads, ctas_per_sm<Tile, kN>())
+    attn_tokens_kernel(const PromptParams p, int splits) {
     constexpr int kHeads = 8 * kN;
+    constexpr int kT = tiles_per_pass<Tile, kN>();  // 16-key tiles of one pass of a warp
+    constexpr int kBlocks = kHeads * kD / kThreads;     // blocks of kThreads outputs; block x is finished by rank x % splits
     __shared__ float s_m[kWarps][kHeads], s_l[kWarps][kHeads];
     __shared__ float s_acc[kWarps][kHeads][kD];
-    __shared__ float s_M[kHeads], s_L[kHeads];
+    __shared__ float s_pm[kHeads], s_pl[kHeads];                  // states attended before: [pass][team]
+    __shared__ alignas(16) float s_pacc[kHeads][kD];
+    // what the cluster's CTAs send: every head's (m, l), and the sums of the outputs that this CTA finishes
+    __shared__ float s_M[kMaxSplits][kHeads], s_L[kMaxSplits][kHeads];
+    __shared__ float s_sent[kMaxSplits + kBlocks][kThreads];      // [x / splits][rank]
 
-    const int split = (int)blockIdx.x % splits;
-    const int item = (int)blockIdx.x / splits;
-    const int b = item / p.tokens_per_row, i0 = item - b * p.tokens_per_row;
-    const int hgroups = (p.g + kHeads - 1) / kHeads;
-    const int hk = (int)blockIdx.y / hgroups, hg = (int)blockIdx.y - hk * hgroups;
+    // splits fastest, then heads, then rows: a block of a paged cache holds all heads of its keys side by side
+    const int hgroups = (p.g + kHeads - 1) / kHeads, hys = p.Hkv * hgroups;
+    const int split = (int)(blockIdx.x % (unsigned)splits), rest = (int)(blockIdx.x / (unsigned)splits);
+    const int b = rest / hys, hy = rest - b * hys;
+    const int hk = hy / hgroups, hg = hy - hk * hgroups;
     const int h0 = hk * p.g + hg * kHeads;                  // first query head
     const int nheads = min(kHeads, p.g - hg * kHeads);      // query heads of this CTA
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
 
-    pdl_wait();
+    // After the tile kernel of the same call only the states that it leaves have to be waited for: it let this grid
+    // start once all of its CTAs had waited for the kernels before it.
+    if (!p.part_ml) pdl_wait();
     int s0 = b, n = 1;
+    int L = p.kv_len ? __ldg(p.kv_len + b) : 0;
+    const int prefix = p.prefix_len ? __ldg(p.prefix_len + b) : 0;
     if (p.row_start) {
         s0 = __ldg(p.row_start + b);
         int s1 = __ldg(p.row_start + b + 1);
-        if ((s0 < 0 || s1 < s0 || s1 > p.T) && split == 0 && blockIdx.y == 0 && i0 == 0 && threadIdx.x == 0)
+        if ((s0 < 0 || s1 < s0 || s1 > p.T || (b == 0 && s0 != 0)) && split == 0 && hy == 0 && threadIdx.x == 0)
             flag_error(p.err, DR_ERRF_ROW_START);
         s0 = min(max(s0, 0), p.T);
         n = min(max(s1, s0), p.T) - s0;
     }
-    if (n == 0 || n > p.few_max || i0 >= n) {   // nothing here, or the tile kernel's row (the same in the cluster)
-        pdl_trigger();
-        return;
-    }
-    int L = p.kv_len ? __ldg(p.kv_len + b) : 0;
+    if (n == 0 || n > p.few_max) return;   // nothing here, or the tile kernel's row (the same in the cluster)
     const int min_len = p.row_start ? n : 0;
     if (L < min_len || L > p.cap) {
-        if (split == 0 && blockIdx.y == 0 && i0 == 0 && threadIdx.x == 0 && p.kv_len) flag_error(p.err, DR_ERRF_SEQ_LEN);
+        if (split == 0 && hy == 0 && threadIdx.x == 0 && p.kv_len) flag_error(p.err, DR_ERRF_SEQ_LEN);
         L = min(max(L, 0), p.cap);
     }
-    const int prefix = p.prefix_len ? __ldg(p.prefix_len + b) : 0;
-    const uint8_t *kc = static_cast<const uint8_t *>(p.k), *vc = static_cast<const uint8_t *>(p.v);
-
-    for (int i = i0; i < n; i += p.tokens_per_row) {
+    // What is sent to another CTA's shared memory needs that CTA to have started: announced here, waited for there.
+    cg::cluster_group cluster = cg::this_cluster();
+    if (splits > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    const auto finish = [&](size_t row, int d, float ls, float o) {
+        const float res = ls == 0.f ? 0.f : o / ls;   // no key: zero; NaN scores leave NaN
+        if (p.out_f32) static_cast<float *>(p.out)[row * kD + d] = res;
+        else static_cast<uint16_t *>(p.out)[row * kD + d] = f32_to_bf16_rn(res);
+    };
+    for (int i = 0; i < n; ++i) {
         const int t = s0 + i;
         const int pos = L - n + i;
         int lo = p.first_key ? max(0, __ldg(p.first_key + t)) : 0;
@@ -151,9 +190,74 @@ __global__ void __launch_bounds__(kThreads) attn_tokens_kernel(const PromptParam
         const int per = (tiles + splits - 1) / splits;
         const int tb = tile0 + min(split * per, tiles), te = tile0 + min((split + 1) * per, tiles);
 
+        // Byte offset of key 16 * tile of this kv head; false: past the end, or a block outside the pool
+        auto tile_base = [&](int tile, size_t &base) -> bool {
+            if (tile >= te) return false;
+            if (kPaged) {
+                const int blk = __ldg(p.table + (size_t)b * p.max_blocks + tile);
+                base = ((size_t)blk * p.Hkv + hk) * kTile * Tile::kRowBytes;
+                if ((unsigned)blk < (unsigned)p.num_blocks) return true;
+                if (lane == 0) flag_error(p.err, DR_ERRF_BLOCK_ID);
+                return false;
+            }
+            base = (((size_t)b * p.Hkv + hk) * (size_t)p.cap + (size_t)tile * kTile) * Tile::kRowBytes;
+            return true;
+        };
+        const uint8_t *kc = static_cast<const uint8_t *>(p.k), *vc = static_cast<const uint8_t *>(p.v);
+        // kT tiles from `first` on: where they lie, which of them are there, and whether all of their keys are attended
+        struct Group {
+            size_t base[kT];
+            unsigned there;
+            bool whole;
+        };
+        auto locate = [&](int first, Group &g) {
+            g.there = 0;
+#pragma unroll
+            for (int y = 0; y < kT; ++y) g.there |= tile_base(first + y, g.base[y]) ? 1u << y : 0u;
+            g.whole = g.there == (1u << kT) - 1 && first * kTile >= lo && (first + kT) * kTile <= hi;
+        };
+        // Keys that are not attended are loaded as zeros
+        auto load = [&](int first, const Group &g, Tile (&x)[kT]) {
+            if (g.whole) {
+#pragma unroll
+                for (int y = 0; y < kT; ++y) {
+                    const uint8_t *kp = kc + g.base[y] + r * Tile::kRowBytes, *vp = vc + g.base[y] + 2 * c * Tile::kRowBytes;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) x[y].load_k(j, kp + 8 * j * Tile::kRowBytes, c);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) x[y].load_v(j, vp + ((j & 1) + 8 * (j >> 1)) * Tile::kRowBytes, r);
+                }
+                return;
+            }
+#pragma unroll
+            for (int y = 0; y < kT; ++y) {
+                const bool there = (g.there >> y) & 1;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int kk = r + 8 * j, key = (first + y) * kTile + kk;
+                    if (there && key >= lo && key < hi) x[y].load_k(j, kc + g.base[y] + kk * Tile::kRowBytes, c);
+                    else x[y].zero_k(j);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int kk = 2 * c + (j & 1) + 8 * (j >> 1), key = (first + y) * kTile + kk;
+                    if (there && key >= lo && key < hi) x[y].load_v(j, vc + g.base[y] + kk * Tile::kRowBytes, r);
+                    else x[y].zero_v(j);
+                }
+            }
+        };
+        // The first keys go out before the query is waited for
+        Tile x[kT];
+        Group cur, nxt;
+        int tile = tb + warp * kT;
+        if (tile < te) {
+            locate(tile, cur);
+            load(tile, cur, x);
+        }
+
         // Q^T fragments (columns = heads): lane's 16 dims of head r of each group
         uint32_t qf[kN][8];
-        float qfac[kN][2];   // e4m3: what a raw score of heads 2c, 2c+1 has to be multiplied by
+        float qfac[kN][2], qmul[kN][2];   // e4m3: what a raw score of heads 2c, 2c+1 has to be multiplied by
         float slope[kN][2];
 #pragma unroll
         for (int a = 0; a < kN; ++a) {
@@ -161,8 +265,8 @@ __global__ void __launch_bounds__(kThreads) attn_tokens_kernel(const PromptParam
             uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
             if (h < nheads) {
                 const uint16_t *src = p.q + (size_t)t * p.q_stride + (size_t)(h0 + h) * kD;
-                w0 = ld_ro16(src + (Tile::kF16 ? 16 * c : 8 * c));
-                w1 = ld_ro16(src + (Tile::kF16 ? 16 * c + 8 : 32 + 8 * c));
+                w0 = ld_ro16(src + 16 * c);
+                w1 = ld_ro16(src + 16 * c + 8);
             }
             if constexpr (Tile::kF16) {
                 float x[8], y[8];
@@ -186,6 +290,8 @@ __global__ void __launch_bounds__(kThreads) attn_tokens_kernel(const PromptParam
                 qf[a][4] = w1.x; qf[a][5] = w1.y; qf[a][6] = w1.z; qf[a][7] = w1.w;
                 qfac[a][0] = qfac[a][1] = 1.0f;
             }
+            qmul[a][0] = qfac[a][0] * p.sscale;
+            qmul[a][1] = qfac[a][1] * p.sscale;
 #pragma unroll
             for (int j = 0; j < 2; ++j)
                 slope[a][j] = p.slopes && a * 8 + 2 * c + j < nheads
@@ -203,86 +309,78 @@ __global__ void __launch_bounds__(kThreads) attn_tokens_kernel(const PromptParam
                 for (int y = 0; y < 4; ++y) acc[a][x][y] = 0.f;
         }
 
-        // Byte offset of key 16 * tile of this kv head; false: a block outside the pool.
-        auto tile_base = [&](int tile, size_t &base) -> bool {
-            if (kPaged) {
-                const int blk = __ldg(p.table + (size_t)b * p.max_blocks + tile);
-                base = ((size_t)blk * p.Hkv + hk) * kTile * Tile::kRowBytes;
-                return (unsigned)blk < (unsigned)p.num_blocks;
-            }
-            base = (((size_t)b * p.Hkv + hk) * (size_t)p.cap + (size_t)tile * kTile) * Tile::kRowBytes;
-            return true;
-        };
-        // 0: nothing to attend, 1: loaded whole, 2: loaded with keys outside [lo, hi) as zeros
-        auto load = [&](int tile, Tile &x) -> int {
-            size_t base;
-            if (!tile_base(tile, base)) {
-                if (lane == 0) flag_error(p.err, DR_ERRF_BLOCK_ID);
-                return 0;
-            }
-            const int key = tile * kTile;
-            if (key >= lo && key + kTile <= hi) {
+        while (tile < te) {
+            float s[kT][kN][4];
 #pragma unroll
-                for (int j = 0; j < 2; ++j) x.load_k(j, kc + base + (size_t)(r + 8 * j) * Tile::kRowBytes, c);
+            for (int y = 0; y < kT; ++y)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    x.load_v(j, vc + base + (size_t)(2 * c + (j & 1) + 8 * (j >> 1)) * Tile::kRowBytes, r);
-                return 1;
-            }
+                for (int a = 0; a < kN; ++a) s[y][a][0] = s[y][a][1] = s[y][a][2] = s[y][a][3] = 0.f;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int kk = r + 8 * j;
-                if (key + kk >= lo && key + kk < hi) x.load_k(j, kc + base + (size_t)kk * Tile::kRowBytes, c);
-                else x.zero_k(j);
-            }
+            for (int st = 0; st < 4; ++st)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int kk = 2 * c + (j & 1) + 8 * (j >> 1);
-                if (key + kk >= lo && key + kk < hi) x.load_v(j, vc + base + (size_t)kk * Tile::kRowBytes, r);
-                else x.zero_v(j);
-            }
-            return 2;
-        };
-        auto consume = [&](int tile, const Tile &x, bool whole) {
-            float s[kN][4];
+                for (int y = 0; y < kT; ++y) {
+                    uint32_t af[4];
+                    x[y].k_words(0, st, af[0], af[2]);
+                    x[y].k_words(1, st, af[1], af[3]);
 #pragma unroll
-            for (int a = 0; a < kN; ++a) s[a][0] = s[a][1] = s[a][2] = s[a][3] = 0.f;
-#pragma unroll
-            for (int st = 0; st < 4; ++st) {
-                const uint32_t af[4] = {x.k_word(0, 2 * st), x.k_word(1, 2 * st), x.k_word(0, 2 * st + 1),
-                                        x.k_word(1, 2 * st + 1)};
-#pragma unroll
-                for (int a = 0; a < kN; ++a) {
-                    if (Tile::kF16) mma_f16(s[a], af, qf[a][2 * st], qf[a][2 * st + 1]);
-                    else mma_bf16(s[a], af, qf[a][2 * st], qf[a][2 * st + 1]);
+                    for (int a = 0; a < kN; ++a) {
+                        if (Tile::kF16) mma_f16(s[y][a], af, qf[a][2 * st], qf[a][2 * st + 1]);
+                        else mma_bf16(s[y][a], af, qf[a][2 * st], qf[a][2 * st + 1]);
+                    }
                 }
+            // s[y][a][0..3]: (key r, head 2c), (key r, head 2c+1), (key r+8, head 2c), (key r+8, head 2c+1) of tile y
+            const int next = tile + kWarps * kT;
+            if (next < te) locate(next, nxt);
+#pragma unroll
+            for (int y = 0; y < kT; ++y)
+#pragma unroll
+                for (int a = 0; a < kN; ++a)
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) {
+                        float v = s[y][a][z];
+                        if (kPlain) {
+                            v *= Tile::kF16 ? qmul[a][z & 1] : p.sscale;
+                        } else {
+                            if (p.cap_c1 != 0.f) v = capped_score(Tile::kF16 ? v * qfac[a][z & 1] : v, p.cap_c1, p.cap_c2);
+                            else v *= Tile::kF16 ? qmul[a][z & 1] : p.sscale;
+                            if (p.slopes)
+                                v -= slope[a][z & 1] * fabsf((float)(pos - (tile + y) * kTile - r - 8 * (z >> 1)));
+                        }
+                        s[y][a][z] = v;
+                    }
+            if (!cur.whole) {
+#pragma unroll
+                for (int y = 0; y < kT; ++y)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int key = (tile + y) * kTile + r + 8 * j;
+                        if (key < lo || key >= hi || !((cur.there >> y) & 1))
+#pragma unroll
+                            for (int a = 0; a < kN; ++a) s[y][a][2 * j] = s[y][a][2 * j + 1] = -INFINITY;
+                    }
             }
-            // s[a][0..3]: (key r, head 2c), (key r, head 2c+1), (key r+8, head 2c), (key r+8, head 2c+1)
-            const int key = tile * kTile + r;
+            float mx[kN][2];
             bool grows = false;
 #pragma unroll
             for (int a = 0; a < kN; ++a)
 #pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    const float raw = Tile::kF16 ? s[a][y] * qfac[a][y & 1] : s[a][y];
-                    float v = p.cap_c1 != 0.f ? capped_score(raw, p.cap_c1, p.cap_c2) : raw * p.sscale;
-                    const int kk = key + 8 * (y >> 1);
-                    if (p.slopes) v -= slope[a][y & 1] * fabsf((float)(pos - kk));
-                    if (!whole && (kk < lo || kk >= hi)) v = -INFINITY;
-                    s[a][y] = v;
-                    grows = grows || v > m[a][y & 1] + kSlack;
+                for (int j = 0; j < 2; ++j) {
+                    mx[a][j] = fmaxf(s[0][a][j], s[0][a][j + 2]);
+#pragma unroll
+                    for (int y = 1; y < kT; ++y) mx[a][j] = fmaxf(mx[a][j], fmaxf(s[y][a][j], s[y][a][j + 2]));
+                    grows = grows || mx[a][j] > m[a][j] + kSlack;
                 }
             if (__any_sync(0xFFFFFFFFu, grows)) {
 #pragma unroll
                 for (int a = 0; a < kN; ++a)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        float mx = fmaxf(m[a][j], fmaxf(s[a][j], s[a][j + 2]));
+                        float top = fmaxf(m[a][j], mx[a][j]);
 #pragma unroll
-                        for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, off));
-                        const float corr = mx == -INFINITY ? 1.f : fast_exp2(m[a][j] - mx);
-                        m[a][j] = mx;
-                        mref[a][j] = mx == -INFINITY ? 0.f : mx;
+                        for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
+                        const float corr = top == -INFINITY ? 1.f : fast_exp2(m[a][j] - top);
+                        m[a][j] = top;
+                        mref[a][j] = top == -INFINITY ? 0.f : top;
                         l[a][j] *= corr;
 #pragma unroll
                         for (int x4 = 0; x4 < 4; ++x4) {
@@ -291,44 +389,41 @@ __global__ void __launch_bounds__(kThreads) attn_tokens_kernel(const PromptParam
                         }
                     }
             }
-            uint32_t pf[kN][2];
+            uint32_t pf[kT][kN][2];
 #pragma unroll
-            for (int a = 0; a < kN; ++a) {
-                float w[4];
-#pragma unroll
-                for (int y = 0; y < 4; ++y) w[y] = fast_exp2(s[a][y] - mref[a][y & 1]);
-                l[a][0] += w[0] + w[2];
-                l[a][1] += w[1] + w[3];
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    pf[a][j] = transpose8x8(Tile::kF16 ? pack_f16(w[2 * j], w[2 * j + 1])
-                                                       : pack_bf16(w[2 * j], w[2 * j + 1]));
-            }
-            uint32_t vw[4][4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) x.v_words(j, vw[j]);
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-                const uint32_t af[4] = {__byte_perm(vw[0][y], vw[1][y], 0x5410), __byte_perm(vw[0][y], vw[1][y], 0x7632),
-                                        __byte_perm(vw[2][y], vw[3][y], 0x5410), __byte_perm(vw[2][y], vw[3][y], 0x7632)};
+            for (int y = 0; y < kT; ++y)
 #pragma unroll
                 for (int a = 0; a < kN; ++a) {
-                    if (Tile::kF16) mma_f16(acc[a][y], af, pf[a][0], pf[a][1]);
-                    else mma_bf16(acc[a][y], af, pf[a][0], pf[a][1]);
+                    float w[4];
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) w[z] = fast_exp2(s[y][a][z] - mref[a][z & 1]);
+                    l[a][0] += w[0] + w[2];
+                    l[a][1] += w[1] + w[3];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        pf[y][a][j] = transpose8x8(Tile::kF16 ? pack_f16(w[2 * j], w[2 * j + 1])
+                                                              : pack_bf16(w[2 * j], w[2 * j + 1]));
+                }
+#pragma unroll
+            for (int y = 0; y < kT; ++y) {
+                uint32_t vw[4][4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[y].v_words(j, vw[j]);
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    const uint32_t af[4] = {
+                        __byte_perm(vw[0][z], vw[1][z], 0x5410), __byte_perm(vw[0][z], vw[1][z], 0x7632),
+                        __byte_perm(vw[2][z], vw[3][z], 0x5410), __byte_perm(vw[2][z], vw[3][z], 0x7632)};
+#pragma unroll
+                    for (int a = 0; a < kN; ++a) {
+                        if (Tile::kF16) mma_f16(acc[a][z], af, pf[y][a][0], pf[y][a][1]);
+                        else mma_bf16(acc[a][z], af, pf[y][a][0], pf[y][a][1]);
+                    }
                 }
             }
-        };
-
-        Tile cur;
-        int tile = tb + warp;
-        int got = tile < te ? load(tile, cur) : 0;
-        for (; tile < te; tile += kWarps) {
-            Tile nxt;
-            const int nt = tile + kWarps;
-            const int ngot = nt < te ? load(nt, nxt) : 0;
-            if (got) consume(tile, cur, got == 1);
+            if (next < te) load(next, nxt, x);
+            tile = next;
             cur = nxt;
-            got = ngot;
         }
 
         // The warp's states: sums over the lanes' keys, then one state per warp in shared memory
@@ -339,6 +434,7 @@ __global__ void __launch_bounds__(kThreads) attn_tokens_kernel(const PromptParam
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) l[a][j] += __shfl_xor_sync(0xFFFFFFFFu, l[a][j], off);
                 const int h = a * 8 + 2 * c + j;
+                if (h >= nheads) continue;
                 if (r == 0) {
                     s_m[warp][h] = m[a][j];
                     s_l[warp][h] = l[a][j];
@@ -349,13 +445,56 @@ __global__ void __launch_bounds__(kThreads) attn_tokens_kernel(const PromptParam
                     s_acc[warp][h][8 * r + 2 * y + 1] = acc[a][y][j + 2];
                 }
             }
+        // The states of key ranges attended before: eight teams of 16 lanes take a head and a share of this CTA's states
+        // each (four dimensions per lane), and leave one state per team and pass beside the warps'.
+        const int tnh = nheads >= 8 ? 8 : nheads > 4 ? 8 : nheads > 2 ? 4 : nheads;   // heads per pass, a power of two
+        if (p.part_ml) {
+            if (i == 0) pdl_wait();   // the tile kernel's states, and what the workspace held before
+            const int team = threadIdx.x >> 4, d4 = threadIdx.x & 15;
+            const size_t rows = (size_t)p.T * p.Hq;
+#pragma unroll
+            for (int pass = 0; pass < kN; ++pass) {
+                const int h = pass * 8 + (team & (tnh - 1));
+                float M = -INFINITY, ls = 0.f;
+                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (h < nheads) {
+                    const size_t row = (size_t)t * p.Hq + h0 + h;
+                    const int step = splits * (8 / tnh);
+                    for (int x = split + splits * (team / tnh); x < p.nparts; x += step) {
+                        const float2 ml = p.part_ml[x * rows + row];
+                        const float4 a = reinterpret_cast<const float4 *>(p.part_acc + (x * rows + row) * kD)[d4];
+                        if (ml.x == -INFINITY) continue;   // an empty share: its sums were not written
+                        const float m2 = fmaxf(M, ml.x), w0 = exp2f(M - m2), w1 = exp2f(ml.x - m2);
+                        M = m2;
+                        ls = ls * w0 + ml.y * w1;
+                        o = make_float4(o.x * w0 + a.x * w1, o.y * w0 + a.y * w1, o.z * w0 + a.z * w1, o.w * w0 + a.w * w1);
+                    }
+                }
+                const int slot = pass * 8 + team;
+                if (d4 == 0) {
+                    s_pm[slot] = M;
+                    s_pl[slot] = ls;
+                }
+                reinterpret_cast<float4 *>(s_pacc[slot])[d4] = o;
+            }
+        }
         __syncthreads();
-        // The CTA's state, in the place of warp 0's
-        for (int e = threadIdx.x; e < nheads * kD; e += kThreads) {
-            const int h = e / kD, d = e % kD;
+        // The CTA's state; of a split row it goes to the CTA that finishes the output (distributed shared memory)
+        if (splits > 1) {
+            if (i == 0) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");   // every CTA has started
+            else cluster.sync();                                                      // the last token's are read
+        }
+        const size_t row0 = (size_t)t * p.Hq + h0;
+#pragma unroll 1
+        for (int blk = 0; blk < kBlocks; ++blk) {
+            const int e = blk * kThreads + threadIdx.x, h = e / kD, d = e % kD;
+            if (h >= nheads) break;
             float M = -INFINITY;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][h]);
+            const int slot0 = (h & ~7) + (h & (tnh - 1));
+            if (p.part_ml)
+                for (int y = 0; y < 8; y += tnh) M = fmaxf(M, s_pm[slot0 + y]);
             float ls = 0.f, o = 0.f;
             if (M != -INFINITY) {
 #pragma unroll
@@ -364,75 +503,81 @@ __global__ void __launch_bounds__(kThreads) attn_tokens_kernel(const PromptParam
                     ls += wt * s_l[w][h];
                     o += wt * s_acc[w][h][d];
                 }
-            }
-            s_acc[0][h][d] = o;   // this thread alone reads and writes column (h, d)
-            if (d == 0) {
-                s_M[h] = M;
-                s_L[h] = ls;
-            }
-        }
-        cg::cluster_group cluster = cg::this_cluster();
-        if (splits > 1) cluster.sync();
-        else __syncthreads();
-        // Every CTA of the cluster finishes its share of the outputs, the CTAs' states in rank order, then the states
-        // of the key ranges attended before
-        for (int e = split * kThreads + threadIdx.x; e < nheads * kD; e += splits * kThreads) {
-            const int h = e / kD, d = e % kD;
-            float M = -INFINITY;
-            for (int x = 0; x < splits; ++x) M = fmaxf(M, splits > 1 ? *cluster.map_shared_rank(&s_M[h], x) : s_M[h]);
-            const size_t row = (size_t)t * p.Hq + h0 + h, rows = (size_t)p.T * p.Hq;
-            for (int x = 0; x < p.nparts; ++x) M = fmaxf(M, p.part_ml[x * rows + row].x);
-            float ls = 0.f, o = 0.f;
-            if (M != -INFINITY) {
-                for (int x = 0; x < splits; ++x) {
-                    const float wt = exp2f((splits > 1 ? *cluster.map_shared_rank(&s_M[h], x) : s_M[h]) - M);
-                    ls += wt * (splits > 1 ? *cluster.map_shared_rank(&s_L[h], x) : s_L[h]);
-                    o += wt * (splits > 1 ? *cluster.map_shared_rank(&s_acc[0][h][d], x) : s_acc[0][h][d]);
-                }
                 o *= p.out_scale;
-                for (int x = 0; x < p.nparts; ++x) {
-                    const float2 ml = p.part_ml[x * rows + row];
-                    if (ml.x == -INFINITY) continue;   // an empty share
-                    const float wt = exp2f(ml.x - M);
-                    ls += wt * ml.y;
-                    o += wt * p.part_acc[(x * rows + row) * kD + d];
-                }
+                if (p.part_ml)
+                    for (int y = 0; y < 8; y += tnh) {
+                        const float wt = exp2f(s_pm[slot0 + y] - M);
+                        ls += wt * s_pl[slot0 + y];
+                        o += wt * s_pacc[slot0 + y][d];
+                    }
             }
-            // a sum of weights that is not zero; NaN scores leave NaN
-            const float res = ls == 0.f ? 0.f : o / ls;
-            if (p.out_f32) static_cast<float *>(p.out)[row * kD + d] = res;
-            else static_cast<uint16_t *>(p.out)[row * kD + d] = f32_to_bf16_rn(res);
+            if (splits == 1) {
+                finish(row0 + h, d, ls, o);
+            } else {
+                const int owner = blk % splits;
+                *cluster.map_shared_rank(&s_sent[blk / splits * splits + split][threadIdx.x], owner) = o;
+                if (d == 0)
+                    for (int y = 0; y < min(splits, kBlocks); ++y) {
+                        *cluster.map_shared_rank(&s_M[split][h], y) = M;
+                        *cluster.map_shared_rank(&s_L[split][h], y) = ls;
+                    }
+            }
         }
-        if (splits > 1) cluster.sync();   // the states stay until every CTA has read them
-        else __syncthreads();
+        if (splits > 1) {
+            cluster.sync();   // nothing reads another CTA's memory after it
+            // This CTA's share of the outputs, the CTAs' states in rank order
+#pragma unroll 1
+            for (int blk = 0; blk < kBlocks; ++blk) {
+                const int e = blk * kThreads + threadIdx.x, h = e / kD, d = e % kD;
+                if (blk % splits != split || h >= nheads) continue;
+                float M = -INFINITY;
+                for (int y = 0; y < splits; ++y) M = fmaxf(M, s_M[y][h]);
+                float ls = 0.f, o = 0.f;
+                if (M != -INFINITY)
+                    for (int y = 0; y < splits; ++y) {
+                        const float wt = exp2f(s_M[y][h] - M);
+                        ls += wt * s_L[y][h];
+                        o += wt * s_sent[blk / splits * splits + y][threadIdx.x];
+                    }
+                finish(row0 + h, d, ls, o);
+            }
+        }
+        __syncthreads();
     }
     pdl_trigger();
 }
 
 }  // namespace
 
-// CTAs (one cluster) that share a token's keys: enough to give every SM a few CTAs, each at least 64 keys.
+// CTAs (one cluster) that share a token's keys: at most 512 KiB of K and V each, and as many as fill the GPU in one wave
+// (a few CTAs more than fit cost a whole second wave: 8 rows of 16 heads, 64..512 keys, 9.1 us with 5 CTAs per row and
+// head, 5.5 with 4), with at least 64 keys each.
 int plan_token_splits(long long items, int Hkv, int g, int max_len, bool fp8, int sms) {
-    const long long rows = items * Hkv * ((g + 15) / 16);
+    const int kn = g > 8 ? 2 : 1;
+    const long long rows = items * Hkv * ((g + 8 * kn - 1) / (8 * kn));
     const long long key_bytes = 2LL * kD * (fp8 ? 1 : 2);
-    long long s = ((long long)max_len * key_bytes + 256 * 1024 - 1) / (256 * 1024);
-    const long long fill = (4LL * sms + rows - 1) / rows;
+    long long s = ((long long)max_len * key_bytes + 512 * 1024 - 1) / (512 * 1024);
+    const int slots = kn == 2 ? ctas_per_sm<Bf16Tile, 2>() : fp8 ? ctas_per_sm<Fp8Tile, 1>() : ctas_per_sm<Bf16Tile, 1>();
+    const long long fill = (long long)slots * sms / rows;
     if (fill > s) s = fill;
     const long long by_keys = ((long long)max_len + 63) / 64;
     if (s > by_keys) s = by_keys;
-    if (s > 8) s = 8;
+    if (s > kMaxSplits) s = kMaxSplits;
     return s < 1 ? 1 : (int)s;
 }
 
 cudaError_t launch_attn_tokens(const PromptParams &p, bool paged, bool fp8, int splits, cudaStream_t stream) {
     const int kn = p.g > 8 ? 2 : 1;
     const unsigned hgroups = (unsigned)((p.g + 8 * kn - 1) / (8 * kn));
-    const dim3 grid((unsigned)((long long)p.B * p.tokens_per_row * splits), (unsigned)p.Hkv * hgroups);
+    const dim3 grid((unsigned)((long long)p.B * p.Hkv * hgroups * splits));
     void (*kern)(PromptParams, int);
-#define DR_PICK(TILE, P) (kn == 2 ? attn_tokens_kernel<TILE, P, 2> : attn_tokens_kernel<TILE, P, 1>)
+    const bool plain = p.cap_c1 == 0.f && !p.slopes;
+#define DR_PICK2(TILE, P, N) (plain ? attn_tokens_kernel<TILE, P, N, true> : attn_tokens_kernel<TILE, P, N, false>)
+#define DR_PICK(TILE, P) (kn == 2 ? DR_PICK2(TILE, P, 2) : DR_PICK2(TILE, P, 1))
     if (fp8) kern = paged ? DR_PICK(Fp8Tile, true) : DR_PICK(Fp8Tile, false);
     else kern = paged ? DR_PICK(Bf16Tile, true) : DR_PICK(Bf16Tile, false);
 #undef DR_PICK
+#undef DR_PICK2
     return launch_kernel(kern, grid, dim3(kThreads), 0, stream, (unsigned)splits, p, splits);
 }
 

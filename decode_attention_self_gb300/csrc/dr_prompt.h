@@ -46,8 +46,8 @@ struct PromptParams {
     void *out;                          // [T][Hq][64]
     int32_t out_f32;
     int32_t *err;
-    // token kernel: items per row, and the most tokens a row may have to be taken by it (more: the tile kernel's)
-    int32_t tokens_per_row, few_max;
+    // the most tokens a row may have to be taken by the token kernel (more: the tile kernel's)
+    int32_t few_max;
     // tile kernel: queries of a shared prefix stand own_len[t] keys past its end (null: at their row's last keys)
     const int32_t *own_len;
     // softmax states of key ranges attended before: [nparts][rows = T*Hq] (m, l) and [nparts][rows][64]; null: none

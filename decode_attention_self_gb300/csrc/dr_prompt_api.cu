@@ -191,7 +191,6 @@ dr_status dr_prompt_attn(const void *q, int64_t q_stride, const dr_kv_cache *cac
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     // Rows of one token go to the token kernel, longer ones to the tile kernel (it reads a row's keys once for all
     // its tokens).  The host knows only T and B: one launch when that settles it, else both.
-    p.tokens_per_row = 1;
     p.few_max = 1;
     const bool few = B > 1 || T == 1, many = T > B;
     if (!many) p.few_max = 0x7FFFFFFF;
@@ -271,7 +270,6 @@ dr_status dr_shared_prefix_attn(const void *q, int64_t q_stride, const dr_kv_cac
     fill_scores(p, own, scale, opts);
     p.kv_len = seq_len;
     p.own_len = nullptr;
-    p.tokens_per_row = 1;
     p.few_max = 0x7FFFFFFF;
     const bool paged = own->layout == DR_KV_PAGED, fp8 = own->kv_dtype == DR_KV_FP8_E4M3;
     const int len = !cache ? 1 : max_seq_len_hint > 0 && max_seq_len_hint < cap ? max_seq_len_hint : cap;
