@@ -122,9 +122,9 @@ struct Fp8Tile {
 // against one tile at 5 CTAs per SM (rows of 1..256 keys lose: 17.3 -> 20.3 us); three CTAs or five (spills) are slower.
 // Groups of 16 heads take one tile: two would spill.
 template <typename Tile, int kN>
-constexpr int tiles_per_pass() { return kN == 2 ? 1 : 2; }
+__host__ __device__ constexpr int tiles_per_pass() { return kN == 2 ? 1 : 2; }
 template <typename Tile, int kN>
-constexpr int ctas_per_sm() { return kN == 2 ? 3 : Tile::kF16 ? 5 : 4; }
+__host__ __device__ constexpr int ctas_per_sm() { return kN == 2 ? 3 : Tile::kF16 ? 5 : 4; }
 constexpr int kMaxSplits = 8;   // CTAs per token and kv head: one portable cluster
 constexpr float kSlack = 8.0f;   // the reference of the weights moves when a score passes it by 2^8
 
