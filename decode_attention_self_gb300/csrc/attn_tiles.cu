@@ -82,6 +82,12 @@ __device__ __forceinline__ bool nonfinite16(uint32_t w, uint32_t exp_mask) {
     return (w & exp_mask) == exp_mask || ((w >> 16) & exp_mask) == exp_mask;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 // Keys [lo, hi) that query i of a row of n queries and L keys sees, and its position.
 __device__ __forceinline__ void visible(const PromptParams &p, int t, int i, int n, int L, int prefix, int &lo, int &hi,
                                         int &pos) {
@@ -547,15 +553,13 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
                 for (int c = 0; c < kKeys; ++c)
                     if (c < a || c >= e || !((bits >> (c / kBlockKeys)) & 1)) s[c] = -INFINITY;
             }
-            float mx0 = s[0], mx1 = s[1], mx2 = s[2], mx3 = s[3];
+            float mx0 = s[0], mx1 = s[1];
 #pragma unroll
-            for (int c = 4; c < kKeys; c += 4) {
-                mx0 = fmaxf(mx0, s[c]);
-                mx1 = fmaxf(mx1, s[c + 1]);
-                mx2 = fmaxf(mx2, s[c + 2]);
-                mx3 = fmaxf(mx3, s[c + 3]);
+            for (int c = 2; c + 3 < kKeys; c += 4) {
+                mx0 = max3(mx0, s[c], s[c + 1]);
+                mx1 = max3(mx1, s[c + 2], s[c + 3]);
             }
-            const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * mul;
+            const float mx = fmaxf(max3(mx0, s[kKeys - 2], s[kKeys - 1]), mx1) * mul;
             float corr = 1.0f;
             if (mx > m + kSlack) {   // also the first visible key (m = -inf)
                 corr = fast_exp2(m - mx);

@@ -128,6 +128,18 @@ __host__ __device__ constexpr int ctas_per_sm() { return kN == 2 ? 3 : Tile::kF1
 constexpr int kMaxSplits = 8;   // CTAs per token and kv head: one portable cluster
 constexpr float kSlack = 8.0f;   // the reference of the weights moves when a score passes it by 2^8
 
+template <int kN>
+struct Shared {
+    static constexpr int kHeads = 8 * kN, kBlocks = kHeads * kD / kThreads;
+    float m[kWarps][kHeads], l[kWarps][kHeads];   // the warps' states
+    float acc[kWarps][kHeads][kD];
+    float pm[kHeads], pl[kHeads];                 // states attended before: [pass][team]
+    alignas(16) float pacc[kHeads][kD];
+    // what the cluster's CTAs send: every head's (m, l), and the sums of the outputs that this CTA finishes
+    float M[kMaxSplits][kHeads], L[kMaxSplits][kHeads];
+    float sent[kMaxSplits + kBlocks][kThreads];   // [block / splits][rank]
+};
+
 // kN: groups of 8 query heads of one kv head; kPlain: no cap, no bias.
 template <typename Tile, bool kPaged, int kN, bool kPlain>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm<Tile, kN>())
@@ -135,13 +147,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<Tile, kN>())
     constexpr int kHeads = 8 * kN;
     constexpr int kT = tiles_per_pass<Tile, kN>();  // 16-key tiles of one pass of a warp
     constexpr int kBlocks = kHeads * kD / kThreads;     // blocks of kThreads outputs; block x is finished by rank x % splits
-    __shared__ float s_m[kWarps][kHeads], s_l[kWarps][kHeads];
-    __shared__ float s_acc[kWarps][kHeads][kD];
-    __shared__ float s_pm[kHeads], s_pl[kHeads];                  // states attended before: [pass][team]
-    __shared__ alignas(16) float s_pacc[kHeads][kD];
-    // what the cluster's CTAs send: every head's (m, l), and the sums of the outputs that this CTA finishes
-    __shared__ float s_M[kMaxSplits][kHeads], s_L[kMaxSplits][kHeads];
-    __shared__ float s_sent[kMaxSplits + kBlocks][kThreads];      // [x / splits][rank]
+    __shared__ Shared<kN> sh;
+    auto &s_m = sh.m, &s_l = sh.l;
+    auto &s_acc = sh.acc;
+    auto &s_pm = sh.pm, &s_pl = sh.pl;
+    auto &s_pacc = sh.pacc;
+    auto &s_M = sh.M, &s_L = sh.L;
+    auto &s_sent = sh.sent;
 
     // splits fastest, then heads, then rows: a block of a paged cache holds all heads of its keys side by side
     const int hgroups = (p.g + kHeads - 1) / kHeads, hys = p.Hkv * hgroups;
@@ -578,6 +590,14 @@ cudaError_t launch_attn_tokens(const PromptParams &p, bool paged, bool fp8, int 
     else kern = paged ? DR_PICK(Bf16Tile, true) : DR_PICK(Bf16Tile, false);
 #undef DR_PICK
 #undef DR_PICK2
+    // The loads in flight live in L1 (128 KB per SM at four CTAs): ask for no more shared memory than the CTAs need.
+    // Left to itself an SM keeps the split of the kernel before, and behind the tile kernel, which takes all of it,
+    // 128 rows of 64..2048 own keys took 125 us instead of 97.
+    const size_t each = (kn == 2 ? sizeof(Shared<2>) : sizeof(Shared<1>)) + 1024;
+    const int ctas = kn == 2 ? ctas_per_sm<Bf16Tile, 2>() : fp8 ? ctas_per_sm<Fp8Tile, 1>() : ctas_per_sm<Bf16Tile, 1>();
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                               (int)((ctas * each * 100 + 228 * 1024 - 1) / (228 * 1024)));
+    if (e != cudaSuccess) return e;
     return launch_kernel(kern, grid, dim3(kThreads), 0, stream, (unsigned)splits, p, splits);
 }
 
