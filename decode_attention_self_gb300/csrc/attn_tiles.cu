@@ -82,6 +82,14 @@ __device__ __forceinline__ bool nonfinite16(uint32_t w, uint32_t exp_mask) {
     return (w & exp_mask) == exp_mask || ((w >> 16) & exp_mask) == exp_mask;
 }
 
+// Zeroes the NaN codes (0x7F, 0xFF) among four e4m3 codes; whether there was one.
+__device__ __forceinline__ bool zero_nan_codes(uint32_t &w) {
+    const uint32_t t = ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;   // bit 7 of the bytes that hold one
+    if (t == 0) return false;
+    w &= ~((t >> 7) * 0xFFu);
+    return true;
+}
+
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -103,7 +111,7 @@ __device__ __forceinline__ void visible(const PromptParams &p, int t, int i, int
     if (lo >= hi) lo = hi = 0;
 }
 
-template <int kWG, bool kFp8, bool kPaged>
+template <int kWG, bool kFp8, bool kPaged, bool kPlain>
 __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>::kCtasPerSm)
     attn_tiles_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                       const TileParams tp) {
@@ -144,18 +152,19 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
     pdl_wait();
     pdl_trigger();
 
-    // Which tile of which row: tiles of the rows in turn, a row's last (longest, when causal) tile first
-    const int split = (int)blockIdx.x % tp.splits;
+    // Which tile of which row: tiles of the rows in turn, a row's last (longest, when causal) tile of all heads first
+    const int hk = (int)(blockIdx.x % (unsigned)p.Hkv), unit = (int)(blockIdx.x / (unsigned)p.Hkv);
+    const int split = unit % tp.splits;
     const int rows_per_cta = kRows * kWG;
     if (warp == 0) {
-        int want = (int)blockIdx.x / tp.splits;
+        int want = unit / tp.splits;
         int b = -1, s0 = 0, n = 0;
         if (!p.row_start) {
             const int tiles = (int)(((long long)p.T * p.g + rows_per_cta - 1) / rows_per_cta);
             if (want < tiles) b = 0;
             n = p.T;
         } else {
-            const bool checks = blockIdx.x == 0 && blockIdx.y == 0;   // this CTA looks every row over
+            const bool checks = blockIdx.x == 0;   // this CTA looks every row over
             for (int base = 0; base < p.B && (b < 0 || checks); base += 32) {
                 int a = 0, e = 0;
                 if (base + lane < p.B) {
@@ -218,7 +227,7 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
         fence_before();
     }
-    const int b = ctl.b, L = ctl.L, n = ctl.n, hk = blockIdx.y;
+    const int b = ctl.b, L = ctl.L, n = ctl.n;
 
     // Query rows: each softmax thread loads its own into the swizzled tile
     const int wg = warp >> 2, row = threadIdx.x & 127;
@@ -312,26 +321,31 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
         if (warp == kProducer) {
             const int kv_row = kPaged ? 0 : b * p.Hkv + hk;
-            // lane i < 8: block i of the tile; z of a missing block is out of range
-            auto block_z = [&](int j, bool &there) -> int {
+            // Block ids of four tiles at a time, one per lane, loaded four tiles ahead (a load per tile, waited for in
+            // turn, took longer than the tile's arithmetic): lane 8 y + x has block x of tile y of the group.  z of a
+            // block that is not there is out of range.
+            const auto group_ids = [&](int j) -> int {   // tiles j .. j + 3
                 const int key = kbase + j * kKeys + lane * kBlockKeys;
-                int blk = -1;
-                if (lane < 8 && key < uhi) {
-                    blk = __ldg(p.table + (size_t)b * p.max_blocks + key / kBlockKeys);
-                    if ((unsigned)blk >= (unsigned)p.num_blocks) {
-                        flag_error(p.err, DR_ERRF_BLOCK_ID);
-                        blk = -1;
-                    }
-                }
-                there = blk >= 0;
-                return blk >= 0 ? blk * p.Hkv + hk : p.num_blocks * p.Hkv;
+                return j < ce && key < uhi ? __ldg(p.table + (size_t)b * p.max_blocks + key / kBlockKeys) : -1;
             };
-            bool there = true;
-            int z = 0;
-            if (kPaged && cb < ce) z = block_z(cb, there);
+            int ids = 0, ids_next = 0;
+            if (kPaged) ids_next = group_ids(cb);
             for (int j = cb, i = 0, s = 0, round = 0; j < ce; ++j, ++i) {
                 if (round > 0 && !__all_sync(0xFFFFFFFFu, mbar_wait(&ctl.k_empty[s], (round - 1) & 1, gave_up))) break;
-                const unsigned bits = kPaged ? __ballot_sync(0xFFFFFFFFu, there) & 0xFFu : 0xFFu;
+                unsigned bits = 0xFFu;
+                int z = 0;
+                if (kPaged) {
+                    if ((i & 3) == 0) {
+                        ids = ids_next;
+                        ids_next = group_ids(j + 4);
+                    }
+                    const int blk = __shfl_sync(0xFFFFFFFFu, ids, (i & 3) * 8 + (lane & 7));
+                    const bool there = (unsigned)blk < (unsigned)p.num_blocks;
+                    const bool wanted = kbase + j * kKeys + (lane & 7) * kBlockKeys < uhi;
+                    if (wanted && !there && lane < 8) flag_error(p.err, DR_ERRF_BLOCK_ID);
+                    bits = __ballot_sync(0xFFFFFFFFu, there) & 0xFFu;
+                    z = there ? blk * p.Hkv + hk : p.num_blocks * p.Hkv;
+                }
                 uint8_t *kd = smem + (kFp8 ? C::kRawK + s * C::kTmaBytes : C::kK + s * kTileBytes);
                 uint8_t *vd = smem + (kFp8 ? C::kRawV + s * C::kTmaBytes : C::kV + s * kTileBytes);
                 if (lane == 0) {
@@ -349,7 +363,6 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
                 __syncwarp();
                 if (kPaged) {
                     if (lane < 8) tma_load_3d(smem_u32(vd + lane * (C::kTmaBytes / 8)), &map_v, 0, 0, z, &ctl.v_full[s]);
-                    if (j + 1 < ce) z = block_z(j + 1, there);
                 } else if (lane == 0) {
                     tma_load_3d(smem_u32(vd), &map_v, 0, kbase + j * kKeys, kv_row, &ctl.v_full[s]);
                 }
@@ -359,56 +372,66 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
                 }
             }
         } else if (warp == kMmaWarp) {
-            if (lane == 0) {
-                constexpr uint32_t id_s = instr_desc(kRows, kKeys, kFp8, false);
-                constexpr uint32_t id_o = instr_desc(kRows, kD, kFp8, true);
-                uint64_t *k_in = kFp8 ? ctl.k_ready : ctl.k_full, *k_out = kFp8 ? ctl.kc_empty : ctl.k_empty;
-                uint64_t *v_out = kFp8 ? ctl.vc_empty : ctl.v_empty;
-                bool ok = true;
-                // step j: S of tile j, then O of tile j - 1
-                int s = 0, round = 0, sp = 0, roundp = 0;
-                for (int j = cb; j <= ce && cb < ce && ok; ++j) {
-                    if (j < ce) ok = mbar_wait(&k_in[s], round & 1, gave_up);
+            // The whole warp waits, one lane issues: descriptors stay warp-uniform (computed by one lane alone, each MMA
+            // took over 100 cycles to issue; the tensor pipe takes one in 45 to 65).
+            constexpr uint32_t id_s = instr_desc(kRows, kKeys, kFp8, false);
+            constexpr uint32_t id_o = instr_desc(kRows, kD, kFp8, true);
+            uint64_t *k_in = kFp8 ? ctl.k_ready : ctl.k_full, *k_out = kFp8 ? ctl.kc_empty : ctl.k_empty;
+            uint64_t *v_out = kFp8 ? ctl.vc_empty : ctl.v_empty;
+            const uint64_t dq = smem_desc(smem_u32(smem + C::kQ)), dk = smem_desc(smem_u32(smem + C::kK)),
+                           dv = smem_desc(smem_u32(smem + C::kV));
+            const bool leader = elect_one();
+            const auto wait = [&](uint64_t *bar, uint32_t parity) {
+                return (bool)__all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, gave_up));
+            };
+            bool ok = true;
+            // Step j: S of tile j, then O of tile j - 1
+            int s = 0, round = 0, sp = 0, roundp = 0;
+            for (int j = cb; j <= ce && cb < ce && ok; ++j) {
+                if (j < ce) ok = wait(&k_in[s], round & 1);
 #pragma unroll
-                    for (int w = 0; w < kWG; ++w) {
-                        if (ok && j < ce && j >= jb[w] && j < je[w]) {
-                            if (j > jb[w]) ok = mbar_wait(&ctl.s_free[w], (j - jb[w] - 1) & 1, gave_up);
-                            if (ok) {
-                                fence_after();
-                                const uint32_t qa = smem_u32(smem + C::kQ + w * kTileBytes);
-                                const uint32_t ka = smem_u32(smem + C::kK + s * kTileBytes);
+                for (int w = 0; w < kWG; ++w) {
+                    if (ok && j < ce && j >= jb[w] && j < je[w]) {
+                        if (j > jb[w]) ok = wait(&ctl.s_free[w], (j - jb[w] - 1) & 1);
+                        if (ok) {
+                            fence_after();
+                            const uint64_t qa = desc_at(dq, w * kTileBytes), ka = desc_at(dk, s * kTileBytes);
+                            if (leader) {
 #pragma unroll
                                 for (int k = 0; k < kD / 16; ++k)
-                                    mma_ss(tmem + 256 * w, smem_desc(qa + 32 * k), smem_desc(ka + 32 * k), id_s, k != 0);
+                                    mma_ss(tmem + 256 * w, desc_at(qa, 32 * k), desc_at(ka, 32 * k), id_s, k != 0);
                                 commit(&ctl.s_full[w]);
                             }
                         }
-                        // (the last stages are not used again: no arrival is left under way when the CTA ends)
-                        if (w == kWG - 1 && ok && j + C::kMma < ce) commit(&k_out[s]);
-                        const int i = j - 1;
-                        if (ok && i >= cb && w == 0) ok = mbar_wait(&ctl.v_ready[sp], roundp & 1, gave_up);
-                        if (ok && i >= jb[w] && i < je[w]) {
-                            ok = mbar_wait(&ctl.p_full[w], (i - jb[w]) & 1, gave_up);
-                            if (ok) {
-                                fence_after();
-                                const uint32_t va = smem_u32(smem + C::kV + sp * kTileBytes);
+                    }
+                    // (the last stages are not used again: no arrival is left under way when the CTA ends)
+                    if (w == kWG - 1 && ok && j + C::kMma < ce && leader) commit(&k_out[s]);
+                    const int i = j - 1;
+                    if (ok && i >= cb && w == 0) ok = wait(&ctl.v_ready[sp], roundp & 1);
+                    if (ok && i >= jb[w] && i < je[w]) {
+                        ok = wait(&ctl.p_full[w], (i - jb[w]) & 1);
+                        if (ok) {
+                            fence_after();
+                            const uint64_t va = desc_at(dv, sp * kTileBytes);
+                            if (leader) {
 #pragma unroll
                                 for (int k = 0; k < kKeys / 16; ++k)
-                                    mma_ts(tmem + 256 * w + 128, tmem + 256 * w + 192 + 8 * k, smem_desc(va + 2048 * k),
-                                           id_o, i > jb[w] || k != 0);
+                                    mma_ts(tmem + 256 * w + 128, tmem + 256 * w + 192 + 8 * k, desc_at(va, 2048 * k), id_o,
+                                           i > jb[w] || k != 0);
                                 commit(&ctl.o_done[w]);
                             }
                         }
-                        if (w == kWG - 1 && ok && i >= cb && i + C::kMma < ce) commit(&v_out[sp]);
                     }
-                    if (j > cb && ++sp == C::kMma) {
-                        sp = 0;
-                        ++roundp;
-                    }
-                    if (++s == C::kMma) {
-                        s = 0;
-                        ++round;
-                    }
+                    if (w == kWG - 1 && ok && i >= cb && i + C::kMma < ce && leader) commit(&v_out[sp]);
+                }
+                __syncwarp();
+                if (j > cb && ++sp == C::kMma) {
+                    sp = 0;
+                    ++roundp;
+                }
+                if (++s == C::kMma) {
+                    s = 0;
+                    ++round;
                 }
             }
         } else {
@@ -431,31 +454,31 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
                         const uint8_t *raw = smem + (kv ? C::kRawV : C::kRawK) + s * C::kTmaBytes;
                         uint8_t *dst = smem + (kv ? C::kV : C::kK) + sc * kTileBytes;
                         bool bad = false;
-                        for (int x = ht; x < kKeys * 4; x += kHt) {
-                            const int r = x >> 2, c = x & 3;
-                            uint4 w = *reinterpret_cast<const uint4 *>(raw + r * 64 + c * 16);
-                            if (kv && mixed) {   // NaN codes (0x7F, 0xFF) of values
-                                uint32_t *ws = &w.x;
+                        constexpr int kChunks = kKeys * 4 / kHt;   // 16 codes each, all loaded before the first is used
+                        uint4 w[kChunks];
 #pragma unroll
-                                for (int y = 0; y < 4; ++y)
+                        for (int e = 0; e < kChunks; ++e) w[e] = *reinterpret_cast<const uint4 *>(raw + (ht + e * kHt) * 16);
+                        if (kv && mixed) {   // NaN codes (0x7F, 0xFF) of values
 #pragma unroll
-                                    for (int z = 0; z < 4; ++z)
-                                        if (((ws[y] >> (8 * z)) & 0x7F) == 0x7F) {
-                                            ws[y] &= ~(0xFFu << (8 * z));
-                                            bad = bad || (key0 + r >= ulo && key0 + r < uhi);
-                                        }
+                            for (int e = 0; e < kChunks; ++e) {
+                                const int key = key0 + ((ht + e * kHt) >> 2);
+                                bool hit = zero_nan_codes(w[e].x);
+                                hit |= zero_nan_codes(w[e].y);
+                                hit |= zero_nan_codes(w[e].z);
+                                hit |= zero_nan_codes(w[e].w);
+                                bad = bad || (hit && key >= ulo && key < uhi);
                             }
-                            uint32_t h[8];
-                            const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+                        }
 #pragma unroll
-                            for (int y = 0; y < 4; ++y) {
-                                const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(in[y] & 0xFFFFu), __NV_E4M3);
-                                const __half2_raw e = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(in[y] >> 16), __NV_E4M3);
-                                h[2 * y] = (uint32_t)a.x | ((uint32_t)a.y << 16);
-                                h[2 * y + 1] = (uint32_t)e.x | ((uint32_t)e.y << 16);
-                            }
-                            *reinterpret_cast<uint4 *>(dst + swz(r, 2 * c)) = make_uint4(h[0], h[1], h[2], h[3]);
-                            *reinterpret_cast<uint4 *>(dst + swz(r, 2 * c + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
+                        for (int e = 0; e < kChunks; ++e) {
+                            const int r = (ht + e * kHt) >> 2, c = (ht + e * kHt) & 3;
+                            uint4 a, d;
+                            codes4_f16(w[e].x, a.x, a.y);
+                            codes4_f16(w[e].y, a.z, a.w);
+                            codes4_f16(w[e].z, d.x, d.y);
+                            codes4_f16(w[e].w, d.z, d.w);
+                            *reinterpret_cast<uint4 *>(dst + swz(r, 2 * c)) = a;
+                            *reinterpret_cast<uint4 *>(dst + swz(r, 2 * c + 1)) = d;
                         }
                         if (bad) ctl.nonfinite = 1;
                         fence_proxy_async();
@@ -476,19 +499,25 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
                     if (mixed) {
                         uint8_t *vt = smem + C::kV + s * kTileBytes;
                         bool bad = false;
-                        for (int x = ht; x < kKeys * 8; x += kHt) {
-                            uint4 w = *reinterpret_cast<const uint4 *>(vt + x * 16);
-                            if (nonfinite16(w.x, 0x7F80u) || nonfinite16(w.y, 0x7F80u) || nonfinite16(w.z, 0x7F80u) ||
-                                nonfinite16(w.w, 0x7F80u)) {
-                                uint32_t *ws = &w.x;
+#pragma unroll 1
+                        for (int x0 = ht; x0 < kKeys * 8; x0 += 8 * kHt) {   // eight chunks of 8 values in flight
+                            uint4 w[8];
 #pragma unroll
-                                for (int y = 0; y < 4; ++y) {
-                                    if ((ws[y] & 0x7F80u) == 0x7F80u) ws[y] &= 0xFFFF0000u;
-                                    if ((ws[y] & 0x7F800000u) == 0x7F800000u) ws[y] &= 0x0000FFFFu;
+                            for (int e = 0; e < 8; ++e) w[e] = *reinterpret_cast<const uint4 *>(vt + (x0 + e * kHt) * 16);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                if (nonfinite16(w[e].x, 0x7F80u) || nonfinite16(w[e].y, 0x7F80u) ||
+                                    nonfinite16(w[e].z, 0x7F80u) || nonfinite16(w[e].w, 0x7F80u)) {
+                                    uint32_t *ws = &w[e].x;
+#pragma unroll
+                                    for (int y = 0; y < 4; ++y) {
+                                        if ((ws[y] & 0x7F80u) == 0x7F80u) ws[y] &= 0xFFFF0000u;
+                                        if ((ws[y] & 0x7F800000u) == 0x7F800000u) ws[y] &= 0x0000FFFFu;
+                                    }
+                                    *reinterpret_cast<uint4 *>(vt + (x0 + e * kHt) * 16) = w[e];
+                                    const int key = key0 + ((x0 + e * kHt) >> 3);
+                                    bad = bad || (key >= ulo && key < uhi);
                                 }
-                                *reinterpret_cast<uint4 *>(vt + x * 16) = w;
-                                const int key = key0 + (x >> 3);
-                                bad = bad || (key >= ulo && key < uhi);
                             }
                         }
                         if (bad) ctl.nonfinite = 1;
@@ -514,7 +543,7 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
         const uint32_t ts = tmem + 256 * wg + ((uint32_t)((warp & 3) * 32) << 16), to = ts + 128, tpw = ts + 192;
         float m = -INFINITY, mref = 0.f, l = 0.f;
         const float scale = p.sscale * qfac, c2 = p.cap_c2 * qfac;
-        const bool capped = p.cap_c1 != 0.f, biased = p.slopes != nullptr;
+        const bool capped = !kPlain && p.cap_c1 != 0.f, biased = !kPlain && p.slopes != nullptr;
         const float slope = biased && valid ? __ldg(p.slopes + head) * 1.4426950408889634f : 0.f;
         const float mul = capped || biased ? 1.0f : scale;
         bool ok = true;
@@ -524,13 +553,27 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
             if (!ok) break;
             fence_after();
             float s[kKeys];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) ld32(ts + 32 * c, s + 32 * c);
-            wait_ld();
-#pragma unroll
-            for (int c = 0; c < 4; ++c) pin32(s + 32 * c);
-            fence_before();
+            ld32(ts, s);
+            ld32(ts + 32, s + 32);
             const int bits = ctl.bits[(j - cb) % kBitsRing];
+            wait_ld();
+            pin32(s);
+            pin32(s + 32);
+            ld32(ts + 64, s + 64);
+            ld32(ts + 96, s + 96);
+            float top[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) top[c] = s[c];
+#pragma unroll
+            for (int c = 8; c < 56; c += 16)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) top[e] = max3(top[e], s[c + 2 * e], s[c + 2 * e + 1]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) top[e] = fmaxf(top[e], s[56 + e]);
+            wait_ld();
+            pin32(s + 64);
+            pin32(s + 96);
+            fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctl.s_free[wg]);
 
@@ -547,19 +590,28 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
                 for (int c = 0; c < kKeys; ++c) s[c] = fmaf(-slope, fabsf(d0 - (float)c), s[c]);
             }
             const bool whole = key0 >= lo && key0 + kKeys <= hi && bits == 0xFF;
-            if (__any_sync(0xFFFFFFFFu, !whole)) {
+            if (__builtin_expect(__any_sync(0xFFFFFFFFu, !whole), 0)) {
                 const int a = lo - key0, e = hi - key0;
 #pragma unroll
                 for (int c = 0; c < kKeys; ++c)
                     if (c < a || c >= e || !((bits >> (c / kBlockKeys)) & 1)) s[c] = -INFINITY;
             }
-            float mx0 = s[0], mx1 = s[1];
+            const bool touched = capped || biased || __any_sync(0xFFFFFFFFu, !whole);   // s is not what was loaded
+            if (touched) {
 #pragma unroll
-            for (int c = 2; c + 3 < kKeys; c += 4) {
-                mx0 = max3(mx0, s[c], s[c + 1]);
-                mx1 = max3(mx1, s[c + 2], s[c + 3]);
+                for (int c = 0; c < 8; ++c) top[c] = s[c];
+#pragma unroll
+                for (int c = 8; c < 56; c += 16)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) top[e] = max3(top[e], s[c + 2 * e], s[c + 2 * e + 1]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) top[e] = fmaxf(top[e], s[56 + e]);
             }
-            const float mx = fmaxf(max3(mx0, s[kKeys - 2], s[kKeys - 1]), mx1) * mul;
+#pragma unroll
+            for (int c = 64; c < kKeys; c += 16)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) top[e] = max3(top[e], s[c + 2 * e], s[c + 2 * e + 1]);
+            const float mx = fmaxf(max3(max3(top[0], top[1], top[2]), top[3], top[4]), max3(top[5], top[6], top[7])) * mul;
             float corr = 1.0f;
             if (mx > m + kSlack) {   // also the first visible key (m = -inf)
                 corr = fast_exp2(m - mx);
@@ -766,10 +818,10 @@ bool encode_cache(CUtensorMap *map, const void *ptr, long long rows, int keys, i
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int kWG, bool kFp8, bool kPaged>
+template <int kWG, bool kFp8, bool kPaged, bool kPlain>
 cudaError_t launch_variant(const PromptParams &p, int splits, cudaStream_t stream) {
     using C = Config<kWG, kFp8>;
-    auto kern = attn_tiles_kernel<kWG, kFp8, kPaged>;
+    auto kern = attn_tiles_kernel<kWG, kFp8, kPaged, kPlain>;
     constexpr size_t smem = C::kEnd + sizeof(Control);
     static_assert(smem <= (kWG == 1 ? 113 * 1024 : 227 * 1024), "shared memory");
     cudaFuncAttributes fa;
@@ -794,15 +846,20 @@ cudaError_t launch_variant(const PromptParams &p, int splits, cudaStream_t strea
     TileParams tp;
     tp.p = p;
     tp.splits = splits;
-    return launch_kernel(kern, dim3((unsigned)(tiles * splits), (unsigned)p.Hkv), dim3(C::kThreads), smem, stream, 1u, mk,
+    return launch_kernel(kern, dim3((unsigned)(tiles * splits * p.Hkv)), dim3(C::kThreads), smem, stream, 1u, mk,
                          mv, tp);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_tiles(const PromptParams &p, bool paged, bool fp8, int splits, cudaStream_t stream) {
-    if (fp8) return paged ? launch_variant<1, true, true>(p, splits, stream) : launch_variant<1, true, false>(p, splits, stream);
-    return paged ? launch_variant<1, false, true>(p, splits, stream) : launch_variant<1, false, false>(p, splits, stream);
+    const bool plain = p.cap_c1 == 0.f && !p.slopes;
+    // e4m3: two tiles per CTA, so that the conversion of a key tile serves both (8192-token prompt, 16 heads: 207 -> 174
+    // us); bf16: two CTAs per SM with a tile each (177 -> 167 us).
+#define DR_PICK2(N, F, P) (plain ? launch_variant<N, F, P, true>(p, splits, stream) : launch_variant<N, F, P, false>(p, splits, stream))
+    if (fp8) return paged ? DR_PICK2(2, true, true) : DR_PICK2(2, true, false);
+    return paged ? DR_PICK2(1, false, true) : DR_PICK2(1, false, false);
+#undef DR_PICK2
 }
 
 // CTAs that share a tile's keys: while the tiles alone leave SMs (of two CTAs each) idle, with 256 keys each at least.

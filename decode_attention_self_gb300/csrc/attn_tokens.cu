@@ -57,13 +57,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
     return d;
 }
 
-// Four e4m3 codes -> two f16x2, exact.
-__device__ __forceinline__ void codes4_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
-    asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}"
-        : "=r"(lo), "=r"(hi)
-        : "r"(w));
-}
-
 // 32-byte read-only load of data read once per call: the lanes of a row cover its 128 bytes in one request.
 __device__ __forceinline__ void ld_stream32(const void *p, uint4 &a, uint4 &b) {
     asm("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"

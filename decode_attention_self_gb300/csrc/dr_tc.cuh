@@ -58,6 +58,8 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
 __device__ __forceinline__ uint64_t smem_desc(uint32_t addr) {
     return ((uint64_t)(addr & 0x3FFFFu) >> 4) | (1ull << 16) | ((1024ull >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
+// The same matrix `bytes` further on (a multiple of 16, within shared memory).
+__device__ __forceinline__ uint64_t desc_at(uint64_t desc, uint32_t bytes) { return desc + (bytes >> 4); }
 // kind::f16 instruction descriptor: fp32 sums, bf16 or f16 operands, A K-major, B K-major or (b_mn) MN-major.
 __host__ __device__ constexpr uint32_t instr_desc(int M, int N, bool f16, bool b_mn) {
     return (1u << 4) | ((f16 ? 0u : 1u) << 7) | ((f16 ? 0u : 1u) << 10) | ((b_mn ? 1u : 0u) << 16) |
@@ -76,6 +78,12 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
             d),
         "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
         : "memory");
+}
+// One lane of a converged warp, the same each time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(e));
+    return e != 0;
 }
 __device__ __forceinline__ void commit(uint64_t *bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
