@@ -61,9 +61,9 @@ struct Config {
 struct Control {   // at Config::kEnd of the dynamic shared memory
     uint64_t k_full[kMaxStages], k_empty[kMaxStages], v_full[kMaxStages], v_empty[kMaxStages];
     uint64_t k_ready[kMaxStages], v_ready[kMaxStages], kc_empty[kMaxStages], vc_empty[kMaxStages];
-    uint64_t s_full[2], s_free[2], p_full[2], o_done[2];
+    uint64_t q_full[2], s_full[2], s_free[2], p_full[2], o_done[2];
     uint32_t tmem;
-    int gave_up, nonfinite;
+    int gave_up, redo, nonfinite;
     int bits[kBitsRing];                 // per tile: which of its eight 16-key blocks are there
     int b, qt, s0, n, L, prefix;         // the CTA's row and tile
     int lo_min[2], hi_max[2];            // keys that some row of the warpgroup sees
@@ -134,6 +134,7 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
             mbar_init(&ctl.vc_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
+            mbar_init(&ctl.q_full[i], 4);
             mbar_init(&ctl.s_full[i], 1);
             mbar_init(&ctl.s_free[i], 4);
             mbar_init(&ctl.p_full[i], 4);
@@ -144,13 +145,21 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
         ctl.lo_max = 0;
         ctl.hi_min = 0x7FFFFFFF;
         ctl.gave_up = (smem_u32(smem) & 1023u) != 0;   // never: the swizzled tiles need 1024-byte alignment
-        ctl.nonfinite = 0;
+        ctl.redo = ctl.nonfinite = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_k)) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_v)) : "memory");
     }
+    __syncthreads();
     pdl_wait();
-    pdl_trigger();
+    // Tensor memory is taken after the wait and before the next grid may start: no CTA that waits for another grid holds
+    // what that grid still has to take.
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ctl.tmem)),
+                     "r"(C::kTmemCols));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        fence_before();
+    }
 
     // Which tile of which row: tiles of the rows in turn, a row's last (longest, when causal) tile of all heads first
     const int hk = (int)(blockIdx.x % (unsigned)p.Hkv), unit = (int)(blockIdx.x / (unsigned)p.Hkv);
@@ -158,16 +167,19 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
     const int rows_per_cta = kRows * kWG;
     if (warp == 0) {
         int want = unit / tp.splits;
-        int b = -1, s0 = 0, n = 0;
+        int b = -1, s0 = 0, n = 0, L = 0, prefix = 0;
         if (!p.row_start) {
             const int tiles = (int)(((long long)p.T * p.g + rows_per_cta - 1) / rows_per_cta);
             if (want < tiles) b = 0;
             n = p.T;
+            L = __ldg(p.kv_len);
         } else {
             const bool checks = blockIdx.x == 0;   // this CTA looks every row over
             for (int base = 0; base < p.B && (b < 0 || checks); base += 32) {
-                int a = 0, e = 0;
+                int a = 0, e = 0, len_l = 0, pre_l = 0;
                 if (base + lane < p.B) {
+                    len_l = __ldg(p.kv_len + base + lane);
+                    pre_l = p.prefix_len ? __ldg(p.prefix_len + base + lane) : 0;
                     a = __ldg(p.row_start + base + lane);
                     e = __ldg(p.row_start + base + lane + 1);
                     if (checks && (a < 0 || e < a || e > p.T || (base + lane == 0 && a != 0)))
@@ -190,6 +202,8 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
                     b = base + src;
                     s0 = __shfl_sync(0xFFFFFFFFu, a, src);
                     n = __shfl_sync(0xFFFFFFFFu, len, src);
+                    L = __shfl_sync(0xFFFFFFFFu, len_l, src);
+                    prefix = __shfl_sync(0xFFFFFFFFu, pre_l, src);
                     const int before = __shfl_sync(0xFFFFFFFFu, sum - tiles, src), mine = __shfl_sync(0xFFFFFFFFu, tiles, src);
                     want = mine - 1 - (want - before);
                 } else {
@@ -198,15 +212,12 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
             }
         }
         if (lane == 0) {
-            int L = 0, prefix = 0;
             if (b >= 0) {
-                L = __ldg(p.kv_len + b);
                 const int min_len = p.row_start ? n : 0;
                 if (L < min_len || L > p.cap) {
                     flag_error(p.err, DR_ERRF_SEQ_LEN);
                     L = min(max(L, 0), p.cap);
                 }
-                prefix = p.prefix_len ? __ldg(p.prefix_len + b) : 0;
             }
             ctl.b = b;
             ctl.qt = want;
@@ -217,84 +228,79 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
         }
     }
     __syncthreads();
+    fence_after();
+    pdl_trigger();
+    const uint32_t tmem = ctl.tmem;
     if (ctl.b < 0 || ctl.gave_up) {   // past the last tile
         if (ctl.gave_up && threadIdx.x == 0) flag_error(p.err, DR_ERRF_TIMEOUT);
+        if (warp == kMmaWarp)
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kTmemCols));
         return;
-    }
-    if (warp == kMmaWarp) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ctl.tmem)),
-                     "r"(C::kTmemCols));
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-        fence_before();
     }
     const int b = ctl.b, L = ctl.L, n = ctl.n;
 
-    // Query rows: each softmax thread loads its own into the swizzled tile
+    // The keys that the softmax threads' rows see, and those that some and all rows of the CTA see
     const int wg = warp >> 2, row = threadIdx.x & 127;
     int lo = 0, hi = 0, pos = 0, token = 0, head = 0;
     bool valid = false;
-    float qfac = 1.0f;
+    const long long flat0 = (long long)ctl.qt * rows_per_cta, flat_end = (long long)n * p.g;
     if (warp < kProducer) {
-        const long long flat = (long long)ctl.qt * rows_per_cta + wg * kRows + row;
-        valid = flat < (long long)n * p.g;
-        uint8_t *qs = smem + C::kQ + wg * kTileBytes;
+        const long long flat = flat0 + wg * kRows + row;
+        valid = flat < flat_end;
         if (valid) {
             const int i = (int)(flat / p.g);
             token = ctl.s0 + i;
             head = hk * p.g + (int)(flat - (long long)i * p.g);
             visible(p, token, i, n, L, ctl.prefix, lo, hi, pos);
-            const uint16_t *src = p.q + (size_t)token * p.q_stride + (size_t)head * kD;
-            uint4 w[8];
-#pragma unroll
-            for (int c = 0; c < 8; ++c) w[c] = ld_ro16(src + 8 * c);
-            if (kFp8) {
-                float big = 0.f;
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    float x[8];
-                    unpack8(w[c], x);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) big = fmaxf(big, fabsf(x[j]));
-                }
-                const float up = pow2_normaliser(big);
-                qfac = 1.0f / up;
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    float x[8];
-                    unpack8(w[c], x);
-                    w[c] = make_uint4(pack_f16(x[0] * up, x[1] * up), pack_f16(x[2] * up, x[3] * up),
-                                      pack_f16(x[4] * up, x[5] * up), pack_f16(x[6] * up, x[7] * up));
-                }
-            }
-#pragma unroll
-            for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4 *>(qs + swz(row, c)) = w[c];
-        } else {
-#pragma unroll
-            for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4 *>(qs + swz(row, c)) = make_uint4(0, 0, 0, 0);
-        }
-        fence_proxy_async();
-        const bool sees = hi > lo;
-        const int a0 = __reduce_min_sync(0xFFFFFFFFu, sees ? lo : 0x7FFFFFFF);
-        const int a1 = __reduce_max_sync(0xFFFFFFFFu, hi);
-        const int b0 = __reduce_max_sync(0xFFFFFFFFu, lo);
-        const int b1 = __reduce_min_sync(0xFFFFFFFFu, sees ? hi : 0x7FFFFFFF);
-        if (lane == 0) {
-            atomicMin(&ctl.lo_min[wg], a0);
-            atomicMax(&ctl.hi_max[wg], a1);
-            atomicMax(&ctl.lo_max, b0);
-            atomicMin(&ctl.hi_min, b1);
         }
     }
-    __syncthreads();
-    fence_after();
-    const uint32_t tmem = ctl.tmem;
+    int lo_min[kWG], hi_max[kWG], clo, chi;
+    if (p.first_key) {
+        if (warp < kProducer) {
+            const bool sees = hi > lo;
+            const int a0 = __reduce_min_sync(0xFFFFFFFFu, sees ? lo : 0x7FFFFFFF);
+            const int a1 = __reduce_max_sync(0xFFFFFFFFu, hi);
+            const int b0 = __reduce_max_sync(0xFFFFFFFFu, lo);
+            const int b1 = __reduce_min_sync(0xFFFFFFFFu, sees ? hi : 0x7FFFFFFF);
+            if (lane == 0) {
+                atomicMin(&ctl.lo_min[wg], a0);
+                atomicMax(&ctl.hi_max[wg], a1);
+                atomicMax(&ctl.lo_max, b0);
+                atomicMin(&ctl.hi_min, b1);
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kWG; ++w) {
+            lo_min[w] = ctl.lo_min[w];
+            hi_max[w] = ctl.hi_max[w];
+        }
+        clo = ctl.lo_max;
+        chi = ctl.hi_min;
+    } else {   // from key 0 to an end that does not fall from one token to the next
+        const auto end_of = [&](long long flat) -> int {
+            int a, e, q;
+            visible(p, ctl.s0, (int)(flat / p.g), n, L, ctl.prefix, a, e, q);
+            return e;
+        };
+        clo = 0;
+        chi = end_of(flat0);
+#pragma unroll
+        for (int w = 0; w < kWG; ++w) {
+            const long long f = flat0 + w * kRows, last = min(f + kRows, flat_end) - 1;
+            lo_min[w] = 0;
+            hi_max[w] = f < flat_end ? end_of(last) : 0;
+        }
+    }
 
     // Key tiles: tile i covers keys [kbase + 128 i, + 128); this split's run, and each warpgroup's part of it
     int ulo = 0x7FFFFFFF, uhi = 0;
 #pragma unroll
     for (int w = 0; w < kWG; ++w) {
-        ulo = min(ulo, ctl.lo_min[w]);
-        uhi = max(uhi, ctl.hi_max[w]);
+        if (lo_min[w] < hi_max[w]) {
+            ulo = min(ulo, lo_min[w]);
+            uhi = max(uhi, hi_max[w]);
+        }
     }
     if (ulo >= uhi) ulo = uhi = 0;
     const int kbase = ulo & ~(kBlockKeys - 1);
@@ -305,17 +311,23 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
 #pragma unroll
     for (int w = 0; w < kWG; ++w) {
         jb[w] = je[w] = t_lo;
-        if (ctl.lo_min[w] < ctl.hi_max[w]) {
-            jb[w] = max(t_lo, (ctl.lo_min[w] - kbase) / kKeys);
-            je[w] = max(jb[w], min(t_hi, (ctl.hi_max[w] - kbase + kKeys - 1) / kKeys));
+        if (lo_min[w] < hi_max[w]) {
+            jb[w] = max(t_lo, (lo_min[w] - kbase) / kKeys);
+            je[w] = max(jb[w], min(t_hi, (hi_max[w] - kbase + kKeys - 1) / kKeys));
         }
         if (je[w] > jb[w]) {
             cb = min(cb, jb[w]);
             ce = max(ce, je[w]);
         }
     }
-    const int clo = ctl.lo_max, chi = ctl.hi_min;
     volatile int *gave_up = &ctl.gave_up;
+    // Twice at most.  A value that is not finite makes a sum of every row of its tile NaN (0 times infinity), of rows that
+    // do not see it too.  So where some row ends up with sums that are not finite, the CTA goes over its keys once more,
+    // with such values kept out of tiles that not every row sees whole, and every row then adds those that it sees.
+    const auto again = [&](int pass) -> bool {   // the same in every thread: all of them get here
+        __syncthreads();
+        return pass == 0 && *(volatile int *)&ctl.redo && !*gave_up;
+    };
 
     if (warp >= kProducer) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
@@ -328,9 +340,11 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
                 const int key = kbase + j * kKeys + lane * kBlockKeys;
                 return j < ce && key < uhi ? __ldg(p.table + (size_t)b * p.max_blocks + key / kBlockKeys) : -1;
             };
+            int s = 0, round = 0, pass = 0;
+            do {
             int ids = 0, ids_next = 0;
             if (kPaged) ids_next = group_ids(cb);
-            for (int j = cb, i = 0, s = 0, round = 0; j < ce; ++j, ++i) {
+            for (int j = cb, i = 0; j < ce; ++j, ++i) {
                 if (round > 0 && !__all_sync(0xFFFFFFFFu, mbar_wait(&ctl.k_empty[s], (round - 1) & 1, gave_up))) break;
                 unsigned bits = 0xFFu;
                 int z = 0;
@@ -371,6 +385,7 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
                     ++round;
                 }
             }
+            } while (again(pass++));
         } else if (warp == kMmaWarp) {
             // The whole warp waits, one lane issues: descriptors stay warp-uniform (computed by one lane alone, each MMA
             // took over 100 cycles to issue; the tensor pipe takes one in 45 to 65).
@@ -385,62 +400,75 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
                 return (bool)__all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, gave_up));
             };
             bool ok = true;
-            // Step j: S of tile j, then O of tile j - 1
-            int s = 0, round = 0, sp = 0, roundp = 0;
-            for (int j = cb; j <= ce && cb < ce && ok; ++j) {
-                if (j < ce) ok = wait(&k_in[s], round & 1);
+            int s = 0, round = 0, sp = 0, roundp = 0, pass = 0;
+            int made[kWG] = {}, used[kWG] = {};   // S and O products so far
 #pragma unroll
-                for (int w = 0; w < kWG; ++w) {
-                    if (ok && j < ce && j >= jb[w] && j < je[w]) {
-                        if (j > jb[w]) ok = wait(&ctl.s_free[w], (j - jb[w] - 1) & 1);
-                        if (ok) {
-                            fence_after();
-                            const uint64_t qa = desc_at(dq, w * kTileBytes), ka = desc_at(dk, s * kTileBytes);
-                            if (leader) {
+            for (int w = 0; w < kWG; ++w) ok = ok && wait(&ctl.q_full[w], 0);
+            do {
+                // Step j: S of tile j, then O of tile j - 1.  What is likely there is waited for before what is not.
+                if (ok && cb < ce) ok = wait(&k_in[s], round & 1);
+                for (int j = cb; j <= ce && cb < ce && ok; ++j) {
+                    const int s1 = s + 1 == C::kMma ? 0 : s + 1, round1 = s + 1 == C::kMma ? round + 1 : round;
 #pragma unroll
-                                for (int k = 0; k < kD / 16; ++k)
-                                    mma_ss(tmem + 256 * w, desc_at(qa, 32 * k), desc_at(ka, 32 * k), id_s, k != 0);
-                                commit(&ctl.s_full[w]);
+                    for (int w = 0; w < kWG; ++w) {
+                        if (ok && j < ce && j >= jb[w] && j < je[w]) {
+                            if (made[w] > 0) ok = wait(&ctl.s_free[w], (made[w] - 1) & 1);
+                            if (ok) {
+                                fence_after();
+                                const uint64_t qa = desc_at(dq, w * kTileBytes), ka = desc_at(dk, s * kTileBytes);
+                                if (leader) {
+#pragma unroll
+                                    for (int k = 0; k < kD / 16; ++k)
+                                        mma_ss(tmem + 256 * w, desc_at(qa, 32 * k), desc_at(ka, 32 * k), id_s, k != 0);
+                                    commit(&ctl.s_full[w]);
+                                }
+                                ++made[w];
                             }
                         }
-                    }
-                    // (the last stages are not used again: no arrival is left under way when the CTA ends)
-                    if (w == kWG - 1 && ok && j + C::kMma < ce && leader) commit(&k_out[s]);
-                    const int i = j - 1;
-                    if (ok && i >= cb && w == 0) ok = wait(&ctl.v_ready[sp], roundp & 1);
-                    if (ok && i >= jb[w] && i < je[w]) {
-                        ok = wait(&ctl.p_full[w], (i - jb[w]) & 1);
-                        if (ok) {
-                            fence_after();
-                            const uint64_t va = desc_at(dv, sp * kTileBytes);
-                            if (leader) {
+                        if (w == kWG - 1 && ok && j < ce && leader) commit(&k_out[s]);
+                        const int i = j - 1;
+                        if (ok && i >= cb && w == 0) ok = wait(&ctl.v_ready[sp], roundp & 1);
+                        if (ok && w == kWG - 1 && j + 1 < ce) ok = wait(&k_in[s1], round1 & 1);
+                        if (ok && i >= jb[w] && i < je[w]) {
+                            ok = wait(&ctl.p_full[w], used[w] & 1);
+                            if (ok) {
+                                fence_after();
+                                const uint64_t va = desc_at(dv, sp * kTileBytes);
+                                if (leader) {
 #pragma unroll
-                                for (int k = 0; k < kKeys / 16; ++k)
-                                    mma_ts(tmem + 256 * w + 128, tmem + 256 * w + 192 + 8 * k, desc_at(va, 2048 * k), id_o,
-                                           i > jb[w] || k != 0);
-                                commit(&ctl.o_done[w]);
+                                    for (int k = 0; k < kKeys / 16; ++k)
+                                        mma_ts(tmem + 256 * w + 128, tmem + 256 * w + 192 + 8 * k, desc_at(va, 2048 * k),
+                                               id_o, i > jb[w] || k != 0);
+                                    commit(&ctl.o_done[w]);
+                                }
+                                ++used[w];
                             }
                         }
+                        if (w == kWG - 1 && ok && i >= cb && leader) commit(&v_out[sp]);
                     }
-                    if (w == kWG - 1 && ok && i >= cb && i + C::kMma < ce && leader) commit(&v_out[sp]);
+                    __syncwarp();
+                    if (j == ce) {   // the last stage's arrival, so that none is under way when the CTA ends
+                        ok = ok && wait(&v_out[sp], roundp & 1);
+                    }
+                    if (j > cb && ++sp == C::kMma) {
+                        sp = 0;
+                        ++roundp;
+                    }
+                    if (j < ce) {
+                        s = s1;
+                        round = round1;
+                    }
                 }
-                __syncwarp();
-                if (j > cb && ++sp == C::kMma) {
-                    sp = 0;
-                    ++roundp;
-                }
-                if (++s == C::kMma) {
-                    s = 0;
-                    ++round;
-                }
-            }
+            } while (again(pass++));
         } else {
             const int ht = (warp - kHelper) * 32 + lane;
             constexpr int kHt = C::kHelperWarps * 32;
             bool ok = true;
-            int s = 0, round = 0, sc = 0, roundc = 0;
+            int s = 0, round = 0, sc = 0, roundc = 0, pass = 0;
+            do {
             for (int j = cb, i = 0; j < ce && ok; ++j, ++i) {
                 const int key0 = kbase + j * kKeys;
+                const bool edge = key0 < ulo || key0 + kKeys > uhi;   // holds keys that no row sees: their values are zeroed
                 if constexpr (kFp8) {
 #pragma unroll
                     for (int kv = 0; kv < 2; ++kv) {
@@ -450,7 +478,7 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
                         ok = __all_sync(0xFFFFFFFFu, ok);
                         if (!ok) break;
                         const int bits = ctl.bits[i % kBitsRing];
-                        const bool mixed = key0 < clo || key0 + kKeys > chi || bits != 0xFF;
+                        const bool mixed = pass && (key0 < clo || key0 + kKeys > chi || bits != 0xFF);
                         const uint8_t *raw = smem + (kv ? C::kRawV : C::kRawK) + s * C::kTmaBytes;
                         uint8_t *dst = smem + (kv ? C::kV : C::kK) + sc * kTileBytes;
                         bool bad = false;
@@ -458,15 +486,21 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
                         uint4 w[kChunks];
 #pragma unroll
                         for (int e = 0; e < kChunks; ++e) w[e] = *reinterpret_cast<const uint4 *>(raw + (ht + e * kHt) * 16);
-                        if (kv && mixed) {   // NaN codes (0x7F, 0xFF) of values
+                        if (kv && edge) {
 #pragma unroll
                             for (int e = 0; e < kChunks; ++e) {
                                 const int key = key0 + ((ht + e * kHt) >> 2);
+                                if (key < ulo || key >= uhi) w[e] = make_uint4(0, 0, 0, 0);
+                            }
+                        }
+                        if (kv && mixed) {   // NaN codes (0x7F, 0xFF) of values
+#pragma unroll
+                            for (int e = 0; e < kChunks; ++e) {
                                 bool hit = zero_nan_codes(w[e].x);
                                 hit |= zero_nan_codes(w[e].y);
                                 hit |= zero_nan_codes(w[e].z);
                                 hit |= zero_nan_codes(w[e].w);
-                                bad = bad || (hit && key >= ulo && key < uhi);
+                                bad = bad || hit;
                             }
                         }
 #pragma unroll
@@ -495,9 +529,17 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
                 } else {
                     ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl.v_full[s], round & 1, gave_up));
                     if (!ok) break;
-                    const bool mixed = key0 < clo || key0 + kKeys > chi;
+                    const bool mixed = pass && (key0 < clo || key0 + kKeys > chi);
+                    uint8_t *vt = smem + C::kV + s * kTileBytes;
+                    if (edge) {
+                        for (int x = ht; x < kKeys * 8; x += kHt) {
+                            const int key = key0 + (x >> 3);
+                            if (key < ulo || key >= uhi) *reinterpret_cast<uint4 *>(vt + x * 16) = make_uint4(0, 0, 0, 0);
+                        }
+                        if (!mixed) fence_proxy_async();
+                    }
                     if (mixed) {
-                        uint8_t *vt = smem + C::kV + s * kTileBytes;
+                        __syncwarp();
                         bool bad = false;
 #pragma unroll 1
                         for (int x0 = ht; x0 < kKeys * 8; x0 += 8 * kHt) {   // eight chunks of 8 values in flight
@@ -515,8 +557,7 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
                                         if ((ws[y] & 0x7F800000u) == 0x7F800000u) ws[y] &= 0x0000FFFFu;
                                     }
                                     *reinterpret_cast<uint4 *>(vt + (x0 + e * kHt) * 16) = w[e];
-                                    const int key = key0 + ((x0 + e * kHt) >> 3);
-                                    bad = bad || (key >= ulo && key < uhi);
+                                    bad = true;
                                 }
                             }
                         }
@@ -531,6 +572,7 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
                     ++round;
                 }
             }
+            } while (again(pass++));
         }
         __syncwarp();
     } else {
@@ -541,15 +583,54 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
             j1 = je[kWG - 1];
         }
         const uint32_t ts = tmem + 256 * wg + ((uint32_t)((warp & 3) * 32) << 16), to = ts + 128, tpw = ts + 192;
-        float m = -INFINITY, mref = 0.f, l = 0.f;
+        // The query row goes to the swizzled tile
+        float qfac = 1.0f;
+        {
+            uint8_t *qs = smem + C::kQ + wg * kTileBytes;
+            uint4 w[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) w[c] = make_uint4(0, 0, 0, 0);
+            if (valid) {
+                const uint16_t *src = p.q + (size_t)token * p.q_stride + (size_t)head * kD;
+#pragma unroll
+                for (int c = 0; c < 8; ++c) w[c] = ld_ro16(src + 8 * c);
+            }
+            if (kFp8) {
+                float big = 0.f;
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    float x[8];
+                    unpack8(w[c], x);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) big = fmaxf(big, fabsf(x[j]));
+                }
+                const float up = pow2_normaliser(big);
+                qfac = 1.0f / up;
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    float x[8];
+                    unpack8(w[c], x);
+                    w[c] = make_uint4(pack_f16(x[0] * up, x[1] * up), pack_f16(x[2] * up, x[3] * up),
+                                      pack_f16(x[4] * up, x[5] * up), pack_f16(x[6] * up, x[7] * up));
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4 *>(qs + swz(row, c)) = w[c];
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl.q_full[wg]);
+        }
         const float scale = p.sscale * qfac, c2 = p.cap_c2 * qfac;
         const bool capped = !kPlain && p.cap_c1 != 0.f, biased = !kPlain && p.slopes != nullptr;
         const float slope = biased && valid ? __ldg(p.slopes + head) * 1.4426950408889634f : 0.f;
         const float mul = capped || biased ? 1.0f : scale;
+        int done = 0, pass = 0;   // tiles so far
+        do {
+        float m = -INFINITY, mref = 0.f, l = 0.f;
         bool ok = true;
         for (int j = j0; j < j1; ++j) {
-            const int k = j - j0, key0 = kbase + j * kKeys;
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl.s_full[wg], k & 1, gave_up));
+            const int key0 = kbase + j * kKeys;
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl.s_full[wg], done & 1, gave_up));
             if (!ok) break;
             fence_after();
             float s[kKeys];
@@ -635,9 +716,9 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
                 pk[c / 2 + 1] = kFp8 ? pack_f16(y.x, y.y) : pack_bf16(y.x, y.y);
             }
             l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
-            if (k > 0) {
+            if (j > j0) {
                 // P and O are the previous tile's until its product is done
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl.o_done[wg], (k - 1) & 1, gave_up));
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl.o_done[wg], (done - 1) & 1, gave_up));
                 if (!ok) break;
                 fence_after();
                 if (__any_sync(0xFFFFFFFFu, corr != 1.0f)) {
@@ -659,11 +740,12 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
             fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctl.p_full[wg]);
+            ++done;
         }
 
         float o[kD];
         if (ok && j1 > j0) {
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl.o_done[wg], (j1 - j0 - 1) & 1, gave_up));
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl.o_done[wg], (done - 1) & 1, gave_up));
             fence_after();
             ld32(to, o);
             ld32(to + 32, o + 32);
@@ -674,10 +756,15 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
 #pragma unroll
             for (int c = 0; c < kD; ++c) o[c] = 0.f;
         }
+        if (ok && valid && pass == 0) {
+            float z = 0.f;
+#pragma unroll
+            for (int c = 0; c < kD; ++c) z = fmaf(o[c], 0.f, z);
+            if (z != 0.f) *(volatile int *)&ctl.redo = 1;   // NaN: some sum is not finite
+        }
         if (ok && valid) {
-            if (*(volatile int *)&ctl.nonfinite) {
-                // Values that are not finite were left out of tiles that some row does not see whole: add those that
-                // this row sees (a positive weight times such a value is such a value)
+            if (pass && *(volatile int *)&ctl.nonfinite) {
+                // the values left out that this row sees: a positive weight times such a value is such a value
                 for (int j = j0; j < j1; ++j) {
                     const int key0 = kbase + j * kKeys;
                     for (int key = max(lo, key0); key < min(hi, key0 + kKeys); ++key) {
@@ -732,6 +819,7 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
             }
         }
         __syncwarp();
+        } while (again(pass++));
     }
     fence_before();
     __syncthreads();
@@ -862,13 +950,27 @@ cudaError_t launch_attn_tiles(const PromptParams &p, bool paged, bool fp8, int s
 #undef DR_PICK2
 }
 
-// CTAs that share a tile's keys: while the tiles alone leave SMs (of two CTAs each) idle, with 256 keys each at least.
-int plan_tile_splits(long long tiles, int Hkv, int max_len, int sms) {
-    long long s = 2LL * sms / (tiles * Hkv);
-    const long long by_keys = max_len / 256;
-    if (s > by_keys) s = by_keys;
-    if (s > 64) s = 64;
-    return s < 1 ? 1 : (int)s;
+// CTAs that share a tile's keys.  Fewer leave SMs idle, or waiting for the one with the longest run of keys; more cost the
+// states that they leave and that are read again.  The plan takes the s with the least
+//   waves x run + 0.7 run (several waves end unevenly) + 2.5 us + states written and read at 4 TB/s  (s > 1),
+// run = key tiles per CTA x 1.2 us (a step of a CTA with a full SM), waves = CTAs / CTAs that fit, at least 1.
+// 3 rows of 300..700 tokens on up to 20000 e4m3 keys, 16 heads: 278 us unsplit, see the measured table for the split.
+int plan_tile_splits(int T, int g, int Hkv, int max_len, bool fp8, int sms) {
+    const int rows = fp8 ? 256 : 128, slots = fp8 ? sms : 2 * sms;
+    const double units = (double)(((long long)T * g + rows - 1) / rows) * Hkv;
+    const int tiles = max_len / kKeys + 1;
+    const double state_us = (double)T * Hkv * g * (kD + 2) * 4 * 2 / 4e6;
+    int best = 1;
+    double best_us = 0;
+    for (int s = 1; s <= 64 && s <= (tiles + 1) / 2; ++s) {
+        const double run = (double)((tiles + s - 1) / s) * 1.2, waves = units * s / slots;
+        const double us = (waves > 1 ? (waves + 0.7) * run : run) + (s > 1 ? 2.5 + s * state_us : 0);
+        if (s == 1 || us < best_us) {
+            best = s;
+            best_us = us;
+        }
+    }
+    return best;
 }
 
 cudaError_t launch_attn_join(const PromptParams &p, cudaStream_t stream) {

@@ -72,8 +72,12 @@ dr_status check_scores(float scale, const dr_score_opts *o) {
     return DR_OK;
 }
 
-// Query tiles of the tile kernel that T tokens of g heads fill, at least.
-long long tiles_of(int T, int g) { return ((long long)T * g + 127) / 128; }
+// The CTAs per tile that the plan gives either cache type (a call that finds less workspace than its plan wants splits
+// less).
+int most_splits(int T, int g, int Hkv, int max_len, int sms) {
+    const int a = dr::plan_tile_splits(T, g, Hkv, max_len, false, sms), b = dr::plan_tile_splits(T, g, Hkv, max_len, true, sms);
+    return a > b ? a : b;
+}
 
 // Softmax states of `splits` key ranges: (m, l) and 64 sums per (token, head).
 size_t states_bytes(int splits, int T, int Hq) {
@@ -201,8 +205,8 @@ dr_status dr_prompt_attn(const void *q, int64_t q_stride, const dr_kv_cache *cac
     } else {
         p.few_max = 0;
     }
-    int splits = dr::plan_tile_splits(tiles_of(T, p.g), Hkv, len, sms);
-    if (splits > 1 && (!ws || ws_bytes < states_bytes(splits, T, Hq))) splits = 1;
+    int splits = dr::plan_tile_splits(T, p.g, Hkv, len, fp8, sms);
+    while (splits > 1 && (!ws || ws_bytes < states_bytes(splits, T, Hq))) --splits;
     if (splits > 1) set_states(p, ws, splits);
     const cudaError_t e = dr::launch_attn_tiles(p, paged, fp8, splits, cs);
     if (e != cudaSuccess || splits == 1) return from_cuda(e);
@@ -212,7 +216,7 @@ dr_status dr_prompt_attn(const void *q, int64_t q_stride, const dr_kv_cache *cac
 size_t dr_prompt_attn_workspace(int T, int B, int Hq, int Hkv, int max_len, int num_sms) {
     if (T < 1 || B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || max_len < 1 || num_sms < 1) return 0;
     if (T <= B) return 0;
-    const int splits = dr::plan_tile_splits(tiles_of(T, Hq / Hkv), Hkv, max_len, num_sms);
+    const int splits = most_splits(T, Hq / Hkv, Hkv, max_len, num_sms);
     return splits > 1 ? states_bytes(splits, T, Hq) : 0;
 }
 
@@ -258,7 +262,7 @@ dr_status dr_shared_prefix_attn(const void *q, int64_t q_stride, const dr_kv_cac
     p.out_f32 = out_dtype == DR_F32;
     p.err = err_flag;
     const int plen = max_prefix_hint > 0 && max_prefix_hint < pcap ? max_prefix_hint : pcap;
-    int splits = dr::plan_tile_splits(tiles_of(B, p.g), Hkv, plen, sms);
+    int splits = dr::plan_tile_splits(B, p.g, Hkv, plen, prefix->kv_dtype == DR_KV_FP8_E4M3, sms);
     while (splits > 1 && ws_bytes < states_bytes(splits, B, Hq)) --splits;
     set_states(p, ws, splits);
     const cudaError_t e = dr::launch_attn_tiles(p, prefix->layout == DR_KV_PAGED,
@@ -278,7 +282,7 @@ dr_status dr_shared_prefix_attn(const void *q, int64_t q_stride, const dr_kv_cac
 
 size_t dr_shared_prefix_attn_workspace(int B, int Hq, int Hkv, int max_prefix, int num_sms) {
     if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || max_prefix < 1 || num_sms < 1) return 0;
-    return states_bytes(dr::plan_tile_splits(tiles_of(B, Hq / Hkv), Hkv, max_prefix, num_sms), B, Hq);
+    return states_bytes(most_splits(B, Hq / Hkv, Hkv, max_prefix, num_sms), B, Hq);
 }
 
 }  // extern "C"
