@@ -40,20 +40,22 @@ constexpr uint32_t kTileBytes = kKeys * kD * 2;   // a K, V or Q tile of 16-bit 
 
 template <int kWG, bool kFp8>
 struct Config {
-    static constexpr int kHelperWarps = 2;
-    static constexpr int kThreads = 128 * kWG + 128;
+    static constexpr int kHelperWarps = 2;                       // per operand that they work on
+    static constexpr int kOtherWarps = kFp8 ? 8 : 4;             // producer, MMA, helpers (e4m3: K's, V's, two idle)
+    static constexpr int kThreads = 128 * kWG + 32 * kOtherWarps;
     static constexpr int kCtasPerSm = kWG == 1 ? 2 : 1;
-    static constexpr int kTma = kFp8 ? 2 : (kWG == 1 ? 3 : 4);   // stages that TMA fills (bf16: the MMA reads them)
-    static constexpr int kMma = kFp8 ? 2 : kTma;                 // stages that the MMA reads
+    static constexpr int kTma = kFp8 ? 4 : (kWG == 1 ? 3 : 4);   // stages that TMA fills (bf16: the MMA reads them)
+    static constexpr int kMma = kFp8 ? 3 : kTma;                 // stages that the MMA reads
     static constexpr uint32_t kTmaBytes = kKeys * kD * (kFp8 ? 1 : 2);
     static constexpr uint32_t kQ = 0, kK = kWG * kTileBytes, kV = kK + kMma * kTileBytes,
                               kRawK = kV + kMma * kTileBytes, kRawV = kRawK + (kFp8 ? kTma * kTmaBytes : 0),
                               kEnd = kRawV + (kFp8 ? kTma * kTmaBytes : 0);
     // Registers: softmax threads hold a row of 128 scores; the rest needs few.  The shares add up to the launch's.
-    static constexpr int kLaunchRegs = kWG == 1 ? 128 : 168;
-    static constexpr int kSoftmaxRegs = kWG == 1 ? 184 : 208;
-    static constexpr int kOtherRegs = kWG == 1 ? 72 : 88;
-    static_assert(128 * kWG * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "register split");
+    static constexpr int kLaunchRegs = 65536 / kCtasPerSm / kThreads;
+    static constexpr int kSoftmaxRegs = kWG == 1 ? 184 : 192;
+    static constexpr int kOtherRegs = kWG == 1 ? 72 : 64;
+    static_assert(128 * kWG * kSoftmaxRegs + 32 * kOtherWarps * kOtherRegs <= kThreads * kLaunchRegs, "register split");
+    static_assert(kLaunchRegs % 8 == 0 && (kWG == 2) == kFp8, "built for one tile of bf16, two of e4m3");
     // tensor memory columns: per warpgroup S (128), O (64), P (64, two weights per column)
     static constexpr uint32_t kTmemCols = 256 * kWG;
 };
@@ -164,12 +166,12 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
     // Which tile of which row: tiles of the rows in turn, a row's last (longest, when causal) tile of all heads first
     const int hk = (int)(blockIdx.x % (unsigned)p.Hkv), unit = (int)(blockIdx.x / (unsigned)p.Hkv);
     const int split = unit % tp.splits;
-    const int rows_per_cta = kRows * kWG;
+    constexpr unsigned rows_per_cta = kRows * kWG;
     if (warp == 0) {
         int want = unit / tp.splits;
         int b = -1, s0 = 0, n = 0, L = 0, prefix = 0;
         if (!p.row_start) {
-            const int tiles = (int)(((long long)p.T * p.g + rows_per_cta - 1) / rows_per_cta);
+            const int tiles = (int)(((unsigned)p.T * (unsigned)p.g + rows_per_cta - 1) / rows_per_cta);
             if (want < tiles) b = 0;
             n = p.T;
             L = __ldg(p.kv_len);
@@ -189,7 +191,7 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
                 }
                 if (b >= 0) continue;
                 const int len = e - a;
-                const int tiles = len > p.few_max ? (int)(((long long)len * p.g + rows_per_cta - 1) / rows_per_cta) : 0;
+                const int tiles = len > p.few_max ? (int)(((unsigned)len * (unsigned)p.g + rows_per_cta - 1) / rows_per_cta) : 0;
                 int sum = tiles;
 #pragma unroll
                 for (int off = 1; off < 32; off <<= 1) {
@@ -243,15 +245,15 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
     const int wg = warp >> 2, row = threadIdx.x & 127;
     int lo = 0, hi = 0, pos = 0, token = 0, head = 0;
     bool valid = false;
-    const long long flat0 = (long long)ctl.qt * rows_per_cta, flat_end = (long long)n * p.g;
+    const unsigned flat0 = (unsigned)ctl.qt * rows_per_cta, flat_end = (unsigned)n * (unsigned)p.g;   // T * Hq < 2^31
     if (warp < kProducer) {
-        const long long flat = flat0 + wg * kRows + row;
+        const unsigned flat = flat0 + wg * kRows + row;
         valid = flat < flat_end;
         if (valid) {
-            const int i = (int)(flat / p.g);
-            token = ctl.s0 + i;
-            head = hk * p.g + (int)(flat - (long long)i * p.g);
-            visible(p, token, i, n, L, ctl.prefix, lo, hi, pos);
+            const unsigned i = p.g == 1 ? flat : flat / (unsigned)p.g;
+            token = ctl.s0 + (int)i;
+            head = hk * p.g + (int)(flat - i * (unsigned)p.g);
+            visible(p, token, (int)i, n, L, ctl.prefix, lo, hi, pos);
         }
     }
     int lo_min[kWG], hi_max[kWG], clo, chi;
@@ -278,16 +280,16 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
         clo = ctl.lo_max;
         chi = ctl.hi_min;
     } else {   // from key 0 to an end that does not fall from one token to the next
-        const auto end_of = [&](long long flat) -> int {
+        const auto end_of = [&](unsigned flat) -> int {
             int a, e, q;
-            visible(p, ctl.s0, (int)(flat / p.g), n, L, ctl.prefix, a, e, q);
+            visible(p, ctl.s0, (int)(p.g == 1 ? flat : flat / (unsigned)p.g), n, L, ctl.prefix, a, e, q);
             return e;
         };
         clo = 0;
         chi = end_of(flat0);
 #pragma unroll
         for (int w = 0; w < kWG; ++w) {
-            const long long f = flat0 + w * kRows, last = min(f + kRows, flat_end) - 1;
+            const unsigned f = flat0 + w * kRows, last = min(f + kRows, flat_end) - 1;
             lo_min[w] = 0;
             hi_max[w] = f < flat_end ? end_of(last) : 0;
         }
@@ -460,52 +462,52 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
                     }
                 }
             } while (again(pass++));
-        } else {
-            const int ht = (warp - kHelper) * 32 + lane;
-            constexpr int kHt = C::kHelperWarps * 32;
+        } else if (kFp8) {
+            // Codes to f16, K by the first helper warps, V by the next
+            const int hw = warp - kHelper, kv = hw / C::kHelperWarps;
+            const int ht = (hw % C::kHelperWarps) * 32 + lane;
+            constexpr int kHt = C::kHelperWarps * 32, kChunks = kKeys * 4 / kHt, kBatch = 4;   // chunks of 16 codes
+            uint64_t *full = kv ? ctl.v_full : ctl.k_full, *empty = kv ? ctl.v_empty : ctl.k_empty;
+            uint64_t *ready = kv ? ctl.v_ready : ctl.k_ready, *free_ = kv ? ctl.vc_empty : ctl.kc_empty;
             bool ok = true;
             int s = 0, round = 0, sc = 0, roundc = 0, pass = 0;
             do {
-            for (int j = cb, i = 0; j < ce && ok; ++j, ++i) {
-                const int key0 = kbase + j * kKeys;
-                const bool edge = key0 < ulo || key0 + kKeys > uhi;   // holds keys that no row sees: their values are zeroed
-                if constexpr (kFp8) {
+                for (int j = cb, i = 0; j < ce && ok && kv < 2; ++j, ++i) {
+                    const int key0 = kbase + j * kKeys;
+                    ok = mbar_wait(&full[s], round & 1, gave_up);
+                    if (ok && roundc > 0) ok = mbar_wait(&free_[sc], (roundc - 1) & 1, gave_up);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
+                    const bool edge = kv && (key0 < ulo || key0 + kKeys > uhi);   // values that no row sees: zeros
+                    const bool mixed = kv && pass && (key0 < clo || key0 + kKeys > chi || ctl.bits[i % kBitsRing] != 0xFF);
+                    const uint8_t *raw = smem + (kv ? C::kRawV : C::kRawK) + s * C::kTmaBytes;
+                    uint8_t *dst = smem + (kv ? C::kV : C::kK) + sc * kTileBytes;
+                    bool bad = false;
 #pragma unroll
-                    for (int kv = 0; kv < 2; ++kv) {
-                        ok = mbar_wait(kv ? &ctl.v_full[s] : &ctl.k_full[s], round & 1, gave_up);
-                        if (ok && roundc > 0)
-                            ok = mbar_wait(kv ? &ctl.vc_empty[sc] : &ctl.kc_empty[sc], (roundc - 1) & 1, gave_up);
-                        ok = __all_sync(0xFFFFFFFFu, ok);
-                        if (!ok) break;
-                        const int bits = ctl.bits[i % kBitsRing];
-                        const bool mixed = pass && (key0 < clo || key0 + kKeys > chi || bits != 0xFF);
-                        const uint8_t *raw = smem + (kv ? C::kRawV : C::kRawK) + s * C::kTmaBytes;
-                        uint8_t *dst = smem + (kv ? C::kV : C::kK) + sc * kTileBytes;
-                        bool bad = false;
-                        constexpr int kChunks = kKeys * 4 / kHt;   // 16 codes each, all loaded before the first is used
-                        uint4 w[kChunks];
+                    for (int e0 = 0; e0 < kChunks; e0 += kBatch) {
+                        uint4 w[kBatch];
 #pragma unroll
-                        for (int e = 0; e < kChunks; ++e) w[e] = *reinterpret_cast<const uint4 *>(raw + (ht + e * kHt) * 16);
-                        if (kv && edge) {
+                        for (int e = 0; e < kBatch; ++e)
+                            w[e] = *reinterpret_cast<const uint4 *>(raw + (ht + (e0 + e) * kHt) * 16);
+                        if (edge) {
 #pragma unroll
-                            for (int e = 0; e < kChunks; ++e) {
-                                const int key = key0 + ((ht + e * kHt) >> 2);
+                            for (int e = 0; e < kBatch; ++e) {
+                                const int key = key0 + ((ht + (e0 + e) * kHt) >> 2);
                                 if (key < ulo || key >= uhi) w[e] = make_uint4(0, 0, 0, 0);
                             }
                         }
-                        if (kv && mixed) {   // NaN codes (0x7F, 0xFF) of values
+                        if (mixed) {   // NaN codes (0x7F, 0xFF)
 #pragma unroll
-                            for (int e = 0; e < kChunks; ++e) {
-                                bool hit = zero_nan_codes(w[e].x);
-                                hit |= zero_nan_codes(w[e].y);
-                                hit |= zero_nan_codes(w[e].z);
-                                hit |= zero_nan_codes(w[e].w);
-                                bad = bad || hit;
+                            for (int e = 0; e < kBatch; ++e) {
+                                bad |= zero_nan_codes(w[e].x);
+                                bad |= zero_nan_codes(w[e].y);
+                                bad |= zero_nan_codes(w[e].z);
+                                bad |= zero_nan_codes(w[e].w);
                             }
                         }
 #pragma unroll
-                        for (int e = 0; e < kChunks; ++e) {
-                            const int r = (ht + e * kHt) >> 2, c = (ht + e * kHt) & 3;
+                        for (int e = 0; e < kBatch; ++e) {
+                            const int r = (ht + (e0 + e) * kHt) >> 2, c = (ht + (e0 + e) * kHt) & 3;
                             uint4 a, d;
                             codes4_f16(w[e].x, a.x, a.y);
                             codes4_f16(w[e].y, a.z, a.w);
@@ -514,64 +516,70 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
                             *reinterpret_cast<uint4 *>(dst + swz(r, 2 * c)) = a;
                             *reinterpret_cast<uint4 *>(dst + swz(r, 2 * c + 1)) = d;
                         }
-                        if (bad) ctl.nonfinite = 1;
-                        fence_proxy_async();
-                        __syncwarp();
-                        if (lane == 0) {
-                            mbar_arrive(kv ? &ctl.v_empty[s] : &ctl.k_empty[s]);
-                            mbar_arrive(kv ? &ctl.v_ready[sc] : &ctl.k_ready[sc]);
-                        }
+                    }
+                    if (bad) ctl.nonfinite = 1;
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&empty[s]);
+                        mbar_arrive(&ready[sc]);
                     }
                     if (++sc == C::kMma) {
                         sc = 0;
                         ++roundc;
                     }
-                } else {
+                    if (++s == C::kTma) {
+                        s = 0;
+                        ++round;
+                    }
+                }
+            } while (again(pass++));
+        } else {
+            // Values that no row sees become zeros (whatever the cache holds there), in the second pass those that are not
+            // finite too
+            const int ht = (warp - kHelper) * 32 + lane;
+            constexpr int kHt = C::kHelperWarps * 32;
+            bool ok = true;
+            int s = 0, round = 0, pass = 0;
+            do {
+                for (int j = cb; j < ce && ok; ++j) {
+                    const int key0 = kbase + j * kKeys;
+                    const bool edge = key0 < ulo || key0 + kKeys > uhi;
+                    const bool mixed = pass && (key0 < clo || key0 + kKeys > chi);
                     ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl.v_full[s], round & 1, gave_up));
                     if (!ok) break;
-                    const bool mixed = pass && (key0 < clo || key0 + kKeys > chi);
                     uint8_t *vt = smem + C::kV + s * kTileBytes;
-                    if (edge) {
+                    bool bad = false;
+                    if (edge)
                         for (int x = ht; x < kKeys * 8; x += kHt) {
                             const int key = key0 + (x >> 3);
                             if (key < ulo || key >= uhi) *reinterpret_cast<uint4 *>(vt + x * 16) = make_uint4(0, 0, 0, 0);
                         }
-                        if (!mixed) fence_proxy_async();
-                    }
-                    if (mixed) {
-                        __syncwarp();
-                        bool bad = false;
+                    if (mixed)
 #pragma unroll 1
-                        for (int x0 = ht; x0 < kKeys * 8; x0 += 8 * kHt) {   // eight chunks of 8 values in flight
-                            uint4 w[8];
+                        for (int x = ht; x < kKeys * 8; x += kHt) {
+                            uint4 w = *reinterpret_cast<const uint4 *>(vt + x * 16);
+                            if (nonfinite16(w.x, 0x7F80u) || nonfinite16(w.y, 0x7F80u) || nonfinite16(w.z, 0x7F80u) ||
+                                nonfinite16(w.w, 0x7F80u)) {
+                                uint32_t *ws = &w.x;
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) w[e] = *reinterpret_cast<const uint4 *>(vt + (x0 + e * kHt) * 16);
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                if (nonfinite16(w[e].x, 0x7F80u) || nonfinite16(w[e].y, 0x7F80u) ||
-                                    nonfinite16(w[e].z, 0x7F80u) || nonfinite16(w[e].w, 0x7F80u)) {
-                                    uint32_t *ws = &w[e].x;
-#pragma unroll
-                                    for (int y = 0; y < 4; ++y) {
-                                        if ((ws[y] & 0x7F80u) == 0x7F80u) ws[y] &= 0xFFFF0000u;
-                                        if ((ws[y] & 0x7F800000u) == 0x7F800000u) ws[y] &= 0x0000FFFFu;
-                                    }
-                                    *reinterpret_cast<uint4 *>(vt + (x0 + e * kHt) * 16) = w[e];
-                                    bad = true;
+                                for (int y = 0; y < 4; ++y) {
+                                    if ((ws[y] & 0x7F80u) == 0x7F80u) ws[y] &= 0xFFFF0000u;
+                                    if ((ws[y] & 0x7F800000u) == 0x7F800000u) ws[y] &= 0x0000FFFFu;
                                 }
+                                *reinterpret_cast<uint4 *>(vt + x * 16) = w;
+                                bad = true;
                             }
                         }
-                        if (bad) ctl.nonfinite = 1;
-                        fence_proxy_async();
-                    }
+                    if (bad) ctl.nonfinite = 1;
+                    if (edge || mixed) fence_proxy_async();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&ctl.v_ready[s]);
+                    if (++s == C::kTma) {
+                        s = 0;
+                        ++round;
+                    }
                 }
-                if (++s == C::kTma) {
-                    s = 0;
-                    ++round;
-                }
-            }
             } while (again(pass++));
         }
         __syncwarp();
@@ -675,7 +683,12 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
                 const int a = lo - key0, e = hi - key0;
 #pragma unroll
                 for (int c = 0; c < kKeys; ++c)
-                    if (c < a || c >= e || !((bits >> (c / kBlockKeys)) & 1)) s[c] = -INFINITY;
+                    if (c < a || c >= e) s[c] = -INFINITY;
+                if (bits != 0xFF) {   // blocks that are not there
+#pragma unroll
+                    for (int c = 0; c < kKeys; ++c)
+                        if (!((bits >> (c / kBlockKeys)) & 1)) s[c] = -INFINITY;
+                }
             }
             const bool touched = capped || biased || __any_sync(0xFFFFFFFFu, !whole);   // s is not what was loaded
             if (touched) {
@@ -839,43 +852,38 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
     }
 }
 
-// out[t][h] from the states of the splits, in split order.  One warp per token: lanes 0-15 and 16-31 take a head each,
-// four dimensions per lane.
+// out[t][h] from the states of the splits, in split order.  A warp takes two heads of a token, 16 lanes each, four
+// dimensions per lane.
 __global__ void __launch_bounds__(256) attn_join_kernel(const PromptParams p) {
     pdl_wait();
     pdl_trigger();
-    const int lane = threadIdx.x & 31;
-    const long long tl = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (tl >= p.T) return;
-    const int t = (int)tl;
+    const int lane = threadIdx.x & 31, pairs = (p.Hq + 1) / 2;
+    const long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (w >= (long long)p.T * pairs) return;
+    const int t = (int)(w / pairs), h = (int)(w - (long long)t * pairs) * 2 + (lane >> 4);
     int s0, s1;
-    if (find_row(p.row_start, p.B, p.T, t, lane, s0, s1, nullptr) < 0 || s1 - s0 <= p.few_max) return;
-    const size_t rows = (size_t)p.T * p.Hq;
-    for (int h = lane >> 4; h < p.Hq; h += 2) {
-        const size_t row = (size_t)t * p.Hq + h;
-        float M = -INFINITY;
-        for (int x = 0; x < p.nparts; ++x) M = fmaxf(M, p.part_ml[x * rows + row].x);
-        float l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int x = 0; x < p.nparts; ++x) {
-            const float2 ml = p.part_ml[x * rows + row];
-            if (ml.x == -INFINITY) continue;
-            const float w = exp2f(ml.x - M);
-            const float4 a = reinterpret_cast<const float4 *>(p.part_acc + (x * rows + row) * kD)[lane & 15];
-            l += w * ml.y;
-            o.x += w * a.x;
-            o.y += w * a.y;
-            o.z += w * a.z;
-            o.w += w * a.w;
-        }
-        const float inv = l == 0.f ? 0.f : 1.0f / l;
-        o = l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-        if (p.out_f32)
-            reinterpret_cast<float4 *>(static_cast<float *>(p.out) + row * kD)[lane & 15] = o;
-        else
-            reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + row * kD)[lane & 15] =
-                make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
+    if (find_row(p.row_start, p.B, p.T, t, lane, s0, s1, nullptr) < 0 || s1 - s0 <= p.few_max || h >= p.Hq) return;
+    const size_t rows = (size_t)p.T * p.Hq, row = (size_t)t * p.Hq + h;
+    float M = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int x = 0; x < p.nparts; ++x) {
+        const float2 ml = p.part_ml[x * rows + row];
+        const float4 a = reinterpret_cast<const float4 *>(p.part_acc + (x * rows + row) * kD)[lane & 15];
+        const float m2 = fmaxf(M, ml.x);
+        if (m2 == -INFINITY) continue;   // no key so far
+        const float w0 = exp2f(M - m2), w1 = exp2f(ml.x - m2);
+        M = m2;
+        l = l * w0 + ml.y * w1;
+        o = make_float4(o.x * w0 + a.x * w1, o.y * w0 + a.y * w1, o.z * w0 + a.z * w1, o.w * w0 + a.w * w1);
     }
+    const float inv = l == 0.f ? 0.f : 1.0f / l;
+    o = l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+    if (p.out_f32)
+        reinterpret_cast<float4 *>(static_cast<float *>(p.out) + row * kD)[lane & 15] = o;
+    else
+        reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + row * kD)[lane & 15] =
+            make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
@@ -916,7 +924,7 @@ cudaError_t launch_variant(const PromptParams &p, int splits, cudaStream_t strea
     cudaError_t e = cudaFuncGetAttributes(&fa, kern);
     if (e != cudaSuccess) return e;
     // the register split draws on what the launch gives: fewer would leave a warpgroup waiting
-    if (fa.numRegs * C::kThreads < 128 * kWG * C::kSoftmaxRegs + 128 * C::kOtherRegs) return cudaErrorInvalidConfiguration;
+    if (fa.numRegs * C::kThreads < 128 * kWG * C::kSoftmaxRegs + 32 * C::kOtherWarps * C::kOtherRegs) return cudaErrorInvalidConfiguration;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     CUtensorMap mk, mv;
@@ -974,7 +982,8 @@ int plan_tile_splits(int T, int g, int Hkv, int max_len, bool fp8, int sms) {
 }
 
 cudaError_t launch_attn_join(const PromptParams &p, cudaStream_t stream) {
-    return launch_kernel(attn_join_kernel, dim3((unsigned)((p.T + 7) / 8)), dim3(256), 0, stream, 1u, p);
+    const long long warps = (long long)p.T * ((p.Hq + 1) / 2);
+    return launch_kernel(attn_join_kernel, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, stream, 1u, p);
 }
 
 }  // namespace dr
