@@ -41,7 +41,7 @@ constexpr uint32_t kTileBytes = kKeys * kD * 2;   // a K, V or Q tile of 16-bit 
 template <int kWG, bool kFp8>
 struct Config {
     static constexpr int kHelperWarps = 2;                       // per operand that they work on
-    static constexpr int kOtherWarps = kFp8 ? 8 : 4;             // producer, MMA, helpers (e4m3: K's, V's, two idle)
+    static constexpr int kOtherWarps = kFp8 ? 8 : 4;             // producer, MMA, helpers (e4m3: K's, V's; one idle)
     static constexpr int kThreads = 128 * kWG + 32 * kOtherWarps;
     static constexpr int kCtasPerSm = kWG == 1 ? 2 : 1;
     static constexpr int kTma = kFp8 ? 4 : (kWG == 1 ? 3 : 4);   // stages that TMA fills (bf16: the MMA reads them)
@@ -75,6 +75,8 @@ struct Control {   // at Config::kEnd of the dynamic shared memory
 struct TileParams {
     PromptParams p;
     int32_t splits;
+    uint32_t g_mul, g_shift;   // n / g = (n + hi32(n * g_mul)) >> g_shift for n < 2^31
+    __device__ __forceinline__ unsigned by_g(unsigned n) const { return (n + __umulhi(n, g_mul)) >> g_shift; }
 };
 
 // Physical byte of 16-byte chunk c of 128-byte row r under the 128-byte swizzle (tile base 1024-byte aligned).
@@ -122,7 +124,7 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
     Control &ctl = *reinterpret_cast<Control *>(smem + C::kEnd);
     const PromptParams &p = tp.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr int kProducer = 4 * kWG, kMmaWarp = kProducer + 1, kHelper = kProducer + 2;
+    constexpr int kProducer = 4 * kWG, kMmaWarp = kProducer + 1, kHelper = kMmaWarp + kWG;   // an MMA warp per tile
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kMaxStages; ++i) {
@@ -132,8 +134,8 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
             mbar_init(&ctl.v_empty[i], kFp8 ? C::kHelperWarps : 1);
             mbar_init(&ctl.k_ready[i], C::kHelperWarps);
             mbar_init(&ctl.v_ready[i], C::kHelperWarps);
-            mbar_init(&ctl.kc_empty[i], 1);
-            mbar_init(&ctl.vc_empty[i], 1);
+            mbar_init(&ctl.kc_empty[i], kWG);
+            mbar_init(&ctl.vc_empty[i], kWG);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ctl.q_full[i], 4);
@@ -250,7 +252,7 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
         const unsigned flat = flat0 + wg * kRows + row;
         valid = flat < flat_end;
         if (valid) {
-            const unsigned i = p.g == 1 ? flat : flat / (unsigned)p.g;
+            const unsigned i = tp.by_g(flat);
             token = ctl.s0 + (int)i;
             head = hk * p.g + (int)(flat - i * (unsigned)p.g);
             visible(p, token, (int)i, n, L, ctl.prefix, lo, hi, pos);
@@ -282,7 +284,7 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
     } else {   // from key 0 to an end that does not fall from one token to the next
         const auto end_of = [&](unsigned flat) -> int {
             int a, e, q;
-            visible(p, ctl.s0, (int)(p.g == 1 ? flat : flat / (unsigned)p.g), n, L, ctl.prefix, a, e, q);
+            visible(p, ctl.s0, (int)tp.by_g(flat), n, L, ctl.prefix, a, e, q);
             return e;
         };
         clo = 0;
@@ -388,7 +390,7 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
                 }
             }
             } while (again(pass++));
-        } else if (warp == kMmaWarp) {
+        } else if (warp < kHelper) {
             // The whole warp waits, one lane issues: descriptors stay warp-uniform (computed by one lane alone, each MMA
             // took over 100 cycles to issue; the tensor pipe takes one in 45 to 65).
             constexpr uint32_t id_s = instr_desc(kRows, kKeys, kFp8, false);
@@ -401,60 +403,62 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
             const auto wait = [&](uint64_t *bar, uint32_t parity) {
                 return (bool)__all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, gave_up));
             };
-            bool ok = true;
-            int s = 0, round = 0, sp = 0, roundp = 0, pass = 0;
-            int made[kWG] = {}, used[kWG] = {};   // S and O products so far
-#pragma unroll
-            for (int w = 0; w < kWG; ++w) ok = ok && wait(&ctl.q_full[w], 0);
+            const auto wait2 = [&](uint64_t *x, uint32_t px, uint64_t *y, uint32_t py) {
+                return (bool)__all_sync(0xFFFFFFFFu, mbar_wait2(x, px, y, py, gave_up));
+            };
+            const int w = warp - kMmaWarp;   // the tile (warpgroup) that this warp serves
+            const int jw = w == 0 ? jb[0] : jb[kWG - 1], jx = w == 0 ? je[0] : je[kWG - 1];
+            const uint32_t td = tmem + 256 * w;
+            int s = 0, round = 0, sp = 0, roundp = 0, made = 0, used = 0, pass = 0;
+            bool ok = wait(&ctl.q_full[w], 0);
             do {
                 // Step j: S of tile j, then O of tile j - 1.  What is likely there is waited for before what is not.
                 if (ok && cb < ce) ok = wait(&k_in[s], round & 1);
                 for (int j = cb; j <= ce && cb < ce && ok; ++j) {
                     const int s1 = s + 1 == C::kMma ? 0 : s + 1, round1 = s + 1 == C::kMma ? round + 1 : round;
+                    if (j < ce) {
+                        if (j >= jw && j < jx) {
+                            if (made > 0) ok = wait(&ctl.s_free[w], (made - 1) & 1);
+                            if (!ok) break;
+                            fence_after();
+                            const uint64_t qa = desc_at(dq, w * kTileBytes), ka = desc_at(dk, s * kTileBytes);
+                            if (leader) {
 #pragma unroll
-                    for (int w = 0; w < kWG; ++w) {
-                        if (ok && j < ce && j >= jb[w] && j < je[w]) {
-                            if (made[w] > 0) ok = wait(&ctl.s_free[w], (made[w] - 1) & 1);
-                            if (ok) {
-                                fence_after();
-                                const uint64_t qa = desc_at(dq, w * kTileBytes), ka = desc_at(dk, s * kTileBytes);
-                                if (leader) {
-#pragma unroll
-                                    for (int k = 0; k < kD / 16; ++k)
-                                        mma_ss(tmem + 256 * w, desc_at(qa, 32 * k), desc_at(ka, 32 * k), id_s, k != 0);
-                                    commit(&ctl.s_full[w]);
-                                }
-                                ++made[w];
+                                for (int k = 0; k < kD / 16; ++k)
+                                    mma_ss(td, desc_at(qa, 32 * k), desc_at(ka, 32 * k), id_s, k != 0);
+                                commit(&ctl.s_full[w]);
                             }
+                            ++made;
                         }
-                        if (w == kWG - 1 && ok && j < ce && leader) commit(&k_out[s]);
-                        const int i = j - 1;
-                        if (ok && i >= cb && w == 0) ok = wait(&ctl.v_ready[sp], roundp & 1);
-                        if (ok && w == kWG - 1 && j + 1 < ce) ok = wait(&k_in[s1], round1 & 1);
-                        if (ok && i >= jb[w] && i < je[w]) {
-                            ok = wait(&ctl.p_full[w], used[w] & 1);
-                            if (ok) {
-                                fence_after();
-                                const uint64_t va = desc_at(dv, sp * kTileBytes);
-                                if (leader) {
+                        if (leader) commit(&k_out[s]);
+                    }
+                    if (j > cb && j + 1 < ce) ok = wait2(&ctl.v_ready[sp], roundp & 1, &k_in[s1], round1 & 1);
+                    else if (j > cb) ok = wait(&ctl.v_ready[sp], roundp & 1);
+                    else if (j + 1 < ce) ok = wait(&k_in[s1], round1 & 1);
+                    if (!ok) break;
+                    if (j > cb) {
+                        if (j - 1 >= jw && j - 1 < jx) {
+                            ok = wait(&ctl.p_full[w], used & 1);
+                            if (!ok) break;
+                            fence_after();
+                            const uint64_t va = desc_at(dv, sp * kTileBytes);
+                            if (leader) {
 #pragma unroll
-                                    for (int k = 0; k < kKeys / 16; ++k)
-                                        mma_ts(tmem + 256 * w + 128, tmem + 256 * w + 192 + 8 * k, desc_at(va, 2048 * k),
-                                               id_o, i > jb[w] || k != 0);
-                                    commit(&ctl.o_done[w]);
-                                }
-                                ++used[w];
+                                for (int k = 0; k < kKeys / 16; ++k)
+                                    mma_ts(td + 128, td + 192 + 8 * k, desc_at(va, 2048 * k), id_o, j - 1 > jw || k != 0);
+                                commit(&ctl.o_done[w]);
                             }
+                            ++used;
                         }
-                        if (w == kWG - 1 && ok && i >= cb && leader) commit(&v_out[sp]);
-                    }
-                    __syncwarp();
-                    if (j == ce) {   // the last stage's arrival, so that none is under way when the CTA ends
-                        ok = ok && wait(&v_out[sp], roundp & 1);
-                    }
-                    if (j > cb && ++sp == C::kMma) {
-                        sp = 0;
-                        ++roundp;
+                        if (leader) commit(&v_out[sp]);
+                        __syncwarp();
+                        if (j == ce) {   // the last stage's arrivals, so that none is under way when the CTA ends
+                            ok = wait(&v_out[sp], roundp & 1);
+                        }
+                        if (++sp == C::kMma) {
+                            sp = 0;
+                            ++roundp;
+                        }
                     }
                     if (j < ce) {
                         s = s1;
@@ -942,6 +946,9 @@ cudaError_t launch_variant(const PromptParams &p, int splits, cudaStream_t strea
     TileParams tp;
     tp.p = p;
     tp.splits = splits;
+    tp.g_shift = 0;
+    while ((1 << tp.g_shift) < p.g) ++tp.g_shift;
+    tp.g_mul = (uint32_t)(((1ull << 32) * ((1ull << tp.g_shift) - p.g)) / p.g + 1);
     return launch_kernel(kern, dim3((unsigned)(tiles * splits * p.Hkv)), dim3(C::kThreads), smem, stream, 1u, mk,
                          mv, tp);
 }

@@ -465,14 +465,29 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<Tile, kN>())
                 if (h < nheads) {
                     const size_t row = (size_t)t * p.Hq + h0 + h;
                     const int step = splits * (8 / tnh);
-                    for (int x = split + splits * (team / tnh); x < p.nparts; x += step) {
-                        const float2 ml = p.part_ml[x * rows + row];
-                        const float4 a = reinterpret_cast<const float4 *>(p.part_acc + (x * rows + row) * kD)[d4];
-                        if (ml.x == -INFINITY) continue;   // an empty share: its sums were not written
-                        const float m2 = fmaxf(M, ml.x), w0 = exp2f(M - m2), w1 = exp2f(ml.x - m2);
+                    for (int x = split + splits * (team / tnh); x < p.nparts; x += 4 * step) {
+                        float2 ml[4];   // four states' loads in flight
+                        float4 a[4];
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            const size_t at = (size_t)min(x + y * step, p.nparts - 1) * rows + row;
+                            ml[y] = p.part_ml[at];
+                            a[y] = reinterpret_cast<const float4 *>(p.part_acc + at * kD)[d4];
+                            if (x + y * step >= p.nparts) ml[y].x = -INFINITY;
+                        }
+                        const float m2 = fmaxf(fmaxf(M, fmaxf(ml[0].x, ml[1].x)), fmaxf(ml[2].x, ml[3].x));
+                        if (m2 == -INFINITY) continue;   // no key so far
+                        const float w0 = exp2f(M - m2);
                         M = m2;
-                        ls = ls * w0 + ml.y * w1;
-                        o = make_float4(o.x * w0 + a.x * w1, o.y * w0 + a.y * w1, o.z * w0 + a.z * w1, o.w * w0 + a.w * w1);
+                        ls *= w0;
+                        o = make_float4(o.x * w0, o.y * w0, o.z * w0, o.w * w0);
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            const float w = exp2f(ml[y].x - m2);
+                            ls += ml[y].x == -INFINITY ? 0.f : ml[y].y * w;
+                            if (ml[y].x != -INFINITY)   // an empty share, or past the last
+                                o = make_float4(o.x + a[y].x * w, o.y + a[y].y * w, o.z + a[y].z * w, o.w + a[y].w * w);
+                        }
                     }
                 }
                 const int slot = pass * 8 + team;
