@@ -14,6 +14,7 @@ from __future__ import annotations
 import ctypes
 import dataclasses
 import os
+import struct
 
 import torch
 
@@ -46,7 +47,7 @@ class dr_score_opts(ctypes.Structure):
 
 _vp, _i, _f = ctypes.c_void_p, ctypes.c_int, ctypes.c_float
 _i64, _sz = ctypes.c_int64, ctypes.c_size_t
-_byref = ctypes.byref
+_cs = ctypes.c_char_p   # a C structure packed as bytes
 _lib.dr_kv_append.argtypes = [ctypes.POINTER(dr_kv_cache), _vp, _vp, _vp, _i, _i, _i, _vp, _vp]
 _lib.dr_decode_self_attn.argtypes = [_vp, ctypes.POINTER(dr_kv_cache), _vp, _i, _i, _i, _i, _f, _vp, _i, _vp, _vp]
 _lib.dr_decode_cross_attn.argtypes = [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _f, _vp, _i, _vp, _vp]
@@ -59,15 +60,13 @@ _lib.dr_lm_head_stall_test.argtypes = [_vp, _vp, _i, _i, _i, _i, _i, _vp, _vp, _
 _lib.dr_decode_self_attn_stall_test.argtypes = [_vp, ctypes.POINTER(dr_kv_cache), _vp, _i, _i, _i, _i, _f, _vp, _i, _vp,
                                                 _i, _vp]
 _lib.dr_rope_table.argtypes = [_vp, _i, _i, ctypes.c_double, _vp]
-_lib.dr_rope_append.argtypes = [ctypes.POINTER(dr_kv_cache), _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp,
+_lib.dr_rope_append.argtypes = [_cs, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp,
                                 _vp, _i, _i, _i, _i, _i, _i, _i, _i, _vp, _vp]
-_lib.dr_prompt_attn.argtypes = [_vp, _i64, ctypes.POINTER(dr_kv_cache), _vp, _vp, ctypes.POINTER(dr_score_opts), _i, _i,
-                                _i, _i, _i, _i, _f, _vp, _i, _vp, _sz, _vp, _vp]
+_lib.dr_prompt_attn.argtypes = [_vp, _i64, _cs, _vp, _vp, _cs, _i, _i, _i, _i, _i, _i, _f, _vp, _i, _vp, _sz, _vp, _vp]
 _lib.dr_prompt_attn_workspace.argtypes = [_i, _i, _i, _i, _i, _i]
 _lib.dr_prompt_attn_workspace.restype = _sz
-_lib.dr_shared_prefix_attn.argtypes = [_vp, _i64, ctypes.POINTER(dr_kv_cache), _vp, ctypes.POINTER(dr_kv_cache), _vp,
-                                       ctypes.POINTER(dr_score_opts), _i, _i, _i, _i, _i, _i, _f, _vp, _i, _vp, _sz, _vp,
-                                       _vp]
+_lib.dr_shared_prefix_attn.argtypes = [_vp, _i64, _cs, _vp, _cs, _vp, _cs, _i, _i, _i, _i, _i, _i, _f, _vp, _i, _vp, _sz,
+                                       _vp, _vp]
 _lib.dr_shared_prefix_attn_workspace.argtypes = [_i, _i, _i, _i, _i]
 _lib.dr_shared_prefix_attn_workspace.restype = _sz
 _lib.dr_plan_splits.argtypes = [_i, _i, _i, _i, _i]
@@ -294,11 +293,15 @@ def dr_lm_head_stall_test(hidden: torch.Tensor, W: torch.Tensor, C: int, logits:
 
 
 # The prompt-side calls below check up to fourteen tensors each, and a small call's device work takes a few
-# microseconds, so their checks are written out flat: a tensor that passes costs three attribute reads, and only one
-# that fails is looked at again to say why.
+# microseconds, so their checks are written out flat: a tensor that passes costs a few attribute reads, and only one
+# that fails is looked at again to say why.  The C structures are packed as bytes (a ctypes.Structure takes twice the time).
 _BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
-_current_device = torch.cuda.current_device
+_device = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_pack_cache = struct.Struct("@iiiiiiPPPff").pack   # dr_kv_cache
+_pack_opts = struct.Struct("@ifPPP").pack          # dr_score_opts
+assert struct.calcsize("@iiiiiiPPPff") == ctypes.sizeof(dr_kv_cache)
+assert struct.calcsize("@ifPPP") == ctypes.sizeof(dr_score_opts)
 
 
 def _refuse(t, dev: int, dtype, shape, name: str):
@@ -313,29 +316,29 @@ def _refuse(t, dev: int, dtype, shape, name: str):
     raise ValueError(f"{name} must be contiguous")
 
 
-def _arg(t, dev: int, dtype, shape, name: str):
-    """Address of a contiguous tensor of this type and shape on device dev; None for None."""
+def _vec(t, dev: int, dtype, n: int, name: str):
+    """Address of n contiguous elements on device dev; None for None."""
     if t is None:
         return None
-    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-        _refuse(t, dev, dtype, shape, name)
+    if t.get_device() != dev or t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
+        _refuse(t, dev, dtype, (n,), name)
     return t.data_ptr()
 
 
-def _rows_arg(t, dev: int, shape, name: str):
+def _rows(t, dev: int, shape, name: str):
     """(address, elements between tokens) of a bf16 [T, heads, D] tensor whose tokens are dense but may lie apart."""
-    if t is None:
-        return None, 0
     if t.get_device() != dev or t.dtype is not _BF16 or t.shape != shape:
         _refuse(t, dev, _BF16, shape, name)
-    s0, s1, s2 = t.stride()
     T, heads, D = shape
+    if t.is_contiguous():
+        return t.data_ptr(), heads * D
+    s0, s1, s2 = t.stride()
     if s2 != 1 or (s1 != D and heads > 1):
         raise ValueError(f"{name} must be [T, heads, D] with contiguous heads")
     return t.data_ptr(), (s0 if T > 1 else heads * D)
 
 
-def _cache_arg(cache: KVCache, dev: int, B: int, Hkv: int, D: int, name: str) -> dr_kv_cache:
+def _cache(cache: KVCache, dev: int, B: int, Hkv: int, D: int, name: str) -> bytes:
     """The C description of a cache of at least B rows of Hkv heads, all of it on device dev."""
     k, v, table = cache.k, cache.v, cache.block_table
     shape, dt = k.shape, k.dtype
@@ -343,21 +346,25 @@ def _cache_arg(cache: KVCache, dev: int, B: int, Hkv: int, D: int, name: str) ->
         raise ValueError(f"{name}.k and {name}.v must be [.., {Hkv}, .., {D}], k is {tuple(shape)}")
     if dt is not _BF16 and dt is not _U8:
         raise ValueError(f"{name}.k must be {_BF16}, or {_U8} for e4m3 codes, got {dt}")
-    kp, vp = _arg(k, dev, dt, shape, name + ".k"), _arg(v, dev, dt, shape, name + ".v")
+    if k.get_device() != dev or not k.is_contiguous():
+        _refuse(k, dev, dt, shape, name + ".k")
+    if v.get_device() != dev or v.dtype is not dt or v.shape != shape or not v.is_contiguous():
+        _refuse(v, dev, dt, shape, name + ".v")
     fp8 = DR_KV_FP8_E4M3 if dt is _U8 else DR_KV_BF16
+    rows, _, keys, _ = shape
     if table is None:
-        rows = shape[0]
-        c = dr_kv_cache(DR_KV_CONTIGUOUS, shape[2], 0, 0, 0, fp8, kp, vp, None, cache.k_scale, cache.v_scale)
+        packed = _pack_cache(DR_KV_CONTIGUOUS, keys, 0, 0, 0, fp8, k.data_ptr(), v.data_ptr(), 0, cache.k_scale,
+                             cache.v_scale)
     else:
-        tshape = table.shape
-        if len(tshape) != 2:
-            raise ValueError(f"{name}.block_table must be [B, max_blocks]")
-        rows = tshape[0]
-        c = dr_kv_cache(DR_KV_PAGED, 0, shape[2], shape[0], tshape[1], fp8, kp, vp,
-                        _arg(table, dev, _I32, tshape, name + ".block_table"), cache.k_scale, cache.v_scale)
+        if table.dim() != 2 or table.get_device() != dev or table.dtype is not _I32 or not table.is_contiguous():
+            _refuse(table, dev, _I32, None if table.dim() == 2 else (B, "max_blocks"), name + ".block_table")
+        blocks = rows
+        rows, width = table.shape
+        packed = _pack_cache(DR_KV_PAGED, 0, keys, blocks, width, fp8, k.data_ptr(), v.data_ptr(), table.data_ptr(),
+                             cache.k_scale, cache.v_scale)
     if rows < B:
         raise ValueError(f"{name} holds {rows} rows, the call has {B}")
-    return c
+    return packed
 
 
 def _stream_arg(stream, dev: int):
@@ -365,26 +372,29 @@ def _stream_arg(stream, dev: int):
 
 
 def _shape3(t, name: str):
-    if t.dim() != 3:
+    shape = t.shape
+    if len(shape) != 3:
         raise ValueError(f"{name} must be [T, heads, D]")
-    return t.shape
+    return shape
 
 
-def _out_arg(out, dev: int, shape):
+def _out(out, dev: int, shape):
     """(address, C type) of an output of the queries' shape."""
     dt = out.dtype
     if dt is not _BF16 and dt is not _F32:
         raise ValueError(f"out must be {_BF16} or {_F32}, got {dt}")
-    return _arg(out, dev, dt, shape, "out"), DR_F32 if dt is _F32 else DR_BF16
+    if out.get_device() != dev or out.shape != shape or not out.is_contiguous():
+        _refuse(out, dev, dt, shape, "out")
+    return out.data_ptr(), DR_F32 if dt is _F32 else DR_BF16
 
 
 def dr_rope_table(table: torch.Tensor, base: float = 10000.0, stream=None) -> torch.Tensor:
     """Fill table [max_pos, rot_dim] float32 with cos (first half) and sin of p * base^(-2i / rot_dim)."""
-    dev = _current_device()
+    dev = _device()
     if table.dim() != 2:
         raise ValueError("table must be [max_pos, rot_dim]")
     n, rot = table.shape
-    _check("dr_rope_table", _lib.dr_rope_table(_arg(table, dev, _F32, table.shape, "table"), n, rot, base,
+    _check("dr_rope_table", _lib.dr_rope_table(_vec(table, dev, _F32, n * rot, "table"), n, rot, base,
                                                _stream_arg(stream, dev)))
     return table
 
@@ -398,7 +408,7 @@ def dr_rope_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, row_start: 
     Row b's tokens row_start[b] .. row_start[b+1]-1 go to slots start_pos[b], start_pos[b]+1, ...; q, k, v and q_out
     may be slices of a fused projection (dense heads, any token stride that is a multiple of 8).
     """
-    dev = _current_device()
+    dev = _device()
     kshape = _shape3(k, "k")
     T, Hkv, D = kshape
     B = start_pos.numel()
@@ -409,29 +419,29 @@ def dr_rope_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, row_start: 
         Hq = qshape[1]
         if qshape[0] != T or qshape[2] != D:
             raise ValueError(f"q must have shape ({T}, heads, {D}), has {tuple(qshape)}")
-    c = _cache_arg(cache, dev, B, Hkv, D, "cache")
-    kp, ks = _rows_arg(k, dev, kshape, "k")
-    vp, vs = _rows_arg(v, dev, kshape, "v")
-    qp, qs = _rows_arg(q, dev, qshape, "q")
-    op, os_ = _rows_arg(q_out, dev, qshape, "q_out")
+    c = _cache(cache, dev, B, Hkv, D, "cache")
+    kp, ks = _rows(k, dev, kshape, "k")
+    vp, vs = _rows(v, dev, kshape, "v")
+    qp, qs = (None, 0) if q is None else _rows(q, dev, qshape, "q")
+    op, os_ = (None, 0) if q_out is None else _rows(q_out, dev, qshape, "q_out")
     if table is None:
         tp = rope_len = rot = 0
     else:
         if table.dim() != 2:
             raise ValueError("table must be [positions, rot_dim]")
         rope_len, rot = table.shape
-        tp = _arg(table, dev, _F32, table.shape, "table")
-    st = _lib.dr_rope_append(_byref(c), qp, qs, kp, ks, vp, vs, op, os_, _arg(row_start, dev, _I32, (B + 1,), "row_start"),
-                             _arg(start_pos, dev, _I32, (B,), "start_pos"),
-                             _arg(pos_offset, dev, _I32, (B,), "pos_offset"), tp, rope_len, rot, 1 if interleaved else 0,
-                             T, B, Hq, Hkv, D, _arg(err_flag, dev, _I32, (1,), "err_flag"), _stream_arg(stream, dev))
+        tp = _vec(table, dev, _F32, rope_len * rot, "table")
+    st = _lib.dr_rope_append(c, qp, qs, kp, ks, vp, vs, op, os_, _vec(row_start, dev, _I32, B + 1, "row_start"),
+                             _vec(start_pos, dev, _I32, B, "start_pos"),
+                             _vec(pos_offset, dev, _I32, B, "pos_offset"), tp, rope_len, rot, 1 if interleaved else 0,
+                             T, B, Hq, Hkv, D, _vec(err_flag, dev, _I32, 1, "err_flag"), _stream_arg(stream, dev))
     if st:
         raise DrError("dr_rope_append", st)
 
 
-def _score_opts(dev: int, causal: bool, softcap: float, slopes, prefix_len, first_key, T: int, B: int, Hq: int):
-    return dr_score_opts(1 if causal else 0, softcap, _arg(slopes, dev, _F32, (Hq,), "slopes"),
-                         _arg(prefix_len, dev, _I32, (B,), "prefix_len"), _arg(first_key, dev, _I32, (T,), "first_key"))
+def _score_opts(dev: int, causal: bool, softcap: float, slopes, prefix_len, first_key, T: int, B: int, Hq: int) -> bytes:
+    return _pack_opts(1 if causal else 0, softcap, _vec(slopes, dev, _F32, Hq, "slopes") or 0,
+                      _vec(prefix_len, dev, _I32, B, "prefix_len") or 0, _vec(first_key, dev, _I32, T, "first_key") or 0)
 
 
 def _sms() -> int:
@@ -446,7 +456,8 @@ def dr_prompt_attn_workspace(T: int, B: int, Hq: int, Hkv: int, max_len: int, nu
 def _workspace_arg(ws, dev: int):
     if ws is None:
         return None, 0
-    return _arg(ws, dev, _U8, ws.shape, "workspace"), ws.numel()
+    n = ws.numel()
+    return _vec(ws, dev, _U8, n, "workspace"), n
 
 
 def dr_prompt_attn(q: torch.Tensor, cache: KVCache, row_start: torch.Tensor, kv_len: torch.Tensor, out: torch.Tensor,
@@ -455,18 +466,18 @@ def dr_prompt_attn(q: torch.Tensor, cache: KVCache, row_start: torch.Tensor, kv_
                    max_len_hint: int = 0, scale: float = 0.0, workspace: torch.Tensor | None = None,
                    err_flag: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Attention of ragged tokens q [T,Hq,D]: row b's tokens are the last of its kv_len[b] keys in the cache."""
-    dev = _current_device()
+    dev = _device()
     qshape = _shape3(q, "q")
     T, Hq, D = qshape
     B, Hkv = kv_len.numel(), cache.k.shape[1]
-    c = _cache_arg(cache, dev, B, Hkv, D, "cache")
-    qp, qs = _rows_arg(q, dev, qshape, "q")
-    op, od = _out_arg(out, dev, qshape)
+    c = _cache(cache, dev, B, Hkv, D, "cache")
+    qp, qs = _rows(q, dev, qshape, "q")
+    op, od = _out(out, dev, qshape)
     o = _score_opts(dev, causal, softcap, slopes, prefix_len, first_key, T, B, Hq)
     wp, wn = _workspace_arg(workspace, dev)
-    st = _lib.dr_prompt_attn(qp, qs, _byref(c), _arg(row_start, dev, _I32, (B + 1,), "row_start"),
-                             _arg(kv_len, dev, _I32, (B,), "kv_len"), _byref(o), T, B, Hq, Hkv, D, max_len_hint, scale,
-                             op, od, wp, wn, _arg(err_flag, dev, _I32, (1,), "err_flag"), _stream_arg(stream, dev))
+    st = _lib.dr_prompt_attn(qp, qs, c, _vec(row_start, dev, _I32, B + 1, "row_start"),
+                             _vec(kv_len, dev, _I32, B, "kv_len"), o, T, B, Hq, Hkv, D, max_len_hint, scale,
+                             op, od, wp, wn, _vec(err_flag, dev, _I32, 1, "err_flag"), _stream_arg(stream, dev))
     if st:
         raise DrError("dr_prompt_attn", st)
     return out
@@ -483,22 +494,22 @@ def dr_shared_prefix_attn(q: torch.Tensor, prefix: KVCache, prefix_len: torch.Te
                           max_seq_len_hint: int = 0, scale: float = 0.0, err_flag: torch.Tensor | None = None,
                           stream=None) -> torch.Tensor:
     """One query per row, q [B,Hq,D], over the one-row cache `prefix` that all rows share and the row's own keys."""
-    dev = _current_device()
+    dev = _device()
     qshape = _shape3(q, "q")
     B, Hq, D = qshape
     Hkv = prefix.k.shape[1]
     if (cache is None) != (seq_len is None):
         raise ValueError("cache and seq_len go together")
-    pc = _cache_arg(prefix, dev, 1, Hkv, D, "prefix")
-    cp = None if cache is None else _byref(_cache_arg(cache, dev, B, Hkv, D, "cache"))
-    qp, qs = _rows_arg(q, dev, qshape, "q")
-    op, od = _out_arg(out, dev, qshape)
+    pc = _cache(prefix, dev, 1, Hkv, D, "prefix")
+    cp = None if cache is None else _cache(cache, dev, B, Hkv, D, "cache")
+    qp, qs = _rows(q, dev, qshape, "q")
+    op, od = _out(out, dev, qshape)
     o = _score_opts(dev, False, softcap, slopes, None, None, B, B, Hq)
     wp, wn = _workspace_arg(workspace, dev)
-    st = _lib.dr_shared_prefix_attn(qp, qs, _byref(pc), _arg(prefix_len, dev, _I32, (1,), "prefix_len"), cp,
-                                    _arg(seq_len, dev, _I32, (B,), "seq_len"), _byref(o), B, Hq, Hkv, D, max_prefix_hint,
+    st = _lib.dr_shared_prefix_attn(qp, qs, pc, _vec(prefix_len, dev, _I32, 1, "prefix_len"), cp,
+                                    _vec(seq_len, dev, _I32, B, "seq_len"), o, B, Hq, Hkv, D, max_prefix_hint,
                                     max_seq_len_hint, scale, op, od, wp, wn,
-                                    _arg(err_flag, dev, _I32, (1,), "err_flag"), _stream_arg(stream, dev))
+                                    _vec(err_flag, dev, _I32, 1, "err_flag"), _stream_arg(stream, dev))
     if st:
         raise DrError("dr_shared_prefix_attn", st)
     return out

@@ -924,12 +924,16 @@ cudaError_t launch_variant(const PromptParams &p, int splits, cudaStream_t strea
     auto kern = attn_tiles_kernel<kWG, kFp8, kPaged, kPlain>;
     constexpr size_t smem = C::kEnd + sizeof(Control);
     static_assert(smem <= (kWG == 1 ? 113 * 1024 : 227 * 1024), "shared memory");
-    cudaFuncAttributes fa;
-    cudaError_t e = cudaFuncGetAttributes(&fa, kern);
-    if (e != cudaSuccess) return e;
-    // the register split draws on what the launch gives: fewer would leave a warpgroup waiting
-    if (fa.numRegs * C::kThreads < 128 * kWG * C::kSoftmaxRegs + 32 * C::kOtherWarps * C::kOtherRegs) return cudaErrorInvalidConfiguration;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static std::atomic<uint64_t> ready{0};
+    const cudaError_t e = once_per_device(ready, [&]() -> cudaError_t {
+        cudaFuncAttributes fa;
+        const cudaError_t e1 = cudaFuncGetAttributes(&fa, kern);
+        if (e1 != cudaSuccess) return e1;
+        // the register split draws on what the launch gives: fewer would leave a warpgroup waiting
+        if (fa.numRegs * C::kThreads < 128 * kWG * C::kSoftmaxRegs + 32 * C::kOtherWarps * C::kOtherRegs)
+            return cudaErrorInvalidConfiguration;
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    });
     if (e != cudaSuccess) return e;
     CUtensorMap mk, mv;
     const long long rows = (long long)(kPaged ? p.num_blocks : (p.row_start ? p.B : 1)) * p.Hkv;

@@ -586,27 +586,41 @@ int plan_token_splits(long long items, int Hkv, int g, int max_len, bool fp8, in
     return s < 1 ? 1 : (int)s;
 }
 
-cudaError_t launch_attn_tokens(const PromptParams &p, bool paged, bool fp8, int splits, cudaStream_t stream) {
-    const int kn = p.g > 8 ? 2 : 1;
-    const unsigned hgroups = (unsigned)((p.g + 8 * kn - 1) / (8 * kn));
-    const dim3 grid((unsigned)((long long)p.B * p.Hkv * hgroups * splits));
-    void (*kern)(PromptParams, int);
-    const bool plain = p.cap_c1 == 0.f && !p.slopes;
-#define DR_PICK2(TILE, P, N) (plain ? attn_tokens_kernel<TILE, P, N, true> : attn_tokens_kernel<TILE, P, N, false>)
-#define DR_PICK(TILE, P) (kn == 2 ? DR_PICK2(TILE, P, 2) : DR_PICK2(TILE, P, 1))
-    if (fp8) kern = paged ? DR_PICK(Fp8Tile, true) : DR_PICK(Fp8Tile, false);
-    else kern = paged ? DR_PICK(Bf16Tile, true) : DR_PICK(Bf16Tile, false);
-#undef DR_PICK
-#undef DR_PICK2
+namespace {
+
+template <typename Tile, bool kPaged, int kN, bool kPlain>
+cudaError_t launch_variant(const PromptParams &p, int splits, cudaStream_t stream) {
+    auto kern = attn_tokens_kernel<Tile, kPaged, kN, kPlain>;
     // The loads in flight live in L1 (128 KB per SM at four CTAs): ask for no more shared memory than the CTAs need.
     // Left to itself an SM keeps the split of the kernel before, and behind the tile kernel, which takes all of it,
     // 128 rows of 64..2048 own keys took 125 us instead of 97.
-    const size_t each = (kn == 2 ? sizeof(Shared<2>) : sizeof(Shared<1>)) + 1024;
-    const int ctas = kn == 2 ? ctas_per_sm<Bf16Tile, 2>() : fp8 ? ctas_per_sm<Fp8Tile, 1>() : ctas_per_sm<Bf16Tile, 1>();
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                               (int)((ctas * each * 100 + 228 * 1024 - 1) / (228 * 1024)));
+    static std::atomic<uint64_t> ready{0};
+    const cudaError_t e = once_per_device(ready, [&] {
+        constexpr size_t all = ctas_per_sm<Tile, kN>() * (sizeof(Shared<kN>) + 1024);
+        return cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                    (int)((all * 100 + 228 * 1024 - 1) / (228 * 1024)));
+    });
     if (e != cudaSuccess) return e;
-    return launch_kernel(kern, grid, dim3(kThreads), 0, stream, (unsigned)splits, p, splits);
+    const unsigned hgroups = (unsigned)((p.g + 8 * kN - 1) / (8 * kN));
+    return launch_kernel(kern, dim3((unsigned)((long long)p.B * p.Hkv * hgroups * splits)), dim3(kThreads), 0, stream,
+                         (unsigned)splits, p, splits);
+}
+
+template <typename Tile, bool kPaged>
+cudaError_t launch_layout(const PromptParams &p, int splits, cudaStream_t stream) {
+    const bool plain = p.cap_c1 == 0.f && !p.slopes;
+    if (p.g > 8)
+        return plain ? launch_variant<Tile, kPaged, 2, true>(p, splits, stream)
+                     : launch_variant<Tile, kPaged, 2, false>(p, splits, stream);
+    return plain ? launch_variant<Tile, kPaged, 1, true>(p, splits, stream)
+                 : launch_variant<Tile, kPaged, 1, false>(p, splits, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_tokens(const PromptParams &p, bool paged, bool fp8, int splits, cudaStream_t stream) {
+    if (fp8) return paged ? launch_layout<Fp8Tile, true>(p, splits, stream) : launch_layout<Fp8Tile, false>(p, splits, stream);
+    return paged ? launch_layout<Bf16Tile, true>(p, splits, stream) : launch_layout<Bf16Tile, false>(p, splits, stream);
 }
 
 }  // namespace dr

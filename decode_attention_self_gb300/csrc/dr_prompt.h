@@ -2,9 +2,24 @@
 // Launch helpers take validated arguments; dr_prompt_api.cu owns all argument checking.
 #pragma once
 
+#include <atomic>
+
 #include "dr_internal.h"
 
 namespace dr {
+
+// Runs a kernel's one-time setup once per device (done: one bit per device; a failure is tried again).
+template <typename F>
+cudaError_t once_per_device(std::atomic<uint64_t> &done, F &&setup) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = setup();
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
+}
 
 struct RopeAppendParams {
     void *k_cache, *v_cache;            // bf16 or e4m3 cache
