@@ -86,6 +86,13 @@ __device__ __forceinline__ bool nonfinite16(uint32_t w, uint32_t exp_mask) {
     return (w & exp_mask) == exp_mask || ((w >> 16) & exp_mask) == exp_mask;
 }
 
+// 32-byte store: a thread's output row is 128 bytes or more, and a request of the warp touches 32 rows.
+__device__ __forceinline__ void st_32(void *p, const uint32_t *w) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
 // Zeroes the NaN codes (0x7F, 0xFF) among four e4m3 codes; whether there was one.
 __device__ __forceinline__ bool zero_nan_codes(uint32_t &w) {
     const uint32_t t = ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;   // bit 7 of the bytes that hold one
@@ -811,27 +818,32 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
             if (p.part_ml) {
                 const size_t at = (size_t)split * ((size_t)p.T * p.Hq) + orow;
                 p.part_ml[at] = make_float2(m, l);
-                float4 *dst = reinterpret_cast<float4 *>(p.part_acc + at * kD);
+                float *dst = p.part_acc + at * kD;
 #pragma unroll
-                for (int c = 0; c < kD / 4; ++c)
-                    dst[c] = make_float4(o[4 * c] * p.out_scale, o[4 * c + 1] * p.out_scale, o[4 * c + 2] * p.out_scale,
-                                         o[4 * c + 3] * p.out_scale);
+                for (int c = 0; c < kD; c += 8) {
+                    uint32_t w[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(o[c + e] * p.out_scale);
+                    st_32(dst + c, w);
+                }
             } else {
                 const float inv = l == 0.f ? 0.f : p.out_scale / l;
                 const bool none = l == 0.f;
 #pragma unroll
                 for (int c = 0; c < kD; ++c) o[c] = none ? 0.f : o[c] * inv;
                 if (p.out_f32) {
-                    float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(p.out) + orow * kD);
+                    float *dst = static_cast<float *>(p.out) + orow * kD;
 #pragma unroll
-                    for (int c = 0; c < kD / 4; ++c)
-                        dst[c] = make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+                    for (int c = 0; c < kD; c += 8) st_32(dst + c, reinterpret_cast<const uint32_t *>(o + c));
                 } else {
-                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + orow * kD);
+                    uint16_t *dst = static_cast<uint16_t *>(p.out) + orow * kD;
 #pragma unroll
-                    for (int c = 0; c < kD / 8; ++c)
-                        dst[c] = make_uint4(pack_bf16(o[8 * c], o[8 * c + 1]), pack_bf16(o[8 * c + 2], o[8 * c + 3]),
-                                            pack_bf16(o[8 * c + 4], o[8 * c + 5]), pack_bf16(o[8 * c + 6], o[8 * c + 7]));
+                    for (int c = 0; c < kD; c += 16) {
+                        uint32_t w[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) w[e] = pack_bf16(o[c + 2 * e], o[c + 2 * e + 1]);
+                        st_32(dst + c, w);
+                    }
                 }
             }
         }

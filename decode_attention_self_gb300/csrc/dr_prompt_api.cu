@@ -7,6 +7,8 @@
 namespace {
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// the attention kernels read keys and write outputs and states 32 bytes at a time
+bool aligned32(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 
 // Validates a cache description; on success stores the keys a row can hold in *cap.
 dr_status check_cache(const dr_kv_cache *c, int *cap) {
@@ -83,7 +85,7 @@ int most_splits(int T, int g, int Hkv, int max_len, int sms) {
 size_t states_bytes(int splits, int T, int Hq) {
     return (size_t)splits * T * Hq * (dr::kHeadDim + 2) * sizeof(float);
 }
-// The sums first: they keep the workspace's 16-byte alignment.
+// The sums first: they keep the workspace's alignment.
 void set_states(dr::PromptParams &p, void *ws, int splits) {
     p.part_acc = static_cast<float *>(ws);
     p.part_ml = reinterpret_cast<float2 *>(p.part_acc + (size_t)splits * p.T * p.Hq * dr::kHeadDim);
@@ -165,10 +167,10 @@ dr_status dr_prompt_attn(const void *q, int64_t q_stride, const dr_kv_cache *cac
     if (st != DR_OK) return st;
     st = check_scores(scale, opts);
     if (st != DR_OK) return st;
-    if (!q || !row_start || !kv_len || !out || !aligned16(q) || !aligned16(out) || bad_stride(q_stride, Hq))
+    if (!q || !row_start || !kv_len || !out || !aligned16(q) || !aligned32(out) || bad_stride(q_stride, Hq))
         return DR_ERR_INVALID_ARG;
     if (out_dtype != DR_BF16 && out_dtype != DR_F32) return DR_ERR_INVALID_ARG;
-    if (!aligned16(ws)) return DR_ERR_INVALID_ARG;
+    if (!aligned32(ws) || !aligned32(cache->k) || !aligned32(cache->v)) return DR_ERR_INVALID_ARG;
     if (opts && opts->prefix_len && !opts->causal) return DR_ERR_INVALID_ARG;
     dr::PromptParams p = {};
     p.q = static_cast<const uint16_t *>(q);
@@ -238,11 +240,13 @@ dr_status dr_shared_prefix_attn(const void *q, int64_t q_stride, const dr_kv_cac
     st = check_scores(scale, opts);
     if (st != DR_OK) return st;
     if (opts && (opts->prefix_len || opts->first_key)) return DR_ERR_INVALID_ARG;
-    if (!q || !prefix_len || !out || !aligned16(q) || !aligned16(out) || bad_stride(q_stride, Hq))
+    if (!q || !prefix_len || !out || !aligned16(q) || !aligned32(out) || bad_stride(q_stride, Hq))
         return DR_ERR_INVALID_ARG;
     if (out_dtype != DR_BF16 && out_dtype != DR_F32) return DR_ERR_INVALID_ARG;
     const int sms = dr::current_device_sms();
-    if (!ws || !aligned16(ws) || ws_bytes < states_bytes(1, B, Hq)) return DR_ERR_INVALID_ARG;
+    if (!aligned32(prefix->k) || !aligned32(prefix->v) || (cache && (!aligned32(cache->k) || !aligned32(cache->v))))
+        return DR_ERR_INVALID_ARG;
+    if (!ws || !aligned32(ws) || ws_bytes < states_bytes(1, B, Hq)) return DR_ERR_INVALID_ARG;
     if (sms <= 0) return DR_ERR_CUDA;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
 

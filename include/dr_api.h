@@ -418,7 +418,7 @@ typedef struct dr_score_opts {
  * do not reach the result whatever they hold.
  *
  *   q        : [T][Hq][D] bf16 (device, 16-byte aligned), tokens q_stride elements apart (multiple of 8, >= Hq*D)
- *   cache    : see dr_kv_cache, with Hkv heads; B rows
+ *   cache    : see dr_kv_cache, with Hkv heads; B rows; k and v 32-byte aligned
  *   row_start: [B+1] int32 (device), rising from 0 to at most T (DR_ERRF_ROW_START otherwise); rows may be empty;
  *              outputs of tokens from row_start[B] on are left as they are
  *   kv_len   : [B] int32 (device), keys per row, its new tokens' included: n <= kv_len[b] <= capacity (clamped to
@@ -426,8 +426,8 @@ typedef struct dr_score_opts {
  *   opts     : nullable (causal, nothing else)
  *   max_len_hint : an upper bound the caller knows for kv_len (<= 0: the capacity); tunes the work split only
  *   scale    : <= 0 selects 1/sqrt(D)
- *   out      : [T][Hq][D] in out_dtype (device, 16-byte aligned)
- *   ws       : nullable workspace (device, 16-byte aligned) of ws_bytes; with at least
+ *   out      : [T][Hq][D] in out_dtype (device, 32-byte aligned)
+ *   ws       : nullable workspace (device, 32-byte aligned) of ws_bytes; with at least
  *              dr_prompt_attn_workspace bytes few queries over many keys are spread over the GPU.  Its contents
  *              mean nothing before and after the call; calls that may overlap need one each
  *   err_flag : nullable device int32 (DR_ERRF_ROW_START, DR_ERRF_SEQ_LEN, DR_ERRF_BLOCK_ID, DR_ERRF_TIMEOUT)
@@ -453,14 +453,15 @@ size_t dr_prompt_attn_workspace(int T, int B, int Hq, int Hkv, int max_len, int 
  * outputs zeros.  For several prefixes, one call per group of rows.
  *
  *   q        : [B][Hq][D] bf16 (device, 16-byte aligned), rows q_stride elements apart (multiple of 8, >= Hq*D)
- *   prefix   : cache of one row (row 0) with Hkv heads; paged: its blocks may lie in the same pool as cache's
+ *   prefix   : cache of one row (row 0) with Hkv heads, k and v 32-byte aligned (cache's too); paged: its blocks may
+ *              lie in the same pool as cache's
  *   prefix_len : [1] int32 (device), 0 <= prefix_len[0] <= the prefix's capacity (else clamped, DR_ERRF_SEQ_LEN)
  *   cache, seq_len : the rows' own keys, B rows with Hkv heads, and [B] int32 (device), 0 <= seq_len[b] <= capacity
  *              (else clamped, DR_ERRF_SEQ_LEN); both null: rows have no own keys (a description that a batch shares)
  *   opts     : nullable; softcap and slopes are used, prefix_len and first_key must be null
  *   max_prefix_hint, max_seq_len_hint : upper bounds the caller knows (<= 0: the capacities); tune the split only
- *   out      : [B][Hq][D] in out_dtype (device, 16-byte aligned)
- *   ws       : workspace (device, 16-byte aligned) of ws_bytes, at least dr_shared_prefix_attn_workspace with
+ *   out      : [B][Hq][D] in out_dtype (device, 32-byte aligned)
+ *   ws       : workspace (device, 32-byte aligned) of ws_bytes, at least dr_shared_prefix_attn_workspace with
  *              max_prefix = 1 (DR_ERR_INVALID_ARG below); as much as it asks for the real bound spreads a prefix over
  *              the GPU.  Its contents mean nothing before and after the call; calls that may overlap need one each
  *   err_flag : nullable device int32 (DR_ERRF_SEQ_LEN, DR_ERRF_BLOCK_ID, DR_ERRF_TIMEOUT)

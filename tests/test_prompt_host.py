@@ -85,7 +85,8 @@ def prompt(lib, cache=None, q=FAKE, qs=1024, rs=FAKE, kl=FAKE, opts=None, T=4, B
     (dict(qs=1029), 1), (dict(od=7), 1), (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1),
     (dict(ws=FAKE + 8, ws_bytes=64), 1), (dict(opts=dict(causal=2)), 1), (dict(opts=dict(causal=1, softcap=-1.0)), 1),
     (dict(opts=dict(causal=1, softcap=float("nan"))), 1), (dict(opts=dict(causal=1, softcap=1e-9)), 1),
-    (dict(opts=dict(causal=0, prefix_len=FAKE)), 1), (dict(Hq=258, Hkv=2, qs=1 << 15), 2),
+    (dict(out=FAKE + 16), 1), (dict(ws=FAKE + 16, ws_bytes=64), 1), (dict(cache=dict(GOOD, k=FAKE + 16)), 1),
+    (dict(cache=dict(GOOD, v=FAKE + 16)), 1), (dict(opts=dict(causal=0, prefix_len=FAKE)), 1), (dict(Hq=258, Hkv=2, qs=1 << 15), 2),
 ])
 def test_prompt_attn_refusals(lib, bad, status):
     assert prompt(lib, **bad) == status
@@ -109,7 +110,8 @@ def shared(lib, prefix=None, own=None, seq=FAKE, opts=None, q=FAKE, qs=1024, pl=
     (dict(B=0), 1), (dict(Hkv=3), 1), (dict(D=128), 2), (dict(q=None), 1), (dict(pl=None), 1), (dict(out=None), 1),
     (dict(seq=None), 1), (dict(own="none"), 1), (dict(ws=None), 1), (dict(ws=FAKE + 8), 1),
     (dict(ws_bytes=2 * 16 * 66 * 4 - 1), 1), (dict(opts=dict(first_key=FAKE)), 1), (dict(opts=dict(causal=1, prefix_len=FAKE)), 1),
-    (dict(od=3), 1), (dict(qs=8), 1), (dict(scale=float("nan")), 1), (dict(out=FAKE + 4), 1),
+    (dict(od=3), 1), (dict(qs=8), 1), (dict(scale=float("nan")), 1), (dict(out=FAKE + 4), 1), (dict(out=FAKE + 16), 1),
+    (dict(ws=FAKE + 16), 1), (dict(prefix=dict(GOOD, k=FAKE + 16)), 1), (dict(own=dict(GOOD, v=FAKE + 16)), 1),
 ])
 def test_shared_prefix_refusals(lib, bad, status):
     assert shared(lib, **bad) == status
