@@ -646,10 +646,10 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
         int done = 0, pass = 0;   // tiles so far
         do {
         float m = -INFINITY, mref = 0.f, l = 0.f;
-        bool ok = true;
+        bool ok = true, s_there = false;
         for (int j = j0; j < j1; ++j) {
             const int key0 = kbase + j * kKeys;
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl.s_full[wg], done & 1, gave_up));
+            if (!s_there) ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl.s_full[wg], done & 1, gave_up));
             if (!ok) break;
             fence_after();
             float s[kKeys];
@@ -723,6 +723,9 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
                 m = mref = mx;
                 l *= corr;
             }
+            // Asked before the exponentials, needed after them
+            const bool o_there = j > j0 && __all_sync(0xFFFFFFFFu, mbar_test(&ctl.o_done[wg], (done - 1) & 1));
+            const bool moved = __any_sync(0xFFFFFFFFu, corr != 1.0f);
             float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
             const float2 mul2 = make_float2(mul, mul), off2 = make_float2(-mref, -mref);
             uint32_t pk[kKeys / 2];
@@ -742,10 +745,10 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
             l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
             if (j > j0) {
                 // P and O are the previous tile's until its product is done
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl.o_done[wg], (done - 1) & 1, gave_up));
+                if (!o_there) ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl.o_done[wg], (done - 1) & 1, gave_up));
                 if (!ok) break;
                 fence_after();
-                if (__any_sync(0xFFFFFFFFu, corr != 1.0f)) {
+                if (moved) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         float o[32];
@@ -758,6 +761,7 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
                     }
                 }
             }
+            s_there = __all_sync(0xFFFFFFFFu, mbar_test(&ctl.s_full[wg], (done + 1) & 1));
             st32(tpw, pk);
             st32(tpw + 32, pk + 32);
             wait_st();
