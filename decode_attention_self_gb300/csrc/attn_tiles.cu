@@ -6,8 +6,8 @@
 // The g query heads of a kv head and consecutive tokens fill a tile's rows together (row = token * g + head), so one
 // pass over the keys serves them all.  A CTA holds one tile per softmax warpgroup (kWG of them) and walks its keys
 // 128 at a time:
-//   producer warp     TMA loads of K and V tiles (a paged tile is eight 16-key boxes, lane i fetching block i; blocks
-//                     outside the pool and past the last visible key come from an out-of-range coordinate: zeros)
+//   producer warps    TMA loads of K and of V tiles (a paged tile is eight 16-key boxes; blocks outside the pool and past
+//                     the last visible key come from an out-of-range coordinate: zeros)
 //   MMA warp          S = Q K^T into tensor memory, one tile ahead of the softmax; O += P V with P read from tensor
 //                     memory and V as the MN-major operand
 //   softmax warps     one thread per query row: S to registers, mask, running maximum, weights, P back to tensor
@@ -40,8 +40,8 @@ constexpr uint32_t kTileBytes = kKeys * kD * 2;   // a K, V or Q tile of 16-bit 
 
 template <int kWG, bool kFp8>
 struct Config {
-    static constexpr int kHelperWarps = 2;                       // per operand that they work on
-    static constexpr int kOtherWarps = kFp8 ? 8 : 4;             // producer, MMA, helpers (e4m3: K's, V's; one idle)
+    static constexpr int kHelperWarps = kFp8 ? 2 : 1;            // per operand that they work on (e4m3: K and V; bf16: V)
+    static constexpr int kOtherWarps = kFp8 ? 8 : 4;             // two producers, an MMA warp per tile, helpers
     static constexpr int kThreads = 128 * kWG + 32 * kOtherWarps;
     static constexpr int kCtasPerSm = kWG == 1 ? 2 : 1;
     static constexpr int kTma = kFp8 ? 4 : (kWG == 1 ? 3 : 4);   // stages that TMA fills (bf16: the MMA reads them)
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
     Control &ctl = *reinterpret_cast<Control *>(smem + C::kEnd);
     const PromptParams &p = tp.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr int kProducer = 4 * kWG, kMmaWarp = kProducer + 1, kHelper = kMmaWarp + kWG;   // an MMA warp per tile
+    constexpr int kProducer = 4 * kWG, kMmaWarp = kProducer + 2, kHelper = kMmaWarp + kWG;   // an MMA warp per tile
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kMaxStages; ++i) {
@@ -342,60 +342,63 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
 
     if (warp >= kProducer) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
-        if (warp == kProducer) {
-            const int kv_row = kPaged ? 0 : b * p.Hkv + hk;
-            // Block ids of four tiles at a time, one per lane, loaded four tiles ahead (a load per tile, waited for in
-            // turn, took longer than the tile's arithmetic): lane 8 y + x has block x of tile y of the group.  z of a
-            // block that is not there is out of range.
+        if (warp < kMmaWarp) {
+            // K by the first producer warp, V by the second.  Block ids of four tiles at a time, one per lane, loaded four
+            // tiles ahead (a load per tile, waited for in turn, took longer than the tile's arithmetic): lane 8 y + x has
+            // block x of tile y of the group.  z of a block that is not there is out of range.
+            const bool is_v = warp != kProducer;
+            const CUtensorMap *map = is_v ? &map_v : &map_k;
+            uint64_t *full = is_v ? ctl.v_full : ctl.k_full, *empty = is_v ? ctl.v_empty : ctl.k_empty;
+            const uint32_t ring = smem_u32(smem + (kFp8 ? (is_v ? C::kRawV : C::kRawK) : (is_v ? C::kV : C::kK)));
+            const int stages = C::kTma, kv_row = kPaged ? 0 : b * p.Hkv + hk;
+            const bool leader = elect_one();
             const auto group_ids = [&](int j) -> int {   // tiles j .. j + 3
                 const int key = kbase + j * kKeys + lane * kBlockKeys;
                 return j < ce && key < uhi ? __ldg(p.table + (size_t)b * p.max_blocks + key / kBlockKeys) : -1;
             };
             int s = 0, round = 0, pass = 0;
             do {
-            int ids = 0, ids_next = 0;
-            if (kPaged) ids_next = group_ids(cb);
-            for (int j = cb, i = 0; j < ce; ++j, ++i) {
-                if (round > 0 && !__all_sync(0xFFFFFFFFu, mbar_wait(&ctl.k_empty[s], (round - 1) & 1, gave_up))) break;
-                unsigned bits = 0xFFu;
-                int z = 0;
-                if (kPaged) {
-                    if ((i & 3) == 0) {
-                        ids = ids_next;
-                        ids_next = group_ids(j + 4);
+                int ids = 0, ids_next = 0;
+                if (kPaged) ids_next = group_ids(cb);
+                for (int j = cb, i = 0; j < ce; ++j, ++i) {
+                    unsigned bits = 0xFFu;
+                    int z[8] = {};
+                    if (kPaged) {
+                        if ((i & 3) == 0) {
+                            ids = ids_next;
+                            ids_next = group_ids(j + 4);
+                            // a block that some row sees and that is not in the pool
+                            if (!is_v && j < ce && kbase + j * kKeys + lane * kBlockKeys < uhi &&
+                                (unsigned)ids >= (unsigned)p.num_blocks && kbase + j * kKeys + lane * kBlockKeys < kbase + ce * kKeys)
+                                flag_error(p.err, DR_ERRF_BLOCK_ID);
+                            ids = (unsigned)ids < (unsigned)p.num_blocks ? ids * p.Hkv + hk : -1;
+                        }
+                        bits = (__ballot_sync(0xFFFFFFFFu, ids >= 0) >> ((i & 3) * 8)) & 0xFFu;
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) {
+                            z[x] = __shfl_sync(0xFFFFFFFFu, ids, (i & 3) * 8 + x);
+                            if (z[x] < 0) z[x] = p.num_blocks * p.Hkv;
+                        }
                     }
-                    const int blk = __shfl_sync(0xFFFFFFFFu, ids, (i & 3) * 8 + (lane & 7));
-                    const bool there = (unsigned)blk < (unsigned)p.num_blocks;
-                    const bool wanted = kbase + j * kKeys + (lane & 7) * kBlockKeys < uhi;
-                    if (wanted && !there && lane < 8) flag_error(p.err, DR_ERRF_BLOCK_ID);
-                    bits = __ballot_sync(0xFFFFFFFFu, there) & 0xFFu;
-                    z = there ? blk * p.Hkv + hk : p.num_blocks * p.Hkv;
+                    if (round > 0 && !__all_sync(0xFFFFFFFFu, mbar_wait(&empty[s], (round - 1) & 1, gave_up))) break;
+                    const uint32_t dst = ring + s * C::kTmaBytes;
+                    // one lane of a converged warp: eight lanes with a box each take turns, and took over 100 cycles per box
+                    if (leader) {
+                        if (!is_v) ctl.bits[i % kBitsRing] = (int)bits;
+                        mbar_expect_tx(&full[s], C::kTmaBytes);
+                        if (kPaged) {
+#pragma unroll
+                            for (int x = 0; x < 8; ++x) tma_load_3d(dst + x * (C::kTmaBytes / 8), map, 0, 0, z[x], &full[s]);
+                        } else {
+                            tma_load_3d(dst, map, 0, kbase + j * kKeys, kv_row, &full[s]);
+                        }
+                    }
+                    __syncwarp();
+                    if (++s == stages) {
+                        s = 0;
+                        ++round;
+                    }
                 }
-                uint8_t *kd = smem + (kFp8 ? C::kRawK + s * C::kTmaBytes : C::kK + s * kTileBytes);
-                uint8_t *vd = smem + (kFp8 ? C::kRawV + s * C::kTmaBytes : C::kV + s * kTileBytes);
-                if (lane == 0) {
-                    ctl.bits[i % kBitsRing] = (int)bits;
-                    mbar_expect_tx(&ctl.k_full[s], C::kTmaBytes);
-                }
-                __syncwarp();
-                if (kPaged) {
-                    if (lane < 8) tma_load_3d(smem_u32(kd + lane * (C::kTmaBytes / 8)), &map_k, 0, 0, z, &ctl.k_full[s]);
-                } else if (lane == 0) {
-                    tma_load_3d(smem_u32(kd), &map_k, 0, kbase + j * kKeys, kv_row, &ctl.k_full[s]);
-                }
-                if (round > 0 && !__all_sync(0xFFFFFFFFu, mbar_wait(&ctl.v_empty[s], (round - 1) & 1, gave_up))) break;
-                if (lane == 0) mbar_expect_tx(&ctl.v_full[s], C::kTmaBytes);
-                __syncwarp();
-                if (kPaged) {
-                    if (lane < 8) tma_load_3d(smem_u32(vd + lane * (C::kTmaBytes / 8)), &map_v, 0, 0, z, &ctl.v_full[s]);
-                } else if (lane == 0) {
-                    tma_load_3d(smem_u32(vd), &map_v, 0, kbase + j * kKeys, kv_row, &ctl.v_full[s]);
-                }
-                if (++s == C::kTma) {
-                    s = 0;
-                    ++round;
-                }
-            }
             } while (again(pass++));
         } else if (warp < kHelper) {
             // The whole warp waits, one lane issues: descriptors stay warp-uniform (computed by one lane alone, each MMA

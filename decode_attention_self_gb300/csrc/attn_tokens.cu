@@ -157,9 +157,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<Tile, kN>())
     const int nheads = min(kHeads, p.g - hg * kHeads);      // query heads of this CTA
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
 
-    // After the tile kernel of the same call only the states that it leaves have to be waited for: it let this grid
-    // start once all of its CTAs had waited for the kernels before it.
-    if (!p.part_ml) pdl_wait();
+    // Behind the tile kernel of the same call nothing but the states that it leaves has to be waited for: it let this grid
+    // start once all of its CTAs had waited for the kernels before it.  (The wait still comes, at the end: who waits for
+    // this grid waits for that one.)
+    if (!p.after_tiles) pdl_wait();
     int s0 = b, n = 1;
     int L = p.kv_len ? __ldg(p.kv_len + b) : 0;
     const int prefix = p.prefix_len ? __ldg(p.prefix_len + b) : 0;
@@ -171,7 +172,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<Tile, kN>())
         s0 = min(max(s0, 0), p.T);
         n = min(max(s1, s0), p.T) - s0;
     }
-    if (n == 0 || n > p.few_max) return;   // nothing here, or the tile kernel's row (the same in the cluster)
+    if (n == 0 || n > p.few_max) {   // nothing here, or the tile kernel's row (the same in the cluster)
+        if (p.after_tiles) pdl_wait();
+        return;
+    }
     const int min_len = p.row_start ? n : 0;
     if (L < min_len || L > p.cap) {
         if (split == 0 && hy == 0 && threadIdx.x == 0 && p.kv_len) flag_error(p.err, DR_ERRF_SEQ_LEN);
@@ -564,6 +568,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<Tile, kN>())
         }
         __syncthreads();
     }
+    if (p.after_tiles && !p.part_ml) pdl_wait();
     pdl_trigger();
 }
 

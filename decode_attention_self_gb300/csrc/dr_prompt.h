@@ -63,6 +63,8 @@ struct PromptParams {
     int32_t *err;
     // the most tokens a row may have to be taken by the token kernel (more: the tile kernel's)
     int32_t few_max;
+    // token kernel: launched right behind the tile kernel of the same call
+    int32_t after_tiles;
     // tile kernel: queries of a shared prefix stand own_len[t] keys past its end (null: at their row's last keys)
     const int32_t *own_len;
     // softmax states of key ranges attended before: [nparts][rows = T*Hq] (m, l) and [nparts][rows][64]; null: none

@@ -200,19 +200,20 @@ dr_status dr_prompt_attn(const void *q, int64_t q_stride, const dr_kv_cache *cac
     p.few_max = 1;
     const bool few = B > 1 || T == 1, many = T > B;
     if (!many) p.few_max = 0x7FFFFFFF;
-    if (few) {
-        const cudaError_t e =
-            dr::launch_attn_tokens(p, paged, fp8, dr::plan_token_splits(B, Hkv, p.g, len, fp8, sms), cs);
-        if (e != cudaSuccess || !many) return from_cuda(e);
-    } else {
-        p.few_max = 0;
-    }
+    const int few_splits = dr::plan_token_splits(B, Hkv, p.g, len, fp8, sms);
+    if (!many) return from_cuda(dr::launch_attn_tokens(p, paged, fp8, few_splits, cs));
+    if (!few) p.few_max = 0;
+    dr::PromptParams tp = p;
     int splits = dr::plan_tile_splits(T, p.g, Hkv, len, fp8, sms);
     while (splits > 1 && (!ws || ws_bytes < states_bytes(splits, T, Hq))) --splits;
-    if (splits > 1) set_states(p, ws, splits);
-    const cudaError_t e = dr::launch_attn_tiles(p, paged, fp8, splits, cs);
-    if (e != cudaSuccess || splits == 1) return from_cuda(e);
-    return from_cuda(dr::launch_attn_join(p, cs));
+    if (splits > 1) set_states(tp, ws, splits);
+    cudaError_t e = dr::launch_attn_tiles(tp, paged, fp8, splits, cs);
+    if (e == cudaSuccess && few) {
+        p.after_tiles = 1;
+        e = dr::launch_attn_tokens(p, paged, fp8, few_splits, cs);
+    }
+    if (e == cudaSuccess && splits > 1) e = dr::launch_attn_join(tp, cs);
+    return from_cuda(e);
 }
 
 size_t dr_prompt_attn_workspace(int T, int B, int Hq, int Hkv, int max_len, int num_sms) {
@@ -279,6 +280,7 @@ dr_status dr_shared_prefix_attn(const void *q, int64_t q_stride, const dr_kv_cac
     p.kv_len = seq_len;
     p.own_len = nullptr;
     p.few_max = 0x7FFFFFFF;
+    p.after_tiles = 1;
     const bool paged = own->layout == DR_KV_PAGED, fp8 = own->kv_dtype == DR_KV_FP8_E4M3;
     const int len = !cache ? 1 : max_seq_len_hint > 0 && max_seq_len_hint < cap ? max_seq_len_hint : cap;
     return from_cuda(dr::launch_attn_tokens(p, paged, fp8, dr::plan_token_splits(B, Hkv, p.g, len, fp8, sms), cs));
