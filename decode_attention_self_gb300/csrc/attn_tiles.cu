@@ -107,6 +107,27 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
+// Weights 2^(s mul - mref) of N scores, packed in pairs; their sum (of the weights before they are rounded).
+template <int N, bool kF16>
+__device__ __forceinline__ float weights(const float (&s)[N], float mul, float mref, uint32_t (&pk)[N / 2]) {
+    float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+    const float2 mul2 = make_float2(mul, mul), off2 = make_float2(-mref, -mref);
+#pragma unroll
+    for (int c = 0; c < N; c += 4) {
+        float2 x = __ffma2_rn(make_float2(s[c], s[c + 1]), mul2, off2);
+        float2 y = __ffma2_rn(make_float2(s[c + 2], s[c + 3]), mul2, off2);
+        x.x = fast_exp2(x.x);
+        x.y = fast_exp2(x.y);
+        y.x = fast_exp2(y.x);
+        y.y = fast_exp2(y.y);
+        sum0 = __fadd2_rn(sum0, x);
+        sum1 = __fadd2_rn(sum1, y);
+        pk[c / 2] = kF16 ? pack_f16(x.x, x.y) : pack_bf16(x.x, x.y);
+        pk[c / 2 + 1] = kF16 ? pack_f16(y.x, y.y) : pack_bf16(y.x, y.y);
+    }
+    return (sum0.x + sum0.y) + (sum1.x + sum1.y);
+}
+
 // Keys [lo, hi) that query i of a row of n queries and L keys sees, and its position.
 __device__ __forceinline__ void visible(const PromptParams &p, int t, int i, int n, int L, int prefix, int &lo, int &hi,
                                         int &pos) {
@@ -646,6 +667,8 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
         const bool capped = !kPlain && p.cap_c1 != 0.f, biased = !kPlain && p.slopes != nullptr;
         const float slope = biased && valid ? __ldg(p.slopes + head) * 1.4426950408889634f : 0.f;
         const float mul = capped || biased ? 1.0f : scale;
+        // A row that sees no key (or is none) goes along with the others of its warp; its state is put right at the end
+        const bool sees = hi > lo, any_sees = __any_sync(0xFFFFFFFFu, sees);
         int done = 0, pass = 0;   // tiles so far
         do {
         float m = -INFINITY, mref = 0.f, l = 0.f;
@@ -655,101 +678,20 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
             if (!s_there) ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl.s_full[wg], done & 1, gave_up));
             if (!ok) break;
             fence_after();
-            float s[kKeys];
-            ld32(ts, s);
-            ld32(ts + 32, s + 32);
             const int bits = ctl.bits[(j - cb) % kBitsRing];
-            wait_ld();
-            pin32(s);
-            pin32(s + 32);
-            ld32(ts + 64, s + 64);
-            ld32(ts + 96, s + 96);
-            float top[8];
-#pragma unroll
-            for (int c = 0; c < 8; ++c) top[c] = s[c];
-#pragma unroll
-            for (int c = 8; c < 56; c += 16)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) top[e] = max3(top[e], s[c + 2 * e], s[c + 2 * e + 1]);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) top[e] = fmaxf(top[e], s[56 + e]);
-            wait_ld();
-            pin32(s + 64);
-            pin32(s + 96);
-            fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl.s_free[wg]);
-
-            if (capped) {
-#pragma unroll
-                for (int c = 0; c < kKeys; ++c) s[c] = capped_score(s[c], p.cap_c1, c2);
-            } else if (biased) {
-#pragma unroll
-                for (int c = 0; c < kKeys; ++c) s[c] *= scale;
-            }
-            if (biased) {
-                const float d0 = (float)(pos - key0);
-#pragma unroll
-                for (int c = 0; c < kKeys; ++c) s[c] = fmaf(-slope, fabsf(d0 - (float)c), s[c]);
-            }
-            const bool whole = key0 >= lo && key0 + kKeys <= hi && bits == 0xFF;
-            if (__builtin_expect(__any_sync(0xFFFFFFFFu, !whole), 0)) {
-                const int a = lo - key0, e = hi - key0;
-#pragma unroll
-                for (int c = 0; c < kKeys; ++c)
-                    if (c < a || c >= e) s[c] = -INFINITY;
-                if (bits != 0xFF) {   // blocks that are not there
-#pragma unroll
-                    for (int c = 0; c < kKeys; ++c)
-                        if (!((bits >> (c / kBlockKeys)) & 1)) s[c] = -INFINITY;
-                }
-            }
-            const bool touched = capped || biased || __any_sync(0xFFFFFFFFu, !whole);   // s is not what was loaded
-            if (touched) {
-#pragma unroll
-                for (int c = 0; c < 8; ++c) top[c] = s[c];
-#pragma unroll
-                for (int c = 8; c < 56; c += 16)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) top[e] = max3(top[e], s[c + 2 * e], s[c + 2 * e + 1]);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) top[e] = fmaxf(top[e], s[56 + e]);
-            }
-#pragma unroll
-            for (int c = 64; c < kKeys; c += 16)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) top[e] = max3(top[e], s[c + 2 * e], s[c + 2 * e + 1]);
-            const float mx = fmaxf(max3(max3(top[0], top[1], top[2]), top[3], top[4]), max3(top[5], top[6], top[7])) * mul;
+            const bool whole = !sees || (key0 >= lo && key0 + kKeys <= hi && bits == 0xFF);
             float corr = 1.0f;
-            if (mx > m + kSlack) {   // also the first visible key (m = -inf)
-                corr = fast_exp2(m - mx);
-                m = mref = mx;
-                l *= corr;
-            }
-            // Asked before the exponentials, needed after them
-            const bool o_there = j > j0 && __all_sync(0xFFFFFFFFu, mbar_test(&ctl.o_done[wg], (done - 1) & 1));
-            const bool moved = __any_sync(0xFFFFFFFFu, corr != 1.0f);
-            float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
-            const float2 mul2 = make_float2(mul, mul), off2 = make_float2(-mref, -mref);
-            uint32_t pk[kKeys / 2];
-#pragma unroll
-            for (int c = 0; c < kKeys; c += 4) {
-                float2 x = __ffma2_rn(make_float2(s[c], s[c + 1]), mul2, off2);
-                float2 y = __ffma2_rn(make_float2(s[c + 2], s[c + 3]), mul2, off2);
-                x.x = fast_exp2(x.x);
-                x.y = fast_exp2(x.y);
-                y.x = fast_exp2(y.x);
-                y.y = fast_exp2(y.y);
-                sum0 = __fadd2_rn(sum0, x);
-                sum1 = __fadd2_rn(sum1, y);
-                pk[c / 2] = kFp8 ? pack_f16(x.x, x.y) : pack_bf16(x.x, x.y);
-                pk[c / 2 + 1] = kFp8 ? pack_f16(y.x, y.y) : pack_bf16(y.x, y.y);
-            }
-            l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
-            if (j > j0) {
-                // P and O are the previous tile's until its product is done
-                if (!o_there) ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl.o_done[wg], (done - 1) & 1, gave_up));
-                if (!ok) break;
+            const auto raise = [&](float mx) {   // also for the first visible key (m = -inf)
+                if (mx > m + kSlack) {
+                    corr = fast_exp2(m - mx);
+                    m = mref = mx;
+                    l *= corr;
+                }
+            };
+            // P and O are the previous tile's until its product is done
+            const auto rescale = [&](bool o_there, bool moved) -> bool {
+                if (j == j0) return true;
+                if (!o_there && !__all_sync(0xFFFFFFFFu, mbar_wait(&ctl.o_done[wg], (done - 1) & 1, gave_up))) return false;
                 fence_after();
                 if (moved) {
 #pragma unroll
@@ -763,10 +705,123 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
                         st32(to + 32 * h, o);
                     }
                 }
+                return true;
+            };
+            if (!any_sees) {
+                // A warp without such rows passes on: what its rows of P and O hold is not used.  It keeps step by the
+                // previous tile's product, or its arrival at p_full would be counted for that tile.
+                if (lane == 0) mbar_arrive(&ctl.s_free[wg]);
+                ok = rescale(false, false);
+                if (!ok) break;
+                s_there = false;
+            } else if (kPlain && __all_sync(0xFFFFFFFFu, whole)) {
+                // The row in registers at once, S given back before the exponentials
+                float s[kKeys];
+                ld32(ts, s);
+                ld32(ts + 32, s + 32);
+                wait_ld();
+                pin32(s);
+                pin32(s + 32);
+                ld32(ts + 64, s + 64);
+                ld32(ts + 96, s + 96);
+                float top[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) top[e] = fmaxf(s[e], s[56 + e]);
+#pragma unroll
+                for (int c = 8; c < 56; c += 16)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) top[e] = max3(top[e], s[c + 2 * e], s[c + 2 * e + 1]);
+                wait_ld();
+                pin32(s + 64);
+                pin32(s + 96);
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl.s_free[wg]);
+#pragma unroll
+                for (int c = 64; c < kKeys; c += 16)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) top[e] = max3(top[e], s[c + 2 * e], s[c + 2 * e + 1]);
+                raise(fmaxf(max3(max3(top[0], top[1], top[2]), top[3], top[4]), max3(top[5], top[6], top[7])) * scale);
+                // Asked before the exponentials, needed after them
+                const bool o_there = j > j0 && __all_sync(0xFFFFFFFFu, mbar_test(&ctl.o_done[wg], (done - 1) & 1));
+                const bool moved = __any_sync(0xFFFFFFFFu, corr != 1.0f);
+                uint32_t pk[kKeys / 2];
+                l += weights<kKeys, kFp8>(s, scale, mref, pk);
+                ok = rescale(o_there, moved);
+                if (!ok) break;
+                s_there = __all_sync(0xFFFFFFFFu, mbar_test(&ctl.s_full[wg], (done + 1) & 1));
+                st32(tpw, pk);
+                st32(tpw + 32, pk + 32);
+            } else {
+                // A quarter at a time in rolled loops: capped, biased and masked scores go back to tensor memory and are
+                // read again for the exponentials.  Straight-line code for all 128 did not stay in the instruction cache
+                // (a quarter of its requests missed): documents of 9 rows, 17..2100 tokens, 72 us.
+                unsigned hidden = 0;   // quarters that no row of the warp sees
+                float mx = -INFINITY;
+#pragma unroll 1
+                for (int k = 0; k < 4; ++k) {
+                    const int first = key0 + 32 * k, blocks = (bits >> (2 * k)) & 3;
+                    if (__all_sync(0xFFFFFFFFu, hi <= first || lo >= first + 32) || blocks == 0) {
+                        hidden |= 1u << k;
+                        continue;
+                    }
+                    float s[32];
+                    ld32(ts + 32 * k, s);
+                    wait_ld();
+                    pin32(s);
+                    if (capped) {
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) s[c] = capped_score(s[c], p.cap_c1, c2);
+                    } else if (biased) {
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) s[c] *= scale;
+                    }
+                    if (biased) {
+                        const float d0 = (float)(pos - first);
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) s[c] = fmaf(-slope, fabsf(d0 - (float)c), s[c]);
+                    }
+                    if (blocks != 3 || !__all_sync(0xFFFFFFFFu, !sees || (lo <= first && hi >= first + 32))) {
+                        const int a = max(lo - first, blocks & 1 ? 0 : kBlockKeys),
+                                  e = min(hi - first, blocks & 2 ? 32 : kBlockKeys);   // a block that is not there
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            if (c < a || c >= e) s[c] = -INFINITY;
+                    }
+                    float top[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                    for (int c = 4; c < 28; c += 8)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) top[e] = max3(top[e], s[c + 2 * e], s[c + 2 * e + 1]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) top[e] = fmaxf(top[e], s[28 + e]);
+                    mx = max3(mx, fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                    st32(ts + 32 * k, s);
+                }
+                wait_st();
+                raise(mx * mul);
+                ok = rescale(false, __any_sync(0xFFFFFFFFu, corr != 1.0f));
+                if (!ok) break;
+#pragma unroll 1
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t pk[16];
+                    if ((hidden >> k) & 1) {
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) pk[c] = 0;
+                    } else {
+                        float s[32];
+                        ld32(ts + 32 * k, s);
+                        wait_ld();
+                        pin32(s);
+                        l += weights<32, kFp8>(s, mul, mref, pk);
+                    }
+                    st16(tpw + 16 * k, pk);
+                }
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl.s_free[wg]);
+                s_there = false;
             }
-            s_there = __all_sync(0xFFFFFFFFu, mbar_test(&ctl.s_full[wg], (done + 1) & 1));
-            st32(tpw, pk);
-            st32(tpw + 32, pk + 32);
             wait_st();
             fence_before();
             __syncwarp();
@@ -784,6 +839,12 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
             pin32(o);
             pin32(o + 32);
         } else {
+#pragma unroll
+            for (int c = 0; c < kD; ++c) o[c] = 0.f;
+        }
+        if (!sees) {
+            m = -INFINITY;
+            l = 0.f;
 #pragma unroll
             for (int c = 0; c < kD; ++c) o[c] = 0.f;
         }

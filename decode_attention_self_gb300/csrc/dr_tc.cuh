@@ -145,6 +145,14 @@ __device__ __forceinline__ void st32(uint32_t taddr, const T *r) {
         DR_TC_W8(q, 8), DR_TC_W8(q, 16), DR_TC_W8(q, 24), "r"(taddr)
         : "memory");
 }
+// 16 columns
+__device__ __forceinline__ void st16(uint32_t taddr, const uint32_t *q) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+        "%14, %15};" ::DR_TC_W8(q, 0),
+        DR_TC_W8(q, 8), "r"(taddr)
+        : "memory");
+}
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 }  // namespace tc
