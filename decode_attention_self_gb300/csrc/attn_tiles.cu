@@ -675,11 +675,11 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
         bool ok = true, s_there = false;
         for (int j = j0; j < j1; ++j) {
             const int key0 = kbase + j * kKeys;
+            const bool inside = __all_sync(0xFFFFFFFFu, !sees || (key0 >= lo && key0 + kKeys <= hi));
             if (!s_there) ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl.s_full[wg], done & 1, gave_up));
             if (!ok) break;
             fence_after();
             const int bits = ctl.bits[(j - cb) % kBitsRing];
-            const bool whole = !sees || (key0 >= lo && key0 + kKeys <= hi && bits == 0xFF);
             float corr = 1.0f;
             const auto raise = [&](float mx) {   // also for the first visible key (m = -inf)
                 if (mx > m + kSlack) {
@@ -714,7 +714,7 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
                 ok = rescale(false, false);
                 if (!ok) break;
                 s_there = false;
-            } else if (kPlain && __all_sync(0xFFFFFFFFu, whole)) {
+            } else if (kPlain && inside && bits == 0xFF) {
                 // The row in registers at once, S given back before the exponentials
                 float s[kKeys];
                 ld32(ts, s);
