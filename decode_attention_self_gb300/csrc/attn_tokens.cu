@@ -57,12 +57,16 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
     return d;
 }
 
-// 32-byte read-only load of data read once per call: the lanes of a row cover its 128 bytes in one request.
-__device__ __forceinline__ void ld_stream32(const void *p, uint4 &a, uint4 &b) {
-    asm("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-        : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
-        : "l"(p));
+// Loads of data read once per call, past L1 (cached in L2 alone).  Behind the tile kernel this grid reads before it waits,
+// and L1 may then still hold lines from before the last writer; the writer's lines themselves are in L2, for it finished
+// before the tile kernel let this grid start.  32 bytes: the lanes of a key cover its row in one request.
+__device__ __forceinline__ void ld_l2_32(const void *p, uint4 &a, uint4 &b) {
+    asm volatile("ld.global.cg.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+                 : "l"(p));
 }
+__device__ __forceinline__ uint4 ld_l2_16(const void *p) { return __ldcg(static_cast<const uint4 *>(p)); }
+__device__ __forceinline__ uint2 ld_l2_8(const void *p) { return __ldcg(static_cast<const uint2 *>(p)); }
 
 // One 16-key tile as a lane holds it, in the cache's format.
 struct Bf16Tile {
@@ -71,10 +75,10 @@ struct Bf16Tile {
     static constexpr size_t kRowBytes = kD * 2;
     static constexpr bool kF16 = false;
     __device__ __forceinline__ void load_k(int i, const uint8_t *row, int c) {
-        ld_stream32(row + 32 * c, k[2 * i], k[2 * i + 1]);
+        ld_l2_32(row + 32 * c, k[2 * i], k[2 * i + 1]);
     }
     __device__ __forceinline__ void load_v(int i, const uint8_t *row, int r) {
-        v[i] = ld_stream16(row + 16 * r);
+        v[i] = ld_l2_16(row + 16 * r);
     }
     __device__ __forceinline__ void zero_k(int i) { k[2 * i] = k[2 * i + 1] = make_uint4(0, 0, 0, 0); }
     __device__ __forceinline__ void zero_v(int i) { v[i] = make_uint4(0, 0, 0, 0); }
@@ -94,10 +98,10 @@ struct Fp8Tile {
     static constexpr size_t kRowBytes = kD;
     static constexpr bool kF16 = true;
     __device__ __forceinline__ void load_k(int i, const uint8_t *row, int c) {
-        k[i] = ld_stream16(row + 16 * c);
+        k[i] = ld_l2_16(row + 16 * c);
     }
     __device__ __forceinline__ void load_v(int i, const uint8_t *row, int r) {
-        v[i] = ld_stream8(row + 8 * r);
+        v[i] = ld_l2_8(row + 8 * r);
     }
     __device__ __forceinline__ void zero_k(int i) { k[i] = make_uint4(0, 0, 0, 0); }
     __device__ __forceinline__ void zero_v(int i) { v[i] = make_uint2(0, 0); }
@@ -162,11 +166,11 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<Tile, kN>())
     // this grid waits for that one.)
     if (!p.after_tiles) pdl_wait();
     int s0 = b, n = 1;
-    int L = p.kv_len ? __ldg(p.kv_len + b) : 0;
-    const int prefix = p.prefix_len ? __ldg(p.prefix_len + b) : 0;
+    int L = p.kv_len ? __ldcg(p.kv_len + b) : 0;
+    const int prefix = p.prefix_len ? __ldcg(p.prefix_len + b) : 0;
     if (p.row_start) {
-        s0 = __ldg(p.row_start + b);
-        int s1 = __ldg(p.row_start + b + 1);
+        s0 = __ldcg(p.row_start + b);
+        int s1 = __ldcg(p.row_start + b + 1);
         if ((s0 < 0 || s1 < s0 || s1 > p.T || (b == 0 && s0 != 0)) && split == 0 && hy == 0 && threadIdx.x == 0)
             flag_error(p.err, DR_ERRF_ROW_START);
         s0 = min(max(s0, 0), p.T);
@@ -192,18 +196,25 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<Tile, kN>())
     for (int i = 0; i < n; ++i) {
         const int t = s0 + i;
         const int pos = L - n + i;
-        int lo = p.first_key ? max(0, __ldg(p.first_key + t)) : 0;
+        int lo = p.first_key ? max(0, __ldcg(p.first_key + t)) : 0;
         int hi = p.causal && p.row_start ? min(L, max(pos + 1, prefix)) : L;
         if (lo >= hi) lo = hi = 0;
         const int tile0 = lo / kTile, tiles = (hi + kTile - 1) / kTile - tile0;
         const int per = (tiles + splits - 1) / splits;
         const int tb = tile0 + min(split * per, tiles), te = tile0 + min((split + 1) * per, tiles);
 
-        // Byte offset of key 16 * tile of this kv head; false: past the end, or a block outside the pool
-        auto tile_base = [&](int tile, size_t &base) -> bool {
+        // Block ids of the warp's next 32 / kT passes, one per lane: lane e has tile e % kT of pass e / kT
+        int ids = 0;
+        const auto fetch_ids = [&](int first) {
+            const int x = first + lane / kT * (kWarps * kT) + lane % kT;
+            ids = x < te ? __ldcg(p.table + (size_t)b * p.max_blocks + x) : -1;
+        };
+        // Byte offset of tile y of pass n of the warp (tile `tile` of the row); false: past the end, or no such block
+        auto tile_base = [&](int n, int y, int tile, size_t &base) -> bool {
+            int blk = 0;
+            if (kPaged) blk = __shfl_sync(0xFFFFFFFFu, ids, n % (32 / kT) * kT + y);
             if (tile >= te) return false;
             if (kPaged) {
-                const int blk = __ldg(p.table + (size_t)b * p.max_blocks + tile);
                 base = ((size_t)blk * p.Hkv + hk) * kTile * Tile::kRowBytes;
                 if ((unsigned)blk < (unsigned)p.num_blocks) return true;
                 if (lane == 0) flag_error(p.err, DR_ERRF_BLOCK_ID);
@@ -219,10 +230,11 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<Tile, kN>())
             unsigned there;
             bool whole;
         };
-        auto locate = [&](int first, Group &g) {
+        auto locate = [&](int n, int first, Group &g) {
+            if (kPaged && n % (32 / kT) == 0) fetch_ids(first);
             g.there = 0;
 #pragma unroll
-            for (int y = 0; y < kT; ++y) g.there |= tile_base(first + y, g.base[y]) ? 1u << y : 0u;
+            for (int y = 0; y < kT; ++y) g.there |= tile_base(n, y, first + y, g.base[y]) ? 1u << y : 0u;
             g.whole = g.there == (1u << kT) - 1 && first * kTile >= lo && (first + kT) * kTile <= hi;
         };
         // Keys that are not attended are loaded as zeros
@@ -258,9 +270,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<Tile, kN>())
         // The first keys go out before the query is waited for
         Tile x[kT];
         Group cur, nxt;
-        int tile = tb + warp * kT;
+        int tile = tb + warp * kT, pass = 0;
         if (tile < te) {
-            locate(tile, cur);
+            locate(0, tile, cur);
             load(tile, cur, x);
         }
 
@@ -274,8 +286,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<Tile, kN>())
             uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
             if (h < nheads) {
                 const uint16_t *src = p.q + (size_t)t * p.q_stride + (size_t)(h0 + h) * kD;
-                w0 = ld_ro16(src + 16 * c);
-                w1 = ld_ro16(src + 16 * c + 8);
+                w0 = ld_l2_16(src + 16 * c);
+                w1 = ld_l2_16(src + 16 * c + 8);
             }
             if constexpr (Tile::kF16) {
                 float x[8], y[8];
@@ -304,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<Tile, kN>())
 #pragma unroll
             for (int j = 0; j < 2; ++j)
                 slope[a][j] = p.slopes && a * 8 + 2 * c + j < nheads
-                                  ? __ldg(p.slopes + h0 + a * 8 + 2 * c + j) * 1.4426950408889634f : 0.f;
+                                  ? __ldcg(p.slopes + h0 + a * 8 + 2 * c + j) * 1.4426950408889634f : 0.f;
         }
 
         float m[kN][2], mref[kN][2], l[kN][2], acc[kN][4][4];
@@ -339,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<Tile, kN>())
                 }
             // s[y][a][0..3]: (key r, head 2c), (key r, head 2c+1), (key r+8, head 2c), (key r+8, head 2c+1) of tile y
             const int next = tile + kWarps * kT;
-            if (next < te) locate(next, nxt);
+            if (next < te) locate(++pass, next, nxt);
 #pragma unroll
             for (int y = 0; y < kT; ++y)
 #pragma unroll
