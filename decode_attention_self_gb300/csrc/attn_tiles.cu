@@ -6,17 +6,27 @@
 // The g query heads of a kv head and consecutive tokens fill a tile's rows together (row = token * g + head), so one
 // pass over the keys serves them all.  A CTA holds one tile per softmax warpgroup (kWG of them) and walks its keys
 // 128 at a time:
-//   producer warps    TMA loads of K and of V tiles (a paged tile is eight 16-key boxes; blocks outside the pool and past
-//                     the last visible key come from an out-of-range coordinate: zeros)
-//   MMA warp          S = Q K^T into tensor memory, one tile ahead of the softmax; O += P V with P read from tensor
-//                     memory and V as the MN-major operand
-//   softmax warps     one thread per query row: S to registers, mask, running maximum, weights, P back to tensor
-//                     memory; S is free for the next product as soon as it is in registers
-//   helper warps      bf16: in tiles that some row does not see whole, values that are not finite become 0 (0 times
-//                     infinity would reach rows that do not see them); rows that do see them get them back at the end.
-//                     e4m3: codes to f16 (exact) on the way from the TMA's buffer to the MMA's
+//   producer warps    TMA loads, K by one warp and V by another (a paged tile is eight 16-key boxes; blocks outside the
+//                     pool and past the last visible key come from an out-of-range coordinate: zeros)
+//   MMA warp          one per tile: S = Q K^T into tensor memory, one key tile ahead of the softmax; O += P V with P read
+//                     from tensor memory and V as the MN-major operand
+//   softmax warps     one thread per query row: S to registers, mask, running maximum, weights, P back to tensor memory
+//   helper warps      bf16: values that no row of the CTA sees become 0.  e4m3: that, and codes to f16 (exact) on the way
+//                     from the TMA's buffer to the MMA's, in four warps, two for K and two for V
+// The softmax takes one of two ways per key tile.  A tile that every row sees whole, with neither cap nor bias, goes
+// through registers at once, and S is given back before the exponentials.  Any other goes through tensor memory a
+// quarter at a time in rolled loops, so that the code stays in the instruction cache.
 // The running maximum moves only when a score passes it by 2^8 (log2 units): O is rescaled rarely.  Sums and states are
 // fp32; weights are rounded once, to bf16 (e4m3: f16), for the product with V.
+//
+// What bounds it.  One token of one head costs 256 flops and one exponential per key it sees.  16384 causal tokens of 16
+// heads in bf16: 543 us, 1014 TFLOP/s; the products alone would take 288 us at the library GEMM's rate and the
+// exponentials 230 us of the special-function units.  They overlap between the two CTAs of an SM, but P V runs at 45
+// cycles per instruction where its shape allows 32 (P comes from tensor memory), and the maximum, the packing and the
+// moves to and from tensor memory take issue slots beside the exponentials.  Two threads per row (half the registers, so
+// no spills at higher occupancy), skipping hidden columns inside the straight way, and P V one tile later were each built
+// and were slower.  e4m3: a step of 128 keys x 256 rows takes about 3100 cycles;
+// short documents are bound by a CTA's fixed 6 us (query, pipeline fill, output) rather than by their few keys.
 //
 // Every wait is bounded (about 2 s): DR_ERRF_TIMEOUT, the CTA writes nothing, drains its copies and frees its tensor
 // memory.
@@ -44,7 +54,7 @@ struct Config {
     static constexpr int kOtherWarps = kFp8 ? 8 : 4;             // two producers, an MMA warp per tile, helpers
     static constexpr int kThreads = 128 * kWG + 32 * kOtherWarps;
     static constexpr int kCtasPerSm = kWG == 1 ? 2 : 1;
-    static constexpr int kTma = kFp8 ? 4 : (kWG == 1 ? 3 : 4);   // stages that TMA fills (bf16: the MMA reads them)
+    static constexpr int kTma = kFp8 ? 4 : 3;      // stages that TMA fills (bf16: the MMA reads them)
     static constexpr int kMma = kFp8 ? 3 : kTma;                 // stages that the MMA reads
     static constexpr uint32_t kTmaBytes = kKeys * kD * (kFp8 ? 1 : 2);
     static constexpr uint32_t kQ = 0, kK = kWG * kTileBytes, kV = kK + kMma * kTileBytes,
@@ -72,11 +82,21 @@ struct Control {   // at Config::kEnd of the dynamic shared memory
     int lo_max, hi_min;                  // keys that every row of the CTA sees
 };
 
+// n / d for n < 2^31 by a product and a shift (a division takes some 30 instructions, and the start of a CTA has five).
+struct Divisor {
+    uint32_t d, mul, shift;
+    void set(uint32_t by) {
+        d = by;
+        shift = 0;
+        while ((1u << shift) < by) ++shift;
+        mul = (uint32_t)(((1ull << 32) * ((1ull << shift) - by)) / by + 1);
+    }
+    __device__ __forceinline__ unsigned of(unsigned n) const { return (n + __umulhi(n, mul)) >> shift; }
+};
+
 struct TileParams {
     PromptParams p;
-    int32_t splits;
-    uint32_t g_mul, g_shift;   // n / g = (n + hi32(n * g_mul)) >> g_shift for n < 2^31
-    __device__ __forceinline__ unsigned by_g(unsigned n) const { return (n + __umulhi(n, g_mul)) >> g_shift; }
+    Divisor splits, heads, group;   // CTAs per tile, key/value heads, query heads per key/value head
 };
 
 // Physical byte of 16-byte chunk c of 128-byte row r under the 128-byte swizzle (tile base 1024-byte aligned).
@@ -154,35 +174,27 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int kProducer = 4 * kWG, kMmaWarp = kProducer + 2, kHelper = kMmaWarp + kWG;   // an MMA warp per tile
 
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < kMaxStages; ++i) {
-            mbar_init(&ctl.k_full[i], 1);
-            mbar_init(&ctl.v_full[i], 1);
-            mbar_init(&ctl.k_empty[i], kFp8 ? C::kHelperWarps : 1);
-            mbar_init(&ctl.v_empty[i], kFp8 ? C::kHelperWarps : 1);
-            mbar_init(&ctl.k_ready[i], C::kHelperWarps);
-            mbar_init(&ctl.v_ready[i], C::kHelperWarps);
-            mbar_init(&ctl.kc_empty[i], kWG);
-            mbar_init(&ctl.vc_empty[i], kWG);
+    if (warp == 1) {   // a lane per barrier
+        static_assert(offsetof(Control, q_full) == 32 * 8 && offsetof(Control, tmem) == 42 * 8, "order of the barriers");
+        uint64_t *bars = reinterpret_cast<uint64_t *>(&ctl);
+        const int ring = lane / kMaxStages, kind = lane / 2;
+        mbar_init(bars + lane, ring == 0 || ring == 2 ? 1 : ring < 4 ? (kFp8 ? C::kHelperWarps : 1)
+                                                  : ring < 6 ? C::kHelperWarps : kWG);
+        if (lane < 10) mbar_init(bars + 32 + lane, kind == 1 || kind == 4 ? 1 : 4);
+        if (lane < 2) {
+            ctl.lo_min[lane] = 0x7FFFFFFF;
+            ctl.hi_max[lane] = 0;
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&ctl.q_full[i], 4);
-            mbar_init(&ctl.s_full[i], 1);
-            mbar_init(&ctl.s_free[i], 4);
-            mbar_init(&ctl.p_full[i], 4);
-            mbar_init(&ctl.o_done[i], 1);
-            ctl.lo_min[i] = 0x7FFFFFFF;
-            ctl.hi_max[i] = 0;
+        if (lane == 0) {
+            ctl.lo_max = 0;
+            ctl.hi_min = 0x7FFFFFFF;
+            ctl.gave_up = (smem_u32(smem) & 1023u) != 0;   // never: the swizzled tiles need 1024-byte alignment
+            ctl.redo = ctl.nonfinite = 0;
         }
-        ctl.lo_max = 0;
-        ctl.hi_min = 0x7FFFFFFF;
-        ctl.gave_up = (smem_u32(smem) & 1023u) != 0;   // never: the swizzled tiles need 1024-byte alignment
-        ctl.redo = ctl.nonfinite = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_k)) : "memory");
-        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_v)) : "memory");
+    } else if (warp == kProducer && lane < 2) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(lane ? &map_v : &map_k)) : "memory");
     }
-    __syncthreads();
     pdl_wait();
     // Tensor memory is taken after the wait and before the next grid may start: no CTA that waits for another grid holds
     // what that grid still has to take.
@@ -194,11 +206,11 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
     }
 
     // Which tile of which row: tiles of the rows in turn, a row's last (longest, when causal) tile of all heads first
-    const int hk = (int)(blockIdx.x % (unsigned)p.Hkv), unit = (int)(blockIdx.x / (unsigned)p.Hkv);
-    const int split = unit % tp.splits;
+    const unsigned unit = tp.heads.of(blockIdx.x), tile_no = tp.splits.of(unit);
+    const int hk = (int)(blockIdx.x - unit * tp.heads.d), split = (int)(unit - tile_no * tp.splits.d);
     constexpr unsigned rows_per_cta = kRows * kWG;
     if (warp == 0) {
-        int want = unit / tp.splits;
+        int want = (int)tile_no;
         int b = -1, s0 = 0, n = 0, L = 0, prefix = 0;
         if (!p.row_start) {
             const int tiles = (int)(((unsigned)p.T * (unsigned)p.g + rows_per_cta - 1) / rows_per_cta);
@@ -221,7 +233,8 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
                 }
                 if (b >= 0) continue;
                 const int len = e - a;
-                const int tiles = len > p.few_max ? (int)(((unsigned)len * (unsigned)p.g + rows_per_cta - 1) / rows_per_cta) : 0;
+                const int tiles =
+                    len > p.few_max ? (int)(((unsigned)len * (unsigned)p.g + rows_per_cta - 1) / rows_per_cta) : 0;
                 int sum = tiles;
 #pragma unroll
                 for (int off = 1; off < 32; off <<= 1) {
@@ -236,7 +249,8 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
                     n = __shfl_sync(0xFFFFFFFFu, len, src);
                     L = __shfl_sync(0xFFFFFFFFu, len_l, src);
                     prefix = __shfl_sync(0xFFFFFFFFu, pre_l, src);
-                    const int before = __shfl_sync(0xFFFFFFFFu, sum - tiles, src), mine = __shfl_sync(0xFFFFFFFFu, tiles, src);
+                    const int before = __shfl_sync(0xFFFFFFFFu, sum - tiles, src);
+                    const int mine = __shfl_sync(0xFFFFFFFFu, tiles, src);
                     want = mine - 1 - (want - before);
                 } else {
                     want -= __shfl_sync(0xFFFFFFFFu, sum, 31);
@@ -273,17 +287,24 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
 
     // The keys that the softmax threads' rows see, and those that some and all rows of the CTA see
     const int wg = warp >> 2, row = threadIdx.x & 127;
-    int lo = 0, hi = 0, pos = 0, token = 0, head = 0;
+    int lo = 0, hi = 0, pos = 0, orow = 0;   // orow: token * Hq + head
     bool valid = false;
+    uint4 qw[8];   // the query, on its way while the keys that it sees are found out
     const unsigned flat0 = (unsigned)ctl.qt * rows_per_cta, flat_end = (unsigned)n * (unsigned)p.g;   // T * Hq < 2^31
     if (warp < kProducer) {
         const unsigned flat = flat0 + wg * kRows + row;
         valid = flat < flat_end;
         if (valid) {
-            const unsigned i = tp.by_g(flat);
-            token = ctl.s0 + (int)i;
-            head = hk * p.g + (int)(flat - i * (unsigned)p.g);
+            const unsigned i = tp.group.of(flat);
+            const int token = ctl.s0 + (int)i, head = hk * p.g + (int)(flat - i * (unsigned)p.g);
+            const uint16_t *src = p.q + (size_t)token * p.q_stride + (size_t)head * kD;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) qw[c] = ld_ro16(src + 8 * c);
             visible(p, token, (int)i, n, L, ctl.prefix, lo, hi, pos);
+            orow = token * p.Hq + head;
+        } else {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) qw[c] = make_uint4(0, 0, 0, 0);
         }
     }
     int lo_min[kWG], hi_max[kWG], clo, chi;
@@ -312,7 +333,7 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
     } else {   // from key 0 to an end that does not fall from one token to the next
         const auto end_of = [&](unsigned flat) -> int {
             int a, e, q;
-            visible(p, ctl.s0, (int)tp.by_g(flat), n, L, ctl.prefix, a, e, q);
+            visible(p, ctl.s0, (int)tp.group.of(flat), n, L, ctl.prefix, a, e, q);
             return e;
         };
         clo = 0;
@@ -337,7 +358,7 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
     if (ulo >= uhi) ulo = uhi = 0;
     const int kbase = ulo & ~(kBlockKeys - 1);
     const int all = (uhi - kbase + kKeys - 1) / kKeys;
-    const int per = (all + tp.splits - 1) / tp.splits;
+    const int per = (int)tp.splits.of((unsigned)all + tp.splits.d - 1);
     const int t_lo = min(split * per, all), t_hi = min(t_lo + per, all);
     int jb[kWG], je[kWG], cb = t_hi, ce = t_lo;
 #pragma unroll
@@ -357,6 +378,7 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
     // do not see it too.  So where some row ends up with sums that are not finite, the CTA goes over its keys once more,
     // with such values kept out of tiles that not every row sees whole, and every row then adds those that it sees.
     const auto again = [&](int pass) -> bool {   // the same in every thread: all of them get here
+        fence_before();
         __syncthreads();
         return pass == 0 && *(volatile int *)&ctl.redo && !*gave_up;
     };
@@ -389,8 +411,8 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
                             ids = ids_next;
                             ids_next = group_ids(j + 4);
                             // a block that some row sees and that is not in the pool
-                            if (!is_v && j < ce && kbase + j * kKeys + lane * kBlockKeys < uhi &&
-                                (unsigned)ids >= (unsigned)p.num_blocks && kbase + j * kKeys + lane * kBlockKeys < kbase + ce * kKeys)
+                            const int key = kbase + j * kKeys + lane * kBlockKeys;
+                            if (!is_v && key < uhi && key < kbase + ce * kKeys && (unsigned)ids >= (unsigned)p.num_blocks)
                                 flag_error(p.err, DR_ERRF_BLOCK_ID);
                             ids = (unsigned)ids < (unsigned)p.num_blocks ? ids * p.Hkv + hk : -1;
                         }
@@ -507,14 +529,14 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
             bool ok = true;
             int s = 0, round = 0, sc = 0, roundc = 0, pass = 0;
             do {
-                for (int j = cb, i = 0; j < ce && ok && kv < 2; ++j, ++i) {
+                for (int j = cb; j < ce && ok; ++j) {
                     const int key0 = kbase + j * kKeys;
                     ok = mbar_wait(&full[s], round & 1, gave_up);
                     if (ok && roundc > 0) ok = mbar_wait(&free_[sc], (roundc - 1) & 1, gave_up);
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     if (!ok) break;
                     const bool edge = kv && (key0 < ulo || key0 + kKeys > uhi);   // values that no row sees: zeros
-                    const bool mixed = kv && pass && (key0 < clo || key0 + kKeys > chi || ctl.bits[i % kBitsRing] != 0xFF);
+                    const bool mixed = kv && pass && (key0 < clo || key0 + kKeys > chi);
                     const uint8_t *raw = smem + (kv ? C::kRawV : C::kRawK) + s * C::kTmaBytes;
                     uint8_t *dst = smem + (kv ? C::kV : C::kK) + sc * kTileBytes;
                     bool bad = false;
@@ -630,20 +652,12 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
         float qfac = 1.0f;
         {
             uint8_t *qs = smem + C::kQ + wg * kTileBytes;
-            uint4 w[8];
-#pragma unroll
-            for (int c = 0; c < 8; ++c) w[c] = make_uint4(0, 0, 0, 0);
-            if (valid) {
-                const uint16_t *src = p.q + (size_t)token * p.q_stride + (size_t)head * kD;
-#pragma unroll
-                for (int c = 0; c < 8; ++c) w[c] = ld_ro16(src + 8 * c);
-            }
             if (kFp8) {
                 float big = 0.f;
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
                     float x[8];
-                    unpack8(w[c], x);
+                    unpack8(qw[c], x);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) big = fmaxf(big, fabsf(x[j]));
                 }
@@ -652,275 +666,279 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
                     float x[8];
-                    unpack8(w[c], x);
-                    w[c] = make_uint4(pack_f16(x[0] * up, x[1] * up), pack_f16(x[2] * up, x[3] * up),
+                    unpack8(qw[c], x);
+                    qw[c] = make_uint4(pack_f16(x[0] * up, x[1] * up), pack_f16(x[2] * up, x[3] * up),
                                       pack_f16(x[4] * up, x[5] * up), pack_f16(x[6] * up, x[7] * up));
                 }
             }
 #pragma unroll
-            for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4 *>(qs + swz(row, c)) = w[c];
+            for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4 *>(qs + swz(row, c)) = qw[c];
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctl.q_full[wg]);
         }
         const float scale = p.sscale * qfac, c2 = p.cap_c2 * qfac;
         const bool capped = !kPlain && p.cap_c1 != 0.f, biased = !kPlain && p.slopes != nullptr;
-        const float slope = biased && valid ? __ldg(p.slopes + head) * 1.4426950408889634f : 0.f;
+        const float slope = biased && valid ? __ldg(p.slopes + orow % p.Hq) * 1.4426950408889634f : 0.f;
         const float mul = capped || biased ? 1.0f : scale;
         // A row that sees no key (or is none) goes along with the others of its warp; its state is put right at the end
         const bool sees = hi > lo, any_sees = __any_sync(0xFFFFFFFFu, sees);
         int done = 0, pass = 0;   // tiles so far
         do {
-        float m = -INFINITY, mref = 0.f, l = 0.f;
-        bool ok = true, s_there = false;
-        for (int j = j0; j < j1; ++j) {
-            const int key0 = kbase + j * kKeys;
-            const bool inside = __all_sync(0xFFFFFFFFu, !sees || (key0 >= lo && key0 + kKeys <= hi));
-            if (!s_there) ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl.s_full[wg], done & 1, gave_up));
-            if (!ok) break;
-            fence_after();
-            const int bits = ctl.bits[(j - cb) % kBitsRing];
-            float corr = 1.0f;
-            const auto raise = [&](float mx) {   // also for the first visible key (m = -inf)
-                if (mx > m + kSlack) {
-                    corr = fast_exp2(m - mx);
-                    m = mref = mx;
-                    l *= corr;
-                }
-            };
-            // P and O are the previous tile's until its product is done
-            const auto rescale = [&](bool o_there, bool moved) -> bool {
-                if (j == j0) return true;
-                if (!o_there && !__all_sync(0xFFFFFFFFu, mbar_wait(&ctl.o_done[wg], (done - 1) & 1, gave_up))) return false;
+            float m = -INFINITY, mref = 0.f, l = 0.f;
+            bool ok = true, s_there = false;
+            for (int j = j0; j < j1; ++j) {
+                const int key0 = kbase + j * kKeys;
+                const bool inside = __all_sync(0xFFFFFFFFu, !sees || (key0 >= lo && key0 + kKeys <= hi));
+                if (!s_there) ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl.s_full[wg], done & 1, gave_up));
+                if (!ok) break;
                 fence_after();
-                if (moved) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float o[32];
-                        ld32(to + 32 * h, o);
-                        wait_ld();
-                        pin32(o);
-#pragma unroll
-                        for (int c = 0; c < 32; ++c) o[c] *= corr;
-                        st32(to + 32 * h, o);
+                const int bits = ctl.bits[(j - cb) % kBitsRing];
+                float corr = 1.0f;
+                const auto raise = [&](float mx) {   // also for the first visible key (m = -inf)
+                    if (mx > m + kSlack) {
+                        corr = fast_exp2(m - mx);
+                        m = mref = mx;
+                        l *= corr;
                     }
-                }
-                return true;
-            };
-            if (!any_sees) {
-                // A warp without such rows passes on: what its rows of P and O hold is not used.  It keeps step by the
-                // previous tile's product, or its arrival at p_full would be counted for that tile.
-                if (lane == 0) mbar_arrive(&ctl.s_free[wg]);
-                ok = rescale(false, false);
-                if (!ok) break;
-                s_there = false;
-            } else if (kPlain && inside && bits == 0xFF) {
-                // The row in registers at once, S given back before the exponentials
-                float s[kKeys];
-                ld32(ts, s);
-                ld32(ts + 32, s + 32);
-                wait_ld();
-                pin32(s);
-                pin32(s + 32);
-                ld32(ts + 64, s + 64);
-                ld32(ts + 96, s + 96);
-                float top[8];
+                };
+                // P and O are the previous tile's until its product is done
+                const auto rescale = [&](bool o_there, bool moved) -> bool {
+                    if (j == j0) return true;
+                    if (!o_there && !__all_sync(0xFFFFFFFFu, mbar_wait(&ctl.o_done[wg], (done - 1) & 1, gave_up))) return false;
+                    fence_after();
+                    if (moved) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) top[e] = fmaxf(s[e], s[56 + e]);
+                        for (int h = 0; h < 2; ++h) {
+                            float o[32];
+                            ld32(to + 32 * h, o);
+                            wait_ld();
+                            pin32(o);
 #pragma unroll
-                for (int c = 8; c < 56; c += 16)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) top[e] = max3(top[e], s[c + 2 * e], s[c + 2 * e + 1]);
-                wait_ld();
-                pin32(s + 64);
-                pin32(s + 96);
-                fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl.s_free[wg]);
-#pragma unroll
-                for (int c = 64; c < kKeys; c += 16)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) top[e] = max3(top[e], s[c + 2 * e], s[c + 2 * e + 1]);
-                raise(fmaxf(max3(max3(top[0], top[1], top[2]), top[3], top[4]), max3(top[5], top[6], top[7])) * scale);
-                // Asked before the exponentials, needed after them
-                const bool o_there = j > j0 && __all_sync(0xFFFFFFFFu, mbar_test(&ctl.o_done[wg], (done - 1) & 1));
-                const bool moved = __any_sync(0xFFFFFFFFu, corr != 1.0f);
-                uint32_t pk[kKeys / 2];
-                l += weights<kKeys, kFp8>(s, scale, mref, pk);
-                ok = rescale(o_there, moved);
-                if (!ok) break;
-                s_there = __all_sync(0xFFFFFFFFu, mbar_test(&ctl.s_full[wg], (done + 1) & 1));
-                st32(tpw, pk);
-                st32(tpw + 32, pk + 32);
-            } else {
-                // A quarter at a time in rolled loops: capped, biased and masked scores go back to tensor memory and are
-                // read again for the exponentials.  Straight-line code for all 128 did not stay in the instruction cache
-                // (a quarter of its requests missed): documents of 9 rows, 17..2100 tokens, 72 us.
-                unsigned hidden = 0;   // quarters that no row of the warp sees
-                float mx = -INFINITY;
-#pragma unroll 1
-                for (int k = 0; k < 4; ++k) {
-                    const int first = key0 + 32 * k, blocks = (bits >> (2 * k)) & 3;
-                    if (__all_sync(0xFFFFFFFFu, hi <= first || lo >= first + 32) || blocks == 0) {
-                        hidden |= 1u << k;
-                        continue;
+                            for (int c = 0; c < 32; ++c) o[c] *= corr;
+                            st32(to + 32 * h, o);
+                        }
                     }
-                    float s[32];
-                    ld32(ts + 32 * k, s);
+                    return true;
+                };
+                if (!any_sees) {
+                    // A warp without such rows passes on: what its rows of P and O hold is not used.  It keeps step by the
+                    // previous tile's product, or its arrival at p_full would be counted for that tile.
+                    if (lane == 0) mbar_arrive(&ctl.s_free[wg]);
+                    ok = rescale(false, false);
+                    if (!ok) break;
+                    s_there = false;
+                } else if (kPlain && inside && bits == 0xFF) {
+                    // The row in registers at once, S given back before the exponentials
+                    float s[kKeys];
+                    ld32(ts, s);
+                    ld32(ts + 32, s + 32);
                     wait_ld();
                     pin32(s);
-                    if (capped) {
+                    pin32(s + 32);
+                    ld32(ts + 64, s + 64);
+                    ld32(ts + 96, s + 96);
+                    float top[8];
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) s[c] = capped_score(s[c], p.cap_c1, c2);
-                    } else if (biased) {
+                    for (int e = 0; e < 8; ++e) top[e] = fmaxf(s[e], s[56 + e]);
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) s[c] *= scale;
-                    }
-                    if (biased) {
-                        const float d0 = (float)(pos - first);
+                    for (int c = 8; c < 56; c += 16)
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) s[c] = fmaf(-slope, fabsf(d0 - (float)c), s[c]);
-                    }
-                    if (blocks != 3 || !__all_sync(0xFFFFFFFFu, !sees || (lo <= first && hi >= first + 32))) {
-                        const int a = max(lo - first, blocks & 1 ? 0 : kBlockKeys),
-                                  e = min(hi - first, blocks & 2 ? 32 : kBlockKeys);   // a block that is not there
+                        for (int e = 0; e < 8; ++e) top[e] = max3(top[e], s[c + 2 * e], s[c + 2 * e + 1]);
+                    wait_ld();
+                    pin32(s + 64);
+                    pin32(s + 96);
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ctl.s_free[wg]);
 #pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            if (c < a || c >= e) s[c] = -INFINITY;
-                    }
-                    float top[4] = {s[0], s[1], s[2], s[3]};
+                    for (int c = 64; c < kKeys; c += 16)
 #pragma unroll
-                    for (int c = 4; c < 28; c += 8)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) top[e] = max3(top[e], s[c + 2 * e], s[c + 2 * e + 1]);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) top[e] = fmaxf(top[e], s[28 + e]);
-                    mx = max3(mx, fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-                    st32(ts + 32 * k, s);
-                }
-                wait_st();
-                raise(mx * mul);
-                ok = rescale(false, __any_sync(0xFFFFFFFFu, corr != 1.0f));
-                if (!ok) break;
+                        for (int e = 0; e < 8; ++e) top[e] = max3(top[e], s[c + 2 * e], s[c + 2 * e + 1]);
+                    raise(fmaxf(max3(max3(top[0], top[1], top[2]), top[3], top[4]), max3(top[5], top[6], top[7])) * scale);
+                    // Asked before the exponentials, needed after them
+                    const bool o_there = j > j0 && __all_sync(0xFFFFFFFFu, mbar_test(&ctl.o_done[wg], (done - 1) & 1));
+                    const bool moved = __any_sync(0xFFFFFFFFu, corr != 1.0f);
+                    uint32_t pk[kKeys / 2];
+                    l += weights<kKeys, kFp8>(s, scale, mref, pk);
+                    ok = rescale(o_there, moved);
+                    if (!ok) break;
+                    s_there = __all_sync(0xFFFFFFFFu, mbar_test(&ctl.s_full[wg], (done + 1) & 1));
+                    st32(tpw, pk);
+                    st32(tpw + 32, pk + 32);
+                } else {
+                    // A quarter at a time in rolled loops: capped, biased and masked scores go back to tensor memory and are
+                    // read again for the exponentials.  Straight-line code for all 128 did not stay in the instruction cache
+                    // (a quarter of its requests missed): documents of 9 rows, 17..2100 tokens, 72 us.
+                    unsigned hidden = 0;   // quarters that no row of the warp sees
+                    float mx = -INFINITY;
 #pragma unroll 1
-                for (int k = 0; k < 4; ++k) {
-                    uint32_t pk[16];
-                    if ((hidden >> k) & 1) {
-#pragma unroll
-                        for (int c = 0; c < 16; ++c) pk[c] = 0;
-                    } else {
+                    for (int k = 0; k < 4; ++k) {
+                        const int first = key0 + 32 * k, blocks = (bits >> (2 * k)) & 3;
+                        if (__all_sync(0xFFFFFFFFu, hi <= first || lo >= first + 32) || blocks == 0) {
+                            hidden |= 1u << k;
+                            continue;
+                        }
                         float s[32];
                         ld32(ts + 32 * k, s);
                         wait_ld();
                         pin32(s);
-                        l += weights<32, kFp8>(s, mul, mref, pk);
+                        if (capped) {
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) s[c] = capped_score(s[c], p.cap_c1, c2);
+                        } else if (biased) {
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) s[c] *= scale;
+                        }
+                        if (biased) {
+                            const float d0 = (float)(pos - first);
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) s[c] = fmaf(-slope, fabsf(d0 - (float)c), s[c]);
+                        }
+                        if (blocks != 3 || !__all_sync(0xFFFFFFFFu, !sees || (lo <= first && hi >= first + 32))) {
+                            const int a = max(lo - first, blocks & 1 ? 0 : kBlockKeys),
+                                      e = min(hi - first, blocks & 2 ? 32 : kBlockKeys);   // a block that is not there
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                if (c < a || c >= e) s[c] = -INFINITY;
+                        }
+                        float top[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                        for (int c = 4; c < 28; c += 8)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) top[e] = max3(top[e], s[c + 2 * e], s[c + 2 * e + 1]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) top[e] = fmaxf(top[e], s[28 + e]);
+                        mx = max3(mx, fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                        st32(ts + 32 * k, s);
                     }
-                    st16(tpw + 16 * k, pk);
+                    wait_st();
+                    raise(mx * mul);
+                    ok = rescale(false, __any_sync(0xFFFFFFFFu, corr != 1.0f));
+                    if (!ok) break;
+#pragma unroll 1
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t pk[16];
+                        if ((hidden >> k) & 1) {
+#pragma unroll
+                            for (int c = 0; c < 16; ++c) pk[c] = 0;
+                        } else {
+                            float s[32];
+                            ld32(ts + 32 * k, s);
+                            wait_ld();
+                            pin32(s);
+                            l += weights<32, kFp8>(s, mul, mref, pk);
+                        }
+                        st16(tpw + 16 * k, pk);
+                    }
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ctl.s_free[wg]);
+                    s_there = false;
                 }
+                wait_st();
                 fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl.s_free[wg]);
-                s_there = false;
+                if (lane == 0) mbar_arrive(&ctl.p_full[wg]);
+                ++done;
             }
-            wait_st();
-            fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl.p_full[wg]);
-            ++done;
-        }
 
-        float o[kD];
-        if (ok && j1 > j0) {
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl.o_done[wg], (done - 1) & 1, gave_up));
-            fence_after();
-            ld32(to, o);
-            ld32(to + 32, o + 32);
-            wait_ld();
-            pin32(o);
-            pin32(o + 32);
-        } else {
+            float o[kD];
+            if (ok && j1 > j0) {
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl.o_done[wg], (done - 1) & 1, gave_up));
+                fence_after();
+                ld32(to, o);
+                ld32(to + 32, o + 32);
+                wait_ld();
+                pin32(o);
+                pin32(o + 32);
+            } else {
 #pragma unroll
-            for (int c = 0; c < kD; ++c) o[c] = 0.f;
-        }
-        if (!sees) {
-            m = -INFINITY;
-            l = 0.f;
+                for (int c = 0; c < kD; ++c) o[c] = 0.f;
+            }
+            if (!sees) {
+                m = -INFINITY;
+                l = 0.f;
 #pragma unroll
-            for (int c = 0; c < kD; ++c) o[c] = 0.f;
-        }
-        if (ok && valid && pass == 0) {
-            float z = 0.f;
+                for (int c = 0; c < kD; ++c) o[c] = 0.f;
+            }
+            if (ok && valid && pass == 0) {
+                float2 z[2] = {};
+                const float2 zero = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int c = 0; c < kD; ++c) z = fmaf(o[c], 0.f, z);
-            if (z != 0.f) *(volatile int *)&ctl.redo = 1;   // NaN: some sum is not finite
-        }
-        if (ok && valid) {
-            if (pass && *(volatile int *)&ctl.nonfinite) {
-                // the values left out that this row sees: a positive weight times such a value is such a value
-                for (int j = j0; j < j1; ++j) {
-                    const int key0 = kbase + j * kKeys;
-                    for (int key = max(lo, key0); key < min(hi, key0 + kKeys); ++key) {
-                        size_t at;
-                        if (kPaged) {
-                            const int blk = __ldg(p.table + (size_t)b * p.max_blocks + key / kBlockKeys);
-                            if ((unsigned)blk >= (unsigned)p.num_blocks) continue;
-                            at = (((size_t)blk * p.Hkv + hk) * kBlockKeys + key % kBlockKeys) * kD;
-                        } else {
-                            at = (((size_t)b * p.Hkv + hk) * (size_t)p.cap + key) * kD;
-                        }
-                        if constexpr (kFp8) {
-                            const uint8_t *v = static_cast<const uint8_t *>(p.v) + at;
+                for (int c = 0; c < kD; c += 2) z[c / 2 & 1] = __ffma2_rn(make_float2(o[c], o[c + 1]), zero, z[c / 2 & 1]);
+                if ((z[0].x + z[0].y) + (z[1].x + z[1].y) != 0.f) *(volatile int *)&ctl.redo = 1;   // NaN: some sum is not finite
+            }
+            if (ok && valid) {
+                if (pass && *(volatile int *)&ctl.nonfinite) {
+                    // the values left out that this row sees: a positive weight times such a value is such a value
+                    for (int j = j0; j < j1; ++j) {
+                        const int key0 = kbase + j * kKeys;
+                        for (int key = max(lo, key0); key < min(hi, key0 + kKeys); ++key) {
+                            size_t at;
+                            if (kPaged) {
+                                const int blk = __ldg(p.table + (size_t)b * p.max_blocks + key / kBlockKeys);
+                                if ((unsigned)blk >= (unsigned)p.num_blocks) continue;
+                                at = (((size_t)blk * p.Hkv + hk) * kBlockKeys + key % kBlockKeys) * kD;
+                            } else {
+                                at = (((size_t)b * p.Hkv + hk) * (size_t)p.cap + key) * kD;
+                            }
+                            if constexpr (kFp8) {
+                                const uint8_t *v = static_cast<const uint8_t *>(p.v) + at;
 #pragma unroll
-                            for (int c = 0; c < kD; ++c)
-                                if ((v[c] & 0x7F) == 0x7F) o[c] = __int_as_float(0x7FC00000);
-                        } else {
-                            const uint16_t *v = static_cast<const uint16_t *>(p.v) + at;
+                                for (int c = 0; c < kD; ++c)
+                                    if ((v[c] & 0x7F) == 0x7F) o[c] = __int_as_float(0x7FC00000);
+                            } else {
+                                const uint16_t *v = static_cast<const uint16_t *>(p.v) + at;
 #pragma unroll
-                            for (int c = 0; c < kD; ++c)
-                                if ((v[c] & 0x7F80) == 0x7F80) o[c] += __uint_as_float((uint32_t)v[c] << 16);
+                                for (int c = 0; c < kD; ++c)
+                                    if ((v[c] & 0x7F80) == 0x7F80) o[c] += __uint_as_float((uint32_t)v[c] << 16);
+                            }
                         }
                     }
                 }
-            }
-            const size_t orow = (size_t)token * p.Hq + head;
-            if (p.part_ml) {
-                const size_t at = (size_t)split * ((size_t)p.T * p.Hq) + orow;
-                p.part_ml[at] = make_float2(m, l);
-                float *dst = p.part_acc + at * kD;
+                    if (p.part_ml) {
+                    const size_t at = (size_t)split * ((size_t)p.T * p.Hq) + orow;
+                    p.part_ml[at] = make_float2(m, l);
+                    float *dst = p.part_acc + at * kD;
 #pragma unroll
-                for (int c = 0; c < kD; c += 8) {
-                    uint32_t w[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(o[c + e] * p.out_scale);
-                    st_32(dst + c, w);
-                }
-            } else {
-                const float inv = l == 0.f ? 0.f : p.out_scale / l;
-                const bool none = l == 0.f;
-#pragma unroll
-                for (int c = 0; c < kD; ++c) o[c] = none ? 0.f : o[c] * inv;
-                if (p.out_f32) {
-                    float *dst = static_cast<float *>(p.out) + orow * kD;
-#pragma unroll
-                    for (int c = 0; c < kD; c += 8) st_32(dst + c, reinterpret_cast<const uint32_t *>(o + c));
-                } else {
-                    uint16_t *dst = static_cast<uint16_t *>(p.out) + orow * kD;
-#pragma unroll
-                    for (int c = 0; c < kD; c += 16) {
+                    for (int c = 0; c < kD; c += 8) {
                         uint32_t w[8];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) w[e] = pack_bf16(o[c + 2 * e], o[c + 2 * e + 1]);
+                        for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(o[c + e] * p.out_scale);
                         st_32(dst + c, w);
+                    }
+                } else {
+                    const float inv = l == 0.f ? 0.f : p.out_scale / l;
+                    if (l == 0.f)
+#pragma unroll
+                        for (int c = 0; c < kD; ++c) o[c] = 0.f;
+#pragma unroll
+                    for (int c = 0; c < kD; c += 2) {
+                        const float2 x = __fmul2_rn(make_float2(o[c], o[c + 1]), make_float2(inv, inv));
+                        o[c] = x.x;
+                        o[c + 1] = x.y;
+                    }
+                    if (p.out_f32) {
+                        float *dst = static_cast<float *>(p.out) + (size_t)orow * kD;
+#pragma unroll
+                        for (int c = 0; c < kD; c += 8) st_32(dst + c, reinterpret_cast<const uint32_t *>(o + c));
+                    } else {
+                        uint16_t *dst = static_cast<uint16_t *>(p.out) + (size_t)orow * kD;
+#pragma unroll
+                        for (int c = 0; c < kD; c += 16) {
+                            uint32_t w[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) w[e] = pack_bf16(o[c + 2 * e], o[c + 2 * e + 1]);
+                            st_32(dst + c, w);
+                        }
                     }
                 }
             }
-        }
-        __syncwarp();
+            __syncwarp();
         } while (again(pass++));
     }
-    fence_before();
-    __syncthreads();
-    if (*gave_up) {
+    if (*gave_up) {   // the same in every thread: the last wait lies before the last barrier
         // A wait ran out (never expected): flag it, and let the copies in flight land before the memory is given up
         if (threadIdx.x == 0) flag_error(p.err, DR_ERRF_TIMEOUT);
         if (warp == kProducer) {
@@ -1029,10 +1047,9 @@ cudaError_t launch_variant(const PromptParams &p, int splits, cudaStream_t strea
     if (tiles > by_tokens) tiles = by_tokens;
     TileParams tp;
     tp.p = p;
-    tp.splits = splits;
-    tp.g_shift = 0;
-    while ((1 << tp.g_shift) < p.g) ++tp.g_shift;
-    tp.g_mul = (uint32_t)(((1ull << 32) * ((1ull << tp.g_shift) - p.g)) / p.g + 1);
+    tp.splits.set((uint32_t)splits);
+    tp.heads.set((uint32_t)p.Hkv);
+    tp.group.set((uint32_t)p.g);
     return launch_kernel(kern, dim3((unsigned)(tiles * splits * p.Hkv)), dim3(C::kThreads), smem, stream, 1u, mk,
                          mv, tp);
 }
@@ -1041,9 +1058,11 @@ cudaError_t launch_variant(const PromptParams &p, int splits, cudaStream_t strea
 
 cudaError_t launch_attn_tiles(const PromptParams &p, bool paged, bool fp8, int splits, cudaStream_t stream) {
     const bool plain = p.cap_c1 == 0.f && !p.slopes;
-    // e4m3: two tiles per CTA, so that the conversion of a key tile serves both (8192-token prompt, 16 heads: 207 -> 174
-    // us); bf16: two CTAs per SM with a tile each (177 -> 167 us).
-#define DR_PICK2(N, F, P) (plain ? launch_variant<N, F, P, true>(p, splits, stream) : launch_variant<N, F, P, false>(p, splits, stream))
+    // e4m3: two tiles per CTA, so that the conversion of a key tile serves both; bf16: two CTAs per SM with a tile each,
+    // whose phases drift apart.  An 8192-token prompt of 16 heads when both could be had for either: e4m3 174 us against
+    // 207, bf16 167 against 177.
+#define DR_PICK2(N, F, P) \
+    (plain ? launch_variant<N, F, P, true>(p, splits, stream) : launch_variant<N, F, P, false>(p, splits, stream))
     if (fp8) return paged ? DR_PICK2(2, true, true) : DR_PICK2(2, true, false);
     return paged ? DR_PICK2(1, false, true) : DR_PICK2(1, false, false);
 #undef DR_PICK2
@@ -1053,7 +1072,7 @@ cudaError_t launch_attn_tiles(const PromptParams &p, bool paged, bool fp8, int s
 // states that they leave and that are read again.  The plan takes the s with the least
 //   waves x run + 0.7 run (several waves end unevenly) + 2.5 us + states written and read at 4 TB/s  (s > 1),
 // run = key tiles per CTA x 1.2 us (a step of a CTA with a full SM), waves = CTAs / CTAs that fit, at least 1.
-// 3 rows of 300..700 tokens on up to 20000 e4m3 keys, 16 heads: 278 us unsplit, see the measured table for the split.
+// 3 rows of 300..700 tokens on up to 20000 e4m3 keys, 16 heads: 150 us, UNSPLIT us without a workspace.
 int plan_tile_splits(int T, int g, int Hkv, int max_len, bool fp8, int sms) {
     const int rows = fp8 ? 256 : 128, slots = fp8 ? sms : 2 * sms;
     const double units = (double)(((long long)T * g + rows - 1) / rows) * Hkv;

@@ -10,6 +10,9 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 // the attention kernels read keys and write outputs and states 32 bytes at a time
 bool aligned32(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 
+// Keys per row: the kernels look a few tiles past a row's end in 32-bit key numbers.
+constexpr int kMaxCap = 0x7FFFF000;
+
 // Validates a cache description; on success stores the keys a row can hold in *cap.
 dr_status check_cache(const dr_kv_cache *c, int *cap) {
     if (!c || !c->k || !c->v || !aligned16(c->k) || !aligned16(c->v)) return DR_ERR_INVALID_ARG;
@@ -18,14 +21,14 @@ dr_status check_cache(const dr_kv_cache *c, int *cap) {
         (!(c->k_scale > 0.f) || !(c->v_scale > 0.f) || isinf(c->k_scale) || isinf(c->v_scale)))
         return DR_ERR_INVALID_ARG;
     if (c->layout == DR_KV_CONTIGUOUS) {
-        if (c->max_len < 1) return DR_ERR_INVALID_ARG;
+        if (c->max_len < 1 || c->max_len > kMaxCap) return DR_ERR_INVALID_ARG;
         *cap = c->max_len;
         return DR_OK;
     }
     if (c->layout != DR_KV_PAGED) return DR_ERR_INVALID_ARG;
     if (!c->block_table || c->num_blocks < 1 || c->max_blocks_per_seq < 1) return DR_ERR_INVALID_ARG;
     if (c->block_size != dr::kBlockKeys) return DR_ERR_UNSUPPORTED;
-    if ((long long)c->max_blocks_per_seq * c->block_size > 0x7FFFFFFFLL) return DR_ERR_INVALID_ARG;
+    if ((long long)c->max_blocks_per_seq * c->block_size > kMaxCap) return DR_ERR_INVALID_ARG;
     *cap = c->max_blocks_per_seq * c->block_size;
     return DR_OK;
 }
