@@ -45,41 +45,36 @@ constexpr int kRows = 128;   // query rows per tile (MMA M) and keys per tile (M
 constexpr int kKeys = 128;
 constexpr float kSlack = 8.0f;
 constexpr int kBitsRing = 8;
-constexpr int kMaxStages = 4;
+constexpr int kMaxStages = 3;
 constexpr uint32_t kTileBytes = kKeys * kD * 2;   // a K, V or Q tile of 16-bit elements: 16 KB
 
-template <int kWG, bool kFp8>
+template <bool kFp8>
 struct Config {
-    static constexpr int kHelperWarps = kFp8 ? 2 : 1;            // per operand that they work on (e4m3: K and V; bf16: V)
-    static constexpr int kOtherWarps = kFp8 ? 8 : 4;             // two producers, an MMA warp per tile, helpers
-    static constexpr int kThreads = 128 * kWG + 32 * kOtherWarps;
-    static constexpr int kCtasPerSm = kWG == 1 ? 2 : 1;
-    static constexpr int kTma = kFp8 ? 4 : 3;      // stages that TMA fills (bf16: the MMA reads them)
-    static constexpr int kMma = kFp8 ? 3 : kTma;                 // stages that the MMA reads
+    static constexpr int kProducers = kFp8 ? 1 : 2;              // e4m3: one warp loads K and V
+    static constexpr int kMmaWarp = 4 + kProducers, kHelper = kMmaWarp + 1;
+    static constexpr int kThreads = 256, kCtasPerSm = 2;
+    static constexpr int kTma = kFp8 ? 2 : 3;                    // stages that TMA fills (bf16: the MMA reads them)
+    static constexpr int kMma = kFp8 ? 2 : kTma;                 // stages that the MMA reads
     static constexpr uint32_t kTmaBytes = kKeys * kD * (kFp8 ? 1 : 2);
-    static constexpr uint32_t kQ = 0, kK = kWG * kTileBytes, kV = kK + kMma * kTileBytes,
-                              kRawK = kV + kMma * kTileBytes, kRawV = kRawK + (kFp8 ? kTma * kTmaBytes : 0),
-                              kEnd = kRawV + (kFp8 ? kTma * kTmaBytes : 0);
-    // Registers: softmax threads hold a row of 128 scores; the rest needs few.  The shares add up to the launch's.
-    static constexpr int kLaunchRegs = 65536 / kCtasPerSm / kThreads;
-    static constexpr int kSoftmaxRegs = kWG == 1 ? 184 : 192;
-    static constexpr int kOtherRegs = kWG == 1 ? 72 : 64;
-    static_assert(128 * kWG * kSoftmaxRegs + 32 * kOtherWarps * kOtherRegs <= kThreads * kLaunchRegs, "register split");
-    static_assert(kLaunchRegs % 8 == 0 && (kWG == 2) == kFp8, "built for one tile of bf16, two of e4m3");
-    // tensor memory columns: per warpgroup S (128), O (64), P (64, two weights per column)
-    static constexpr uint32_t kTmemCols = 256 * kWG;
+    static constexpr uint32_t kQ = 0, kK = kTileBytes, kV = kK + kMma * kTileBytes, kRawK = kV + kMma * kTileBytes,
+                              kRawV = kRawK + (kFp8 ? kTma * kTmaBytes : 0), kEnd = kRawV + (kFp8 ? kTma * kTmaBytes : 0);
 };
+// Registers: softmax threads hold a row of 128 scores; the rest needs few.  The shares add up to the launch's.
+constexpr int kLaunchRegs = 128, kSoftmaxRegs = 184, kOtherRegs = 72;
+static_assert(kSoftmaxRegs + kOtherRegs <= 2 * kLaunchRegs, "register split");
+// tensor memory columns: S (128), O (64), P (64, two weights per column)
+constexpr uint32_t kTmemCols = 256;
 
 struct Control {   // at Config::kEnd of the dynamic shared memory
     uint64_t k_full[kMaxStages], k_empty[kMaxStages], v_full[kMaxStages], v_empty[kMaxStages];
     uint64_t k_ready[kMaxStages], v_ready[kMaxStages], kc_empty[kMaxStages], vc_empty[kMaxStages];
-    uint64_t q_full[2], s_full[2], s_free[2], p_full[2], o_done[2];
+    uint64_t q_full, s_full, s_free, p_full, o_done;
     uint32_t tmem;
     int gave_up, redo, nonfinite;
     int bits[kBitsRing];                 // per tile: which of its eight 16-key blocks are there
     int b, qt, s0, n, L, prefix;         // the CTA's row and tile
-    int lo_min[2], hi_max[2];            // keys that some row of the warpgroup sees
-    int lo_max, hi_min;                  // keys that every row of the CTA sees
+    int lo_min, hi_max;                  // keys that some row sees
+    int lo_max, hi_min;                  // keys that every row sees
 };
 
 // n / d for n < 2^31 by a product and a shift (a division takes some 30 instructions, and the start of a CTA has five).
@@ -163,29 +158,28 @@ __device__ __forceinline__ void visible(const PromptParams &p, int t, int i, int
     if (lo >= hi) lo = hi = 0;
 }
 
-template <int kWG, bool kFp8, bool kPaged, bool kPlain>
-__global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>::kCtasPerSm)
+template <bool kFp8, bool kPaged, bool kPlain>
+__global__ void __launch_bounds__(Config<kFp8>::kThreads, Config<kFp8>::kCtasPerSm)
     attn_tiles_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                       const TileParams tp) {
-    using C = Config<kWG, kFp8>;
+    using C = Config<kFp8>;
     extern __shared__ __align__(1024) uint8_t smem[];
     Control &ctl = *reinterpret_cast<Control *>(smem + C::kEnd);
     const PromptParams &p = tp.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr int kProducer = 4 * kWG, kMmaWarp = kProducer + 2, kHelper = kMmaWarp + kWG;   // an MMA warp per tile
+    constexpr int kProducer = 4, kMmaWarp = C::kMmaWarp, kHelper = C::kHelper;
 
     if (warp == 1) {   // a lane per barrier
-        static_assert(offsetof(Control, q_full) == 32 * 8 && offsetof(Control, tmem) == 42 * 8, "order of the barriers");
+        constexpr int kRing = 8 * kMaxStages;
+        static_assert(kRing <= 32 && offsetof(Control, q_full) == kRing * 8 && offsetof(Control, tmem) == (kRing + 5) * 8,
+                      "order of the barriers");
         uint64_t *bars = reinterpret_cast<uint64_t *>(&ctl);
-        const int ring = lane / kMaxStages, kind = lane / 2;
-        mbar_init(bars + lane, ring == 0 || ring == 2 ? 1 : ring < 4 ? (kFp8 ? C::kHelperWarps : 1)
-                                                  : ring < 6 ? C::kHelperWarps : kWG);
-        if (lane < 10) mbar_init(bars + 32 + lane, kind == 1 || kind == 4 ? 1 : 4);
-        if (lane < 2) {
-            ctl.lo_min[lane] = 0x7FFFFFFF;
-            ctl.hi_max[lane] = 0;
-        }
+        // the four softmax warps arrive at q_full, s_free and p_full, one thread or the tensor pipe at the others
+        if (lane < kRing + 5)
+            mbar_init(bars + lane, lane == kRing || lane == kRing + 2 || lane == kRing + 3 ? 4 : 1);
         if (lane == 0) {
+            ctl.lo_min = 0x7FFFFFFF;
+            ctl.hi_max = 0;
             ctl.lo_max = 0;
             ctl.hi_min = 0x7FFFFFFF;
             ctl.gave_up = (smem_u32(smem) & 1023u) != 0;   // never: the swizzled tiles need 1024-byte alignment
@@ -200,7 +194,7 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
     // what that grid still has to take.
     if (warp == kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ctl.tmem)),
-                     "r"(C::kTmemCols));
+                     "r"(kTmemCols));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
         fence_before();
     }
@@ -208,12 +202,11 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
     // Which tile of which row: tiles of the rows in turn, a row's last (longest, when causal) tile of all heads first
     const unsigned unit = tp.heads.of(blockIdx.x), tile_no = tp.splits.of(unit);
     const int hk = (int)(blockIdx.x - unit * tp.heads.d), split = (int)(unit - tile_no * tp.splits.d);
-    constexpr unsigned rows_per_cta = kRows * kWG;
     if (warp == 0) {
         int want = (int)tile_no;
         int b = -1, s0 = 0, n = 0, L = 0, prefix = 0;
         if (!p.row_start) {
-            const int tiles = (int)(((unsigned)p.T * (unsigned)p.g + rows_per_cta - 1) / rows_per_cta);
+            const int tiles = (int)(((unsigned)p.T * (unsigned)p.g + kRows - 1) / (unsigned)kRows);
             if (want < tiles) b = 0;
             n = p.T;
             L = __ldg(p.kv_len);
@@ -234,7 +227,7 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
                 if (b >= 0) continue;
                 const int len = e - a;
                 const int tiles =
-                    len > p.few_max ? (int)(((unsigned)len * (unsigned)p.g + rows_per_cta - 1) / rows_per_cta) : 0;
+                    len > p.few_max ? (int)(((unsigned)len * (unsigned)p.g + kRows - 1) / (unsigned)kRows) : 0;
                 int sum = tiles;
 #pragma unroll
                 for (int off = 1; off < 32; off <<= 1) {
@@ -280,19 +273,19 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
     if (ctl.b < 0 || ctl.gave_up) {   // past the last tile
         if (ctl.gave_up && threadIdx.x == 0) flag_error(p.err, DR_ERRF_TIMEOUT);
         if (warp == kMmaWarp)
-            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kTmemCols));
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
         return;
     }
     const int b = ctl.b, L = ctl.L, n = ctl.n;
 
     // The keys that the softmax threads' rows see, and those that some and all rows of the CTA see
-    const int wg = warp >> 2, row = threadIdx.x & 127;
+    const int row = threadIdx.x;
     int lo = 0, hi = 0, pos = 0, orow = 0;   // orow: token * Hq + head
     bool valid = false;
     uint4 qw[8];   // the query, on its way while the keys that it sees are found out
-    const unsigned flat0 = (unsigned)ctl.qt * rows_per_cta, flat_end = (unsigned)n * (unsigned)p.g;   // T * Hq < 2^31
+    const unsigned flat0 = (unsigned)ctl.qt * (unsigned)kRows, flat_end = (unsigned)n * (unsigned)p.g;   // T * Hq < 2^31
     if (warp < kProducer) {
-        const unsigned flat = flat0 + wg * kRows + row;
+        const unsigned flat = flat0 + row;
         valid = flat < flat_end;
         if (valid) {
             const unsigned i = tp.group.of(flat);
@@ -307,7 +300,7 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
             for (int c = 0; c < 8; ++c) qw[c] = make_uint4(0, 0, 0, 0);
         }
     }
-    int lo_min[kWG], hi_max[kWG], clo, chi;
+    int ulo, uhi, clo, chi;
     if (p.first_key) {
         if (warp < kProducer) {
             const bool sees = hi > lo;
@@ -316,63 +309,34 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
             const int b0 = __reduce_max_sync(0xFFFFFFFFu, lo);
             const int b1 = __reduce_min_sync(0xFFFFFFFFu, sees ? hi : 0x7FFFFFFF);
             if (lane == 0) {
-                atomicMin(&ctl.lo_min[wg], a0);
-                atomicMax(&ctl.hi_max[wg], a1);
+                atomicMin(&ctl.lo_min, a0);
+                atomicMax(&ctl.hi_max, a1);
                 atomicMax(&ctl.lo_max, b0);
                 atomicMin(&ctl.hi_min, b1);
             }
         }
         __syncthreads();
-#pragma unroll
-        for (int w = 0; w < kWG; ++w) {
-            lo_min[w] = ctl.lo_min[w];
-            hi_max[w] = ctl.hi_max[w];
-        }
+        ulo = ctl.lo_min;
+        uhi = ctl.hi_max;
         clo = ctl.lo_max;
         chi = ctl.hi_min;
+        if (ulo >= uhi) ulo = uhi = 0;
     } else {   // from key 0 to an end that does not fall from one token to the next
         const auto end_of = [&](unsigned flat) -> int {
             int a, e, q;
             visible(p, ctl.s0, (int)tp.group.of(flat), n, L, ctl.prefix, a, e, q);
             return e;
         };
-        clo = 0;
+        ulo = clo = 0;
         chi = end_of(flat0);
-#pragma unroll
-        for (int w = 0; w < kWG; ++w) {
-            const unsigned f = flat0 + w * kRows, last = min(f + kRows, flat_end) - 1;
-            lo_min[w] = 0;
-            hi_max[w] = f < flat_end ? end_of(last) : 0;
-        }
+        uhi = end_of(min(flat0 + kRows, flat_end) - 1);
     }
 
-    // Key tiles: tile i covers keys [kbase + 128 i, + 128); this split's run, and each warpgroup's part of it
-    int ulo = 0x7FFFFFFF, uhi = 0;
-#pragma unroll
-    for (int w = 0; w < kWG; ++w) {
-        if (lo_min[w] < hi_max[w]) {
-            ulo = min(ulo, lo_min[w]);
-            uhi = max(uhi, hi_max[w]);
-        }
-    }
-    if (ulo >= uhi) ulo = uhi = 0;
+    // Key tiles: tile i covers keys [kbase + 128 i, + 128); this split's run of them
     const int kbase = ulo & ~(kBlockKeys - 1);
-    const int all = (uhi - kbase + kKeys - 1) / kKeys;
+    const int all = (int)((unsigned)(uhi - kbase + kKeys - 1) / kKeys);
     const int per = (int)tp.splits.of((unsigned)all + tp.splits.d - 1);
-    const int t_lo = min(split * per, all), t_hi = min(t_lo + per, all);
-    int jb[kWG], je[kWG], cb = t_hi, ce = t_lo;
-#pragma unroll
-    for (int w = 0; w < kWG; ++w) {
-        jb[w] = je[w] = t_lo;
-        if (lo_min[w] < hi_max[w]) {
-            jb[w] = max(t_lo, (lo_min[w] - kbase) / kKeys);
-            je[w] = max(jb[w], min(t_hi, (hi_max[w] - kbase + kKeys - 1) / kKeys));
-        }
-        if (je[w] > jb[w]) {
-            cb = min(cb, jb[w]);
-            ce = max(ce, je[w]);
-        }
-    }
+    const int cb = min(split * per, all), ce = min(cb + per, all);
     volatile int *gave_up = &ctl.gave_up;
     // Twice at most.  A value that is not finite makes a sum of every row of its tile NaN (0 times infinity), of rows that
     // do not see it too.  So where some row ends up with sums that are not finite, the CTA goes over its keys once more,
@@ -384,16 +348,15 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
     };
 
     if (warp >= kProducer) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp < kMmaWarp) {
-            // K by the first producer warp, V by the second.  Block ids of four tiles at a time, one per lane, loaded four
-            // tiles ahead (a load per tile, waited for in turn, took longer than the tile's arithmetic): lane 8 y + x has
-            // block x of tile y of the group.  z of a block that is not there is out of range.
-            const bool is_v = warp != kProducer;
-            const CUtensorMap *map = is_v ? &map_v : &map_k;
-            uint64_t *full = is_v ? ctl.v_full : ctl.k_full, *empty = is_v ? ctl.v_empty : ctl.k_empty;
-            const uint32_t ring = smem_u32(smem + (kFp8 ? (is_v ? C::kRawV : C::kRawK) : (is_v ? C::kV : C::kK)));
-            const int stages = C::kTma, kv_row = kPaged ? 0 : b * p.Hkv + hk;
+            // bf16: K by the first producer warp, V by the second.  Block ids of four tiles at a time, one per lane, loaded
+            // four tiles ahead (a load per tile, waited for in turn, took longer than the tile's arithmetic): lane 8 y + x
+            // has block x of tile y of the group.  z of a block that is not there is out of range.
+            const bool does_k = warp == kProducer, does_v = kFp8 || warp != kProducer;
+            const uint32_t ring_k = smem_u32(smem + (kFp8 ? C::kRawK : C::kK)),
+                           ring_v = smem_u32(smem + (kFp8 ? C::kRawV : C::kV));
+            const int kv_row = kPaged ? 0 : b * p.Hkv + hk;
             const bool leader = elect_one();
             const auto group_ids = [&](int j) -> int {   // tiles j .. j + 3
                 const int key = kbase + j * kKeys + lane * kBlockKeys;
@@ -412,7 +375,7 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
                             ids_next = group_ids(j + 4);
                             // a block that some row sees and that is not in the pool
                             const int key = kbase + j * kKeys + lane * kBlockKeys;
-                            if (!is_v && key < uhi && key < kbase + ce * kKeys && (unsigned)ids >= (unsigned)p.num_blocks)
+                            if (does_k && key < uhi && key < kbase + ce * kKeys && (unsigned)ids >= (unsigned)p.num_blocks)
                                 flag_error(p.err, DR_ERRF_BLOCK_ID);
                             ids = (unsigned)ids < (unsigned)p.num_blocks ? ids * p.Hkv + hk : -1;
                         }
@@ -423,21 +386,27 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
                             if (z[x] < 0) z[x] = p.num_blocks * p.Hkv;
                         }
                     }
-                    if (round > 0 && !__all_sync(0xFFFFFFFFu, mbar_wait(&empty[s], (round - 1) & 1, gave_up))) break;
-                    const uint32_t dst = ring + s * C::kTmaBytes;
-                    // one lane of a converged warp: eight lanes with a box each take turns, and took over 100 cycles per box
-                    if (leader) {
-                        if (!is_v) ctl.bits[i % kBitsRing] = (int)bits;
-                        mbar_expect_tx(&full[s], C::kTmaBytes);
-                        if (kPaged) {
+                    // Boxes by one lane of a converged warp: eight lanes with one each take turns, and took over 100 cycles
+                    // per box
+                    const auto load = [&](const CUtensorMap *map, uint32_t dst, uint64_t *full, uint64_t *empty) -> bool {
+                        if (round > 0 && !__all_sync(0xFFFFFFFFu, mbar_wait(empty, (round - 1) & 1, gave_up))) return false;
+                        if (leader) {
+                            if (map == &map_k) ctl.bits[i % kBitsRing] = (int)bits;
+                            mbar_expect_tx(full, C::kTmaBytes);
+                            if (kPaged) {
 #pragma unroll
-                            for (int x = 0; x < 8; ++x) tma_load_3d(dst + x * (C::kTmaBytes / 8), map, 0, 0, z[x], &full[s]);
-                        } else {
-                            tma_load_3d(dst, map, 0, kbase + j * kKeys, kv_row, &full[s]);
+                                for (int x = 0; x < 8; ++x)
+                                    tma_load_3d(dst + x * (C::kTmaBytes / 8), map, 0, 0, z[x], full);
+                            } else {
+                                tma_load_3d(dst, map, 0, kbase + j * kKeys, kv_row, full);
+                            }
                         }
-                    }
-                    __syncwarp();
-                    if (++s == stages) {
+                        __syncwarp();
+                        return true;
+                    };
+                    if (does_k && !load(&map_k, ring_k + s * C::kTmaBytes, &ctl.k_full[s], &ctl.k_empty[s])) break;
+                    if (does_v && !load(&map_v, ring_v + s * C::kTmaBytes, &ctl.v_full[s], &ctl.v_empty[s])) break;
+                    if (++s == C::kTma) {
                         s = 0;
                         ++round;
                     }
@@ -459,52 +428,46 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
             const auto wait2 = [&](uint64_t *x, uint32_t px, uint64_t *y, uint32_t py) {
                 return (bool)__all_sync(0xFFFFFFFFu, mbar_wait2(x, px, y, py, gave_up));
             };
-            const int w = warp - kMmaWarp;   // the tile (warpgroup) that this warp serves
-            const int jw = w == 0 ? jb[0] : jb[kWG - 1], jx = w == 0 ? je[0] : je[kWG - 1];
-            const uint32_t td = tmem + 256 * w;
             int s = 0, round = 0, sp = 0, roundp = 0, made = 0, used = 0, pass = 0;
-            bool ok = wait(&ctl.q_full[w], 0);
+            bool ok = wait(&ctl.q_full, 0);
             do {
                 // Step j: S of tile j, then O of tile j - 1.  What is likely there is waited for before what is not.
                 if (ok && cb < ce) ok = wait(&k_in[s], round & 1);
                 for (int j = cb; j <= ce && cb < ce && ok; ++j) {
                     const int s1 = s + 1 == C::kMma ? 0 : s + 1, round1 = s + 1 == C::kMma ? round + 1 : round;
                     if (j < ce) {
-                        if (j >= jw && j < jx) {
-                            if (made > 0) ok = wait(&ctl.s_free[w], (made - 1) & 1);
-                            if (!ok) break;
-                            fence_after();
-                            const uint64_t qa = desc_at(dq, w * kTileBytes), ka = desc_at(dk, s * kTileBytes);
-                            if (leader) {
+                        if (made > 0) ok = wait(&ctl.s_free, (made - 1) & 1);
+                        if (!ok) break;
+                        fence_after();
+                        const uint64_t ka = desc_at(dk, s * kTileBytes);
+                        if (leader) {
 #pragma unroll
-                                for (int k = 0; k < kD / 16; ++k)
-                                    mma_ss(td, desc_at(qa, 32 * k), desc_at(ka, 32 * k), id_s, k != 0);
-                                commit(&ctl.s_full[w]);
-                            }
-                            ++made;
+                            for (int k = 0; k < kD / 16; ++k)
+                                mma_ss(tmem, desc_at(dq, 32 * k), desc_at(ka, 32 * k), id_s, k != 0);
+                            commit(&ctl.s_full);
+                            commit(&k_out[s]);
                         }
-                        if (leader) commit(&k_out[s]);
+                        __syncwarp();
+                        ++made;
                     }
                     if (j > cb && j + 1 < ce) ok = wait2(&ctl.v_ready[sp], roundp & 1, &k_in[s1], round1 & 1);
                     else if (j > cb) ok = wait(&ctl.v_ready[sp], roundp & 1);
                     else if (j + 1 < ce) ok = wait(&k_in[s1], round1 & 1);
                     if (!ok) break;
                     if (j > cb) {
-                        if (j - 1 >= jw && j - 1 < jx) {
-                            ok = wait(&ctl.p_full[w], used & 1);
-                            if (!ok) break;
-                            fence_after();
-                            const uint64_t va = desc_at(dv, sp * kTileBytes);
-                            if (leader) {
+                        ok = wait(&ctl.p_full, used & 1);
+                        if (!ok) break;
+                        fence_after();
+                        const uint64_t va = desc_at(dv, sp * kTileBytes);
+                        if (leader) {
 #pragma unroll
-                                for (int k = 0; k < kKeys / 16; ++k)
-                                    mma_ts(td + 128, td + 192 + 8 * k, desc_at(va, 2048 * k), id_o, j - 1 > jw || k != 0);
-                                commit(&ctl.o_done[w]);
-                            }
-                            ++used;
+                            for (int k = 0; k < kKeys / 16; ++k)
+                                mma_ts(tmem + 128, tmem + 192 + 8 * k, desc_at(va, 2048 * k), id_o, j - 1 > cb || k != 0);
+                            commit(&ctl.o_done);
+                            commit(&v_out[sp]);
                         }
-                        if (leader) commit(&v_out[sp]);
                         __syncwarp();
+                        ++used;
                         if (j == ce) {   // the last stage's arrivals, so that none is under way when the CTA ends
                             ok = wait(&v_out[sp], roundp & 1);
                         }
@@ -520,10 +483,9 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
                 }
             } while (again(pass++));
         } else if (kFp8) {
-            // Codes to f16, K by the first helper warps, V by the next
-            const int hw = warp - kHelper, kv = hw / C::kHelperWarps;
-            const int ht = (hw % C::kHelperWarps) * 32 + lane;
-            constexpr int kHt = C::kHelperWarps * 32, kChunks = kKeys * 4 / kHt, kBatch = 4;   // chunks of 16 codes
+            // Codes to f16, K by the first helper warp, V by the second
+            const int kv = warp - kHelper;
+            constexpr int kChunks = kKeys * 4 / 32, kBatch = 4;   // a lane's chunks of 16 codes
             uint64_t *full = kv ? ctl.v_full : ctl.k_full, *empty = kv ? ctl.v_empty : ctl.k_empty;
             uint64_t *ready = kv ? ctl.v_ready : ctl.k_ready, *free_ = kv ? ctl.vc_empty : ctl.kc_empty;
             bool ok = true;
@@ -531,45 +493,49 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
             do {
                 for (int j = cb; j < ce && ok; ++j) {
                     const int key0 = kbase + j * kKeys;
-                    ok = mbar_wait(&full[s], round & 1, gave_up);
-                    if (ok && roundc > 0) ok = mbar_wait(&free_[sc], (roundc - 1) & 1, gave_up);
+                    ok = roundc > 0 ? mbar_wait2(&full[s], round & 1, &free_[sc], (roundc - 1) & 1, gave_up)
+                                    : mbar_wait(&full[s], round & 1, gave_up);
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     if (!ok) break;
                     const bool edge = kv && (key0 < ulo || key0 + kKeys > uhi);   // values that no row sees: zeros
                     const bool mixed = kv && pass && (key0 < clo || key0 + kKeys > chi);
-                    const uint8_t *raw = smem + (kv ? C::kRawV : C::kRawK) + s * C::kTmaBytes;
+                    const uint4 *raw = reinterpret_cast<const uint4 *>(smem + (kv ? C::kRawV : C::kRawK) + s * C::kTmaBytes);
                     uint8_t *dst = smem + (kv ? C::kV : C::kK) + sc * kTileBytes;
                     bool bad = false;
+                    // the next batch is read before the last is written: the reads' latency is hidden
+                    uint4 w[2][kBatch];
+#pragma unroll
+                    for (int e = 0; e < kBatch; ++e) w[0][e] = raw[lane + e * 32];
 #pragma unroll
                     for (int e0 = 0; e0 < kChunks; e0 += kBatch) {
-                        uint4 w[kBatch];
+                        uint4 *now = w[e0 / kBatch & 1], *next = w[(e0 / kBatch + 1) & 1];
+                        if (e0 + kBatch < kChunks)
 #pragma unroll
-                        for (int e = 0; e < kBatch; ++e)
-                            w[e] = *reinterpret_cast<const uint4 *>(raw + (ht + (e0 + e) * kHt) * 16);
+                            for (int e = 0; e < kBatch; ++e) next[e] = raw[lane + (e0 + kBatch + e) * 32];
                         if (edge) {
 #pragma unroll
                             for (int e = 0; e < kBatch; ++e) {
-                                const int key = key0 + ((ht + (e0 + e) * kHt) >> 2);
-                                if (key < ulo || key >= uhi) w[e] = make_uint4(0, 0, 0, 0);
+                                const int key = key0 + ((lane + (e0 + e) * 32) >> 2);
+                                if (key < ulo || key >= uhi) now[e] = make_uint4(0, 0, 0, 0);
                             }
                         }
                         if (mixed) {   // NaN codes (0x7F, 0xFF)
 #pragma unroll
                             for (int e = 0; e < kBatch; ++e) {
-                                bad |= zero_nan_codes(w[e].x);
-                                bad |= zero_nan_codes(w[e].y);
-                                bad |= zero_nan_codes(w[e].z);
-                                bad |= zero_nan_codes(w[e].w);
+                                bad |= zero_nan_codes(now[e].x);
+                                bad |= zero_nan_codes(now[e].y);
+                                bad |= zero_nan_codes(now[e].z);
+                                bad |= zero_nan_codes(now[e].w);
                             }
                         }
 #pragma unroll
                         for (int e = 0; e < kBatch; ++e) {
-                            const int r = (ht + (e0 + e) * kHt) >> 2, c = (ht + (e0 + e) * kHt) & 3;
+                            const int r = (lane >> 2) + (e0 + e) * 8, c = lane & 3;
                             uint4 a, d;
-                            codes4_f16(w[e].x, a.x, a.y);
-                            codes4_f16(w[e].y, a.z, a.w);
-                            codes4_f16(w[e].z, d.x, d.y);
-                            codes4_f16(w[e].w, d.z, d.w);
+                            codes4_f16(now[e].x, a.x, a.y);
+                            codes4_f16(now[e].y, a.z, a.w);
+                            codes4_f16(now[e].z, d.x, d.y);
+                            codes4_f16(now[e].w, d.z, d.w);
                             *reinterpret_cast<uint4 *>(dst + swz(r, 2 * c)) = a;
                             *reinterpret_cast<uint4 *>(dst + swz(r, 2 * c + 1)) = d;
                         }
@@ -594,8 +560,8 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
         } else {
             // Values that no row sees become zeros (whatever the cache holds there), in the second pass those that are not
             // finite too
-            const int ht = (warp - kHelper) * 32 + lane;
-            constexpr int kHt = C::kHelperWarps * 32;
+            const int ht = lane;
+            constexpr int kHt = 32;
             bool ok = true;
             int s = 0, round = 0, pass = 0;
             do {
@@ -641,17 +607,12 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
         }
         __syncwarp();
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
-        int j0 = jb[0], j1 = je[0];
-        if (kWG == 2 && wg == 1) {
-            j0 = jb[kWG - 1];
-            j1 = je[kWG - 1];
-        }
-        const uint32_t ts = tmem + 256 * wg + ((uint32_t)((warp & 3) * 32) << 16), to = ts + 128, tpw = ts + 192;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        const uint32_t ts = tmem + ((uint32_t)((warp & 3) * 32) << 16), to = ts + 128, tpw = ts + 192;
         // The query row goes to the swizzled tile
         float qfac = 1.0f;
         {
-            uint8_t *qs = smem + C::kQ + wg * kTileBytes;
+            uint8_t *qs = smem + C::kQ;
             if (kFp8) {
                 float big = 0.f;
 #pragma unroll
@@ -675,7 +636,7 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
             for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4 *>(qs + swz(row, c)) = qw[c];
             fence_proxy_async();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl.q_full[wg]);
+            if (lane == 0) mbar_arrive(&ctl.q_full);
         }
         const float scale = p.sscale * qfac, c2 = p.cap_c2 * qfac;
         const bool capped = !kPlain && p.cap_c1 != 0.f, biased = !kPlain && p.slopes != nullptr;
@@ -687,10 +648,10 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
         do {
             float m = -INFINITY, mref = 0.f, l = 0.f;
             bool ok = true, s_there = false;
-            for (int j = j0; j < j1; ++j) {
+            for (int j = cb; j < ce; ++j) {
                 const int key0 = kbase + j * kKeys;
                 const bool inside = __all_sync(0xFFFFFFFFu, !sees || (key0 >= lo && key0 + kKeys <= hi));
-                if (!s_there) ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl.s_full[wg], done & 1, gave_up));
+                if (!s_there) ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl.s_full, done & 1, gave_up));
                 if (!ok) break;
                 fence_after();
                 const int bits = ctl.bits[(j - cb) % kBitsRing];
@@ -704,8 +665,8 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
                 };
                 // P and O are the previous tile's until its product is done
                 const auto rescale = [&](bool o_there, bool moved) -> bool {
-                    if (j == j0) return true;
-                    if (!o_there && !__all_sync(0xFFFFFFFFu, mbar_wait(&ctl.o_done[wg], (done - 1) & 1, gave_up))) return false;
+                    if (j == cb) return true;
+                    if (!o_there && !__all_sync(0xFFFFFFFFu, mbar_wait(&ctl.o_done, (done - 1) & 1, gave_up))) return false;
                     fence_after();
                     if (moved) {
 #pragma unroll
@@ -724,7 +685,7 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
                 if (!any_sees) {
                     // A warp without such rows passes on: what its rows of P and O hold is not used.  It keeps step by the
                     // previous tile's product, or its arrival at p_full would be counted for that tile.
-                    if (lane == 0) mbar_arrive(&ctl.s_free[wg]);
+                    if (lane == 0) mbar_arrive(&ctl.s_free);
                     ok = rescale(false, false);
                     if (!ok) break;
                     s_there = false;
@@ -750,20 +711,20 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
                     pin32(s + 96);
                     fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&ctl.s_free[wg]);
+                    if (lane == 0) mbar_arrive(&ctl.s_free);
 #pragma unroll
                     for (int c = 64; c < kKeys; c += 16)
 #pragma unroll
                         for (int e = 0; e < 8; ++e) top[e] = max3(top[e], s[c + 2 * e], s[c + 2 * e + 1]);
                     raise(fmaxf(max3(max3(top[0], top[1], top[2]), top[3], top[4]), max3(top[5], top[6], top[7])) * scale);
                     // Asked before the exponentials, needed after them
-                    const bool o_there = j > j0 && __all_sync(0xFFFFFFFFu, mbar_test(&ctl.o_done[wg], (done - 1) & 1));
+                    const bool o_there = j > cb && __all_sync(0xFFFFFFFFu, mbar_test(&ctl.o_done, (done - 1) & 1));
                     const bool moved = __any_sync(0xFFFFFFFFu, corr != 1.0f);
                     uint32_t pk[kKeys / 2];
                     l += weights<kKeys, kFp8>(s, scale, mref, pk);
                     ok = rescale(o_there, moved);
                     if (!ok) break;
-                    s_there = __all_sync(0xFFFFFFFFu, mbar_test(&ctl.s_full[wg], (done + 1) & 1));
+                    s_there = __all_sync(0xFFFFFFFFu, mbar_test(&ctl.s_full, (done + 1) & 1));
                     st32(tpw, pk);
                     st32(tpw + 32, pk + 32);
                 } else {
@@ -833,19 +794,19 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
                     }
                     fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&ctl.s_free[wg]);
+                    if (lane == 0) mbar_arrive(&ctl.s_free);
                     s_there = false;
                 }
                 wait_st();
                 fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl.p_full[wg]);
+                if (lane == 0) mbar_arrive(&ctl.p_full);
                 ++done;
             }
 
             float o[kD];
-            if (ok && j1 > j0) {
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl.o_done[wg], (done - 1) & 1, gave_up));
+            if (ok && ce > cb) {
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl.o_done, (done - 1) & 1, gave_up));
                 fence_after();
                 ld32(to, o);
                 ld32(to + 32, o + 32);
@@ -872,7 +833,7 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
             if (ok && valid) {
                 if (pass && *(volatile int *)&ctl.nonfinite) {
                     // the values left out that this row sees: a positive weight times such a value is such a value
-                    for (int j = j0; j < j1; ++j) {
+                    for (int j = cb; j < ce; ++j) {
                         const int key0 = kbase + j * kKeys;
                         for (int key = max(lo, key0); key < min(hi, key0 + kKeys); ++key) {
                             size_t at;
@@ -950,7 +911,7 @@ __global__ void __launch_bounds__(Config<kWG, kFp8>::kThreads, Config<kWG, kFp8>
     }
     if (warp == kMmaWarp) {
         fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kTmemCols));
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
     }
 }
 
@@ -1016,19 +977,19 @@ bool encode_cache(CUtensorMap *map, const void *ptr, long long rows, int keys, i
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int kWG, bool kFp8, bool kPaged, bool kPlain>
+template <bool kFp8, bool kPaged, bool kPlain>
 cudaError_t launch_variant(const PromptParams &p, int splits, cudaStream_t stream) {
-    using C = Config<kWG, kFp8>;
-    auto kern = attn_tiles_kernel<kWG, kFp8, kPaged, kPlain>;
+    using C = Config<kFp8>;
+    auto kern = attn_tiles_kernel<kFp8, kPaged, kPlain>;
     constexpr size_t smem = C::kEnd + sizeof(Control);
-    static_assert(smem <= (kWG == 1 ? 113 * 1024 : 227 * 1024), "shared memory");
+    static_assert(smem <= 113 * 1024, "shared memory of two CTAs per SM");
     static std::atomic<uint64_t> ready{0};
     const cudaError_t e = once_per_device(ready, [&]() -> cudaError_t {
         cudaFuncAttributes fa;
         const cudaError_t e1 = cudaFuncGetAttributes(&fa, kern);
         if (e1 != cudaSuccess) return e1;
         // the register split draws on what the launch gives: fewer would leave a warpgroup waiting
-        if (fa.numRegs * C::kThreads < 128 * kWG * C::kSoftmaxRegs + 32 * C::kOtherWarps * C::kOtherRegs)
+        if (fa.numRegs != kLaunchRegs)
             return cudaErrorInvalidConfiguration;
         return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     });
@@ -1039,11 +1000,10 @@ cudaError_t launch_variant(const PromptParams &p, int splits, cudaStream_t strea
     if (rows >= 0x7FFFFFFFLL) return cudaErrorInvalidValue;
     if (!encode_cache(&mk, p.k, rows, keys, box, kFp8) || !encode_cache(&mv, p.v, rows, keys, box, kFp8))
         return cudaErrorInvalidValue;
-    const long long rpc = kRows * kWG;
     // every row may end in a part of a tile; no row has more tiles than tokens
     const long long per_row = p.row_start ? p.B : 1;
-    long long tiles = ((long long)p.T * p.g + per_row * (rpc - 1)) / rpc;
-    const long long by_tokens = ((long long)p.T * ((p.g + rpc - 1) / rpc));
+    long long tiles = ((long long)p.T * p.g + per_row * (kRows - 1)) / kRows;
+    const long long by_tokens = ((long long)p.T * ((p.g + kRows - 1) / kRows));
     if (tiles > by_tokens) tiles = by_tokens;
     TileParams tp;
     tp.p = p;
@@ -1058,13 +1018,10 @@ cudaError_t launch_variant(const PromptParams &p, int splits, cudaStream_t strea
 
 cudaError_t launch_attn_tiles(const PromptParams &p, bool paged, bool fp8, int splits, cudaStream_t stream) {
     const bool plain = p.cap_c1 == 0.f && !p.slopes;
-    // e4m3: two tiles per CTA, so that the conversion of a key tile serves both; bf16: two CTAs per SM with a tile each,
-    // whose phases drift apart.  An 8192-token prompt of 16 heads when both could be had for either: e4m3 174 us against
-    // 207, bf16 167 against 177.
-#define DR_PICK2(N, F, P) \
-    (plain ? launch_variant<N, F, P, true>(p, splits, stream) : launch_variant<N, F, P, false>(p, splits, stream))
-    if (fp8) return paged ? DR_PICK2(2, true, true) : DR_PICK2(2, true, false);
-    return paged ? DR_PICK2(1, false, true) : DR_PICK2(1, false, false);
+#define DR_PICK2(F, P) \
+    (plain ? launch_variant<F, P, true>(p, splits, stream) : launch_variant<F, P, false>(p, splits, stream))
+    if (fp8) return paged ? DR_PICK2(true, true) : DR_PICK2(true, false);
+    return paged ? DR_PICK2(false, true) : DR_PICK2(false, false);
 #undef DR_PICK2
 }
 
@@ -1074,8 +1031,8 @@ cudaError_t launch_attn_tiles(const PromptParams &p, bool paged, bool fp8, int s
 // run = key tiles per CTA x 1.2 us (a step of a CTA with a full SM), waves = CTAs / CTAs that fit, at least 1.
 // 3 rows of 300..700 tokens on up to 20000 e4m3 keys, 16 heads: 150 us, UNSPLIT us without a workspace.
 int plan_tile_splits(int T, int g, int Hkv, int max_len, bool fp8, int sms) {
-    const int rows = fp8 ? 256 : 128, slots = fp8 ? sms : 2 * sms;
-    const double units = (double)(((long long)T * g + rows - 1) / rows) * Hkv;
+    const int slots = 2 * sms;
+    const double units = (double)(((long long)T * g + kRows - 1) / kRows) * Hkv;
     const int tiles = max_len / kKeys + 1;
     const double state_us = (double)T * Hkv * g * (kD + 2) * 4 * 2 / 4e6;
     int best = 1;
