@@ -1025,21 +1025,27 @@ cudaError_t launch_attn_tiles(const PromptParams &p, bool paged, bool fp8, int s
 #undef DR_PICK2
 }
 
-// CTAs that share a tile's keys.  Fewer leave SMs idle, or waiting for the one with the longest run of keys; more cost the
-// states that they leave and that are read again.  The plan takes the s with the least
-//   waves x run + 0.7 run (several waves end unevenly) + 2.5 us + states written and read at 4 TB/s  (s > 1),
-// run = key tiles per CTA x 1.2 us (a step of a CTA with a full SM), waves = CTAs / CTAs that fit, at least 1.
-// 3 rows of 300..700 tokens on up to 20000 e4m3 keys, 16 heads: 150 us, UNSPLIT us without a workspace.
-int plan_tile_splits(int T, int g, int Hkv, int max_len, bool fp8, int sms) {
-    const int slots = 2 * sms;
+// CTAs that share a tile's keys.  Fewer leave SMs idle, or waiting for the one with the longest run of keys; more cost
+// each its start and end, and the states that they leave and that are read again.  The plan takes the s with the least
+//   run x step + 5 us, once per wave of CTAs and half a wave more where there are several (they end unevenly),
+//   + s x states, written and read at 4 TB/s, + 2.5 us for the launch that joins them (prompts, s > 1),
+// run = key tiles per CTA, step = 0.83 us for a CTA that has an SM to itself, 1.25 for two on an SM (e4m3 0.92, 1.45).
+// A shared prefix's states are read by CTAs that stream the rows' own keys (own_us of them) and are dearer there, up to
+// three times.  Measured: a chunk of 3 x 300..700 tokens on up to 20000 keys, 16 heads, bf16: 136 us unsplit, 105 by 2,
+// 108 by 4, 123 by 8, 170 by 16; 200 tokens of 4 heads in groups of 4 on 30000 keys: 195 us, 49 by 5, 57 by 6, 43 by 10, 56
+// by 12; a prefix of 500 keys for 8 rows of 16 heads: 10.4 us, 7.8 by 4; of 4096 keys for 128 rows with 64..2048 own:
+// 107 us, 97 by 3, 103 by 10, 112 by 32.
+int plan_tile_splits(int T, int g, int Hkv, int max_len, bool fp8, int sms, bool joined, double own_us) {
     const double units = (double)(((long long)T * g + kRows - 1) / kRows) * Hkv;
     const int tiles = max_len / kKeys + 1;
-    const double state_us = (double)T * Hkv * g * (kD + 2) * 4 * 2 / 4e6;
+    const double state_us = (double)T * Hkv * g * (kD + 2) * 4 * 2 / 4e6 * (own_us < 40 ? 1 + own_us / 20 : 3);
+    const double alone = fp8 ? 0.92 : 0.83, two = fp8 ? 1.45 : 1.25;
     int best = 1;
     double best_us = 0;
-    for (int s = 1; s <= 64 && s <= (tiles + 1) / 2; ++s) {
-        const double run = (double)((tiles + s - 1) / s) * 1.2, waves = units * s / slots;
-        const double us = (waves > 1 ? (waves + 0.7) * run : run) + (s > 1 ? 2.5 + s * state_us : 0);
+    for (int s = 1; s <= 64 && s <= tiles; ++s) {
+        const double run = (tiles + s - 1) / s, waves = units * s / (2 * sms);
+        const double cta = run * (units * s <= sms ? alone : two) + 5;
+        const double us = (waves > 1 ? waves + 0.5 : 1) * cta + (s > 1 ? s * state_us + (joined ? 2.5 : 0) : 0);
         if (s == 1 || us < best_us) {
             best = s;
             best_us = us;

@@ -80,7 +80,7 @@ cudaError_t launch_attn_tokens(const PromptParams &p, bool paged, bool fp8, int 
 cudaError_t launch_attn_tiles(const PromptParams &p, bool paged, bool fp8, int splits, cudaStream_t stream);
 // Joins the states that the tile kernel's splits left (rows of more than few_max tokens).
 cudaError_t launch_attn_join(const PromptParams &p, cudaStream_t stream);
-int plan_tile_splits(int T, int g, int Hkv, int max_len, bool fp8, int sms);
+int plan_tile_splits(int T, int g, int Hkv, int max_len, bool fp8, int sms, bool joined, double own_us);
 int plan_token_splits(long long items, int Hkv, int g, int max_len, bool fp8, int sms);
 
 }  // namespace dr

@@ -79,8 +79,9 @@ dr_status check_scores(float scale, const dr_score_opts *o) {
 
 // The CTAs per tile that the plan gives either cache type (a call that finds less workspace than its plan wants splits
 // less).
-int most_splits(int T, int g, int Hkv, int max_len, int sms) {
-    const int a = dr::plan_tile_splits(T, g, Hkv, max_len, false, sms), b = dr::plan_tile_splits(T, g, Hkv, max_len, true, sms);
+int most_splits(int T, int g, int Hkv, int max_len, int sms, bool joined) {
+    const int a = dr::plan_tile_splits(T, g, Hkv, max_len, false, sms, joined, 0),
+              b = dr::plan_tile_splits(T, g, Hkv, max_len, true, sms, joined, 0);
     return a > b ? a : b;
 }
 
@@ -207,7 +208,7 @@ dr_status dr_prompt_attn(const void *q, int64_t q_stride, const dr_kv_cache *cac
     if (!many) return from_cuda(dr::launch_attn_tokens(p, paged, fp8, few_splits, cs));
     if (!few) p.few_max = 0;
     dr::PromptParams tp = p;
-    int splits = dr::plan_tile_splits(T, p.g, Hkv, len, fp8, sms);
+    int splits = dr::plan_tile_splits(T, p.g, Hkv, len, fp8, sms, true, 0);
     while (splits > 1 && (!ws || ws_bytes < states_bytes(splits, T, Hq))) --splits;
     if (splits > 1) set_states(tp, ws, splits);
     cudaError_t e = dr::launch_attn_tiles(tp, paged, fp8, splits, cs);
@@ -222,7 +223,7 @@ dr_status dr_prompt_attn(const void *q, int64_t q_stride, const dr_kv_cache *cac
 size_t dr_prompt_attn_workspace(int T, int B, int Hq, int Hkv, int max_len, int num_sms) {
     if (T < 1 || B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || max_len < 1 || num_sms < 1) return 0;
     if (T <= B) return 0;
-    const int splits = most_splits(T, Hq / Hkv, Hkv, max_len, num_sms);
+    const int splits = most_splits(T, Hq / Hkv, Hkv, max_len, num_sms, true);
     return splits > 1 ? states_bytes(splits, T, Hq) : 0;
 }
 
@@ -270,28 +271,31 @@ dr_status dr_shared_prefix_attn(const void *q, int64_t q_stride, const dr_kv_cac
     p.out_f32 = out_dtype == DR_F32;
     p.err = err_flag;
     const int plen = max_prefix_hint > 0 && max_prefix_hint < pcap ? max_prefix_hint : pcap;
-    int splits = dr::plan_tile_splits(B, p.g, Hkv, plen, prefix->kv_dtype == DR_KV_FP8_E4M3, sms);
+    const dr_kv_cache *own = cache ? cache : prefix;   // no own keys: the token kernel only joins
+    const bool own_fp8 = own->kv_dtype == DR_KV_FP8_E4M3;
+    const int len = !cache ? 1 : max_seq_len_hint > 0 && max_seq_len_hint < cap ? max_seq_len_hint : cap;
+    // rows are half as long as the longest, or so; 6.7 TB/s
+    const double own_us = !cache ? 0 : (double)B * Hkv * len / 2 * (own_fp8 ? 128 : 256) / 6.7e6;
+    int splits = dr::plan_tile_splits(B, p.g, Hkv, plen, prefix->kv_dtype == DR_KV_FP8_E4M3, sms, false, own_us);
     while (splits > 1 && ws_bytes < states_bytes(splits, B, Hq)) --splits;
     set_states(p, ws, splits);
     const cudaError_t e = dr::launch_attn_tiles(p, prefix->layout == DR_KV_PAGED,
                                                 prefix->kv_dtype == DR_KV_FP8_E4M3, splits, cs);
     if (e != cudaSuccess) return DR_ERR_CUDA;
 
-    const dr_kv_cache *own = cache ? cache : prefix;   // no own keys: the token kernel only joins
     fill_cache(p, own, cache ? cap : pcap);
     fill_scores(p, own, scale, opts);
     p.kv_len = seq_len;
     p.own_len = nullptr;
     p.few_max = 0x7FFFFFFF;
     p.after_tiles = 1;
-    const bool paged = own->layout == DR_KV_PAGED, fp8 = own->kv_dtype == DR_KV_FP8_E4M3;
-    const int len = !cache ? 1 : max_seq_len_hint > 0 && max_seq_len_hint < cap ? max_seq_len_hint : cap;
-    return from_cuda(dr::launch_attn_tokens(p, paged, fp8, dr::plan_token_splits(B, Hkv, p.g, len, fp8, sms), cs));
+    return from_cuda(dr::launch_attn_tokens(p, own->layout == DR_KV_PAGED, own_fp8,
+                                            dr::plan_token_splits(B, Hkv, p.g, len, own_fp8, sms), cs));
 }
 
 size_t dr_shared_prefix_attn_workspace(int B, int Hq, int Hkv, int max_prefix, int num_sms) {
     if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || max_prefix < 1 || num_sms < 1) return 0;
-    return states_bytes(most_splits(B, Hq / Hkv, Hkv, max_prefix, num_sms), B, Hq);
+    return states_bytes(most_splits(B, Hq / Hkv, Hkv, max_prefix, num_sms, false), B, Hq);
 }
 
 }  // extern "C"
