@@ -4,29 +4,30 @@
 //   S = Q K^T (128 query rows x 128 keys, D = 64),  P = 2^(S' - m),  O = O 2^(m_old - m) + P V,  l = l 2^(..) + sum P
 //
 // The g query heads of a kv head and consecutive tokens fill a tile's rows together (row = token * g + head), so one
-// pass over the keys serves them all.  A CTA holds one tile per softmax warpgroup (kWG of them) and walks its keys
-// 128 at a time:
-//   producer warps    TMA loads, K by one warp and V by another (a paged tile is eight 16-key boxes; blocks outside the
-//                     pool and past the last visible key come from an out-of-range coordinate: zeros)
-//   MMA warp          one per tile: S = Q K^T into tensor memory, one key tile ahead of the softmax; O += P V with P read
-//                     from tensor memory and V as the MN-major operand
-//   softmax warps     one thread per query row: S to registers, mask, running maximum, weights, P back to tensor memory
-//   helper warps      bf16: values that no row of the CTA sees become 0.  e4m3: that, and codes to f16 (exact) on the way
-//                     from the TMA's buffer to the MMA's, in four warps, two for K and two for V
-// The softmax takes one of two ways per key tile.  A tile that every row sees whole, with neither cap nor bias, goes
-// through registers at once, and S is given back before the exponentials.  Any other goes through tensor memory a
-// quarter at a time in rolled loops, so that the code stays in the instruction cache.
+// pass over the keys serves them all.  A CTA holds one tile of 128 rows and walks its keys 128 at a time; two CTAs share
+// an SM and their phases drift apart, so that one's products run under the other's exponentials.  Warps of a CTA:
+//   softmax (4)    one thread per query row: S to registers, mask, running maximum, weights, P back to tensor memory
+//   producers      TMA loads, K by one and V by another, e4m3 both by one (a paged tile is eight 16-key boxes; blocks
+//                  outside the pool and past the last visible key come from an out-of-range coordinate: zeros)
+//   MMA            S = Q K^T into tensor memory, one key tile ahead of the softmax; O += P V with P read from tensor
+//                  memory and V as the MN-major operand
+//   helpers        bf16, one: values that no row of the CTA sees become 0.  e4m3, one for K and one for V: that, and
+//                  codes to f16 (exact) on the way from the TMA's buffer to the MMA's
+// The softmax takes one of two ways per key tile.  A tile that every row of the warp sees whole, not capped, goes through
+// registers at once, and S is given back before the exponentials.  Any other goes through tensor memory a quarter at a
+// time in rolled loops, so that the code stays in the instruction cache.
 // The running maximum moves only when a score passes it by 2^8 (log2 units): O is rescaled rarely.  Sums and states are
 // fp32; weights are rounded once, to bf16 (e4m3: f16), for the product with V.
 //
 // What bounds it.  One token of one head costs 256 flops and one exponential per key it sees.  16384 causal tokens of 16
-// heads in bf16: 543 us, 1014 TFLOP/s; the products alone would take 288 us at the library GEMM's rate and the
-// exponentials 230 us of the special-function units.  They overlap between the two CTAs of an SM, but P V runs at 45
-// cycles per instruction where its shape allows 32 (P comes from tensor memory), and the maximum, the packing and the
-// moves to and from tensor memory take issue slots beside the exponentials.  Two threads per row (half the registers, so
-// no spills at higher occupancy), skipping hidden columns inside the straight way, and P V one tile later were each built
-// and were slower.  e4m3: a step of 128 keys x 256 rows takes about 3100 cycles;
-// short documents are bound by a CTA's fixed 6 us (query, pipeline fill, output) rather than by their few keys.
+// heads, bf16: 519 us, 1059 TFLOP/s; the products alone would take 288 us at the library GEMM's rate and the exponentials
+// 230 us of the special-function units.  P V runs at 45 cycles per instruction where its shape allows 32 (P comes from
+// tensor memory), and the maximum, the packing and the moves to and from tensor memory take issue slots beside the
+// exponentials.  Two threads per row (half the registers), skipping hidden columns inside the straight way, and P V one
+// tile later were each built and were slower.  e4m3: 639 us in CTAs of two tiles, 665 in these, where each CTA converts
+// for itself; these win below 4096 tokens (2048: 27.5 us against 31.6) and need no second form.  Short rows are bound by
+// a CTA's start and end: 1304 CTAs without any key take 22 us (9 rows of 364..1812 tokens, 4 heads in groups of 4), the
+// same rows causal 63, capped 118 (three special-function results per score), biased 80.
 //
 // Every wait is bounded (about 2 s): DR_ERRF_TIMEOUT, the CTA writes nothing, drains its copies and frees its tensor
 // memory.
@@ -158,7 +159,10 @@ __device__ __forceinline__ void visible(const PromptParams &p, int t, int i, int
     if (lo >= hi) lo = hi = 0;
 }
 
-template <bool kFp8, bool kPaged, bool kPlain>
+// kMode: what is done to scores before the softmax
+enum : int { kPlain, kBiased, kCapped };   // capped: biased too, or not
+
+template <bool kFp8, bool kPaged, int kMode>
 __global__ void __launch_bounds__(Config<kFp8>::kThreads, Config<kFp8>::kCtasPerSm)
     attn_tiles_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                       const TileParams tp) {
@@ -639,9 +643,11 @@ __global__ void __launch_bounds__(Config<kFp8>::kThreads, Config<kFp8>::kCtasPer
             if (lane == 0) mbar_arrive(&ctl.q_full);
         }
         const float scale = p.sscale * qfac, c2 = p.cap_c2 * qfac;
-        const bool capped = !kPlain && p.cap_c1 != 0.f, biased = !kPlain && p.slopes != nullptr;
+        const bool capped = kMode == kCapped, biased = kMode == kBiased || (kMode == kCapped && p.slopes != nullptr);
         const float slope = biased && valid ? __ldg(p.slopes + orow % p.Hq) * 1.4426950408889634f : 0.f;
         const float mul = capped || biased ? 1.0f : scale;
+        // Where a key lies before the query the bias is linear in the key's number
+        const int whole_hi = kMode == kBiased ? min(hi, pos + 1) : hi;
         // A row that sees no key (or is none) goes along with the others of its warp; its state is put right at the end
         const bool sees = hi > lo, any_sees = __any_sync(0xFFFFFFFFu, sees);
         int done = 0, pass = 0;   // tiles so far
@@ -650,7 +656,7 @@ __global__ void __launch_bounds__(Config<kFp8>::kThreads, Config<kFp8>::kCtasPer
             bool ok = true, s_there = false;
             for (int j = cb; j < ce; ++j) {
                 const int key0 = kbase + j * kKeys;
-                const bool inside = __all_sync(0xFFFFFFFFu, !sees || (key0 >= lo && key0 + kKeys <= hi));
+                const bool inside = __all_sync(0xFFFFFFFFu, !sees || (key0 >= lo && key0 + kKeys <= whole_hi));
                 if (!s_there) ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl.s_full, done & 1, gave_up));
                 if (!ok) break;
                 fence_after();
@@ -689,7 +695,7 @@ __global__ void __launch_bounds__(Config<kFp8>::kThreads, Config<kFp8>::kCtasPer
                     ok = rescale(false, false);
                     if (!ok) break;
                     s_there = false;
-                } else if (kPlain && inside && bits == 0xFF) {
+                } else if (kMode != kCapped && inside && bits == 0xFF) {
                     // The row in registers at once, S given back before the exponentials
                     float s[kKeys];
                     ld32(ts, s);
@@ -699,6 +705,20 @@ __global__ void __launch_bounds__(Config<kFp8>::kThreads, Config<kFp8>::kCtasPer
                     pin32(s + 32);
                     ld32(ts + 64, s + 64);
                     ld32(ts + 96, s + 96);
+                    const float base = slope * (float)(key0 - pos);
+                    const auto bias = [&](int c0) {
+                        if constexpr (kMode == kBiased) {
+                            const float2 slope2 = make_float2(slope, slope), base2 = make_float2(base, base);
+#pragma unroll
+                            for (int c = c0; c < c0 + 64; c += 2) {
+                                const float2 off = __ffma2_rn(make_float2((float)c, (float)(c + 1)), slope2, base2);
+                                const float2 x = __ffma2_rn(make_float2(s[c], s[c + 1]), make_float2(scale, scale), off);
+                                s[c] = x.x;
+                                s[c + 1] = x.y;
+                            }
+                        }
+                    };
+                    bias(0);
                     float top[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) top[e] = fmaxf(s[e], s[56 + e]);
@@ -712,16 +732,17 @@ __global__ void __launch_bounds__(Config<kFp8>::kThreads, Config<kFp8>::kCtasPer
                     fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&ctl.s_free);
+                    bias(64);
 #pragma unroll
                     for (int c = 64; c < kKeys; c += 16)
 #pragma unroll
                         for (int e = 0; e < 8; ++e) top[e] = max3(top[e], s[c + 2 * e], s[c + 2 * e + 1]);
-                    raise(fmaxf(max3(max3(top[0], top[1], top[2]), top[3], top[4]), max3(top[5], top[6], top[7])) * scale);
+                    raise(fmaxf(max3(max3(top[0], top[1], top[2]), top[3], top[4]), max3(top[5], top[6], top[7])) * mul);
                     // Asked before the exponentials, needed after them
                     const bool o_there = j > cb && __all_sync(0xFFFFFFFFu, mbar_test(&ctl.o_done, (done - 1) & 1));
                     const bool moved = __any_sync(0xFFFFFFFFu, corr != 1.0f);
                     uint32_t pk[kKeys / 2];
-                    l += weights<kKeys, kFp8>(s, scale, mref, pk);
+                    l += weights<kKeys, kFp8>(s, mul, mref, pk);
                     ok = rescale(o_there, moved);
                     if (!ok) break;
                     s_there = __all_sync(0xFFFFFFFFu, mbar_test(&ctl.s_full, (done + 1) & 1));
@@ -977,10 +998,10 @@ bool encode_cache(CUtensorMap *map, const void *ptr, long long rows, int keys, i
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool kFp8, bool kPaged, bool kPlain>
+template <bool kFp8, bool kPaged, int kMode>
 cudaError_t launch_variant(const PromptParams &p, int splits, cudaStream_t stream) {
     using C = Config<kFp8>;
-    auto kern = attn_tiles_kernel<kFp8, kPaged, kPlain>;
+    auto kern = attn_tiles_kernel<kFp8, kPaged, kMode>;
     constexpr size_t smem = C::kEnd + sizeof(Control);
     static_assert(smem <= 113 * 1024, "shared memory of two CTAs per SM");
     static std::atomic<uint64_t> ready{0};
@@ -1017,9 +1038,11 @@ cudaError_t launch_variant(const PromptParams &p, int splits, cudaStream_t strea
 }  // namespace
 
 cudaError_t launch_attn_tiles(const PromptParams &p, bool paged, bool fp8, int splits, cudaStream_t stream) {
-    const bool plain = p.cap_c1 == 0.f && !p.slopes;
-#define DR_PICK2(F, P) \
-    (plain ? launch_variant<F, P, true>(p, splits, stream) : launch_variant<F, P, false>(p, splits, stream))
+    const int mode = p.cap_c1 != 0.f ? kCapped : p.slopes ? kBiased : kPlain;
+#define DR_PICK2(F, P)                                                                  \
+    (mode == kPlain    ? launch_variant<F, P, kPlain>(p, splits, stream)                \
+     : mode == kBiased ? launch_variant<F, P, kBiased>(p, splits, stream)               \
+                       : launch_variant<F, P, kCapped>(p, splits, stream))
     if (fp8) return paged ? DR_PICK2(true, true) : DR_PICK2(true, false);
     return paged ? DR_PICK2(false, true) : DR_PICK2(false, false);
 #undef DR_PICK2
