@@ -24,10 +24,10 @@
 // 230 us of the special-function units.  P V runs at 45 cycles per instruction where its shape allows 32 (P comes from
 // tensor memory), and the maximum, the packing and the moves to and from tensor memory take issue slots beside the
 // exponentials.  Two threads per row (half the registers), skipping hidden columns inside the straight way, and P V one
-// tile later were each built and were slower.  e4m3: 639 us in CTAs of two tiles, 665 in these, where each CTA converts
-// for itself; these win below 4096 tokens (2048: 27.5 us against 31.6) and need no second form.  Short rows are bound by
-// a CTA's start and end: 1304 CTAs without any key take 22 us (9 rows of 364..1812 tokens, 4 heads in groups of 4), the
-// same rows causal 63, capped 118 (three special-function results per score), biased 80.
+// tile later were each built and were slower.  e4m3: 608 us; 639 in CTAs of two tiles, which convert the keys once for
+// both but are alone on their SM.  Short rows are bound by a CTA's start and end: 1304 CTAs without any key take 22 us (9
+// rows of 364..1812 tokens, 4 heads in groups of 4), the same rows causal 63, biased 80, capped 118 (three
+// special-function results per score).
 //
 // Every wait is bounded (about 2 s): DR_ERRF_TIMEOUT, the CTA writes nothing, drains its copies and frees its tensor
 // memory.
@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(Config<kFp8>::kThreads, Config<kFp8>::kCtasPer
         } else if (kFp8) {
             // Codes to f16, K by the first helper warp, V by the second
             const int kv = warp - kHelper;
-            constexpr int kChunks = kKeys * 4 / 32, kBatch = 4;   // a lane's chunks of 16 codes
+            constexpr int kChunks = kKeys * 4 / 32, kBatch = 8;   // a lane's chunks of 16 codes
             uint64_t *full = kv ? ctl.v_full : ctl.k_full, *empty = kv ? ctl.v_empty : ctl.k_empty;
             uint64_t *ready = kv ? ctl.v_ready : ctl.k_ready, *free_ = kv ? ctl.vc_empty : ctl.kc_empty;
             bool ok = true;
@@ -506,42 +506,40 @@ __global__ void __launch_bounds__(Config<kFp8>::kThreads, Config<kFp8>::kCtasPer
                     const uint4 *raw = reinterpret_cast<const uint4 *>(smem + (kv ? C::kRawV : C::kRawK) + s * C::kTmaBytes);
                     uint8_t *dst = smem + (kv ? C::kV : C::kK) + sc * kTileBytes;
                     bool bad = false;
-                    // the next batch is read before the last is written: the reads' latency is hidden
-                    uint4 w[2][kBatch];
+                    const auto convert = [&](const uint4 &now, int e) {
+                        const int r = (lane >> 2) + e * 8, c = lane & 3;
+                        uint4 a, d;
+                        codes4_f16(now.x, a.x, a.y);
+                        codes4_f16(now.y, a.z, a.w);
+                        codes4_f16(now.z, d.x, d.y);
+                        codes4_f16(now.w, d.z, d.w);
+                        *reinterpret_cast<uint4 *>(dst + swz(r, 2 * c)) = a;
+                        *reinterpret_cast<uint4 *>(dst + swz(r, 2 * c + 1)) = d;
+                    };
+                    // Eight reads in flight and nothing else in the loop: what bounds a helper is the latency of its own
+                    // instructions (8192-token prompt: two reads in flight 202 us, four 189, eight 172, none converted 163)
+                    if (!edge && !mixed) {
 #pragma unroll
-                    for (int e = 0; e < kBatch; ++e) w[0][e] = raw[lane + e * 32];
+                        for (int e0 = 0; e0 < kChunks; e0 += kBatch) {
+                            uint4 w[kBatch];
 #pragma unroll
-                    for (int e0 = 0; e0 < kChunks; e0 += kBatch) {
-                        uint4 *now = w[e0 / kBatch & 1], *next = w[(e0 / kBatch + 1) & 1];
-                        if (e0 + kBatch < kChunks)
+                            for (int e = 0; e < kBatch; ++e) w[e] = raw[lane + (e0 + e) * 32];
 #pragma unroll
-                            for (int e = 0; e < kBatch; ++e) next[e] = raw[lane + (e0 + kBatch + e) * 32];
-                        if (edge) {
-#pragma unroll
-                            for (int e = 0; e < kBatch; ++e) {
-                                const int key = key0 + ((lane + (e0 + e) * 32) >> 2);
-                                if (key < ulo || key >= uhi) now[e] = make_uint4(0, 0, 0, 0);
-                            }
+                            for (int e = 0; e < kBatch; ++e) convert(w[e], e0 + e);
                         }
-                        if (mixed) {   // NaN codes (0x7F, 0xFF)
-#pragma unroll
-                            for (int e = 0; e < kBatch; ++e) {
-                                bad |= zero_nan_codes(now[e].x);
-                                bad |= zero_nan_codes(now[e].y);
-                                bad |= zero_nan_codes(now[e].z);
-                                bad |= zero_nan_codes(now[e].w);
+                    } else {
+#pragma unroll 1
+                        for (int e = 0; e < kChunks; ++e) {
+                            uint4 now = raw[lane + e * 32];
+                            const int key = key0 + (lane >> 2) + e * 8;
+                            if (key < ulo || key >= uhi) now = make_uint4(0, 0, 0, 0);
+                            if (mixed) {   // NaN codes (0x7F, 0xFF)
+                                bad |= zero_nan_codes(now.x);
+                                bad |= zero_nan_codes(now.y);
+                                bad |= zero_nan_codes(now.z);
+                                bad |= zero_nan_codes(now.w);
                             }
-                        }
-#pragma unroll
-                        for (int e = 0; e < kBatch; ++e) {
-                            const int r = (lane >> 2) + (e0 + e) * 8, c = lane & 3;
-                            uint4 a, d;
-                            codes4_f16(now[e].x, a.x, a.y);
-                            codes4_f16(now[e].y, a.z, a.w);
-                            codes4_f16(now[e].z, d.x, d.y);
-                            codes4_f16(now[e].w, d.z, d.w);
-                            *reinterpret_cast<uint4 *>(dst + swz(r, 2 * c)) = a;
-                            *reinterpret_cast<uint4 *>(dst + swz(r, 2 * c + 1)) = d;
+                            convert(now, e);
                         }
                     }
                     if (bad) ctl.nonfinite = 1;
@@ -749,9 +747,9 @@ __global__ void __launch_bounds__(Config<kFp8>::kThreads, Config<kFp8>::kCtasPer
                     st32(tpw, pk);
                     st32(tpw + 32, pk + 32);
                 } else {
-                    // A quarter at a time in rolled loops: capped, biased and masked scores go back to tensor memory and are
-                    // read again for the exponentials.  Straight-line code for all 128 did not stay in the instruction cache
-                    // (a quarter of its requests missed): documents of 9 rows, 17..2100 tokens, 72 us.
+                    // A quarter at a time in rolled loops: capped, biased and masked scores go back to tensor memory and
+                    // are read again for the exponentials.  With straight-line code for all 128 in place of the loops a
+                    // quarter of the requests to the instruction cache missed (9 rows of documents: 72 us against 61).
                     unsigned hidden = 0;   // quarters that no row of the warp sees
                     float mx = -INFINITY;
 #pragma unroll 1
@@ -1052,7 +1050,7 @@ cudaError_t launch_attn_tiles(const PromptParams &p, bool paged, bool fp8, int s
 // each its start and end, and the states that they leave and that are read again.  The plan takes the s with the least
 //   run x step + 5 us, once per wave of CTAs and half a wave more where there are several (they end unevenly),
 //   + s x states, written and read at 4 TB/s, + 2.5 us for the launch that joins them (prompts, s > 1),
-// run = key tiles per CTA, step = 0.83 us for a CTA that has an SM to itself, 1.25 for two on an SM (e4m3 0.92, 1.45).
+// run = key tiles per CTA, step = 0.83 us for a CTA that has an SM to itself, 1.25 for two on an SM (e4m3 0.88, 1.35).
 // A shared prefix's states are read by CTAs that stream the rows' own keys (own_us of them) and are dearer there, up to
 // three times.  Measured: a chunk of 3 x 300..700 tokens on up to 20000 keys, 16 heads, bf16: 136 us unsplit, 105 by 2,
 // 108 by 4, 123 by 8, 170 by 16; 200 tokens of 4 heads in groups of 4 on 30000 keys: 195 us, 49 by 5, 57 by 6, 43 by 10, 56
@@ -1062,7 +1060,7 @@ int plan_tile_splits(int T, int g, int Hkv, int max_len, bool fp8, int sms, bool
     const double units = (double)(((long long)T * g + kRows - 1) / kRows) * Hkv;
     const int tiles = max_len / kKeys + 1;
     const double state_us = (double)T * Hkv * g * (kD + 2) * 4 * 2 / 4e6 * (own_us < 40 ? 1 + own_us / 20 : 3);
-    const double alone = fp8 ? 0.92 : 0.83, two = fp8 ? 1.45 : 1.25;
+    const double alone = fp8 ? 0.88 : 0.83, two = fp8 ? 1.35 : 1.25;
     int best = 1;
     double best_us = 0;
     for (int s = 1; s <= 64 && s <= tiles; ++s) {
