@@ -26,6 +26,7 @@ struct RopeAppendParams {
     const int32_t *block_table;         // paged only
     int32_t cap, max_blocks, num_blocks, kv_fp8;
     float k_scale, v_scale;
+    float k_inv, v_inv;   // 1 / scale where the scale is a power of two, else 0
     const uint16_t *q, *k, *v;          // [T][heads][64] bf16, tokens *_stride elements apart; q may be null
     uint16_t *q_out;
     int64_t q_stride, k_stride, v_stride, q_out_stride;

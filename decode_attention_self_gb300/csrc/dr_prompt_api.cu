@@ -44,6 +44,13 @@ dr_status check_sizes(int T, int B, int Hq, int Hkv, int D) {
 // A token stride in elements: whole tokens, 16-byte steps.
 bool bad_stride(int64_t stride, int heads) { return stride < (int64_t)heads * dr::kHeadDim || stride % 8 != 0; }
 
+// 1 / x where x is a power of two and both are normal numbers, so that y / x and y * (1 / x) are the same for every y;
+// else 0.
+float exact_inverse(float x) {
+    int e;
+    return frexpf(x, &e) == 0.5f && e > -125 && e < 126 ? 1.0f / x : 0.f;
+}
+
 dr_status from_cuda(cudaError_t e) { return e == cudaSuccess ? DR_OK : DR_ERR_CUDA; }
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -136,6 +143,8 @@ dr_status dr_rope_append(const dr_kv_cache *cache, const void *q, int64_t q_stri
     p.kv_fp8 = cache->kv_dtype == DR_KV_FP8_E4M3;
     p.k_scale = cache->k_scale;
     p.v_scale = cache->v_scale;
+    p.k_inv = exact_inverse(p.k_scale);
+    p.v_inv = exact_inverse(p.v_scale);
     p.q = static_cast<const uint16_t *>(q);
     p.k = static_cast<const uint16_t *>(k);
     p.v = static_cast<const uint16_t *>(v);

@@ -30,12 +30,19 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-__device__ __forceinline__ uint2 codes8(const float (&f)[8], float scale) {
+// Codes of f / scale, inv as in RopeAppendParams
+__device__ __forceinline__ uint2 codes8(const float (&f)[8], float scale, float inv) {
+    float2 x[4];
+    if (inv != 0.f) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = make_float2(__fmul_rn(f[2 * i], inv), __fmul_rn(f[2 * i + 1], inv));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = make_float2(__fdiv_rn(f[2 * i], scale), __fdiv_rn(f[2 * i + 1], scale));
+    }
     uint32_t pk[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        pk[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(
-            make_float2(__fdiv_rn(f[2 * i], scale), __fdiv_rn(f[2 * i + 1], scale)), __NV_SATFINITE, __NV_E4M3);
+    for (int i = 0; i < 4; ++i) pk[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(x[i], __NV_SATFINITE, __NV_E4M3);
     return make_uint2(pk[0] | (pk[1] << 16), pk[2] | (pk[3] << 16));
 }
 
@@ -142,9 +149,9 @@ __global__ void __launch_bounds__(kThreads, 3) rope_append_kernel(const RopeAppe
                 const size_t off = dst + (size_t)(h - nq - (is_v ? p.Hkv : 0)) * dst_head;
                 if (kFp8) {
                     uint8_t *o = static_cast<uint8_t *>(is_v ? p.v_cache : p.k_cache) + off;
-                    const float sc = is_v ? p.v_scale : p.k_scale;
-                    *reinterpret_cast<uint2 *>(o + 8 * u0) = codes8(x, sc);
-                    *reinterpret_cast<uint2 *>(o + 8 * u1) = codes8(y, sc);
+                    const float sc = is_v ? p.v_scale : p.k_scale, inv = is_v ? p.v_inv : p.k_inv;
+                    *reinterpret_cast<uint2 *>(o + 8 * u0) = codes8(x, sc, inv);
+                    *reinterpret_cast<uint2 *>(o + 8 * u1) = codes8(y, sc, inv);
                 } else {
                     uint16_t *o = static_cast<uint16_t *>(is_v ? p.v_cache : p.k_cache) + off;
                     *reinterpret_cast<uint4 *>(o + 8 * u0) = pack8(x);

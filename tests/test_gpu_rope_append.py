@@ -132,6 +132,23 @@ def test_unrotated_append_equals_kv_append(api, cuda_device):
         assert torch.equal(a.k.view(view), b.k.view(view)) and torch.equal(a.v.view(view), b.v.view(view))
 
 
+@pytest.mark.parametrize("k_scale,v_scale", [(1 / 64, 0.0173), (0.75, 2.0 ** -20), (2.0 ** -126, 3e-39), (2.0 ** 90, 7.3),
+                                             (2.0 ** 127, 2.0 ** -124)])
+def test_codes_of_any_scale_equal_kv_append(api, cuda_device, k_scale, v_scale):
+    """The same codes as dr_kv_append's divisions, for scales that are powers of two and others, ties and tiny values."""
+    dev = cuda_device
+    cache = Cache([40, 17, 300], 16, True, True, seed=3, k_scale=k_scale, v_scale=v_scale)
+    gain = torch.tensor([1.0, 2.0 ** -9, 200.0]).view(3, 1, 1)
+    k, v = ((W.randn_bf16((3, 16, D), "cpu", i).float() * gain * s).to(torch.bfloat16).to(dev)
+            for i, s in ((1, k_scale), (2, v_scale)))
+    pos = torch.tensor([39, 0, 255], dtype=torch.int32, device=dev)
+    a, b = cache.gpu(api, dev), cache.gpu(api, dev)
+    api.dr_kv_append(a, k, v, pos)
+    api.dr_rope_append(b, k, v, starts([1, 1, 1]).to(dev), pos)
+    assert torch.equal(a.k, b.k) and torch.equal(a.v, b.v)
+    assert len(a.k.unique()) > 100
+
+
 def test_rotation_in_place(api, cuda_device):
     dev = cuda_device
     q = W.randn_bf16((50, 16, D), dev, 1)
