@@ -8,9 +8,11 @@
 // One warp serves one token (several warps when there are few tokens): lane (s, c) = (lane / 4, lane % 4) holds a
 // pair of 16-byte chunks of head s, s + 8, ... of q, k and v in turn, chosen so that both elements of every rotated
 // pair are in the lane, and reads its 16 table values once for all heads.  The first heads are loaded before the token's
-// row and position are known, and three CTAs fit an SM (80 registers): 65536 tokens, 16 + 2 x 16 heads, 126 us, 6.5 TB/s
-// (150 us with the loads behind the row search and two CTAs per SM); 22000 ragged tokens into an e4m3 cache 28 us, where
-// the exact divisions count.
+// row and position are known, and 24 warps fit an SM (80 registers) in CTAs of four, which leave a shorter tail than CTAs
+// of eight: 65536 tokens, 16 + 2 x 16 heads, 124 us, 6.64 TB/s (126 in CTAs of eight; 150 with the loads behind the row
+// search and 16 warps per SM; 161 with a run of tokens per warp, whose loads wait for the stores before).  22000 ragged
+// tokens into an e4m3 cache take 25 us, where scales that are powers of two save the division (28 us with it): each warp's
+// chain row - position - table is as long as its transfers.
 #include "dr_device.cuh"
 #include "dr_prompt.h"
 #include "dr_rows.cuh"
@@ -18,7 +20,7 @@
 namespace dr {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBatch = 3;   // heads per lane in flight
 
@@ -47,7 +49,7 @@ __device__ __forceinline__ uint2 codes8(const float (&f)[8], float scale, float 
 }
 
 template <bool kPaged, bool kFp8, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads, 3) rope_append_kernel(const RopeAppendParams p, int warps_per_token) {
+__global__ void __launch_bounds__(kThreads, 6) rope_append_kernel(const RopeAppendParams p, int warps_per_token) {
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31;
