@@ -31,6 +31,8 @@
 //
 // Every wait is bounded (about 2 s): DR_ERRF_TIMEOUT, the CTA writes nothing, drains its copies and frees its tensor
 // memory.
+#include <math.h>
+
 #include "dr_prompt.h"
 #include "dr_rows.cuh"
 #include "dr_score.cuh"
@@ -1051,11 +1053,11 @@ cudaError_t launch_attn_tiles(const PromptParams &p, bool paged, bool fp8, int s
 //   run x step + 5 us, once per wave of CTAs and half a wave more where there are several (they end unevenly),
 //   + s x states, written and read at 4 TB/s, + 2.5 us for the launch that joins them (prompts, s > 1),
 // run = key tiles per CTA, step = 0.83 us for a CTA that has an SM to itself, 1.25 for two on an SM (e4m3 0.88, 1.35).
-// A shared prefix's states are read by CTAs that stream the rows' own keys (own_us of them) and are dearer there, up to
-// three times.  Measured: a chunk of 3 x 300..700 tokens on up to 20000 keys, 16 heads, bf16: 136 us unsplit, 105 by 2,
+// The rows' own keys, streamed beside a shared prefix (own_us of them), hide about a quarter of their time of it; the
+// states are read by the same CTAs and are dearer there, up to three times.  Measured: a chunk of 3 x 300..700 tokens on up to 20000 keys, 16 heads, bf16: 136 us unsplit, 105 by 2,
 // 108 by 4, 123 by 8, 170 by 16; 200 tokens of 4 heads in groups of 4 on 30000 keys: 195 us, 49 by 5, 57 by 6, 43 by 10, 56
 // by 12; a prefix of 500 keys for 8 rows of 16 heads: 10.4 us, 7.8 by 4; of 4096 keys for 128 rows with 64..2048 own:
-// 107 us, 97 by 3, 103 by 10, 112 by 32.
+// 107 us, 97 by 2 to 4, 103 by 10, 112 by 32.
 int plan_tile_splits(int T, int g, int Hkv, int max_len, bool fp8, int sms, bool joined, double own_us) {
     const double units = (double)(((long long)T * g + kRows - 1) / kRows) * Hkv;
     const int tiles = max_len / kKeys + 1;
@@ -1066,7 +1068,8 @@ int plan_tile_splits(int T, int g, int Hkv, int max_len, bool fp8, int sms, bool
     for (int s = 1; s <= 64 && s <= tiles; ++s) {
         const double run = (tiles + s - 1) / s, waves = units * s / (2 * sms);
         const double cta = run * (units * s <= sms ? alone : two) + 5;
-        const double us = (waves > 1 ? waves + 0.5 : 1) * cta + (s > 1 ? s * state_us + (joined ? 2.5 : 0) : 0);
+        const double us = fmax((waves > 1 ? waves + 0.5 : 1) * cta, own_us / 4) +
+                          (s > 1 ? s * state_us + (joined ? 2.5 : 0) : 0);
         if (s == 1 || us < best_us) {
             best = s;
             best_us = us;
