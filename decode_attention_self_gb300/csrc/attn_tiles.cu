@@ -646,8 +646,6 @@ __global__ void __launch_bounds__(Config<kFp8>::kThreads, Config<kFp8>::kCtasPer
         const bool capped = kMode == kCapped, biased = kMode == kBiased || (kMode == kCapped && p.slopes != nullptr);
         const float slope = biased && valid ? __ldg(p.slopes + orow % p.Hq) * 1.4426950408889634f : 0.f;
         const float mul = capped || biased ? 1.0f : scale;
-        // Where a key lies before the query the bias is linear in the key's number
-        const int whole_hi = kMode == kBiased ? min(hi, pos + 1) : hi;
         // A row that sees no key (or is none) goes along with the others of its warp; its state is put right at the end
         const bool sees = hi > lo, any_sees = __any_sync(0xFFFFFFFFu, sees);
         int done = 0, pass = 0;   // tiles so far
@@ -656,7 +654,9 @@ __global__ void __launch_bounds__(Config<kFp8>::kThreads, Config<kFp8>::kCtasPer
             bool ok = true, s_there = false;
             for (int j = cb; j < ce; ++j) {
                 const int key0 = kbase + j * kKeys;
-                const bool inside = __all_sync(0xFFFFFFFFu, !sees || (key0 >= lo && key0 + kKeys <= whole_hi));
+                const bool inside = __all_sync(0xFFFFFFFFu, !sees || (key0 >= lo && key0 + kKeys <= hi));
+                // where every visible key lies before the query the bias is linear in the key's number
+                const bool linear = kMode != kBiased || __all_sync(0xFFFFFFFFu, !sees || min(hi, key0 + kKeys) <= pos + 1);
                 if (!s_there) ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl.s_full, done & 1, gave_up));
                 if (!ok) break;
                 fence_after();
@@ -695,22 +695,16 @@ __global__ void __launch_bounds__(Config<kFp8>::kThreads, Config<kFp8>::kCtasPer
                     ok = rescale(false, false);
                     if (!ok) break;
                     s_there = false;
-                } else if (kMode != kCapped && inside && bits == 0xFF) {
+                } else if (kMode == kPlain || (kMode == kBiased && linear)) {
                     // The row in registers at once, S given back before the exponentials
                     float s[kKeys];
-                    ld32(ts, s);
-                    ld32(ts + 32, s + 32);
-                    wait_ld();
-                    pin32(s);
-                    pin32(s + 32);
-                    ld32(ts + 64, s + 64);
-                    ld32(ts + 96, s + 96);
+                    float top[8];
                     const float base = slope * (float)(key0 - pos);
-                    const auto bias = [&](int c0) {
+                    const auto bias = [&] {
                         if constexpr (kMode == kBiased) {
                             const float2 slope2 = make_float2(slope, slope), base2 = make_float2(base, base);
 #pragma unroll
-                            for (int c = c0; c < c0 + 64; c += 2) {
+                            for (int c = 0; c < kKeys; c += 2) {
                                 const float2 off = __ffma2_rn(make_float2((float)c, (float)(c + 1)), slope2, base2);
                                 const float2 x = __ffma2_rn(make_float2(s[c], s[c + 1]), make_float2(scale, scale), off);
                                 s[c] = x.x;
@@ -718,25 +712,62 @@ __global__ void __launch_bounds__(Config<kFp8>::kThreads, Config<kFp8>::kCtasPer
                             }
                         }
                     };
-                    bias(0);
-                    float top[8];
+                    const auto top_first = [&] {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) top[e] = fmaxf(s[e], s[56 + e]);
+                        for (int e = 0; e < 8; ++e) top[e] = fmaxf(s[e], s[56 + e]);
 #pragma unroll
-                    for (int c = 8; c < 56; c += 16)
+                        for (int c = 8; c < 56; c += 16)
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) top[e] = max3(top[e], s[c + 2 * e], s[c + 2 * e + 1]);
+                            for (int e = 0; e < 8; ++e) top[e] = max3(top[e], s[c + 2 * e], s[c + 2 * e + 1]);
+                    };
+                    const auto top_second = [&] {
+#pragma unroll
+                        for (int c = 64; c < kKeys; c += 16)
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) top[e] = max3(top[e], s[c + 2 * e], s[c + 2 * e + 1]);
+                    };
+                    const auto give_back = [&] {
+                        fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&ctl.s_free);
+                    };
+                    ld32(ts, s);
+                    ld32(ts + 32, s + 32);
                     wait_ld();
-                    pin32(s + 64);
-                    pin32(s + 96);
-                    fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&ctl.s_free);
-                    bias(64);
+                    pin32(s);
+                    pin32(s + 32);
+                    ld32(ts + 64, s + 64);
+                    ld32(ts + 96, s + 96);
+                    const bool whole = inside && bits == 0xFF;
+                    // Long prompts gain by an unmasked way of its own (519 us against 544); with a bias the code would grow
+                    // too long for the instruction cache (documents 57 us against 54)
+                    if (kMode == kPlain && whole) {
+                        top_first();
+                        wait_ld();
+                        pin32(s + 64);
+                        pin32(s + 96);
+                        give_back();
+                        top_second();
+                    } else {
+                        wait_ld();
+                        pin32(s + 64);
+                        pin32(s + 96);
+                        give_back();
+                        bias();
+                        const auto below = [](int x) { return __funnelshift_lc(0xFFFFFFFFu, 0u, min(max(x, 0), 32)); };
+                        if (!whole)   // hidden keys, and those of blocks that are not there
 #pragma unroll
-                    for (int c = 64; c < kKeys; c += 16)
+                            for (int k = 0; k < 4; ++k) {
+                                const unsigned there =
+                                    (bits >> (2 * k) & 1 ? 0xFFFFu : 0u) | (bits >> (2 * k) & 2 ? 0xFFFF0000u : 0u);
+                                const unsigned seen = below(hi - key0 - 32 * k) & ~below(lo - key0 - 32 * k) & there;
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) top[e] = max3(top[e], s[c + 2 * e], s[c + 2 * e + 1]);
+                                for (int c = 0; c < 32; ++c)
+                                    if (!(seen & (1u << c))) s[32 * k + c] = -INFINITY;
+                            }
+                        top_first();
+                        top_second();
+                    }
                     raise(fmaxf(max3(max3(top[0], top[1], top[2]), top[3], top[4]), max3(top[5], top[6], top[7])) * mul);
                     // Asked before the exponentials, needed after them
                     const bool o_there = j > cb && __all_sync(0xFFFFFFFFu, mbar_test(&ctl.o_done, (done - 1) & 1));
