@@ -13,9 +13,9 @@
 //                  memory and V as the MN-major operand
 //   helpers        bf16, one: values that no row of the CTA sees become 0.  e4m3, one for K and one for V: that, and
 //                  codes to f16 (exact) on the way from the TMA's buffer to the MMA's
-// The softmax takes one of two ways per key tile.  A tile that every row of the warp sees whole, not capped, goes through
-// registers at once, and S is given back before the exponentials.  Any other goes through tensor memory a quarter at a
-// time in rolled loops, so that the code stays in the instruction cache.
+// The softmax holds a row's 128 scores in registers and gives S back before the exponentials, so that the next product runs
+// under them.  Biases on keys behind the query, and caps with a bias, would make that code too long for the instruction
+// cache: such tiles go through tensor memory a quarter at a time in rolled loops.
 // The running maximum moves only when a score passes it by 2^8 (log2 units): O is rescaled rarely.  Sums and states are
 // fp32; weights are rounded once, to bf16 (e4m3: f16), for the product with V.
 //
@@ -25,9 +25,9 @@
 // tensor memory), and the maximum, the packing and the moves to and from tensor memory take issue slots beside the
 // exponentials.  Two threads per row (half the registers), skipping hidden columns inside the straight way, and P V one
 // tile later were each built and were slower.  e4m3: 608 us; 639 in CTAs of two tiles, which convert the keys once for
-// both but are alone on their SM.  Short rows are bound by a CTA's start and end: 1304 CTAs without any key take 22 us (9
-// rows of 364..1812 tokens, 4 heads in groups of 4), the same rows causal 63, biased 80, capped 118 (three
-// special-function results per score).
+// both but are alone on their SM.  Short rows are bound by a CTA's start and end: 1304 CTAs without any key take 23 us (9
+// rows of 364..1812 tokens, 4 heads in groups of 4), the same rows causal 61, biased 79, capped 110 (three
+// special-function results per score), cut into documents 50.
 //
 // Every wait is bounded (about 2 s): DR_ERRF_TIMEOUT, the CTA writes nothing, drains its copies and frees its tensor
 // memory.
@@ -695,8 +695,9 @@ __global__ void __launch_bounds__(Config<kFp8>::kThreads, Config<kFp8>::kCtasPer
                     ok = rescale(false, false);
                     if (!ok) break;
                     s_there = false;
-                } else if (kMode == kPlain || (kMode == kBiased && linear)) {
-                    // The row in registers at once, S given back before the exponentials
+                } else if (kMode == kPlain || (kMode == kBiased && linear) || (kMode == kCapped && !biased)) {
+                    // The row in registers at once, S given back before the exponentials.  Masked tiles by the rolled way
+                    // below: documents 60 us against 50; capped ones: 118 against 110.
                     float s[kKeys];
                     float top[8];
                     const float base = slope * (float)(key0 - pos);
@@ -754,6 +755,10 @@ __global__ void __launch_bounds__(Config<kFp8>::kThreads, Config<kFp8>::kCtasPer
                         pin32(s + 96);
                         give_back();
                         bias();
+                        if constexpr (kMode == kCapped) {
+#pragma unroll
+                            for (int c = 0; c < kKeys; ++c) s[c] = capped_score(s[c], p.cap_c1, c2);
+                        }
                         const auto below = [](int x) { return __funnelshift_lc(0xFFFFFFFFu, 0u, min(max(x, 0), 32)); };
                         if (!whole)   // hidden keys, and those of blocks that are not there
 #pragma unroll
@@ -781,8 +786,8 @@ __global__ void __launch_bounds__(Config<kFp8>::kThreads, Config<kFp8>::kCtasPer
                     st32(tpw + 32, pk + 32);
                 } else {
                     // A quarter at a time in rolled loops: capped, biased and masked scores go back to tensor memory and
-                    // are read again for the exponentials.  With straight-line code for all 128 in place of the loops a
-                    // quarter of the requests to the instruction cache missed (9 rows of documents: 72 us against 61).
+                    // are read again for the exponentials.  With straight-line code for every combination a quarter of the
+                    // requests to the instruction cache missed (documents with a bias: 72 us against 61).
                     unsigned hidden = 0;   // quarters that no row of the warp sees
                     float mx = -INFINITY;
 #pragma unroll 1
