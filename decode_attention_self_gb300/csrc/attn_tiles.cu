@@ -1090,10 +1090,10 @@ cudaError_t launch_attn_tiles(const PromptParams &p, bool paged, bool fp8, int s
 //   + s x states, written and read at 4 TB/s, + 2.5 us for the launch that joins them (prompts, s > 1),
 // run = key tiles per CTA, step = 0.83 us for a CTA that has an SM to itself, 1.25 for two on an SM (e4m3 0.88, 1.35).
 // The rows' own keys, streamed beside a shared prefix (own_us of them), hide about a quarter of their time of it; the
-// states are read by the same CTAs and are dearer there, up to three times.  Measured: a chunk of 3 x 300..700 tokens on up to 20000 keys, 16 heads, bf16: 136 us unsplit, 105 by 2,
-// 108 by 4, 123 by 8, 170 by 16; 200 tokens of 4 heads in groups of 4 on 30000 keys: 195 us, 49 by 5, 57 by 6, 43 by 10, 56
-// by 12; a prefix of 500 keys for 8 rows of 16 heads: 10.4 us, 7.8 by 4; of 4096 keys for 128 rows with 64..2048 own:
-// 107 us, 97 by 2 to 4, 103 by 10, 112 by 32.
+// states are read by the same CTAs and are dearer there, up to three times.  Measured, bf16: a chunk of 3 x 300..700 tokens
+// on up to 20000 keys, 16 heads: 136 us unsplit, 105 by 2, 108 by 4, 123 by 8, 170 by 16; 200 tokens of 4 heads in groups
+// of 4 on 30000 keys: 195 us, 49 by 5, 57 by 6, 43 by 10, 56 by 12; a prefix of 500 keys for 8 rows of 16 heads: 10.4 us,
+// 7.8 by 4; of 4096 keys for 128 rows with 64..2048 own: 107 us, 97 by 2 to 4, 103 by 10, 112 by 32.
 int plan_tile_splits(int T, int g, int Hkv, int max_len, bool fp8, int sms, bool joined, double own_us) {
     const double units = (double)(((long long)T * g + kRows - 1) / kRows) * Hkv;
     const int tiles = max_len / kKeys + 1;
