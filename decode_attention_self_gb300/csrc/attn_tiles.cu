@@ -24,7 +24,7 @@
 // 230 us of the special-function units.  P V runs at 45 cycles per instruction where its shape allows 32 (P comes from
 // tensor memory), and the maximum, the packing and the moves to and from tensor memory take issue slots beside the
 // exponentials.  Two threads per row (half the registers), skipping hidden columns inside the straight way, and P V one
-// tile later were each built and were slower.  e4m3: 608 us; 639 in CTAs of two tiles, which convert the keys once for
+// tile later were each built and were slower.  e4m3: 602 us; 639 in CTAs of two tiles, which convert the keys once for
 // both but are alone on their SM.  Short rows are bound by a CTA's start and end: 1304 CTAs without any key take 23 us (9
 // rows of 364..1812 tokens, 4 heads in groups of 4), the same rows causal 61, biased 79, capped 110 (three
 // special-function results per score), cut into documents 50.

@@ -370,7 +370,7 @@ dr_status dr_rope_table(float *table, int max_pos, int rot_dim, double base, voi
  * once: to bf16, or to the e4m3 code of fl32(x / scale) as in dr_kv_append.
  * Tokens from row_start[B] on are left as they are (q_out and cache).
  *
- *   cache    : see dr_kv_cache, with Hkv heads; B rows
+ *   cache    : see dr_kv_cache, with Hkv heads; B rows of at most 2^31 - 4096 keys
  *   q        : nullable [T][Hq][D] bf16 (device, 16-byte aligned), tokens q_stride elements apart (a multiple
  *              of 8, at least Hq*D: a slice of a fused projection's output will do)
  *   k, v     : [T][Hkv][D] bf16 likewise, k_stride and v_stride
@@ -418,7 +418,7 @@ typedef struct dr_score_opts {
  * do not reach the result whatever they hold.
  *
  *   q        : [T][Hq][D] bf16 (device, 16-byte aligned), tokens q_stride elements apart (multiple of 8, >= Hq*D)
- *   cache    : see dr_kv_cache, with Hkv heads; B rows; k and v 32-byte aligned
+ *   cache    : see dr_kv_cache, with Hkv heads; B rows of at most 2^31 - 4096 keys; k and v 32-byte aligned
  *   row_start: [B+1] int32 (device), rising from 0 to at most T (DR_ERRF_ROW_START otherwise); rows may be empty;
  *              outputs of tokens from row_start[B] on are left as they are
  *   kv_len   : [B] int32 (device), keys per row, its new tokens' included: n <= kv_len[b] <= capacity (clamped to

@@ -25,6 +25,8 @@ BAD_CACHES = [(dict(GOOD, k=None), 1), (dict(GOOD, v=FAKE + 8), 1), (dict(GOOD, 
               (dict(GOOD, kv_dtype=1, k_scale=1.0, v_scale=float("inf")), 1),
               (dict(layout=1, block_size=16, num_blocks=4, max_blocks_per_seq=2, k=FAKE, v=FAKE), 1),
               (dict(layout=1, block_size=32, num_blocks=4, max_blocks_per_seq=2, k=FAKE, v=FAKE, block_table=FAKE), 2),
+              (dict(GOOD, max_len=2 ** 31 - 4095), 1),     # key numbers past a row's end have to fit 32 bits
+              (dict(layout=1, block_size=16, num_blocks=4, max_blocks_per_seq=1 << 27, k=FAKE, v=FAKE, block_table=FAKE), 1),
               (dict(layout=1, block_size=16, num_blocks=0, max_blocks_per_seq=2, k=FAKE, v=FAKE, block_table=FAKE), 1)]
 
 
