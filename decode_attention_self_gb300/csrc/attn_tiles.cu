@@ -917,7 +917,7 @@ __global__ void __launch_bounds__(Config<kFp8>::kThreads, Config<kFp8>::kCtasPer
                 }
                     if (p.part_ml) {
                     const size_t at = (size_t)split * ((size_t)p.T * p.Hq) + orow;
-                    p.part_ml[at] = make_float2(m, l);
+                    p.part_ml[at] = make_float2(state_max(m, l), l);
                     float *dst = p.part_acc + at * kD;
 #pragma unroll
                     for (int c = 0; c < kD; c += 8) {

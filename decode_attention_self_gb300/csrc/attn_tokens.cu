@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<Tile, kN>())
     cg::cluster_group cluster = cg::this_cluster();
     if (splits > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     const auto finish = [&](size_t row, int d, float ls, float o) {
-        const float res = ls == 0.f ? 0.f : o / ls;   // no key: zero; NaN scores leave NaN
+        const float res = ls == 0.f ? 0.f : o / ls;   // no key: zero; NaN scores leave NaN (state_max)
         if (p.out_f32) static_cast<float *>(p.out)[row * kD + d] = res;
         else static_cast<uint16_t *>(p.out)[row * kD + d] = f32_to_bf16_rn(res);
     };
@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<Tile, kN>())
                 const int h = a * 8 + 2 * c + j;
                 if (h >= nheads) continue;
                 if (r == 0) {
-                    s_m[warp][h] = m[a][j];
+                    s_m[warp][h] = state_max(m[a][j], l[a][j]);
                     s_l[warp][h] = l[a][j];
                 }
 #pragma unroll

@@ -12,6 +12,10 @@ __device__ __forceinline__ float capped_score(float raw, float c1, float c2) {
     return c1 - __fdividef(2.0f * c1, fast_exp2(raw * c2) + 1.0f);
 }
 
+// The maximum to store with a softmax state.  m = -inf marks a state without keys, and the maxima drop NaN: a state whose
+// scores were all NaN (its sum l is NaN) gets a maximum that no merge takes for an empty one.
+__device__ __forceinline__ float state_max(float m, float l) { return m == -INFINITY && l != 0.f ? 0.f : m; }
+
 // The power of two that brings x into [0.5, 1); 1 for zero, infinite and NaN x.  Exponents are kept where both the
 // factor and its reciprocal are normal numbers.
 __device__ __forceinline__ float pow2_normaliser(float x) {
