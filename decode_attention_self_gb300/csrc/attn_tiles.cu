@@ -642,7 +642,8 @@ __global__ void __launch_bounds__(Config<kFp8>::kThreads, Config<kFp8>::kCtasPer
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctl.q_full);
         }
-        const float scale = p.sscale * qfac, c2 = p.cap_c2 * qfac;
+        const float scale = p.sscale * qfac;
+        const ScoreCap cap(p.cap_c1, p.cap_c2 * qfac, scale);
         const bool capped = kMode == kCapped, biased = kMode == kBiased || (kMode == kCapped && p.slopes != nullptr);
         const float slope = biased && valid ? __ldg(p.slopes + orow % p.Hq) * 1.4426950408889634f : 0.f;
         const float mul = capped || biased ? 1.0f : scale;
@@ -755,10 +756,7 @@ __global__ void __launch_bounds__(Config<kFp8>::kThreads, Config<kFp8>::kCtasPer
                         pin32(s + 96);
                         give_back();
                         bias();
-                        if constexpr (kMode == kCapped) {
-#pragma unroll
-                            for (int c = 0; c < kKeys; ++c) s[c] = capped_score(s[c], p.cap_c1, c2);
-                        }
+                        if constexpr (kMode == kCapped) cap(s);
                         const auto below = [](int x) { return __funnelshift_lc(0xFFFFFFFFu, 0u, min(max(x, 0), 32)); };
                         if (!whole)   // hidden keys, and those of blocks that are not there
 #pragma unroll
@@ -802,8 +800,7 @@ __global__ void __launch_bounds__(Config<kFp8>::kThreads, Config<kFp8>::kCtasPer
                         wait_ld();
                         pin32(s);
                         if (capped) {
-#pragma unroll
-                            for (int c = 0; c < 32; ++c) s[c] = capped_score(s[c], p.cap_c1, c2);
+                            cap(s);
                         } else if (biased) {
 #pragma unroll
                             for (int c = 0; c < 32; ++c) s[c] *= scale;

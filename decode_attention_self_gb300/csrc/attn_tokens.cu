@@ -352,6 +352,17 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<Tile, kN>())
             // s[y][a][0..3]: (key r, head 2c), (key r, head 2c+1), (key r+8, head 2c), (key r+8, head 2c+1) of tile y
             const int next = tile + kWarps * kT;
             if (next < te) locate(++pass, next, nxt);
+            if (!kPlain && p.cap_c1 != 0.f) {
+                float raw[kT * kN * 4];
+#pragma unroll
+                for (int e = 0; e < kT * kN * 4; ++e) {
+                    raw[e] = s[e / (kN * 4)][e / 4 % kN][e % 4];
+                    if (Tile::kF16) raw[e] *= qfac[e / 4 % kN][e & 1];
+                }
+                ScoreCap(p.cap_c1, p.cap_c2, p.sscale)(raw);
+#pragma unroll
+                for (int e = 0; e < kT * kN * 4; ++e) s[e / (kN * 4)][e / 4 % kN][e % 4] = raw[e];
+            }
 #pragma unroll
             for (int y = 0; y < kT; ++y)
 #pragma unroll
@@ -359,14 +370,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<Tile, kN>())
 #pragma unroll
                     for (int z = 0; z < 4; ++z) {
                         float v = s[y][a][z];
-                        if (kPlain) {
-                            v *= Tile::kF16 ? qmul[a][z & 1] : p.sscale;
-                        } else {
-                            if (p.cap_c1 != 0.f) v = capped_score(Tile::kF16 ? v * qfac[a][z & 1] : v, p.cap_c1, p.cap_c2);
-                            else v *= Tile::kF16 ? qmul[a][z & 1] : p.sscale;
-                            if (p.slopes)
-                                v -= slope[a][z & 1] * fabsf((float)(pos - (tile + y) * kTile - r - 8 * (z >> 1)));
-                        }
+                        if (kPlain || p.cap_c1 == 0.f) v *= Tile::kF16 ? qmul[a][z & 1] : p.sscale;
+                        if (!kPlain && p.slopes)
+                            v -= slope[a][z & 1] * fabsf((float)(pos - (tile + y) * kTile - r - 8 * (z >> 1)));
                         s[y][a][z] = v;
                     }
             if (!cur.whole) {

@@ -51,7 +51,7 @@ struct PromptParams {
     int32_t cap, max_blocks, num_blocks;
     float sscale;                       // scores in log2 units: raw * sscale (scale * log2 e * k_scale)
     float out_scale;                    // v_scale of an e4m3 cache, else 1
-    float cap_c1, cap_c2;               // score cap: c1 - 2 c1 / (2^(raw c2) + 1); c1 = 0: no cap
+    float cap_c1, cap_c2;               // score cap in log2 units: c1 tanh(raw c2); c1 = 0: no cap
     const float *slopes;                // [Hq] or null: s -= slope * |pos - key|
     const int32_t *row_start;           // [B+1]; null: one query per row, token b = row b
     const int32_t *kv_len;              // [B]; null: no keys (a row's state is its prefix part alone)

@@ -72,7 +72,7 @@ void fill_scores(dr::PromptParams &p, const dr_kv_cache *c, float scale, const d
     p.sscale = s * kLog2e;
     p.slopes = o ? o->slopes : nullptr;
     p.cap_c1 = o ? o->softcap * kLog2e : 0.f;
-    p.cap_c2 = o && o->softcap > 0.f ? 2.0f * kLog2e * s / o->softcap : 0.f;
+    p.cap_c2 = o && o->softcap > 0.f ? s / o->softcap : 0.f;
 }
 
 // A cap so small that 2 log2(e) scale / cap overflows is refused with the other bad numbers.
