@@ -66,20 +66,25 @@ void fill_cache(dr::PromptParams &p, const dr_kv_cache *c, int cap) {
     p.out_scale = fp8 ? c->v_scale : 1.f;
 }
 
+// What a raw score q.k (codes, for an e4m3 cache) is multiplied by.
+float score_scale(const dr_kv_cache *c, float scale) {
+    return (scale > 0.f ? scale : 1.0f / sqrtf((float)dr::kHeadDim)) * (c->kv_dtype == DR_KV_FP8_E4M3 ? c->k_scale : 1.f);
+}
+
 void fill_scores(dr::PromptParams &p, const dr_kv_cache *c, float scale, const dr_score_opts *o) {
-    const float s = (scale > 0.f ? scale : 1.0f / sqrtf((float)dr::kHeadDim)) *
-                    (c && c->kv_dtype == DR_KV_FP8_E4M3 ? c->k_scale : 1.f);
+    const float s = score_scale(c, scale);
     p.sscale = s * kLog2e;
     p.slopes = o ? o->slopes : nullptr;
     p.cap_c1 = o ? o->softcap * kLog2e : 0.f;
     p.cap_c2 = o && o->softcap > 0.f ? s / o->softcap : 0.f;
 }
 
-// A cap so small that 2 log2(e) scale / cap overflows is refused with the other bad numbers.
-dr_status check_scores(float scale, const dr_score_opts *o) {
-    if (!(scale == scale) || isinf(scale)) return DR_ERR_INVALID_ARG;
+// The kernels compute with scale k_scale log2 e and scale k_scale / softcap: refused where one of them overflows.
+dr_status check_scores(const dr_kv_cache *c, float scale, const dr_score_opts *o) {
+    if (!(scale == scale) || isinf(scale) || isinf(score_scale(c, scale) * kLog2e)) return DR_ERR_INVALID_ARG;
     if (!o) return DR_OK;
     if (!(o->softcap >= 0.f) || o->softcap > 1e30f || (o->softcap > 0.f && o->softcap < 1e-6f)) return DR_ERR_INVALID_ARG;
+    if (o->softcap > 0.f && isinf(score_scale(c, scale) / o->softcap)) return DR_ERR_INVALID_ARG;
     if (o->causal != 0 && o->causal != 1) return DR_ERR_INVALID_ARG;
     return DR_OK;
 }
@@ -178,7 +183,7 @@ dr_status dr_prompt_attn(const void *q, int64_t q_stride, const dr_kv_cache *cac
     int cap = 0;
     st = check_cache(cache, &cap);
     if (st != DR_OK) return st;
-    st = check_scores(scale, opts);
+    st = check_scores(cache, scale, opts);
     if (st != DR_OK) return st;
     if (!q || !row_start || !kv_len || !out || !aligned16(q) || !aligned32(out) || bad_stride(q_stride, Hq))
         return DR_ERR_INVALID_ARG;
@@ -251,7 +256,8 @@ dr_status dr_shared_prefix_attn(const void *q, int64_t q_stride, const dr_kv_cac
         st = check_cache(cache, &cap);
         if (st != DR_OK) return st;
     }
-    st = check_scores(scale, opts);
+    st = check_scores(prefix, scale, opts);
+    if (st == DR_OK && cache) st = check_scores(cache, scale, opts);
     if (st != DR_OK) return st;
     if (opts && (opts->prefix_len || opts->first_key)) return DR_ERR_INVALID_ARG;
     if (!q || !prefix_len || !out || !aligned16(q) || !aligned32(out) || bad_stride(q_stride, Hq))

@@ -425,7 +425,8 @@ typedef struct dr_score_opts {
  *              [0, capacity] and flagged DR_ERRF_SEQ_LEN otherwise)
  *   opts     : nullable (causal, nothing else)
  *   max_len_hint : an upper bound the caller knows for kv_len (<= 0: the capacity); tunes the work split only
- *   scale    : <= 0 selects 1/sqrt(D)
+ *   scale    : <= 0 selects 1/sqrt(D); scale * log2 e and scale / softcap, times k_scale for an e4m3 cache, have
+ *              to be finite (DR_ERR_INVALID_ARG otherwise)
  *   out      : [T][Hq][D] in out_dtype (device, 32-byte aligned)
  *   ws       : nullable workspace (device, 32-byte aligned) of ws_bytes; with at least
  *              dr_prompt_attn_workspace bytes few queries over many keys are spread over the GPU.  Its contents
