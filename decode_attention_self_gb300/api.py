@@ -63,10 +63,12 @@ _lib.dr_rope_table.argtypes = [_vp, _i, _i, ctypes.c_double, _vp]
 _lib.dr_rope_append.argtypes = [_cs, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp,
                                 _vp, _i, _i, _i, _i, _i, _i, _i, _i, _vp, _vp]
 _lib.dr_prompt_attn.argtypes = [_vp, _i64, _cs, _vp, _vp, _cs, _i, _i, _i, _i, _i, _i, _f, _vp, _i, _vp, _sz, _vp, _vp]
+_lib.dr_prompt_attn_stall_test.argtypes = _lib.dr_prompt_attn.argtypes[:-1] + [_i, _vp]
 _lib.dr_prompt_attn_workspace.argtypes = [_i, _i, _i, _i, _i, _i]
 _lib.dr_prompt_attn_workspace.restype = _sz
 _lib.dr_shared_prefix_attn.argtypes = [_vp, _i64, _cs, _vp, _cs, _vp, _cs, _i, _i, _i, _i, _i, _i, _f, _vp, _i, _vp, _sz,
                                        _vp, _vp]
+_lib.dr_shared_prefix_attn_stall_test.argtypes = _lib.dr_shared_prefix_attn.argtypes[:-1] + [_i, _vp]
 _lib.dr_shared_prefix_attn_workspace.argtypes = [_i, _i, _i, _i, _i]
 _lib.dr_shared_prefix_attn_workspace.restype = _sz
 _lib.dr_plan_splits.argtypes = [_i, _i, _i, _i, _i]
@@ -76,7 +78,7 @@ _lib.dr_status_string.restype = ctypes.c_char_p
 for _fn in ("dr_kv_append", "dr_decode_self_attn", "dr_decode_cross_attn", "dr_decode_layer",
             "dr_sample_topk_delayed", "dr_embed_tokens", "dr_lm_head", "dr_lm_head_stall_test",
             "dr_decode_self_attn_stall_test", "dr_rope_table", "dr_rope_append", "dr_prompt_attn",
-            "dr_shared_prefix_attn"):
+            "dr_shared_prefix_attn", "dr_prompt_attn_stall_test", "dr_shared_prefix_attn_stall_test"):
     getattr(_lib, _fn).restype = _i
 
 
@@ -464,7 +466,7 @@ def dr_prompt_attn(q: torch.Tensor, cache: KVCache, row_start: torch.Tensor, kv_
                    causal: bool = True, softcap: float = 0.0, slopes: torch.Tensor | None = None,
                    prefix_len: torch.Tensor | None = None, first_key: torch.Tensor | None = None,
                    max_len_hint: int = 0, scale: float = 0.0, workspace: torch.Tensor | None = None,
-                   err_flag: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+                   err_flag: torch.Tensor | None = None, stream=None, _stall_head=None) -> torch.Tensor:
     """Attention of ragged tokens q [T,Hq,D]: row b's tokens are the last of its kv_len[b] keys in the cache."""
     dev = _device()
     qshape = _shape3(q, "q")
@@ -475,12 +477,20 @@ def dr_prompt_attn(q: torch.Tensor, cache: KVCache, row_start: torch.Tensor, kv_
     op, od = _out(out, dev, qshape)
     o = _score_opts(dev, causal, softcap, slopes, prefix_len, first_key, T, B, Hq)
     wp, wn = _workspace_arg(workspace, dev)
-    st = _lib.dr_prompt_attn(qp, qs, c, _vec(row_start, dev, _I32, B + 1, "row_start"),
-                             _vec(kv_len, dev, _I32, B, "kv_len"), o, T, B, Hq, Hkv, D, max_len_hint, scale,
-                             op, od, wp, wn, _vec(err_flag, dev, _I32, 1, "err_flag"), _stream_arg(stream, dev))
+    args = (qp, qs, c, _vec(row_start, dev, _I32, B + 1, "row_start"), _vec(kv_len, dev, _I32, B, "kv_len"), o, T, B, Hq,
+            Hkv, D, max_len_hint, scale, op, od, wp, wn, _vec(err_flag, dev, _I32, 1, "err_flag"))
+    if _stall_head is None:
+        st = _lib.dr_prompt_attn(*args, _stream_arg(stream, dev))
+    else:
+        st = _lib.dr_prompt_attn_stall_test(*args, _stall_head, _stream_arg(stream, dev))
     if st:
         raise DrError("dr_prompt_attn", st)
     return out
+
+
+def dr_prompt_attn_stall_test(stall_head: int, *args, **kwargs) -> torch.Tensor:
+    """Test hook: dr_prompt_attn with one CTA of key/value head stall_head made to time out (see dr_api.h)."""
+    return dr_prompt_attn(*args, _stall_head=int(stall_head), **kwargs)
 
 
 def dr_shared_prefix_attn_workspace(B: int, Hq: int, Hkv: int, max_prefix: int, num_sms: int | None = None) -> int:
@@ -492,7 +502,7 @@ def dr_shared_prefix_attn(q: torch.Tensor, prefix: KVCache, prefix_len: torch.Te
                           workspace: torch.Tensor, cache: KVCache | None = None, seq_len: torch.Tensor | None = None,
                           softcap: float = 0.0, slopes: torch.Tensor | None = None, max_prefix_hint: int = 0,
                           max_seq_len_hint: int = 0, scale: float = 0.0, err_flag: torch.Tensor | None = None,
-                          stream=None) -> torch.Tensor:
+                          stream=None, _stall_head=None) -> torch.Tensor:
     """One query per row, q [B,Hq,D], over the one-row cache `prefix` that all rows share and the row's own keys."""
     dev = _device()
     qshape = _shape3(q, "q")
@@ -506,13 +516,21 @@ def dr_shared_prefix_attn(q: torch.Tensor, prefix: KVCache, prefix_len: torch.Te
     op, od = _out(out, dev, qshape)
     o = _score_opts(dev, False, softcap, slopes, None, None, B, B, Hq)
     wp, wn = _workspace_arg(workspace, dev)
-    st = _lib.dr_shared_prefix_attn(qp, qs, pc, _vec(prefix_len, dev, _I32, 1, "prefix_len"), cp,
-                                    _vec(seq_len, dev, _I32, B, "seq_len"), o, B, Hq, Hkv, D, max_prefix_hint,
-                                    max_seq_len_hint, scale, op, od, wp, wn,
-                                    _vec(err_flag, dev, _I32, 1, "err_flag"), _stream_arg(stream, dev))
+    args = (qp, qs, pc, _vec(prefix_len, dev, _I32, 1, "prefix_len"), cp, _vec(seq_len, dev, _I32, B, "seq_len"), o, B,
+            Hq, Hkv, D, max_prefix_hint, max_seq_len_hint, scale, op, od, wp, wn,
+            _vec(err_flag, dev, _I32, 1, "err_flag"))
+    if _stall_head is None:
+        st = _lib.dr_shared_prefix_attn(*args, _stream_arg(stream, dev))
+    else:
+        st = _lib.dr_shared_prefix_attn_stall_test(*args, _stall_head, _stream_arg(stream, dev))
     if st:
         raise DrError("dr_shared_prefix_attn", st)
     return out
+
+
+def dr_shared_prefix_attn_stall_test(stall_head: int, *args, **kwargs) -> torch.Tensor:
+    """Test hook: dr_shared_prefix_attn with one CTA of key/value head stall_head made to time out (see dr_api.h)."""
+    return dr_shared_prefix_attn(*args, _stall_head=int(stall_head), **kwargs)
 
 
 def loaded_library_path() -> str:

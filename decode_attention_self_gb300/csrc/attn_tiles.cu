@@ -29,8 +29,8 @@
 // rows of 364..1812 tokens, 4 heads in groups of 4), the same rows causal 61, biased 79, capped 110 (three
 // special-function results per score), cut into documents 50.
 //
-// Every wait is bounded (about 2 s): DR_ERRF_TIMEOUT, the CTA writes nothing, drains its copies and frees its tensor
-// memory.
+// Every wait is bounded (about 2 s): DR_ERRF_TIMEOUT, the CTA writes no output (a state that others join becomes NaN), waits
+// for its own copies and products in flight and frees its tensor memory.
 #include <math.h>
 
 #include "dr_prompt.h"
@@ -72,6 +72,7 @@ struct Control {   // at Config::kEnd of the dynamic shared memory
     uint64_t k_full[kMaxStages], k_empty[kMaxStages], v_full[kMaxStages], v_empty[kMaxStages];
     uint64_t k_ready[kMaxStages], v_ready[kMaxStages], kc_empty[kMaxStages], vc_empty[kMaxStages];
     uint64_t q_full, s_full, s_free, p_full, o_done;
+    uint64_t drained;                    // after a wait that ran out: the products in flight
     uint32_t tmem;
     int gave_up, redo, nonfinite;
     int bits[kBitsRing];                 // per tile: which of its eight 16-key blocks are there
@@ -175,20 +176,22 @@ __global__ void __launch_bounds__(Config<kFp8>::kThreads, Config<kFp8>::kCtasPer
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int kProducer = 4, kMmaWarp = C::kMmaWarp, kHelper = C::kHelper;
 
+    // never: the swizzled tiles need 1024-byte alignment.  Such a CTA sees no key and ends as after a wait that ran out.
+    const bool misplaced = (smem_u32(smem) & 1023u) != 0;
     if (warp == 1) {   // a lane per barrier
         constexpr int kRing = 8 * kMaxStages;
-        static_assert(kRing <= 32 && offsetof(Control, q_full) == kRing * 8 && offsetof(Control, tmem) == (kRing + 5) * 8,
+        static_assert(kRing <= 32 && offsetof(Control, q_full) == kRing * 8 && offsetof(Control, tmem) == (kRing + 6) * 8,
                       "order of the barriers");
         uint64_t *bars = reinterpret_cast<uint64_t *>(&ctl);
         // the four softmax warps arrive at q_full, s_free and p_full, one thread or the tensor pipe at the others
-        if (lane < kRing + 5)
+        if (lane < kRing + 6)
             mbar_init(bars + lane, lane == kRing || lane == kRing + 2 || lane == kRing + 3 ? 4 : 1);
         if (lane == 0) {
             ctl.lo_min = 0x7FFFFFFF;
             ctl.hi_max = 0;
             ctl.lo_max = 0;
             ctl.hi_min = 0x7FFFFFFF;
-            ctl.gave_up = (smem_u32(smem) & 1023u) != 0;   // never: the swizzled tiles need 1024-byte alignment
+            ctl.gave_up = misplaced;
             ctl.redo = ctl.nonfinite = 0;
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -268,7 +271,7 @@ __global__ void __launch_bounds__(Config<kFp8>::kThreads, Config<kFp8>::kCtasPer
             ctl.qt = want;
             ctl.s0 = s0;
             ctl.n = n;
-            ctl.L = L;
+            ctl.L = misplaced ? 0 : L;
             ctl.prefix = prefix;
         }
     }
@@ -276,8 +279,7 @@ __global__ void __launch_bounds__(Config<kFp8>::kThreads, Config<kFp8>::kCtasPer
     fence_after();
     pdl_trigger();
     const uint32_t tmem = ctl.tmem;
-    if (ctl.b < 0 || ctl.gave_up) {   // past the last tile
-        if (ctl.gave_up && threadIdx.x == 0) flag_error(p.err, DR_ERRF_TIMEOUT);
+    if (ctl.b < 0) {   // past the last tile
         if (warp == kMmaWarp)
             asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
         return;
@@ -368,11 +370,13 @@ __global__ void __launch_bounds__(Config<kFp8>::kThreads, Config<kFp8>::kCtasPer
                 const int key = kbase + j * kKeys + lane * kBlockKeys;
                 return j < ce && key < uhi ? __ldg(p.table + (size_t)b * p.max_blocks + key / kBlockKeys) : -1;
             };
-            int s = 0, round = 0, pass = 0;
+            // (Test hook: the stalled CTA's first keys are never asked for, and the waits for them run out.)
+            const int skip = does_k && (int)blockIdx.x == p.stall - 1 ? 1 : 0;
+            int s = skip, round = 0, pass = 0, ahead = 0;   // ahead: K of a tile whose V could not be loaded
             do {
                 int ids = 0, ids_next = 0;
                 if (kPaged) ids_next = group_ids(cb);
-                for (int j = cb, i = 0; j < ce; ++j, ++i) {
+                for (int j = cb + skip, i = skip; j < ce; ++j, ++i) {
                     unsigned bits = 0xFFu;
                     int z[8] = {};
                     if (kPaged) {
@@ -411,13 +415,23 @@ __global__ void __launch_bounds__(Config<kFp8>::kThreads, Config<kFp8>::kCtasPer
                         return true;
                     };
                     if (does_k && !load(&map_k, ring_k + s * C::kTmaBytes, &ctl.k_full[s], &ctl.k_empty[s])) break;
-                    if (does_v && !load(&map_v, ring_v + s * C::kTmaBytes, &ctl.v_full[s], &ctl.v_empty[s])) break;
+                    if (does_v && !load(&map_v, ring_v + s * C::kTmaBytes, &ctl.v_full[s], &ctl.v_empty[s])) {
+                        ahead = does_k;
+                        break;
+                    }
                     if (++s == C::kTma) {
                         s = 0;
                         ++round;
                     }
                 }
             } while (again(pass++));
+            if (*gave_up) {   // the last load of each stage
+                const int nv = round * C::kTma + s, nk = nv + ahead;
+                for (int x = 0; x < C::kTma; ++x) {
+                    if (does_k && nk > x && x >= skip) mbar_drain(&ctl.k_full[x], ((nk - 1 - x) / C::kTma) & 1);
+                    if (does_v && nv > x && x >= skip) mbar_drain(&ctl.v_full[x], ((nv - 1 - x) / C::kTma) & 1);
+                }
+            }
         } else if (warp < kHelper) {
             // The whole warp waits, one lane issues: descriptors stay warp-uniform (computed by one lane alone, each MMA
             // took over 100 cycles to issue; the tensor pipe takes one in 45 to 65).
@@ -488,6 +502,11 @@ __global__ void __launch_bounds__(Config<kFp8>::kThreads, Config<kFp8>::kCtasPer
                     }
                 }
             } while (again(pass++));
+            if (*gave_up) {
+                if (leader) commit(&ctl.drained);
+                __syncwarp();
+                mbar_drain(&ctl.drained, 0);
+            }
         } else if (kFp8) {
             // Codes to f16, K by the first helper warp, V by the second
             const int kv = warp - kHelper;
@@ -652,7 +671,7 @@ __global__ void __launch_bounds__(Config<kFp8>::kThreads, Config<kFp8>::kCtasPer
         int done = 0, pass = 0;   // tiles so far
         do {
             float m = -INFINITY, mref = 0.f, l = 0.f;
-            bool ok = true, s_there = false;
+            bool ok = !misplaced, s_there = false;
             for (int j = cb; j < ce; ++j) {
                 const int key0 = kbase + j * kKeys;
                 const bool inside = __all_sync(0xFFFFFFFFu, !sees || (key0 >= lo && key0 + kKeys <= hi));
@@ -884,8 +903,12 @@ __global__ void __launch_bounds__(Config<kFp8>::kThreads, Config<kFp8>::kCtasPer
                 for (int c = 0; c < kD; c += 2) z[c / 2 & 1] = __ffma2_rn(make_float2(o[c], o[c + 1]), zero, z[c / 2 & 1]);
                 if ((z[0].x + z[0].y) + (z[1].x + z[1].y) != 0.f) *(volatile int *)&ctl.redo = 1;   // NaN: some sum is not finite
             }
-            if (ok && valid) {
-                if (pass && *(volatile int *)&ctl.nonfinite) {
+            if (!ok) {   // what is joined must not be an earlier call's: NaN
+                m = 0.f;
+                l = __int_as_float(0x7FC00000);
+            }
+            if ((ok || p.part_ml) && valid) {
+                if (ok && pass && *(volatile int *)&ctl.nonfinite) {
                     // the values left out that this row sees: a positive weight times such a value is such a value
                     for (int j = cb; j < ce; ++j) {
                         const int key0 = kbase + j * kKeys;
@@ -912,7 +935,7 @@ __global__ void __launch_bounds__(Config<kFp8>::kThreads, Config<kFp8>::kCtasPer
                         }
                     }
                 }
-                    if (p.part_ml) {
+                if (p.part_ml) {
                     const size_t at = (size_t)split * ((size_t)p.T * p.Hq) + orow;
                     p.part_ml[at] = make_float2(state_max(m, l), l);
                     float *dst = p.part_acc + at * kD;
@@ -954,14 +977,8 @@ __global__ void __launch_bounds__(Config<kFp8>::kThreads, Config<kFp8>::kCtasPer
         } while (again(pass++));
     }
     if (*gave_up) {   // the same in every thread: the last wait lies before the last barrier
-        // A wait ran out (never expected): flag it, and let the copies in flight land before the memory is given up
         if (threadIdx.x == 0) flag_error(p.err, DR_ERRF_TIMEOUT);
-        if (warp == kProducer) {
-            const long long t0 = clock64();
-            while (clock64() - t0 < (1LL << 20)) {
-            }
-        }
-        __syncthreads();
+        __syncthreads();   // the drained copies and products before the memory is given up
     }
     if (warp == kMmaWarp) {
         fence_after();

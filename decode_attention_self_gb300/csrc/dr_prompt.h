@@ -66,6 +66,8 @@ struct PromptParams {
     int32_t few_max;
     // token kernel: launched right behind the tile kernel of the same call
     int32_t after_tiles;
+    // tile kernel, test hook: CTA stall - 1 never loads its first keys (0: none)
+    int32_t stall;
     // tile kernel: queries of a shared prefix stand own_len[t] keys past its end (null: at their row's last keys)
     const int32_t *own_len;
     // softmax states of key ranges attended before: [nparts][rows = T*Hq] (m, l) and [nparts][rows][64]; null: none

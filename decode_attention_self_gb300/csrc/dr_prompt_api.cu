@@ -108,6 +108,136 @@ void set_states(dr::PromptParams &p, void *ws, int splits) {
     p.nparts = splits;
 }
 
+// dr_prompt_attn's checks, plan and launches; stall_head >= 0 only from the test hook.
+dr_status prompt_call(const void *q, int64_t q_stride, const dr_kv_cache *cache, const int32_t *row_start,
+                      const int32_t *kv_len, const dr_score_opts *opts, int T, int B, int Hq, int Hkv, int D,
+                      int max_len_hint, float scale, void *out, dr_dtype out_dtype, void *ws, size_t ws_bytes,
+                      int32_t *err_flag, int stall_head, void *stream) {
+    dr_status st = check_sizes(T, B, Hq, Hkv, D);
+    if (st != DR_OK) return st;
+    int cap = 0;
+    st = check_cache(cache, &cap);
+    if (st != DR_OK) return st;
+    st = check_scores(cache, scale, opts);
+    if (st != DR_OK) return st;
+    if (!q || !row_start || !kv_len || !out || !aligned16(q) || !aligned32(out) || bad_stride(q_stride, Hq))
+        return DR_ERR_INVALID_ARG;
+    if (out_dtype != DR_BF16 && out_dtype != DR_F32) return DR_ERR_INVALID_ARG;
+    if (!aligned32(ws) || !aligned32(cache->k) || !aligned32(cache->v)) return DR_ERR_INVALID_ARG;
+    if (opts && opts->prefix_len && !opts->causal) return DR_ERR_INVALID_ARG;
+    dr::PromptParams p = {};
+    p.q = static_cast<const uint16_t *>(q);
+    p.q_stride = q_stride;
+    fill_cache(p, cache, cap);
+    fill_scores(p, cache, scale, opts);
+    p.row_start = row_start;
+    p.kv_len = kv_len;
+    p.causal = opts ? opts->causal : 1;
+    p.prefix_len = opts ? opts->prefix_len : nullptr;
+    p.first_key = opts ? opts->first_key : nullptr;
+    p.T = T;
+    p.B = B;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.g = Hq / Hkv;
+    p.out = out;
+    p.out_f32 = out_dtype == DR_F32;
+    p.err = err_flag;
+    const int sms = dr::current_device_sms();
+    if (sms <= 0) return DR_ERR_CUDA;
+    const bool paged = cache->layout == DR_KV_PAGED, fp8 = cache->kv_dtype == DR_KV_FP8_E4M3;
+    const int len = max_len_hint > 0 && max_len_hint < cap ? max_len_hint : cap;
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    // Rows of one token go to the token kernel, longer ones to the tile kernel (it reads a row's keys once for all
+    // its tokens).  The host knows only T and B: one launch when that settles it, else both.
+    p.few_max = 1;
+    const bool few = B > 1 || T == 1, many = T > B;
+    if (!many) p.few_max = 0x7FFFFFFF;
+    const int few_splits = dr::plan_token_splits(B, Hkv, p.g, len, fp8, sms);
+    if (!many) return from_cuda(dr::launch_attn_tokens(p, paged, fp8, few_splits, cs));
+    if (!few) p.few_max = 0;
+    dr::PromptParams tp = p;
+    tp.stall = stall_head + 1;
+    int splits = dr::plan_tile_splits(T, p.g, Hkv, len, fp8, sms, true, 0);
+    while (splits > 1 && (!ws || ws_bytes < states_bytes(splits, T, Hq))) --splits;
+    if (splits > 1) set_states(tp, ws, splits);
+    cudaError_t e = dr::launch_attn_tiles(tp, paged, fp8, splits, cs);
+    if (e == cudaSuccess && few) {
+        p.after_tiles = 1;
+        e = dr::launch_attn_tokens(p, paged, fp8, few_splits, cs);
+    }
+    if (e == cudaSuccess && splits > 1) e = dr::launch_attn_join(tp, cs);
+    return from_cuda(e);
+}
+
+// dr_shared_prefix_attn's checks, plan and launches; stall_head >= 0 only from the test hook.
+dr_status shared_call(const void *q, int64_t q_stride, const dr_kv_cache *prefix, const int32_t *prefix_len,
+                      const dr_kv_cache *cache, const int32_t *seq_len, const dr_score_opts *opts, int B, int Hq, int Hkv,
+                      int D, int max_prefix_hint, int max_seq_len_hint, float scale, void *out, dr_dtype out_dtype,
+                      void *ws, size_t ws_bytes, int32_t *err_flag, int stall_head, void *stream) {
+    dr_status st = check_sizes(B, B, Hq, Hkv, D);
+    if (st != DR_OK) return st;
+    int pcap = 0, cap = 0;
+    st = check_cache(prefix, &pcap);
+    if (st != DR_OK) return st;
+    if ((cache == nullptr) != (seq_len == nullptr)) return DR_ERR_INVALID_ARG;
+    if (cache) {
+        st = check_cache(cache, &cap);
+        if (st != DR_OK) return st;
+    }
+    st = check_scores(prefix, scale, opts);
+    if (st == DR_OK && cache) st = check_scores(cache, scale, opts);
+    if (st != DR_OK) return st;
+    if (opts && (opts->prefix_len || opts->first_key)) return DR_ERR_INVALID_ARG;
+    if (!q || !prefix_len || !out || !aligned16(q) || !aligned32(out) || bad_stride(q_stride, Hq))
+        return DR_ERR_INVALID_ARG;
+    if (out_dtype != DR_BF16 && out_dtype != DR_F32) return DR_ERR_INVALID_ARG;
+    const int sms = dr::current_device_sms();
+    if (!aligned32(prefix->k) || !aligned32(prefix->v) || (cache && (!aligned32(cache->k) || !aligned32(cache->v))))
+        return DR_ERR_INVALID_ARG;
+    if (!ws || !aligned32(ws) || ws_bytes < states_bytes(1, B, Hq)) return DR_ERR_INVALID_ARG;
+    if (sms <= 0) return DR_ERR_CUDA;
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+
+    dr::PromptParams p = {};
+    p.q = static_cast<const uint16_t *>(q);
+    p.q_stride = q_stride;
+    fill_cache(p, prefix, pcap);
+    fill_scores(p, prefix, scale, opts);
+    p.kv_len = prefix_len;
+    p.own_len = seq_len;
+    p.stall = stall_head + 1;
+    p.T = B;
+    p.B = B;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.g = Hq / Hkv;
+    p.out = out;
+    p.out_f32 = out_dtype == DR_F32;
+    p.err = err_flag;
+    const int plen = max_prefix_hint > 0 && max_prefix_hint < pcap ? max_prefix_hint : pcap;
+    const dr_kv_cache *own = cache ? cache : prefix;   // no own keys: the token kernel only joins
+    const bool own_fp8 = own->kv_dtype == DR_KV_FP8_E4M3;
+    const int len = !cache ? 1 : max_seq_len_hint > 0 && max_seq_len_hint < cap ? max_seq_len_hint : cap;
+    // rows are half as long as the longest, or so; 6.7 TB/s
+    const double own_us = !cache ? 0 : (double)B * Hkv * len / 2 * (own_fp8 ? 128 : 256) / 6.7e6;
+    int splits = dr::plan_tile_splits(B, p.g, Hkv, plen, prefix->kv_dtype == DR_KV_FP8_E4M3, sms, false, own_us);
+    while (splits > 1 && ws_bytes < states_bytes(splits, B, Hq)) --splits;
+    set_states(p, ws, splits);
+    const cudaError_t e = dr::launch_attn_tiles(p, prefix->layout == DR_KV_PAGED,
+                                                prefix->kv_dtype == DR_KV_FP8_E4M3, splits, cs);
+    if (e != cudaSuccess) return DR_ERR_CUDA;
+
+    fill_cache(p, own, cache ? cap : pcap);
+    fill_scores(p, own, scale, opts);
+    p.kv_len = seq_len;
+    p.own_len = nullptr;
+    p.few_max = 0x7FFFFFFF;
+    p.after_tiles = 1;
+    return from_cuda(dr::launch_attn_tokens(p, own->layout == DR_KV_PAGED, own_fp8,
+                                            dr::plan_token_splits(B, Hkv, p.g, len, own_fp8, sms), cs));
+}
+
 }  // namespace
 
 extern "C" {
@@ -178,60 +308,18 @@ dr_status dr_prompt_attn(const void *q, int64_t q_stride, const dr_kv_cache *cac
                          const int32_t *kv_len, const dr_score_opts *opts, int T, int B, int Hq, int Hkv, int D,
                          int max_len_hint, float scale, void *out, dr_dtype out_dtype, void *ws, size_t ws_bytes,
                          int32_t *err_flag, void *stream) {
-    dr_status st = check_sizes(T, B, Hq, Hkv, D);
-    if (st != DR_OK) return st;
-    int cap = 0;
-    st = check_cache(cache, &cap);
-    if (st != DR_OK) return st;
-    st = check_scores(cache, scale, opts);
-    if (st != DR_OK) return st;
-    if (!q || !row_start || !kv_len || !out || !aligned16(q) || !aligned32(out) || bad_stride(q_stride, Hq))
-        return DR_ERR_INVALID_ARG;
-    if (out_dtype != DR_BF16 && out_dtype != DR_F32) return DR_ERR_INVALID_ARG;
-    if (!aligned32(ws) || !aligned32(cache->k) || !aligned32(cache->v)) return DR_ERR_INVALID_ARG;
-    if (opts && opts->prefix_len && !opts->causal) return DR_ERR_INVALID_ARG;
-    dr::PromptParams p = {};
-    p.q = static_cast<const uint16_t *>(q);
-    p.q_stride = q_stride;
-    fill_cache(p, cache, cap);
-    fill_scores(p, cache, scale, opts);
-    p.row_start = row_start;
-    p.kv_len = kv_len;
-    p.causal = opts ? opts->causal : 1;
-    p.prefix_len = opts ? opts->prefix_len : nullptr;
-    p.first_key = opts ? opts->first_key : nullptr;
-    p.T = T;
-    p.B = B;
-    p.Hq = Hq;
-    p.Hkv = Hkv;
-    p.g = Hq / Hkv;
-    p.out = out;
-    p.out_f32 = out_dtype == DR_F32;
-    p.err = err_flag;
-    const int sms = dr::current_device_sms();
-    if (sms <= 0) return DR_ERR_CUDA;
-    const bool paged = cache->layout == DR_KV_PAGED, fp8 = cache->kv_dtype == DR_KV_FP8_E4M3;
-    const int len = max_len_hint > 0 && max_len_hint < cap ? max_len_hint : cap;
-    cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    // Rows of one token go to the token kernel, longer ones to the tile kernel (it reads a row's keys once for all
-    // its tokens).  The host knows only T and B: one launch when that settles it, else both.
-    p.few_max = 1;
-    const bool few = B > 1 || T == 1, many = T > B;
-    if (!many) p.few_max = 0x7FFFFFFF;
-    const int few_splits = dr::plan_token_splits(B, Hkv, p.g, len, fp8, sms);
-    if (!many) return from_cuda(dr::launch_attn_tokens(p, paged, fp8, few_splits, cs));
-    if (!few) p.few_max = 0;
-    dr::PromptParams tp = p;
-    int splits = dr::plan_tile_splits(T, p.g, Hkv, len, fp8, sms, true, 0);
-    while (splits > 1 && (!ws || ws_bytes < states_bytes(splits, T, Hq))) --splits;
-    if (splits > 1) set_states(tp, ws, splits);
-    cudaError_t e = dr::launch_attn_tiles(tp, paged, fp8, splits, cs);
-    if (e == cudaSuccess && few) {
-        p.after_tiles = 1;
-        e = dr::launch_attn_tokens(p, paged, fp8, few_splits, cs);
-    }
-    if (e == cudaSuccess && splits > 1) e = dr::launch_attn_join(tp, cs);
-    return from_cuda(e);
+    return prompt_call(q, q_stride, cache, row_start, kv_len, opts, T, B, Hq, Hkv, D, max_len_hint, scale, out, out_dtype,
+                       ws, ws_bytes, err_flag, -1, stream);
+}
+
+dr_status dr_prompt_attn_stall_test(const void *q, int64_t q_stride, const dr_kv_cache *cache, const int32_t *row_start,
+                                    const int32_t *kv_len, const dr_score_opts *opts, int T, int B, int Hq, int Hkv, int D,
+                                    int max_len_hint, float scale, void *out, dr_dtype out_dtype, void *ws, size_t ws_bytes,
+                                    int32_t *err_flag, int stall_head, void *stream) {
+    if (stall_head < 0 || stall_head >= Hkv) return DR_ERR_INVALID_ARG;
+    if (T <= B) return DR_ERR_UNSUPPORTED;
+    return prompt_call(q, q_stride, cache, row_start, kv_len, opts, T, B, Hq, Hkv, D, max_len_hint, scale, out, out_dtype,
+                       ws, ws_bytes, err_flag, stall_head, stream);
 }
 
 size_t dr_prompt_attn_workspace(int T, int B, int Hq, int Hkv, int max_len, int num_sms) {
@@ -246,66 +334,18 @@ dr_status dr_shared_prefix_attn(const void *q, int64_t q_stride, const dr_kv_cac
                                 int Hq, int Hkv, int D, int max_prefix_hint, int max_seq_len_hint, float scale,
                                 void *out, dr_dtype out_dtype, void *ws, size_t ws_bytes, int32_t *err_flag,
                                 void *stream) {
-    dr_status st = check_sizes(B, B, Hq, Hkv, D);
-    if (st != DR_OK) return st;
-    int pcap = 0, cap = 0;
-    st = check_cache(prefix, &pcap);
-    if (st != DR_OK) return st;
-    if ((cache == nullptr) != (seq_len == nullptr)) return DR_ERR_INVALID_ARG;
-    if (cache) {
-        st = check_cache(cache, &cap);
-        if (st != DR_OK) return st;
-    }
-    st = check_scores(prefix, scale, opts);
-    if (st == DR_OK && cache) st = check_scores(cache, scale, opts);
-    if (st != DR_OK) return st;
-    if (opts && (opts->prefix_len || opts->first_key)) return DR_ERR_INVALID_ARG;
-    if (!q || !prefix_len || !out || !aligned16(q) || !aligned32(out) || bad_stride(q_stride, Hq))
-        return DR_ERR_INVALID_ARG;
-    if (out_dtype != DR_BF16 && out_dtype != DR_F32) return DR_ERR_INVALID_ARG;
-    const int sms = dr::current_device_sms();
-    if (!aligned32(prefix->k) || !aligned32(prefix->v) || (cache && (!aligned32(cache->k) || !aligned32(cache->v))))
-        return DR_ERR_INVALID_ARG;
-    if (!ws || !aligned32(ws) || ws_bytes < states_bytes(1, B, Hq)) return DR_ERR_INVALID_ARG;
-    if (sms <= 0) return DR_ERR_CUDA;
-    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    return shared_call(q, q_stride, prefix, prefix_len, cache, seq_len, opts, B, Hq, Hkv, D, max_prefix_hint,
+                       max_seq_len_hint, scale, out, out_dtype, ws, ws_bytes, err_flag, -1, stream);
+}
 
-    dr::PromptParams p = {};
-    p.q = static_cast<const uint16_t *>(q);
-    p.q_stride = q_stride;
-    fill_cache(p, prefix, pcap);
-    fill_scores(p, prefix, scale, opts);
-    p.kv_len = prefix_len;
-    p.own_len = seq_len;
-    p.T = B;
-    p.B = B;
-    p.Hq = Hq;
-    p.Hkv = Hkv;
-    p.g = Hq / Hkv;
-    p.out = out;
-    p.out_f32 = out_dtype == DR_F32;
-    p.err = err_flag;
-    const int plen = max_prefix_hint > 0 && max_prefix_hint < pcap ? max_prefix_hint : pcap;
-    const dr_kv_cache *own = cache ? cache : prefix;   // no own keys: the token kernel only joins
-    const bool own_fp8 = own->kv_dtype == DR_KV_FP8_E4M3;
-    const int len = !cache ? 1 : max_seq_len_hint > 0 && max_seq_len_hint < cap ? max_seq_len_hint : cap;
-    // rows are half as long as the longest, or so; 6.7 TB/s
-    const double own_us = !cache ? 0 : (double)B * Hkv * len / 2 * (own_fp8 ? 128 : 256) / 6.7e6;
-    int splits = dr::plan_tile_splits(B, p.g, Hkv, plen, prefix->kv_dtype == DR_KV_FP8_E4M3, sms, false, own_us);
-    while (splits > 1 && ws_bytes < states_bytes(splits, B, Hq)) --splits;
-    set_states(p, ws, splits);
-    const cudaError_t e = dr::launch_attn_tiles(p, prefix->layout == DR_KV_PAGED,
-                                                prefix->kv_dtype == DR_KV_FP8_E4M3, splits, cs);
-    if (e != cudaSuccess) return DR_ERR_CUDA;
-
-    fill_cache(p, own, cache ? cap : pcap);
-    fill_scores(p, own, scale, opts);
-    p.kv_len = seq_len;
-    p.own_len = nullptr;
-    p.few_max = 0x7FFFFFFF;
-    p.after_tiles = 1;
-    return from_cuda(dr::launch_attn_tokens(p, own->layout == DR_KV_PAGED, own_fp8,
-                                            dr::plan_token_splits(B, Hkv, p.g, len, own_fp8, sms), cs));
+dr_status dr_shared_prefix_attn_stall_test(const void *q, int64_t q_stride, const dr_kv_cache *prefix, const int32_t *prefix_len,
+                                           const dr_kv_cache *cache, const int32_t *seq_len, const dr_score_opts *opts, int B,
+                                           int Hq, int Hkv, int D, int max_prefix_hint, int max_seq_len_hint, float scale,
+                                           void *out, dr_dtype out_dtype, void *ws, size_t ws_bytes, int32_t *err_flag,
+                                           int stall_head, void *stream) {
+    if (stall_head < 0 || stall_head >= Hkv) return DR_ERR_INVALID_ARG;
+    return shared_call(q, q_stride, prefix, prefix_len, cache, seq_len, opts, B, Hq, Hkv, D, max_prefix_hint,
+                       max_seq_len_hint, scale, out, out_dtype, ws, ws_bytes, err_flag, stall_head, stream);
 }
 
 size_t dr_shared_prefix_attn_workspace(int B, int Hq, int Hkv, int max_prefix, int num_sms) {

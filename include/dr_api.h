@@ -88,7 +88,7 @@ typedef enum dr_kv_dtype {
 #define DR_ERRF_BLOCK_ID 2 /* a needed block-table entry outside [0, num_blocks); its keys were skipped */
 #define DR_ERRF_POS 4      /* an append position outside [0, capacity) or on an unmapped block; row skipped */
 #define DR_ERRF_TOKEN 8    /* a token outside [0, V) in dr_embed_tokens; that codebook's row was skipped */
-#define DR_ERRF_TIMEOUT 16 /* a bounded on-chip wait gave up (never expected); that CTA's results were not written */
+#define DR_ERRF_TIMEOUT 16 /* a bounded on-chip wait gave up (never expected); that CTA's results were not written, or are NaN where they are joined with others' */
 #define DR_ERRF_ROW_START 32 /* row_start does not rise from 0 to at most T; rows were cut to [0, T) */
 
 /* Sampler flags. */
@@ -438,6 +438,25 @@ dr_status dr_prompt_attn(const void *q, int64_t q_stride, const dr_kv_cache *cac
                          int max_len_hint, float scale, void *out, dr_dtype out_dtype, void *ws, size_t ws_bytes,
                          int32_t *err_flag, void *stream);
 
+/*
+ * dr_prompt_attn_stall_test -- TEST HOOK, never needed in use.  The same call
+ * as dr_prompt_attn, except that one CTA of the tile kernel never loads its
+ * first keys: that of the first tile's first key range, key/value head
+ * stall_head (the tile: the last 128 (token, query head) pairs of that head in
+ * the first row of several tokens).  The CTA's bounded waits then run out
+ * (after about 2 s): DR_ERRF_TIMEOUT is ORed into *err_flag, it waits for its
+ * copies in flight, frees its tensor memory and exits.  Its outputs are left
+ * unwritten, or NaN where key ranges are joined; every other output is written
+ * as by dr_prompt_attn.  Nothing faults or hangs, and later calls on the same
+ * context work normally.
+ *   T > B (DR_ERR_UNSUPPORTED otherwise: no tile kernel), 0 <= stall_head < Hkv
+ *   (DR_ERR_INVALID_ARG otherwise); the rest as dr_prompt_attn.
+ */
+dr_status dr_prompt_attn_stall_test(const void *q, int64_t q_stride, const dr_kv_cache *cache, const int32_t *row_start,
+                                    const int32_t *kv_len, const dr_score_opts *opts, int T, int B, int Hq, int Hkv,
+                                    int D, int max_len_hint, float scale, void *out, dr_dtype out_dtype, void *ws,
+                                    size_t ws_bytes, int32_t *err_flag, int stall_head, void *stream);
+
 /* Host-only: workspace bytes dr_prompt_attn wants for such a call on a GPU with num_sms SMs (0: none needed). */
 size_t dr_prompt_attn_workspace(int T, int B, int Hq, int Hkv, int max_len, int num_sms);
 
@@ -472,6 +491,19 @@ dr_status dr_shared_prefix_attn(const void *q, int64_t q_stride, const dr_kv_cac
                                 int Hq, int Hkv, int D, int max_prefix_hint, int max_seq_len_hint, float scale,
                                 void *out, dr_dtype out_dtype, void *ws, size_t ws_bytes, int32_t *err_flag,
                                 void *stream);
+
+/*
+ * dr_shared_prefix_attn_stall_test -- TEST HOOK, as dr_prompt_attn_stall_test:
+ * the CTA of the prefix's first key range and the first 128 (row, query head)
+ * pairs of key/value head stall_head never loads its first keys.  Those
+ * outputs are NaN.
+ */
+dr_status dr_shared_prefix_attn_stall_test(const void *q, int64_t q_stride, const dr_kv_cache *prefix,
+                                           const int32_t *prefix_len, const dr_kv_cache *cache, const int32_t *seq_len,
+                                           const dr_score_opts *opts, int B, int Hq, int Hkv, int D,
+                                           int max_prefix_hint, int max_seq_len_hint, float scale, void *out,
+                                           dr_dtype out_dtype, void *ws, size_t ws_bytes, int32_t *err_flag,
+                                           int stall_head, void *stream);
 
 /* Host-only: workspace bytes of dr_shared_prefix_attn for prefixes of up to max_prefix keys on num_sms SMs. */
 size_t dr_shared_prefix_attn_workspace(int B, int Hq, int Hkv, int max_prefix, int num_sms);
