@@ -8,9 +8,17 @@ namespace dr {
 // The row of token t, by the whole warp (each lane gets it), with the row's token range [s0, s1); -1 when t is in no
 // row.  row_start is expected to rise from 0 to at most T; whatever it holds, the result is a row whose range, cut to
 // [0, T), holds t, or -1.  The first guess is the row of an even batch, which is exact for one token per row; then a
-// 32-way search (two dependent loads for up to 1024 rows).
+// 32-way search (two dependent loads for up to 1024 rows).  With err, the T warps look over all rows between them, one per
+// lane (those loads are under way while the row is found).
 __device__ __forceinline__ int find_row(const int32_t *row_start, int B, int T, int t, int lane, int &s0, int &s1,
                                         int32_t *err) {
+    long long x = 32LL * t + lane;   // the first row that this lane looks over
+    const bool looks = err && x < B;
+    int from = 0, to = 0;
+    if (looks) {
+        from = __ldg(row_start + x);
+        to = __ldg(row_start + x + 1);
+    }
     int b = (int)((long long)t * B / T);
     s0 = __ldg(row_start + b);
     s1 = __ldg(row_start + b + 1);
@@ -29,8 +37,15 @@ __device__ __forceinline__ int find_row(const int32_t *row_start, int B, int T, 
         s0 = __ldg(row_start + b);
         s1 = __ldg(row_start + b + 1);
     }
-    if (t == 0 && lane == 0 && (__ldg(row_start) != 0 || (unsigned)__ldg(row_start + B) > (unsigned)T))
-        flag_error(err, DR_ERRF_ROW_START);
+    if (looks) {
+        while (true) {
+            if (from < 0 || to < from || to > T || (x == 0 && from != 0)) flag_error(err, DR_ERRF_ROW_START);
+            x += 32LL * T;
+            if (x >= B) break;
+            from = __ldg(row_start + x);
+            to = __ldg(row_start + x + 1);
+        }
+    }
     if (!(s0 >= 0 && s0 <= t && t < s1)) return -1;
     s1 = min(s1, T);
     return b;

@@ -376,7 +376,8 @@ dr_status dr_rope_table(float *table, int max_pos, int rot_dim, double base, voi
  *   k, v     : [T][Hkv][D] bf16 likewise, k_stride and v_stride
  *   q_out    : rotated queries, [T][Hq][D] bf16 likewise; null exactly when q is; may be q itself with the same
  *              stride, else it overlaps no input
- *   row_start: [B+1] int32 (device), rising from 0 to at most T (DR_ERRF_ROW_START otherwise); rows may be empty
+ *   row_start: [B+1] int32 (device), rising from 0 to at most T (DR_ERRF_ROW_START otherwise: a token then goes by
+ *              one of the rows that hold it, or is left out); rows may be empty
  *   start_pos: [B] int32 (device), cache slot of each row's first new token.  DR_ERRF_POS and no key or value is
  *              written where a slot is outside [0, capacity) or its block outside the pool
  *   pos_offset : nullable [B] int32 (device), added to the slot for the rotation (keys before the row's own
