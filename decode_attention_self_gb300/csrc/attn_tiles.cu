@@ -155,7 +155,7 @@ __device__ __forceinline__ void visible(const PromptParams &p, int t, int i, int
         lo = p.first_key ? max(0, __ldg(p.first_key + t)) : 0;
         hi = p.causal ? min(L, max(pos + 1, prefix)) : L;
     } else {   // shared prefix: every query stands behind it
-        pos = L + (p.own_len ? max(0, __ldg(p.own_len + t)) : 0) - 1;
+        pos = L + (p.own_len ? min(max(0, __ldg(p.own_len + t)), p.own_cap) : 0) - 1;
         lo = 0;
         hi = L;
     }

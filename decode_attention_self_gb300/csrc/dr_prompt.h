@@ -70,6 +70,7 @@ struct PromptParams {
     int32_t stall;
     // tile kernel: queries of a shared prefix stand own_len[t] keys past its end (null: at their row's last keys)
     const int32_t *own_len;
+    int32_t own_cap;                    // own_len is clamped to it
     // softmax states of key ranges attended before: [nparts][rows = T*Hq] (m, l) and [nparts][rows][64]; null: none
     float2 *part_ml;
     float *part_acc;

@@ -206,6 +206,7 @@ dr_status shared_call(const void *q, int64_t q_stride, const dr_kv_cache *prefix
     fill_scores(p, prefix, scale, opts);
     p.kv_len = prefix_len;
     p.own_len = seq_len;
+    p.own_cap = cap;
     p.stall = stall_head + 1;
     p.T = B;
     p.B = B;
