@@ -20,8 +20,10 @@
 //
 // e4m3 caches: the codes convert exactly to f16, and the products run in f16 with fp32 sums: q is brought to
 // [0.5, 1) times a power of two per head, which f16 holds exactly down to 2^-15 of the largest element (below that
-// the error is under 2^-25 of it), and the weights keep 11 bits.  bf16 caches: weights are rounded to bf16 (8 bits)
-// for the product with V, their sum is taken in fp32.
+// the error is under 2^-25 of it), and the weights keep 11 bits.  bf16 caches: a weight goes to the product with V as its
+// upper 8 bits and the rest rounded to bf16, 16 bits in all; their sum is taken in fp32.  With groups of up to 4 heads the
+// rests go through columns that are idle otherwise, at no instruction more (189.4 us with 8-bit weights, 189.7 so; 196 as
+// products of their own); larger groups take four more instructions per 16 keys and 8 heads (groups of 16: 55 -> 57 us).
 #include <cooperative_groups.h>
 
 #include "dr_prompt.h"
@@ -137,8 +139,9 @@ struct Shared {
     float sent[kMaxSplits + kBlocks][kThreads];   // [block / splits][rank]
 };
 
-// kN: groups of 8 query heads of one kv head; kPlain: no cap, no bias.
-template <typename Tile, bool kPaged, int kN, bool kPlain>
+// kN: groups of 8 query heads of one kv head; kPlain: no cap, no bias; kTwice (bf16, up to 4 heads): columns 4 .. 7 repeat
+// the heads of columns 0 .. 3 and carry the rests of their weights.
+template <typename Tile, bool kPaged, int kN, bool kPlain, bool kTwice>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm<Tile, kN>())
     attn_tokens_kernel(const PromptParams p, int splits) {
     constexpr int kHeads = 8 * kN;
@@ -282,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<Tile, kN>())
         float slope[kN][2];
 #pragma unroll
         for (int a = 0; a < kN; ++a) {
-            const int h = a * 8 + r;
+            const int h = kTwice ? r & 3 : a * 8 + r;
             uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
             if (h < nheads) {
                 const uint16_t *src = p.q + (size_t)t * p.q_stride + (size_t)(h0 + h) * kD;
@@ -314,9 +317,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<Tile, kN>())
             qmul[a][0] = qfac[a][0] * p.sscale;
             qmul[a][1] = qfac[a][1] * p.sscale;
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-                slope[a][j] = p.slopes && a * 8 + 2 * c + j < nheads
-                                  ? __ldcg(p.slopes + h0 + a * 8 + 2 * c + j) * 1.4426950408889634f : 0.f;
+            for (int j = 0; j < 2; ++j) {
+                const int h = kTwice ? (2 * c + j) & 3 : a * 8 + 2 * c + j;
+                slope[a][j] = p.slopes && h < nheads ? __ldcg(p.slopes + h0 + h) * 1.4426950408889634f : 0.f;
+            }
         }
 
         float m[kN][2], mref[kN][2], l[kN][2], acc[kN][4][4];
@@ -416,7 +420,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<Tile, kN>())
                         }
                     }
             }
-            uint32_t pf[kT][kN][2];
+            // bf16: a weight is its upper 8 bits and the rest rounded to bf16, 16 bits in all
+            uint32_t pf[kT][kN][2], pr[kT][kN][2];
+            const float own = kTwice && c >= 2 ? 1.f : 0.f, upper = kTwice && c >= 2 ? -1.f : 1.f;
 #pragma unroll
             for (int y = 0; y < kT; ++y)
 #pragma unroll
@@ -427,9 +433,23 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<Tile, kN>())
                     l[a][0] += w[0] + w[2];
                     l[a][1] += w[1] + w[3];
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        pf[y][a][j] = transpose8x8(Tile::kF16 ? pack_f16(w[2 * j], w[2 * j + 1])
-                                                              : pack_bf16(w[2 * j], w[2 * j + 1]));
+                    for (int j = 0; j < 2; ++j) {
+                        if constexpr (Tile::kF16) {
+                            pf[y][a][j] = transpose8x8(pack_f16(w[2 * j], w[2 * j + 1]));
+                        } else {
+                            const float2 v = make_float2(w[2 * j], w[2 * j + 1]);
+                            const float2 up = make_float2(__uint_as_float(__float_as_uint(v.x) & 0xFFFF0000u),
+                                                          __uint_as_float(__float_as_uint(v.y) & 0xFFFF0000u));
+                            if constexpr (kTwice) {   // exact: upper bits, or weight minus upper bits
+                                const float2 x = __ffma2_rn(up, make_float2(upper, upper),
+                                                            __fmul2_rn(v, make_float2(own, own)));
+                                pf[y][a][j] = transpose8x8(pack_bf16(x.x, x.y));
+                            } else {
+                                pf[y][a][j] = transpose8x8(pack_bf16(up.x, up.y));
+                                pr[y][a][j] = transpose8x8(pack_bf16(v.x - up.x, v.y - up.y));
+                            }
+                        }
+                    }
                 }
 #pragma unroll
             for (int y = 0; y < kT; ++y) {
@@ -443,8 +463,12 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<Tile, kN>())
                         __byte_perm(vw[2][z], vw[3][z], 0x5410), __byte_perm(vw[2][z], vw[3][z], 0x7632)};
 #pragma unroll
                     for (int a = 0; a < kN; ++a) {
-                        if (Tile::kF16) mma_f16(acc[a][z], af, pf[y][a][0], pf[y][a][1]);
-                        else mma_bf16(acc[a][z], af, pf[y][a][0], pf[y][a][1]);
+                        if constexpr (Tile::kF16) {
+                            mma_f16(acc[a][z], af, pf[y][a][0], pf[y][a][1]);
+                        } else {
+                            if constexpr (!kTwice) mma_bf16(acc[a][z], af, pr[y][a][0], pr[y][a][1]);
+                            mma_bf16(acc[a][z], af, pf[y][a][0], pf[y][a][1]);
+                        }
                     }
                 }
             }
@@ -461,8 +485,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<Tile, kN>())
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) l[a][j] += __shfl_xor_sync(0xFFFFFFFFu, l[a][j], off);
                 const int h = a * 8 + 2 * c + j;
-                if (h >= nheads) continue;
-                if (r == 0) {
+                const bool rests = kTwice && h >= 4;   // sums of head h - 4, added where they are read
+                if (h - (rests ? 4 : 0) >= nheads) continue;
+                if (r == 0 && !rests) {
                     s_m[warp][h] = state_max(m[a][j], l[a][j]);
                     s_l[warp][h] = l[a][j];
                 }
@@ -543,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<Tile, kN>())
                 for (int w = 0; w < kWarps; ++w) {
                     const float wt = exp2f(s_m[w][h] - M);
                     ls += wt * s_l[w][h];
-                    o += wt * s_acc[w][h][d];
+                    o += wt * (kTwice ? s_acc[w][h][d] + s_acc[w][h + 4][d] : s_acc[w][h][d]);
                 }
                 o *= p.out_scale;
                 if (p.part_ml)
@@ -611,9 +636,9 @@ int plan_token_splits(long long items, int Hkv, int g, int max_len, bool fp8, in
 
 namespace {
 
-template <typename Tile, bool kPaged, int kN, bool kPlain>
+template <typename Tile, bool kPaged, int kN, bool kPlain, bool kTwice = false>
 cudaError_t launch_variant(const PromptParams &p, int splits, cudaStream_t stream) {
-    auto kern = attn_tokens_kernel<Tile, kPaged, kN, kPlain>;
+    auto kern = attn_tokens_kernel<Tile, kPaged, kN, kPlain, kTwice>;
     // The loads in flight live in L1 (128 KB per SM at four CTAs): ask for no more shared memory than the CTAs need.
     // Left to itself an SM keeps the split of the kernel before, and behind the tile kernel, which takes all of it,
     // 128 rows of 64..2048 own keys took 125 us instead of 97.
@@ -635,6 +660,9 @@ cudaError_t launch_layout(const PromptParams &p, int splits, cudaStream_t stream
     if (p.g > 8)
         return plain ? launch_variant<Tile, kPaged, 2, true>(p, splits, stream)
                      : launch_variant<Tile, kPaged, 2, false>(p, splits, stream);
+    if (!Tile::kF16 && p.g <= 4)
+        return plain ? launch_variant<Tile, kPaged, 1, true, !Tile::kF16>(p, splits, stream)
+                     : launch_variant<Tile, kPaged, 1, false, !Tile::kF16>(p, splits, stream);
     return plain ? launch_variant<Tile, kPaged, 1, true>(p, splits, stream)
                  : launch_variant<Tile, kPaged, 1, false>(p, splits, stream);
 }

@@ -413,9 +413,11 @@ typedef struct dr_score_opts {
  *   out[t][h] = sum_j softmax(s)_j V_j over the keys j in [lo, hi),
  *   lo = max(0, first_key[t]), hi = min(kv_len[b], max(p + 1, prefix_len[b])) when causal, else kv_len[b].
  * A query that sees no key outputs zeros.  Scores, softmax statistics and sums
- * are fp32; the weights are rounded for the product with V to bf16 (e4m3
- * caches: to f16, which also holds the codes and, scaled by a power of two per
- * head, q).  Keys at or past kv_len and keys that no query of the call may see
+ * are fp32; the weights are rounded for the product with V: over a bf16 cache to
+ * 16 bits in rows of one token (and calls with T <= B) and to bf16 in longer
+ * rows, where they are an operand of the matrix unit, which takes bf16 beside
+ * bf16 values; over an e4m3 cache to f16, which also holds the codes and, scaled
+ * by a power of two per head, q.  Keys at or past kv_len and keys that no query of the call may see
  * do not reach the result whatever they hold.
  *
  *   q        : [T][Hq][D] bf16 (device, 16-byte aligned), tokens q_stride elements apart (multiple of 8, >= Hq*D)
@@ -470,7 +472,8 @@ size_t dr_prompt_attn_workspace(int T, int B, int Hq, int Hkv, int max_len, int 
  *   out[b][h] = sum_j softmax(s)_j V_j over both
  * The prefix is read once per 128 query rows (all rows' heads on its key/value
  * head together), not once per row; the softmax states of the two parts are
- * merged in fp32.  Rounding as in dr_prompt_attn.  A row with no key at all
+ * merged in fp32.  Rounding as in dr_prompt_attn (own keys as rows of one token,
+ * the prefix as longer ones).  A row with no key at all
  * outputs zeros.  For several prefixes, one call per group of rows.
  *
  *   q        : [B][Hq][D] bf16 (device, 16-byte aligned), rows q_stride elements apart (multiple of 8, >= Hq*D)
