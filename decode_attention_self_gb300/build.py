@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import os
+import re
 import subprocess
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -21,6 +22,20 @@ SOURCES = ["dr_api.cu", "attention.cu", "kv_append.cu", "sampler.cu", "heads.cu"
            "rope_append.cu", "attn_tokens.cu", "attn_tiles.cu", "dr_prompt_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
+
+# Kernels that share a launch's registers out between their warps, and the registers per thread that they count on: a launch
+# with another number is refused at run time, so the build looks at what ptxas gave them.
+LAUNCH_REGISTERS = {"attn_tiles.cu": ("attn_tiles_kernel", 128)}
+
+
+def check_registers(src: str, ptxas: str) -> None:
+    """Raise unless ptxas's report (-v) gives every kernel of LAUNCH_REGISTERS[src] its registers."""
+    kernel, want = LAUNCH_REGISTERS[src]
+    used = [(name, int(n)) for name, n in re.findall(r"entry function '(\w+)'.*?Used (\d+) registers", ptxas, flags=re.S)
+            if kernel in name]
+    bad = [f"{name}: {n}" for name, n in used if n != want]
+    if bad or not used:
+        raise RuntimeError(f"{src}: {kernel} needs {want} registers per thread, ptxas reports " + (", ".join(bad) or "none"))
 
 
 def _nvcc() -> str:
@@ -44,12 +59,15 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
 
     def compile_one(src: str) -> str:
         obj = os.path.join(BUILD_DIR, src.replace(".cu", ".o"))
-        cmd = [nvcc] + flags + ["-c", os.path.join(CSRC, src), "-o", obj]
+        report = ["-Xptxas", "-v"] if src in LAUNCH_REGISTERS and "-v" not in flags else []
+        cmd = [nvcc] + flags + report + ["-c", os.path.join(CSRC, src), "-o", obj]
         if verbose:
             print(" ".join(cmd), flush=True)
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
+        if src in LAUNCH_REGISTERS:
+            check_registers(src, r.stdout + r.stderr)
         if verbose and (r.stdout or r.stderr):
             print(r.stdout + r.stderr, flush=True)
         return obj
