@@ -17,17 +17,18 @@
 // under them.  Biases on keys behind the query, and caps with a bias, would make that code too long for the instruction
 // cache: such tiles go through tensor memory a quarter at a time in rolled loops.
 // The running maximum moves only when a score passes it by 2^8 (log2 units): O is rescaled rarely.  Sums and states are
-// fp32; weights are rounded once, to bf16 (e4m3: f16), for the product with V.
+// fp32; weights are rounded once, to bf16 (e4m3: f16), for the product with V: the instruction takes both operands in one
+// type, and the rests of bf16 weights would need 64 more columns of tensor memory (two CTAs fill it) and P V a second time.
 //
 // What bounds it.  One token of one head costs 256 flops and one exponential per key it sees.  16384 causal tokens of 16
-// heads, bf16: 519 us, 1059 TFLOP/s; the products alone would take 288 us at the library GEMM's rate and the exponentials
+// heads, bf16: 518 us, 1060 TFLOP/s; the products alone would take 288 us at the library GEMM's rate and the exponentials
 // 230 us of the special-function units.  P V runs at 45 cycles per instruction where its shape allows 32 (P comes from
 // tensor memory), and the maximum, the packing and the moves to and from tensor memory take issue slots beside the
 // exponentials.  Two threads per row (half the registers), skipping hidden columns inside the straight way, and P V one
-// tile later were each built and were slower.  e4m3: 602 us; 639 in CTAs of two tiles, which convert the keys once for
-// both but are alone on their SM.  Short rows are bound by a CTA's start and end: 1304 CTAs without any key take 23 us (9
-// rows of 364..1812 tokens, 4 heads in groups of 4), the same rows causal 61, biased 79, capped 110 (three
-// special-function results per score), cut into documents 50.
+// tile later were each built and were slower.  e4m3: 600 us; CTAs of two tiles, which convert the keys once for both but
+// are alone on their SM, took 6% longer.  24 to 52 bytes per thread are spilled.  Short rows are bound by a CTA's start
+// and end: 1304 CTAs without any key take 23 us (9 rows of 364..1812 tokens, 4 kv heads in groups of 4), the same rows
+// causal 61, causal with a bias 77, with a cap 106, cut into about three documents each 51, documents with a bias 62.
 //
 // Every wait is bounded (about 2 s): DR_ERRF_TIMEOUT, the CTA writes no output (a state that others join becomes NaN), waits
 // for its own copies and products in flight and frees its tensor memory.
@@ -81,7 +82,7 @@ struct Control {   // at Config::kEnd of the dynamic shared memory
     int lo_max, hi_min;                  // keys that every row sees
 };
 
-// n / d for n < 2^31 by a product and a shift (a division takes some 30 instructions, and the start of a CTA has five).
+// n / d for n < 2^31 by a product and a shift, the method of Granlund and Montgomery (1994) (a division takes some 30 instructions, and the start of a CTA has five).
 struct Divisor {
     uint32_t d, mul, shift;
     void set(uint32_t by) {
@@ -538,7 +539,7 @@ __global__ void __launch_bounds__(Config<kFp8>::kThreads, Config<kFp8>::kCtasPer
                         *reinterpret_cast<uint4 *>(dst + swz(r, 2 * c + 1)) = d;
                     };
                     // Eight reads in flight and nothing else in the loop: what bounds a helper is the latency of its own
-                    // instructions (8192-token prompt: two reads in flight 202 us, four 189, eight 172, none converted 163)
+                    // instructions (8192-token prompt: two reads in flight take 17% longer, four 10%; no conversions 5% less)
                     if (!edge && !mixed) {
 #pragma unroll
                         for (int e0 = 0; e0 < kChunks; e0 += kBatch) {
@@ -716,8 +717,8 @@ __global__ void __launch_bounds__(Config<kFp8>::kThreads, Config<kFp8>::kCtasPer
                     if (!ok) break;
                     s_there = false;
                 } else if (kMode == kPlain || (kMode == kBiased && linear) || (kMode == kCapped && !biased)) {
-                    // The row in registers at once, S given back before the exponentials.  Masked tiles by the rolled way
-                    // below: documents 60 us against 50; capped ones: 118 against 110.
+                    // The row in registers at once, S given back before the exponentials.  By the rolled way below, documents
+                    // without a bias took a fifth longer, and capped rows 7%.
                     float s[kKeys];
                     float top[8];
                     const float base = slope * (float)(key0 - pos);
@@ -760,8 +761,8 @@ __global__ void __launch_bounds__(Config<kFp8>::kThreads, Config<kFp8>::kCtasPer
                     ld32(ts + 64, s + 64);
                     ld32(ts + 96, s + 96);
                     const bool whole = inside && bits == 0xFF;
-                    // Long prompts gain by an unmasked way of its own (519 us against 544); with a bias the code would grow
-                    // too long for the instruction cache (documents 57 us against 54)
+                    // Long prompts gain 5% by an unmasked way of its own; with a bias the code would grow too long for the
+                    // instruction cache (documents with a bias took 5% longer)
                     if (kMode == kPlain && whole) {
                         top_first();
                         wait_ld();
@@ -804,7 +805,7 @@ __global__ void __launch_bounds__(Config<kFp8>::kThreads, Config<kFp8>::kCtasPer
                 } else {
                     // A quarter at a time in rolled loops: capped, biased and masked scores go back to tensor memory and
                     // are read again for the exponentials.  With straight-line code for every combination a quarter of the
-                    // requests to the instruction cache missed (documents with a bias: 72 us against 61).
+                    // requests to the instruction cache missed, and documents with a bias took 18% longer.
                     unsigned hidden = 0;   // quarters that no row of the warp sees
                     float mx = -INFINITY;
 #pragma unroll 1
@@ -1104,10 +1105,13 @@ cudaError_t launch_attn_tiles(const PromptParams &p, bool paged, bool fp8, int s
 //   + s x states, written and read at 4 TB/s, + 2.5 us for the launch that joins them (prompts, s > 1),
 // run = key tiles per CTA, step = 0.83 us for a CTA that has an SM to itself, 1.25 for two on an SM (e4m3 0.88, 1.35).
 // The rows' own keys, streamed beside a shared prefix (own_us of them), hide about a quarter of their time of it; the
-// states are read by the same CTAs and are dearer there, up to three times.  Measured, bf16: a chunk of 3 x 300..700 tokens
-// on up to 20000 keys, 16 heads: 136 us unsplit, 105 by 2, 108 by 4, 123 by 8, 170 by 16; 200 tokens of 4 heads in groups
-// of 4 on 30000 keys: 195 us, 49 by 5, 57 by 6, 43 by 10, 56 by 12; a prefix of 500 keys for 8 rows of 16 heads: 10.4 us,
-// 7.8 by 4; of 4096 keys for 128 rows with 64..2048 own: 107 us, 97 by 2 to 4, 103 by 10, 112 by 32.
+// states are read by the same CTAs and are dearer there, up to three times.  Measured, bf16: 300, 500 and 700 tokens on
+// 9000, 14000 and 18000 keys, 16 heads: 162 us unsplit, 136 by 2, 134 by 3 or 4, 151 by 8 (the plan: 135); 200 tokens of 4
+// heads in groups of 4 on 30000 keys: 197 us, 49 by 5, 57 by 6, 43 by 10 (the plan's), 59 by 12; a prefix of 500 keys for 8
+// rows of 16 heads: 9.8 us, 7.8 by 4 (the plan's); of 4096 keys for 128 rows with 64..2048 own: 107 us, 98 by 2 (the plan's),
+// 97 by 3, 103 by 10, 113 by 32.  The plan takes ceil(T g / 128) tiles; rows that end within one make more, and many short
+// rows over long pasts are split too far: 32 rows of 4 tokens, 4 heads, 16384 keys 150 us, 88 by 2; 64 rows of 20 tokens, 2
+// heads, 8192 keys 77 us, 51 by 2.
 int plan_tile_splits(int T, int g, int Hkv, int max_len, bool fp8, int sms, bool joined, double own_us) {
     const double units = (double)(((long long)T * g + kRows - 1) / kRows) * Hkv;
     const int tiles = max_len / kKeys + 1;

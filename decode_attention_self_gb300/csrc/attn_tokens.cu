@@ -14,7 +14,7 @@
 // loads): lane (r, c) = (lane / 4, lane % 4) holds dims 16c .. 16c + 15 of keys r and r + 8, and dims 8r .. 8r + 7 of
 // keys 2c, 2c + 1, 2c + 8, 2c + 9.  P^T comes from S^T by two 8x8 register transposes.
 // Bound by memory: 4 KB of K and V per 16 keys (bf16); even one head in eight columns leaves the matrix instructions
-// mostly idle.  Measured: 128 rows of 512..4096 keys, 16 heads, 178 us (6.7 TB/s); e4m3 115 us (5.2 TB/s, where the
+// mostly idle.  Measured: 128 rows of 512..4096 keys, 16 heads, 190 us (6.7 TB/s); e4m3 123 us (5.2 TB/s, where the
 // conversions count).  A ring of bulk copies in shared memory (4 tiles in flight per warp) was slower at every size:
 // what the loads wait for is the row's chain length - block id - keys, and fewer CTAs per SM hide less of it.
 //
@@ -22,8 +22,9 @@
 // [0.5, 1) times a power of two per head, which f16 holds exactly down to 2^-15 of the largest element (below that
 // the error is under 2^-25 of it), and the weights keep 11 bits.  bf16 caches: a weight goes to the product with V as its
 // upper 8 bits and the rest rounded to bf16, 16 bits in all; their sum is taken in fp32.  With groups of up to 4 heads the
-// rests go through columns that are idle otherwise, at no instruction more (189.4 us with 8-bit weights, 189.7 so; 196 as
-// products of their own); larger groups take four more instructions per 16 keys and 8 heads (groups of 16: 55 -> 57 us).
+// rests go through columns that are idle otherwise, at no matrix instruction more (the rows above: 189.4 us with 8-bit
+// weights, 189.7 so, 196 as products of their own); larger groups take four more per 16 keys and 8 heads (groups of 16, 2 kv
+// heads: 55 -> 57 us).
 #include <cooperative_groups.h>
 
 #include "dr_prompt.h"
@@ -117,8 +118,8 @@ struct Fp8Tile {
 };
 
 // 16-key tiles of one pass of a warp, and CTAs per SM.  With groups of up to 8 heads two tiles per pass give the chain
-// scores - maximum - weights - sums two independent halves: 128 rows of 512..4096 bf16 keys, 16 heads, 186 -> 178 us
-// against one tile at 5 CTAs per SM (rows of 1..256 keys lose: 17.3 -> 20.3 us); three CTAs or five (spills) are slower.
+// scores - maximum - weights - sums two independent halves: 128 rows of 512..4096 bf16 keys, 16 heads, 4% less
+// against one tile at 5 CTAs per SM (rows of 1..256 keys lose 17%); three CTAs or five (spills) are slower.
 // Groups of 16 heads take one tile: two would spill.
 template <typename Tile, int kN>
 __host__ __device__ constexpr int tiles_per_pass() { return kN == 2 ? 1 : 2; }
@@ -618,8 +619,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<Tile, kN>())
 }  // namespace
 
 // CTAs (one cluster) that share a token's keys: at most 512 KiB of K and V each, and as many as fill the GPU in one wave
-// (a few CTAs more than fit cost a whole second wave: 8 rows of 16 heads, 64..512 keys, 9.1 us with 5 CTAs per row and
-// head, 5.5 with 4), with at least 64 keys each.
+// (a few CTAs more than fit cost a whole second wave: 8 rows of 16 heads, 64..512 keys, took two thirds longer with 5
+// CTAs per row and head than with 4), with at least 64 keys each.
 int plan_token_splits(long long items, int Hkv, int g, int max_len, bool fp8, int sms) {
     const int kn = g > 8 ? 2 : 1;
     const long long rows = items * Hkv * ((g + 8 * kn - 1) / (8 * kn));
@@ -641,7 +642,7 @@ cudaError_t launch_variant(const PromptParams &p, int splits, cudaStream_t strea
     auto kern = attn_tokens_kernel<Tile, kPaged, kN, kPlain, kTwice>;
     // The loads in flight live in L1 (128 KB per SM at four CTAs): ask for no more shared memory than the CTAs need.
     // Left to itself an SM keeps the split of the kernel before, and behind the tile kernel, which takes all of it,
-    // 128 rows of 64..2048 own keys took 125 us instead of 97.
+    // 128 rows of 64..2048 own keys took a quarter longer.
     static std::atomic<uint64_t> ready{0};
     const cudaError_t e = once_per_device(ready, [&] {
         constexpr size_t all = ctas_per_sm<Tile, kN>() * (sizeof(Shared<kN>) + 1024);

@@ -9,9 +9,9 @@
 // pair of 16-byte chunks of head s, s + 8, ... of q, k and v in turn, chosen so that both elements of every rotated
 // pair are in the lane, and reads its 16 table values once for all heads.  The first heads are loaded before the token's
 // row and position are known, and 24 warps fit an SM (80 registers) in CTAs of four, which leave a shorter tail than CTAs
-// of eight: 65536 tokens, 16 + 2 x 16 heads, 124 us, 6.64 TB/s (126 in CTAs of eight; 150 with the loads behind the row
-// search and 16 warps per SM; 161 with a run of tokens per warp, whose loads wait for the stores before).  22000 ragged
-// tokens into an e4m3 cache take 25 us, where scales that are powers of two save the division (28 us with it): each warp's
+// of eight: 65536 tokens, 16 + 2 x 16 heads, 125 us, 6.59 TB/s (CTAs of eight 1% more; the loads behind the row search and 16
+// warps per SM a fifth more; a run of tokens per warp, whose loads wait for the stores before, 30%).  22000 ragged tokens
+// into an e4m3 cache take 26 us, where scales that are powers of two save the division (10% more with it): each warp's
 // chain row - position - table is as long as its transfers.
 #include "dr_device.cuh"
 #include "dr_prompt.h"

@@ -88,7 +88,8 @@ typedef enum dr_kv_dtype {
 #define DR_ERRF_BLOCK_ID 2 /* a needed block-table entry outside [0, num_blocks); its keys were skipped */
 #define DR_ERRF_POS 4      /* an append position outside [0, capacity) or on an unmapped block; row skipped */
 #define DR_ERRF_TOKEN 8    /* a token outside [0, V) in dr_embed_tokens; that codebook's row was skipped */
-#define DR_ERRF_TIMEOUT 16 /* a bounded on-chip wait gave up (never expected); that CTA's results were not written, or are NaN where they are joined with others' */
+#define DR_ERRF_TIMEOUT 16 /* a bounded on-chip wait gave up (never expected); that CTA's results were not written,
+                              or are NaN where they are joined with others' */
 #define DR_ERRF_ROW_START 32 /* row_start does not rise from 0 to at most T; rows were cut to [0, T) */
 
 /* Sampler flags. */
@@ -417,8 +418,11 @@ typedef struct dr_score_opts {
  * 16 bits in rows of one token (and calls with T <= B) and to bf16 in longer
  * rows, where they are an operand of the matrix unit, which takes bf16 beside
  * bf16 values; over an e4m3 cache to f16, which also holds the codes and, scaled
- * by a power of two per head, q.  Keys at or past kv_len and keys that no query of the call may see
- * do not reach the result whatever they hold.
+ * by a power of two per head, q.  Keys at or past kv_len and keys that no query
+ * of the call may see do not reach the result whatever they hold; a NaN in a
+ * query or in a key that it sees makes its outputs NaN.  With T <= B a row's
+ * tokens are taken one after another (each reads the row's keys again): prompts
+ * in a batch of mostly empty rows are faster in a call over their rows alone.
  *
  *   q        : [T][Hq][D] bf16 (device, 16-byte aligned), tokens q_stride elements apart (multiple of 8, >= Hq*D)
  *   cache    : see dr_kv_cache, with Hkv heads; B rows of at most 2^31 - 4096 keys; k and v 32-byte aligned
@@ -473,8 +477,10 @@ size_t dr_prompt_attn_workspace(int T, int B, int Hq, int Hkv, int max_len, int 
  * The prefix is read once per 128 query rows (all rows' heads on its key/value
  * head together), not once per row; the softmax states of the two parts are
  * merged in fp32.  Rounding as in dr_prompt_attn (own keys as rows of one token,
- * the prefix as longer ones).  A row with no key at all
- * outputs zeros.  For several prefixes, one call per group of rows.
+ * the prefix as longer ones).  A row with no key at all outputs zeros.  For
+ * several prefixes, one call per group of rows.  A row's own prompt behind the prefix is a dr_prompt_attn call over a block table that
+ * begins with the prefix's blocks (one pool, a prefix of whole blocks), with the
+ * prefix counted in kv_len.
  *
  *   q        : [B][Hq][D] bf16 (device, 16-byte aligned), rows q_stride elements apart (multiple of 8, >= Hq*D)
  *   prefix   : cache of one row (row 0) with Hkv heads, k and v 32-byte aligned (cache's too); paged: its blocks may
