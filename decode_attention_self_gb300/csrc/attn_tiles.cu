@@ -47,7 +47,6 @@ using namespace tc;
 constexpr int kD = kHeadDim;
 constexpr int kRows = 128;   // query rows per tile (MMA M) and keys per tile (MMA N of S, K of O)
 constexpr int kKeys = 128;
-constexpr float kSlack = 8.0f;
 constexpr int kBitsRing = 8;
 constexpr int kMaxStages = 3;
 constexpr uint32_t kTileBytes = kKeys * kD * 2;   // a K, V or Q tile of 16-bit elements: 16 KB
@@ -686,7 +685,8 @@ __global__ void __launch_bounds__(Config<kFp8>::kThreads, Config<kFp8>::kCtasPer
                 const auto raise = [&](float mx) {   // also for the first visible key (m = -inf)
                     if (mx > m + kSlack) {
                         corr = fast_exp2(m - mx);
-                        m = mref = mx;
+                        m = mx;
+                        mref = mx - kLift<kFp8>;
                         l *= corr;
                     }
                 };
@@ -938,7 +938,7 @@ __global__ void __launch_bounds__(Config<kFp8>::kThreads, Config<kFp8>::kCtasPer
                 }
                 if (p.part_ml) {
                     const size_t at = (size_t)split * ((size_t)p.T * p.Hq) + orow;
-                    p.part_ml[at] = make_float2(state_max(m, l), l);
+                    p.part_ml[at] = make_float2(state_max(m - kLift<kFp8>, l), l);
                     float *dst = p.part_acc + at * kD;
 #pragma unroll
                     for (int c = 0; c < kD; c += 8) {

@@ -20,7 +20,7 @@
 //
 // e4m3 caches: the codes convert exactly to f16, and the products run in f16 with fp32 sums: q is brought to
 // [0.5, 1) times a power of two per head, which f16 holds exactly down to 2^-15 of the largest element (below that
-// the error is under 2^-25 of it), and the weights keep 11 bits.  bf16 caches: a weight goes to the product with V as its
+// the error is under 2^-25 of it), and the weights keep 11 bits down to 2^-21 of the row's largest (kLift).  bf16 caches: a weight goes to the product with V as its
 // upper 8 bits and the rest rounded to bf16, 16 bits in all; their sum is taken in fp32.  With groups of up to 4 heads the
 // rests go through columns that are idle otherwise, at no matrix instruction more (the rows above: 189.4 us with 8-bit
 // weights, 189.7 so, 196 as products of their own); larger groups take four more per 16 keys and 8 heads (groups of 16, 2 kv
@@ -126,7 +126,6 @@ __host__ __device__ constexpr int tiles_per_pass() { return kN == 2 ? 1 : 2; }
 template <typename Tile, int kN>
 __host__ __device__ constexpr int ctas_per_sm() { return kN == 2 ? 3 : Tile::kF16 ? 5 : 4; }
 constexpr int kMaxSplits = 8;   // CTAs per token and kv head: one portable cluster
-constexpr float kSlack = 8.0f;   // the reference of the weights moves when a score passes it by 2^8
 
 template <int kN>
 struct Shared {
@@ -412,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<Tile, kN>())
                         for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
                         const float corr = top == -INFINITY ? 1.f : fast_exp2(m[a][j] - top);
                         m[a][j] = top;
-                        mref[a][j] = top == -INFINITY ? 0.f : top;
+                        mref[a][j] = top == -INFINITY ? 0.f : top - kLift<Tile::kF16>;
                         l[a][j] *= corr;
 #pragma unroll
                         for (int x4 = 0; x4 < 4; ++x4) {
@@ -489,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<Tile, kN>())
                 const bool rests = kTwice && h >= 4;   // sums of head h - 4, added where they are read
                 if (h - (rests ? 4 : 0) >= nheads) continue;
                 if (r == 0 && !rests) {
-                    s_m[warp][h] = state_max(m[a][j], l[a][j]);
+                    s_m[warp][h] = state_max(m[a][j] - kLift<Tile::kF16>, l[a][j]);
                     s_l[warp][h] = l[a][j];
                 }
 #pragma unroll

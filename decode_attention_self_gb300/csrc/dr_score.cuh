@@ -53,6 +53,13 @@ struct ScoreCap {
     }
 };
 
+// The running maximum of a row moves when a score passes it by 2^8 (log2 units): sums are rescaled rarely.
+constexpr float kSlack = 8.0f;
+// f16 weights are held 2^7 times as large as their ratio to the running maximum: below 2^15, and with steps of 2^-32 of the
+// row's largest at least, where 2^-25 would lose thousands of small weights whose sum counts.  (bf16 holds any ratio.)
+template <bool kF16>
+constexpr float kLift = kF16 ? 7.0f : 0.0f;
+
 // The maximum to store with a softmax state.  m = -inf marks a state without keys, and the maxima drop NaN: a state whose
 // scores were all NaN (its sum l is NaN) gets a maximum that no merge takes for an empty one.
 __device__ __forceinline__ float state_max(float m, float l) { return m == -INFINITY && l != 0.f ? 0.f : m; }

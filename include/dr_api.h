@@ -417,8 +417,9 @@ typedef struct dr_score_opts {
  * are fp32; the weights are rounded for the product with V: over a bf16 cache to
  * 16 bits in rows of one token (and calls with T <= B) and to bf16 in longer
  * rows, where they are an operand of the matrix unit, which takes bf16 beside
- * bf16 values; over an e4m3 cache to f16, which also holds the codes and, scaled
- * by a power of two per head, q.  Keys at or past kv_len and keys that no query
+ * bf16 values; over an e4m3 cache to f16 (below 2^-21 of the row's largest weight
+ * to steps of 2^-31), which also holds the codes and, scaled by a power of two
+ * per head, q.  Keys at or past kv_len and keys that no query
  * of the call may see do not reach the result whatever they hold; a NaN in a
  * query or in a key that it sees makes its outputs NaN.  With T <= B a row's
  * tokens are taken one after another (each reads the row's keys again): prompts
