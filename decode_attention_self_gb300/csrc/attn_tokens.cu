@@ -18,13 +18,13 @@
 // conversions count).  A ring of bulk copies in shared memory (4 tiles in flight per warp) was slower at every size:
 // what the loads wait for is the row's chain length - block id - keys, and fewer CTAs per SM hide less of it.
 //
-// e4m3 caches: the codes convert exactly to f16, and the products run in f16 with fp32 sums: q is brought to
-// [0.5, 1) times a power of two per head, which f16 holds exactly down to 2^-15 of the largest element (below that
-// the error is under 2^-25 of it), and the weights keep 11 bits down to 2^-21 of the row's largest (kLift).  bf16 caches: a weight goes to the product with V as its
-// upper 8 bits and the rest rounded to bf16, 16 bits in all; their sum is taken in fp32.  With groups of up to 4 heads the
-// rests go through columns that are idle otherwise, at no matrix instruction more (the rows above: 189.4 us with 8-bit
-// weights, 189.7 so, 196 as products of their own); larger groups take four more per 16 keys and 8 heads (groups of 16, 2 kv
-// heads: 55 -> 57 us).
+// e4m3 caches: the codes convert exactly to f16, and the products run in f16 with fp32 sums: q is brought below 2^15 by
+// a power of two per head, which f16 holds exactly down to 2^-31 of the largest element (below that the error is under
+// 2^-39 of it), and the weights keep 11 bits down to 2^-21 of the row's largest (kLift).  bf16 caches: a weight goes to
+// the product with V as its upper 8 bits and the rest rounded to bf16, 16 bits in all; their sum is taken in fp32.  With
+// groups of up to 4 heads the rests go through columns that are idle otherwise, at no matrix instruction more (the rows
+// above: 189.4 us with 8-bit weights, 189.7 so, 196 as products of their own); larger groups take four more per 16 keys
+// and 8 heads (groups of 16, 2 kv heads: 55 -> 57 us).
 #include <cooperative_groups.h>
 
 #include "dr_prompt.h"

@@ -64,12 +64,12 @@ constexpr float kLift = kF16 ? 7.0f : 0.0f;
 // scores were all NaN (its sum l is NaN) gets a maximum that no merge takes for an empty one.
 __device__ __forceinline__ float state_max(float m, float l) { return m == -INFINITY && l != 0.f ? 0.f : m; }
 
-// The power of two that brings x into [0.5, 1); 1 for zero, infinite and NaN x.  Exponents are kept where both the
+// The power of two that brings x into [2^14, 2^15), the upper end of f16; 1 for zero, infinite and NaN x.  Exponents are kept where both the
 // factor and its reciprocal are normal numbers.
 __device__ __forceinline__ float pow2_normaliser(float x) {
     const int e = (int)(__float_as_uint(x) >> 23) & 0xFF;   // x >= 0
     if (x == 0.f || e == 255) return 1.0f;
-    const int f = min(max(253 - e, 2), 252);               // 2^(126 - e) has the exponent field 253 - e
+    const int f = min(max(268 - e, 2), 252);               // 2^(141 - e) has the exponent field 268 - e
     return __uint_as_float((uint32_t)f << 23);
 }
 
