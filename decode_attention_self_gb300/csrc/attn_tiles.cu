@@ -997,7 +997,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const PromptParams p) {
     if (w >= (long long)p.T * pairs) return;
     const int t = (int)(w / pairs), h = (int)(w - (long long)t * pairs) * 2 + (lane >> 4);
     int s0, s1;
-    if (find_row(p.row_start, p.B, p.T, t, lane, s0, s1, nullptr) < 0 || s1 - s0 <= p.few_max || h >= p.Hq) return;
+    if (find_row(p.row_start, p.B, p.T, t, lane, s0, s1, nullptr, 0, 1) < 0 || s1 - s0 <= p.few_max || h >= p.Hq) return;
     const size_t rows = (size_t)p.T * p.Hq, row = (size_t)t * p.Hq + h;
     float M = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);

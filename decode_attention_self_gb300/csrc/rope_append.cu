@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(kThreads, 6) rope_append_kernel(const RopeAppe
     };
     load(part * 8 + hs);   // in flight while the row and the position are found
     int s0, s1;
-    const int b = find_row(p.row_start, p.B, p.T, t, lane, s0, s1, part == 0 ? p.err : nullptr);
+    const int b = find_row(p.row_start, p.B, p.T, t, lane, s0, s1, p.err, gw, (long long)p.T * warps_per_token);
     if (b < 0) return;   // behind the last row: left as it is
 
     const long long slot = (long long)__ldg(p.start_pos + b) + (t - s0);
