@@ -27,6 +27,9 @@ DR_BF16, DR_F32 = 0, 1
 DR_KV_BF16, DR_KV_FP8_E4M3 = 0, 1
 DR_ERRF_SEQ_LEN, DR_ERRF_BLOCK_ID, DR_ERRF_POS, DR_ERRF_TOKEN, DR_ERRF_TIMEOUT, DR_ERRF_ROW_START = 1, 2, 4, 8, 16, 32
 DR_SAMPLE_ADVANCE = 1
+DR_ACT_NONE, DR_ACT_RELU, DR_ACT_GELU, DR_ACT_GELU_TANH, DR_ACT_SILU = 0, 1, 2, 3, 4
+DR_NORM_NONE, DR_NORM_LAYER, DR_NORM_RMS = 0, 1, 2
+DR_LINEAR_MAX_OUTS = 4
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is missing: build it with `python -c 'import __graft_entry__ as g; g.build()'`")
@@ -43,6 +46,19 @@ class dr_kv_cache(ctypes.Structure):
 class dr_score_opts(ctypes.Structure):
     _fields_ = [("causal", ctypes.c_int32), ("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p),
                 ("prefix_len", ctypes.c_void_p), ("first_key", ctypes.c_void_p)]
+
+
+class dr_linear_opts(ctypes.Structure):
+    _fields_ = [("act", ctypes.c_int32), ("gated", ctypes.c_int32), ("bias", ctypes.c_void_p),
+                ("residual", ctypes.c_void_p), ("residual_stride", ctypes.c_int64)]
+
+
+class dr_linear_out(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("stride", ctypes.c_int64), ("cols", ctypes.c_int32)]
+
+
+class dr_norm(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("eps", ctypes.c_float), ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p)]
 
 
 _vp, _i, _f = ctypes.c_void_p, ctypes.c_int, ctypes.c_float
@@ -71,6 +87,9 @@ _lib.dr_shared_prefix_attn.argtypes = [_vp, _i64, _cs, _vp, _cs, _vp, _cs, _i, _
 _lib.dr_shared_prefix_attn_stall_test.argtypes = _lib.dr_shared_prefix_attn.argtypes[:-1] + [_i, _vp]
 _lib.dr_shared_prefix_attn_workspace.argtypes = [_i, _i, _i, _i, _i]
 _lib.dr_shared_prefix_attn_workspace.restype = _sz
+_lib.dr_linear.argtypes = [_vp, _i64, _vp, _cs, _i, _i, _i, _cs, _i, _i, _vp, _vp]
+_lib.dr_linear_stall_test.argtypes = _lib.dr_linear.argtypes[:-1] + [_i, _vp]
+_lib.dr_residual_norm.argtypes = [_vp, _i64, _i, _cs, _vp, _i64, _f, _vp, _i64, _vp, _i64, _i, _cs, _vp, _i64, _i, _i, _i, _vp]
 _lib.dr_plan_splits.argtypes = [_i, _i, _i, _i, _i]
 _lib.dr_plan_splits.restype = _i
 _lib.dr_status_string.argtypes = [_i]
@@ -78,7 +97,8 @@ _lib.dr_status_string.restype = ctypes.c_char_p
 for _fn in ("dr_kv_append", "dr_decode_self_attn", "dr_decode_cross_attn", "dr_decode_layer",
             "dr_sample_topk_delayed", "dr_embed_tokens", "dr_lm_head", "dr_lm_head_stall_test",
             "dr_decode_self_attn_stall_test", "dr_rope_table", "dr_rope_append", "dr_prompt_attn",
-            "dr_shared_prefix_attn", "dr_prompt_attn_stall_test", "dr_shared_prefix_attn_stall_test"):
+            "dr_shared_prefix_attn", "dr_prompt_attn_stall_test", "dr_shared_prefix_attn_stall_test",
+            "dr_linear", "dr_linear_stall_test", "dr_residual_norm"):
     getattr(_lib, _fn).restype = _i
 
 
@@ -531,6 +551,145 @@ def dr_shared_prefix_attn(q: torch.Tensor, prefix: KVCache, prefix_len: torch.Te
 def dr_shared_prefix_attn_stall_test(stall_head: int, *args, **kwargs) -> torch.Tensor:
     """Test hook: dr_shared_prefix_attn with one CTA of key/value head stall_head made to time out (see dr_api.h)."""
     return dr_shared_prefix_attn(*args, _stall_head=int(stall_head), **kwargs)
+
+
+# The layer calls: as above, checks written out flat.
+_ACTS = {None: DR_ACT_NONE, "none": DR_ACT_NONE, "relu": DR_ACT_RELU, "gelu": DR_ACT_GELU, "gelu_tanh": DR_ACT_GELU_TANH,
+         "silu": DR_ACT_SILU}
+_NORMS = {"none": DR_NORM_NONE, "layer": DR_NORM_LAYER, "rms": DR_NORM_RMS}
+_pack_linear_opts = struct.Struct("@iiPPq").pack   # dr_linear_opts
+_pack_linear_out = struct.Struct("@Pqi4x").pack    # dr_linear_out
+_pack_norm = struct.Struct("@ifPP").pack           # dr_norm
+assert struct.calcsize("@iiPPq") == ctypes.sizeof(dr_linear_opts)
+assert struct.calcsize("@Pqi4x") == ctypes.sizeof(dr_linear_out)
+assert struct.calcsize("@ifPP") == ctypes.sizeof(dr_norm)
+
+
+def _tokens(t, dev: int, dtype, T: int, n: int, name: str):
+    """(address, elements between tokens) of a [T, n] tensor whose rows are dense but may lie apart."""
+    if t.get_device() != dev or t.dtype is not dtype or t.shape != (T, n):
+        _refuse(t, dev, dtype, (T, n), name)
+    s0, s1 = t.stride()
+    if s1 != 1 and n > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t.data_ptr(), (s0 if T > 1 else -(-n // 8) * 8)
+
+
+def _float_type(t, name: str):
+    dt = t.dtype
+    if dt is _BF16:
+        return DR_BF16
+    if dt is _F32:
+        return DR_F32
+    raise ValueError(f"{name} must be {_BF16} or {_F32}, got {dt}")
+
+
+def dr_linear(x: torch.Tensor, W: torch.Tensor, out, bias: torch.Tensor | None = None, act: str | None = None,
+              gated: bool = False, residual: torch.Tensor | None = None, err_flag: torch.Tensor | None = None, stream=None,
+              _stall_tile=None):
+    """out = residual + act(x W^T + bias): x [T, K] bf16, W [N, K] bf16 ([2N, K] when gated), out [T, N] bf16 or float32.
+
+    act: None, "relu", "gelu", "gelu_tanh" or "silu"; gated: the activated first N columns times the last N.  out may be
+    a list of up to four [T, n] tensors of one type that share the columns (all but the last a multiple of 64 wide).
+    x, out and residual may be slices with dense rows; residual may be out itself.
+    """
+    dev = _device()
+    if x.dim() != 2 or W.dim() != 2:
+        raise ValueError("x must be [T, K] and W [N, K]")
+    T, K = x.shape
+    rows = W.shape[0]
+    xp, xs = _tokens(x, dev, _BF16, T, K, "x")
+    outs = out if isinstance(out, (list, tuple)) else (out,)
+    if not outs:
+        raise ValueError("out must hold at least one tensor")
+    od = _float_type(outs[0], "out")
+    N = 0
+    packed = b""
+    for o in outs:
+        if o.dim() != 2:
+            raise ValueError("out must be [T, N]")
+        n = o.shape[1]
+        op, os_ = _tokens(o, dev, outs[0].dtype, T, n, "out")
+        packed += _pack_linear_out(op, os_, n)
+        N += n
+    if rows != (2 * N if gated else N):
+        raise ValueError(f"W must have {2 * N if gated else N} rows for {N} columns, has {rows}")
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {sorted(k for k in _ACTS if k)}, got {act!r}")
+    wp = _vec(W, dev, _BF16, rows * K, "W")
+    if residual is None:
+        rp = rs = 0
+    else:
+        rp, rs = _tokens(residual, dev, outs[0].dtype, T, N, "residual")
+    opts = _pack_linear_opts(_ACTS[act], 1 if gated else 0, _vec(bias, dev, _BF16, rows, "bias") or 0, rp, rs)
+    args = (xp, xs, wp, opts, T, K, N, packed, len(outs), od, _vec(err_flag, dev, _I32, 1, "err_flag"))
+    if _stall_tile is None:
+        st = _lib.dr_linear(*args, _stream_arg(stream, dev))
+    else:
+        st = _lib.dr_linear_stall_test(*args, _stall_tile, _stream_arg(stream, dev))
+    if st:
+        raise DrError("dr_linear", st)
+    return out
+
+
+def dr_linear_stall_test(stall_tile: int, *args, **kwargs):
+    """Test hook: dr_linear with the CTAs of output tile `stall_tile` made to time out (see dr_api.h)."""
+    return dr_linear(*args, _stall_tile=int(stall_tile), **kwargs)
+
+
+@dataclasses.dataclass
+class Norm:
+    """A norm over a token's elements: kind "layer" or "rms" ("none": nothing), weight and bias [Dm] bf16 or None."""
+
+    kind: str
+    eps: float = 1e-5
+    weight: torch.Tensor | None = None
+    bias: torch.Tensor | None = None
+
+
+def _norm_arg(n: Norm | None, dev: int, Dm: int, name: str):
+    if n is None:
+        return None
+    kind = _NORMS.get(n.kind)
+    if kind is None:
+        raise ValueError(f"{name}.kind must be one of {sorted(_NORMS)}, got {n.kind!r}")
+    return _pack_norm(kind, n.eps, _vec(n.weight, dev, _BF16, Dm, name + ".weight") or 0,
+                      _vec(n.bias, dev, _BF16, Dm, name + ".bias") or 0)
+
+
+def dr_residual_norm(x: torch.Tensor, y: torch.Tensor | None = None, pre: Norm | None = None,
+                     residual: torch.Tensor | None = None, h: torch.Tensor | None = None, post: Norm | None = None,
+                     gate: torch.Tensor | None = None, scale: float = 1.0, stream=None) -> None:
+    """h = residual + scale * gate * post(x) and y = pre(h), rows of [T, Dm]; what is None is left out.
+
+    x, y: bf16 or float32; residual and h: of one type, bf16 or float32 (h may be residual itself); gate: bf16 [Dm] for all
+    tokens or [T, Dm].
+    """
+    dev = _device()
+    if x.dim() != 2:
+        raise ValueError("x must be [T, Dm]")
+    T, Dm = x.shape
+    xd = _float_type(x, "x")
+    xp, xs = _tokens(x, dev, x.dtype, T, Dm, "x")
+    hd, rp, rs, hp, hs, yp, ys, yd, gp, gs = DR_BF16, None, 0, None, 0, None, 0, DR_BF16, None, 0
+    if residual is not None:
+        hd = _float_type(residual, "residual")
+        rp, rs = _tokens(residual, dev, residual.dtype, T, Dm, "residual")
+    if h is not None:
+        hd = _float_type(h, "h")
+        hp, hs = _tokens(h, dev, h.dtype if residual is None else residual.dtype, T, Dm, "h")
+    if y is not None:
+        yd = _float_type(y, "y")
+        yp, ys = _tokens(y, dev, y.dtype, T, Dm, "y")
+    if gate is not None:
+        if gate.dim() == 1:
+            gp = _vec(gate, dev, _BF16, Dm, "gate")
+        else:
+            gp, gs = _tokens(gate, dev, _BF16, T, Dm, "gate")
+    st = _lib.dr_residual_norm(xp, xs, xd, _norm_arg(post, dev, Dm, "post"), gp, gs, scale, rp, rs, hp, hs, hd,
+                               _norm_arg(pre, dev, Dm, "pre"), yp, ys, yd, T, Dm, _stream_arg(stream, dev))
+    if st:
+        raise DrError("dr_residual_norm", st)
 
 
 def loaded_library_path() -> str:

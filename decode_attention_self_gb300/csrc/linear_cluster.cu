@@ -1,0 +1,319 @@
+// Matrix product with an epilogue for some tens to hundreds of tokens: out = residual + act(x W^T + bias).
+//
+// One CTA multiplies up to 128 tokens by NB rows of W over its share of K on the tensor cores: the tokens are the MMA's
+// M = 128 operand, the weight rows its N operand, both K-major bf16 in shared memory with the 128-byte swizzle, the fp32
+// sums in tensor memory (a lane per token).  Few tokens make W's bytes the cost, and N / NB tiles alone would leave SMs
+// idle, so the S CTAs of a cluster share K: each pushes its partial sums, row by row, into the shared memory of the CTA
+// that owns the row (rows / S each), and after one cluster barrier the owner adds the S parts in rank order and finishes
+// its rows with 16-byte accesses.  The order of sums is fixed: results are the same bits from call to call.
+//   warp 0: TMA producer of 64-wide K chunks;  warp 1: MMA issuer;  all 4 warps: push, sum, epilogue.
+// Tensor-core sums are cut off, not rounded: each addition may lose the last bit towards zero, so a chain over K drifts by about
+// 1e-9 K (measured: 1.0e-6 at K = 1024, 2.1e-6 at 2048).  fp32 outputs therefore break the chain every 512 of K into
+// accumulators of their own (pieces), added in fp32; bf16 outputs, whose rounding is 1000 times that, do not.
+// Tensor memory and clusters: a CTA that waits for its cluster must not keep another cluster's CTA waiting for tensor
+// memory.  A CTA takes at least 80 KB of shared memory and at most 256 columns, so that the two that fit on an SM (or one and two
+// of the LM head's, 72 KB and 128 columns at the least and most) never need more than the 512 there are.
+// Every mbarrier wait is bounded; one that runs out sets DR_ERRF_TIMEOUT, and the cluster's tile is not written.
+#include "dr_tc.cuh"
+#include "linear_epilogue.cuh"
+
+namespace dr {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kRows = 128;        // tokens per tile (MMA M)
+constexpr int kChunkK = 64;       // K per stage: one 128-byte swizzled row
+constexpr int kMaxStages = 8;
+constexpr int kPieceChunks = 8;   // fp32 outputs: K of 512 per accumulator
+constexpr int kMaxCols = 256;     // tensor-memory columns of a CTA (see above)
+constexpr size_t kMinSmem = 80 * 1024;
+constexpr size_t kMaxSmem = 226 * 1024;
+
+struct ClusterPlan {
+    int nb;            // weight rows per tile (MMA N): nb output columns, or nb / 2 when gated
+    int split;         // CTAs (one cluster) that share K
+    int box_rows;      // tokens per tile that are loaded
+    int piece_chunks;  // K chunks per accumulator
+    int stages;
+    int cols;          // tensor-memory columns
+    size_t smem;
+};
+
+struct ClusterArgs {
+    LinearParams p;
+    ClusterPlan plan;
+};
+
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(tc::smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+__global__ void __launch_bounds__(kThreads)
+    linear_cluster_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
+                          const __grid_constant__ ClusterArgs args) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], done;
+    __shared__ uint32_t tmem_base;
+    __shared__ int gave_up, issued;   // a wait ran out; chunks whose copies were issued (and all before, but for a stalled one)
+    __shared__ int part_ok[8];
+
+    const LinearParams &p = args.p;
+    const ClusterPlan &pl = args.plan;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int S = pl.split, rank = blockIdx.x, stages = pl.stages;
+    const int bn = p.gated ? pl.nb / 2 : pl.nb;   // output columns of a tile
+    const int n0 = blockIdx.y * bn, t0 = blockIdx.z * kRows;
+    const int all_chunks = (p.K + kChunkK - 1) / kChunkK;
+    const int c_begin = (int)((int64_t)all_chunks * rank / S), c_end = (int)((int64_t)all_chunks * (rank + 1) / S);
+    const int chunks = c_end - c_begin;
+    const uint32_t bytes_x = pl.box_rows * 128, bytes_w = pl.nb * 128;
+
+    const uint32_t ring = (tc::smem_u32(smem_raw) + 1023) & ~1023u;
+    const uint32_t sx = ring, sw = ring + stages * (kRows * 128);
+    const uint32_t recv_off = ring - tc::smem_u32(smem_raw) + stages * (kRows * 128 + bytes_w);
+
+    if (threadIdx.x == 0) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_x)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_w)) : "memory");
+        for (int s = 0; s < stages; ++s) {
+            tc::mbar_init(&full[s], 1);
+            tc::mbar_init(&empty[s], 1);
+        }
+        tc::mbar_init(&done, 1);
+        gave_up = issued = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc::smem_u32(&tmem_base)),
+                     "r"(pl.cols));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = tmem_base;
+    if (S > 1) cluster_arrive();   // waited for before the first remote write: every CTA of the cluster runs by then
+    // the first weight boxes on their way into L2 while the kernel before this one ends (a hint: nothing is read)
+    if (warp == 0 && tc::elect_one()) {
+        const int ahead = min(chunks, stages);
+        for (int c = 0; c < ahead; ++c)
+            asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
+                             reinterpret_cast<uint64_t>(&map_w)),
+                         "r"((c_begin + c) * kChunkK), "r"(n0)
+                         : "memory");
+    }
+    pdl_wait();
+
+    if (warp == 0) {
+        // stage s of round r waits for the products of round r - 1.  (Test hook: the stalled tile's producer starts at
+        // chunk 1, so the wait for chunk 0 runs out.)
+        const bool stalled = (int)(blockIdx.z * gridDim.y + blockIdx.y) == p.stall_tile;
+        const int first = stalled ? 1 : 0;
+        int c = first;
+        for (int s = c % stages, r = c / stages; c < chunks; ++c) {
+            if (r > 0 && !tc::mbar_wait(&empty[s], (r - 1) & 1, &gave_up)) break;
+            if (tc::elect_one()) {
+                const int k = (c_begin + c) * kChunkK;
+                tc::mbar_expect_tx(&full[s], bytes_x + bytes_w);
+                const uint32_t w_at = sw + s * bytes_w;
+                tma_load_2d(w_at, &map_w, k, n0, &full[s]);
+                if (p.gated) tma_load_2d(w_at + bytes_w / 2, &map_w, k, p.N + n0, &full[s]);
+                tma_load_2d(sx + s * (kRows * 128), &map_x, k, t0, &full[s]);
+            }
+            __syncwarp();
+            if (++s == stages) {
+                s = 0;
+                ++r;
+            }
+        }
+        if (lane == 0) issued = c;
+    } else if (warp == 1) {
+        const uint32_t idesc = tc::instr_desc(kRows, pl.nb, false, false);
+        const uint64_t dx = tc::smem_desc(sx), dw = tc::smem_desc(sw);
+        bool ok = true;
+        for (int c = 0, s = 0, r = 0, in_piece = 0, d = tmem; c < chunks; ++c) {
+            if (!tc::mbar_wait(&full[s], r & 1, &gave_up)) {
+                ok = false;
+                break;
+            }
+            tc::fence_after();
+            if (tc::elect_one()) {
+#pragma unroll
+                for (int k = 0; k < kChunkK / 16; ++k)
+                    tc::mma_ss(d, tc::desc_at(dx, s * (kRows * 128) + k * 32), tc::desc_at(dw, s * bytes_w + k * 32), idesc,
+                               (in_piece | k) != 0);
+                tc::commit(&empty[s]);   // the stage is free once these products have read it
+            }
+            __syncwarp();
+            if (++in_piece == pl.piece_chunks) {
+                in_piece = 0;
+                d += pl.nb;
+            }
+            if (++s == stages) {
+                s = 0;
+                ++r;
+            }
+        }
+        if (!ok && lane == 0) flag_error(p.err, DR_ERRF_TIMEOUT);
+        // on every path: with `done` the products in flight have ended (a commit follows those before it)
+        if (tc::elect_one()) tc::commit(&done);
+        __syncwarp();
+    }
+    __syncthreads();
+    pdl_trigger();
+    bool ok = tc::mbar_wait(&done, 0, &gave_up);
+    if (gave_up) {
+        // copies in flight end by themselves; wait for them before this CTA's shared memory goes away
+        if (warp == 0 && lane == 0) {
+            for (int c = max(p.stall_tile < 0 ? 0 : 1, issued - stages); c < issued; ++c)
+                tc::mbar_drain(&full[c % stages], (c / stages) & 1);
+            flag_error(p.err, DR_ERRF_TIMEOUT);
+        }
+        ok = false;
+    }
+    ok = __syncthreads_and(ok);
+    tc::fence_after();
+
+    // partial sums, row by row, to the CTA that owns the row
+    const int rows = min(kRows, p.T - t0);
+    const int share = (rows + S - 1) / S;   // rows that a CTA owns
+    const int nb = pl.nb;
+    const uint32_t recv = tc::smem_u32(smem_raw) + recv_off;
+    if (S > 1) cluster_wait();
+    const int pieces = (chunks + pl.piece_chunks - 1) / pl.piece_chunks;
+    const int row = warp * 32 + lane;
+    if (ok && warp * 32 < rows) {
+        const int owner = row / share;
+        const uint32_t slot = recv + (uint32_t)((rank * share + row - owner * share) * nb) * 4;
+        const uint32_t dst = S > 1 ? mapa(slot, min(owner, S - 1)) : slot;
+        for (int c0 = 0; c0 < nb; c0 += 32) {
+            float acc[32];
+            tc::ld32(tmem + ((uint32_t)(warp * 32) << 16) + c0, acc);
+            tc::wait_ld();
+            tc::pin32(acc);
+            for (int i = 1; i < pieces; ++i) {
+                float more[32];
+                tc::ld32(tmem + ((uint32_t)(warp * 32) << 16) + i * nb + c0, more);
+                tc::wait_ld();
+                tc::pin32(more);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) acc[j] += more[j];
+            }
+            if (row < rows) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)   // 16-byte steps, turned by the row so that a warp's stores spread over the banks
+                    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                     dst + (((c0 / 4 + j) ^ (row & 7)) * 16)),
+                                 "f"(acc[4 * j]), "f"(acc[4 * j + 1]), "f"(acc[4 * j + 2]), "f"(acc[4 * j + 3])
+                                 : "memory");
+            }
+        }
+    }
+    if (threadIdx.x < S) {
+        const uint32_t at = tc::smem_u32(&part_ok[rank]);
+        asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(S > 1 ? mapa(at, threadIdx.x) : at), "r"((int)ok) : "memory");
+    }
+    tc::fence_before();
+    if (S > 1) {
+        cluster_arrive();
+        cluster_wait();
+    } else {
+        __syncthreads();
+    }
+    if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(pl.cols));
+    for (int i = 0; i < S; ++i)
+        if (!part_ok[i]) return;
+
+    const int mine = min(share, rows - rank * share), groups = bn / 8;
+    const float *sums = reinterpret_cast<const float *>(smem_raw + recv_off);
+    for (int i = threadIdx.x; i < mine * groups; i += kThreads) {
+        const int r = i / groups, g = i - r * groups, key = (rank * share + r) & 7;
+        float a[8] = {}, b[8] = {};
+        for (int s = 0; s < S; ++s) {
+            const float4 *from = reinterpret_cast<const float4 *>(sums + (size_t)(s * share + r) * nb);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float4 v = from[(2 * g + h) ^ key];
+                a[4 * h] += v.x; a[4 * h + 1] += v.y; a[4 * h + 2] += v.z; a[4 * h + 3] += v.w;
+            }
+            if (p.gated) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float4 v = from[(bn / 4 + 2 * g + h) ^ key];
+                    b[4 * h] += v.x; b[4 * h + 1] += v.y; b[4 * h + 2] += v.z; b[4 * h + 3] += v.w;
+                }
+            }
+        }
+        lin::finish8(p, t0 + rank * share + r, n0 + g * 8, a, b);
+    }
+}
+
+ClusterPlan make_plan(const LinearParams &p, int sms) {
+    ClusterPlan pl;
+    const int chunks = (p.K + kChunkK - 1) / kChunkK;
+    const int mtiles = (p.T + kRows - 1) / kRows;
+    pl.nb = 64;
+    const int bn = p.gated ? pl.nb / 2 : pl.nb;
+    const int64_t tiles = (int64_t)mtiles * ((p.N + bn - 1) / bn);
+    pl.split = 1;
+    while (pl.split < 8 && tiles * pl.split * 2 <= sms && pl.split * 4 <= chunks) pl.split *= 2;
+    const int rows = p.T < kRows ? p.T : kRows;
+    pl.box_rows = (rows + 7) / 8 * 8;
+    const int most = (chunks + pl.split - 1) / pl.split;   // chunks of a CTA
+    pl.piece_chunks = most;
+    int pieces = 1;
+    if (p.out_f32) {
+        pl.piece_chunks = kPieceChunks;
+        while ((most + pl.piece_chunks - 1) / pl.piece_chunks > kMaxCols / pl.nb) ++pl.piece_chunks;
+        pieces = (most + pl.piece_chunks - 1) / pl.piece_chunks;
+    }
+    pl.cols = 32;
+    while (pl.cols < pl.nb * pieces) pl.cols *= 2;
+    const size_t stage = (kRows + pl.nb) * 128;
+    const size_t recv = (size_t)(rows + pl.split) * pl.nb * 4;
+    pl.stages = most < kMaxStages ? most : kMaxStages;
+    while (pl.stages > 2 && 1024 + pl.stages * stage + recv > kMaxSmem) --pl.stages;
+    pl.smem = 1024 + pl.stages * stage + recv;
+    if (pl.smem < kMinSmem) pl.smem = kMinSmem;
+    return pl;
+}
+
+}  // namespace
+
+int linear_cluster_tiles(const LinearParams &p, int sms) {
+    const ClusterPlan pl = make_plan(p, sms);
+    const int bn = p.gated ? pl.nb / 2 : pl.nb;
+    const int64_t n = (int64_t)((p.T + kRows - 1) / kRows) * ((p.N + bn - 1) / bn);
+    return n > 0x7FFFFFFF ? 0x7FFFFFFF : (int)n;
+}
+
+cudaError_t launch_linear_cluster(const LinearParams &p, int sms, cudaStream_t stream) {
+    ClusterArgs a;
+    a.p = p;
+    a.plan = make_plan(p, sms);
+    const ClusterPlan &pl = a.plan;
+    const int bn = p.gated ? pl.nb / 2 : pl.nb;
+    CUtensorMap map_x, map_w;
+    if (!encode_rows(&map_x, p.x, p.T, p.K, p.x_stride, pl.box_rows) ||
+        !encode_rows(&map_w, p.W, (int64_t)p.N * (p.gated ? 2 : 1), p.K, p.K, bn))
+        return cudaErrorInvalidValue;
+    static std::atomic<uint64_t> ready{0};
+    cudaError_t e = once_per_device(ready, [] {
+        return cudaFuncSetAttribute(linear_cluster_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem);
+    });
+    if (e != cudaSuccess) return e;
+    const dim3 grid((unsigned)pl.split, (unsigned)((p.N + bn - 1) / bn), (unsigned)((p.T + kRows - 1) / kRows));
+    return launch_kernel(linear_cluster_kernel, grid, dim3(kThreads), pl.smem, stream, (unsigned)pl.split, map_x, map_w, a);
+}
+
+}  // namespace dr

@@ -25,6 +25,11 @@
  *                           document masks;
  *   dr_shared_prefix_attn   single-query attention of a batch whose rows share a
  *                           long prefix, which is read once for all of them.
+ * Between a layer's attention calls, for steps and prompts alike:
+ *   dr_linear               matrix product (projections, MLP) with bias, activation,
+ *                           gating and residual in its epilogue;
+ *   dr_residual_norm        the norms after and before a block with its gate,
+ *                           residual scale and residual.
  *
  * Conventions shared by every call
  *   - Every pointer argument except `stream` is a DEVICE pointer owned by the
@@ -518,6 +523,123 @@ dr_status dr_shared_prefix_attn_stall_test(const void *q, int64_t q_stride, cons
 
 /* Host-only: workspace bytes of dr_shared_prefix_attn for prefixes of up to max_prefix keys on num_sms SMs. */
 size_t dr_shared_prefix_attn_workspace(int B, int Hq, int Hkv, int max_prefix, int num_sms);
+
+/* Activations of dr_linear, computed in fp32. */
+typedef enum dr_act {
+    DR_ACT_NONE = 0,
+    DR_ACT_RELU = 1,      /* max(a, 0) */
+    DR_ACT_GELU = 2,      /* a * Phi(a), Phi the normal distribution function */
+    DR_ACT_GELU_TANH = 3, /* a * (1 + tanh(sqrt(2 / pi) * (a + 0.044715 a^3))) / 2 */
+    DR_ACT_SILU = 4       /* a / (1 + exp(-a)) */
+} dr_act;
+
+/* What dr_linear does with its sums (read on the host during the call; the arrays are device pointers). */
+typedef struct dr_linear_opts {
+    int32_t act;             /* dr_act */
+    int32_t gated;           /* 1: W has 2N rows; the activated first N columns are multiplied by the last N */
+    const void *bias;        /* nullable [N] ([2N] when gated) bf16, 16-byte aligned: added before the activation */
+    const void *residual;    /* nullable [T][N] in out_dtype: added last; may be the output itself with its stride */
+    int64_t residual_stride; /* elements between its tokens, at least N */
+} dr_linear_opts;
+
+/* One output of dr_linear: `cols` columns, after those of the outputs before it. */
+typedef struct dr_linear_out {
+    void *ptr;      /* [T][cols] in out_dtype (device, aligned to its elements) */
+    int64_t stride; /* elements between tokens, at least cols */
+    int32_t cols;   /* a multiple of 64 (whole heads) for all but the last */
+} dr_linear_out;
+
+#define DR_LINEAR_MAX_OUTS 4
+
+/*
+ * dr_linear -- matrix product of tokens with a weight matrix, and what follows
+ * it in a decoder layer: bias, activation, gating, residual.
+ *
+ *   a[t][n]   = sum_k x[t][k] * W[n][k] + bias[n]
+ *   v[t][n]   = act(a[t][n]), or act(a[t][n]) * a[t][N + n] when gated
+ *   out[t][n] = residual[t][n] + v[t][n]
+ * Sums and everything after them are fp32, rounded once to out_dtype.  The
+ * columns may go to several outputs in turn (queries, keys and values of a
+ * merged projection).  Any number of tokens: single steps, batches and prompts
+ * take kernels of their own, chosen by T, K and N.
+ * For every T the sums over K run on the tensor cores, which cut off rather
+ * than round (about 1e-9 K of the value, towards zero); with fp32 outputs the
+ * chains are broken every 512 of K and added in fp32.  A NaN or infinity in a
+ * token or weight row reaches that token's or column's outputs and no others;
+ * at a = -inf gelu, gelu_tanh and silu give their limit 0.
+ *
+ *   x        : [T][K] bf16 (device, 16-byte aligned), tokens x_stride elements apart (a multiple of 8, >= K)
+ *   W        : [N][K] bf16, [2N][K] when gated (device, 16-byte aligned)
+ *   opts     : nullable (no bias, activation or residual)
+ *   T        : at least 1;  K : a multiple of 8;  N : any, the columns of all outputs together
+ *   outs     : n_outs (1 .. DR_LINEAR_MAX_OUTS) outputs, read on the host during the call; a residual takes a single
+ *              one.  16-byte aligned pointers and strides make them faster, and so for the residual.  Outputs overlap
+ *              neither each other nor x, W and bias
+ *   err_flag : nullable device int32; DR_ERRF_TIMEOUT if a CTA's bounded pipeline wait gave up (its outputs are then
+ *              not written)
+ * Same inputs, sizes and device give the same bits from call to call.
+ */
+dr_status dr_linear(const void *x, int64_t x_stride, const void *W, const dr_linear_opts *opts, int T, int K, int N,
+                    const dr_linear_out *outs, int n_outs, dr_dtype out_dtype, int32_t *err_flag, void *stream);
+
+/*
+ * dr_linear_stall_test -- TEST HOOK, never needed in use.  The same call as
+ * dr_linear, except that the CTAs of output tile `stall_tile` never load their
+ * first K chunk.  Their bounded waits then run out (after about 2 s):
+ * DR_ERRF_TIMEOUT is ORed into *err_flag, that tile's outputs (and those of
+ * tiles that the same CTAs would have taken after it) are left unwritten, and
+ * every other output is written as by dr_linear.  Nothing faults or hangs, and
+ * later calls on the same context work normally.
+ *   DR_ERR_UNSUPPORTED where the call's kernel has no waits; DR_ERR_INVALID_ARG
+ *   where there is no such tile; the rest as dr_linear.
+ */
+dr_status dr_linear_stall_test(const void *x, int64_t x_stride, const void *W, const dr_linear_opts *opts, int T, int K,
+                               int N, const dr_linear_out *outs, int n_outs, dr_dtype out_dtype, int32_t *err_flag,
+                               int stall_tile, void *stream);
+
+/* Norms of dr_residual_norm. */
+typedef enum dr_norm_kind {
+    DR_NORM_NONE = 0,
+    DR_NORM_LAYER = 1, /* (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps) * weight + bias */
+    DR_NORM_RMS = 2    /* v / sqrt(mean(v^2) + eps) * weight + bias */
+} dr_norm_kind;
+
+/* A norm over the Dm elements of a token (read on the host during the call; the arrays are device pointers). */
+typedef struct dr_norm {
+    int32_t kind;       /* dr_norm_kind */
+    float eps;          /* >= 0 and finite */
+    const void *weight; /* nullable [Dm] bf16, 16-byte aligned (null: ones) */
+    const void *bias;   /* nullable [Dm] bf16, 16-byte aligned (null: zeros) */
+} dr_norm;
+
+/*
+ * dr_residual_norm -- what stands between one block of a decoder layer and the
+ * next, in one pass: the norm after a block, its gate and residual scale, the
+ * residual, and the norm before the next block.
+ *
+ *   h[t] = residual[t] + scale * gate[t] * post(x[t])
+ *   y[t] = pre(h[t])
+ * Each part may be left out: post or pre (null: nothing is normed), gate,
+ * residual (h is then the rest), h or y (not written).  Statistics and all
+ * arithmetic are fp32; layer norm takes its mean first and the squared
+ * differences after.  y comes from h before h is rounded to its type.  A NaN
+ * or infinity stays in its token.
+ *
+ *   x        : [T][Dm] in x_dtype, tokens x_stride elements apart
+ *   gate     : nullable bf16, [Dm] for all tokens (gate_stride 0) or [T][Dm] (gate_stride >= Dm)
+ *   scale    : finite
+ *   residual : nullable [T][Dm] in h_dtype;  h : nullable [T][Dm] in h_dtype, may be residual or x itself with the
+ *              same stride and type
+ *   y        : nullable [T][Dm] in y_dtype; may be x or residual itself with the same stride and type where h is not
+ *              it; h and y are not both null
+ *   Dm       : a multiple of 8, at most 16384 (DR_ERR_UNSUPPORTED above)
+ * Pointers are device pointers, 16-byte aligned; strides are in elements, multiples of 16 bytes, at least Dm.  h and y
+ * overlap the inputs and each other only as said.
+ */
+dr_status dr_residual_norm(const void *x, int64_t x_stride, dr_dtype x_dtype, const dr_norm *post, const void *gate,
+                           int64_t gate_stride, float scale, const void *residual, int64_t residual_stride, void *h,
+                           int64_t h_stride, dr_dtype h_dtype, const dr_norm *pre, void *y, int64_t y_stride,
+                           dr_dtype y_dtype, int T, int Dm, void *stream);
 
 /*
  * dr_plan_splits -- host-only query: how many CTAs (one thread-block
