@@ -32,14 +32,18 @@ struct LinearParams {
     int32_t stall_tile = -1;  // test hook: the CTAs of this output tile never load their first K chunk
 };
 
-// Tensor map of a bf16 matrix [rows][K], rows `stride` elements apart: boxes of box_rows x 64, 128-byte swizzle.
-bool encode_rows(CUtensorMap *map, const void *ptr, int64_t rows, int K, int64_t stride, int box_rows);
+// Tensor map of a bf16 or fp32 matrix [rows][cols], rows `stride` elements apart: boxes of box_rows x box_cols (128 bytes),
+// 128-byte swizzle, zeros outside.
+bool encode_matrix(CUtensorMap *map, const void *ptr, bool f32, int64_t rows, int cols, int64_t stride, int box_rows,
+                   int box_cols);
 
 // Output tiles of a launch as the test hook counts them; 0 where the call runs a kernel without waits.
 int linear_tiles(const LinearParams &p, int sms);
 cudaError_t launch_linear(const LinearParams &p, cudaStream_t stream);
 cudaError_t launch_linear_cluster(const LinearParams &p, int sms, cudaStream_t stream);
 int linear_cluster_tiles(const LinearParams &p, int sms);
+cudaError_t launch_linear_tiles(const LinearParams &p, int sms, cudaStream_t stream);
+int linear_tiles_tiles(const LinearParams &p);
 
 struct NormParams {
     int32_t kind;             // DR_NORM_*

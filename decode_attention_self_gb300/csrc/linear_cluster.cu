@@ -304,8 +304,8 @@ cudaError_t launch_linear_cluster(const LinearParams &p, int sms, cudaStream_t s
     const ClusterPlan &pl = a.plan;
     const int bn = p.gated ? pl.nb / 2 : pl.nb;
     CUtensorMap map_x, map_w;
-    if (!encode_rows(&map_x, p.x, p.T, p.K, p.x_stride, pl.box_rows) ||
-        !encode_rows(&map_w, p.W, (int64_t)p.N * (p.gated ? 2 : 1), p.K, p.K, bn))
+    if (!encode_matrix(&map_x, p.x, false, p.T, p.K, p.x_stride, pl.box_rows, kChunkK) ||
+        !encode_matrix(&map_w, p.W, false, (int64_t)p.N * (p.gated ? 2 : 1), p.K, p.K, bn, kChunkK))
         return cudaErrorInvalidValue;
     static std::atomic<uint64_t> ready{0};
     cudaError_t e = once_per_device(ready, [] {
