@@ -26,7 +26,7 @@ NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-
 
 # Kernels that share a launch's registers out between their warps, and the registers per thread that they count on: a launch
 # with another number is refused at run time, so the build looks at what ptxas gave them.
-LAUNCH_REGISTERS = {"attn_tiles.cu": ("attn_tiles_kernel", 128)}
+LAUNCH_REGISTERS = {"attn_tiles.cu": ("attn_tiles_kernel", 128), "linear_tiles.cu": ("linear_tiles_kernel", 96)}
 
 
 def check_registers(src: str, ptxas: str) -> None:

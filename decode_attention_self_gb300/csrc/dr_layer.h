@@ -27,13 +27,13 @@ struct LinearParams {
     int32_t T, K, N;          // N: output columns
     int32_t act, gated;
     int32_t out_f32;
-    int32_t vec_out, vec_res; // 16-byte accesses to the outputs (the residual) are aligned
+    int32_t vec_out, vec_res; // rows of the outputs (the residual) start on 32 bytes (2), on 16 (1) or anywhere (0)
     int32_t *err;
     int32_t stall_tile = -1;  // test hook: the CTAs of this output tile never load their first K chunk
 };
 
-// Tensor map of a bf16 or fp32 matrix [rows][cols], rows `stride` elements apart: boxes of box_rows x box_cols (128 bytes),
-// 128-byte swizzle, zeros outside.
+// Tensor map of a bf16 or fp32 matrix [rows][cols], rows `stride` elements apart: boxes of box_rows x box_cols (128 or 64
+// bytes, and the swizzle of that width), zeros outside.
 bool encode_matrix(CUtensorMap *map, const void *ptr, bool f32, int64_t rows, int cols, int64_t stride, int box_rows,
                    int box_cols);
 

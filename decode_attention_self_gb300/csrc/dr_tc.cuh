@@ -136,6 +136,16 @@ __device__ __forceinline__ void ld32(uint32_t taddr, T *r) {
         : DR_TC_R8(q, 0), DR_TC_R8(q, 8), DR_TC_R8(q, 16), DR_TC_R8(q, 24)
         : "r"(taddr));
 }
+// 16 columns
+template <typename T>
+__device__ __forceinline__ void ld16(uint32_t taddr, T *r) {
+    uint32_t *q = reinterpret_cast<uint32_t *>(r);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+        "[%16];"
+        : DR_TC_R8(q, 0), DR_TC_R8(q, 8)
+        : "r"(taddr));
+}
 __device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 // Ties 32 registers to this point of the program: what reads them afterwards cannot move above a wait_ld before it.
 #define DR_TC_P8(r, o) "+r"(r[o]), "+r"(r[o + 1]), "+r"(r[o + 2]), "+r"(r[o + 3]), "+r"(r[o + 4]), "+r"(r[o + 5]), \
@@ -145,6 +155,11 @@ __device__ __forceinline__ void pin32(T *r) {
     uint32_t *q = reinterpret_cast<uint32_t *>(r);
     asm volatile("" : DR_TC_P8(q, 0), DR_TC_P8(q, 8));
     asm volatile("" : DR_TC_P8(q, 16), DR_TC_P8(q, 24));
+}
+template <typename T>
+__device__ __forceinline__ void pin16(T *r) {
+    uint32_t *q = reinterpret_cast<uint32_t *>(r);
+    asm volatile("" : DR_TC_P8(q, 0), DR_TC_P8(q, 8));
 }
 template <typename T>
 __device__ __forceinline__ void st32(uint32_t taddr, const T *r) {

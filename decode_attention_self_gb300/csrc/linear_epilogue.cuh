@@ -19,50 +19,63 @@ __device__ __forceinline__ float fast_rcp(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// x / (1 + e^-x); 0 at -inf (e^-x of a large -x is +inf, whose reciprocal is 0)
-__device__ __forceinline__ float silu(float x) {
-    const float r = fast_rcp(1.0f + fast_exp2(-1.4426950408889634f * x));
-    return x == -INFINITY ? 0.0f : x * r;
+// The activations take two values at a time: the packed fp32 instructions need half the issue slots.
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// v r, and 0 at v = -inf, where r is 0
+__device__ __forceinline__ float2 times_tail(float2 v, float2 r) {
+    return make_float2(v.x == -INFINITY ? 0.0f : v.x * r.x, v.y == -INFINITY ? 0.0f : v.y * r.y);
+}
+// 1 / (1 + 2^-v); e^-x of a large -x is +inf, whose reciprocal is 0
+__device__ __forceinline__ float2 sigmoid2(float2 v) {
+    const float2 d = __fadd2_rn(make_float2(fast_exp2(-v.x), fast_exp2(-v.y)), both(1.0f));
+    return make_float2(fast_rcp(d.x), fast_rcp(d.y));
+}
+// x / (1 + e^-x)
+__device__ __forceinline__ float2 silu(float2 x) { return times_tail(x, sigmoid2(__fmul2_rn(x, both(1.4426950408889634f)))); }
+// x (1 + tanh u) / 2 = x / (1 + e^-2u), u = sqrt(2 / pi) (x + 0.044715 x^3)
+__device__ __forceinline__ float2 gelu_tanh(float2 x) {
+    const float2 c = __ffma2_rn(__fmul2_rn(x, x), both(0.10294324f), both(2.3022082f));   // 2 u log2(e) / x
+    return times_tail(x, sigmoid2(__fmul2_rn(x, c)));
 }
 // x Phi(x) = max(x, 0) - m Q(m), m = |x|, Q the normal distribution's upper tail.  Q(m) e^(m^2/2) is smooth and is fitted
 // here by a polynomial in t = 1 / (1 + 0.36 m), the form of Abramowitz and Stegun 7.1.26, with coefficients of its own:
 // least squares reweighted to the least largest relative error on [0, 13], 7e-7 (1e-6 in fp32).  No cancellation: the
 // sum's error is at most 2e-7 anywhere.  m is cut at 30, where Q is 0 in fp32, so that infinities give their limits.
-__device__ __forceinline__ float gelu(float x) {
-    const float m = fminf(fabsf(x), 30.0f);
-    const float t = fast_rcp(fmaf(0.36f, m, 1.0f));
-    float q = 0.047649674117565155f;
-    q = fmaf(q, t, -0.18179528415203094f);
-    q = fmaf(q, t, 0.18371888995170593f);
-    q = fmaf(q, t, 0.024642769247293472f);
-    q = fmaf(q, t, 0.14041736721992493f);
-    q = fmaf(q, t, 0.14164447784423828f);
-    q = fmaf(q, t, 0.14372217655181885f);
-    const float e = fast_exp2(m * m * -0.72134752044448170f);   // e^(-m^2 / 2)
-    return fmaf(-m * t * q, e, relu(x));
-}
-// x (1 + tanh u) / 2 = x / (1 + e^-2u), u = sqrt(2 / pi) (x + 0.044715 x^3)
-__device__ __forceinline__ float gelu_tanh(float x) {
-    const float v = x * fmaf(0.10294324f, x * x, 2.3022082f);   // 2 u log2(e)
-    const float r = fast_rcp(1.0f + fast_exp2(-v));
-    return x == -INFINITY ? 0.0f : x * r;
+__device__ __forceinline__ float2 gelu(float2 x) {
+    const float2 m = make_float2(fminf(fabsf(x.x), 30.0f), fminf(fabsf(x.y), 30.0f));
+    const float2 d = __ffma2_rn(both(0.36f), m, both(1.0f));
+    const float2 t = make_float2(fast_rcp(d.x), fast_rcp(d.y));
+    float2 q = __ffma2_rn(both(-0.047649674117565155f), t, both(0.18179528415203094f));   // -q: the sign goes with it
+    q = __ffma2_rn(q, t, both(-0.18371888995170593f));
+    q = __ffma2_rn(q, t, both(-0.024642769247293472f));
+    q = __ffma2_rn(q, t, both(-0.14041736721992493f));
+    q = __ffma2_rn(q, t, both(-0.14164447784423828f));
+    q = __ffma2_rn(q, t, both(-0.14372217655181885f));
+    const float2 a = __fmul2_rn(__fmul2_rn(m, both(-0.72134752044448170f)), m);
+    const float2 e = make_float2(fast_exp2(a.x), fast_exp2(a.y));   // e^(-m^2 / 2)
+    return __ffma2_rn(__fmul2_rn(__fmul2_rn(m, t), q), e, make_float2(relu(x.x), relu(x.y)));
 }
 
 // act: one of DR_ACT_*, the same for every thread of a launch
 template <int n>
 __device__ __forceinline__ void activate(float *v, int act) {
+    const auto each = [&](auto f) {
+#pragma unroll
+        for (int i = 0; i < n; i += 2) {
+            const float2 y = f(make_float2(v[i], v[i + 1]));
+            v[i] = y.x;
+            v[i + 1] = y.y;
+        }
+    };
     if (act == DR_ACT_GELU) {
-#pragma unroll
-        for (int i = 0; i < n; ++i) v[i] = gelu(v[i]);
+        each([](float2 x) { return gelu(x); });
     } else if (act == DR_ACT_SILU) {
-#pragma unroll
-        for (int i = 0; i < n; ++i) v[i] = silu(v[i]);
+        each([](float2 x) { return silu(x); });
     } else if (act == DR_ACT_GELU_TANH) {
-#pragma unroll
-        for (int i = 0; i < n; ++i) v[i] = gelu_tanh(v[i]);
+        each([](float2 x) { return gelu_tanh(x); });
     } else if (act == DR_ACT_RELU) {
-#pragma unroll
-        for (int i = 0; i < n; ++i) v[i] = relu(v[i]);
+        each([](float2 x) { return make_float2(relu(x.x), relu(x.y)); });
     }
 }
 
@@ -75,20 +88,32 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     return r;
 }
 
+// v[0 .. 8) += bias[i .. i+8); places from `have` on are left out.  bias is 16-byte aligned.
+__device__ __forceinline__ void add_bias8(float *v, const uint16_t *bias, int64_t i, int have) {
+    if (have >= 8 && i % 8 == 0) {
+        float f[8];
+        unpack8(ld_ro16(bias + i), f);
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+            const float2 y = __fadd2_rn(make_float2(v[j], v[j + 1]), make_float2(f[j], f[j + 1]));
+            v[j] = y.x;
+            v[j + 1] = y.y;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < have) v[j] += bf16_at(bias, i + j);
+    }
+}
+
 // Eight columns n .. n+7 (n a multiple of 8) of token t: bias, activation, gating and residual on the sums a (and b, the
 // sums of the rows that are multiplied in), stored to the output that holds them.  Columns from N on are left out.
 __device__ __forceinline__ void finish8(const LinearParams &p, int t, int n, float (&a)[8], float (&b)[8]) {
     const int have = min(8, p.N - n);
     if (have <= 0) return;
     if (p.bias) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < have) a[i] += bf16_at(p.bias, n + i);
-        if (p.gated) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i < have) b[i] += bf16_at(p.bias, (int64_t)p.N + n + i);
-        }
+        add_bias8(a, p.bias, n, have);
+        if (p.gated) add_bias8(b, p.bias, (int64_t)p.N + n, have);
     }
     activate<8>(a, p.act);
     if (p.gated) {

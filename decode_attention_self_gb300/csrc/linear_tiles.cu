@@ -7,32 +7,42 @@
 // 128 x 256 tile of its own would take.
 //   warp 0      TMA producer of its CTA's halves: 64-wide K chunks in a ring of kStages, counted on the first CTA's barrier
 //   warp 1      MMA issuer (first CTA only)
-//   warps 4-11  epilogue: warp w owns 32 tokens (tensor-memory lanes) and half of the tile's columns
+//   warps 2, 3  carriers, each for eight epilogue warps: bias and residual in, results out, by TMA
+//   warps 4-19  epilogue, in two sets of eight: bf16 outputs take the tiles in turn, 128 of a tile's sums per token and
+//               warp; fp32 outputs share each tile, 64 a warp
 // The sums of a tile take 256 of the 512 tensor-memory columns; the next tile is multiplied while the epilogue works on
-// the one before.  The epilogue goes through a 4 KB box per warp in shared memory (32 tokens of 128 bytes, 128-byte
-// swizzle): the residual's box comes in by TMA before the sums are ready, is added to in place and goes out by TMA, so
-// rows may end anywhere.  Outputs or residuals whose rows are not 16-byte aligned go between box and memory element by
-// element, a row of the box at a time.
+// the one before.  A tile of K = 1024 is multiplied in 8192 cycles, during which reading its operands and writing them by TMA
+// take all of shared memory's 128 bytes a cycle: whatever else goes through there costs the products time, and latencies
+// are long (a read of tensor memory 2000 cycles, a load of bias 1000, the fence between writing a box and its store 2000).
+// So an epilogue warp's results pass shared memory once, as a 4 KB box (32 tokens of 128 bytes, swizzled) that already
+// holds the residual; what takes long is done ahead or afterwards by the carriers; and the two sets are half a period apart.
+// Outputs or residuals whose rows are not 16-byte aligned are moved by the epilogue warps, a row of 32 columns at a time.
 // fp32 outputs: tensor-core chains drift by about 1e-9 K, so each 512 of K is a tile's sums of its own, added up in the
-// epilogue warps' registers (128 columns a thread).
+// epilogue warps' registers.
 // Every mbarrier wait is bounded; after one that runs out the pair's further tiles are not written, and copies and
 // products in flight are waited for before it exits.
+#include <type_traits>
+
 #include "dr_tc.cuh"
 #include "linear_epilogue.cuh"
 
 namespace dr {
 namespace {
 
-constexpr int kThreads = 384;
-constexpr int kEpiWarp = 4, kEpiWarps = 8;
+constexpr int kThreads = 640;
+constexpr int kEpiWarp = 4, kEpiWarps = 16;
+// Registers: the launch has 640 x 96; four warps give some of theirs to the other sixteen.
+constexpr int kLaunchRegs = 96, kOtherRegs = 32, kEpiRegs = 112;
+static_assert(kEpiWarp * 32 * kOtherRegs + kEpiWarps * 32 * kEpiRegs <= kThreads * kLaunchRegs, "more than the launch has");
 constexpr int kTileT = 256;       // tokens per pair
 constexpr int kTileW = 256;       // weight rows per pair (MMA N)
 constexpr int kStages = 5;
 constexpr int kHalf = 128 * 128;  // bytes of a CTA's tokens or weight rows in a stage
 constexpr int kBox = 32 * 128;    // bytes of an epilogue box
+constexpr int kCarrier = 2, kCarried = 8;   // first carrier warp, epilogue warps of each
 constexpr int kPieceChunks = 8;   // fp32 outputs: K of 512 per chain
 constexpr int kGroup = 8;         // token tiles that share their weight tiles' stay in L2
-constexpr size_t kSmem = 1024 + (size_t)kStages * 2 * kHalf + kEpiWarps * 2 * kBox;
+constexpr size_t kSmem = (size_t)kStages * 2 * kHalf + kEpiWarps * kBox + 2 * kTileW * sizeof(float) + 512;   // and Control
 
 struct TileArgs {
     LinearParams p;
@@ -50,10 +60,12 @@ struct Control {
     uint64_t empty[kStages];   // the products that read the stage are over
     uint64_t sums_full[2];     // a chain's sums are in tensor memory
     uint64_t sums_free[2];     // first CTA's: both CTAs' epilogue warps have read them
-    uint64_t res[kEpiWarps][2];
+    uint64_t box_ready[kEpiWarps];   // the box may be written, and holds the residual
+    uint64_t boxes_full[2];          // a carrier's boxes hold results
+    uint64_t bias_ready[2];
     uint64_t done;
     uint32_t tmem;
-    int gave_up;
+    int gave_up;   // some wait ran out
 };
 
 __device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank) {
@@ -84,9 +96,13 @@ __device__ __forceinline__ void box_store(const CUtensorMap *map, int x, int y, 
                  "r"(x), "r"(y), "r"(src)
                  : "memory");
 }
-template <int n>
-__device__ __forceinline__ void stores_read() {   // all but the last n box stores have read their boxes
-    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(n) : "memory");
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts16(uint32_t a, uint4 v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 __device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
     asm volatile(
@@ -105,162 +121,144 @@ __device__ __forceinline__ void pair_commit(uint64_t *bar) {
 __device__ __forceinline__ void remote_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ uint4 lds16(uint32_t a) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
-    return v;
-}
-__device__ __forceinline__ void sts16(uint32_t a, uint4 v) {
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-}
-
 // Tile i: groups of kGroup token tiles take all column tiles in turn, so that both operands' tiles stay in L2.
-__device__ __forceinline__ void tile_at(const TileArgs &a, int64_t i, int &tt, int &ct) {
-    const int64_t per_group = (int64_t)kGroup * a.col_tiles;
-    const int g = (int)(i / per_group);
-    const int r = (int)(i - g * per_group), n = min(kGroup, a.token_tiles - g * kGroup);
+__device__ __forceinline__ void tile_at(const TileArgs &a, int i, int &tt, int &ct) {
+    const int per_group = kGroup * a.col_tiles, g = i / per_group;
+    const int r = i - g * per_group, n = min(kGroup, a.token_tiles - g * kGroup);
     ct = r / n;
     tt = g * kGroup + (r - ct * n);
 }
 
-// 32 columns n .. n+31 of bias added to the sums; columns past `have` have none.
-__device__ __forceinline__ void add_bias(float *v, const uint16_t *bias, int64_t n, int have) {
-    if (have >= 32 && n % 8 == 0) {
+// The output that holds column n.
+__device__ __forceinline__ int out_of(const LinearParams &p, int n) {
+    int s = 0;
+    for (int i = 1; i < p.n_outs; ++i)
+        if (n >= p.out[i].col0) s = i;
+    return s;
+}
+
+// 16 bytes c of row `row` of a box with rows of 128 (64) bytes, as TMA's swizzle of that width lays them.
+template <bool kNarrow>
+__device__ __forceinline__ uint32_t box_chunk(uint32_t at, int row, int c) {
+    return kNarrow ? at + row * 64 + ((c ^ (row >> 1 & 3)) << 4) : at + row * 128 + ((c ^ (row & 7)) << 4);
+}
+
+// 32 results of this lane's token into its box, from 16-byte piece c0 on, added to what the box holds.
+template <bool kF32, bool kNarrow>
+__device__ __forceinline__ void put32(float *v, uint32_t at, int lane, int c0, bool add) {
+    if constexpr (kF32) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            float f[8];
-            unpack8(ld_ro16(bias + n + 8 * c), f);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[8 * c + j] += f[j];
+        for (int c = 0; c < 8; ++c) {
+            const uint32_t to = box_chunk<kNarrow>(at, lane, c);
+            float *u = v + 4 * c;
+            if (add) {
+                const uint4 r = lds16(to);
+                u[0] += __uint_as_float(r.x);
+                u[1] += __uint_as_float(r.y);
+                u[2] += __uint_as_float(r.z);
+                u[3] += __uint_as_float(r.w);
+            }
+            sts16(to, make_uint4(__float_as_uint(u[0]), __float_as_uint(u[1]), __float_as_uint(u[2]), __float_as_uint(u[3])));
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-            if (j < have) v[j] += lin::bf16_at(bias, n + j);
-    }
-}
-
-// Bias, activation and gating of 32 columns from n on.
-__device__ __forceinline__ void finish32(const LinearParams &p, float *a, float *b, int n) {
-    if (p.bias) {
-        add_bias(a, p.bias, n, p.N - n);
-        if (p.gated) add_bias(b, p.bias, (int64_t)p.N + n, p.N - n);
-    }
-    lin::activate<32>(a, p.act);
-    if (p.gated) {
+        for (int c = 0; c < 4; ++c) {
+            const uint32_t to = box_chunk<kNarrow>(at, lane, c0 + c);
+            float *u = v + 8 * c;
+            if (add) {
+                float f[8];
+                unpack8(lds16(to), f);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) a[j] *= b[j];
+                for (int j = 0; j < 8; ++j) u[j] += f[j];
+            }
+            sts16(to, make_uint4(lin::pack2(u[0], u[1]), lin::pack2(u[2], u[3]), lin::pack2(u[4], u[5]), lin::pack2(u[6], u[7])));
+        }
     }
 }
 
-// An epilogue warp's box of 32 tokens from t0 on and 128 bytes of columns from n on: residual in, sums added, out.
+// 32 columns n .. n+31 of a warp's 32 tokens between registers (lane = token) and rows that may start anywhere (lane =
+// column), through a box of 32 x 32 fp32 values, column c of row r at r * 32 + (c ^ r).
 template <bool kF32>
-struct Box {
-    static constexpr int kCols = kF32 ? 32 : 64;
-    const LinearParams &p;
-    const Maps &maps;
-    uint32_t at;   // 1024-byte aligned shared memory
-    int t0, n, lane;
+struct LooseRows {
+    using T = typename std::conditional<kF32, float, uint16_t>::type;
 
-    __device__ __forceinline__ uint32_t chunk(int row, int c) const { return at + row * 128 + ((c ^ (row & 7)) << 4); }
-
-    // element by element, for a residual without 16-byte rows
-    __device__ __forceinline__ void read_residual() const {
+    static __device__ __forceinline__ void add_residual(const LinearParams &p, float *v, float *box, int t0, int n, int lane) {
         const int rows = min(32, p.T - t0);
-        for (int r = 0; r < rows; ++r)
-            for (int c = lane; c < kCols && n + c < p.N; c += 32) {
-                const int64_t from = (int64_t)(t0 + r) * p.res_stride + n + c;
-                if constexpr (kF32) {
-                    const float v = static_cast<const float *>(p.residual)[from];
-                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(chunk(r, c >> 2) + (c & 3) * 4), "f"(v) : "memory");
-                } else {
-                    const uint16_t v = static_cast<const uint16_t *>(p.residual)[from];
-                    asm volatile("st.shared.u16 [%0], %1;" ::"r"(chunk(r, c >> 3) + (c & 7) * 2), "h"(v) : "memory");
-                }
+        const T *res = static_cast<const T *>(p.residual) + (int64_t)t0 * p.res_stride + n + lane;
+        for (int r = 0; r < rows; ++r, res += p.res_stride)
+            if (n + lane < p.N) {
+                if constexpr (kF32) box[r * 32 + (lane ^ r)] = *res;
+                else box[r * 32 + (lane ^ r)] = __uint_as_float((uint32_t)*res << 16);
             }
         __syncwarp();
-    }
-    // columns c0 .. c0+31 of this thread's token
-    __device__ __forceinline__ void put32(float *v, int c0) const {
-        if constexpr (kF32) {
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                const uint32_t to = chunk(lane, c);
-                if (p.residual) {
-                    const uint4 r = lds16(to);
-                    v[4 * c] += __uint_as_float(r.x);
-                    v[4 * c + 1] += __uint_as_float(r.y);
-                    v[4 * c + 2] += __uint_as_float(r.z);
-                    v[4 * c + 3] += __uint_as_float(r.w);
-                }
-                sts16(to, make_uint4(__float_as_uint(v[4 * c]), __float_as_uint(v[4 * c + 1]), __float_as_uint(v[4 * c + 2]),
-                                     __float_as_uint(v[4 * c + 3])));
-            }
-        } else {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const uint32_t to = chunk(lane, c0 / 8 + c);
-                float *u = v + 8 * c;
-                if (p.residual) {
-                    float f[8];
-                    unpack8(lds16(to), f);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) u[j] += f[j];
-                }
-                sts16(to, make_uint4(lin::pack2(u[0], u[1]), lin::pack2(u[2], u[3]), lin::pack2(u[4], u[5]),
-                                     lin::pack2(u[6], u[7])));
-            }
-        }
-    }
-    __device__ __forceinline__ void store() const {
-        int s = 0;
-        for (int i = 1; i < p.n_outs; ++i)
-            if (n >= p.out[i].col0) s = i;
-        const LinearOut &o = p.out[s];
-        const int col = n - o.col0;
-        if (p.vec_out) {
-            tc::fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) {
-                if (t0 < p.T && col < o.cols) box_store(&maps.out[s], col, t0, at);
-                asm volatile("cp.async.bulk.commit_group;" ::: "memory");   // one group per box, if empty
-            }
-            return;
-        }
+        for (int c = 0; c < 32; ++c) v[c] += box[lane * 32 + (c ^ lane)];   // rows and columns past the end hold anything
         __syncwarp();
-        const int rows = min(32, p.T - t0);
-        for (int r = 0; r < rows; ++r)
-            for (int c = lane; c < kCols && col + c < o.cols; c += 32) {
-                const int64_t to = (int64_t)(t0 + r) * o.stride + col + c;
-                if constexpr (kF32) {
-                    float v;
-                    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(chunk(r, c >> 2) + (c & 3) * 4) : "memory");
-                    static_cast<float *>(o.ptr)[to] = v;
-                } else {
-                    uint16_t v;
-                    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(chunk(r, c >> 3) + (c & 7) * 2) : "memory");
-                    static_cast<uint16_t *>(o.ptr)[to] = v;
-                }
+    }
+    static __device__ __forceinline__ void store(const LinearParams &p, const float *v, float *box, int t0, int n, int lane) {
+#pragma unroll
+        for (int c = 0; c < 32; ++c) box[lane * 32 + (c ^ lane)] = v[c];
+        __syncwarp();
+        const LinearOut &o = p.out[out_of(p, n)];   // the 32 columns lie in one output
+        const int rows = min(32, p.T - t0), col = n - o.col0 + lane;
+        T *to = static_cast<T *>(o.ptr) + (int64_t)t0 * o.stride + col;
+        for (int r = 0; r < rows; ++r, to += o.stride)
+            if (col < o.cols) {
+                const float x = box[r * 32 + (lane ^ r)];
+                if constexpr (kF32) *to = x;
+                else *to = f32_to_bf16_rn(x);
             }
         __syncwarp();
     }
 };
 
+// Which tiles and columns an epilogue warp takes.  bf16: the tiles of its set, half of the columns in two passes; fp32: all
+// tiles, a quarter of the columns.
+template <bool kF32>
+struct Share {
+    int first, step;   // tiles
+    int col0, cols;    // columns of the first pass, and of each
+    static constexpr int kPasses = kF32 ? 1 : 2;
+    __device__ __forceinline__ Share(int e, int first_tile, int tile_step, int tile_cols) {
+        const int set = e / kCarried, part = e >> 2;
+        first = kF32 ? first_tile : first_tile + set * tile_step;
+        step = kF32 ? tile_step : 2 * tile_step;
+        cols = tile_cols / 4;
+        col0 = kF32 ? part * cols : (part & 1) * 2 * cols;
+    }
+};
+
+__device__ __forceinline__ void add_bias32(float *v, const float *bias) {
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+        const float4 b = *reinterpret_cast<const float4 *>(bias + j);
+        const float2 x = __fadd2_rn(make_float2(v[j], v[j + 1]), make_float2(b.x, b.y)),
+                     y = __fadd2_rn(make_float2(v[j + 2], v[j + 3]), make_float2(b.z, b.w));
+        v[j] = x.x;
+        v[j + 1] = x.y;
+        v[j + 2] = y.x;
+        v[j + 3] = y.y;
+    }
+}
+
 template <bool kF32>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ TileArgs args) {
-    extern __shared__ uint8_t smem_raw[];
-    __shared__ Control ctl;
+    extern __shared__ __align__(1024) uint8_t smem[];   // all there is: nothing in front of it
+    static_assert(sizeof(Control) <= 512, "kSmem");
+    Control &ctl = *reinterpret_cast<Control *>(smem + kSmem - 512);
 
     const LinearParams &p = args.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = blockIdx.x & 1;   // the cluster's first CTA issues the products of both
-    const int64_t tiles = (int64_t)args.token_tiles * args.col_tiles;
-    const int64_t first = blockIdx.x / 2, step = gridDim.x / 2;
-    const uint32_t ring = (tc::smem_u32(smem_raw) + 1023) & ~1023u;
+    const int tiles = args.token_tiles * args.col_tiles, first = blockIdx.x / 2, step = gridDim.x / 2;
+    const uint32_t ring = tc::smem_u32(smem);
     const uint32_t sx = ring, sw = ring + kStages * kHalf, boxes = ring + 2 * kStages * kHalf;
+    float *const bias = reinterpret_cast<float *>(smem + 2 * kStages * kHalf + kEpiWarps * kBox);   // two tiles' sums'
     const int tile_cols = p.gated ? kTileW / 2 : kTileW;
     volatile int *gave_up = &ctl.gave_up;
+    // whole 16-byte pieces of rows: boxes carried by TMA
+    const bool boxed = p.vec_out && (!p.residual || p.vec_res);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -269,10 +267,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             tc::mbar_init(&ctl.sums_full[b], 1);
-            tc::mbar_init(&ctl.sums_free[b], 2 * kEpiWarps);
+            tc::mbar_init(&ctl.sums_free[b], 2 * (kF32 ? kEpiWarps : kCarried));
+            tc::mbar_init(&ctl.boxes_full[b], kCarried);
+            tc::mbar_init(&ctl.bias_ready[b], 1);
         }
-        for (int w = 0; w < kEpiWarps; ++w)
-            for (int b = 0; b < 2; ++b) tc::mbar_init(&ctl.res[w][b], 1);
+        for (int w = 0; w < kEpiWarps; ++w) tc::mbar_init(&ctl.box_ready[w], 1);
         tc::mbar_init(&ctl.done, 1);
         ctl.gave_up = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -289,223 +288,239 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = ctl.tmem;
     pdl_wait();
 
-    if (warp == 0) {
-        int s = 0, r = 0;
-        unsigned armed = 0;   // stages whose copies were issued, and how often (parity of the last)
-        unsigned parity = 0;
-        bool ok = true;
-        for (int64_t i = first; ok && i < tiles; i += step) {
-            int tt, ct;
-            tile_at(args, i, tt, ct);
-            const int t = tt * kTileT + (int)rank * 128;
-            // rows of W: the pair's 256 in halves, or 128 and those that multiply them
-            const int w = p.gated ? (int)rank * p.N + ct * tile_cols : ct * tile_cols + (int)rank * 128;
-            for (int c = 0; c < args.chunks; ++c) {
-                if (!(c == 0 && i == p.stall_tile)) {
-                    if (r > 0 && !tc::mbar_wait(&ctl.empty[s], (r - 1) & 1, gave_up)) {
-                        ok = false;
-                        break;
+    if (warp < kEpiWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (warp == 0) {
+            int s = 0, r = 0;
+            unsigned armed = 0;   // stages whose copies were issued, and how often (parity of the last)
+            unsigned parity = 0;
+            bool ok = true;
+            for (int i = first; ok && i < tiles; i += step) {
+                int tt, ct;
+                tile_at(args, i, tt, ct);
+                const int t = tt * kTileT + (int)rank * 128;
+                // rows of W: the pair's 256 in halves, or 128 and those that multiply them
+                const int w = p.gated ? (int)rank * p.N + ct * tile_cols : ct * tile_cols + (int)rank * 128;
+                for (int c = 0; c < args.chunks; ++c) {
+                    if (!(c == 0 && i == p.stall_tile)) {
+                        if (r > 0 && !tc::mbar_wait(&ctl.empty[s], (r - 1) & 1, gave_up)) {
+                            ok = false;
+                            break;
+                        }
+                        if (tc::elect_one()) {
+                            const uint32_t bar = mapa(tc::smem_u32(&ctl.full[s]), 0);
+                            if (rank == 0) tc::mbar_expect_tx(&ctl.full[s], 4 * kHalf);
+                            pair_load(sx + s * kHalf, &maps.x, c * 64, t, bar);
+                            pair_load(sw + s * kHalf, &maps.w, c * 64, w, bar);
+                        }
+                        __syncwarp();
+                        armed |= 1u << s;
+                        parity = (parity & ~(1u << s)) | ((unsigned)(r & 1) << s);
                     }
-                    if (tc::elect_one()) {
-                        const uint32_t bar = mapa(tc::smem_u32(&ctl.full[s]), 0);
-                        if (rank == 0) tc::mbar_expect_tx(&ctl.full[s], 4 * kHalf);
-                        pair_load(sx + s * kHalf, &maps.x, c * 64, t, bar);
-                        pair_load(sw + s * kHalf, &maps.w, c * 64, w, bar);
-                    }
-                    __syncwarp();
-                    armed |= 1u << s;
-                    parity = (parity & ~(1u << s)) | ((unsigned)(r & 1) << s);
-                }
-                if (++s == kStages) {
-                    s = 0;
-                    ++r;
-                }
-            }
-        }
-        pdl_trigger();
-        if (!ok) {
-            if (lane == 0) flag_error(p.err, DR_ERRF_TIMEOUT);
-            // both CTAs' copies count on the first CTA's barriers; the second waits for it at the end
-            if (rank == 0)
-                for (int k = 0; k < kStages; ++k)
-                    if (armed >> k & 1) tc::mbar_drain(&ctl.full[k], parity >> k & 1);
-        }
-    } else if (warp == 1 && rank == 0) {
-        const uint32_t idesc = tc::instr_desc(kTileT, kTileW, false, false);
-        const uint64_t dx = tc::smem_desc(sx), dw = tc::smem_desc(sw);
-        int s = 0, r = 0;
-        int64_t chain = 0;
-        bool ok = true;
-        for (int64_t i = first; ok && i < tiles; i += step) {
-            for (int c = 0; ok && c < args.chunks; ++chain) {
-                const int b = (int)(chain & 1);
-                if (chain >= 2 && !tc::mbar_wait(&ctl.sums_free[b], (unsigned)((chain >> 1) - 1) & 1, gave_up)) {
-                    ok = false;
-                    break;
-                }
-                tc::fence_after();
-                const uint32_t d = tmem + b * kTileW;
-                const int end = min(args.chunks, c + args.piece_chunks);
-                for (int c0 = c; c < end; ++c) {
-                    if (!tc::mbar_wait(&ctl.full[s], r & 1, gave_up)) {
-                        ok = false;
-                        break;
-                    }
-                    tc::fence_after();
-                    if (tc::elect_one()) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            pair_mma(d, tc::desc_at(dx, s * kHalf + k * 32), tc::desc_at(dw, s * kHalf + k * 32), idesc,
-                                     c > c0 || k > 0);
-                        pair_commit(&ctl.empty[s]);
-                        if (c + 1 == end) pair_commit(&ctl.sums_full[b]);
-                    }
-                    __syncwarp();
                     if (++s == kStages) {
                         s = 0;
                         ++r;
                     }
                 }
             }
-        }
-        if (!ok) {
-            if (lane == 0) flag_error(p.err, DR_ERRF_TIMEOUT);
-            if (tc::elect_one()) pair_commit(&ctl.done);
+            pdl_trigger();
+            if (!ok) {
+                if (lane == 0) flag_error(p.err, DR_ERRF_TIMEOUT);
+                // both CTAs' copies count on the first CTA's barriers; the second waits for it at the end
+                if (rank == 0)
+                    for (int k = 0; k < kStages; ++k)
+                        if (armed >> k & 1) tc::mbar_drain(&ctl.full[k], parity >> k & 1);
+            }
+        } else if (warp == 1 && rank == 0) {
+            const uint32_t idesc = tc::instr_desc(kTileT, kTileW, false, false);
+            const uint64_t dx = tc::smem_desc(sx), dw = tc::smem_desc(sw);
+            int s = 0, r = 0;
+            unsigned chain = 0;
+            bool ok = true;
+            for (int i = first; ok && i < tiles; i += step) {
+                for (int c = 0; ok && c < args.chunks; ++chain) {
+                    const int b = (int)(chain & 1);
+                    if (chain >= 2 && !tc::mbar_wait(&ctl.sums_free[b], ((chain >> 1) - 1) & 1, gave_up)) {
+                        ok = false;
+                        break;
+                    }
+                    tc::fence_after();
+                    const uint32_t d = tmem + b * kTileW;
+                    const int end = min(args.chunks, c + args.piece_chunks);
+                    for (int c0 = c; c < end; ++c) {
+                        if (!tc::mbar_wait(&ctl.full[s], r & 1, gave_up)) {
+                            ok = false;
+                            break;
+                        }
+                        tc::fence_after();
+                        if (tc::elect_one()) {
+    #pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                pair_mma(d, tc::desc_at(dx, s * kHalf + k * 32), tc::desc_at(dw, s * kHalf + k * 32), idesc,
+                                         c > c0 || k > 0);
+                            pair_commit(&ctl.empty[s]);
+                            if (c + 1 == end) pair_commit(&ctl.sums_full[b]);
+                        }
+                        __syncwarp();
+                        if (++s == kStages) {
+                            s = 0;
+                            ++r;
+                        }
+                    }
+                }
+            }
+            if (!ok) {
+                if (lane == 0) flag_error(p.err, DR_ERRF_TIMEOUT);
+                if (tc::elect_one()) pair_commit(&ctl.done);
+                __syncwarp();
+                tc::mbar_drain(&ctl.done, 0);
+            }
+        } else if (warp >= kCarrier) {
+            const int set = warp - kCarrier, e = set * kCarried + (lane & (kCarried - 1));
+            const bool mine = lane < kCarried;   // a lane per box
+            const Share<kF32> share(e, first, step, tile_cols);
+            const uint32_t at = boxes + e * kBox;
+            const int uses = kF32 && !p.gated ? 2 : Share<kF32>::kPasses;   // boxes per tile and warp
+            const int use_cols = kF32 ? 32 : share.cols;
+            float *const to = bias + set * kTileW;
+            unsigned phase = 0;
+            bool ok = true;
+            for (int i = share.first; ok && i < tiles; i += share.step) {
+                int tt, ct;
+                tile_at(args, i, tt, ct);
+                const int n0 = ct * tile_cols;
+                if (p.bias) {   // the tile before is done with it
+                    for (int j = lane; j < kTileW; j += 32) {
+                        const int n = n0 + (j & (tile_cols - 1));
+                        to[j] = n < p.N ? lin::bf16_at(p.bias, j < tile_cols ? n : (int64_t)p.N + n) : 0.f;
+                    }
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&ctl.bias_ready[set]);
+                }
+                for (int u = 0; u < uses; ++u, phase ^= 1) {
+                    const int t0 = tt * kTileT + (int)rank * 128 + (e & 3) * 32, n = n0 + share.col0 + u * use_cols;
+                    if (mine && boxed) {
+                        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");   // the store before has read the box
+                        if (p.residual) {
+                            tc::mbar_expect_tx(&ctl.box_ready[e], !kF32 && p.gated ? kBox / 2 : kBox);
+                            own_load(at, &maps.res, n, t0, &ctl.box_ready[e]);
+                        } else {
+                            tc::mbar_arrive(&ctl.box_ready[e]);
+                        }
+                    }
+                    __syncwarp();
+                    ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(&ctl.boxes_full[set], phase, gave_up));
+                    if (!ok) break;
+                    tc::fence_proxy_async();   // what the epilogue warps wrote, for the stores below
+                    if (mine && boxed) {
+                        const int s = out_of(p, n);
+                        if (t0 < p.T && n - p.out[s].col0 < p.out[s].cols) box_store(&maps.out[s], n - p.out[s].col0, t0, at);
+                        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                    }
+                    __syncwarp();
+                }
+            }
+            if (!ok) {
+                if (lane == 0) flag_error(p.err, DR_ERRF_TIMEOUT);
+                if (boxed && p.residual)
+                    for (int k = 0; k < kCarried; ++k) tc::mbar_drain(&ctl.box_ready[set * kCarried + k], phase);   // on their way
+            }
+            if (mine) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
             __syncwarp();
-            tc::mbar_drain(&ctl.done, 0);
         }
-    } else if (warp >= kEpiWarp) {
-        const int e = warp - kEpiWarp, quad = warp & 3, half = e >> 2;
-        constexpr int kCols = Box<kF32>::kCols;
-        const int n_boxes = tile_cols / 2 / kCols;   // of this warp
-        const bool res_tma = p.residual && p.vec_res;
-        const uint32_t my_boxes = boxes + e * 2 * kBox;
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
+        const int e = warp - kEpiWarp, set = e / kCarried, quad = warp & 3;
+        const Share<kF32> share(e, first, step, tile_cols);
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-        unsigned res_asked = 0, res_odd = 0;   // per buffer: whether a residual box was asked for, and an odd number of times
+        const int pieces = kF32 ? (args.chunks + args.piece_chunks - 1) / args.piece_chunks : 1;
+        const uint32_t box = boxes + e * kBox;
+        float *const loose = reinterpret_cast<float *>(smem + (box - ring));
+        unsigned chain = kF32 ? 0 : set, box_phase = 0, bias_phase = 0;   // bf16: a set has the even or the odd chains
         bool ok = true;
-        int64_t chain = 0;
-        for (int64_t i = first; ok && i < tiles; i += step) {
+        for (int i = share.first; ok && i < tiles; i += share.step) {
             int tt, ct;
             tile_at(args, i, tt, ct);
-            Box<kF32> box{p, maps, my_boxes, tt * kTileT + (int)rank * 128 + quad * 32, 0, lane};
-            const int n0 = ct * tile_cols + half * (tile_cols / 2);
-            const auto ask_residual = [&](int k) {
-                if (lane == 0) {
-                    tc::mbar_expect_tx(&ctl.res[e][k & 1], kBox);
-                    own_load(my_boxes + (k & 1) * kBox, &maps.res, n0 + k * kCols, box.t0, &ctl.res[e][k & 1]);
-                }
-                res_asked |= 1u << (k & 1);
-                res_odd ^= 1u << (k & 1);
-            };
-            if (lane == 0) stores_read<0>();
-            __syncwarp();
-            if (res_tma)
-                for (int k = 0; k < 2 && k < n_boxes; ++k) ask_residual(k);
-            float acc[kF32 ? 128 : 1];
-            uint32_t sums = 0;
-            if constexpr (kF32) {
-                // thread's columns: 128 of the tile, or 64 and the 64 that multiply them
-                const int pieces = (args.chunks + args.piece_chunks - 1) / args.piece_chunks;
-                for (int k = 0; k < pieces; ++k, ++chain) {
-                    const int b = (int)(chain & 1);
-                    ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(&ctl.sums_full[b], (unsigned)(chain >> 1) & 1, gave_up));
+            const int t0 = tt * kTileT + (int)rank * 128 + quad * 32;
+#pragma unroll 1
+            for (int pass = 0; ok && pass < Share<kF32>::kPasses; ++pass) {
+                const int col = share.col0 + pass * share.cols;                    // its columns of the tile,
+                const int other = p.gated ? kTileW / 2 + col : col + 32;           // and where its second 32 sums are
+                float acc[64];
+                for (int k = 0; k < pieces; ++k) {
+                    ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(&ctl.sums_full[chain & 1], (chain >> 1) & 1, gave_up));
                     if (!ok) break;
                     tc::fence_after();
-                    const uint32_t from = tmem + lanes + b * kTileW;
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const int col = p.gated ? (q >> 1) * 128 + half * 64 + (q & 1) * 32 : half * 128 + q * 32;
-                        if (k == 0) {
-                            tc::ld32(from + col, acc + 32 * q);
-                        } else {
-                            float more[32];
-                            tc::ld32(from + col, more);
-                            tc::wait_ld();
-                            tc::pin32(more);
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) acc[32 * q + j] += more[j];
-                        }
-                    }
-                    tc::wait_ld();
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) tc::pin32(acc + 32 * q);
-                    tc::fence_before();
-                    __syncwarp();
-                    if (lane == 0) remote_arrive(mapa(tc::smem_u32(&ctl.sums_free[b]), 0));
-                }
-                if (!ok) break;
-            } else {
-                const int b = (int)(chain & 1);
-                ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(&ctl.sums_full[b], (unsigned)(chain >> 1) & 1, gave_up));
-                if (!ok) break;
-                tc::fence_after();
-                sums = tmem + lanes + b * kTileW;
-            }
-            const auto begin_box = [&](int k) {
-                box.at = my_boxes + (k & 1) * kBox;
-                box.n = n0 + k * kCols;
-                if (k >= 2 && !res_tma) {   // the box's store two boxes ago has read it
-                    if (lane == 0) stores_read<1>();
-                    __syncwarp();
-                }
-                if (res_tma) {
-                    ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(&ctl.res[e][k & 1], ~(res_odd >> (k & 1)) & 1, gave_up));
-                } else if (p.residual) {
-                    box.read_residual();
-                }
-            };
-            const auto end_box = [&](int k) {
-                box.store();
-                if (res_tma && k + 2 < n_boxes) {
-                    if (lane == 0) stores_read<0>();
-                    __syncwarp();
-                    ask_residual(k + 2);
-                }
-            };
-            if constexpr (kF32) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if (k >= n_boxes) break;
-                    begin_box(k);
-                    if (!ok) break;
-                    finish32(p, acc + 32 * k, acc + (32 * k + 64) % 128, box.n);
-                    box.put32(acc + 32 * k, 0);
-                    end_box(k);
-                }
-            } else {
-#pragma unroll 1
-                for (int k = 0; k < n_boxes; ++k) {
-                    begin_box(k);
-                    if (!ok) break;
-#pragma unroll 1
-                    for (int c0 = 0; c0 < 64; c0 += 32) {
-                        const int col = half * (tile_cols / 2) + k * kCols + c0;
-                        float a[32], g[32];
-                        tc::ld32(sums + col, a);
-                        if (p.gated) tc::ld32(sums + 128 + col, g);
+                    const uint32_t from = tmem + lanes + (chain & 1) * kTileW;
+                    if (!kF32 || k == 0) {
+                        tc::ld32(from + col, acc);
+                        tc::ld32(from + other, acc + 32);
                         tc::wait_ld();
-                        tc::pin32(a);
-                        if (p.gated) tc::pin32(g);
-                        if (k + 1 == n_boxes && c0 == 32) {   // the last sums are read: the next tile may have their place
-                            tc::fence_before();
-                            __syncwarp();
-                            if (lane == 0) remote_arrive(mapa(tc::smem_u32(&ctl.sums_free[chain & 1]), 0));
+                        tc::pin32(acc);
+                        tc::pin32(acc + 32);
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            float more[16];
+                            tc::ld16(from + (q < 2 ? col : other) + (q & 1) * 16, more);
+                            tc::wait_ld();
+                            tc::pin16(more);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) acc[16 * q + j] += more[j];
                         }
-                        finish32(p, a, g, box.n + c0);
-                        box.put32(a, c0);
                     }
-                    end_box(k);
+                    if (kF32 || pass == 1) {   // this warp has its sums: the place may have another tile's
+                        tc::fence_before();
+                        __syncwarp();
+                        if (lane == 0) remote_arrive(mapa(tc::smem_u32(&ctl.sums_free[chain & 1]), 0));
+                        chain += kF32 ? 1 : 2;
+                    }
                 }
-                ++chain;
+                if (!ok) break;
+                if (p.bias && pass == 0) {
+                    ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(&ctl.bias_ready[set], bias_phase, gave_up));
+                    if (!ok) break;
+                    bias_phase ^= 1;
+                }
+                // 32 columns at a time, the second 32 moved to the first ones' registers: one copy of the code
+#pragma unroll 1
+                for (int c0 = 0;; c0 += 32) {
+                    if (p.bias) {
+                        const float *b = bias + set * kTileW;
+                        add_bias32(acc, b + col + c0);
+                        if (p.gated) add_bias32(acc + 32, b + other);
+                    }
+                    lin::activate<32>(acc, p.act);
+                    if (p.gated) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) acc[j] *= acc[32 + j];
+                    }
+                    const bool last = c0 + 32 == share.cols;
+                    if (boxed) {
+                        if (kF32 || c0 == 0) {
+                            ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(&ctl.box_ready[e], box_phase, gave_up));
+                            if (!ok) break;
+                            box_phase ^= 1;
+                        }
+                        if (!kF32 && p.gated) put32<kF32, true>(acc, box, lane, 0, p.residual);
+                        else put32<kF32, false>(acc, box, lane, c0 / 8, p.residual);
+                    } else {
+                        const int n = ct * tile_cols + col + c0;
+                        if (n < p.N) {
+                            if (p.residual) LooseRows<kF32>::add_residual(p, acc, loose, t0, n, lane);
+                            LooseRows<kF32>::store(p, acc, loose, t0, n, lane);
+                        }
+                    }
+                    if (kF32 || last) {
+                        __syncwarp();
+                        if (lane == 0) tc::mbar_arrive(&ctl.boxes_full[set]);
+                    }
+                    if (last) break;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) acc[j] = acc[32 + j];
+                }
             }
         }
-        if (!ok) {
-            if (lane == 0) flag_error(p.err, DR_ERRF_TIMEOUT);
-            for (int b = 0; b < 2; ++b)   // residual boxes still on their way
-                if (res_asked >> b & 1) tc::mbar_drain(&ctl.res[e][b], ~(res_odd >> b) & 1);
-        }
-        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-        __syncwarp();
     }
     __syncwarp();
     tc::fence_before();
@@ -547,9 +562,9 @@ cudaError_t most_pairs(int sms, int *pairs) {
     return cudaSuccess;
 }
 
-// Tensor map of an output or residual: boxes of 32 tokens and 128 bytes.
-bool encode_box(CUtensorMap *map, const void *ptr, int64_t T, int cols, int64_t stride, bool f32) {
-    return encode_matrix(map, ptr, f32, T, cols, stride, 32, f32 ? 32 : 64);
+// Tensor map of an output or residual: boxes of 32 tokens.
+bool encode_box(CUtensorMap *map, const void *ptr, const LinearParams &p, int cols, int64_t stride) {
+    return encode_matrix(map, ptr, p.out_f32, p.T, cols, stride, 32, p.out_f32 || p.gated ? 32 : 64);
 }
 
 template <bool kF32>
@@ -565,16 +580,18 @@ cudaError_t launch(const LinearParams &p, int sms, cudaStream_t stream) {
     if (!encode_matrix(&m.x, p.x, false, p.T, p.K, p.x_stride, 128, 64) ||
         !encode_matrix(&m.w, p.W, false, (int64_t)p.N * (p.gated ? 2 : 1), p.K, p.K, 128, 64))
         return cudaErrorInvalidValue;
+    // maps that the kernel does not use stay copies
     m.res = m.x;
     for (int i = 0; i < DR_LINEAR_MAX_OUTS; ++i) m.out[i] = m.x;
     if (p.vec_out)
         for (int i = 0; i < p.n_outs; ++i)
-            if (!encode_box(&m.out[i], p.out[i].ptr, p.T, p.out[i].cols, p.out[i].stride, kF32)) return cudaErrorInvalidValue;
-    if (p.vec_res && !encode_box(&m.res, p.residual, p.T, p.N, p.res_stride, kF32)) return cudaErrorInvalidValue;
+            if (!encode_box(&m.out[i], p.out[i].ptr, p, p.out[i].cols, p.out[i].stride)) return cudaErrorInvalidValue;
+    if (p.vec_res && !encode_box(&m.res, p.residual, p, p.N, p.res_stride)) return cudaErrorInvalidValue;
     int pairs = 0;
     const cudaError_t e = most_pairs<kF32>(sms, &pairs);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (int64_t)a.token_tiles * a.col_tiles;
+    if (tiles > 0x3FFFFFFF) return cudaErrorInvalidValue;   // tiles are counted in 32 bits: 2^46 outputs
     if (tiles < pairs) pairs = (int)tiles;
     return launch_kernel(linear_tiles_kernel<kF32>, dim3((unsigned)(2 * pairs)), dim3(kThreads), kSmem, stream, 2, m, a);
 }
