@@ -435,89 +435,103 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
         const int pieces = kF32 ? (args.chunks + args.piece_chunks - 1) / args.piece_chunks : 1;
         const uint32_t box = boxes + e * kBox;
-        float *const loose = reinterpret_cast<float *>(smem + (box - ring));
         unsigned chain = kF32 ? 0 : set, box_phase = 0, bias_phase = 0;   // bf16: a set has the even or the odd chains
         bool ok = true;
+        const int blocks = (kF32 ? 1 : 2) * (p.gated ? 1 : 2);   // of 32 output columns
+        const int apart = p.gated ? kTileW / 2 : 32;             // from a block's sums to those that multiply it, or the next block's
+        const auto release = [&] {   // this warp has its sums: the place may have another tile's
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) remote_arrive(mapa(tc::smem_u32(&ctl.sums_free[chain & 1]), 0));
+            chain += kF32 ? 1 : 2;
+        };
         for (int i = share.first; ok && i < tiles; i += share.step) {
-            int tt, ct;
-            tile_at(args, i, tt, ct);
-            const int t0 = tt * kTileT + (int)rank * 128 + quad * 32;
-#pragma unroll 1
-            for (int pass = 0; ok && pass < Share<kF32>::kPasses; ++pass) {
-                const int col = share.col0 + pass * share.cols;                    // its columns of the tile,
-                const int other = p.gated ? kTileW / 2 + col : col + 32;           // and where its second 32 sums are
-                float acc[64];
-                for (int k = 0; k < pieces; ++k) {
-                    ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(&ctl.sums_full[chain & 1], (chain >> 1) & 1, gave_up));
-                    if (!ok) break;
-                    tc::fence_after();
-                    const uint32_t from = tmem + lanes + (chain & 1) * kTileW;
-                    if (!kF32 || k == 0) {
-                        tc::ld32(from + col, acc);
-                        tc::ld32(from + other, acc + 32);
-                        tc::wait_ld();
-                        tc::pin32(acc);
-                        tc::pin32(acc + 32);
-                    } else {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            float more[16];
-                            tc::ld16(from + (q < 2 ? col : other) + (q & 1) * 16, more);
-                            tc::wait_ld();
-                            tc::pin16(more);
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) acc[16 * q + j] += more[j];
-                        }
-                    }
-                    if (kF32 || pass == 1) {   // this warp has its sums: the place may have another tile's
-                        tc::fence_before();
-                        __syncwarp();
-                        if (lane == 0) remote_arrive(mapa(tc::smem_u32(&ctl.sums_free[chain & 1]), 0));
-                        chain += kF32 ? 1 : 2;
-                    }
-                }
+            float acc[64];
+            uint32_t from = 0;
+            for (int k = 0; k < pieces; ++k) {
+                ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(&ctl.sums_full[chain & 1], (chain >> 1) & 1, gave_up));
                 if (!ok) break;
-                if (p.bias && pass == 0) {
-                    ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(&ctl.bias_ready[set], bias_phase, gave_up));
-                    if (!ok) break;
-                    bias_phase ^= 1;
-                }
-                // 32 columns at a time, the second 32 moved to the first ones' registers: one copy of the code
-#pragma unroll 1
-                for (int c0 = 0;; c0 += 32) {
-                    if (p.bias) {
-                        const float *b = bias + set * kTileW;
-                        add_bias32(acc, b + col + c0);
-                        if (p.gated) add_bias32(acc + 32, b + other);
-                    }
-                    lin::activate<32>(acc, p.act);
-                    if (p.gated) {
+                tc::fence_after();
+                from = tmem + lanes + (chain & 1) * kTileW + share.col0;
+                if (!kF32 || k == 0) {
+                    tc::ld32(from, acc);
+                    tc::ld32(from + apart, acc + 32);
+                    tc::wait_ld();
+                    tc::pin32(acc);
+                    tc::pin32(acc + 32);
+                } else {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) acc[j] *= acc[32 + j];
+                    for (int q = 0; q < 4; ++q) {
+                        float more[16];
+                        tc::ld16(from + (q < 2 ? 0 : apart) + (q & 1) * 16, more);
+                        tc::wait_ld();
+                        tc::pin16(more);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) acc[16 * q + j] += more[j];
                     }
-                    const bool last = c0 + 32 == share.cols;
-                    if (boxed) {
-                        if (kF32 || c0 == 0) {
-                            ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(&ctl.box_ready[e], box_phase, gave_up));
-                            if (!ok) break;
-                            box_phase ^= 1;
-                        }
-                        if (!kF32 && p.gated) put32<kF32, true>(acc, box, lane, 0, p.residual);
-                        else put32<kF32, false>(acc, box, lane, c0 / 8, p.residual);
-                    } else {
-                        const int n = ct * tile_cols + col + c0;
-                        if (n < p.N) {
-                            if (p.residual) LooseRows<kF32>::add_residual(p, acc, loose, t0, n, lane);
-                            LooseRows<kF32>::store(p, acc, loose, t0, n, lane);
-                        }
+                }
+                if (kF32) release();
+            }
+            if (!ok) break;
+            if (p.bias) {
+                ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(&ctl.bias_ready[set], bias_phase, gave_up));
+                if (!ok) break;
+                bias_phase ^= 1;
+            }
+            const float *b = bias + set * kTileW + share.col0;
+            // One copy of the code for all blocks: the next block's sums move to the first registers, and the one after it
+            // is read behind them while this one is worked on.
+#pragma unroll 1
+            for (int k = 0;; ++k, b += 32) {
+                if (p.bias) {
+                    add_bias32(acc, b);
+                    if (p.gated) add_bias32(acc + 32, b + apart);
+                }
+                lin::activate<32>(acc, p.act);
+                if (p.gated) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) acc[j] *= acc[32 + j];
+                }
+                const bool opens = kF32 || p.gated || k % 2 == 0, closes = kF32 || p.gated || k % 2 == 1;   // a box
+                if (boxed) {
+                    if (opens) {
+                        ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(&ctl.box_ready[e], box_phase, gave_up));
+                        if (!ok) break;
+                        box_phase ^= 1;
                     }
-                    if (kF32 || last) {
-                        __syncwarp();
-                        if (lane == 0) tc::mbar_arrive(&ctl.boxes_full[set]);
+                    if (!kF32 && p.gated) put32<kF32, true>(acc, box, lane, 0, p.residual);
+                    else put32<kF32, false>(acc, box, lane, opens ? 0 : 4, p.residual);
+                } else {
+                    int tt, ct;
+                    tile_at(args, i, tt, ct);
+                    const int t0 = tt * kTileT + (int)rank * 128 + quad * 32, n = ct * tile_cols + share.col0 + k * 32;
+                    float *const loose = reinterpret_cast<float *>(smem + (box - ring));
+                    if (n < p.N) {
+                        if (p.residual) LooseRows<kF32>::add_residual(p, acc, loose, t0, n, lane);
+                        LooseRows<kF32>::store(p, acc, loose, t0, n, lane);
                     }
-                    if (last) break;
+                }
+                if (closes) {
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&ctl.boxes_full[set]);
+                }
+                if (k + 1 == blocks) break;
+                if (!kF32 && p.gated) {
+                    tc::ld32(from + 32, acc);
+                    tc::ld32(from + 32 + apart, acc + 32);
+                    tc::wait_ld();
+                    tc::pin32(acc);
+                    tc::pin32(acc + 32);
+                    release();
+                } else {
+                    if (!kF32 && k > 0) {
+                        tc::wait_ld();
+                        tc::pin32(acc + 32);
+                        if (k == 2) release();
+                    }
 #pragma unroll
                     for (int j = 0; j < 32; ++j) acc[j] = acc[32 + j];
+                    if (!kF32 && k < 2) tc::ld32(from + 32 * (k + 2), acc + 32);
                 }
             }
         }
