@@ -1,4 +1,5 @@
 // Matrix product with an epilogue: which kernel takes a call, and the tensor maps that they share.
+#include <stdlib.h>
 #include <cudaTypedefs.h>
 
 #include "dr_layer.h"
@@ -40,6 +41,7 @@ namespace {
 // Prompts go to the pairs of CTAs.
 bool takes_tiles(const LinearParams &p, int sms) {
     const int64_t tiles = linear_tiles_tiles(p);
+    if (getenv("LCL") && atoi(getenv("LCL"))) return false;
     return tiles * 2 >= sms / 2;
 }
 

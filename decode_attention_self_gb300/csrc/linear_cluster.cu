@@ -2,32 +2,35 @@
 //
 // One CTA multiplies up to 128 tokens by NB rows of W over its share of K on the tensor cores: the tokens are the MMA's
 // M = 128 operand, the weight rows its N operand, both K-major bf16 in shared memory with the 128-byte swizzle, the fp32
-// sums in tensor memory (a lane per token).  Few tokens make W's bytes the cost, and N / NB tiles alone would leave SMs
-// idle, so the S CTAs of a cluster share K: each pushes its partial sums, row by row, into the shared memory of the CTA
-// that owns the row (rows / S each), and after one cluster barrier the owner adds the S parts in rank order and finishes
-// its rows with 16-byte accesses.  The order of sums is fixed: results are the same bits from call to call.
-//   warp 0: TMA producer of 64-wide K chunks;  warp 1: MMA issuer;  all 4 warps: push, sum, epilogue.
+// sums in tensor memory (a lane per token).  What such a call costs is the way of its operands: W from memory, and both
+// from L2 into each SM at some 70 bytes a cycle, so tiles and splits are chosen for few bytes per SM (make_plan).  Where the
+// tiles leave SMs idle the S CTAs of a cluster share K: each lays its partial sums down in its shared memory and copies them, in
+// bulk, to the CTAs that own the rows (rows / S each), which add the S parts in rank order and finish their rows.  The
+// order of sums is fixed: results are the same bits from call to call.
+//   warp 0: TMA producer of 64-wide K chunks;  warp 1: MMA issuer;  all 8 warps: sums, epilogue.
+// The kernel runs once through its code, so there is little of it: one form of the epilogue, 16 columns of a token at a time.
 // Tensor-core sums are cut off, not rounded: each addition may lose the last bit towards zero, so a chain over K drifts by about
 // 1e-9 K (measured: 1.0e-6 at K = 1024, 2.1e-6 at 2048).  fp32 outputs therefore break the chain every 512 of K into
 // accumulators of their own (pieces), added in fp32; bf16 outputs, whose rounding is 1000 times that, do not.
 // Tensor memory and clusters: a CTA that waits for its cluster must not keep another cluster's CTA waiting for tensor
 // memory.  A CTA takes at least 80 KB of shared memory and at most 256 columns, so that the two that fit on an SM (or one and two
 // of the LM head's, 72 KB and 128 columns at the least and most) never need more than the 512 there are.
-// Every mbarrier wait is bounded; one that runs out sets DR_ERRF_TIMEOUT, and the cluster's tile is not written.
+// Every mbarrier wait is bounded; one that runs out sets DR_ERRF_TIMEOUT, and the rows that lack its sums are not written.
+#include <stdlib.h>
 #include "dr_tc.cuh"
 #include "linear_epilogue.cuh"
 
 namespace dr {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 256;
 constexpr int kRows = 128;        // tokens per tile (MMA M)
 constexpr int kChunkK = 64;       // K per stage: one 128-byte swizzled row
 constexpr int kMaxStages = 8;
 constexpr int kPieceChunks = 8;   // fp32 outputs: K of 512 per accumulator
-constexpr int kMaxCols = 256;     // tensor-memory columns of a CTA (see above)
+constexpr int kMaxCols = 256;     // tensor-memory columns of a CTA (see above); also the largest NB
 constexpr size_t kMinSmem = 80 * 1024;
-constexpr size_t kMaxSmem = 226 * 1024;
+constexpr size_t kMaxSmem = 225 * 1024;
 
 struct ClusterPlan {
     int nb;            // weight rows per tile (MMA N): nb output columns, or nb / 2 when gated
@@ -36,8 +39,11 @@ struct ClusterPlan {
     int piece_chunks;  // K chunks per accumulator
     int stages;
     int cols;          // tensor-memory columns
+    uint32_t recv_at;  // where the parts of a cluster's other CTAs go, behind the ring and the CTA's own sums
     size_t smem;
 };
+
+size_t parts_bytes(int rows, const ClusterPlan &pl) { return (size_t)rows * pl.nb * 4; }
 
 struct ClusterArgs {
     LinearParams p;
@@ -50,6 +56,12 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(tc::smem_u32(bar))
         : "memory");
 }
+// A copy from this CTA's shared memory to that of another of the cluster, counted on a barrier there.
+__device__ __forceinline__ void copy_to_peer(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "r"(src),
+                 "r"(bytes), "r"(bar)
+                 : "memory");
+}
 __device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank) {
     uint32_t r;
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
@@ -58,14 +70,15 @@ __device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
+template <bool kF32>
 __global__ void __launch_bounds__(kThreads)
     linear_cluster_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                           const __grid_constant__ ClusterArgs args) {
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], done;
+    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], done, parts;
     __shared__ uint32_t tmem_base;
     __shared__ int gave_up, issued;   // a wait ran out; chunks whose copies were issued (and all before, but for a stalled one)
-    __shared__ int part_ok[8];
+    __shared__ float bias[kMaxCols];   // of the tile's sums
 
     const LinearParams &p = args.p;
     const ClusterPlan &pl = args.plan;
@@ -78,11 +91,17 @@ __global__ void __launch_bounds__(kThreads)
     const int chunks = c_end - c_begin;
     const uint32_t bytes_x = pl.box_rows * 128, bytes_w = pl.nb * 128;
 
+    // Ring of tokens, ring of weight rows, partial sums of the cluster.  The MMA reads 128 token rows from each stage, however
+    // few there are: rows past the stage's own are whatever follows in shared memory (plan: there is as much), and the sums
+    // of their lanes are not looked at.
     const uint32_t ring = (tc::smem_u32(smem_raw) + 1023) & ~1023u;
-    const uint32_t sx = ring, sw = ring + stages * (kRows * 128);
-    const uint32_t recv_off = ring - tc::smem_u32(smem_raw) + stages * (kRows * 128 + bytes_w);
+    const uint32_t sx = ring, sw = ring + stages * bytes_x;
+    const int rows = min(kRows, p.T - t0), share = (rows + S - 1) / S;   // rows of the tile, and that a CTA owns
+    const int mine = min(share, rows - rank * share);
+    uint8_t *const staged = smem_raw + (ring - tc::smem_u32(smem_raw));              // own sums, over the ring once it is idle
+    uint8_t *const received = staged + pl.recv_at;                                   // the other CTAs', part by part
 
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 32) {
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_x)) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_w)) : "memory");
         for (int s = 0; s < stages; ++s) {
@@ -90,10 +109,12 @@ __global__ void __launch_bounds__(kThreads)
             tc::mbar_init(&empty[s], 1);
         }
         tc::mbar_init(&done, 1);
+        tc::mbar_init(&parts, 1);
+        if (S > 1 && mine > 0) tc::mbar_expect_tx(&parts, (uint32_t)((S - 1) * mine * pl.nb) * 4);
         gave_up = issued = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 0) {
+    if (warp == 2) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc::smem_u32(&tmem_base)),
                      "r"(pl.cols));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -113,6 +134,13 @@ __global__ void __launch_bounds__(kThreads)
                          : "memory");
     }
     pdl_wait();
+    // The next kernel may start as far as it fits beside this one: it sets up, and prefetches its weights.
+    pdl_trigger();
+    if (p.bias && threadIdx.x >= 64)
+        for (int j = threadIdx.x - 64; j < pl.nb; j += kThreads - 64) {
+            const int n = n0 + (j < bn ? j : j - bn);
+            bias[j] = n < p.N ? lin::bf16_at(p.bias, j < bn ? n : (int64_t)p.N + n) : 0.f;
+        }
 
     if (warp == 0) {
         // stage s of round r waits for the products of round r - 1.  (Test hook: the stalled tile's producer starts at
@@ -128,7 +156,7 @@ __global__ void __launch_bounds__(kThreads)
                 const uint32_t w_at = sw + s * bytes_w;
                 tma_load_2d(w_at, &map_w, k, n0, &full[s]);
                 if (p.gated) tma_load_2d(w_at + bytes_w / 2, &map_w, k, p.N + n0, &full[s]);
-                tma_load_2d(sx + s * (kRows * 128), &map_x, k, t0, &full[s]);
+                tma_load_2d(sx + s * bytes_x, &map_x, k, t0, &full[s]);
             }
             __syncwarp();
             if (++s == stages) {
@@ -150,7 +178,7 @@ __global__ void __launch_bounds__(kThreads)
             if (tc::elect_one()) {
 #pragma unroll
                 for (int k = 0; k < kChunkK / 16; ++k)
-                    tc::mma_ss(d, tc::desc_at(dx, s * (kRows * 128) + k * 32), tc::desc_at(dw, s * bytes_w + k * 32), idesc,
+                    tc::mma_ss(d, tc::desc_at(dx, s * bytes_x + k * 32), tc::desc_at(dw, s * bytes_w + k * 32), idesc,
                                (in_piece | k) != 0);
                 tc::commit(&empty[s]);   // the stage is free once these products have read it
             }
@@ -170,7 +198,6 @@ __global__ void __launch_bounds__(kThreads)
         __syncwarp();
     }
     __syncthreads();
-    pdl_trigger();
     bool ok = tc::mbar_wait(&done, 0, &gave_up);
     if (gave_up) {
         // copies in flight end by themselves; wait for them before this CTA's shared memory goes away
@@ -184,89 +211,102 @@ __global__ void __launch_bounds__(kThreads)
     ok = __syncthreads_and(ok);
     tc::fence_after();
 
-    // partial sums, row by row, to the CTA that owns the row
-    const int rows = min(kRows, p.T - t0);
-    const int share = (rows + S - 1) / S;   // rows that a CTA owns
-    const int nb = pl.nb;
-    const uint32_t recv = tc::smem_u32(smem_raw) + recv_off;
-    if (S > 1) cluster_wait();
-    const int pieces = (chunks + pl.piece_chunks - 1) / pl.piece_chunks;
-    const int row = warp * 32 + lane;
-    if (ok && warp * 32 < rows) {
-        const int owner = row / share;
-        const uint32_t slot = recv + (uint32_t)((rank * share + row - owner * share) * nb) * 4;
-        const uint32_t dst = S > 1 ? mapa(slot, min(owner, S - 1)) : slot;
-        for (int c0 = 0; c0 < nb; c0 += 32) {
-            float acc[32];
-            tc::ld32(tmem + ((uint32_t)(warp * 32) << 16) + c0, acc);
+    // Sums to shared memory, [row][nb] fp32 in 16-byte pieces that the row turns, so that a warp's stores spread over the banks.
+    // The ring is idle: all its copies were multiplied.
+    const int nb = pl.nb, pieces = (chunks + pl.piece_chunks - 1) / pl.piece_chunks;
+    if (ok && (warp & 3) * 32 < rows) {
+        const int row = (warp & 3) * 32 + lane;
+        const uint32_t from = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        float4 *to = reinterpret_cast<float4 *>(staged) + row * (nb / 4);
+#pragma unroll 1
+        for (int c = (warp >> 2) * 16; c < nb; c += 32) {
+            float v[16];
+            tc::ld16(from + c, v);
             tc::wait_ld();
-            tc::pin32(acc);
-            for (int i = 1; i < pieces; ++i) {
-                float more[32];
-                tc::ld32(tmem + ((uint32_t)(warp * 32) << 16) + i * nb + c0, more);
-                tc::wait_ld();
-                tc::pin32(more);
+            tc::pin16(v);
+            if constexpr (kF32)
+#pragma unroll 1
+                for (int i = 1; i < pieces; ++i) {
+                    float more[16];
+                    tc::ld16(from + i * nb + c, more);
+                    tc::wait_ld();
+                    tc::pin16(more);
 #pragma unroll
-                for (int j = 0; j < 32; ++j) acc[j] += more[j];
-            }
-            if (row < rows) {
+                    for (int j = 0; j < 16; ++j) v[j] += more[j];
+                }
+            if (row < rows)
 #pragma unroll
-                for (int j = 0; j < 8; ++j)   // 16-byte steps, turned by the row so that a warp's stores spread over the banks
-                    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                     dst + (((c0 / 4 + j) ^ (row & 7)) * 16)),
-                                 "f"(acc[4 * j]), "f"(acc[4 * j + 1]), "f"(acc[4 * j + 2]), "f"(acc[4 * j + 3])
-                                 : "memory");
-            }
+                for (int j = 0; j < 4; ++j) to[(c / 4 + j) ^ (row & 7)] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
         }
-    }
-    if (threadIdx.x < S) {
-        const uint32_t at = tc::smem_u32(&part_ok[rank]);
-        asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(S > 1 ? mapa(at, threadIdx.x) : at), "r"((int)ok) : "memory");
     }
     tc::fence_before();
     if (S > 1) {
-        cluster_arrive();
-        cluster_wait();
-    } else {
-        __syncthreads();
+        tc::fence_proxy_async();
+        cluster_wait();   // every CTA of the cluster has set its barrier up
     }
-    if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(pl.cols));
-    for (int i = 0; i < S; ++i)
-        if (!part_ok[i]) return;
-
-    const int mine = min(share, rows - rank * share), groups = bn / 8;
-    const float *sums = reinterpret_cast<const float *>(smem_raw + recv_off);
-    for (int i = threadIdx.x; i < mine * groups; i += kThreads) {
-        const int r = i / groups, g = i - r * groups, key = (rank * share + r) & 7;
-        float a[8] = {}, b[8] = {};
-        for (int s = 0; s < S; ++s) {
-            const float4 *from = reinterpret_cast<const float4 *>(sums + (size_t)(s * share + r) * nb);
+    __syncthreads();
+    if (warp == 2) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(pl.cols));
+    if (S > 1) {
+        if (ok && warp == 0 && lane < S && lane != rank) {   // a lane per owner
+            const int theirs = min(share, rows - lane * share);
+            const uint32_t slot = (uint32_t)(rank - (rank > lane)) * (theirs * nb * 4);   // parts in rank order, without the owner's
+            if (theirs > 0)
+                copy_to_peer(mapa(tc::smem_u32(received) + slot, lane), tc::smem_u32(staged) + lane * share * nb * 4, theirs * nb * 4,
+                             mapa(tc::smem_u32(&parts), lane));
+        }
+        __syncwarp();
+        if (mine > 0 && !tc::mbar_wait(&parts, 0, &gave_up)) {
+            if (threadIdx.x == 0) flag_error(p.err, DR_ERRF_TIMEOUT);
+            ok = false;
+        }
+        ok = __syncthreads_and(ok);
+        cluster_arrive();   // this CTA has its parts; none exits before the copies out of it have landed
+    }
+    if (ok) {
+        const int groups = bn / 16;
+#pragma unroll 1
+        for (int i = threadIdx.x; i < mine * groups; i += kThreads) {
+            const int r = i / groups, g = i - r * groups, row = rank * share + r, key = row & 7;
+            float a[16], b[16];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const float4 v = from[(2 * g + h) ^ key];
-                a[4 * h] += v.x; a[4 * h + 1] += v.y; a[4 * h + 2] += v.z; a[4 * h + 3] += v.w;
-            }
-            if (p.gated) {
+            for (int j = 0; j < 16; ++j) a[j] = b[j] = 0.f;
+#pragma unroll 1
+            for (int s = 0; s < S; ++s) {
+                const float4 *from = s == rank ? reinterpret_cast<const float4 *>(staged) + row * (nb / 4)
+                                               : reinterpret_cast<const float4 *>(received) + ((s - (s > rank)) * mine + r) * (nb / 4);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float4 v = from[(bn / 4 + 2 * g + h) ^ key];
-                    b[4 * h] += v.x; b[4 * h + 1] += v.y; b[4 * h + 2] += v.z; b[4 * h + 3] += v.w;
+                for (int h = 0; h < 4; ++h) {
+                    const float4 v = from[(4 * g + h) ^ key];
+                    a[4 * h] += v.x; a[4 * h + 1] += v.y; a[4 * h + 2] += v.z; a[4 * h + 3] += v.w;
+                }
+                if (p.gated) {
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        const float4 v = from[(bn / 4 + 4 * g + h) ^ key];
+                        b[4 * h] += v.x; b[4 * h + 1] += v.y; b[4 * h + 2] += v.z; b[4 * h + 3] += v.w;
+                    }
                 }
             }
+            lin::finish16<kF32>(p, bias + g * 16, bias + bn + g * 16, t0 + row, n0 + g * 16, a, b);
         }
-        lin::finish8(p, t0 + rank * share + r, n0 + g * 8, a, b);
     }
+    if (S > 1) cluster_wait();
 }
 
+// Tile width and split of a call.
 ClusterPlan make_plan(const LinearParams &p, int sms) {
     ClusterPlan pl;
     const int chunks = (p.K + kChunkK - 1) / kChunkK;
     const int mtiles = (p.T + kRows - 1) / kRows;
     pl.nb = 64;
-    const int bn = p.gated ? pl.nb / 2 : pl.nb;
-    const int64_t tiles = (int64_t)mtiles * ((p.N + bn - 1) / bn);
     pl.split = 1;
-    while (pl.split < 8 && tiles * pl.split * 2 <= sms && pl.split * 4 <= chunks) pl.split *= 2;
+    {
+        const int bn = p.gated ? pl.nb / 2 : pl.nb;
+        const int64_t tiles = (int64_t)mtiles * ((p.N + bn - 1) / bn);
+        while (pl.split < 8 && tiles * pl.split * 2 <= sms && pl.split * 4 <= chunks) pl.split *= 2;
+    }
+    if (getenv("LNB")) pl.nb = atoi(getenv("LNB"));
+    if (getenv("LSP")) pl.split = atoi(getenv("LSP"));
     const int rows = p.T < kRows ? p.T : kRows;
     pl.box_rows = (rows + 7) / 8 * 8;
     const int most = (chunks + pl.split - 1) / pl.split;   // chunks of a CTA
@@ -279,11 +319,18 @@ ClusterPlan make_plan(const LinearParams &p, int sms) {
     }
     pl.cols = 32;
     while (pl.cols < pl.nb * pieces) pl.cols *= 2;
-    const size_t stage = (kRows + pl.nb) * 128;
-    const size_t recv = (size_t)(rows + pl.split) * pl.nb * 4;
-    pl.stages = most < kMaxStages ? most : kMaxStages;
-    while (pl.stages > 2 && 1024 + pl.stages * stage + recv > kMaxSmem) --pl.stages;
-    pl.smem = 1024 + pl.stages * stage + recv;
+    // shared memory: the ring, with what its last stage's products may read past it, or after it the CTA's own sums; the parts
+    const size_t stage = (size_t)(pl.box_rows + pl.nb) * 128, own = parts_bytes(rows, pl);
+    const size_t parts = pl.split > 1 ? parts_bytes(rows + pl.split, pl) : 0;
+    const auto ring = [&](int n) {
+        const size_t over = n * stage > (size_t)(n * pl.box_rows + kRows) * 128 ? n * stage : (size_t)(n * pl.box_rows + kRows) * 128;
+        return over > own ? over : own;
+    };
+    int lim = getenv("LST") ? atoi(getenv("LST")) : kMaxStages;
+    pl.stages = most < lim ? most : lim;
+    while (pl.stages > 2 && 1024 + ring(pl.stages) + parts > kMaxSmem) --pl.stages;
+    pl.recv_at = (uint32_t)ring(pl.stages);
+    pl.smem = 1024 + ring(pl.stages) + parts;
     if (pl.smem < kMinSmem) pl.smem = kMinSmem;
     return pl;
 }
@@ -309,11 +356,13 @@ cudaError_t launch_linear_cluster(const LinearParams &p, int sms, cudaStream_t s
         return cudaErrorInvalidValue;
     static std::atomic<uint64_t> ready{0};
     cudaError_t e = once_per_device(ready, [] {
-        return cudaFuncSetAttribute(linear_cluster_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem);
+        const cudaError_t err = cudaFuncSetAttribute(linear_cluster_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem);
+        return err != cudaSuccess ? err : cudaFuncSetAttribute(linear_cluster_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem);
     });
     if (e != cudaSuccess) return e;
+    auto kern = p.out_f32 ? linear_cluster_kernel<true> : linear_cluster_kernel<false>;
     const dim3 grid((unsigned)pl.split, (unsigned)((p.N + bn - 1) / bn), (unsigned)((p.T + kRows - 1) / kRows));
-    return launch_kernel(linear_cluster_kernel, grid, dim3(kThreads), pl.smem, stream, (unsigned)pl.split, map_x, map_w, a);
+    return launch_kernel(kern, grid, dim3(kThreads), pl.smem, stream, (unsigned)pl.split, map_x, map_w, a);
 }
 
 }  // namespace dr

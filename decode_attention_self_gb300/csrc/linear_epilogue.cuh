@@ -88,90 +88,83 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     return r;
 }
 
-// v[0 .. 8) += bias[i .. i+8); places from `have` on are left out.  bias is 16-byte aligned.
-__device__ __forceinline__ void add_bias8(float *v, const uint16_t *bias, int64_t i, int have) {
-    if (have >= 8 && i % 8 == 0) {
-        float f[8];
-        unpack8(ld_ro16(bias + i), f);
-#pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-            const float2 y = __fadd2_rn(make_float2(v[j], v[j + 1]), make_float2(f[j], f[j + 1]));
-            v[j] = y.x;
-            v[j + 1] = y.y;
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (j < have) v[j] += bf16_at(bias, i + j);
-    }
+// The output that holds column n.
+__device__ __forceinline__ int out_of(const LinearParams &p, int n) {
+    int s = 0;
+    for (int i = 1; i < p.n_outs; ++i)
+        if (n >= p.out[i].col0) s = i;
+    return s;
 }
 
-// Eight columns n .. n+7 (n a multiple of 8) of token t: bias, activation, gating and residual on the sums a (and b, the
-// sums of the rows that are multiplied in), stored to the output that holds them.  Columns from N on are left out.
-__device__ __forceinline__ void finish8(const LinearParams &p, int t, int n, float (&a)[8], float (&b)[8]) {
-    const int have = min(8, p.N - n);
+// Sixteen columns n .. n+15 (n a multiple of 16) of token t: bias (of these columns, fp32), activation, gating and residual on
+// the sums a (and b, the sums of the rows that are multiplied in), stored to the output that holds them.  Columns from N on
+// are left out.
+template <bool kF32>
+__device__ __forceinline__ void finish16(const LinearParams &p, const float *bias_a, const float *bias_b, int t, int n, float (&a)[16],
+                                         float (&b)[16]) {
+    constexpr int kWords = kF32 ? 16 : 8;   // 32-bit words of the 16 columns
+    const int have = p.N - n;
     if (have <= 0) return;
-    if (p.bias) {
-        add_bias8(a, p.bias, n, have);
-        if (p.gated) add_bias8(b, p.bias, (int64_t)p.N + n, have);
+    uint4 r[kWords / 4];
+    const bool quick_res = p.vec_res && have >= 16;
+    const int64_t res_at = (int64_t)t * p.res_stride + n;
+    if (quick_res) {   // on its way during the arithmetic
+        const uint4 *from = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p.residual) + res_at * (kF32 ? 4 : 2));
+#pragma unroll
+        for (int i = 0; i < kWords / 4; ++i) r[i] = from[i];
     }
-    activate<8>(a, p.act);
+    if (p.bias) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) a[i] += bias_a[i];
+        if (p.gated) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) b[i] += bias_b[i];
+        }
+    }
+    activate<16>(a, p.act);
     if (p.gated) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) a[i] *= b[i];
+        for (int i = 0; i < 16; ++i) a[i] *= b[i];
     }
-    if (p.residual) {
-        const int64_t at = (int64_t)t * p.res_stride + n;
-        if (p.out_f32) {
-            const float *r = static_cast<const float *>(p.residual) + at;
-            if (p.vec_res && have == 8) {
-                const float4 r0 = *reinterpret_cast<const float4 *>(r), r1 = *reinterpret_cast<const float4 *>(r + 4);
-                a[0] += r0.x; a[1] += r0.y; a[2] += r0.z; a[3] += r0.w;
-                a[4] += r1.x; a[5] += r1.y; a[6] += r1.z; a[7] += r1.w;
+    if (quick_res) {
+        const uint32_t *w = reinterpret_cast<const uint32_t *>(r);
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+            if constexpr (kF32) {
+                a[i] += __uint_as_float(w[i]);
             } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (i < have) a[i] += r[i];
-            }
-        } else {
-            const uint16_t *r = static_cast<const uint16_t *>(p.residual) + at;
-            if (p.vec_res && have == 8) {
-                float f[8];
-                unpack8(*reinterpret_cast<const uint4 *>(r), f);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) a[i] += f[i];
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (i < have) a[i] += __uint_as_float((uint32_t)r[i] << 16);
+                a[2 * i] += bf16_lo(w[i]);
+                a[2 * i + 1] += bf16_hi(w[i]);
             }
         }
+    } else if (p.residual) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (i < have) {
+                if constexpr (kF32) a[i] += static_cast<const float *>(p.residual)[res_at + i];
+                else a[i] += __uint_as_float((uint32_t)static_cast<const uint16_t *>(p.residual)[res_at + i] << 16);
+            }
     }
-    int s = 0;
+    const LinearOut &o = p.out[out_of(p, n)];
+    const int64_t at = (int64_t)t * o.stride + (n - o.col0);
+    if (p.vec_out && have >= 16) {
+        uint4 *to = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(o.ptr) + at * (kF32 ? 4 : 2));
 #pragma unroll
-    for (int i = 1; i < DR_LINEAR_MAX_OUTS; ++i)
-        if (i < p.n_outs && n >= p.out[i].col0) s = i;
-    const int64_t at = (int64_t)t * p.out[s].stride + (n - p.out[s].col0);
-    if (p.out_f32) {
-        float *o = static_cast<float *>(p.out[s].ptr) + at;
-        if (p.vec_out && have == 8) {
-            *reinterpret_cast<float4 *>(o) = make_float4(a[0], a[1], a[2], a[3]);
-            *reinterpret_cast<float4 *>(o + 4) = make_float4(a[4], a[5], a[6], a[7]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i < have) o[i] = a[i];
+        for (int i = 0; i < kWords / 4; ++i) {
+            if constexpr (kF32)
+                to[i] = make_uint4(__float_as_uint(a[4 * i]), __float_as_uint(a[4 * i + 1]), __float_as_uint(a[4 * i + 2]),
+                                   __float_as_uint(a[4 * i + 3]));
+            else
+                to[i] = make_uint4(pack2(a[8 * i], a[8 * i + 1]), pack2(a[8 * i + 2], a[8 * i + 3]), pack2(a[8 * i + 4], a[8 * i + 5]),
+                                   pack2(a[8 * i + 6], a[8 * i + 7]));
         }
     } else {
-        uint16_t *o = static_cast<uint16_t *>(p.out[s].ptr) + at;
-        if (p.vec_out && have == 8) {
-            *reinterpret_cast<uint4 *>(o) =
-                make_uint4(pack2(a[0], a[1]), pack2(a[2], a[3]), pack2(a[4], a[5]), pack2(a[6], a[7]));
-        } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i < have) o[i] = f32_to_bf16_rn(a[i]);
-        }
+        for (int i = 0; i < 16; ++i)
+            if (i < have) {
+                if constexpr (kF32) static_cast<float *>(o.ptr)[at + i] = a[i];
+                else static_cast<uint16_t *>(o.ptr)[at + i] = f32_to_bf16_rn(a[i]);
+            }
     }
 }
 

@@ -129,14 +129,6 @@ __device__ __forceinline__ void tile_at(const TileArgs &a, int i, int &tt, int &
     tt = g * kGroup + (r - ct * n);
 }
 
-// The output that holds column n.
-__device__ __forceinline__ int out_of(const LinearParams &p, int n) {
-    int s = 0;
-    for (int i = 1; i < p.n_outs; ++i)
-        if (n >= p.out[i].col0) s = i;
-    return s;
-}
-
 // 16 bytes c of row `row` of a box with rows of 128 (64) bytes, as TMA's swizzle of that width lays them.
 template <bool kNarrow>
 __device__ __forceinline__ uint32_t box_chunk(uint32_t at, int row, int c) {
@@ -199,7 +191,7 @@ struct LooseRows {
 #pragma unroll
         for (int c = 0; c < 32; ++c) box[lane * 32 + (c ^ lane)] = v[c];
         __syncwarp();
-        const LinearOut &o = p.out[out_of(p, n)];   // the 32 columns lie in one output
+        const LinearOut &o = p.out[lin::out_of(p, n)];   // the 32 columns lie in one output
         const int rows = min(32, p.T - t0), col = n - o.col0 + lane;
         T *to = static_cast<T *>(o.ptr) + (int64_t)t0 * o.stride + col;
         for (int r = 0; r < rows; ++r, to += o.stride)
@@ -413,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!ok) break;
                     tc::fence_proxy_async();   // what the epilogue warps wrote, for the stores below
                     if (mine && boxed) {
-                        const int s = out_of(p, n);
+                        const int s = lin::out_of(p, n);
                         if (t0 < p.T && n - p.out[s].col0 < p.out[s].cols) box_store(&maps.out[s], n - p.out[s].col0, t0, at);
                         asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                     }
