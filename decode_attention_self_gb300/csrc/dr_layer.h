@@ -43,7 +43,7 @@ cudaError_t launch_linear(const LinearParams &p, cudaStream_t stream);
 cudaError_t launch_linear_cluster(const LinearParams &p, int sms, cudaStream_t stream);
 int linear_cluster_tiles(const LinearParams &p, int sms);
 cudaError_t launch_linear_tiles(const LinearParams &p, int sms, cudaStream_t stream);
-int linear_tiles_tiles(const LinearParams &p);
+int linear_tiles_tiles(const LinearParams &p, int sms);
 
 struct NormParams {
     int32_t kind;             // DR_NORM_*

@@ -40,15 +40,15 @@ namespace {
 
 // Prompts go to the pairs of CTAs.
 bool takes_tiles(const LinearParams &p, int sms) {
-    const int64_t tiles = linear_tiles_tiles(p);
-    if (getenv("LCL") && atoi(getenv("LCL"))) return false;
+    const int64_t tiles = linear_tiles_tiles(p, sms);
+    if (getenv("LCL")) return !atoi(getenv("LCL"));
     return tiles * 2 >= sms / 2;
 }
 
 }  // namespace
 
 int linear_tiles(const LinearParams &p, int sms) {
-    return takes_tiles(p, sms) ? linear_tiles_tiles(p) : linear_cluster_tiles(p, sms);
+    return takes_tiles(p, sms) ? linear_tiles_tiles(p, sms) : linear_cluster_tiles(p, sms);
 }
 
 cudaError_t launch_linear(const LinearParams &p, cudaStream_t stream) {

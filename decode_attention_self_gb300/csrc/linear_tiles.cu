@@ -8,8 +8,8 @@
 //   warp 0      TMA producer of its CTA's halves: 64-wide K chunks in a ring of kStages, counted on the first CTA's barrier
 //   warp 1      MMA issuer (first CTA only)
 //   warps 2, 3  carriers, each for eight epilogue warps: bias and residual in, results out, by TMA
-//   warps 4-19  epilogue, in two sets of eight: bf16 outputs take the tiles in turn, 128 of a tile's sums per token and
-//               warp; fp32 outputs share each tile, 64 a warp
+//   warps 4-19  epilogue.  Where a pair has several tiles, two sets of eight warps take them in turn, 128 of a tile's sums per
+//               token and warp; where it has one, or outputs are fp32, all sixteen share each tile, 64 sums a warp
 // The sums of a tile take 256 of the 512 tensor-memory columns; the next tile is multiplied while the epilogue works on
 // the one before.  A tile of K = 1024 is multiplied in 8192 cycles, during which reading its operands and writing them by TMA
 // take all of shared memory's 128 bytes a cycle: whatever else goes through there costs the products time, and latencies
@@ -21,6 +21,7 @@
 // epilogue warps' registers.
 // Every mbarrier wait is bounded; after one that runs out the pair's further tiles are not written, and copies and
 // products in flight are waited for before it exits.
+#include <stdlib.h>
 #include <type_traits>
 
 #include "dr_tc.cuh"
@@ -35,7 +36,7 @@ constexpr int kEpiWarp = 4, kEpiWarps = 16;
 constexpr int kLaunchRegs = 96, kOtherRegs = 32, kEpiRegs = 112;
 static_assert(kEpiWarp * 32 * kOtherRegs + kEpiWarps * 32 * kEpiRegs <= kThreads * kLaunchRegs, "more than the launch has");
 constexpr int kTileT = 256;       // tokens per pair
-constexpr int kTileW = 256;       // weight rows per pair (MMA N)
+constexpr int kTileW = 256;       // most weight rows per pair (MMA N), and tensor-memory columns of a tile
 constexpr int kStages = 5;
 constexpr int kHalf = 128 * 128;  // bytes of a CTA's tokens or weight rows in a stage
 constexpr int kBox = 32 * 128;    // bytes of an epilogue box
@@ -49,6 +50,8 @@ struct TileArgs {
     int32_t chunks;         // of 64 of K
     int32_t piece_chunks;   // chunks per chain
     int32_t token_tiles, col_tiles;
+    int32_t tile_w;         // weight rows per pair: 256, or 128 or 64 where tiles are few
+    int32_t shared;         // 1: the epilogue warps share each tile; 0: their two sets take tiles in turn
 };
 
 struct Maps {
@@ -204,19 +207,22 @@ struct LooseRows {
     }
 };
 
-// Which tiles and columns an epilogue warp takes.  bf16: the tiles of its set, half of the columns in two passes; fp32: all
-// tiles, a quarter of the columns.
-template <bool kF32>
+// Which tiles and columns an epilogue warp takes.
 struct Share {
-    int first, step;   // tiles
-    int col0, cols;    // columns of the first pass, and of each
-    static constexpr int kPasses = kF32 ? 1 : 2;
-    __device__ __forceinline__ Share(int e, int first_tile, int tile_step, int tile_cols) {
-        const int set = e / kCarried, part = e >> 2;
-        first = kF32 ? first_tile : first_tile + set * tile_step;
-        step = kF32 ? tile_step : 2 * tile_step;
-        cols = tile_cols / 4;
-        col0 = kF32 ? part * cols : (part & 1) * 2 * cols;
+    int first, step;    // tiles
+    int col0, span;     // columns
+    int blocks;         // of 32 columns
+    int box_cols;       // columns of a box: 128 bytes, or 64 where a warp's results come 32 bf16 columns at a time
+    bool active;
+    __device__ __forceinline__ Share(const TileArgs &a, int e, int first_tile, int tile_step, bool f32) {
+        const int cols = a.p.gated ? a.tile_w / 2 : a.tile_w, set = e / kCarried, part = e >> 2;
+        first = a.shared ? first_tile : first_tile + set * tile_step;
+        step = a.shared ? tile_step : 2 * tile_step;
+        span = a.shared ? max(32, cols / 4) : cols / 2;
+        col0 = (a.shared ? part : part & 1) * span;
+        blocks = span / 32;
+        box_cols = f32 || a.p.gated || span == 32 ? 32 : 64;
+        active = col0 < cols;
     }
 };
 
@@ -247,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t ring = tc::smem_u32(smem);
     const uint32_t sx = ring, sw = ring + kStages * kHalf, boxes = ring + 2 * kStages * kHalf;
     float *const bias = reinterpret_cast<float *>(smem + 2 * kStages * kHalf + kEpiWarps * kBox);   // two tiles' sums'
-    const int tile_cols = p.gated ? kTileW / 2 : kTileW;
+    const int tile_cols = p.gated ? args.tile_w / 2 : args.tile_w;
     volatile int *gave_up = &ctl.gave_up;
     // whole 16-byte pieces of rows: boxes carried by TMA
     const bool boxed = p.vec_out && (!p.residual || p.vec_res);
@@ -259,8 +265,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             tc::mbar_init(&ctl.sums_full[b], 1);
-            tc::mbar_init(&ctl.sums_free[b], 2 * (kF32 ? kEpiWarps : kCarried));
-            tc::mbar_init(&ctl.boxes_full[b], kCarried);
+            const Share share(args, 0, 0, 0, kF32);
+            const int warps = args.shared ? 4 * (tile_cols / share.span) : kCarried;   // that take a tile
+            tc::mbar_init(&ctl.sums_free[b], 2 * warps);
+            tc::mbar_init(&ctl.boxes_full[b], args.shared ? max(1, min(kCarried, warps - b * kCarried)) : kCarried);
             tc::mbar_init(&ctl.bias_ready[b], 1);
         }
         for (int w = 0; w < kEpiWarps; ++w) tc::mbar_init(&ctl.box_ready[w], 1);
@@ -291,8 +299,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 int tt, ct;
                 tile_at(args, i, tt, ct);
                 const int t = tt * kTileT + (int)rank * 128;
-                // rows of W: the pair's 256 in halves, or 128 and those that multiply them
-                const int w = p.gated ? (int)rank * p.N + ct * tile_cols : ct * tile_cols + (int)rank * 128;
+                // rows of W: the pair's in halves, or the first half and those that multiply it
+                const int w = p.gated ? (int)rank * p.N + ct * tile_cols : ct * tile_cols + (int)rank * (args.tile_w / 2);
                 for (int c = 0; c < args.chunks; ++c) {
                     if (!(c == 0 && i == p.stall_tile)) {
                         if (r > 0 && !tc::mbar_wait(&ctl.empty[s], (r - 1) & 1, gave_up)) {
@@ -301,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         if (tc::elect_one()) {
                             const uint32_t bar = mapa(tc::smem_u32(&ctl.full[s]), 0);
-                            if (rank == 0) tc::mbar_expect_tx(&ctl.full[s], 4 * kHalf);
+                            if (rank == 0) tc::mbar_expect_tx(&ctl.full[s], 2 * kHalf + args.tile_w * 128);
                             pair_load(sx + s * kHalf, &maps.x, c * 64, t, bar);
                             pair_load(sw + s * kHalf, &maps.w, c * 64, w, bar);
                         }
@@ -324,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (armed >> k & 1) tc::mbar_drain(&ctl.full[k], parity >> k & 1);
             }
         } else if (warp == 1 && rank == 0) {
-            const uint32_t idesc = tc::instr_desc(kTileT, kTileW, false, false);
+            const uint32_t idesc = tc::instr_desc(kTileT, args.tile_w, false, false);
             const uint64_t dx = tc::smem_desc(sx), dw = tc::smem_desc(sw);
             int s = 0, r = 0;
             unsigned chain = 0;
@@ -369,20 +377,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         } else if (warp >= kCarrier) {
             const int set = warp - kCarrier, e = set * kCarried + (lane & (kCarried - 1));
-            const bool mine = lane < kCarried;   // a lane per box
-            const Share<kF32> share(e, first, step, tile_cols);
+            const Share share(args, e, first, step, kF32);
+            const bool mine = lane < kCarried && share.active;   // a lane per box
+            const bool any = Share(args, set * kCarried, first, step, kF32).active;
             const uint32_t at = boxes + e * kBox;
-            const int uses = kF32 && !p.gated ? 2 : Share<kF32>::kPasses;   // boxes per tile and warp
-            const int use_cols = kF32 ? 32 : share.cols;
+            const int uses = share.span / share.box_cols;   // boxes per tile and warp
             float *const to = bias + set * kTileW;
             unsigned phase = 0;
             bool ok = true;
-            for (int i = share.first; ok && i < tiles; i += share.step) {
+            for (int i = share.first; any && ok && i < tiles; i += share.step) {
                 int tt, ct;
                 tile_at(args, i, tt, ct);
                 const int n0 = ct * tile_cols;
                 if (p.bias) {   // the tile before is done with it
-                    for (int j = lane; j < kTileW; j += 32) {
+                    for (int j = lane; j < args.tile_w; j += 32) {
                         const int n = n0 + (j & (tile_cols - 1));
                         to[j] = n < p.N ? lin::bf16_at(p.bias, j < tile_cols ? n : (int64_t)p.N + n) : 0.f;
                     }
@@ -390,11 +398,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0) tc::mbar_arrive(&ctl.bias_ready[set]);
                 }
                 for (int u = 0; u < uses; ++u, phase ^= 1) {
-                    const int t0 = tt * kTileT + (int)rank * 128 + (e & 3) * 32, n = n0 + share.col0 + u * use_cols;
+                    const int t0 = tt * kTileT + (int)rank * 128 + (e & 3) * 32, n = n0 + share.col0 + u * share.box_cols;
                     if (mine && boxed) {
                         asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");   // the store before has read the box
                         if (p.residual) {
-                            tc::mbar_expect_tx(&ctl.box_ready[e], !kF32 && p.gated ? kBox / 2 : kBox);
+                            tc::mbar_expect_tx(&ctl.box_ready[e], !kF32 && share.box_cols == 32 ? kBox / 2 : kBox);
                             own_load(at, &maps.res, n, t0, &ctl.box_ready[e]);
                         } else {
                             tc::mbar_arrive(&ctl.box_ready[e]);
@@ -414,30 +422,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!ok) {
                 if (lane == 0) flag_error(p.err, DR_ERRF_TIMEOUT);
-                if (boxed && p.residual)
-                    for (int k = 0; k < kCarried; ++k) tc::mbar_drain(&ctl.box_ready[set * kCarried + k], phase);   // on their way
+                if (boxed && p.residual && mine) tc::mbar_drain(&ctl.box_ready[e], phase);   // on its way
             }
-            if (mine) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+            if (mine) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
             __syncwarp();
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
         const int e = warp - kEpiWarp, set = e / kCarried, quad = warp & 3;
-        const Share<kF32> share(e, first, step, tile_cols);
+        const Share share(args, e, first, step, kF32);
+        const bool shared = kF32 || args.shared, narrow = !kF32 && share.box_cols == 32;
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
         const int pieces = kF32 ? (args.chunks + args.piece_chunks - 1) / args.piece_chunks : 1;
         const uint32_t box = boxes + e * kBox;
-        unsigned chain = kF32 ? 0 : set, box_phase = 0, bias_phase = 0;   // bf16: a set has the even or the odd chains
+        unsigned chain = shared ? 0 : set, box_phase = 0, bias_phase = 0;   // in turn, a set has the even or the odd chains
         bool ok = true;
-        const int blocks = (kF32 ? 1 : 2) * (p.gated ? 1 : 2);   // of 32 output columns
-        const int apart = p.gated ? kTileW / 2 : 32;             // from a block's sums to those that multiply it, or the next block's
+        const int apart = p.gated ? args.tile_w / 2 : 32;   // from a block's sums to those that multiply it, or the next block's
+        const bool two = p.gated || share.span > 32;        // whether there are such
         const auto release = [&] {   // this warp has its sums: the place may have another tile's
             tc::fence_before();
             __syncwarp();
             if (lane == 0) remote_arrive(mapa(tc::smem_u32(&ctl.sums_free[chain & 1]), 0));
-            chain += kF32 ? 1 : 2;
+            chain += shared ? 1 : 2;
         };
-        for (int i = share.first; ok && i < tiles; i += share.step) {
+        for (int i = share.first; share.active && ok && i < tiles; i += share.step) {
             float acc[64];
             uint32_t from = 0;
             for (int k = 0; k < pieces; ++k) {
@@ -447,13 +455,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 from = tmem + lanes + (chain & 1) * kTileW + share.col0;
                 if (!kF32 || k == 0) {
                     tc::ld32(from, acc);
-                    tc::ld32(from + apart, acc + 32);
+                    if (two) tc::ld32(from + apart, acc + 32);
                     tc::wait_ld();
                     tc::pin32(acc);
                     tc::pin32(acc + 32);
                 } else {
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
+                        if (q >= 2 && !two) break;
                         float more[16];
                         tc::ld16(from + (q < 2 ? 0 : apart) + (q & 1) * 16, more);
                         tc::wait_ld();
@@ -462,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int j = 0; j < 16; ++j) acc[16 * q + j] += more[j];
                     }
                 }
-                if (kF32) release();
+                if (shared) release();
             }
             if (!ok) break;
             if (p.bias) {
@@ -484,14 +493,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int j = 0; j < 32; ++j) acc[j] *= acc[32 + j];
                 }
-                const bool opens = kF32 || p.gated || k % 2 == 0, closes = kF32 || p.gated || k % 2 == 1;   // a box
+                const bool opens = kF32 || narrow || k % 2 == 0, closes = kF32 || narrow || k % 2 == 1;   // a box
                 if (boxed) {
                     if (opens) {
                         ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(&ctl.box_ready[e], box_phase, gave_up));
                         if (!ok) break;
                         box_phase ^= 1;
                     }
-                    if (!kF32 && p.gated) put32<kF32, true>(acc, box, lane, 0, p.residual);
+                    if (narrow) put32<kF32, true>(acc, box, lane, 0, p.residual);
                     else put32<kF32, false>(acc, box, lane, opens ? 0 : 4, p.residual);
                 } else {
                     int tt, ct;
@@ -507,8 +516,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     if (lane == 0) tc::mbar_arrive(&ctl.boxes_full[set]);
                 }
-                if (k + 1 == blocks) break;
-                if (!kF32 && p.gated) {
+                if (k + 1 == share.blocks) break;
+                if (!shared && p.gated) {
                     tc::ld32(from + 32, acc);
                     tc::ld32(from + 32 + apart, acc + 32);
                     tc::wait_ld();
@@ -516,14 +525,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc::pin32(acc + 32);
                     release();
                 } else {
-                    if (!kF32 && k > 0) {
+                    if (!shared && k > 0) {
                         tc::wait_ld();
                         tc::pin32(acc + 32);
                         if (k == 2) release();
                     }
 #pragma unroll
                     for (int j = 0; j < 32; ++j) acc[j] = acc[32 + j];
-                    if (!kF32 && k < 2) tc::ld32(from + 32 * (k + 2), acc + 32);
+                    if (!shared && k < 2) tc::ld32(from + 32 * (k + 2), acc + 32);
                 }
             }
         }
@@ -568,9 +577,22 @@ cudaError_t most_pairs(int sms, int *pairs) {
     return cudaSuccess;
 }
 
+// Weight rows of a pair's tile: fewer where that puts more pairs to work at once.
+int tile_width(const LinearParams &p, int pairs) {
+    const int64_t token_tiles = (p.T + kTileT - 1) / kTileT;
+    int w = kTileW;
+    if (getenv("LTW")) return atoi(getenv("LTW"));
+    while (w > 64) {
+        const int cols = p.gated ? w / 4 : w / 2;
+        if (token_tiles * ((p.N + cols - 1) / cols) > pairs) break;
+        w /= 2;
+    }
+    return w;
+}
+
 // Tensor map of an output or residual: boxes of 32 tokens.
-bool encode_box(CUtensorMap *map, const void *ptr, const LinearParams &p, int cols, int64_t stride) {
-    return encode_matrix(map, ptr, p.out_f32, p.T, cols, stride, 32, p.out_f32 || p.gated ? 32 : 64);
+bool encode_box(CUtensorMap *map, const void *ptr, const LinearParams &p, int cols, int64_t stride, bool wide) {
+    return encode_matrix(map, ptr, p.out_f32, p.T, cols, stride, 32, wide ? 64 : 32);
 }
 
 template <bool kF32>
@@ -579,33 +601,36 @@ cudaError_t launch(const LinearParams &p, int sms, cudaStream_t stream) {
     a.p = p;
     a.chunks = (p.K + 63) / 64;
     a.piece_chunks = kF32 ? kPieceChunks : a.chunks;
-    const int cols = p.gated ? kTileW / 2 : kTileW;
+    int pairs = 0;
+    const cudaError_t e = most_pairs<kF32>(sms, &pairs);
+    if (e != cudaSuccess) return e;
+    a.tile_w = tile_width(p, pairs);
+    const int cols = p.gated ? a.tile_w / 2 : a.tile_w;
     a.token_tiles = (p.T + kTileT - 1) / kTileT;
     a.col_tiles = (p.N + cols - 1) / cols;
+    const int64_t tiles = (int64_t)a.token_tiles * a.col_tiles;
+    if (tiles > 0x3FFFFFFF) return cudaErrorInvalidValue;   // tiles are counted in 32 bits: 2^46 outputs
+    if (tiles < pairs) pairs = (int)tiles;
+    a.shared = kF32 || a.tile_w < kTileW || tiles <= pairs;
+    const bool wide = !kF32 && !p.gated && a.tile_w == kTileW;
     Maps m;
     if (!encode_matrix(&m.x, p.x, false, p.T, p.K, p.x_stride, 128, 64) ||
-        !encode_matrix(&m.w, p.W, false, (int64_t)p.N * (p.gated ? 2 : 1), p.K, p.K, 128, 64))
+        !encode_matrix(&m.w, p.W, false, (int64_t)p.N * (p.gated ? 2 : 1), p.K, p.K, a.tile_w / 2, 64))
         return cudaErrorInvalidValue;
     // maps that the kernel does not use stay copies
     m.res = m.x;
     for (int i = 0; i < DR_LINEAR_MAX_OUTS; ++i) m.out[i] = m.x;
     if (p.vec_out)
         for (int i = 0; i < p.n_outs; ++i)
-            if (!encode_box(&m.out[i], p.out[i].ptr, p, p.out[i].cols, p.out[i].stride)) return cudaErrorInvalidValue;
-    if (p.vec_res && !encode_box(&m.res, p.residual, p, p.N, p.res_stride)) return cudaErrorInvalidValue;
-    int pairs = 0;
-    const cudaError_t e = most_pairs<kF32>(sms, &pairs);
-    if (e != cudaSuccess) return e;
-    const int64_t tiles = (int64_t)a.token_tiles * a.col_tiles;
-    if (tiles > 0x3FFFFFFF) return cudaErrorInvalidValue;   // tiles are counted in 32 bits: 2^46 outputs
-    if (tiles < pairs) pairs = (int)tiles;
+            if (!encode_box(&m.out[i], p.out[i].ptr, p, p.out[i].cols, p.out[i].stride, wide)) return cudaErrorInvalidValue;
+    if (p.vec_res && !encode_box(&m.res, p.residual, p, p.N, p.res_stride, wide)) return cudaErrorInvalidValue;
     return launch_kernel(linear_tiles_kernel<kF32>, dim3((unsigned)(2 * pairs)), dim3(kThreads), kSmem, stream, 2, m, a);
 }
 
 }  // namespace
 
-int linear_tiles_tiles(const LinearParams &p) {
-    const int cols = p.gated ? kTileW / 2 : kTileW;
+int linear_tiles_tiles(const LinearParams &p, int sms) {
+    const int w = tile_width(p, sms / 2), cols = p.gated ? w / 2 : w;
     const int64_t n = (int64_t)((p.T + kTileT - 1) / kTileT) * ((p.N + cols - 1) / cols);
     return n > 0x7FFFFFFF ? 0x7FFFFFFF : (int)n;
 }
