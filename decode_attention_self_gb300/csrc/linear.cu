@@ -1,5 +1,4 @@
 // Matrix product with an epilogue: which kernel takes a call, and the tensor maps that they share.
-#include <stdlib.h>
 #include <cudaTypedefs.h>
 
 #include "dr_layer.h"
@@ -38,11 +37,12 @@ bool encode_matrix(CUtensorMap *map, const void *ptr, bool f32, int64_t rows, in
 
 namespace {
 
-// Prompts go to the pairs of CTAs.
+// Whether the pairs of CTAs take a call: where the other kernel's tiles, 128 tokens by 64 weight rows, are more than one wave.
+// Measured, us: 512 tokens 1024 -> 4096 (256 such tiles) 9.0 against 9.1, 1024 tokens 1024 -> 4096 11.5 against 15;
+// 1024 tokens 4096 -> 1024 (128 tiles) 18 against 12.6, 256 tokens 1024 -> 4096 (128) 8.3 against 6.7.
 bool takes_tiles(const LinearParams &p, int sms) {
-    const int64_t tiles = linear_tiles_tiles(p, sms);
-    if (getenv("LCL")) return !atoi(getenv("LCL"));
-    return tiles * 2 >= sms / 2;
+    const int64_t rows = (int64_t)p.N * (p.gated ? 2 : 1);
+    return ((int64_t)p.T + 127) / 128 * ((rows + 63) / 64) > sms;
 }
 
 }  // namespace

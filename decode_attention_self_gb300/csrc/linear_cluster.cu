@@ -7,7 +7,10 @@
 // tiles leave SMs idle the S CTAs of a cluster share K: each lays its partial sums down in its shared memory and copies them, in
 // bulk, to the CTAs that own the rows (rows / S each), which add the S parts in rank order and finish their rows.  The
 // order of sums is fixed: results are the same bits from call to call.
-//   warp 0: TMA producer of 64-wide K chunks;  warp 1: MMA issuer;  all 8 warps: sums, epilogue.
+//   warps 0, 1: TMA producers of 64-wide K chunks, even and odd;  warps 2, 3: MMA issuers, even and odd chunks, each into
+//   sums of its own;  all 8 warps: sums, epilogue.
+// (One warp takes some 400 cycles to issue a chunk's four products, wait and commit, and 310 to issue its copies, whatever
+// their size: with one of each, 128 tokens of 1024 -> 4096 took 8700 cycles for 16 chunks, which ran in 2700.)
 // The kernel runs once through its code, so there is little of it: one form of the epilogue, 16 columns of a token at a time.
 // Tensor-core sums are cut off, not rounded: each addition may lose the last bit towards zero, so a chain over K drifts by about
 // 1e-9 K (measured: 1.0e-6 at K = 1024, 2.1e-6 at 2048).  fp32 outputs therefore break the chain every 512 of K into
@@ -16,7 +19,6 @@
 // memory.  A CTA takes at least 80 KB of shared memory and at most 256 columns, so that the two that fit on an SM (or one and two
 // of the LM head's, 72 KB and 128 columns at the least and most) never need more than the 512 there are.
 // Every mbarrier wait is bounded; one that runs out sets DR_ERRF_TIMEOUT, and the rows that lack its sums are not written.
-#include <stdlib.h>
 #include "dr_tc.cuh"
 #include "linear_epilogue.cuh"
 
@@ -36,7 +38,8 @@ struct ClusterPlan {
     int nb;            // weight rows per tile (MMA N): nb output columns, or nb / 2 when gated
     int split;         // CTAs (one cluster) that share K
     int box_rows;      // tokens per tile that are loaded
-    int piece_chunks;  // K chunks per accumulator
+    int issuers;       // warps that issue products: 2, or 1 where the tensor memory holds no second sums
+    int piece_chunks;  // K chunks of an issuer per accumulator
     int stages;
     int cols;          // tensor-memory columns
     uint32_t recv_at;  // where the parts of a cluster's other CTAs go, behind the ring and the CTA's own sums
@@ -77,7 +80,7 @@ __global__ void __launch_bounds__(kThreads)
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t full[kMaxStages], empty[kMaxStages], done, parts;
     __shared__ uint32_t tmem_base;
-    __shared__ int gave_up, issued;   // a wait ran out; chunks whose copies were issued (and all before, but for a stalled one)
+    __shared__ int gave_up, issued[2];   // a wait ran out; the chunk at which each producer ended
     __shared__ float bias[kMaxCols];   // of the tile's sums
 
     const LinearParams &p = args.p;
@@ -108,10 +111,10 @@ __global__ void __launch_bounds__(kThreads)
             tc::mbar_init(&full[s], 1);
             tc::mbar_init(&empty[s], 1);
         }
-        tc::mbar_init(&done, 1);
+        tc::mbar_init(&done, pl.issuers);
         tc::mbar_init(&parts, 1);
         if (S > 1 && mine > 0) tc::mbar_expect_tx(&parts, (uint32_t)((S - 1) * mine * pl.nb) * 4);
-        gave_up = issued = 0;
+        gave_up = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 2) {
@@ -142,15 +145,14 @@ __global__ void __launch_bounds__(kThreads)
             bias[j] = n < p.N ? lin::bf16_at(p.bias, j < bn ? n : (int64_t)p.N + n) : 0.f;
         }
 
-    if (warp == 0) {
-        // stage s of round r waits for the products of round r - 1.  (Test hook: the stalled tile's producer starts at
-        // chunk 1, so the wait for chunk 0 runs out.)
+    if (warp < 2) {
+        // stage s of round r waits for the products of round r - 1.  (Test hook: the stalled tile's first chunk is left out, so
+        // the wait for it runs out.)
         const bool stalled = (int)(blockIdx.z * gridDim.y + blockIdx.y) == p.stall_tile;
-        const int first = stalled ? 1 : 0;
-        int c = first;
-        for (int s = c % stages, r = c / stages; c < chunks; ++c) {
+        int c = warp;
+        for (int s = c % stages, r = c / stages; c < chunks; c += 2) {
             if (r > 0 && !tc::mbar_wait(&empty[s], (r - 1) & 1, &gave_up)) break;
-            if (tc::elect_one()) {
+            if (tc::elect_one() && !(stalled && c == 0)) {
                 const int k = (c_begin + c) * kChunkK;
                 tc::mbar_expect_tx(&full[s], bytes_x + bytes_w);
                 const uint32_t w_at = sw + s * bytes_w;
@@ -159,17 +161,21 @@ __global__ void __launch_bounds__(kThreads)
                 tma_load_2d(sx + s * bytes_x, &map_x, k, t0, &full[s]);
             }
             __syncwarp();
-            if (++s == stages) {
-                s = 0;
+            s += 2;
+            if (s >= stages) {
+                s -= stages;
                 ++r;
             }
         }
-        if (lane == 0) issued = c;
-    } else if (warp == 1) {
+        if (lane == 0) issued[warp] = c;
+    } else if (warp < 2 + pl.issuers) {
         const uint32_t idesc = tc::instr_desc(kRows, pl.nb, false, false);
         const uint64_t dx = tc::smem_desc(sx), dw = tc::smem_desc(sw);
+        const int issuer = warp - 2, step = pl.issuers;
         bool ok = true;
-        for (int c = 0, s = 0, r = 0, in_piece = 0, d = tmem; c < chunks; ++c) {
+        int c = issuer, in_piece = 0;
+        uint32_t d = tmem + issuer * pl.nb;
+        for (int s = c % stages, r = c / stages; c < chunks; c += step) {
             if (!tc::mbar_wait(&full[s], r & 1, &gave_up)) {
                 ok = false;
                 break;
@@ -185,10 +191,11 @@ __global__ void __launch_bounds__(kThreads)
             __syncwarp();
             if (++in_piece == pl.piece_chunks) {
                 in_piece = 0;
-                d += pl.nb;
+                d += step * pl.nb;
             }
-            if (++s == stages) {
-                s = 0;
+            s += step;
+            if (s >= stages) {
+                s -= stages;
                 ++r;
             }
         }
@@ -202,8 +209,9 @@ __global__ void __launch_bounds__(kThreads)
     if (gave_up) {
         // copies in flight end by themselves; wait for them before this CTA's shared memory goes away
         if (warp == 0 && lane == 0) {
-            for (int c = max(p.stall_tile < 0 ? 0 : 1, issued - stages); c < issued; ++c)
-                tc::mbar_drain(&full[c % stages], (c / stages) & 1);
+            for (int w = 0; w < 2; ++w)
+                for (int c = issued[w] - 2; c >= max(p.stall_tile < 0 ? 0 : 1, issued[w] - stages); c -= 2)
+                    tc::mbar_drain(&full[c % stages], (c / stages) & 1);
             flag_error(p.err, DR_ERRF_TIMEOUT);
         }
         ok = false;
@@ -213,7 +221,11 @@ __global__ void __launch_bounds__(kThreads)
 
     // Sums to shared memory, [row][nb] fp32 in 16-byte pieces that the row turns, so that a warp's stores spread over the banks.
     // The ring is idle: all its copies were multiplied.
-    const int nb = pl.nb, pieces = (chunks + pl.piece_chunks - 1) / pl.piece_chunks;
+    const int nb = pl.nb;
+    // accumulators in use: an issuer has one for each piece_chunks of its chunks, in turn with the other's
+    const auto ceil_div = [](int a, int b) { return (a + b - 1) / b; };
+    const int pieces = pl.issuers == 1 ? ceil_div(chunks, pl.piece_chunks)
+                                       : ceil_div((chunks + 1) / 2, pl.piece_chunks) + ceil_div(chunks / 2, pl.piece_chunks);
     if (ok && (warp & 3) * 32 < rows) {
         const int row = (warp & 3) * 32 + lane;
         const uint32_t from = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -224,16 +236,15 @@ __global__ void __launch_bounds__(kThreads)
             tc::ld16(from + c, v);
             tc::wait_ld();
             tc::pin16(v);
-            if constexpr (kF32)
 #pragma unroll 1
-                for (int i = 1; i < pieces; ++i) {
-                    float more[16];
-                    tc::ld16(from + i * nb + c, more);
-                    tc::wait_ld();
-                    tc::pin16(more);
+            for (int i = 1; i < pieces; ++i) {
+                float more[16];
+                tc::ld16(from + i * nb + c, more);
+                tc::wait_ld();
+                tc::pin16(more);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) v[j] += more[j];
-                }
+                for (int j = 0; j < 16; ++j) v[j] += more[j];
+            }
             if (row < rows)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) to[(c / 4 + j) ^ (row & 7)] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
@@ -262,18 +273,21 @@ __global__ void __launch_bounds__(kThreads)
         ok = __syncthreads_and(ok);
         cluster_arrive();   // this CTA has its parts; none exits before the copies out of it have landed
     }
-    if (ok) {
+    const auto part = [&](int s, int r) {   // the sums of this CTA's row r that CTA s of the cluster made
+        return s == rank ? reinterpret_cast<const float *>(staged) + (rank * share + r) * nb
+                         : reinterpret_cast<const float *>(received) + ((s - (s > rank)) * mine + r) * nb;
+    };
+    if (ok && p.vec_out && (!p.residual || p.vec_res)) {   // rows of whole 16-byte pieces: 16 columns a thread
         const int groups = bn / 16;
 #pragma unroll 1
         for (int i = threadIdx.x; i < mine * groups; i += kThreads) {
-            const int r = i / groups, g = i - r * groups, row = rank * share + r, key = row & 7;
+            const int r = i / groups, g = i - r * groups, key = (rank * share + r) & 7;
             float a[16], b[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) a[j] = b[j] = 0.f;
 #pragma unroll 1
             for (int s = 0; s < S; ++s) {
-                const float4 *from = s == rank ? reinterpret_cast<const float4 *>(staged) + row * (nb / 4)
-                                               : reinterpret_cast<const float4 *>(received) + ((s - (s > rank)) * mine + r) * (nb / 4);
+                const float4 *from = reinterpret_cast<const float4 *>(part(s, r));
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
                     const float4 v = from[(4 * g + h) ^ key];
@@ -287,35 +301,55 @@ __global__ void __launch_bounds__(kThreads)
                     }
                 }
             }
-            lin::finish16<kF32>(p, bias + g * 16, bias + bn + g * 16, t0 + row, n0 + g * 16, a, b);
+            lin::finish16<kF32>(p, bias + g * 16, bias + bn + g * 16, t0 + rank * share + r, n0 + g * 16, a, b);
+        }
+    } else if (ok) {   // a column of eight rows a thread: a warp's accesses lie side by side
+#pragma unroll 1
+        for (int i = threadIdx.x; i < (mine + 7) / 8 * bn; i += kThreads) {
+            const int c = i % bn, r0 = i / bn * 8;
+            float a[8], b[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) a[j] = b[j] = 0.f;
+#pragma unroll 1
+            for (int s = 0; s < S; ++s)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int r = min(r0 + j, mine - 1), key = (rank * share + r) & 7;
+                    const float *from = part(s, r);
+                    a[j] += from[((c / 4) ^ key) * 4 + c % 4];
+                    if (p.gated) b[j] += from[(((bn + c) / 4) ^ key) * 4 + c % 4];
+                }
+            lin::finish_column8<kF32>(p, bias[c], bias[p.gated ? bn + c : c], t0 + rank * share + r0, mine - r0, n0 + c, a, b);
         }
     }
     if (S > 1) cluster_wait();
 }
 
-// Tile width and split of a call.
+// Tile width and split of a call.  Measured with one wave of tiles of 32 against 64 rows of W, us: 128 tokens 1024 -> 4096 5.9
+// and 7.0, 4096 -> 1024 (4 CTAs per tile) 7.3 and 8.1; 256 tokens 1024 -> 4096, where tiles of 32 are two waves, 7.8 and 6.7.
+// A CTA of a split keeps 16 chunks: 128 tokens 1024 -> 1536 whole 5.4, halved 5.6; 4096 -> 1024 in 2, 4, 8 parts 8.7, 7.3, 8.3.
 ClusterPlan make_plan(const LinearParams &p, int sms) {
     ClusterPlan pl;
     const int chunks = (p.K + kChunkK - 1) / kChunkK;
-    const int mtiles = (p.T + kRows - 1) / kRows;
-    pl.nb = 64;
+    const int64_t mtiles = (p.T + kRows - 1) / kRows;
+    const auto tiles = [&](int nb) {
+        const int bn = p.gated ? nb / 2 : nb;
+        return mtiles * ((p.N + bn - 1) / bn);
+    };
+    pl.nb = tiles(32) <= sms ? 32 : tiles(64) <= sms ? 64 : 128;
     pl.split = 1;
-    {
-        const int bn = p.gated ? pl.nb / 2 : pl.nb;
-        const int64_t tiles = (int64_t)mtiles * ((p.N + bn - 1) / bn);
-        while (pl.split < 8 && tiles * pl.split * 2 <= sms && pl.split * 4 <= chunks) pl.split *= 2;
-    }
-    if (getenv("LNB")) pl.nb = atoi(getenv("LNB"));
-    if (getenv("LSP")) pl.split = atoi(getenv("LSP"));
+    while (pl.split < 8 && tiles(pl.nb) * pl.split * 2 <= sms && chunks / (2 * pl.split) >= 16) pl.split *= 2;
     const int rows = p.T < kRows ? p.T : kRows;
     pl.box_rows = (rows + 7) / 8 * 8;
     const int most = (chunks + pl.split - 1) / pl.split;   // chunks of a CTA
-    pl.piece_chunks = most;
-    int pieces = 1;
+    pl.issuers = 2 * pl.nb <= kMaxCols ? 2 : 1;
+    const int own_chunks = (most + pl.issuers - 1) / pl.issuers;
+    pl.piece_chunks = own_chunks;
+    int pieces = pl.issuers;
     if (p.out_f32) {
         pl.piece_chunks = kPieceChunks;
-        while ((most + pl.piece_chunks - 1) / pl.piece_chunks > kMaxCols / pl.nb) ++pl.piece_chunks;
-        pieces = (most + pl.piece_chunks - 1) / pl.piece_chunks;
+        while (pl.issuers * ((own_chunks + pl.piece_chunks - 1) / pl.piece_chunks) > kMaxCols / pl.nb) ++pl.piece_chunks;
+        pieces = pl.issuers * ((own_chunks + pl.piece_chunks - 1) / pl.piece_chunks);
     }
     pl.cols = 32;
     while (pl.cols < pl.nb * pieces) pl.cols *= 2;
@@ -326,9 +360,11 @@ ClusterPlan make_plan(const LinearParams &p, int sms) {
         const size_t over = n * stage > (size_t)(n * pl.box_rows + kRows) * 128 ? n * stage : (size_t)(n * pl.box_rows + kRows) * 128;
         return over > own ? over : own;
     };
-    int lim = getenv("LST") ? atoi(getenv("LST")) : kMaxStages;
-    pl.stages = most < lim ? most : lim;
-    while (pl.stages > 2 && 1024 + ring(pl.stages) + parts > kMaxSmem) --pl.stages;
+    // an even number: a stage always belongs to the even or the odd chunks, so a warp that waits for one of its rounds has seen
+    // the round before (a wait by parity cannot tell a phase from the one two before it)
+    pl.stages = most < kMaxStages ? most : kMaxStages;
+    pl.stages += pl.stages & 1;
+    while (pl.stages > 2 && 1024 + ring(pl.stages) + parts > kMaxSmem) pl.stages -= 2;
     pl.recv_at = (uint32_t)ring(pl.stages);
     pl.smem = 1024 + ring(pl.stages) + parts;
     if (pl.smem < kMinSmem) pl.smem = kMinSmem;

@@ -106,7 +106,7 @@ __device__ __forceinline__ void finish16(const LinearParams &p, const float *bia
     const int have = p.N - n;
     if (have <= 0) return;
     uint4 r[kWords / 4];
-    const bool quick_res = p.vec_res && have >= 16;
+    const bool quick_res = p.residual && have >= 16;
     const int64_t res_at = (int64_t)t * p.res_stride + n;
     if (quick_res) {   // on its way during the arithmetic
         const uint4 *from = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p.residual) + res_at * (kF32 ? 4 : 2));
@@ -147,7 +147,7 @@ __device__ __forceinline__ void finish16(const LinearParams &p, const float *bia
     }
     const LinearOut &o = p.out[out_of(p, n)];
     const int64_t at = (int64_t)t * o.stride + (n - o.col0);
-    if (p.vec_out && have >= 16) {
+    if (have >= 16) {
         uint4 *to = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(o.ptr) + at * (kF32 ? 4 : 2));
 #pragma unroll
         for (int i = 0; i < kWords / 4; ++i) {
@@ -165,6 +165,47 @@ __device__ __forceinline__ void finish16(const LinearParams &p, const float *bia
                 if constexpr (kF32) static_cast<float *>(o.ptr)[at + i] = a[i];
                 else static_cast<uint16_t *>(o.ptr)[at + i] = f32_to_bf16_rn(a[i]);
             }
+    }
+}
+
+// The same for one column n of eight tokens t .. t+7, the first `have` of them: the lanes of a warp take columns side by side,
+// where rows are not of whole 16-byte pieces.
+template <bool kF32>
+__device__ __forceinline__ void finish_column8(const LinearParams &p, float bias_a, float bias_b, int t, int have, int n, float (&a)[8],
+                                               float (&b)[8]) {
+    if (n >= p.N) return;
+    float r[8];
+    if (p.residual) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int64_t at = (int64_t)(t + i) * p.res_stride + n;
+            if (i < have) {
+                if constexpr (kF32) r[i] = static_cast<const float *>(p.residual)[at];
+                else r[i] = __uint_as_float((uint32_t)static_cast<const uint16_t *>(p.residual)[at] << 16);
+            }
+        }
+    }
+    if (p.bias) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            a[i] += bias_a;
+            b[i] += bias_b;
+        }
+    }
+    activate<8>(a, p.act);
+    if (p.gated) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) a[i] *= b[i];
+    }
+    const LinearOut &o = p.out[out_of(p, n)];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int64_t at = (int64_t)(t + i) * o.stride + (n - o.col0);
+        if (p.residual) a[i] += r[i];
+        if (i < have) {
+            if constexpr (kF32) static_cast<float *>(o.ptr)[at] = a[i];
+            else static_cast<uint16_t *>(o.ptr)[at] = f32_to_bf16_rn(a[i]);
+        }
     }
 }
 

@@ -21,7 +21,6 @@
 // epilogue warps' registers.
 // Every mbarrier wait is bounded; after one that runs out the pair's further tiles are not written, and copies and
 // products in flight are waited for before it exits.
-#include <stdlib.h>
 #include <type_traits>
 
 #include "dr_tc.cuh"
@@ -581,7 +580,6 @@ cudaError_t most_pairs(int sms, int *pairs) {
 int tile_width(const LinearParams &p, int pairs) {
     const int64_t token_tiles = (p.T + kTileT - 1) / kTileT;
     int w = kTileW;
-    if (getenv("LTW")) return atoi(getenv("LTW"));
     while (w > 64) {
         const int cols = p.gated ? w / 4 : w / 2;
         if (token_tiles * ((p.N + cols - 1) / cols) > pairs) break;
