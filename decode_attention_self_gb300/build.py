@@ -20,7 +20,7 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libdecoderattn.so")
 SOURCES = ["dr_api.cu", "attention.cu", "kv_append.cu", "sampler.cu", "heads.cu", "lm_head_tc.cu",
            "rope_append.cu", "attn_tokens.cu", "attn_tiles.cu", "dr_prompt_api.cu",
-           "linear.cu", "linear_cluster.cu", "linear_tiles.cu", "residual_norm.cu", "dr_layer_api.cu"]
+           "linear.cu", "linear_rows.cu", "linear_cluster.cu", "linear_tiles.cu", "residual_norm.cu", "dr_layer_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

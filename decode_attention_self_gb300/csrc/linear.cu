@@ -48,12 +48,14 @@ bool takes_tiles(const LinearParams &p, int sms) {
 }  // namespace
 
 int linear_tiles(const LinearParams &p, int sms) {
+    if (p.T <= kLinearRows) return 0;
     return takes_tiles(p, sms) ? linear_tiles_tiles(p, sms) : linear_cluster_tiles(p, sms);
 }
 
 cudaError_t launch_linear(const LinearParams &p, cudaStream_t stream) {
     const int sms = current_device_sms();
     if (sms <= 0) return cudaErrorInvalidDevice;
+    if (p.T <= kLinearRows) return launch_linear_rows(p, sms, stream);
     return takes_tiles(p, sms) ? launch_linear_tiles(p, sms, stream) : launch_linear_cluster(p, sms, stream);
 }
 

@@ -79,9 +79,9 @@ __device__ __forceinline__ void activate(float *v, int act) {
     }
 }
 
-__device__ __forceinline__ float bf16_at(const uint16_t *p, int64_t i) {
-    return __uint_as_float((uint32_t)__ldg(p + i) << 16);
-}
+// Plain loads throughout: what another kernel may still be writing while this one starts must not be read before the wait, and
+// the compiler may move read-only loads.
+__device__ __forceinline__ float bf16_at(const uint16_t *p, int64_t i) { return __uint_as_float((uint32_t)p[i] << 16); }
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));

@@ -99,13 +99,13 @@ __device__ __forceinline__ void norm(float (&v)[V][8], const NormParams &n, cons
         if (d >= p.Dm) break;
         float w[8], b[8];
         if (n.weight) {
-            unpack8(ld_ro16(n.weight + d), w);
+            unpack8(*reinterpret_cast<const uint4 *>(n.weight + d), w);
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j) w[j] = 1.f;
         }
         if (n.bias) {
-            unpack8(ld_ro16(n.bias + d), b);
+            unpack8(*reinterpret_cast<const uint4 *>(n.bias + d), b);
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[i][j] = fmaf(v[i][j] * r, w[j], b[j]);
         } else {
