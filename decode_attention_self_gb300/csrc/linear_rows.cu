@@ -174,21 +174,45 @@ __global__ void __launch_bounds__(kMaxWarps * 32) linear_rows_kernel(const __gri
     }
 }
 
-template <int kBlocks>
-cudaError_t launch(const LinearParams &p, int warps, cudaStream_t stream) {
-    const int cols = (p.gated ? kBlocks / 2 : kBlocks) * 8;
-    const dim3 grid((unsigned)((p.N + cols - 1) / cols));
-    return p.T > 8 ? launch_kernel(linear_rows_kernel<true, kBlocks>, grid, dim3((unsigned)(warps * 32)), 0, stream, 1, p)
-                   : launch_kernel(linear_rows_kernel<false, kBlocks>, grid, dim3((unsigned)(warps * 32)), 0, stream, 1, p);
+using Kernel = void (*)(const LinearParams);
+Kernel kernel_of(bool tall, int blocks) {
+    return tall ? (blocks == 2 ? linear_rows_kernel<true, 2> : linear_rows_kernel<true, 1>)
+                : (blocks == 2 ? linear_rows_kernel<false, 2> : linear_rows_kernel<false, 1>);
+}
+
+// CTAs of such a kernel that an SM holds (asked once per device).
+int resident(bool tall, int blocks, int warps) {
+    static std::atomic<int> known[64][2][2][3];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+    std::atomic<int> *slot = dev < 64 ? &known[dev][tall][blocks - 1][warps == 16 ? 2 : warps == 8 ? 1 : 0] : nullptr;
+    if (slot && (n = slot->load(std::memory_order_relaxed)) > 0) return n;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel_of(tall, blocks), warps * 32, 0) != cudaSuccess || n < 1) n = 1;
+    if (slot) slot->store(n, std::memory_order_relaxed);
+    return n;
 }
 
 }  // namespace
 
+// Blocks of 8 weight rows per CTA (1 or 2) and warps: as many warps as leave the grid one wave and each of them a full group
+// of loads; of the two block counts the one with more warps; where they tie, one, or two where the tokens' rows (more than 8 of
+// them, read by every CTA) are worth sharing.  Measured (one and two blocks, warps, us): one token 1024 -> 4096 3.4 (4) and 3.1 (8),
+// 1536 -> 6144 5.3 (4) and 6.1 (4), 4096 -> 1024 4.0 (16) and 5.2 (16); 16 tokens 1536 -> 6144 9.6 (4) and 6.5 (4).
 cudaError_t launch_linear_rows(const LinearParams &p, int sms, cudaStream_t stream) {
-    const int rows = p.gated ? 2 * p.N : p.N;
-    const int warps = p.K > 1024 ? 16 : 8;
-    if (p.gated || rows >= 16 * 4 * sms) return launch<2>(p, warps, stream);
-    return launch<1>(p, warps, stream);
+    const bool tall = p.T > 8;
+    const int rows = p.gated ? 2 * p.N : p.N, steps = (p.K + 31) / 32;
+    int best = 0, warps = 0;
+    for (int blocks = p.gated ? 2 : 1; blocks <= 2; ++blocks) {
+        const int ctas = (rows + blocks * 8 - 1) / (blocks * 8);
+        int w = kMaxWarps;
+        while (w > 4 && (ctas > sms * resident(tall, blocks, w) || steps < w * kGroup)) w /= 2;
+        if (w > warps || (w == warps && tall && ctas >= sms)) {
+            best = blocks;
+            warps = w;
+        }
+    }
+    const int cols = (p.gated ? best / 2 : best) * 8;
+    return launch_kernel(kernel_of(tall, best), dim3((unsigned)((p.N + cols - 1) / cols)), dim3((unsigned)(warps * 32)), 0, stream, 1, p);
 }
 
 }  // namespace dr
