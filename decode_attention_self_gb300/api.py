@@ -565,14 +565,20 @@ assert struct.calcsize("@Pqi4x") == ctypes.sizeof(dr_linear_out)
 assert struct.calcsize("@ifPP") == ctypes.sizeof(dr_norm)
 
 
-def _tokens(t, dev: int, dtype, T: int, n: int, name: str):
-    """(address, elements between tokens) of a [T, n] tensor whose rows are dense but may lie apart."""
-    if t.get_device() != dev or t.dtype is not dtype or t.shape != (T, n):
-        _refuse(t, dev, dtype, (T, n), name)
+def _tokens(t, dev: int, dtype, shape, name: str):
+    """(address, elements between tokens) of a tensor of shape (T, n) whose rows are dense but may lie apart."""
+    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape:
+        _refuse(t, dev, dtype, shape, name)
+    if shape[0] == 1:
+        if shape[1] > 1 and t.stride(1) != 1:
+            raise ValueError(f"{name} must have contiguous rows")
+        return t.data_ptr(), (shape[1] + 7) & -8   # no second row: any stride will do
+    if t.is_contiguous():
+        return t.data_ptr(), shape[1]
     s0, s1 = t.stride()
-    if s1 != 1 and n > 1:
+    if s1 != 1 and shape[1] > 1:
         raise ValueError(f"{name} must have contiguous rows")
-    return t.data_ptr(), (s0 if T > 1 else -(-n // 8) * 8)
+    return t.data_ptr(), s0
 
 
 def _float_type(t, name: str):
@@ -594,35 +600,42 @@ def dr_linear(x: torch.Tensor, W: torch.Tensor, out, bias: torch.Tensor | None =
     x, out and residual may be slices with dense rows; residual may be out itself.
     """
     dev = _device()
-    if x.dim() != 2 or W.dim() != 2:
+    shape, wshape = x.shape, W.shape
+    if len(shape) != 2 or len(wshape) != 2:
         raise ValueError("x must be [T, K] and W [N, K]")
-    T, K = x.shape
-    rows = W.shape[0]
-    xp, xs = _tokens(x, dev, _BF16, T, K, "x")
-    outs = out if isinstance(out, (list, tuple)) else (out,)
-    if not outs:
-        raise ValueError("out must hold at least one tensor")
-    od = _float_type(outs[0], "out")
-    N = 0
-    packed = b""
-    for o in outs:
-        if o.dim() != 2:
+    T, K = shape
+    rows = wshape[0]
+    xp, xs = _tokens(x, dev, _BF16, shape, "x")
+    if wshape[1] != K or W.get_device() != dev or W.dtype is not _BF16 or not W.is_contiguous():
+        _refuse(W, dev, _BF16, (rows, K), "W")
+    if isinstance(out, torch.Tensor):
+        od, dt = _float_type(out, "out"), out.dtype
+        if out.dim() != 2:
             raise ValueError("out must be [T, N]")
-        n = o.shape[1]
-        op, os_ = _tokens(o, dev, outs[0].dtype, T, n, "out")
-        packed += _pack_linear_out(op, os_, n)
-        N += n
+        N, n_outs = out.shape[1], 1
+        packed = _pack_linear_out(*_tokens(out, dev, dt, (T, N), "out"), N)
+    else:
+        n_outs = len(out)
+        if n_outs < 1 or n_outs > DR_LINEAR_MAX_OUTS:
+            raise ValueError(f"out must hold 1 to {DR_LINEAR_MAX_OUTS} tensors")
+        od, dt = _float_type(out[0], "out"), out[0].dtype
+        N, packed = 0, b""
+        for o in out:
+            if o.dim() != 2:
+                raise ValueError("out must be [T, N]")
+            n = o.shape[1]
+            packed += _pack_linear_out(*_tokens(o, dev, dt, (T, n), "out"), n)
+            N += n
     if rows != (2 * N if gated else N):
         raise ValueError(f"W must have {2 * N if gated else N} rows for {N} columns, has {rows}")
-    if act not in _ACTS:
+    code = _ACTS.get(act)
+    if code is None:
         raise ValueError(f"act must be one of {sorted(k for k in _ACTS if k)}, got {act!r}")
-    wp = _vec(W, dev, _BF16, rows * K, "W")
-    if residual is None:
-        rp = rs = 0
-    else:
-        rp, rs = _tokens(residual, dev, outs[0].dtype, T, N, "residual")
-    opts = _pack_linear_opts(_ACTS[act], 1 if gated else 0, _vec(bias, dev, _BF16, rows, "bias") or 0, rp, rs)
-    args = (xp, xs, wp, opts, T, K, N, packed, len(outs), od, _vec(err_flag, dev, _I32, 1, "err_flag"))
+    rp, rs = (0, 0) if residual is None else _tokens(residual, dev, dt, (T, N), "residual")
+    bp = 0 if bias is None else _vec(bias, dev, _BF16, rows, "bias")
+    opts = _pack_linear_opts(code, 1 if gated else 0, bp, rp, rs)
+    args = (xp, xs, W.data_ptr(), opts, T, K, N, packed, n_outs, od,
+            None if err_flag is None else _vec(err_flag, dev, _I32, 1, "err_flag"))
     if _stall_tile is None:
         st = _lib.dr_linear(*args, _stream_arg(stream, dev))
     else:
@@ -647,14 +660,13 @@ class Norm:
     bias: torch.Tensor | None = None
 
 
-def _norm_arg(n: Norm | None, dev: int, Dm: int, name: str):
-    if n is None:
-        return None
+def _norm_arg(n: Norm, dev: int, Dm: int, name: str):
     kind = _NORMS.get(n.kind)
     if kind is None:
         raise ValueError(f"{name}.kind must be one of {sorted(_NORMS)}, got {n.kind!r}")
-    return _pack_norm(kind, n.eps, _vec(n.weight, dev, _BF16, Dm, name + ".weight") or 0,
-                      _vec(n.bias, dev, _BF16, Dm, name + ".bias") or 0)
+    w, b = n.weight, n.bias
+    return _pack_norm(kind, n.eps, 0 if w is None else _vec(w, dev, _BF16, Dm, name + ".weight"),
+                      0 if b is None else _vec(b, dev, _BF16, Dm, name + ".bias"))
 
 
 def dr_residual_norm(x: torch.Tensor, y: torch.Tensor | None = None, pre: Norm | None = None,
@@ -666,28 +678,30 @@ def dr_residual_norm(x: torch.Tensor, y: torch.Tensor | None = None, pre: Norm |
     tokens or [T, Dm].
     """
     dev = _device()
-    if x.dim() != 2:
+    shape = x.shape
+    if len(shape) != 2:
         raise ValueError("x must be [T, Dm]")
-    T, Dm = x.shape
+    T, Dm = shape
     xd = _float_type(x, "x")
-    xp, xs = _tokens(x, dev, x.dtype, T, Dm, "x")
+    xp, xs = _tokens(x, dev, x.dtype, shape, "x")
     hd, rp, rs, hp, hs, yp, ys, yd, gp, gs = DR_BF16, None, 0, None, 0, None, 0, DR_BF16, None, 0
     if residual is not None:
         hd = _float_type(residual, "residual")
-        rp, rs = _tokens(residual, dev, residual.dtype, T, Dm, "residual")
+        rp, rs = _tokens(residual, dev, residual.dtype, shape, "residual")
     if h is not None:
         hd = _float_type(h, "h")
-        hp, hs = _tokens(h, dev, h.dtype if residual is None else residual.dtype, T, Dm, "h")
+        hp, hs = _tokens(h, dev, h.dtype if residual is None else residual.dtype, shape, "h")
     if y is not None:
         yd = _float_type(y, "y")
-        yp, ys = _tokens(y, dev, y.dtype, T, Dm, "y")
+        yp, ys = _tokens(y, dev, y.dtype, shape, "y")
     if gate is not None:
         if gate.dim() == 1:
             gp = _vec(gate, dev, _BF16, Dm, "gate")
         else:
-            gp, gs = _tokens(gate, dev, _BF16, T, Dm, "gate")
-    st = _lib.dr_residual_norm(xp, xs, xd, _norm_arg(post, dev, Dm, "post"), gp, gs, scale, rp, rs, hp, hs, hd,
-                               _norm_arg(pre, dev, Dm, "pre"), yp, ys, yd, T, Dm, _stream_arg(stream, dev))
+            gp, gs = _tokens(gate, dev, _BF16, shape, "gate")
+    st = _lib.dr_residual_norm(xp, xs, xd, None if post is None else _norm_arg(post, dev, Dm, "post"), gp, gs, scale, rp, rs, hp,
+                               hs, hd, None if pre is None else _norm_arg(pre, dev, Dm, "pre"), yp, ys, yd, T, Dm,
+                               _stream_arg(stream, dev))
     if st:
         raise DrError("dr_residual_norm", st)
 
