@@ -6,7 +6,10 @@
 // A row lives in the registers of `lanes` threads (8 elements per vector, V vectors per thread), so each input is read once and
 // each output written once, and layer norm takes its mean first and the squared differences after, without cancellation.
 // Everything between the loads and the stores is fp32; y comes from h before it is rounded for storing.  Row sums go
-// over warp shuffles, and over shared memory where a row has several warps, in a fixed order.
+// over warp shuffles, and over shared memory where a row has several warps, in a fixed order.  Memory bounds many rows,
+// latency few; arithmetic comes close to both (packed fp32 instructions: a row of 1024 took 690 instructions a lane without).
+// CTAs that stay and take rows in turn were slower than a grid of short ones (fp32 stream of 65536 x 1024: 145 us, 116 now): the
+// SMs run at different rates, and a fixed share of the rows cannot follow that.
 #include "dr_layer.h"
 #include "dr_device.cuh"
 
@@ -21,43 +24,57 @@ template <bool f32>
 struct Raw;
 template <>
 struct Raw<false> {
+    using T = uint16_t;
     uint4 w;
-    __device__ __forceinline__ void load(const void *p, int64_t i) {
-        w = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + i);
+    __device__ __forceinline__ void load(const T *p) { w = *reinterpret_cast<const uint4 *>(p); }
+    __device__ __forceinline__ void get(float2 (&f)[4]) const {
+        f[0] = make_float2(bf16_lo(w.x), bf16_hi(w.x));
+        f[1] = make_float2(bf16_lo(w.y), bf16_hi(w.y));
+        f[2] = make_float2(bf16_lo(w.z), bf16_hi(w.z));
+        f[3] = make_float2(bf16_lo(w.w), bf16_hi(w.w));
     }
-    __device__ __forceinline__ void get(float (&f)[8]) const { unpack8(w, f); }
 };
 template <>
 struct Raw<true> {
+    using T = float;
     float4 a, b;
-    __device__ __forceinline__ void load(const void *p, int64_t i) {
-        const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
-        a = q[0];
-        b = q[1];
+    __device__ __forceinline__ void load(const T *p) {
+        a = reinterpret_cast<const float4 *>(p)[0];
+        b = reinterpret_cast<const float4 *>(p)[1];
     }
-    __device__ __forceinline__ void get(float (&f)[8]) const {
-        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    __device__ __forceinline__ void get(float2 (&f)[4]) const {
+        f[0] = make_float2(a.x, a.y);
+        f[1] = make_float2(a.z, a.w);
+        f[2] = make_float2(b.x, b.y);
+        f[3] = make_float2(b.z, b.w);
     }
 };
+using Bf16 = Raw<false>;
 
-__device__ __forceinline__ void store8(void *p, int64_t i, bool f32, const float (&f)[8]) {
+__device__ __forceinline__ uint32_t pack2(float2 v) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(v.y), "f"(v.x));
+    return r;
+}
+__device__ __forceinline__ void store8(void *p, int64_t i, bool f32, const float2 (&f)[4]) {
     if (f32) {
         float4 *q = reinterpret_cast<float4 *>(static_cast<float *>(p) + i);
-        q[0] = make_float4(f[0], f[1], f[2], f[3]);
-        q[1] = make_float4(f[4], f[5], f[6], f[7]);
+        q[0] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+        q[1] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
     } else {
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            w[j] = (uint32_t)f32_to_bf16_rn(f[2 * j]) | ((uint32_t)f32_to_bf16_rn(f[2 * j + 1]) << 16);
-        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + i) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + i) = make_uint4(pack2(f[0]), pack2(f[1]), pack2(f[2]), pack2(f[3]));
     }
 }
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
-// The sum over a row's threads, the same in each of them.  `lanes`: a power of two; of 64 and more a CTA holds one row.
+// The sum over a row's threads, the same in each of them.  `lanes`: a power of two in a warp, or the warps of a CTA.
 __device__ __forceinline__ float row_sum(float v, int lanes, float *shared) {
-    for (int o = min(lanes, 32) / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    if (lanes >= 32) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    } else {
+        for (int o = lanes / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    }
     if (lanes > 32) {
         const int warps = lanes / 32;
         if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = v;
@@ -68,139 +85,183 @@ __device__ __forceinline__ float row_sum(float v, int lanes, float *shared) {
     return v;
 }
 
-// The norm of the row that v holds (elements past the row are 0 and stay out of the sums).
-template <int V>
-__device__ __forceinline__ void norm(float (&v)[V][8], const NormParams &n, const ResidualNormParams &p, int first, int lanes,
-                                     float *shared) {
-    const float inv = 1.0f / (float)p.Dm;
+// The norm of the row that v holds (elements past the row are 0 and stay out of the sums).  kFull: the row fills its threads.
+template <int V, bool kFull>
+__device__ __forceinline__ void norm(float2 (&v)[V][4], const NormParams &n, int Dm, int d0, int dstep, int lanes, float *shared) {
+    const float inv = 1.0f / (float)Dm;
     if (n.kind == DR_NORM_LAYER) {
-        float s = 0.f;
+        float2 s = both(0.f);
 #pragma unroll
         for (int i = 0; i < V; ++i)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) s += v[i][j];
-        const float mean = row_sum(s, lanes, shared) * inv;
+            for (int j = 0; j < 4; ++j) s = __fadd2_rn(s, v[i][j]);
+        const float2 mean = both(-row_sum(s.x + s.y, lanes, shared) * inv);
         shared += kMaxWarps;
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            if ((first + i * lanes) * 8 < p.Dm)
+            if (kFull || d0 + i * dstep < Dm)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[i][j] -= mean;
+                for (int j = 0; j < 4; ++j) v[i][j] = __fadd2_rn(v[i][j], mean);
     }
-    float s = 0.f;
+    float2 s = both(0.f);
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s = fmaf(v[i][j], v[i][j], s);
-    const float r = 1.0f / sqrtf(row_sum(s, lanes, shared) * inv + n.eps);
+        for (int j = 0; j < 4; ++j) s = __ffma2_rn(v[i][j], v[i][j], s);
+    const float2 r = both(1.0f / sqrtf(row_sum(s.x + s.y, lanes, shared) * inv + n.eps));
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int d = (first + i * lanes) * 8;
-        if (d >= p.Dm) break;
-        float w[8], b[8];
-        if (n.weight) {
-            unpack8(*reinterpret_cast<const uint4 *>(n.weight + d), w);
-        } else {
+        const int d = d0 + i * dstep;
+        if (!kFull && d >= Dm) break;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) w[j] = 1.f;
-        }
-        if (n.bias) {
-            unpack8(*reinterpret_cast<const uint4 *>(n.bias + d), b);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = fmaf(v[i][j] * r, w[j], b[j]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * r * w[j];
-        }
+        for (int j = 0; j < 4; ++j) v[i][j] = __fmul2_rn(v[i][j], r);
     }
+    if (n.weight)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int d = d0 + i * dstep;
+            if (!kFull && d >= Dm) break;
+            Bf16 raw;
+            float2 w[4];
+            raw.load(n.weight + d);
+            raw.get(w);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[i][j] = __fmul2_rn(v[i][j], w[j]);
+        }
+    if (n.bias)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int d = d0 + i * dstep;
+            if (!kFull && d >= Dm) break;
+            Bf16 raw;
+            float2 b[4];
+            raw.load(n.bias + d);
+            raw.get(b);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[i][j] = __fadd2_rn(v[i][j], b[j]);
+        }
 }
 
-template <int V, bool kXf32, bool kResF32>
-__global__ void __launch_bounds__(kMaxRowThreads) residual_norm_kernel(const ResidualNormParams p, const int lanes) {
-    __shared__ float sums[4][kMaxWarps];   // a row of slots per sum, so that none is written again while it is read
+// A CTA takes `rounds` times as many rows as its threads hold, one after the other; a row's inputs are on their way while the
+// row before is stored and normed.
+template <int V, bool kXf32, bool kResF32, bool kFull>
+__global__ void __launch_bounds__(kMaxRowThreads) residual_norm_kernel(const ResidualNormParams p, const int lanes, const int rounds) {
+    // slots per sum and, in turn, per row: none is written again while a slower warp may read it
+    __shared__ float sums[2][4][kMaxWarps];
     const int per_cta = blockDim.x / lanes;
-    const int first = threadIdx.x & (lanes - 1);
-    const int64_t row = (int64_t)blockIdx.x * per_cta + threadIdx.x / lanes;
-    const bool live = row < p.T;   // the other threads take part in the shuffles
-    const int64_t t = live ? row : 0;
+    const int d0 = (lanes > 32 ? threadIdx.x : threadIdx.x & (lanes - 1)) * 8, dstep = lanes * 8;
+    const int64_t base = (int64_t)blockIdx.x * rounds * per_cta;
+    int64_t row = base + threadIdx.x / lanes;
     pdl_wait();
     Raw<kXf32> rx[V];
     Raw<kResF32> rr[V];
-    uint4 rg[V];
+    Bf16 rg[V];
+    const auto load = [&](int64_t t) {
+        const auto *x = static_cast<const typename Raw<kXf32>::T *>(p.x) + t * p.x_stride + d0;
+        const auto *r = static_cast<const typename Raw<kResF32>::T *>(p.residual) + t * p.res_stride + d0;
+        const uint16_t *g = p.gate + t * p.gate_stride + d0;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int d = (first + i * lanes) * 8;
-        if (d < p.Dm) {
-            rx[i].load(p.x, t * p.x_stride + d);
-            if (p.residual) rr[i].load(p.residual, t * p.res_stride + d);
-            if (p.gate) rg[i] = *reinterpret_cast<const uint4 *>(p.gate + t * p.gate_stride + d);
+        for (int i = 0; i < V; ++i)
+            if (kFull || d0 + i * dstep < p.Dm) rx[i].load(x + i * dstep);
+        if (p.residual)
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (kFull || d0 + i * dstep < p.Dm) rr[i].load(r + i * dstep);
+        if (p.gate)
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (kFull || d0 + i * dstep < p.Dm) rg[i].load(g + i * dstep);
+    };
+    if (row < p.T) load(row);
+    // all threads of a CTA stay together: those without a row take part in the shuffles and barriers
+#pragma unroll 1
+    for (int round = 0; round < rounds && base + (int64_t)round * per_cta < p.T; ++round, row += per_cta) {
+        const bool live = row < p.T;
+        float2 v[V][4];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            if (live && (kFull || d0 + i * dstep < p.Dm)) {
+                rx[i].get(v[i]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[i][j] = both(0.f);
+            }
         }
-    }
-    float v[V][8];
+        if (p.post.kind != DR_NORM_NONE) norm<V, kFull>(v, p.post, p.Dm, d0, dstep, lanes, sums[round & 1][0]);
+        if (p.gate)
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        if ((first + i * lanes) * 8 < p.Dm) {
-            rx[i].get(v[i]);
-        } else {
+            for (int i = 0; i < V; ++i) {
+                if (!kFull && d0 + i * dstep >= p.Dm) break;
+                float2 g[4];
+                rg[i].get(g);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
-        }
-    }
-    pdl_trigger();
-    if (p.post.kind != DR_NORM_NONE) norm<V>(v, p.post, p, first, lanes, sums[0]);
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int d = (first + i * lanes) * 8;
-        if (d >= p.Dm) break;
-        if (p.gate) {
-            float g[8];
-            unpack8(rg[i], g);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] *= g[j];
-        }
+                for (int j = 0; j < 4; ++j) v[i][j] = __fmul2_rn(v[i][j], g[j]);
+            }
         if (p.residual) {
-            float r[8];
-            rr[i].get(r);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = fmaf(v[i][j], p.scale, r[j]);
-        } else {
+            for (int i = 0; i < V; ++i) {
+                if (!live || (!kFull && d0 + i * dstep >= p.Dm)) break;
+                float2 r[4];
+                rr[i].get(r);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] *= p.scale;
+                for (int j = 0; j < 4; ++j) v[i][j] = __ffma2_rn(v[i][j], both(p.scale), r[j]);
+            }
+        } else if (p.scale != 1.0f) {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[i][j] = __fmul2_rn(v[i][j], both(p.scale));
         }
-        if (p.h && live) store8(p.h, t * p.h_stride + d, p.res_f32, v[i]);
-    }
-    if (!p.y) return;
-    if (p.pre.kind != DR_NORM_NONE) norm<V>(v, p.pre, p, first, lanes, sums[2]);
+        if (round + 1 < rounds && row + per_cta < p.T) load(row + per_cta);
+        if (round == 0) pdl_trigger();
+        if (p.h && live)
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int d = (first + i * lanes) * 8;
-        if (d < p.Dm && live) store8(p.y, t * p.y_stride + d, p.y_f32, v[i]);
+            for (int i = 0; i < V; ++i)
+                if (kFull || d0 + i * dstep < p.Dm) store8(p.h, row * p.h_stride + d0 + i * dstep, p.res_f32, v[i]);
+        if (!p.y) continue;
+        if (p.pre.kind != DR_NORM_NONE) norm<V, kFull>(v, p.pre, p.Dm, d0, dstep, lanes, sums[round & 1][2]);
+        if (live)
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (kFull || d0 + i * dstep < p.Dm) store8(p.y, row * p.y_stride + d0 + i * dstep, p.y_f32, v[i]);
     }
 }
 
-template <int V>
-cudaError_t launch(const ResidualNormParams &p, int lanes, int threads, cudaStream_t stream) {
-    const int per_cta = threads / lanes;
-    const dim3 grid((unsigned)((p.T + (int64_t)per_cta - 1) / per_cta));
-    auto kern = p.x_f32 ? (p.res_f32 ? residual_norm_kernel<V, true, true> : residual_norm_kernel<V, true, false>)
-                        : (p.res_f32 ? residual_norm_kernel<V, false, true> : residual_norm_kernel<V, false, false>);
-    return launch_kernel(kern, grid, dim3((unsigned)threads), 0, stream, 1, p, lanes);
+template <int V, bool kFull>
+auto kernel_of(bool x_f32, bool res_f32) {
+    return x_f32 ? (res_f32 ? residual_norm_kernel<V, true, true, kFull> : residual_norm_kernel<V, true, false, kFull>)
+                 : (res_f32 ? residual_norm_kernel<V, false, true, kFull> : residual_norm_kernel<V, false, false, kFull>);
 }
 
 }  // namespace
 
 cudaError_t launch_residual_norm(const ResidualNormParams &p, cudaStream_t stream) {
+    const int sms = current_device_sms();
+    if (sms <= 0) return cudaErrorInvalidDevice;
+    // Few rows: 8 elements a thread, for the shortest way through a row.  Many: 32 a thread (16 where a stream is fp32), which
+    // leaves less to do per element and, up to 1024 elements, no barrier; and two rows in turn, the second's inputs on their way
+    // during the first.  65536 x 1024, RMS norm of a sum, us: 8 elements 97, 16 a thread 84, 32 83, 32 and two rows 80, four rows
+    // 81 (80 at the rate of a copy); 128 x 1024, layer norm: 8 elements 2.1, 16 2.4, 32 2.4.
     const int vecs = p.Dm / 8;
-    int V = 1, lanes = 8;
-    while (lanes < 256 && lanes < vecs) lanes *= 2;
-    while (V < 4 && V * lanes < vecs) V *= 2;
-    while (lanes < kMaxRowThreads && V * lanes < vecs) lanes *= 2;
-    const int threads = lanes < 64 ? 128 : lanes;
-    switch (V) {
-        case 1: return launch<1>(p, lanes, threads, stream);
-        case 2: return launch<2>(p, lanes, threads, stream);
-        default: return launch<4>(p, lanes, threads, stream);
+    int V = p.T <= 2 * sms ? 1 : p.x_f32 || p.res_f32 ? 2 : 4;
+    while (V > 1 && vecs <= V * 4) V /= 2;
+    while ((vecs + V - 1) / V > kMaxRowThreads) V *= 2;
+    int lanes = (vecs + V - 1) / V;   // threads of a row: a power of two in a warp, or whole warps
+    if (lanes > 32) {
+        lanes = (lanes + 31) / 32 * 32;
+    } else {
+        int n = 8;
+        while (n < lanes) n *= 2;
+        lanes = n;
     }
+    const int threads = lanes <= 32 ? 128 : lanes, per_cta = threads / lanes;
+    const int rounds = (int64_t)p.T / per_cta >= 32LL * sms ? 2 : 1;
+    const bool full = V * lanes == vecs, xf = p.x_f32, rf = p.res_f32;
+    const auto kernel = V == 1 ? (full ? kernel_of<1, true>(xf, rf) : kernel_of<1, false>(xf, rf))
+                        : V == 2 ? (full ? kernel_of<2, true>(xf, rf) : kernel_of<2, false>(xf, rf))
+                                 : (full ? kernel_of<4, true>(xf, rf) : kernel_of<4, false>(xf, rf));
+    const int64_t rows = (int64_t)per_cta * rounds;
+    return launch_kernel(kernel, dim3((unsigned)((p.T + rows - 1) / rows)), dim3((unsigned)threads), 0, stream, 1, p, lanes, rounds);
 }
 
 }  // namespace dr
