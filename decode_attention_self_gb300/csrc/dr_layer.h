@@ -40,8 +40,7 @@ bool encode_matrix(CUtensorMap *map, const void *ptr, bool f32, int64_t rows, in
 // Output tiles of a launch as the test hook counts them; 0 where the call runs a kernel without waits.
 int linear_tiles(const LinearParams &p, int sms);
 cudaError_t launch_linear(const LinearParams &p, cudaStream_t stream);
-// Up to 16 tokens (kLinearRows).
-constexpr int kLinearRows = 16;
+// Up to 32 tokens.
 cudaError_t launch_linear_rows(const LinearParams &p, int sms, cudaStream_t stream);
 cudaError_t launch_linear_cluster(const LinearParams &p, int sms, cudaStream_t stream);
 int linear_cluster_tiles(const LinearParams &p, int sms);

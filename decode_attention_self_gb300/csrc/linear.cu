@@ -37,26 +37,38 @@ bool encode_matrix(CUtensorMap *map, const void *ptr, bool f32, int64_t rows, in
 
 namespace {
 
-// Whether the pairs of CTAs take a call: where the other kernel's tiles, 128 tokens by 64 weight rows, are more than one wave.
-// Measured, us: 512 tokens 1024 -> 4096 (256 such tiles) 9.0 against 9.1, 1024 tokens 1024 -> 4096 11.5 against 15;
-// 1024 tokens 4096 -> 1024 (128 tiles) 18 against 12.6, 256 tokens 1024 -> 4096 (128) 8.3 against 6.7.
-bool takes_tiles(const LinearParams &p, int sms) {
+enum class Way { kRows, kCluster, kTiles };
+
+// Which kernel takes a call; measured on both sides of each border, us.
+// Rows or cluster: 16 tokens 8192 -> 8192 24 and 29; 32 tokens, where a CTA's tokens weigh more, 1024 -> 1536 3.5 and 5.2,
+// 1024 -> 4096 4.9 and 6.4, 4096 -> 1024 6.8 and 6.6, 1536 -> 6144 10.0 and 8.0, 8192 -> 8192 44 and 29.
+// Cluster or tiles: the pairs take what is more than one wave of tiles of 128 tokens by 64 weight rows.  512 tokens 1024 -> 4096
+// (256 such tiles) 9.1 and 9.0, 1024 tokens 1024 -> 4096 (512) 15 and 11.5; 1024 tokens 4096 -> 1024 (128) 12.6 and 18, 256
+// tokens 1024 -> 4096 (128) 6.7 and 8.3.
+Way way_of(const LinearParams &p, int sms) {
     const int64_t rows = (int64_t)p.N * (p.gated ? 2 : 1);
-    return ((int64_t)p.T + 127) / 128 * ((rows + 63) / 64) > sms;
+    if (p.T <= 16 || (p.T <= 32 && rows * p.K <= 6 << 20)) return Way::kRows;
+    return ((int64_t)p.T + 127) / 128 * ((rows + 63) / 64) > sms ? Way::kTiles : Way::kCluster;
 }
 
 }  // namespace
 
 int linear_tiles(const LinearParams &p, int sms) {
-    if (p.T <= kLinearRows) return 0;
-    return takes_tiles(p, sms) ? linear_tiles_tiles(p, sms) : linear_cluster_tiles(p, sms);
+    switch (way_of(p, sms)) {
+        case Way::kRows: return 0;
+        case Way::kCluster: return linear_cluster_tiles(p, sms);
+        default: return linear_tiles_tiles(p, sms);
+    }
 }
 
 cudaError_t launch_linear(const LinearParams &p, cudaStream_t stream) {
     const int sms = current_device_sms();
     if (sms <= 0) return cudaErrorInvalidDevice;
-    if (p.T <= kLinearRows) return launch_linear_rows(p, sms, stream);
-    return takes_tiles(p, sms) ? launch_linear_tiles(p, sms, stream) : launch_linear_cluster(p, sms, stream);
+    switch (way_of(p, sms)) {
+        case Way::kRows: return launch_linear_rows(p, sms, stream);
+        case Way::kCluster: return launch_linear_cluster(p, sms, stream);
+        default: return launch_linear_tiles(p, sms, stream);
+    }
 }
 
 }  // namespace dr

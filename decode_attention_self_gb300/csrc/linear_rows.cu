@@ -1,7 +1,7 @@
-// Matrix product with an epilogue for up to 16 tokens: out = residual + act(x W^T + bias), bound by W's way from memory.
+// Matrix product with an epilogue for up to 32 tokens: out = residual + act(x W^T + bias), bound by W's way from memory.
 //
 // A CTA takes 8 or 16 output columns and all tokens; its warps share K in steps of 32.  W goes from memory to the operand
-// registers of mma.sync (m16n8k16) without shared memory: the tokens are the 16 rows of one operand, 8 weight rows the
+// registers of mma.sync (m16n8k16) without shared memory: 16 tokens are the rows of one operand, 8 weight rows the
 // columns of the other, and since a sum over k may take its terms in any order, a lane's 16 bytes of a row (8 values of k)
 // serve as the k slots that the instruction gives that lane, four for one product and four for the next, in both operands
 // alike.  A warp's load reads 64 contiguous bytes of each of 8 rows; a group of kGroup steps is on its way while the group
@@ -13,9 +13,9 @@
 namespace dr {
 namespace {
 
-constexpr int kGroup = 4;        // steps of 32 k in flight per warp, and again as many ahead
 constexpr int kMaxWarps = 16;
-constexpr int kRows = 16;
+// steps of 32 k in flight per warp, and again as many ahead
+template <int kEights> constexpr int kGroup = kEights > 2 ? 2 : 4;
 
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
@@ -31,10 +31,12 @@ __device__ __forceinline__ uint4 load_once(const void *p) {
     return r;
 }
 
-// kTall: more than 8 tokens;  kBlocks: blocks of 8 weight rows (gated: the second half multiplies the first)
-template <bool kTall, int kBlocks>
+// kEights: tokens in eights, 1, 2 or 4;  kBlocks: blocks of 8 weight rows (gated: the second half multiplies the first)
+template <int kEights, int kBlocks>
 __global__ void __launch_bounds__(kMaxWarps * 32) linear_rows_kernel(const __grid_constant__ LinearParams p) {
-    __shared__ float sums[kMaxWarps][kRows][kBlocks * 8];
+    constexpr int kTiles = (kEights + 1) / 2, kSteps = kGroup<kEights>, kRows = kEights * 8;
+    extern __shared__ float sums_raw[];
+    const auto sums = reinterpret_cast<float (*)[kRows][kBlocks * 8]>(sums_raw);   // of each warp
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
     const int g = lane >> 2, t = lane & 3;
     const int blocks = p.gated ? kBlocks / 2 : kBlocks;   // of output columns
@@ -60,16 +62,21 @@ __global__ void __launch_bounds__(kMaxWarps * 32) linear_rows_kernel(const __gri
         in_w[i] = row < all_rows;
         w[i] = p.W + (int64_t)(in_w[i] ? row : 0) * p.K;
     }
-    const bool in_x0 = g < p.T, in_x1 = kTall && g + 8 < p.T;
-    const uint16_t *x0 = p.x + (in_x0 ? g : 0) * p.x_stride, *x1 = p.x + (in_x1 ? g + 8 : 0) * p.x_stride;
+    bool in_x[kEights];
+    const uint16_t *x[kEights];
+#pragma unroll
+    for (int e = 0; e < kEights; ++e) {
+        in_x[e] = e * 8 + g < p.T;
+        x[e] = p.x + (in_x[e] ? e * 8 + g : 0) * p.x_stride;
+    }
     const uint4 zero = make_uint4(0, 0, 0, 0);
 
-    float acc[kBlocks][4] = {};
-    uint4 wv[kGroup][kBlocks];
+    float acc[kTiles][kBlocks][4] = {};
+    uint4 wv[kSteps][kBlocks];
     const int steps = (p.K + 31) / 32;
     const auto load_w = [&](int s0) {
 #pragma unroll
-        for (int u = 0; u < kGroup; ++u) {
+        for (int u = 0; u < kSteps; ++u) {
             const int k = (s0 + u * warps) * 32 + t * 8;
 #pragma unroll
             for (int i = 0; i < kBlocks; ++i) wv[u][i] = k < p.K && in_w[i] ? load_once(w[i] + k) : zero;
@@ -77,37 +84,43 @@ __global__ void __launch_bounds__(kMaxWarps * 32) linear_rows_kernel(const __gri
     };
     load_w(warp);
 #pragma unroll 1
-    for (int s0 = warp; s0 < steps; s0 += kGroup * warps) {
-        uint4 xa[kGroup], xb[kTall ? kGroup : 1], now[kGroup][kBlocks];
+    for (int s0 = warp; s0 < steps; s0 += kSteps * warps) {
+        uint4 xv[kSteps][kEights], now[kSteps][kBlocks];
 #pragma unroll
-        for (int u = 0; u < kGroup; ++u) {
+        for (int u = 0; u < kSteps; ++u) {
             const int k = (s0 + u * warps) * 32 + t * 8;
-            xa[u] = k < p.K && in_x0 ? *reinterpret_cast<const uint4 *>(x0 + k) : zero;
-            if constexpr (kTall) xb[u] = k < p.K && in_x1 ? *reinterpret_cast<const uint4 *>(x1 + k) : zero;
+#pragma unroll
+            for (int e = 0; e < kEights; ++e) xv[u][e] = k < p.K && in_x[e] ? *reinterpret_cast<const uint4 *>(x[e] + k) : zero;
 #pragma unroll
             for (int i = 0; i < kBlocks; ++i) now[u][i] = wv[u][i];
         }
-        if (s0 + kGroup * warps < steps) load_w(s0 + kGroup * warps);
-        float part[kBlocks][4] = {};
+        if (s0 + kSteps * warps < steps) load_w(s0 + kSteps * warps);
+        float part[kTiles][kBlocks][4] = {};
 #pragma unroll
-        for (int u = 0; u < kGroup; ++u) {
-            const uint4 b = kTall ? xb[kTall ? u : 0] : zero;
+        for (int u = 0; u < kSteps; ++u)
 #pragma unroll
-            for (int i = 0; i < kBlocks; ++i) {
-                mma(part[i], xa[u].x, b.x, xa[u].y, b.y, now[u][i].x, now[u][i].y);
-                mma(part[i], xa[u].z, b.z, xa[u].w, b.w, now[u][i].z, now[u][i].w);
+            for (int m = 0; m < kTiles; ++m) {
+                const uint4 a = xv[u][2 * m], b = kEights > 1 ? xv[u][kEights > 1 ? 2 * m + 1 : 0] : zero;
+#pragma unroll
+                for (int i = 0; i < kBlocks; ++i) {
+                    mma(part[m][i], a.x, b.x, a.y, b.y, now[u][i].x, now[u][i].y);
+                    mma(part[m][i], a.z, b.z, a.w, b.w, now[u][i].z, now[u][i].w);
+                }
             }
+#pragma unroll
+        for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+            for (int i = 0; i < kBlocks; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[m][i][j] += part[m][i][j];
+    }
+#pragma unroll
+    for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+        for (int i = 0; i < kBlocks; ++i) {
+            *reinterpret_cast<float2 *>(&sums[warp][16 * m + g][i * 8 + 2 * t]) = make_float2(acc[m][i][0], acc[m][i][1]);
+            if (kEights > 1) *reinterpret_cast<float2 *>(&sums[warp][(16 * m + g + 8) % kRows][i * 8 + 2 * t]) = make_float2(acc[m][i][2], acc[m][i][3]);
         }
-#pragma unroll
-        for (int i = 0; i < kBlocks; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][j] += part[i][j];
-    }
-#pragma unroll
-    for (int i = 0; i < kBlocks; ++i) {
-        *reinterpret_cast<float2 *>(&sums[warp][g][i * 8 + 2 * t]) = make_float2(acc[i][0], acc[i][1]);
-        if (kTall) *reinterpret_cast<float2 *>(&sums[warp][g + 8][i * 8 + 2 * t]) = make_float2(acc[i][2], acc[i][3]);
-    }
     __syncthreads();
 
     // a pair of columns a thread
@@ -175,19 +188,24 @@ __global__ void __launch_bounds__(kMaxWarps * 32) linear_rows_kernel(const __gri
 }
 
 using Kernel = void (*)(const LinearParams);
-Kernel kernel_of(bool tall, int blocks) {
-    return tall ? (blocks == 2 ? linear_rows_kernel<true, 2> : linear_rows_kernel<true, 1>)
-                : (blocks == 2 ? linear_rows_kernel<false, 2> : linear_rows_kernel<false, 1>);
+Kernel kernel_of(int eights, int blocks) {
+    return eights == 4 ? (blocks == 2 ? linear_rows_kernel<4, 2> : linear_rows_kernel<4, 1>)
+           : eights == 2 ? (blocks == 2 ? linear_rows_kernel<2, 2> : linear_rows_kernel<2, 1>)
+                         : (blocks == 2 ? linear_rows_kernel<1, 2> : linear_rows_kernel<1, 1>);
 }
+size_t sums_bytes(int eights, int blocks, int warps) { return (size_t)warps * eights * 8 * blocks * 8 * sizeof(float); }
 
 // CTAs of such a kernel that an SM holds (asked once per device).
-int resident(bool tall, int blocks, int warps) {
-    static std::atomic<int> known[64][2][2][3];
+int resident(int eights, int blocks, int warps) {
+    static std::atomic<int> known[64][3][2][3];
     int dev = 0, n = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 1;
-    std::atomic<int> *slot = dev < 64 ? &known[dev][tall][blocks - 1][warps == 16 ? 2 : warps == 8 ? 1 : 0] : nullptr;
+    std::atomic<int> *slot = dev < 64 ? &known[dev][eights / 2][blocks - 1][warps / 8] : nullptr;
     if (slot && (n = slot->load(std::memory_order_relaxed)) > 0) return n;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel_of(tall, blocks), warps * 32, 0) != cudaSuccess || n < 1) n = 1;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel_of(eights, blocks), warps * 32, sums_bytes(eights, blocks, warps)) !=
+            cudaSuccess ||
+        n < 1)
+        n = 1;
     if (slot) slot->store(n, std::memory_order_relaxed);
     return n;
 }
@@ -199,20 +217,21 @@ int resident(bool tall, int blocks, int warps) {
 // them, read by every CTA) are worth sharing.  Measured (one and two blocks, warps, us): one token 1024 -> 4096 3.4 (4) and 3.1 (8),
 // 1536 -> 6144 5.3 (4) and 6.1 (4), 4096 -> 1024 4.0 (16) and 5.2 (16); 16 tokens 1536 -> 6144 9.6 (4) and 6.5 (4).
 cudaError_t launch_linear_rows(const LinearParams &p, int sms, cudaStream_t stream) {
-    const bool tall = p.T > 8;
+    const int eights = p.T <= 8 ? 1 : p.T <= 16 ? 2 : 4;
     const int rows = p.gated ? 2 * p.N : p.N, steps = (p.K + 31) / 32;
     int best = 0, warps = 0;
     for (int blocks = p.gated ? 2 : 1; blocks <= 2; ++blocks) {
         const int ctas = (rows + blocks * 8 - 1) / (blocks * 8);
         int w = kMaxWarps;
-        while (w > 4 && (ctas > sms * resident(tall, blocks, w) || steps < w * kGroup)) w /= 2;
-        if (w > warps || (w == warps && tall && ctas >= sms)) {
+        while (w > 4 && (ctas > sms * resident(eights, blocks, w) || steps < w * (eights == 4 ? kGroup<4> : kGroup<1>))) w /= 2;
+        if (w > warps || (w == warps && eights > 1 && ctas >= sms)) {
             best = blocks;
             warps = w;
         }
     }
     const int cols = (p.gated ? best / 2 : best) * 8;
-    return launch_kernel(kernel_of(tall, best), dim3((unsigned)((p.N + cols - 1) / cols)), dim3((unsigned)(warps * 32)), 0, stream, 1, p);
+    return launch_kernel(kernel_of(eights, best), dim3((unsigned)((p.N + cols - 1) / cols)), dim3((unsigned)(warps * 32)),
+                         sums_bytes(eights, best, warps), stream, 1, p);
 }
 
 }  // namespace dr
