@@ -16,8 +16,9 @@
 // 1e-9 K (measured: 1.0e-6 at K = 1024, 2.1e-6 at 2048).  fp32 outputs therefore break the chain every 512 of K into
 // accumulators of their own (pieces), added in fp32; bf16 outputs, whose rounding is 1000 times that, do not.
 // Tensor memory and clusters: a CTA that waits for its cluster must not keep another cluster's CTA waiting for tensor
-// memory.  A CTA takes at least 80 KB of shared memory and at most 256 columns, so that the two that fit on an SM (or one and two
-// of the LM head's, 72 KB and 128 columns at the least and most) never need more than the 512 there are.
+// memory.  A CTA of a cluster takes at least 80 KB of shared memory and at most 256 columns, so that the two that fit on an SM (or
+// one and two of the LM head's, 72 KB and 128 columns at the least and most) never need more than the 512 there are.  A CTA that
+// shares its tile with no other waits for nobody and may take all 512.
 // Every mbarrier wait is bounded; one that runs out sets DR_ERRF_TIMEOUT, and the rows that lack its sums are not written.
 #include "dr_tc.cuh"
 #include "linear_epilogue.cuh"
@@ -30,7 +31,8 @@ constexpr int kRows = 128;        // tokens per tile (MMA M)
 constexpr int kChunkK = 64;       // K per stage: one 128-byte swizzled row
 constexpr int kMaxStages = 8;
 constexpr int kPieceChunks = 8;   // fp32 outputs: K of 512 per accumulator
-constexpr int kMaxCols = 256;     // tensor-memory columns of a CTA (see above); also the largest NB
+constexpr int kMaxNb = 64;        // weight rows per tile
+constexpr int kIssuers = 2;
 constexpr size_t kMinSmem = 80 * 1024;
 constexpr size_t kMaxSmem = 225 * 1024;
 
@@ -38,7 +40,6 @@ struct ClusterPlan {
     int nb;            // weight rows per tile (MMA N): nb output columns, or nb / 2 when gated
     int split;         // CTAs (one cluster) that share K
     int box_rows;      // tokens per tile that are loaded
-    int issuers;       // warps that issue products: 2, or 1 where the tensor memory holds no second sums
     int piece_chunks;  // K chunks of an issuer per accumulator
     int stages;
     int cols;          // tensor-memory columns
@@ -81,7 +82,7 @@ __global__ void __launch_bounds__(kThreads)
     __shared__ uint64_t full[kMaxStages], empty[kMaxStages], done, parts;
     __shared__ uint32_t tmem_base;
     __shared__ int gave_up, issued[2];   // a wait ran out; the chunk at which each producer ended
-    __shared__ float bias[kMaxCols];   // of the tile's sums
+    __shared__ float bias[kMaxNb];   // of the tile's sums
 
     const LinearParams &p = args.p;
     const ClusterPlan &pl = args.plan;
@@ -111,7 +112,7 @@ __global__ void __launch_bounds__(kThreads)
             tc::mbar_init(&full[s], 1);
             tc::mbar_init(&empty[s], 1);
         }
-        tc::mbar_init(&done, pl.issuers);
+        tc::mbar_init(&done, kIssuers);
         tc::mbar_init(&parts, 1);
         if (S > 1 && mine > 0) tc::mbar_expect_tx(&parts, (uint32_t)((S - 1) * mine * pl.nb) * 4);
         gave_up = 0;
@@ -168,10 +169,10 @@ __global__ void __launch_bounds__(kThreads)
             }
         }
         if (lane == 0) issued[warp] = c;
-    } else if (warp < 2 + pl.issuers) {
+    } else if (warp < 2 + kIssuers) {
         const uint32_t idesc = tc::instr_desc(kRows, pl.nb, false, false);
         const uint64_t dx = tc::smem_desc(sx), dw = tc::smem_desc(sw);
-        const int issuer = warp - 2, step = pl.issuers;
+        const int issuer = warp - 2, step = kIssuers;
         bool ok = true;
         int c = issuer, in_piece = 0;
         uint32_t d = tmem + issuer * pl.nb;
@@ -224,8 +225,7 @@ __global__ void __launch_bounds__(kThreads)
     const int nb = pl.nb;
     // accumulators in use: an issuer has one for each piece_chunks of its chunks, in turn with the other's
     const auto ceil_div = [](int a, int b) { return (a + b - 1) / b; };
-    const int pieces = pl.issuers == 1 ? ceil_div(chunks, pl.piece_chunks)
-                                       : ceil_div((chunks + 1) / 2, pl.piece_chunks) + ceil_div(chunks / 2, pl.piece_chunks);
+    const int pieces = ceil_div((chunks + 1) / 2, pl.piece_chunks) + ceil_div(chunks / 2, pl.piece_chunks);
     if (ok && (warp & 3) * 32 < rows) {
         const int row = (warp & 3) * 32 + lane;
         const uint32_t from = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -336,23 +336,18 @@ ClusterPlan make_plan(const LinearParams &p, int sms) {
         const int bn = p.gated ? nb / 2 : nb;
         return mtiles * ((p.N + bn - 1) / bn);
     };
-    pl.nb = tiles(32) <= sms ? 32 : tiles(64) <= sms ? 64 : 128;
+    pl.nb = tiles(32) <= sms ? 32 : kMaxNb;   // (more than one wave of tiles of 64 goes to the pairs)
     pl.split = 1;
     while (pl.split < 8 && tiles(pl.nb) * pl.split * 2 <= sms && chunks / (2 * pl.split) >= 16) pl.split *= 2;
     const int rows = p.T < kRows ? p.T : kRows;
     pl.box_rows = (rows + 7) / 8 * 8;
     const int most = (chunks + pl.split - 1) / pl.split;   // chunks of a CTA
-    pl.issuers = 2 * pl.nb <= kMaxCols ? 2 : 1;
-    const int own_chunks = (most + pl.issuers - 1) / pl.issuers;
-    pl.piece_chunks = own_chunks;
-    int pieces = pl.issuers;
-    if (p.out_f32) {
-        pl.piece_chunks = kPieceChunks;
-        while (pl.issuers * ((own_chunks + pl.piece_chunks - 1) / pl.piece_chunks) > kMaxCols / pl.nb) ++pl.piece_chunks;
-        pieces = pl.issuers * ((own_chunks + pl.piece_chunks - 1) / pl.piece_chunks);
-    }
+    const int own_chunks = (most + kIssuers - 1) / kIssuers, max_cols = pl.split > 1 ? 256 : 512;
+    const auto pieces = [&] { return kIssuers * ((own_chunks + pl.piece_chunks - 1) / pl.piece_chunks); };
+    pl.piece_chunks = p.out_f32 ? kPieceChunks : own_chunks;
+    while (pieces() * pl.nb > max_cols) ++pl.piece_chunks;
     pl.cols = 32;
-    while (pl.cols < pl.nb * pieces) pl.cols *= 2;
+    while (pl.cols < pl.nb * pieces()) pl.cols *= 2;
     // shared memory: the ring, with what its last stage's products may read past it, or after it the CTA's own sums; the parts
     const size_t stage = (size_t)(pl.box_rows + pl.nb) * 128, own = parts_bytes(rows, pl);
     const size_t parts = pl.split > 1 ? parts_bytes(rows + pl.split, pl) : 0;
@@ -372,6 +367,8 @@ ClusterPlan make_plan(const LinearParams &p, int sms) {
 }
 
 }  // namespace
+
+bool linear_cluster_keeps(const LinearParams &p, int sms) { return !p.out_f32 || make_plan(p, sms).piece_chunks <= kPieceChunks; }
 
 int linear_cluster_tiles(const LinearParams &p, int sms) {
     const ClusterPlan pl = make_plan(p, sms);

@@ -42,7 +42,7 @@ def run_and_check(api, T, K, N, act=None, gated=False, bias=True, residual=False
 
 
 TOKENS = [1, 2, 3, 7, 8, 9, 15, 16, 17, 24, 31, 32, 33, 48, 63, 64, 65, 100, 127, 128, 129, 200, 255, 256, 257, 300, 513, 700,
-          1030]
+          1030, 2700]
 
 
 @pytest.mark.parametrize("T", TOKENS)
@@ -51,7 +51,7 @@ def test_token_counts(api, T, out):
     run_and_check(api, T, 1024, 1024, "gelu", bias=True, residual=True, out=out, seed=T)
 
 
-@pytest.mark.parametrize("T", [1, 5, 17, 64, 130, 400, 2100])
+@pytest.mark.parametrize("T", [1, 5, 17, 30, 64, 130, 400, 2100, 19600])
 @pytest.mark.parametrize("K,N", [(8, 1), (8, 64), (16, 7), (24, 9), (56, 63), (64, 8), (72, 65), (128, 100), (200, 127),
                                  (264, 129), (1000, 1089), (520, 257), (64, 2048)])
 def test_odd_sizes(api, T, K, N):
@@ -75,13 +75,13 @@ def test_prompt_sizes(api, T, K, N, out, act, gated, residual):
 
 @pytest.mark.parametrize("act", [None, "none", "relu", "gelu", "gelu_tanh", "silu"])
 @pytest.mark.parametrize("gated", [False, True])
-@pytest.mark.parametrize("T", [3, 40, 1300])
+@pytest.mark.parametrize("T", [3, 14, 25, 40, 1300, 5000])
 def test_activations(api, act, gated, T):
     for bias, residual, out in ((True, True, F32), (False, False, BF16)):
         run_and_check(api, T, 320, 200, act, gated, bias, residual, out, seed=T)
 
 
-@pytest.mark.parametrize("T", [1, 6, 33, 150, 1500])
+@pytest.mark.parametrize("T", [1, 6, 20, 33, 150, 1500, 5000])
 @pytest.mark.parametrize("out", [BF16, F32])
 @pytest.mark.parametrize("pad", [1, 3, 8, 64])
 def test_slices_and_places(api, T, out, pad):
@@ -103,7 +103,7 @@ def test_slices_and_places(api, T, out, pad):
     assert (around == 7.0).all()
 
 
-@pytest.mark.parametrize("T", [1, 12, 90, 1400])
+@pytest.mark.parametrize("T", [1, 12, 31, 90, 1400, 6000])
 @pytest.mark.parametrize("out", [BF16, F32])
 @pytest.mark.parametrize("widths", [(64,), (128, 64, 64), (64, 192, 64, 9), (1024, 256, 256), (320, 1), (64, 64, 64, 64)])
 def test_outputs_share_the_columns(api, T, out, widths):
@@ -119,7 +119,7 @@ def test_outputs_share_the_columns(api, T, out, widths):
         at += w
 
 
-@pytest.mark.parametrize("T", [1, 10, 70, 300, 2000])
+@pytest.mark.parametrize("T", [1, 10, 29, 70, 300, 2000, 5000])
 @pytest.mark.parametrize("out", [BF16, F32])
 @pytest.mark.parametrize("N", [512, 509])
 def test_residual_in_place(api, T, out, N):
@@ -129,18 +129,18 @@ def test_residual_in_place(api, T, out, N):
     assert_within(r, ref, tol, "in place")
 
 
-@pytest.mark.parametrize("T", [1, 16, 100, 1000])
-def test_fp32_outputs_keep_long_sums(api, T):
+@pytest.mark.parametrize("T,N", [(1, 256), (16, 256), (30, 256), (100, 256), (1000, 256), (1000, 1024), (5000, 256)])
+def test_fp32_outputs_keep_long_sums(api, T, N):
     # A chain of tensor-core additions over K = 8192 drifts by 8e-6 of the value.  Broken every 512 of K it loses at most
     # one bit of the partial sum at each of 32 additions, two thirds of the value on average: 32 * 2/3 * 2^-23.
-    x, W = randn((T, 8192), 1), randn((256, 8192), 2, 8192 ** -0.5)
-    o = torch.empty((T, 256), dtype=F32, device="cuda")
+    x, W = randn((T, 8192), 1), randn((N, 8192), 2, 8192 ** -0.5)
+    o = torch.empty((T, N), dtype=F32, device="cuda")
     api.dr_linear(x.cuda(), W.cuda(), o)
     ref = x.double() @ W.double().T
     assert ((o.double().cpu() - ref).norm() / ref.norm()).item() <= 32 * 2 / 3 * 2.0 ** -23
 
 
-@pytest.mark.parametrize("T", [1, 9, 65, 260, 1800])
+@pytest.mark.parametrize("T", [1, 9, 18, 65, 260, 1800, 7000])
 @pytest.mark.parametrize("gated", [False, True])
 def test_nan_and_infinity_stay_in_their_rows_and_columns(api, T, gated):
     K, N = 200, 130
@@ -163,7 +163,7 @@ def test_nan_and_infinity_stay_in_their_rows_and_columns(api, T, gated):
 
 
 @pytest.mark.parametrize("act,at_minus", [("relu", 0.0), ("gelu", 0.0), ("gelu_tanh", 0.0), ("silu", 0.0), (None, -np.inf)])
-@pytest.mark.parametrize("T", [2, 50, 1200])
+@pytest.mark.parametrize("T", [2, 24, 50, 1200, 19600])
 def test_activations_at_the_ends(api, act, at_minus, T):
     # sums of exactly one product: +-inf, the largest and smallest bf16, signed zeros
     vals = torch.tensor([np.inf, -np.inf, 3e38, -3e38, 1e-38, -1e-38, 0.0, -0.0, 30.0, -30.0, 100.0, -100.0], dtype=BF16)
@@ -192,7 +192,8 @@ def test_activations_at_the_ends(api, act, at_minus, T):
 
 def test_same_bits_from_call_to_call_on_two_streams_and_in_a_graph(api):
     s2 = torch.cuda.Stream()
-    for T, K, N, out in ((1, 1024, 1024, BF16), (40, 2048, 512, F32), (128, 4096, 1024, BF16), (1500, 1024, 512, F32)):
+    for T, K, N, out in ((1, 1024, 1024, BF16), (40, 2048, 512, F32), (128, 4096, 1024, BF16), (1500, 1024, 512, F32), (5000, 1024, 512, BF16),
+                         (30, 1024, 512, BF16)):
         (x, W, b, r), ref, tol = problem(T, K, N, "gelu", False, True, True, out, seed=T)
         first = torch.empty((T, N), dtype=out, device="cuda")
         api.dr_linear(x, W, first, bias=b, act="gelu", residual=r)
@@ -217,7 +218,7 @@ def test_same_bits_from_call_to_call_on_two_streams_and_in_a_graph(api):
 
 def test_a_chain_of_products_reads_what_the_one_before_wrote(api):
     # launches overlap their predecessors' ends; each must still see all of its predecessor's output
-    for T in (1, 24, 128, 1100):
+    for T in (1, 24, 128, 1100, 3000):
         Ws = [randn((512, 512), 10 + i, 512 ** -0.5).cuda() for i in range(6)]
         x = randn((T, 512), 3).cuda()
         bufs = [torch.empty((T, 512), dtype=BF16, device="cuda") for _ in Ws]
@@ -261,7 +262,7 @@ def test_many_tokens_pass_32_bit_offsets(api):
     assert_within(o[rows.cuda()], ref, tol, "far inputs")
 
 
-@pytest.mark.parametrize("T,K,N", [(64, 1024, 512), (128, 4096, 256), (600, 512, 512)])
+@pytest.mark.parametrize("T,K,N", [(64, 1024, 512), (128, 4096, 256), (600, 512, 512), (2500, 512, 512), (6000, 576, 1024)])
 def test_wait_that_runs_out(api, T, K, N):
     # Test hook: one output tile's CTAs never load their first K chunk; their waits give up after about 2 s, the tile is
     # left as it was, others are right, and the next call on the same context is right everywhere.
