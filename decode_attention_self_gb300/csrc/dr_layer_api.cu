@@ -6,6 +6,11 @@
 
 namespace {
 
+// The kernels look a tile past the last token and a group of steps past the last k in 32-bit numbers; tensor maps take
+// strides below 2^40 bytes.
+constexpr int kMaxTokens = 0x7FFFF000, kMaxK = 1 << 30;
+constexpr int64_t kMaxStride = 1LL << 37;
+
 bool aligned(const void *p, int bytes) { return reinterpret_cast<uintptr_t>(p) % (uintptr_t)bytes == 0; }
 
 // Whether rows start on 32 bytes (2), on 16 (1) or anywhere (0).
@@ -19,9 +24,9 @@ dr_status from_cuda(cudaError_t e) { return e == cudaSuccess ? DR_OK : DR_ERR_CU
 dr_status linear_call(const void *x, int64_t x_stride, const void *W, const dr_linear_opts *opts, int T, int K, int N,
                       const dr_linear_out *outs, int n_outs, dr_dtype out_dtype, int32_t *err_flag, bool stall,
                       int stall_tile, void *stream) {
-    if (!x || !W || !outs || T < 1 || K < 8 || K % 8 != 0 || N < 1) return DR_ERR_INVALID_ARG;
+    if (!x || !W || !outs || T < 1 || T > kMaxTokens || K < 8 || K > kMaxK || K % 8 != 0 || N < 1) return DR_ERR_INVALID_ARG;
     if (n_outs < 1 || n_outs > DR_LINEAR_MAX_OUTS) return DR_ERR_INVALID_ARG;
-    if (!aligned(x, 16) || !aligned(W, 16) || x_stride < K || x_stride % 8 != 0 || x_stride > (1LL << 38))
+    if (!aligned(x, 16) || !aligned(W, 16) || x_stride < K || x_stride % 8 != 0 || x_stride > kMaxStride)
         return DR_ERR_INVALID_ARG;
     if (out_dtype != DR_BF16 && out_dtype != DR_F32) return DR_ERR_INVALID_ARG;
     const int e = out_dtype == DR_F32 ? 4 : 2;
@@ -41,7 +46,7 @@ dr_status linear_call(const void *x, int64_t x_stride, const void *W, const dr_l
         p.residual = opts->residual;
         p.res_stride = opts->residual_stride;
         // one residual, one output; in place only row by row
-        if (p.residual && (n_outs != 1 || p.res_stride < N ||
+        if (p.residual && (n_outs != 1 || p.res_stride < N || p.res_stride > kMaxStride ||
                            (p.residual == outs[0].ptr && p.res_stride != outs[0].stride && T > 1)))
             return DR_ERR_INVALID_ARG;
     }
@@ -50,7 +55,9 @@ dr_status linear_call(const void *x, int64_t x_stride, const void *W, const dr_l
     int64_t at = 0;
     for (int i = 0; i < n_outs; ++i) {
         const dr_linear_out &o = outs[i];
-        if (!o.ptr || o.cols < 1 || o.stride < o.cols || !aligned(o.ptr, e)) return DR_ERR_INVALID_ARG;
+        if (!o.ptr || o.cols < 1 || o.stride < o.cols || o.stride > kMaxStride || !aligned(o.ptr, e)) return DR_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (outs[j].ptr == o.ptr) return DR_ERR_INVALID_ARG;
         if (i + 1 < n_outs && o.cols % 64 != 0) return DR_ERR_INVALID_ARG;
         p.vec_out = min(p.vec_out, row_alignment(o.ptr, o.stride * e));
         if (at + o.cols > N) return DR_ERR_INVALID_ARG;
@@ -121,7 +128,7 @@ dr_status dr_residual_norm(const void *x, int64_t x_stride, dr_dtype x_dtype, co
                            int64_t gate_stride, float scale, const void *residual, int64_t residual_stride, void *h,
                            int64_t h_stride, dr_dtype h_dtype, const dr_norm *pre, void *y, int64_t y_stride,
                            dr_dtype y_dtype, int T, int Dm, void *stream) {
-    if (!x || (!h && !y) || T < 1 || Dm < 8 || Dm % 8 != 0) return DR_ERR_INVALID_ARG;
+    if (!x || (!h && !y) || T < 1 || T > kMaxTokens || Dm < 8 || Dm % 8 != 0) return DR_ERR_INVALID_ARG;
     if ((x_dtype != DR_BF16 && x_dtype != DR_F32) || (h_dtype != DR_BF16 && h_dtype != DR_F32) ||
         (y_dtype != DR_BF16 && y_dtype != DR_F32))
         return DR_ERR_INVALID_ARG;
@@ -131,13 +138,14 @@ dr_status dr_residual_norm(const void *x, int64_t x_stride, dr_dtype x_dtype, co
     if (gate && (!aligned(gate, 16) || gate_stride % 8 != 0 || (gate_stride != 0 && gate_stride < Dm)))
         return DR_ERR_INVALID_ARG;
     if (!(scale == scale) || isinf(scale)) return DR_ERR_INVALID_ARG;
-    // in place only row by row
-    if (h && T > 1 &&
-        ((h == residual && h_stride != residual_stride) || (h == x && (h_stride != x_stride || h_dtype != x_dtype))))
+    // in place only element by element
+    const auto other = [&](const void *out, int64_t out_stride, dr_dtype out_type, const void *in, int64_t in_stride, dr_dtype in_type) {
+        return out && out == in && (out_type != in_type || (T > 1 && out_stride != in_stride));
+    };
+    if (other(h, h_stride, h_dtype, residual, residual_stride, h_dtype) || other(h, h_stride, h_dtype, x, x_stride, x_dtype) ||
+        other(y, y_stride, y_dtype, residual, residual_stride, h_dtype) || other(y, y_stride, y_dtype, x, x_stride, x_dtype))
         return DR_ERR_INVALID_ARG;
-    if (y && T > 1 && ((y == x && (y_stride != x_stride || y_dtype != x_dtype)) ||
-                       (y == residual && (y_stride != residual_stride || y_dtype != h_dtype))))
-        return DR_ERR_INVALID_ARG;
+    if (gate && (gate == h || gate == y)) return DR_ERR_INVALID_ARG;
     if (h && h == y) return DR_ERR_INVALID_ARG;
     dr::ResidualNormParams p;
     if (!fill_norm(p.post, post) || !fill_norm(p.pre, pre)) return DR_ERR_INVALID_ARG;

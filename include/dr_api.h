@@ -560,18 +560,19 @@ typedef struct dr_linear_out {
  *   out[t][n] = residual[t][n] + v[t][n]
  * Sums and everything after them are fp32, rounded once to out_dtype.  The
  * columns may go to several outputs in turn (queries, keys and values of a
- * merged projection).  Any number of tokens: single steps, batches and prompts
- * take kernels of their own, chosen by T, K and N.
- * For every T the sums over K run on the tensor cores, which cut off rather
- * than round (about 1e-9 K of the value, towards zero); with fp32 outputs the
- * chains are broken every 512 of K and added in fp32.  A NaN or infinity in a
- * token or weight row reaches that token's or column's outputs and no others;
+ * merged projection).  Single steps, batches and prompts take kernels of their
+ * own, chosen by T, K, N and gated.  The products run on the tensor cores, whose
+ * sums are cut off rather than rounded (about 1e-9 of the value, towards zero,
+ * per term of K): with fp32 outputs no such sum is longer than 512 terms, and
+ * the sums are added in fp32.  A NaN or infinity in a token, weight row or
+ * residual reaches that token's, column's or element's outputs and no others;
  * at a = -inf gelu, gelu_tanh and silu give their limit 0.
  *
  *   x        : [T][K] bf16 (device, 16-byte aligned), tokens x_stride elements apart (a multiple of 8, >= K)
  *   W        : [N][K] bf16, [2N][K] when gated (device, 16-byte aligned)
  *   opts     : nullable (no bias, activation or residual)
- *   T        : at least 1;  K : a multiple of 8;  N : any, the columns of all outputs together
+ *   T        : 1 .. 2^31 - 4096;  K : a multiple of 8, at most 2^30;  N : the columns of all outputs together, any number
+ *              below 2^30
  *   outs     : n_outs (1 .. DR_LINEAR_MAX_OUTS) outputs, read on the host during the call; a residual takes a single
  *              one.  16-byte aligned pointers and strides make them faster, and so for the residual.  Outputs overlap
  *              neither each other nor x, W and bias
@@ -632,7 +633,7 @@ typedef struct dr_norm {
  *              same stride and type
  *   y        : nullable [T][Dm] in y_dtype; may be x or residual itself with the same stride and type where h is not
  *              it; h and y are not both null
- *   Dm       : a multiple of 8, at most 16384 (DR_ERR_UNSUPPORTED above)
+ *   T        : 1 .. 2^31 - 4096;  Dm : a multiple of 8, at most 16384 (DR_ERR_UNSUPPORTED above)
  * Pointers are device pointers, 16-byte aligned; strides are in elements, multiples of 16 bytes, at least Dm.  h and y
  * overlap the inputs and each other only as said.
  */

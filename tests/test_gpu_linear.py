@@ -58,6 +58,12 @@ def test_odd_sizes(api, T, K, N):
     run_and_check(api, T, K, N, "silu", bias=True, out=BF16 if (T + N) % 2 else F32, seed=T + K)
 
 
+@pytest.mark.parametrize("T", [1, 11, 27, 70, 500, 19600])
+@pytest.mark.parametrize("N", [1, 7, 33, 63, 65, 129])
+def test_odd_gated_sizes(api, T, N):
+    run_and_check(api, T, 104, N, "gelu_tanh", gated=True, residual=True, out=F32 if (T + N) % 3 else BF16, seed=T + N)
+
+
 @pytest.mark.parametrize("T", [1, 4, 20, 96, 128, 384])
 @pytest.mark.parametrize("K,N", [(2048, 1536), (4096, 1024), (1024, 4096), (8192, 512), (6144, 64), (16384, 128)])
 def test_model_sizes(api, T, K, N):
@@ -214,6 +220,71 @@ def test_same_bits_from_call_to_call_on_two_streams_and_in_a_graph(api):
             g.replay()
             torch.cuda.synchronize()
             assert torch.equal(o, first)
+
+
+def test_first_calls_of_a_process_in_a_capture():
+    # what a kernel sets up once is set up during the capture
+    import os
+    import subprocess
+    import sys
+
+    code = """
+import sys, torch
+from decode_attention_self_gb300 import api
+T, K, N = map(int, sys.argv[1:])
+x = torch.randn(T, K, device='cuda').bfloat16()
+W = (torch.randn(N, K, device='cuda') / K ** 0.5).bfloat16()
+o, y = torch.zeros(T, N, device='cuda', dtype=torch.bfloat16), torch.zeros(T, N, device='cuda', dtype=torch.bfloat16)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    api.dr_linear(x, W, o)
+    api.dr_residual_norm(o, y=y, pre=api.Norm('rms'))
+g.replay()
+torch.cuda.synchronize()
+ref = x.double() @ W.double().T
+assert ((o.double() - ref).norm() / ref.norm()).item() < 2 ** -8
+ref = o.double() / (o.double() ** 2).mean(1, keepdim=True).add(1e-5).sqrt()
+assert ((y.double() - ref).norm() / ref.norm()).item() < 2 ** -7
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    for size in ("4 512 512", "28 512 512", "200 2048 512", "4000 512 1024"):
+        subprocess.run([sys.executable, "-c", code, *size.split()], check=True, cwd=root, timeout=300)
+
+
+def test_kernels_side_by_side_on_four_streams(api):
+    # products of every kind, the LM head and a prompt's attention share the SMs and their tensor memory
+    B, H, L = 2, 16, 700
+    q = randn((B * L, H, 64), 50).cuda()
+    cache = api.KVCache(randn((B, H, 1024, 64), 51).cuda(), randn((B, H, 1024, 64), 52).cuda())
+    rs = torch.tensor([0, L, 2 * L], dtype=torch.int32, device="cuda")
+    kl = torch.tensor([L, L], dtype=torch.int32, device="cuda")
+    hid, head = randn((16, 1024), 53).cuda(), randn((9 * 1088, 1024), 54, 0.03).cuda()
+    jobs = []
+    for T, K, N, out in ((2600, 1024, 1024, BF16), (128, 4096, 1024, BF16), (700, 2048, 512, F32), (20, 1024, 1024, BF16)):
+        x, W = randn((T, K), T).cuda(), randn((N, K), T + 1, K ** -0.5).cuda()
+        jobs.append((lambda s, o, x=x, W=W: api.dr_linear(x, W, o, act="gelu", stream=s), (T, N), out))
+    jobs.append((lambda s, o: api.dr_lm_head(hid, head, 9, o, stream=s), (16, 9, 1088), F32))
+    jobs.append((lambda s, o: api.dr_prompt_attn(q, cache, rs, kl, o, stream=s), (B * L, H, 64), BF16))
+    want = []
+    for call, shape, dt in jobs:
+        o = torch.empty(shape, dtype=dt, device="cuda")
+        call(None, o)
+        want.append(o)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    rng = np.random.default_rng(0)
+    runs = []
+    for i in range(400):
+        j = int(rng.integers(len(jobs)))
+        call, shape, dt = jobs[j]
+        s = streams[int(rng.integers(4))]
+        with torch.cuda.stream(s):
+            o = torch.empty(shape, dtype=dt, device="cuda")
+        call(s, o)
+        runs.append((j, o))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want[j]) for j, o in runs)
 
 
 def test_a_chain_of_products_reads_what_the_one_before_wrote(api):

@@ -52,6 +52,8 @@ def linear(lib, x=FAKE, xs=1024, W=FAKE, opts=None, T=4, K=1024, N=1024, outs=No
     dict(opts=dict(residual=FAKE, residual_stride=1000)), dict(opts=dict(residual=FAKE + 1, residual_stride=1024)),
     dict(opts=dict(residual=FAKE, residual_stride=2048)),             # the output itself with another stride
     dict(opts=dict(residual=FAKE, residual_stride=1024), outs=[(FAKE, 512, 512), (FAKE, 512, 512)]),
+    dict(outs=[(FAKE, 512, 512), (FAKE, 512, 512)]),                  # two outputs in one place
+    dict(T=2 ** 31 - 4095), dict(K=2 ** 30 + 8, xs=2 ** 30 + 8), dict(xs=2 ** 37 + 8), dict(outs=[(FAKE, 2 ** 37 + 8, 1024)]),
     dict(stall=-1), dict(N=1 << 30, outs=[(FAKE, 1 << 30, 1 << 30)]),
 ])
 def test_linear_refusals(lib, bad):
@@ -77,6 +79,8 @@ def norm(lib, x=FAKE, xs=1024, xd=0, post=None, gate=None, gs=0, scale=1.0, res=
     (dict(res=FAKE + 0x10000, h=FAKE + 0x10000, hs=2048), 1),         # in place with another stride
     (dict(h=FAKE, hs=2048), 1), (dict(h=FAKE, hd=1), 1),              # x itself with another stride or type
     (dict(y=FAKE, ys=2048), 1), (dict(y=FAKE, yd=1), 1), (dict(h=FAKE + 0x100000), 1),
+    (dict(h=FAKE, hd=1, T=1), 1), (dict(y=FAKE, yd=1, T=1), 1),       # also for a single token
+    (dict(res=FAKE + 0x200000, y=FAKE + 0x200000, hd=1), 1), (dict(gate=FAKE + 0x100000), 1), (dict(T=2 ** 31 - 4095), 1),
     (dict(xs=1026, xd=1), 1), (dict(Dm=16392, xs=16392, ys=16392), 2),
 ])
 def test_residual_norm_refusals(lib, bad, status):
