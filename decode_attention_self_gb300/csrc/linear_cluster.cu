@@ -7,10 +7,10 @@
 // tiles leave SMs idle the S CTAs of a cluster share K: each lays its partial sums down in its shared memory and copies them, in
 // bulk, to the CTAs that own the rows (rows / S each), which add the S parts in rank order and finish their rows.  The
 // order of sums is fixed: results are the same bits from call to call.
-//   warps 0, 1: TMA producers of 64-wide K chunks, even and odd;  warps 2, 3: MMA issuers, even and odd chunks, each into
-//   sums of its own;  all 8 warps: sums, epilogue.
+//   warps 0-3: TMA producers of 64-wide K chunks, each of every fourth;  warps 4-7: MMA issuers, likewise, each into sums of its
+//   own;  all 8 warps: sums, epilogue.
 // (One warp takes some 400 cycles to issue a chunk's four products, wait and commit, and 310 to issue its copies, whatever
-// their size: with one of each, 128 tokens of 1024 -> 4096 took 8700 cycles for 16 chunks, which ran in 2700.)
+// their size: with one of each, 128 tokens of 1024 -> 4096 took 8700 cycles for 16 chunks, with two 5300.)
 // The kernel runs once through its code, so there is little of it: one form of the epilogue, 16 columns of a token at a time.
 // Tensor-core sums are cut off, not rounded: each addition may lose the last bit towards zero, so a chain over K drifts by about
 // 1e-9 K (measured: 1.0e-6 at K = 1024, 2.1e-6 at 2048).  fp32 outputs therefore break the chain every 512 of K into
@@ -32,7 +32,7 @@ constexpr int kChunkK = 64;       // K per stage: one 128-byte swizzled row
 constexpr int kMaxStages = 8;
 constexpr int kPieceChunks = 8;   // fp32 outputs: K of 512 per accumulator
 constexpr int kMaxNb = 64;        // weight rows per tile
-constexpr int kIssuers = 2;
+constexpr int kWays = 4;          // producers, and issuers
 constexpr size_t kMinSmem = 80 * 1024;
 constexpr size_t kMaxSmem = 225 * 1024;
 
@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(kThreads)
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t full[kMaxStages], empty[kMaxStages], done, parts;
     __shared__ uint32_t tmem_base;
-    __shared__ int gave_up, issued[2];   // a wait ran out; the chunk at which each producer ended
+    __shared__ int gave_up, issued[kWays];   // a wait ran out; the chunk at which each producer ended
     __shared__ float bias[kMaxNb];   // of the tile's sums
 
     const LinearParams &p = args.p;
@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kThreads)
             tc::mbar_init(&full[s], 1);
             tc::mbar_init(&empty[s], 1);
         }
-        tc::mbar_init(&done, kIssuers);
+        tc::mbar_init(&done, kWays);
         tc::mbar_init(&parts, 1);
         if (S > 1 && mine > 0) tc::mbar_expect_tx(&parts, (uint32_t)((S - 1) * mine * pl.nb) * 4);
         gave_up = 0;
@@ -146,12 +146,12 @@ __global__ void __launch_bounds__(kThreads)
             bias[j] = n < p.N ? lin::bf16_at(p.bias, j < bn ? n : (int64_t)p.N + n) : 0.f;
         }
 
-    if (warp < 2) {
+    if (warp < kWays) {
         // stage s of round r waits for the products of round r - 1.  (Test hook: the stalled tile's first chunk is left out, so
         // the wait for it runs out.)
         const bool stalled = (int)(blockIdx.z * gridDim.y + blockIdx.y) == p.stall_tile;
         int c = warp;
-        for (int s = c % stages, r = c / stages; c < chunks; c += 2) {
+        for (int s = c % stages, r = c / stages; c < chunks; c += kWays) {
             if (r > 0 && !tc::mbar_wait(&empty[s], (r - 1) & 1, &gave_up)) break;
             if (tc::elect_one() && !(stalled && c == 0)) {
                 const int k = (c_begin + c) * kChunkK;
@@ -162,21 +162,21 @@ __global__ void __launch_bounds__(kThreads)
                 tma_load_2d(sx + s * bytes_x, &map_x, k, t0, &full[s]);
             }
             __syncwarp();
-            s += 2;
+            s += kWays;
             if (s >= stages) {
                 s -= stages;
                 ++r;
             }
         }
         if (lane == 0) issued[warp] = c;
-    } else if (warp < 2 + kIssuers) {
+    } else {
         const uint32_t idesc = tc::instr_desc(kRows, pl.nb, false, false);
         const uint64_t dx = tc::smem_desc(sx), dw = tc::smem_desc(sw);
-        const int issuer = warp - 2, step = kIssuers;
+        const int issuer = warp - kWays;
         bool ok = true;
         int c = issuer, in_piece = 0;
         uint32_t d = tmem + issuer * pl.nb;
-        for (int s = c % stages, r = c / stages; c < chunks; c += step) {
+        for (int s = c % stages, r = c / stages; c < chunks; c += kWays) {
             if (!tc::mbar_wait(&full[s], r & 1, &gave_up)) {
                 ok = false;
                 break;
@@ -192,9 +192,9 @@ __global__ void __launch_bounds__(kThreads)
             __syncwarp();
             if (++in_piece == pl.piece_chunks) {
                 in_piece = 0;
-                d += step * pl.nb;
+                d += kWays * pl.nb;
             }
-            s += step;
+            s += kWays;
             if (s >= stages) {
                 s -= stages;
                 ++r;
@@ -210,8 +210,8 @@ __global__ void __launch_bounds__(kThreads)
     if (gave_up) {
         // copies in flight end by themselves; wait for them before this CTA's shared memory goes away
         if (warp == 0 && lane == 0) {
-            for (int w = 0; w < 2; ++w)
-                for (int c = issued[w] - 2; c >= max(p.stall_tile < 0 ? 0 : 1, issued[w] - stages); c -= 2)
+            for (int w = 0; w < kWays; ++w)
+                for (int c = issued[w] - kWays; c >= max(p.stall_tile < 0 ? 0 : 1, issued[w] - stages); c -= kWays)
                     tc::mbar_drain(&full[c % stages], (c / stages) & 1);
             flag_error(p.err, DR_ERRF_TIMEOUT);
         }
@@ -223,9 +223,10 @@ __global__ void __launch_bounds__(kThreads)
     // Sums to shared memory, [row][nb] fp32 in 16-byte pieces that the row turns, so that a warp's stores spread over the banks.
     // The ring is idle: all its copies were multiplied.
     const int nb = pl.nb;
-    // accumulators in use: an issuer has one for each piece_chunks of its chunks, in turn with the other's
+    // accumulators in use: an issuer has one for each piece_chunks of its chunks, in turn with the others
     const auto ceil_div = [](int a, int b) { return (a + b - 1) / b; };
-    const int pieces = ceil_div((chunks + 1) / 2, pl.piece_chunks) + ceil_div(chunks / 2, pl.piece_chunks);
+    int pieces = 0;
+    for (int w = 0; w < kWays; ++w) pieces += ceil_div(ceil_div(max(chunks - w, 0), kWays), pl.piece_chunks);
     if (ok && (warp & 3) * 32 < rows) {
         const int row = (warp & 3) * 32 + lane;
         const uint32_t from = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -342,8 +343,8 @@ ClusterPlan make_plan(const LinearParams &p, int sms) {
     const int rows = p.T < kRows ? p.T : kRows;
     pl.box_rows = (rows + 7) / 8 * 8;
     const int most = (chunks + pl.split - 1) / pl.split;   // chunks of a CTA
-    const int own_chunks = (most + kIssuers - 1) / kIssuers, max_cols = pl.split > 1 ? 256 : 512;
-    const auto pieces = [&] { return kIssuers * ((own_chunks + pl.piece_chunks - 1) / pl.piece_chunks); };
+    const int own_chunks = (most + kWays - 1) / kWays, max_cols = pl.split > 1 ? 256 : 512;
+    const auto pieces = [&] { return kWays * ((own_chunks + pl.piece_chunks - 1) / pl.piece_chunks); };
     pl.piece_chunks = p.out_f32 ? kPieceChunks : own_chunks;
     while (pieces() * pl.nb > max_cols) ++pl.piece_chunks;
     pl.cols = 32;
@@ -355,11 +356,10 @@ ClusterPlan make_plan(const LinearParams &p, int sms) {
         const size_t over = n * stage > (size_t)(n * pl.box_rows + kRows) * 128 ? n * stage : (size_t)(n * pl.box_rows + kRows) * 128;
         return over > own ? over : own;
     };
-    // an even number: a stage always belongs to the even or the odd chunks, so a warp that waits for one of its rounds has seen
-    // the round before (a wait by parity cannot tell a phase from the one two before it)
-    pl.stages = most < kMaxStages ? most : kMaxStages;
-    pl.stages += pl.stages & 1;
-    while (pl.stages > 2 && 1024 + ring(pl.stages) + parts > kMaxSmem) pl.stages -= 2;
+    // a multiple of kWays: a stage always belongs to the same producer and issuer, so a warp that waits for one of its rounds has
+    // seen the round before (a wait by parity cannot tell a phase from the one two before it)
+    pl.stages = most <= kWays ? kWays : kMaxStages;
+    while (pl.stages > kWays && 1024 + ring(pl.stages) + parts > kMaxSmem) pl.stages -= kWays;
     pl.recv_at = (uint32_t)ring(pl.stages);
     pl.smem = 1024 + ring(pl.stages) + parts;
     if (pl.smem < kMinSmem) pl.smem = kMinSmem;
