@@ -479,60 +479,71 @@ __global__ void __launch_bounds__(kThreads, 1)
                 bias_phase ^= 1;
             }
             const float *b = bias + set * kTileW + share.col0;
-            // One copy of the code for all blocks: the next block's sums move to the first registers, and the one after it
-            // is read behind them while this one is worked on.
-#pragma unroll 1
-            for (int k = 0;; ++k, b += 32) {
+            // 32 columns: the sums v (gated: times those in g) to the box or the output
+            const auto block = [&](float *v, float *g, int k) {
                 if (p.bias) {
-                    add_bias32(acc, b);
-                    if (p.gated) add_bias32(acc + 32, b + apart);
+                    add_bias32(v, b + k * 32);
+                    if (p.gated) add_bias32(g, b + k * 32 + apart);
                 }
-                lin::activate<32>(acc, p.act);
+                lin::activate<32>(v, p.act);
                 if (p.gated) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) acc[j] *= acc[32 + j];
+                    for (int j = 0; j < 32; ++j) v[j] *= g[j];
                 }
                 const bool opens = kF32 || narrow || k % 2 == 0, closes = kF32 || narrow || k % 2 == 1;   // a box
                 if (boxed) {
                     if (opens) {
-                        ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(&ctl.box_ready[e], box_phase, gave_up));
-                        if (!ok) break;
+                        if (!__all_sync(0xFFFFFFFFu, tc::mbar_wait(&ctl.box_ready[e], box_phase, gave_up))) return false;
                         box_phase ^= 1;
                     }
-                    if (narrow) put32<kF32, true>(acc, box, lane, 0, p.residual);
-                    else put32<kF32, false>(acc, box, lane, opens ? 0 : 4, p.residual);
+                    if (narrow) put32<kF32, true>(v, box, lane, 0, p.residual);
+                    else put32<kF32, false>(v, box, lane, opens ? 0 : 4, p.residual);
                 } else {
                     int tt, ct;
                     tile_at(args, i, tt, ct);
                     const int t0 = tt * kTileT + (int)rank * 128 + quad * 32, n = ct * tile_cols + share.col0 + k * 32;
                     float *const loose = reinterpret_cast<float *>(smem + (box - ring));
                     if (n < p.N) {
-                        if (p.residual) LooseRows<kF32>::add_residual(p, acc, loose, t0, n, lane);
-                        LooseRows<kF32>::store(p, acc, loose, t0, n, lane);
+                        if (p.residual) LooseRows<kF32>::add_residual(p, v, loose, t0, n, lane);
+                        LooseRows<kF32>::store(p, v, loose, t0, n, lane);
                     }
                 }
                 if (closes) {
                     __syncwarp();
                     if (lane == 0) tc::mbar_arrive(&ctl.boxes_full[set]);
                 }
-                if (k + 1 == share.blocks) break;
-                if (!shared && p.gated) {
+                return true;
+            };
+            // Blocks in turn in either half of the registers; while one is worked on the other's successor is read.
+#pragma unroll 1
+            for (int k = 0;;) {
+                ok = block(acc, acc + 32, k);
+                if (!ok || k + 1 == share.blocks) break;
+                if (p.gated) {   // (two blocks of its set's share)
                     tc::ld32(from + 32, acc);
                     tc::ld32(from + 32 + apart, acc + 32);
                     tc::wait_ld();
                     tc::pin32(acc);
                     tc::pin32(acc + 32);
                     release();
-                } else {
-                    if (!shared && k > 0) {
+                    ++k;
+                    continue;
+                }
+                if (!shared) {
+                    if (k == 0) {
+                        tc::ld32(from + 64, acc);
+                    } else {
                         tc::wait_ld();
                         tc::pin32(acc + 32);
-                        if (k == 2) release();
+                        release();
                     }
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) acc[j] = acc[32 + j];
-                    if (!shared && k < 2) tc::ld32(from + 32 * (k + 2), acc + 32);
                 }
+                ok = block(acc + 32, acc, k + 1);
+                k += 2;
+                if (!ok || k == share.blocks) break;
+                tc::wait_ld();
+                tc::pin32(acc);
+                tc::ld32(from + 96, acc + 32);
             }
         }
     }
