@@ -71,7 +71,8 @@ __device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank) {
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+// (relaxed: the barriers' set-up has a fence of its own, and what is copied is counted)
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 template <bool kF32>
@@ -105,19 +106,29 @@ __global__ void __launch_bounds__(kThreads)
     uint8_t *const staged = smem_raw + (ring - tc::smem_u32(smem_raw));              // own sums, over the ring once it is idle
     uint8_t *const received = staged + pl.recv_at;                                   // the other CTAs', part by part
 
-    if (threadIdx.x == 32) {
-        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_x)) : "memory");
-        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_w)) : "memory");
-        for (int s = 0; s < stages; ++s) {
-            tc::mbar_init(&full[s], 1);
-            tc::mbar_init(&empty[s], 1);
+    if (warp == 1) {   // a lane per barrier of a kind
+        if (lane < stages) {
+            tc::mbar_init(&full[lane], 1);
+            tc::mbar_init(&empty[lane], 1);
         }
-        tc::mbar_init(&done, kWays);
-        tc::mbar_init(&parts, 1);
-        if (S > 1 && mine > 0) tc::mbar_expect_tx(&parts, (uint32_t)((S - 1) * mine * pl.nb) * 4);
-        gave_up = 0;
+        if (lane == 0) {
+            tc::mbar_init(&done, kWays);
+            tc::mbar_init(&parts, 1);
+            if (S > 1 && mine > 0) tc::mbar_expect_tx(&parts, (uint32_t)((S - 1) * mine * pl.nb) * 4);
+            gave_up = 0;
+        }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        __syncwarp();
     }
+    // The first weight boxes, one a warp, on their way into L2 while the kernel before this one ends (a hint: nothing is read).
+    if (warp < min(chunks, stages) && tc::elect_one()) {
+        if (warp == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_x)) : "memory");
+        for (int half = 0; half <= p.gated; ++half)
+            asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(&map_w)),
+                         "r"((c_begin + warp) * kChunkK), "r"(half ? p.N + n0 : n0)
+                         : "memory");
+    }
+    __syncwarp();
     if (warp == 2) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc::smem_u32(&tmem_base)),
                      "r"(pl.cols));
@@ -128,15 +139,6 @@ __global__ void __launch_bounds__(kThreads)
     tc::fence_after();
     const uint32_t tmem = tmem_base;
     if (S > 1) cluster_arrive();   // waited for before the first remote write: every CTA of the cluster runs by then
-    // the first weight boxes on their way into L2 while the kernel before this one ends (a hint: nothing is read)
-    if (warp == 0 && tc::elect_one()) {
-        const int ahead = min(chunks, stages);
-        for (int c = 0; c < ahead; ++c)
-            asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
-                             reinterpret_cast<uint64_t>(&map_w)),
-                         "r"((c_begin + c) * kChunkK), "r"(n0)
-                         : "memory");
-    }
     pdl_wait();
     // The next kernel may start as far as it fits beside this one: it sets up, and prefetches its weights.
     pdl_trigger();

@@ -75,8 +75,10 @@ __device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank) {
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
+// All threads of both CTAs have come here.  Relaxed: the barriers' set-up has a fence of its own, and at the end nothing is handed
+// over (a release would wait for the last stores, some 1400 cycles).
 __device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // A copy into this CTA's shared memory that counts on a barrier of either CTA of the pair (a cluster address).
@@ -257,25 +259,32 @@ __global__ void __launch_bounds__(kThreads, 1)
     // whole 16-byte pieces of rows: boxes carried by TMA
     const bool boxed = p.vec_out && (!p.residual || p.vec_res);
 
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) {
-            tc::mbar_init(&ctl.full[s], 1);
-            tc::mbar_init(&ctl.empty[s], 1);
+    if (warp == 0) {   // a lane per barrier of a kind: one after the other they take some 400 cycles
+        if (lane < kStages) {
+            tc::mbar_init(&ctl.full[lane], 1);
+            tc::mbar_init(&ctl.empty[lane], 1);
         }
-        for (int b = 0; b < 2; ++b) {
-            tc::mbar_init(&ctl.sums_full[b], 1);
+        if (lane < 2) {
             const Share share(args, 0, 0, 0, kF32);
             const int warps = args.shared ? 4 * (tile_cols / share.span) : kCarried;   // that take a tile
-            tc::mbar_init(&ctl.sums_free[b], 2 * warps);
-            tc::mbar_init(&ctl.boxes_full[b], args.shared ? max(1, min(kCarried, warps - b * kCarried)) : kCarried);
-            tc::mbar_init(&ctl.bias_ready[b], 1);
+            tc::mbar_init(&ctl.sums_full[lane], 1);
+            tc::mbar_init(&ctl.sums_free[lane], 2 * warps);
+            tc::mbar_init(&ctl.boxes_full[lane], args.shared ? max(1, min(kCarried, warps - lane * kCarried)) : kCarried);
+            tc::mbar_init(&ctl.bias_ready[lane], 1);
         }
-        for (int w = 0; w < kEpiWarps; ++w) tc::mbar_init(&ctl.box_ready[w], 1);
-        tc::mbar_init(&ctl.done, 1);
-        ctl.gave_up = 0;
+        if (lane < kEpiWarps) tc::mbar_init(&ctl.box_ready[lane], 1);
+        if (lane == 0) {
+            tc::mbar_init(&ctl.done, 1);
+            ctl.gave_up = 0;
+        }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.x)) : "memory");
-        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.w)) : "memory");
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0) {
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.x)) : "memory");
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.w)) : "memory");
+        }
+        __syncwarp();
     }
     if (warp == 2) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(tc::smem_u32(&ctl.tmem)));
