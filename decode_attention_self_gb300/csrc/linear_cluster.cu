@@ -307,22 +307,25 @@ __global__ void __launch_bounds__(kThreads)
             lin::finish16<kF32>(p, bias + g * 16, bias + bn + g * 16, t0 + rank * share + r, n0 + g * 16, a, b);
         }
     } else if (ok) {   // a column of eight rows a thread: a warp's accesses lie side by side
+        const int shift = 31 - __clz(bn);   // bn is a power of two
 #pragma unroll 1
         for (int i = threadIdx.x; i < (mine + 7) / 8 * bn; i += kThreads) {
-            const int c = i % bn, r0 = i / bn * 8;
+            const int c = i & (bn - 1), r0 = (i >> shift) * 8, have = min(8, mine - r0);
             float a[8], b[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) a[j] = b[j] = 0.f;
 #pragma unroll 1
-            for (int s = 0; s < S; ++s)
+            for (int s = 0; s < S; ++s) {
+                const float *from = part(s, r0);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int r = min(r0 + j, mine - 1), key = (rank * share + r) & 7;
-                    const float *from = part(s, r);
-                    a[j] += from[((c / 4) ^ key) * 4 + c % 4];
-                    if (p.gated) b[j] += from[(((bn + c) / 4) ^ key) * 4 + c % 4];
-                }
-            lin::finish_column8<kF32>(p, bias[c], bias[p.gated ? bn + c : c], t0 + rank * share + r0, mine - r0, n0 + c, a, b);
+                for (int j = 0; j < 8; ++j, from += nb)
+                    if (j < have) {
+                        const int key = (rank * share + r0 + j) & 7;
+                        a[j] += from[((c >> 2) ^ key) * 4 + (c & 3)];
+                        if (p.gated) b[j] += from[(((bn + c) >> 2) ^ key) * 4 + (c & 3)];
+                    }
+            }
+            lin::finish_column8<kF32>(p, bias[c], bias[p.gated ? bn + c : c], t0 + rank * share + r0, have, n0 + c, a, b);
         }
     }
     if (S > 1) cluster_wait();

@@ -1,6 +1,8 @@
 // What follows a matrix product's sums: activations, residual and the outputs' rows.
 #pragma once
 
+#include <type_traits>
+
 #include "dr_device.cuh"
 #include "dr_layer.h"
 
@@ -174,16 +176,16 @@ template <bool kF32>
 __device__ __forceinline__ void finish_column8(const LinearParams &p, float bias_a, float bias_b, int t, int have, int n, float (&a)[8],
                                                float (&b)[8]) {
     if (n >= p.N) return;
+    using T = typename std::conditional<kF32, float, uint16_t>::type;
     float r[8];
     if (p.residual) {
+        const T *from = static_cast<const T *>(p.residual) + (int64_t)t * p.res_stride + n;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int64_t at = (int64_t)(t + i) * p.res_stride + n;
+        for (int i = 0; i < 8; ++i, from += p.res_stride)
             if (i < have) {
-                if constexpr (kF32) r[i] = static_cast<const float *>(p.residual)[at];
-                else r[i] = __uint_as_float((uint32_t)static_cast<const uint16_t *>(p.residual)[at] << 16);
+                if constexpr (kF32) r[i] = *from;
+                else r[i] = __uint_as_float((uint32_t)*from << 16);
             }
-        }
     }
     if (p.bias) {
 #pragma unroll
@@ -198,13 +200,14 @@ __device__ __forceinline__ void finish_column8(const LinearParams &p, float bias
         for (int i = 0; i < 8; ++i) a[i] *= b[i];
     }
     const LinearOut &o = p.out[out_of(p, n)];
+    T *to = static_cast<T *>(o.ptr) + (int64_t)t * o.stride + (n - o.col0);
+    const int64_t stride = o.stride;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int64_t at = (int64_t)(t + i) * o.stride + (n - o.col0);
+    for (int i = 0; i < 8; ++i, to += stride) {
         if (p.residual) a[i] += r[i];
         if (i < have) {
-            if constexpr (kF32) static_cast<float *>(o.ptr)[at] = a[i];
-            else static_cast<uint16_t *>(o.ptr)[at] = f32_to_bf16_rn(a[i]);
+            if constexpr (kF32) *to = a[i];
+            else *to = f32_to_bf16_rn(a[i]);
         }
     }
 }
