@@ -56,6 +56,7 @@ dr_status linear_call(const void *x, int64_t x_stride, const void *W, const dr_l
     for (int i = 0; i < n_outs; ++i) {
         const dr_linear_out &o = outs[i];
         if (!o.ptr || o.cols < 1 || o.stride < o.cols || o.stride > kMaxStride || !aligned(o.ptr, e)) return DR_ERR_INVALID_ARG;
+        if (o.ptr == x || o.ptr == W || o.ptr == (opts ? opts->bias : nullptr)) return DR_ERR_INVALID_ARG;
         for (int j = 0; j < i; ++j)
             if (outs[j].ptr == o.ptr) return DR_ERR_INVALID_ARG;
         if (i + 1 < n_outs && o.cols % 64 != 0) return DR_ERR_INVALID_ARG;

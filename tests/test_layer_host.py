@@ -4,6 +4,7 @@ import ctypes
 import pytest
 
 FAKE = 0x10000   # a 16-byte aligned non-null address; never dereferenced on the host
+OUT = FAKE + 0x1000000
 NAN, INF = float("nan"), float("inf")
 
 
@@ -32,7 +33,7 @@ def vp(x):
 
 
 def linear(lib, x=FAKE, xs=1024, W=FAKE, opts=None, T=4, K=1024, N=1024, outs=None, n_outs=None, od=0, stall=None):
-    outs = [(FAKE, 1024, 1024)] if outs is None else outs
+    outs = [(OUT, 1024, 1024)] if outs is None else outs
     arr = (Out * max(1, len(outs)))(*[Out(*o) for o in outs])
     o = None if opts is None else ctypes.byref(Opts(**opts))
     args = (vp(x), ctypes.c_int64(xs), vp(W), o, T, K, N, arr, len(outs) if n_outs is None else n_outs, od, None)
@@ -44,17 +45,18 @@ def linear(lib, x=FAKE, xs=1024, W=FAKE, opts=None, T=4, K=1024, N=1024, outs=No
 @pytest.mark.parametrize("bad", [
     dict(T=0), dict(T=-1), dict(K=0), dict(K=1020), dict(K=4), dict(N=0), dict(x=None), dict(W=None), dict(x=FAKE + 8),
     dict(W=FAKE + 2), dict(xs=1016), dict(xs=1028), dict(od=2), dict(n_outs=0), dict(n_outs=5),
-    dict(outs=[(None, 1024, 1024)]), dict(outs=[(FAKE, 1023, 1024)]), dict(outs=[(FAKE + 1, 1024, 1024)]),
-    dict(outs=[(FAKE + 2, 1024, 1024)], od=1), dict(outs=[(FAKE, 1024, 1000)]), dict(outs=[(FAKE, 1100, 1100)]),
-    dict(outs=[(FAKE, 1000, 1000), (FAKE, 24, 24)]), dict(outs=[(FAKE, 64, 0), (FAKE, 1024, 1024)]),
-    dict(outs=[(FAKE, 512, 512), (FAKE, 1024, 1024)]),
+    dict(outs=[(None, 1024, 1024)]), dict(outs=[(OUT, 1023, 1024)]), dict(outs=[(OUT + 1, 1024, 1024)]),
+    dict(outs=[(OUT + 2, 1024, 1024)], od=1), dict(outs=[(OUT, 1024, 1000)]), dict(outs=[(OUT, 1100, 1100)]),
+    dict(outs=[(OUT, 1000, 1000), (OUT + 0x100000, 24, 24)]), dict(outs=[(OUT, 64, 0), (OUT + 0x100000, 1024, 1024)]),
+    dict(outs=[(OUT, 512, 512), (OUT + 0x100000, 1024, 1024)]),
     dict(opts=dict(act=5)), dict(opts=dict(act=-1)), dict(opts=dict(gated=2)), dict(opts=dict(bias=FAKE + 2)),
     dict(opts=dict(residual=FAKE, residual_stride=1000)), dict(opts=dict(residual=FAKE + 1, residual_stride=1024)),
-    dict(opts=dict(residual=FAKE, residual_stride=2048)),             # the output itself with another stride
-    dict(opts=dict(residual=FAKE, residual_stride=1024), outs=[(FAKE, 512, 512), (FAKE, 512, 512)]),
-    dict(outs=[(FAKE, 512, 512), (FAKE, 512, 512)]),                  # two outputs in one place
-    dict(T=2 ** 31 - 4095), dict(K=2 ** 30 + 8, xs=2 ** 30 + 8), dict(xs=2 ** 37 + 8), dict(outs=[(FAKE, 2 ** 37 + 8, 1024)]),
-    dict(stall=-1), dict(N=1 << 30, outs=[(FAKE, 1 << 30, 1 << 30)]),
+    dict(opts=dict(residual=OUT, residual_stride=2048)),             # the output itself with another stride
+    dict(opts=dict(residual=FAKE, residual_stride=1024), outs=[(OUT, 512, 512), (OUT + 0x100000, 512, 512)]),
+    dict(outs=[(OUT, 512, 512), (OUT, 512, 512)]),                  # two outputs in one place
+    dict(outs=[(FAKE, 1024, 1024)]), dict(W=OUT), dict(opts=dict(bias=OUT)),   # an output that is an input
+    dict(T=2 ** 31 - 4095), dict(K=2 ** 30 + 8, xs=2 ** 30 + 8), dict(xs=2 ** 37 + 8), dict(outs=[(OUT, 2 ** 37 + 8, 1024)]),
+    dict(stall=-1), dict(N=1 << 30, outs=[(OUT, 1 << 30, 1 << 30)]),
 ])
 def test_linear_refusals(lib, bad):
     assert linear(lib, **bad) == 1
