@@ -44,7 +44,7 @@ cudaError_t launch_linear(const LinearParams &p, cudaStream_t stream);
 cudaError_t launch_linear_rows(const LinearParams &p, int sms, cudaStream_t stream);
 cudaError_t launch_linear_cluster(const LinearParams &p, int sms, cudaStream_t stream);
 int linear_cluster_tiles(const LinearParams &p, int sms);
-bool linear_cluster_keeps(const LinearParams &p, int sms);   // whether fp32 outputs have all the accumulators that they want
+bool linear_cluster_takes(const LinearParams &p, int sms);   // whether its tiles and accumulators suffice
 cudaError_t launch_linear_tiles(const LinearParams &p, int sms, cudaStream_t stream);
 int linear_tiles_tiles(const LinearParams &p, int sms);
 

@@ -42,14 +42,15 @@ enum class Way { kRows, kCluster, kTiles };
 // Which kernel takes a call; measured on both sides of each border, us.
 // Rows or cluster: 16 tokens 8192 -> 8192 24 and 29; 32 tokens, where a CTA's tokens weigh more, 1024 -> 1536 3.5 and 5.2,
 // 1024 -> 4096 4.9 and 6.4, 4096 -> 1024 6.8 and 6.6, 1536 -> 6144 10.0 and 8.0, 8192 -> 8192 44 and 29.
-// Cluster or tiles: the pairs take what is more than one wave of tiles of 128 tokens by 64 weight rows.  512 tokens 1024 -> 4096
-// (256 such tiles) 9.1 and 9.0, 1024 tokens 1024 -> 4096 (512) 15 and 11.5; 1024 tokens 4096 -> 1024 (128) 12.6 and 18, 256
-// tokens 1024 -> 4096 (128) 6.7 and 8.3.  So do fp32 outputs of a K too long for the other kernel's short sums.
+// Cluster or tiles: the pairs that stay take what is more than one wave of tiles of 128 tokens by 64 weight rows and, with bf16
+// outputs, of pairs' tiles of 256 by 128.  1024 tokens 4096 -> 1024 (128 of 128 by 64) 12.6 and 18, 256 tokens 1024 -> 4096 (128) 6.7 and
+// 8.3; 512 tokens 1024 -> 4096 (64 of 256 by 128) 8.0 and 9.7, 2048 tokens 4096 -> 1024 (64) 15.4 and 19.3, 700 tokens 1024 -> 4096 (96)
+// 13.6 and 10.9; fp32 with a residual 1024 tokens 1024 -> 2048 (64) 10.6 and 9.7.  So do fp32 outputs of a K too long for the other
+// kernel's short sums.
 Way way_of(const LinearParams &p, int sms) {
     const int64_t rows = (int64_t)p.N * (p.gated ? 2 : 1);
     if (p.T <= 16 || (p.T <= 32 && rows * p.K <= 6 << 20)) return Way::kRows;
-    if (((int64_t)p.T + 127) / 128 * ((rows + 63) / 64) > sms || !linear_cluster_keeps(p, sms)) return Way::kTiles;
-    return Way::kCluster;
+    return linear_cluster_takes(p, sms) ? Way::kCluster : Way::kTiles;
 }
 
 }  // namespace

@@ -8,10 +8,17 @@
 // bulk, to the CTAs that own the rows (rows / S each), which add the S parts in rank order and finish their rows.  The
 // order of sums is fixed: results are the same bits from call to call.
 //   warps 0-3: TMA producers of 64-wide K chunks, each of every fourth;  warps 4-7: MMA issuers, likewise, each into sums of its
-//   own;  all 8 warps: sums, epilogue.
+//   own;  all 8 or 16 warps: sums, epilogue.
+// Where the tiles of 64 rows would be more than a wave, but those of 256 tokens by 128 rows are not, two CTAs (a cluster) multiply
+// such a tile with two-CTA products (kPair): each loads and keeps 128 of the tokens and 64 of the weight rows, which halves what comes
+// from L2 per product; the first CTA issues (two warps: a product is four times as long).  512 tokens 1024 -> 4096 with gelu 9.7 us
+// by the pairs that stay, 8.0 here: set-up and epilogue of a single tile are what this kernel is short of.
 // (One warp takes some 400 cycles to issue a chunk's four products, wait and commit, and 310 to issue its copies, whatever
 // their size: with one of each, 128 tokens of 1024 -> 4096 took 8700 cycles for 16 chunks, with two 5300.)
-// The kernel runs once through its code, so there is little of it: one form of the epilogue, 16 columns of a token at a time.
+// The kernel runs once through its code, so there is little of it: 16 columns of a token at a time, from tensor memory to the
+// outputs.  (By way of shared memory, with a warp's stores side by side, 256 tokens 1024 -> 4096 took 7.7 us, now 6.8.)  A pass
+// costs some 1300 cycles, 2000 with gelu, of which little is arithmetic: two warps per scheduler cannot hide its latencies, so
+// tiles of 64 and 128 rows have 16 warps.
 // Tensor-core sums are cut off, not rounded: each addition may lose the last bit towards zero, so a chain over K drifts by about
 // 1e-9 K (measured: 1.0e-6 at K = 1024, 2.1e-6 at 2048).  fp32 outputs therefore break the chain every 512 of K into
 // accumulators of their own (pieces), added in fp32; bf16 outputs, whose rounding is 1000 times that, do not.
@@ -26,23 +33,26 @@
 namespace dr {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kMaxThreads = 512;
 constexpr int kRows = 128;        // tokens per tile (MMA M)
 constexpr int kChunkK = 64;       // K per stage: one 128-byte swizzled row
 constexpr int kMaxStages = 8;
 constexpr int kPieceChunks = 8;   // fp32 outputs: K of 512 per accumulator
-constexpr int kMaxNb = 64;        // weight rows per tile
+constexpr int kMaxNb = 128;       // weight rows per tile
 constexpr int kWays = 4;          // producers, and issuers
+constexpr int kPairNb = 128, kPairIssuers = 2;   // a pair's
 constexpr size_t kMinSmem = 80 * 1024;
 constexpr size_t kMaxSmem = 225 * 1024;
 
 struct ClusterPlan {
+    int pair;          // 1: two CTAs multiply a tile of 256 tokens
     int nb;            // weight rows per tile (MMA N): nb output columns, or nb / 2 when gated
     int split;         // CTAs (one cluster) that share K
     int box_rows;      // tokens per tile that are loaded
     int piece_chunks;  // K chunks of an issuer per accumulator
     int stages;
     int cols;          // tensor-memory columns
+    int threads;       // 64 per 8 columns of the tile, at most kMaxThreads
     uint32_t recv_at;  // where the parts of a cluster's other CTAs go, behind the ring and the CTA's own sums
     size_t smem;
 };
@@ -66,45 +76,48 @@ __device__ __forceinline__ void copy_to_peer(uint32_t dst, uint32_t src, uint32_
                  "r"(bytes), "r"(bar)
                  : "memory");
 }
-__device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank) {
-    uint32_t r;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-    return r;
-}
 // (relaxed: the barriers' set-up has a fence of its own, and what is copied is counted)
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
-template <bool kF32>
-__global__ void __launch_bounds__(kThreads)
+template <bool kF32, bool kPair>
+__global__ void __launch_bounds__(kMaxThreads)
     linear_cluster_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                           const __grid_constant__ ClusterArgs args) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t full[kMaxStages], empty[kMaxStages], done, parts;
     __shared__ uint32_t tmem_base;
     __shared__ int gave_up, issued[kWays];   // a wait ran out; the chunk at which each producer ended
-    __shared__ float bias[kMaxNb];   // of the tile's sums
+    __shared__ __align__(16) float bias[kMaxNb];   // of the tile's sums
 
     const LinearParams &p = args.p;
     const ClusterPlan &pl = args.plan;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int S = pl.split, rank = blockIdx.x, stages = pl.stages;
+    constexpr int kIssuers = kPair ? kPairIssuers : kWays;
+    const int S = kPair ? 1 : pl.split, rank = kPair ? 0 : blockIdx.x, stages = pl.stages;
+    const int half = kPair ? blockIdx.x : 0;   // of a pair's tokens and weight rows; the first CTA issues the products of both
     const int bn = p.gated ? pl.nb / 2 : pl.nb;   // output columns of a tile
-    const int n0 = blockIdx.y * bn, t0 = blockIdx.z * kRows;
+    const int n0 = blockIdx.y * bn, t0 = (kPair ? blockIdx.z * 2 + half : blockIdx.z) * kRows;
     const int all_chunks = (p.K + kChunkK - 1) / kChunkK;
     const int c_begin = (int)((int64_t)all_chunks * rank / S), c_end = (int)((int64_t)all_chunks * (rank + 1) / S);
     const int chunks = c_end - c_begin;
-    const uint32_t bytes_x = pl.box_rows * 128, bytes_w = pl.nb * 128;
+    const uint32_t bytes_x = pl.box_rows * 128, bytes_w = (kPair ? pl.nb / 2 : pl.nb) * 128;
+    const int w0 = !kPair ? n0 : p.gated ? half * p.N + n0 : n0 + half * (pl.nb / 2);   // first of the CTA's weight rows
 
     // Ring of tokens, ring of weight rows, partial sums of the cluster.  The MMA reads 128 token rows from each stage, however
     // few there are: rows past the stage's own are whatever follows in shared memory (plan: there is as much), and the sums
     // of their lanes are not looked at.
     const uint32_t ring = (tc::smem_u32(smem_raw) + 1023) & ~1023u;
     const uint32_t sx = ring, sw = ring + stages * bytes_x;
-    const int rows = min(kRows, p.T - t0), share = (rows + S - 1) / S;   // rows of the tile, and that a CTA owns
+    const int rows = max(0, min(kRows, p.T - t0)), share = (rows + S - 1) / S;   // rows of the tile, and that a CTA owns
     const int mine = min(share, rows - rank * share);
     uint8_t *const staged = smem_raw + (ring - tc::smem_u32(smem_raw));              // own sums, over the ring once it is idle
     uint8_t *const received = staged + pl.recv_at;                                   // the other CTAs', part by part
+
+    // accumulators in use: an issuer has one for each piece_chunks of its chunks, in turn with the others
+    const auto ceil_div = [](int a, int b) { return (a + b - 1) / b; };
+    int pieces = 0;
+    for (int w = 0; w < kIssuers; ++w) pieces += ceil_div(ceil_div(max(chunks - w, 0), kIssuers), pl.piece_chunks);
 
     if (warp == 1) {   // a lane per barrier of a kind
         if (lane < stages) {
@@ -112,7 +125,7 @@ __global__ void __launch_bounds__(kThreads)
             tc::mbar_init(&empty[lane], 1);
         }
         if (lane == 0) {
-            tc::mbar_init(&done, kWays);
+            tc::mbar_init(&done, kIssuers);
             tc::mbar_init(&parts, 1);
             if (S > 1 && mine > 0) tc::mbar_expect_tx(&parts, (uint32_t)((S - 1) * mine * pl.nb) * 4);
             gave_up = 0;
@@ -123,19 +136,29 @@ __global__ void __launch_bounds__(kThreads)
     // The first weight boxes, one a warp, on their way into L2 while the kernel before this one ends (a hint: nothing is read).
     if (warp < min(chunks, stages) && tc::elect_one()) {
         if (warp == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_x)) : "memory");
-        for (int half = 0; half <= p.gated; ++half)
+        for (int part = 0; part <= (kPair ? 0 : p.gated); ++part)
             asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(&map_w)),
-                         "r"((c_begin + warp) * kChunkK), "r"(half ? p.N + n0 : n0)
+                         "r"((c_begin + warp) * kChunkK), "r"(part ? p.N + n0 : w0)
                          : "memory");
     }
     __syncwarp();
     if (warp == 2) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc::smem_u32(&tmem_base)),
-                     "r"(pl.cols));
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        if constexpr (kPair) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc::smem_u32(&tmem_base)),
+                         "r"(pl.cols));
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc::smem_u32(&tmem_base)),
+                         "r"(pl.cols));
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        }
     }
     tc::fence_before();
     __syncthreads();
+    if (kPair) {   // both CTAs' barriers are set up, and both have their tensor memory
+        cluster_arrive();
+        cluster_wait();
+    }
     tc::fence_after();
     const uint32_t tmem = tmem_base;
     if (S > 1) cluster_arrive();   // waited for before the first remote write: every CTA of the cluster runs by then
@@ -143,7 +166,7 @@ __global__ void __launch_bounds__(kThreads)
     // The next kernel may start as far as it fits beside this one: it sets up, and prefetches its weights.
     pdl_trigger();
     if (p.bias && threadIdx.x >= 64)
-        for (int j = threadIdx.x - 64; j < pl.nb; j += kThreads - 64) {
+        for (int j = threadIdx.x - 64; j < pl.nb; j += blockDim.x - 64) {
             const int n = n0 + (j < bn ? j : j - bn);
             bias[j] = n < p.N ? lin::bf16_at(p.bias, j < bn ? n : (int64_t)p.N + n) : 0.f;
         }
@@ -157,11 +180,18 @@ __global__ void __launch_bounds__(kThreads)
             if (r > 0 && !tc::mbar_wait(&empty[s], (r - 1) & 1, &gave_up)) break;
             if (tc::elect_one() && !(stalled && c == 0)) {
                 const int k = (c_begin + c) * kChunkK;
-                tc::mbar_expect_tx(&full[s], bytes_x + bytes_w);
                 const uint32_t w_at = sw + s * bytes_w;
-                tma_load_2d(w_at, &map_w, k, n0, &full[s]);
-                if (p.gated) tma_load_2d(w_at + bytes_w / 2, &map_w, k, p.N + n0, &full[s]);
-                tma_load_2d(sx + s * bytes_x, &map_x, k, t0, &full[s]);
+                if constexpr (kPair) {
+                    const uint32_t bar = tc::mapa(tc::smem_u32(&full[s]), 0);
+                    if (half == 0) tc::mbar_expect_tx(&full[s], 2 * (bytes_x + bytes_w));
+                    tc::pair_load(w_at, &map_w, k, w0, bar);
+                    tc::pair_load(sx + s * bytes_x, &map_x, k, t0, bar);
+                } else {
+                    tc::mbar_expect_tx(&full[s], bytes_x + bytes_w);
+                    tma_load_2d(w_at, &map_w, k, n0, &full[s]);
+                    if (p.gated) tma_load_2d(w_at + bytes_w / 2, &map_w, k, p.N + n0, &full[s]);
+                    tma_load_2d(sx + s * bytes_x, &map_x, k, t0, &full[s]);
+                }
             }
             __syncwarp();
             s += kWays;
@@ -171,14 +201,14 @@ __global__ void __launch_bounds__(kThreads)
             }
         }
         if (lane == 0) issued[warp] = c;
-    } else {
-        const uint32_t idesc = tc::instr_desc(kRows, pl.nb, false, false);
+    } else if (warp < kWays + kIssuers && half == 0) {
+        const uint32_t idesc = tc::instr_desc(kPair ? 2 * kRows : kRows, pl.nb, false, false);
         const uint64_t dx = tc::smem_desc(sx), dw = tc::smem_desc(sw);
         const int issuer = warp - kWays;
         bool ok = true;
         int c = issuer, in_piece = 0;
         uint32_t d = tmem + issuer * pl.nb;
-        for (int s = c % stages, r = c / stages; c < chunks; c += kWays) {
+        for (int s = c % stages, r = c / stages; c < chunks; c += kIssuers) {
             if (!tc::mbar_wait(&full[s], r & 1, &gave_up)) {
                 ok = false;
                 break;
@@ -186,17 +216,21 @@ __global__ void __launch_bounds__(kThreads)
             tc::fence_after();
             if (tc::elect_one()) {
 #pragma unroll
-                for (int k = 0; k < kChunkK / 16; ++k)
-                    tc::mma_ss(d, tc::desc_at(dx, s * bytes_x + k * 32), tc::desc_at(dw, s * bytes_w + k * 32), idesc,
-                               (in_piece | k) != 0);
-                tc::commit(&empty[s]);   // the stage is free once these products have read it
+                for (int k = 0; k < kChunkK / 16; ++k) {
+                    const uint64_t a = tc::desc_at(dx, s * bytes_x + k * 32), b = tc::desc_at(dw, s * bytes_w + k * 32);
+                    if constexpr (kPair) tc::pair_mma(d, a, b, idesc, (in_piece | k) != 0);
+                    else tc::mma_ss(d, a, b, idesc, (in_piece | k) != 0);
+                }
+                // the stage is free once these products have read it
+                if constexpr (kPair) tc::pair_commit(&empty[s]);
+                else tc::commit(&empty[s]);
             }
             __syncwarp();
             if (++in_piece == pl.piece_chunks) {
                 in_piece = 0;
-                d += kWays * pl.nb;
+                d += kIssuers * pl.nb;
             }
-            s += kWays;
+            s += kIssuers;
             if (s >= stages) {
                 s -= stages;
                 ++r;
@@ -204,7 +238,10 @@ __global__ void __launch_bounds__(kThreads)
         }
         if (!ok && lane == 0) flag_error(p.err, DR_ERRF_TIMEOUT);
         // on every path: with `done` the products in flight have ended (a commit follows those before it)
-        if (tc::elect_one()) tc::commit(&done);
+        if (tc::elect_one()) {
+            if constexpr (kPair) tc::pair_commit(&done, ok ? 3 : 1);   // (the second CTA's wait runs out too)
+            else tc::commit(&done);
+        }
         __syncwarp();
     }
     __syncthreads();
@@ -212,7 +249,7 @@ __global__ void __launch_bounds__(kThreads)
     if (gave_up) {
         // copies in flight end by themselves; wait for them before this CTA's shared memory goes away
         if (warp == 0 && lane == 0) {
-            for (int w = 0; w < kWays; ++w)
+            for (int w = 0; half == 0 && w < kWays; ++w)   // both CTAs' copies count on the first one's barriers
                 for (int c = issued[w] - kWays; c >= max(p.stall_tile < 0 ? 0 : 1, issued[w] - stages); c -= kWays)
                     tc::mbar_drain(&full[c % stages], (c / stages) & 1);
             flag_error(p.err, DR_ERRF_TIMEOUT);
@@ -222,35 +259,54 @@ __global__ void __launch_bounds__(kThreads)
     ok = __syncthreads_and(ok);
     tc::fence_after();
 
-    // Sums to shared memory, [row][nb] fp32 in 16-byte pieces that the row turns, so that a warp's stores spread over the banks.
-    // The ring is idle: all its copies were multiplied.
     const int nb = pl.nb;
-    // accumulators in use: an issuer has one for each piece_chunks of its chunks, in turn with the others
-    const auto ceil_div = [](int a, int b) { return (a + b - 1) / b; };
-    int pieces = 0;
-    for (int w = 0; w < kWays; ++w) pieces += ceil_div(ceil_div(max(chunks - w, 0), kWays), pl.piece_chunks);
-    if (ok && (warp & 3) * 32 < rows) {
-        const int row = (warp & 3) * 32 + lane;
-        const uint32_t from = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        float4 *to = reinterpret_cast<float4 *>(staged) + row * (nb / 4);
+    const int row = (warp & 3) * 32 + lane;   // whose sums this thread reads
+    const uint32_t from = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const auto sums = [&](int c, float (&v)[16]) {   // columns c .. c+15 of the row, all pieces of K
+        tc::ld16(from + c, v);
 #pragma unroll 1
-        for (int c = (warp >> 2) * 16; c < nb; c += 32) {
-            float v[16];
-            tc::ld16(from + c, v);
+        for (int i = 1; i < pieces; i += 2) {
+            float one[16], two[16];
+            tc::ld16(from + i * nb + c, one);
+            if (i + 1 < pieces) tc::ld16(from + (i + 1) * nb + c, two);
             tc::wait_ld();
             tc::pin16(v);
-#pragma unroll 1
-            for (int i = 1; i < pieces; ++i) {
-                float more[16];
-                tc::ld16(from + i * nb + c, more);
-                tc::wait_ld();
-                tc::pin16(more);
+            tc::pin16(one);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) v[j] += more[j];
+            for (int j = 0; j < 16; ++j) v[j] += one[j];
+            if (i + 1 < pieces) {
+                tc::pin16(two);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[j] += two[j];
             }
-            if (row < rows)
+        }
+        tc::wait_ld();
+        tc::pin16(v);
+    };
+    const int col0 = (warp >> 2) * 16, cols = blockDim.x / 128 * 16;   // this warp's columns: the first, and to the next
+    const bool boxed = p.vec_out && (!p.residual || p.vec_res);   // rows of whole 16-byte pieces
+    const bool direct = S == 1 && boxed;                          // from tensor memory to the outputs
+    if (ok && (warp & 3) * 32 < rows) {
+        if (direct) {
+#pragma unroll 1
+            for (int c = col0; c < bn; c += cols) {
+                float a[16], b[16];
+                sums(c, a);
+                if (p.gated) sums(bn + c, b);
+                if (row < rows) lin::finish16<kF32>(p, bias + c, bias + bn + c, t0 + row, n0 + c, a, b);
+            }
+        } else {
+            // To shared memory, [row][nb] fp32 in 16-byte pieces that the row turns, so that a warp's stores spread over the
+            // banks.  The ring is idle: all its copies were multiplied.
+            float4 *to = reinterpret_cast<float4 *>(staged) + row * (nb / 4);
+#pragma unroll 1
+            for (int c = col0; c < nb; c += cols) {
+                float v[16];
+                sums(c, v);
+                if (row < rows)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) to[(c / 4 + j) ^ (row & 7)] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                    for (int j = 0; j < 4; ++j) to[(c / 4 + j) ^ (row & 7)] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+            }
         }
     }
     tc::fence_before();
@@ -259,14 +315,15 @@ __global__ void __launch_bounds__(kThreads)
         cluster_wait();   // every CTA of the cluster has set its barrier up
     }
     __syncthreads();
-    if (warp == 2) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(pl.cols));
+    if (kPair) cluster_arrive();
+    if (!kPair && warp == 2) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(pl.cols));
     if (S > 1) {
         if (ok && warp == 0 && lane < S && lane != rank) {   // a lane per owner
             const int theirs = min(share, rows - lane * share);
             const uint32_t slot = (uint32_t)(rank - (rank > lane)) * (theirs * nb * 4);   // parts in rank order, without the owner's
             if (theirs > 0)
-                copy_to_peer(mapa(tc::smem_u32(received) + slot, lane), tc::smem_u32(staged) + lane * share * nb * 4, theirs * nb * 4,
-                             mapa(tc::smem_u32(&parts), lane));
+                copy_to_peer(tc::mapa(tc::smem_u32(received) + slot, lane), tc::smem_u32(staged) + lane * share * nb * 4, theirs * nb * 4,
+                             tc::mapa(tc::smem_u32(&parts), lane));
         }
         __syncwarp();
         if (mine > 0 && !tc::mbar_wait(&parts, 0, &gave_up)) {
@@ -280,10 +337,10 @@ __global__ void __launch_bounds__(kThreads)
         return s == rank ? reinterpret_cast<const float *>(staged) + (rank * share + r) * nb
                          : reinterpret_cast<const float *>(received) + ((s - (s > rank)) * mine + r) * nb;
     };
-    if (ok && p.vec_out && (!p.residual || p.vec_res)) {   // rows of whole 16-byte pieces: 16 columns a thread
+    if (ok && boxed && !direct) {   // 16 columns a thread
         const int groups = bn / 16;
 #pragma unroll 1
-        for (int i = threadIdx.x; i < mine * groups; i += kThreads) {
+        for (int i = threadIdx.x; i < mine * groups; i += blockDim.x) {
             const int r = i / groups, g = i - r * groups, key = (rank * share + r) & 7;
             float a[16], b[16];
 #pragma unroll
@@ -306,10 +363,10 @@ __global__ void __launch_bounds__(kThreads)
             }
             lin::finish16<kF32>(p, bias + g * 16, bias + bn + g * 16, t0 + rank * share + r, n0 + g * 16, a, b);
         }
-    } else if (ok) {   // a column of eight rows a thread: a warp's accesses lie side by side
+    } else if (ok && !boxed) {   // a column of eight rows a thread: a warp's accesses lie side by side
         const int shift = 31 - __clz(bn);   // bn is a power of two
 #pragma unroll 1
-        for (int i = threadIdx.x; i < (mine + 7) / 8 * bn; i += kThreads) {
+        for (int i = threadIdx.x; i < (mine + 7) / 8 * bn; i += blockDim.x) {
             const int c = i & (bn - 1), r0 = (i >> shift) * 8, have = min(8, mine - r0);
             float a[8], b[8];
 #pragma unroll
@@ -328,11 +385,13 @@ __global__ void __launch_bounds__(kThreads)
             lin::finish_column8<kF32>(p, bias[c], bias[p.gated ? bn + c : c], t0 + rank * share + r0, have, n0 + c, a, b);
         }
     }
-    if (S > 1) cluster_wait();
+    if (kPair || S > 1) cluster_wait();
+    if (kPair && warp == 2) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(pl.cols));
 }
 
-// Tile width and split of a call.  Measured with one wave of tiles of 32 against 64 rows of W, us: 128 tokens 1024 -> 4096 5.9
-// and 7.0, 4096 -> 1024 (4 CTAs per tile) 7.3 and 8.1; 256 tokens 1024 -> 4096, where tiles of 32 are two waves, 7.8 and 6.7.
+// Tiles and split of a call.  Measured with one wave of tiles of 32 against 64 rows of W, us: 128 tokens 1024 -> 4096 5.9
+// and 7.0, 4096 -> 1024 (4 CTAs per tile) 7.3 and 8.1; 256 tokens 1024 -> 4096, where tiles of 32 are two waves, 7.8 and 6.7.  Tiles of
+// 64 against pairs, where both are a wave: 512 tokens 1024 -> 2048 6.3 and 6.7, 1024 tokens 4096 -> 1024 12.5 and 13.4.
 // A CTA of a split keeps 16 chunks: 128 tokens 1024 -> 1536 whole 5.4, halved 5.6; 4096 -> 1024 in 2, 4, 8 parts 8.7, 7.3, 8.3.
 ClusterPlan make_plan(const LinearParams &p, int sms) {
     ClusterPlan pl;
@@ -342,20 +401,23 @@ ClusterPlan make_plan(const LinearParams &p, int sms) {
         const int bn = p.gated ? nb / 2 : nb;
         return mtiles * ((p.N + bn - 1) / bn);
     };
-    pl.nb = tiles(32) <= sms ? 32 : kMaxNb;   // (more than one wave of tiles of 64 goes to the pairs)
+    pl.pair = tiles(64) > sms;
+    pl.nb = pl.pair ? kPairNb : tiles(32) <= sms ? 32 : 64;
+    pl.threads = pl.nb == 32 ? 256 : kMaxThreads;
     pl.split = 1;
-    while (pl.split < 8 && tiles(pl.nb) * pl.split * 2 <= sms && chunks / (2 * pl.split) >= 16) pl.split *= 2;
+    while (!pl.pair && pl.split < 8 && tiles(pl.nb) * pl.split * 2 <= sms && chunks / (2 * pl.split) >= 16) pl.split *= 2;
     const int rows = p.T < kRows ? p.T : kRows;
     pl.box_rows = (rows + 7) / 8 * 8;
     const int most = (chunks + pl.split - 1) / pl.split;   // chunks of a CTA
-    const int own_chunks = (most + kWays - 1) / kWays, max_cols = pl.split > 1 ? 256 : 512;
-    const auto pieces = [&] { return kWays * ((own_chunks + pl.piece_chunks - 1) / pl.piece_chunks); };
+    const int issuers = pl.pair ? kPairIssuers : kWays;
+    const int own_chunks = (most + issuers - 1) / issuers, max_cols = pl.pair || pl.split > 1 ? 256 : 512;
+    const auto pieces = [&] { return issuers * ((own_chunks + pl.piece_chunks - 1) / pl.piece_chunks); };
     pl.piece_chunks = p.out_f32 ? kPieceChunks : own_chunks;
     while (pieces() * pl.nb > max_cols) ++pl.piece_chunks;
     pl.cols = 32;
     while (pl.cols < pl.nb * pieces()) pl.cols *= 2;
     // shared memory: the ring, with what its last stage's products may read past it, or after it the CTA's own sums; the parts
-    const size_t stage = (size_t)(pl.box_rows + pl.nb) * 128, own = parts_bytes(rows, pl);
+    const size_t stage = (size_t)(pl.box_rows + (pl.pair ? pl.nb / 2 : pl.nb)) * 128, own = parts_bytes(rows, pl);
     const size_t parts = pl.split > 1 ? parts_bytes(rows + pl.split, pl) : 0;
     const auto ring = [&](int n) {
         const size_t over = n * stage > (size_t)(n * pl.box_rows + kRows) * 128 ? n * stage : (size_t)(n * pl.box_rows + kRows) * 128;
@@ -371,16 +433,25 @@ ClusterPlan make_plan(const LinearParams &p, int sms) {
     return pl;
 }
 
+using Kernel = void (*)(const CUtensorMap, const CUtensorMap, const ClusterArgs);
+Kernel kernel_of(bool f32, bool pair) {
+    return f32 ? linear_cluster_kernel<true, false> : pair ? linear_cluster_kernel<false, true> : linear_cluster_kernel<false, false>;
+}
+
+int64_t plan_tiles(const LinearParams &p, const ClusterPlan &pl) {
+    const int bn = p.gated ? pl.nb / 2 : pl.nb, bt = pl.pair ? 2 * kRows : kRows;
+    return ((int64_t)p.T + bt - 1) / bt * ((p.N + bn - 1) / bn);
+}
+
 }  // namespace
 
-bool linear_cluster_keeps(const LinearParams &p, int sms) { return !p.out_f32 || make_plan(p, sms).piece_chunks <= kPieceChunks; }
-
-int linear_cluster_tiles(const LinearParams &p, int sms) {
+bool linear_cluster_takes(const LinearParams &p, int sms) {
     const ClusterPlan pl = make_plan(p, sms);
-    const int bn = p.gated ? pl.nb / 2 : pl.nb;
-    const int64_t n = (int64_t)((p.T + kRows - 1) / kRows) * ((p.N + bn - 1) / bn);
-    return n > 0x7FFFFFFF ? 0x7FFFFFFF : (int)n;
+    if (pl.pair) return !p.out_f32 && p.T > kRows && plan_tiles(p, pl) <= sms / 2;
+    return !p.out_f32 || pl.piece_chunks <= kPieceChunks;
 }
+
+int linear_cluster_tiles(const LinearParams &p, int sms) { return (int)plan_tiles(p, make_plan(p, sms)); }
 
 cudaError_t launch_linear_cluster(const LinearParams &p, int sms, cudaStream_t stream) {
     ClusterArgs a;
@@ -390,17 +461,20 @@ cudaError_t launch_linear_cluster(const LinearParams &p, int sms, cudaStream_t s
     const int bn = p.gated ? pl.nb / 2 : pl.nb;
     CUtensorMap map_x, map_w;
     if (!encode_matrix(&map_x, p.x, false, p.T, p.K, p.x_stride, pl.box_rows, kChunkK) ||
-        !encode_matrix(&map_w, p.W, false, (int64_t)p.N * (p.gated ? 2 : 1), p.K, p.K, bn, kChunkK))
+        !encode_matrix(&map_w, p.W, false, (int64_t)p.N * (p.gated ? 2 : 1), p.K, p.K, pl.pair ? pl.nb / 2 : bn, kChunkK))
         return cudaErrorInvalidValue;
     static std::atomic<uint64_t> ready{0};
     cudaError_t e = once_per_device(ready, [] {
-        const cudaError_t err = cudaFuncSetAttribute(linear_cluster_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem);
-        return err != cudaSuccess ? err : cudaFuncSetAttribute(linear_cluster_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem);
+        for (const Kernel k : {kernel_of(false, false), kernel_of(false, true), kernel_of(true, false)}) {
+            const cudaError_t err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem);
+            if (err != cudaSuccess) return err;
+        }
+        return cudaSuccess;
     });
     if (e != cudaSuccess) return e;
-    auto kern = p.out_f32 ? linear_cluster_kernel<true> : linear_cluster_kernel<false>;
-    const dim3 grid((unsigned)pl.split, (unsigned)((p.N + bn - 1) / bn), (unsigned)((p.T + kRows - 1) / kRows));
-    return launch_kernel(kern, grid, dim3(kThreads), pl.smem, stream, (unsigned)pl.split, map_x, map_w, a);
+    const int cluster = pl.pair ? 2 : pl.split, bt = pl.pair ? 2 * kRows : kRows;
+    const dim3 grid((unsigned)cluster, (unsigned)((p.N + bn - 1) / bn), (unsigned)((p.T + bt - 1) / bt));
+    return launch_kernel(kernel_of(p.out_f32, pl.pair), grid, dim3((unsigned)pl.threads), pl.smem, stream, (unsigned)cluster, map_x, map_w, a);
 }
 
 }  // namespace dr

@@ -90,12 +90,34 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     return r;
 }
 
-// The output that holds column n.
+// The output that holds column n (and by value: constant operands, where a looked-up place of the parameters is a load).
 __device__ __forceinline__ int out_of(const LinearParams &p, int n) {
     int s = 0;
     for (int i = 1; i < p.n_outs; ++i)
         if (n >= p.out[i].col0) s = i;
     return s;
+}
+__device__ __forceinline__ LinearOut output_of(const LinearParams &p, int n) {
+    LinearOut o = p.out[0];
+    if (p.n_outs > 1)
+#pragma unroll
+        for (int i = 1; i < DR_LINEAR_MAX_OUTS; ++i)
+            if (i < p.n_outs && n >= p.out[i].col0) o = p.out[i];
+    return o;
+}
+
+template <int n>
+__device__ __forceinline__ void add_bias(float *v, const float *bias) {   // bias: 16-byte aligned
+#pragma unroll
+    for (int j = 0; j < n; j += 4) {
+        const float4 b = *reinterpret_cast<const float4 *>(bias + j);
+        const float2 x = __fadd2_rn(make_float2(v[j], v[j + 1]), make_float2(b.x, b.y)),
+                     y = __fadd2_rn(make_float2(v[j + 2], v[j + 3]), make_float2(b.z, b.w));
+        v[j] = x.x;
+        v[j + 1] = x.y;
+        v[j + 2] = y.x;
+        v[j + 3] = y.y;
+    }
 }
 
 // Sixteen columns n .. n+15 (n a multiple of 16) of token t: bias (of these columns, fp32), activation, gating and residual on
@@ -116,12 +138,8 @@ __device__ __forceinline__ void finish16(const LinearParams &p, const float *bia
         for (int i = 0; i < kWords / 4; ++i) r[i] = from[i];
     }
     if (p.bias) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) a[i] += bias_a[i];
-        if (p.gated) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) b[i] += bias_b[i];
-        }
+        add_bias<16>(a, bias_a);
+        if (p.gated) add_bias<16>(b, bias_b);
     }
     activate<16>(a, p.act);
     if (p.gated) {
@@ -147,7 +165,7 @@ __device__ __forceinline__ void finish16(const LinearParams &p, const float *bia
                 else a[i] += __uint_as_float((uint32_t)static_cast<const uint16_t *>(p.residual)[res_at + i] << 16);
             }
     }
-    const LinearOut &o = p.out[out_of(p, n)];
+    const LinearOut o = output_of(p, n);
     const int64_t at = (int64_t)t * o.stride + (n - o.col0);
     if (have >= 16) {
         uint4 *to = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(o.ptr) + at * (kF32 ? 4 : 2));
@@ -199,7 +217,7 @@ __device__ __forceinline__ void finish_column8(const LinearParams &p, float bias
 #pragma unroll
         for (int i = 0; i < 8; ++i) a[i] *= b[i];
     }
-    const LinearOut &o = p.out[out_of(p, n)];
+    const LinearOut o = output_of(p, n);
     T *to = static_cast<T *>(o.ptr) + (int64_t)t * o.stride + (n - o.col0);
     const int64_t stride = o.stride;
 #pragma unroll

@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) linear_rows_kernel(const __gri
             a[0] *= b[0] + bias[2];
             a[1] *= b[1] + bias[3];
         }
-        const LinearOut &o = p.out[lin::out_of(p, n)];
+        const LinearOut o = lin::output_of(p, n);
         const int64_t at = (int64_t)row * o.stride + (n - o.col0);
         if (p.residual) {
             a[0] = r[0] + a[0];

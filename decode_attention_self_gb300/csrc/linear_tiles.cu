@@ -70,23 +70,11 @@ struct Control {
     int gave_up;   // some wait ran out
 };
 
-__device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank) {
-    uint32_t r;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-    return r;
-}
 // All threads of both CTAs have come here.  Relaxed: the barriers' set-up has a fence of its own, and at the end nothing is handed
 // over (a release would wait for the last stores, some 1400 cycles).
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// A copy into this CTA's shared memory that counts on a barrier of either CTA of the pair (a cluster address).
-__device__ __forceinline__ void pair_load(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], "
-        "[%4];" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
-        : "memory");
 }
 __device__ __forceinline__ void own_load(uint32_t dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
     asm volatile(
@@ -107,20 +95,6 @@ __device__ __forceinline__ uint4 lds16(uint32_t a) {
 }
 __device__ __forceinline__ void sts16(uint32_t a, uint4 v) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-}
-__device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
-        : "memory");
-}
-// Arrives on the barrier at this place in both CTAs once the products issued so far are over.
-__device__ __forceinline__ void pair_commit(uint64_t *bar) {
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-            tc::smem_u32(bar)),
-        "h"((uint16_t)3)
-        : "memory");
 }
 __device__ __forceinline__ void remote_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -195,7 +169,7 @@ struct LooseRows {
 #pragma unroll
         for (int c = 0; c < 32; ++c) box[lane * 32 + (c ^ lane)] = v[c];
         __syncwarp();
-        const LinearOut &o = p.out[lin::out_of(p, n)];   // the 32 columns lie in one output
+        const LinearOut o = lin::output_of(p, n);   // the 32 columns lie in one output
         const int rows = min(32, p.T - t0), col = n - o.col0 + lane;
         T *to = static_cast<T *>(o.ptr) + (int64_t)t0 * o.stride + col;
         for (int r = 0; r < rows; ++r, to += o.stride)
@@ -226,19 +200,6 @@ struct Share {
         active = col0 < cols;
     }
 };
-
-__device__ __forceinline__ void add_bias32(float *v, const float *bias) {
-#pragma unroll
-    for (int j = 0; j < 32; j += 4) {
-        const float4 b = *reinterpret_cast<const float4 *>(bias + j);
-        const float2 x = __fadd2_rn(make_float2(v[j], v[j + 1]), make_float2(b.x, b.y)),
-                     y = __fadd2_rn(make_float2(v[j + 2], v[j + 3]), make_float2(b.z, b.w));
-        v[j] = x.x;
-        v[j + 1] = x.y;
-        v[j + 2] = y.x;
-        v[j + 3] = y.y;
-    }
-}
 
 template <bool kF32>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -316,10 +277,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                             break;
                         }
                         if (tc::elect_one()) {
-                            const uint32_t bar = mapa(tc::smem_u32(&ctl.full[s]), 0);
+                            const uint32_t bar = tc::mapa(tc::smem_u32(&ctl.full[s]), 0);
                             if (rank == 0) tc::mbar_expect_tx(&ctl.full[s], 2 * kHalf + args.tile_w * 128);
-                            pair_load(sx + s * kHalf, &maps.x, c * 64, t, bar);
-                            pair_load(sw + s * kHalf, &maps.w, c * 64, w, bar);
+                            tc::pair_load(sx + s * kHalf, &maps.x, c * 64, t, bar);
+                            tc::pair_load(sw + s * kHalf, &maps.w, c * 64, w, bar);
                         }
                         __syncwarp();
                         armed |= 1u << s;
@@ -364,10 +325,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (tc::elect_one()) {
     #pragma unroll
                             for (int k = 0; k < 4; ++k)
-                                pair_mma(d, tc::desc_at(dx, s * kHalf + k * 32), tc::desc_at(dw, s * kHalf + k * 32), idesc,
-                                         c > c0 || k > 0);
-                            pair_commit(&ctl.empty[s]);
-                            if (c + 1 == end) pair_commit(&ctl.sums_full[b]);
+                                tc::pair_mma(d, tc::desc_at(dx, s * kHalf + k * 32), tc::desc_at(dw, s * kHalf + k * 32), idesc,
+                                             c > c0 || k > 0);
+                            tc::pair_commit(&ctl.empty[s]);
+                            if (c + 1 == end) tc::pair_commit(&ctl.sums_full[b]);
                         }
                         __syncwarp();
                         if (++s == kStages) {
@@ -379,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!ok) {
                 if (lane == 0) flag_error(p.err, DR_ERRF_TIMEOUT);
-                if (tc::elect_one()) pair_commit(&ctl.done);
+                if (tc::elect_one()) tc::pair_commit(&ctl.done);
                 __syncwarp();
                 tc::mbar_drain(&ctl.done, 0);
             }
@@ -450,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const auto release = [&] {   // this warp has its sums: the place may have another tile's
             tc::fence_before();
             __syncwarp();
-            if (lane == 0) remote_arrive(mapa(tc::smem_u32(&ctl.sums_free[chain & 1]), 0));
+            if (lane == 0) remote_arrive(tc::mapa(tc::smem_u32(&ctl.sums_free[chain & 1]), 0));
             chain += shared ? 1 : 2;
         };
         for (int i = share.first; share.active && ok && i < tiles; i += share.step) {
@@ -491,8 +452,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // 32 columns: the sums v (gated: times those in g) to the box or the output
             const auto block = [&](float *v, float *g, int k) {
                 if (p.bias) {
-                    add_bias32(v, b + k * 32);
-                    if (p.gated) add_bias32(g, b + k * 32 + apart);
+                    lin::add_bias<32>(v, b + k * 32);
+                    if (p.gated) lin::add_bias<32>(g, b + k * 32 + apart);
                 }
                 lin::activate<32>(v, p.act);
                 if (p.gated) {

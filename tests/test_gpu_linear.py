@@ -248,7 +248,7 @@ ref = o.double() / (o.double() ** 2).mean(1, keepdim=True).add(1e-5).sqrt()
 assert ((y.double() - ref).norm() / ref.norm()).item() < 2 ** -7
 """
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
-    for size in ("4 512 512", "28 512 512", "200 2048 512", "4000 512 1024"):
+    for size in ("4 512 512", "28 512 512", "200 2048 512", "2000 512 1024", "4000 512 1024"):
         subprocess.run([sys.executable, "-c", code, *size.split()], check=True, cwd=root, timeout=300)
 
 
@@ -261,7 +261,8 @@ def test_kernels_side_by_side_on_four_streams(api):
     kl = torch.tensor([L, L], dtype=torch.int32, device="cuda")
     hid, head = randn((16, 1024), 53).cuda(), randn((9 * 1088, 1024), 54, 0.03).cuda()
     jobs = []
-    for T, K, N, out in ((2600, 1024, 1024, BF16), (128, 4096, 1024, BF16), (700, 2048, 512, F32), (20, 1024, 1024, BF16)):
+    for T, K, N, out in ((2600, 1024, 1024, BF16), (128, 4096, 1024, BF16), (700, 2048, 512, F32), (20, 1024, 1024, BF16),
+                         (2000, 1024, 1024, BF16), (1200, 256, 1024, BF16)):
         x, W = randn((T, K), T).cuda(), randn((N, K), T + 1, K ** -0.5).cuda()
         jobs.append((lambda s, o, x=x, W=W: api.dr_linear(x, W, o, act="gelu", stream=s), (T, N), out))
     jobs.append((lambda s, o: api.dr_lm_head(hid, head, 9, o, stream=s), (16, 9, 1088), F32))
@@ -289,7 +290,7 @@ def test_kernels_side_by_side_on_four_streams(api):
 
 def test_a_chain_of_products_reads_what_the_one_before_wrote(api):
     # launches overlap their predecessors' ends; each must still see all of its predecessor's output
-    for T in (1, 24, 128, 1100, 3000):
+    for T in (1, 24, 128, 1100, 3000, 4500):
         Ws = [randn((512, 512), 10 + i, 512 ** -0.5).cuda() for i in range(6)]
         x = randn((T, 512), 3).cuda()
         bufs = [torch.empty((T, 512), dtype=BF16, device="cuda") for _ in Ws]
@@ -347,6 +348,95 @@ def test_wait_that_runs_out(api, T, K, N):
     hole = got.isnan()
     assert hole.any() and not hole.all()
     assert_within(torch.where(hole, ref.float(), got), ref, tol + half_step(F32) * ref.abs(), "tiles that ran")
+    err.zero_()
+    api.dr_linear(x, W, o, bias=b, err_flag=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    assert_within(o, ref, tol, "the call after")
+
+
+# Tiles of 256 tokens by 128 weight rows, one for each pair of CTAs: bf16 outputs, more than a wave of smaller tiles, no more
+# than a wave of these.
+PAIRED = [(130, 64, 9600), (257, 8, 4000), (1900, 72, 1089), (2000, 1000, 1088), (1400, 1024, 1536), (512, 4096, 2560),
+          (1025, 520, 1800), (2048, 320, 1024), (4600, 2048, 500)]
+
+
+@pytest.mark.parametrize("T,K,N", PAIRED)
+@pytest.mark.parametrize("act,gated,bias,residual", [(None, False, False, False), ("gelu", False, True, True), ("silu", True, True, False),
+                                                     ("relu", True, False, True)])
+def test_paired_sizes(api, T, K, N, act, gated, bias, residual):
+    run_and_check(api, T, K, N // 2 if gated else N, act, gated, bias, residual, BF16, seed=T + N)
+
+
+@pytest.mark.parametrize("T", [1300, 1900])
+@pytest.mark.parametrize("pad", [1, 8, 16])
+def test_paired_slices_in_place(api, T, pad):
+    K, N = 264, 1000
+    (x, W, b, r), ref, tol = problem(T, K, N, "gelu", False, True, True, BF16, seed=T)
+    xb = torch.full((T, K + 72), float("nan"), dtype=BF16, device="cuda")
+    xb[:, 8:8 + K] = x
+    ob = torch.full((T + 2, N + 2 * pad), 7.0, dtype=BF16, device="cuda")
+    o = ob[1:T + 1, pad:pad + N]
+    o.copy_(r)
+    api.dr_linear(xb[:, 8:8 + K], W, o, bias=b, act="gelu", residual=o)
+    torch.cuda.synchronize()
+    assert_within(o, ref, tol, "in place")
+    ob[1:T + 1, pad:pad + N] = 7.0
+    assert (ob == 7.0).all()
+
+
+def test_paired_nan_and_infinity_stay_in_their_rows_and_columns(api):
+    T, K, N = 1900, 200, 1030
+    (x, W, b, r), ref, tol = problem(T, K, N, None, False, True, True, BF16, seed=6)
+    x, W = x.clone(), W.clone()
+    x[1000, 3] = float("nan")
+    x[1899] = float("inf")
+    W[77, 5] = float("nan")
+    o = torch.empty((T, N), dtype=BF16, device="cuda")
+    api.dr_linear(x, W, o, bias=b, residual=r)
+    o = o.cpu()
+    assert o[1000].isnan().all() and not o[1899].isfinite().any() and o[:, 77].isnan().all()
+    keep = torch.ones((T, N), dtype=torch.bool)
+    keep[1000], keep[1899], keep[:, 77] = False, False, False
+    assert_within(torch.where(keep, o.float(), ref.float()), ref, tol + 1e-6 * ref.abs(), "the others")
+
+
+def test_paired_same_bits_on_two_streams_and_in_a_graph(api):
+    s2 = torch.cuda.Stream()
+    (x, W, b, r), ref, tol = problem(1900, 1024, 1024, "gelu", False, True, True, BF16, seed=8)
+    first = torch.empty((1900, 1024), dtype=BF16, device="cuda")
+    api.dr_linear(x, W, first, bias=b, act="gelu", residual=r)
+    torch.cuda.synchronize()
+    assert_within(first, ref, tol, "first")
+    outs = [torch.empty_like(first) for _ in range(40)]
+    for i, o in enumerate(outs):
+        api.dr_linear(x, W, o, bias=b, act="gelu", residual=r, stream=s2 if i % 2 else None)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, first) for o in outs)
+    g, o = torch.cuda.CUDAGraph(), torch.empty_like(first)
+    with torch.cuda.graph(g):
+        for _ in range(2):
+            api.dr_linear(x, W, o, bias=b, act="gelu", residual=r)
+    for _ in range(3):
+        o.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, first)
+
+
+@pytest.mark.parametrize("T,K,N,tile", [(2048, 512, 1024, 1), (1900, 72, 1089, 71)])
+def test_paired_wait_that_runs_out(api, T, K, N, tile):
+    (x, W, b, _), ref, tol = problem(T, K, N, None, False, True, False, BF16, seed=T)
+    o = torch.full((T, N), float("nan"), dtype=BF16, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    api.dr_linear_stall_test(tile, x, W, o, bias=b, err_flag=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) & api.DR_ERRF_TIMEOUT
+    got = o.cpu()
+    t0, n0 = tile // -(-N // 128) * 256, tile % -(-N // 128) * 128
+    assert got[t0:t0 + 256, n0:n0 + 128].isnan().all()   # both CTAs' halves
+    got[t0:t0 + 256, n0:n0 + 128] = ref[t0:t0 + 256, n0:n0 + 128].to(BF16)
+    assert_within(got, ref, tol, "tiles that ran")
     err.zero_()
     api.dr_linear(x, W, o, bias=b, err_flag=err)
     torch.cuda.synchronize()
