@@ -40,8 +40,8 @@ namespace {
 enum class Way { kRows, kCluster, kTiles };
 
 // Which kernel takes a call; measured on both sides of each border, us.
-// Rows or cluster: 16 tokens 8192 -> 8192 24 and 29; 32 tokens, where a CTA's tokens weigh more, 1024 -> 1536 3.5 and 5.2,
-// 1024 -> 4096 4.9 and 6.4, 4096 -> 1024 6.8 and 6.6, 1536 -> 6144 10.0 and 8.0, 8192 -> 8192 44 and 29.
+// Rows or cluster: 16 tokens 8192 -> 8192 24.6 and 27.8, 4096 -> 1024 5.2 and 6.2; 32 tokens, where a CTA's tokens weigh more, 1024 ->
+// 1536 3.6 and 4.4, 1024 -> 4096 4.6 and 5.6, 4096 -> 1024 7.0 and 6.3, 1536 -> 6144 10.0 and 7.8, 8192 -> 8192 44 and 28.
 // Cluster or tiles: the pairs that stay take what is more than one wave of tiles of 128 tokens by 64 weight rows and, with bf16
 // outputs, of pairs' tiles of 256 by 128.  1024 tokens 4096 -> 1024 (128 of 128 by 64) 12.6 and 18, 256 tokens 1024 -> 4096 (128) 6.7 and
 // 8.3; 512 tokens 1024 -> 4096 (64 of 256 by 128) 8.0 and 9.7, 2048 tokens 4096 -> 1024 (64) 15.4 and 19.3, 700 tokens 1024 -> 4096 (96)

@@ -389,10 +389,12 @@ __global__ void __launch_bounds__(kMaxThreads)
     if (kPair && warp == 2) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(pl.cols));
 }
 
-// Tiles and split of a call.  Measured with one wave of tiles of 32 against 64 rows of W, us: 128 tokens 1024 -> 4096 5.9
-// and 7.0, 4096 -> 1024 (4 CTAs per tile) 7.3 and 8.1; 256 tokens 1024 -> 4096, where tiles of 32 are two waves, 7.8 and 6.7.  Tiles of
+// Tiles and split of a call.  Measured with one wave of tiles of 32 against 64 rows of W, us: 128 tokens 1024 -> 4096 5.8
+// and 6.9, 4096 -> 1024 (4 CTAs per tile) 6.7 and 8.6; 256 tokens 1024 -> 4096, where tiles of 32 are two waves, 7.8 and 6.8.  Tiles of
 // 64 against pairs, where both are a wave: 512 tokens 1024 -> 2048 6.3 and 6.7, 1024 tokens 4096 -> 1024 12.5 and 13.4.
-// A CTA of a split keeps 16 chunks: 128 tokens 1024 -> 1536 whole 5.4, halved 5.6; 4096 -> 1024 in 2, 4, 8 parts 8.7, 7.3, 8.3.
+// A CTA of a split keeps 4 chunks (or 6, 8, 16, us): 128 tokens 1000 -> 500 5.0 (5.6, 5.6, 7.3), 1024 -> 1024 4.8 (5.0, 5.0, 5.1), 2048 ->
+// 1024 5.6 (5.6, 5.5, 6.0); 64 tokens 1536 -> 1024 4.4 (4.4, 5.0, 5.4).  Eight chunks are not split: 64 tokens 512 -> 512 3.7 whole, 3.9
+// halved.
 ClusterPlan make_plan(const LinearParams &p, int sms) {
     ClusterPlan pl;
     const int chunks = (p.K + kChunkK - 1) / kChunkK;
@@ -405,7 +407,7 @@ ClusterPlan make_plan(const LinearParams &p, int sms) {
     pl.nb = pl.pair ? kPairNb : tiles(32) <= sms ? 32 : 64;
     pl.threads = pl.nb == 32 ? 256 : kMaxThreads;
     pl.split = 1;
-    while (!pl.pair && pl.split < 8 && tiles(pl.nb) * pl.split * 2 <= sms && chunks / (2 * pl.split) >= 16) pl.split *= 2;
+    while (!pl.pair && chunks > 8 && pl.split < 8 && tiles(pl.nb) * pl.split * 2 <= sms && chunks / (2 * pl.split) >= 4) pl.split *= 2;
     const int rows = p.T < kRows ? p.T : kRows;
     pl.box_rows = (rows + 7) / 8 * 8;
     const int most = (chunks + pl.split - 1) / pl.split;   // chunks of a CTA
