@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(kMaxThreads)
                 float a[16], b[16];
                 sums(c, a);
                 if (p.gated) sums(bn + c, b);
-                if (row < rows) lin::finish16<kF32>(p, bias + c, bias + bn + c, t0 + row, n0 + c, a, b);
+                if (row < rows) lin::finish<kF32, 16>(p, bias + c, bias + bn + c, t0 + row, n0 + c, a, b);
             }
         } else {
             // To shared memory, [row][nb] fp32 in 16-byte pieces that the row turns, so that a warp's stores spread over the
@@ -337,31 +337,23 @@ __global__ void __launch_bounds__(kMaxThreads)
         return s == rank ? reinterpret_cast<const float *>(staged) + (rank * share + r) * nb
                          : reinterpret_cast<const float *>(received) + ((s - (s > rank)) * mine + r) * nb;
     };
-    if (ok && boxed && !direct) {   // 16 columns a thread
-        const int groups = bn / 16;
+    if (ok && boxed && !direct) {   // four columns a thread
+        const int shift = 29 - __clz(bn);   // bn is a power of two
 #pragma unroll 1
-        for (int i = threadIdx.x; i < mine * groups; i += blockDim.x) {
-            const int r = i / groups, g = i - r * groups, key = (rank * share + r) & 7;
-            float a[16], b[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) a[j] = b[j] = 0.f;
+        for (int i = threadIdx.x; i < mine << shift; i += blockDim.x) {
+            const int r = i >> shift, g = i - (r << shift), key = (rank * share + r) & 7;
+            float a[4] = {0.f, 0.f, 0.f, 0.f}, b[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
             for (int s = 0; s < S; ++s) {
                 const float4 *from = reinterpret_cast<const float4 *>(part(s, r));
-#pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    const float4 v = from[(4 * g + h) ^ key];
-                    a[4 * h] += v.x; a[4 * h + 1] += v.y; a[4 * h + 2] += v.z; a[4 * h + 3] += v.w;
-                }
+                const float4 v = from[g ^ key];
+                a[0] += v.x; a[1] += v.y; a[2] += v.z; a[3] += v.w;
                 if (p.gated) {
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        const float4 v = from[(bn / 4 + 4 * g + h) ^ key];
-                        b[4 * h] += v.x; b[4 * h + 1] += v.y; b[4 * h + 2] += v.z; b[4 * h + 3] += v.w;
-                    }
+                    const float4 u = from[(bn / 4 + g) ^ key];
+                    b[0] += u.x; b[1] += u.y; b[2] += u.z; b[3] += u.w;
                 }
             }
-            lin::finish16<kF32>(p, bias + g * 16, bias + bn + g * 16, t0 + rank * share + r, n0 + g * 16, a, b);
+            lin::finish<kF32, 4>(p, bias + g * 4, bias + bn + g * 4, t0 + rank * share + r, n0 + g * 4, a, b);
         }
     } else if (ok && !boxed) {   // a column of eight rows a thread: a warp's accesses lie side by side
         const int shift = 31 - __clz(bn);   // bn is a power of two

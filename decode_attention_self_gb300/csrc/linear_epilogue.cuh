@@ -120,46 +120,51 @@ __device__ __forceinline__ void add_bias(float *v, const float *bias) {   // bia
     }
 }
 
-// Sixteen columns n .. n+15 (n a multiple of 16) of token t: bias (of these columns, fp32), activation, gating and residual on
-// the sums a (and b, the sums of the rows that are multiplied in), stored to the output that holds them.  Columns from N on
-// are left out.
-template <bool kF32>
-__device__ __forceinline__ void finish16(const LinearParams &p, const float *bias_a, const float *bias_b, int t, int n, float (&a)[16],
-                                         float (&b)[16]) {
-    constexpr int kWords = kF32 ? 16 : 8;   // 32-bit words of the 16 columns
+// kN columns n .. n + kN - 1 (4 or 16, n a multiple of it) of token t: bias (of these columns, fp32), activation, gating and
+// residual on the sums a (and b, the sums of the rows that are multiplied in), stored to the output that holds them.  Columns
+// from N on are left out.
+template <bool kF32, int kN>
+__device__ __forceinline__ void finish(const LinearParams &p, const float *bias_a, const float *bias_b, int t, int n, float (&a)[kN],
+                                       float (&b)[kN]) {
+    constexpr int kWords = kF32 ? kN : kN / 2;   // 32-bit words of the columns
+    using Piece = typename std::conditional<kWords % 4 == 0, uint4, uint2>::type;
+    constexpr int kPieces = kWords * 4 / (int)sizeof(Piece);
+    union Words {
+        Piece piece[kPieces];
+        uint32_t w[kWords];
+    };
     const int have = p.N - n;
     if (have <= 0) return;
-    uint4 r[kWords / 4];
-    const bool quick_res = p.residual && have >= 16;
+    Words r;
+    const bool quick_res = p.residual && have >= kN;
     const int64_t res_at = (int64_t)t * p.res_stride + n;
     if (quick_res) {   // on its way during the arithmetic
-        const uint4 *from = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p.residual) + res_at * (kF32 ? 4 : 2));
+        const Piece *from = reinterpret_cast<const Piece *>(static_cast<const uint8_t *>(p.residual) + res_at * (kF32 ? 4 : 2));
 #pragma unroll
-        for (int i = 0; i < kWords / 4; ++i) r[i] = from[i];
+        for (int i = 0; i < kPieces; ++i) r.piece[i] = from[i];
     }
     if (p.bias) {
-        add_bias<16>(a, bias_a);
-        if (p.gated) add_bias<16>(b, bias_b);
+        add_bias<kN>(a, bias_a);
+        if (p.gated) add_bias<kN>(b, bias_b);
     }
-    activate<16>(a, p.act);
+    activate<kN>(a, p.act);
     if (p.gated) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) a[i] *= b[i];
+        for (int i = 0; i < kN; ++i) a[i] *= b[i];
     }
     if (quick_res) {
-        const uint32_t *w = reinterpret_cast<const uint32_t *>(r);
 #pragma unroll
         for (int i = 0; i < kWords; ++i) {
             if constexpr (kF32) {
-                a[i] += __uint_as_float(w[i]);
+                a[i] += __uint_as_float(r.w[i]);
             } else {
-                a[2 * i] += bf16_lo(w[i]);
-                a[2 * i + 1] += bf16_hi(w[i]);
+                a[2 * i] += bf16_lo(r.w[i]);
+                a[2 * i + 1] += bf16_hi(r.w[i]);
             }
         }
     } else if (p.residual) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
+        for (int i = 0; i < kN; ++i)
             if (i < have) {
                 if constexpr (kF32) a[i] += static_cast<const float *>(p.residual)[res_at + i];
                 else a[i] += __uint_as_float((uint32_t)static_cast<const uint16_t *>(p.residual)[res_at + i] << 16);
@@ -167,20 +172,19 @@ __device__ __forceinline__ void finish16(const LinearParams &p, const float *bia
     }
     const LinearOut o = output_of(p, n);
     const int64_t at = (int64_t)t * o.stride + (n - o.col0);
-    if (have >= 16) {
-        uint4 *to = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(o.ptr) + at * (kF32 ? 4 : 2));
+    if (have >= kN) {
+        Words y;
 #pragma unroll
-        for (int i = 0; i < kWords / 4; ++i) {
-            if constexpr (kF32)
-                to[i] = make_uint4(__float_as_uint(a[4 * i]), __float_as_uint(a[4 * i + 1]), __float_as_uint(a[4 * i + 2]),
-                                   __float_as_uint(a[4 * i + 3]));
-            else
-                to[i] = make_uint4(pack2(a[8 * i], a[8 * i + 1]), pack2(a[8 * i + 2], a[8 * i + 3]), pack2(a[8 * i + 4], a[8 * i + 5]),
-                                   pack2(a[8 * i + 6], a[8 * i + 7]));
+        for (int i = 0; i < kWords; ++i) {
+            if constexpr (kF32) y.w[i] = __float_as_uint(a[i]);
+            else y.w[i] = pack2(a[2 * i], a[2 * i + 1]);
         }
+        Piece *to = reinterpret_cast<Piece *>(static_cast<uint8_t *>(o.ptr) + at * (kF32 ? 4 : 2));
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) to[i] = y.piece[i];
     } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
+        for (int i = 0; i < kN; ++i)
             if (i < have) {
                 if constexpr (kF32) static_cast<float *>(o.ptr)[at + i] = a[i];
                 else static_cast<uint16_t *>(o.ptr)[at + i] = f32_to_bf16_rn(a[i]);
