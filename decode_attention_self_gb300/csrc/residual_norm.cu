@@ -238,27 +238,28 @@ auto kernel_of(bool x_f32, bool res_f32) {
 cudaError_t launch_residual_norm(const ResidualNormParams &p, cudaStream_t stream) {
     const int sms = current_device_sms();
     if (sms <= 0) return cudaErrorInvalidDevice;
-    // Few rows: 8 elements a thread, for the shortest way through a row.  Many: 32 a thread (16 where a stream is fp32), which
-    // leaves less to do per element and, up to 1024 elements, no barrier; and two rows in turn, the second's inputs on their way
-    // during the first.  65536 x 1024, RMS norm of a sum, us: 8 elements 97, 16 a thread 84, 32 83, 32 and two rows 80, four rows
-    // 81 (80 at the rate of a copy); 128 x 1024, layer norm: 8 elements 2.1, 16 2.4, 32 2.4.
+    // Few rows: 8 elements a thread, for the shortest way through a row.  Many: 16 to 32 a thread (to 24 where a stream is fp32),
+    // which leaves less to do per element, two rows in turn, the second's inputs on their way during the first, and of these
+    // the most that leaves the fewest threads without work.  us: 65536 x 1024, RMS norm of a sum, 8 elements 97, 16 a thread 84, 32
+    // 83, 32 and two rows 80, four rows 81 (80 at the rate of a copy); 32768 x 1536, both norms and a gate, 8 elements 121, 16 108, 24
+    // 101, 32 (a quarter of the threads idle) 118, with an fp32 stream 126, 118, 107; 32768 x 768 58, 54, 47, 56 and 61, 70, 54.
+    // Border: 400 x 1536 8 elements 3.5, 24 4.1; 1000 x 768 4.2 and 3.9, 1000 x 1536 6.2 and 5.1; 128 x 1024 8 elements 2.1, 16 2.4.
     const int vecs = p.Dm / 8;
-    int V = p.T <= 2 * sms ? 1 : p.x_f32 || p.res_f32 ? 2 : 4;
-    while (V > 1 && vecs <= V * 4) V /= 2;
-    while ((vecs + V - 1) / V > kMaxRowThreads) V *= 2;
-    int lanes = (vecs + V - 1) / V;   // threads of a row: a power of two in a warp, or whole warps
-    if (lanes > 32) {
-        lanes = (lanes + 31) / 32 * 32;
-    } else {
-        int n = 8;
-        while (n < lanes) n *= 2;
-        lanes = n;
-    }
+    const auto lanes_of = [&](int v) {   // threads of a row: a power of two in a warp, or whole warps
+        const int n = (vecs + v - 1) / v;
+        return n > 32 ? (n + 31) / 32 * 32 : n > 16 ? 32 : n > 8 ? 16 : 8;
+    };
+    int V = p.T <= 2 * sms || (int64_t)p.T * vecs <= 600LL * sms ? 1 : p.x_f32 || p.res_f32 ? 3 : 4;
+    for (int v = V - 1; v > 0; --v)
+        if (v * lanes_of(v) < V * lanes_of(V)) V = v;
+    if (lanes_of(V) > kMaxRowThreads) V = lanes_of(2) > kMaxRowThreads ? 4 : 2;
+    const int lanes = lanes_of(V);
     const int threads = lanes <= 32 ? 128 : lanes, per_cta = threads / lanes;
     const int rounds = (int64_t)p.T / per_cta >= 32LL * sms ? 2 : 1;
     const bool full = V * lanes == vecs, xf = p.x_f32, rf = p.res_f32;
     const auto kernel = V == 1 ? (full ? kernel_of<1, true>(xf, rf) : kernel_of<1, false>(xf, rf))
                         : V == 2 ? (full ? kernel_of<2, true>(xf, rf) : kernel_of<2, false>(xf, rf))
+                        : V == 3 ? (full ? kernel_of<3, true>(xf, rf) : kernel_of<3, false>(xf, rf))
                                  : (full ? kernel_of<4, true>(xf, rf) : kernel_of<4, false>(xf, rf));
     const int64_t rows = (int64_t)per_cta * rounds;
     return launch_kernel(kernel, dim3((unsigned)((p.T + rows - 1) / rows)), dim3((unsigned)threads), 0, stream, 1, p, lanes, rounds);

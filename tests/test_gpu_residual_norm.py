@@ -62,6 +62,15 @@ def test_widths(api, D, T):
     check(api, T, D, pre="rms", post="layer", gate="channel", x_dtype=F32, h_dtype=F32, y_dtype=F32, seed=D)
 
 
+@pytest.mark.parametrize("D", [8, 24, 40, 64, 104, 192, 384, 504, 768, 1000, 1152, 1280, 1536, 2304, 2560, 4608, 8192, 12288, 16384])
+@pytest.mark.parametrize("x_dtype,h_dtype", [(BF16, BF16), (BF16, F32), (F32, BF16)])
+def test_widths_of_many_rows(api, D, x_dtype, h_dtype):
+    # rows of several elements a thread, one after the other or two in turn
+    check(api, 1201, D, x_dtype, h_dtype, BF16, "layer", "rms", "token", 0.5, seed=D)
+    if D <= 1536:
+        check(api, 20011, D, x_dtype, h_dtype, F32, "rms", None, "channel", 1.0, seed=D)
+
+
 @pytest.mark.parametrize("T", [1, 2, 5, 16, 127, 128, 129, 1000, 5001])
 @pytest.mark.parametrize("D", [64, 1024, 2048])
 def test_token_counts(api, T, D):
