@@ -575,7 +575,7 @@ typedef struct dr_linear_out {
  *              below 2^30
  *   outs     : n_outs (1 .. DR_LINEAR_MAX_OUTS) outputs, read on the host during the call; a residual takes a single
  *              one.  16-byte aligned pointers and strides make them faster, and so for the residual.  Outputs overlap
- *              neither each other nor x, W and bias
+ *              neither each other nor x, W and bias (DR_ERR_INVALID_ARG where one starts in the place of another)
  *   err_flag : nullable device int32; DR_ERRF_TIMEOUT if a CTA's bounded pipeline wait gave up (its outputs are then
  *              not written)
  * Same inputs, sizes and device give the same bits from call to call.
