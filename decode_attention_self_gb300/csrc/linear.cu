@@ -44,7 +44,7 @@ enum class Way { kRows, kCluster, kTiles };
 // 1536 3.6 and 4.4, 1024 -> 4096 4.6 and 5.6, 4096 -> 1024 7.0 and 6.3, 1536 -> 6144 10.0 and 7.8, 8192 -> 8192 44 and 28.
 // Cluster or tiles: the pairs that stay take what is more than one wave of tiles of 128 tokens by 64 weight rows and, with bf16
 // outputs, of pairs' tiles of 256 by 128.  1024 tokens 4096 -> 1024 (128 of 128 by 64) 12.6 and 18, 256 tokens 1024 -> 4096 (128) 6.7 and
-// 8.3; 512 tokens 1024 -> 4096 (64 of 256 by 128) 8.0 and 9.7, 2048 tokens 4096 -> 1024 (64) 15.4 and 19.3, 700 tokens 1024 -> 4096 (96)
+// 8.3; 512 tokens 1024 -> 4096 (64 of 256 by 128) 7.9 and 9.7, 2048 tokens 4096 -> 1024 (64) 14.9 and 19.3, 700 tokens 1024 -> 4096 (96)
 // 13.6 and 10.9; fp32 with a residual 1024 tokens 1024 -> 2048 (64) 10.6 and 9.7.  So do fp32 outputs of a K too long for the other
 // kernel's short sums.
 Way way_of(const LinearParams &p, int sms) {

@@ -12,7 +12,7 @@
 // Where the tiles of 64 rows would be more than a wave, but those of 256 tokens by 128 rows are not, two CTAs (a cluster) multiply
 // such a tile with two-CTA products (kPair): each loads and keeps 128 of the tokens and 64 of the weight rows, which halves what comes
 // from L2 per product; the first CTA issues (two warps: a product is four times as long).  512 tokens 1024 -> 4096 with gelu 9.7 us
-// by the pairs that stay, 8.0 here: set-up and epilogue of a single tile are what this kernel is short of.
+// by the pairs that stay, 7.9 here: set-up and epilogue of a single tile are what this kernel is short of.
 // (One warp takes some 400 cycles to issue a chunk's four products, wait and commit, and 310 to issue its copies, whatever
 // their size: with one of each, 128 tokens of 1024 -> 4096 took 8700 cycles for 16 chunks, with two 5300.)
 // The kernel runs once through its code, so there is little of it: 16 columns of a token at a time, from tensor memory to the
@@ -245,6 +245,12 @@ __global__ void __launch_bounds__(kMaxThreads)
         __syncwarp();
     }
     __syncthreads();
+    const int row = (warp & 3) * 32 + lane;   // whose sums this thread reads
+    const int col0 = (warp >> 2) * 16, cols = blockDim.x / 128 * 16;   // this warp's columns: the first, and to the next
+    const bool boxed = p.vec_out && (!p.residual || p.vec_res);   // rows of whole 16-byte pieces
+    const bool direct = S == 1 && boxed;                          // from tensor memory to the outputs
+    lin::Columns<kF32, 16> res;   // on its way during the last products
+    if (direct && row < rows && col0 < bn) lin::load_residual(p, t0 + row, n0 + col0, res);
     bool ok = tc::mbar_wait(&done, 0, &gave_up);
     if (gave_up) {
         // copies in flight end by themselves; wait for them before this CTA's shared memory goes away
@@ -260,7 +266,6 @@ __global__ void __launch_bounds__(kMaxThreads)
     tc::fence_after();
 
     const int nb = pl.nb;
-    const int row = (warp & 3) * 32 + lane;   // whose sums this thread reads
     const uint32_t from = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const auto sums = [&](int c, float (&v)[16]) {   // columns c .. c+15 of the row, all pieces of K
         tc::ld16(from + c, v);
@@ -283,9 +288,6 @@ __global__ void __launch_bounds__(kMaxThreads)
         tc::wait_ld();
         tc::pin16(v);
     };
-    const int col0 = (warp >> 2) * 16, cols = blockDim.x / 128 * 16;   // this warp's columns: the first, and to the next
-    const bool boxed = p.vec_out && (!p.residual || p.vec_res);   // rows of whole 16-byte pieces
-    const bool direct = S == 1 && boxed;                          // from tensor memory to the outputs
     if (ok && (warp & 3) * 32 < rows) {
         if (direct) {
 #pragma unroll 1
@@ -293,7 +295,10 @@ __global__ void __launch_bounds__(kMaxThreads)
                 float a[16], b[16];
                 sums(c, a);
                 if (p.gated) sums(bn + c, b);
-                if (row < rows) lin::finish<kF32, 16>(p, bias + c, bias + bn + c, t0 + row, n0 + c, a, b);
+                if (row < rows) {
+                    lin::finish(p, bias + c, bias + bn + c, t0 + row, n0 + c, a, b, res);
+                    if (c + cols < bn) lin::load_residual(p, t0 + row, n0 + c + cols, res);
+                }
             }
         } else {
             // To shared memory, [row][nb] fp32 in 16-byte pieces that the row turns, so that a warp's stores spread over the
@@ -337,12 +342,14 @@ __global__ void __launch_bounds__(kMaxThreads)
         return s == rank ? reinterpret_cast<const float *>(staged) + (rank * share + r) * nb
                          : reinterpret_cast<const float *>(received) + ((s - (s > rank)) * mine + r) * nb;
     };
-    if (ok && boxed && !direct) {   // four columns a thread
+    if (ok && boxed && !direct) {   // four columns a thread (their residual loaded before the wait for the parts: no gain)
         const int shift = 29 - __clz(bn);   // bn is a power of two
 #pragma unroll 1
         for (int i = threadIdx.x; i < mine << shift; i += blockDim.x) {
             const int r = i >> shift, g = i - (r << shift), key = (rank * share + r) & 7;
             float a[4] = {0.f, 0.f, 0.f, 0.f}, b[4] = {0.f, 0.f, 0.f, 0.f};
+            lin::Columns<kF32, 4> own;
+            lin::load_residual(p, t0 + rank * share + r, n0 + g * 4, own);
 #pragma unroll 1
             for (int s = 0; s < S; ++s) {
                 const float4 *from = reinterpret_cast<const float4 *>(part(s, r));
@@ -353,10 +360,10 @@ __global__ void __launch_bounds__(kMaxThreads)
                     b[0] += u.x; b[1] += u.y; b[2] += u.z; b[3] += u.w;
                 }
             }
-            lin::finish<kF32, 4>(p, bias + g * 4, bias + bn + g * 4, t0 + rank * share + r, n0 + g * 4, a, b);
+            lin::finish(p, bias + g * 4, bias + bn + g * 4, t0 + rank * share + r, n0 + g * 4, a, b, own);
         }
     } else if (ok && !boxed) {   // a column of eight rows a thread: a warp's accesses lie side by side
-        const int shift = 31 - __clz(bn);   // bn is a power of two
+        const int shift = 31 - __clz(bn);
 #pragma unroll 1
         for (int i = threadIdx.x; i < (mine + 7) / 8 * bn; i += blockDim.x) {
             const int c = i & (bn - 1), r0 = (i >> shift) * 8, have = min(8, mine - r0);

@@ -120,29 +120,35 @@ __device__ __forceinline__ void add_bias(float *v, const float *bias) {   // bia
     }
 }
 
+// kN columns of a row as they lie in memory.
+template <bool kF32, int kN>
+union Columns {
+    static constexpr int kWords = kF32 ? kN : kN / 2;   // of 32 bits
+    using Piece = typename std::conditional<kWords % 4 == 0, uint4, uint2>::type;
+    static constexpr int kPieces = kWords * 4 / (int)sizeof(Piece);
+    Piece piece[kPieces];
+    uint32_t w[kWords];
+};
+// The residual of columns n .. n + kN - 1 of token t, where there is one and N has so many; finish() looks at no other.
+template <bool kF32, int kN>
+__device__ __forceinline__ void load_residual(const LinearParams &p, int t, int n, Columns<kF32, kN> &r) {
+    using C = Columns<kF32, kN>;
+    if (!p.residual || p.N - n < kN) return;
+    const typename C::Piece *from = reinterpret_cast<const typename C::Piece *>(
+        static_cast<const uint8_t *>(p.residual) + ((int64_t)t * p.res_stride + n) * (kF32 ? 4 : 2));
+#pragma unroll
+    for (int i = 0; i < C::kPieces; ++i) r.piece[i] = from[i];
+}
+
 // kN columns n .. n + kN - 1 (4 or 16, n a multiple of it) of token t: bias (of these columns, fp32), activation, gating and
-// residual on the sums a (and b, the sums of the rows that are multiplied in), stored to the output that holds them.  Columns
-// from N on are left out.
+// residual (r, loaded before) on the sums a (and b, the sums of the rows that are multiplied in), stored to the output that holds
+// them.  Columns from N on are left out.
 template <bool kF32, int kN>
 __device__ __forceinline__ void finish(const LinearParams &p, const float *bias_a, const float *bias_b, int t, int n, float (&a)[kN],
-                                       float (&b)[kN]) {
-    constexpr int kWords = kF32 ? kN : kN / 2;   // 32-bit words of the columns
-    using Piece = typename std::conditional<kWords % 4 == 0, uint4, uint2>::type;
-    constexpr int kPieces = kWords * 4 / (int)sizeof(Piece);
-    union Words {
-        Piece piece[kPieces];
-        uint32_t w[kWords];
-    };
+                                       float (&b)[kN], const Columns<kF32, kN> &r) {
+    using C = Columns<kF32, kN>;
     const int have = p.N - n;
     if (have <= 0) return;
-    Words r;
-    const bool quick_res = p.residual && have >= kN;
-    const int64_t res_at = (int64_t)t * p.res_stride + n;
-    if (quick_res) {   // on its way during the arithmetic
-        const Piece *from = reinterpret_cast<const Piece *>(static_cast<const uint8_t *>(p.residual) + res_at * (kF32 ? 4 : 2));
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i) r.piece[i] = from[i];
-    }
     if (p.bias) {
         add_bias<kN>(a, bias_a);
         if (p.gated) add_bias<kN>(b, bias_b);
@@ -152,9 +158,9 @@ __device__ __forceinline__ void finish(const LinearParams &p, const float *bias_
 #pragma unroll
         for (int i = 0; i < kN; ++i) a[i] *= b[i];
     }
-    if (quick_res) {
+    if (p.residual && have >= kN) {
 #pragma unroll
-        for (int i = 0; i < kWords; ++i) {
+        for (int i = 0; i < C::kWords; ++i) {
             if constexpr (kF32) {
                 a[i] += __uint_as_float(r.w[i]);
             } else {
@@ -163,6 +169,7 @@ __device__ __forceinline__ void finish(const LinearParams &p, const float *bias_
             }
         }
     } else if (p.residual) {
+        const int64_t res_at = (int64_t)t * p.res_stride + n;
 #pragma unroll
         for (int i = 0; i < kN; ++i)
             if (i < have) {
@@ -173,15 +180,15 @@ __device__ __forceinline__ void finish(const LinearParams &p, const float *bias_
     const LinearOut o = output_of(p, n);
     const int64_t at = (int64_t)t * o.stride + (n - o.col0);
     if (have >= kN) {
-        Words y;
+        C y;
 #pragma unroll
-        for (int i = 0; i < kWords; ++i) {
+        for (int i = 0; i < C::kWords; ++i) {
             if constexpr (kF32) y.w[i] = __float_as_uint(a[i]);
             else y.w[i] = pack2(a[2 * i], a[2 * i + 1]);
         }
-        Piece *to = reinterpret_cast<Piece *>(static_cast<uint8_t *>(o.ptr) + at * (kF32 ? 4 : 2));
+        typename C::Piece *to = reinterpret_cast<typename C::Piece *>(static_cast<uint8_t *>(o.ptr) + at * (kF32 ? 4 : 2));
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) to[i] = y.piece[i];
+        for (int i = 0; i < C::kPieces; ++i) to[i] = y.piece[i];
     } else {
 #pragma unroll
         for (int i = 0; i < kN; ++i)
