@@ -45,8 +45,8 @@ enum class Way { kRows, kCluster, kTiles };
 // Cluster or tiles: the pairs that stay take what is more than one wave of tiles of 128 tokens by 64 weight rows and, with bf16
 // outputs, of pairs' tiles of 256 by 128.  1024 tokens 4096 -> 1024 (128 of 128 by 64) 12.6 and 18, 256 tokens 1024 -> 4096 (128) 6.7 and
 // 8.3; 512 tokens 1024 -> 4096 (64 of 256 by 128) 7.9 and 9.7, 2048 tokens 4096 -> 1024 (64) 14.9 and 19.3, 700 tokens 1024 -> 4096 (96)
-// 13.6 and 10.9; fp32 with a residual 1024 tokens 1024 -> 2048 (64) 10.6 and 9.7.  So do fp32 outputs of a K too long for the other
-// kernel's short sums.
+// 13.6 and 10.9; fp32 outputs, to pairs' tiles: 1024 tokens 1024 -> 1536 (48) with a residual 10.9 and 9.3, without one 9.5 and 9.1, 2048
+// tokens 1024 -> 1024 (64) 9.8 and 9.6, 8.0 and 9.1.  So do fp32 outputs of a K too long for the other kernel's short sums.
 Way way_of(const LinearParams &p, int sms) {
     const int64_t rows = (int64_t)p.N * (p.gated ? 2 : 1);
     if (p.T <= 16 || (p.T <= 32 && rows * p.K <= 6 << 20)) return Way::kRows;
