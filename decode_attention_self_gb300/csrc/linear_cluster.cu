@@ -299,6 +299,7 @@ __global__ void __launch_bounds__(kMaxThreads)
                     lin::finish(p, bias + c, bias + bn + c, t0 + row, n0 + c, a, b, res);
                     if (c + cols < bn) lin::load_residual(p, t0 + row, n0 + c + cols, res);
                 }
+                __syncwarp();   // whole again: the next sums' instructions want all lanes at once
             }
         } else {
             // To shared memory, [row][nb] fp32 in 16-byte pieces that the row turns, so that a warp's stores spread over the
@@ -311,10 +312,12 @@ __global__ void __launch_bounds__(kMaxThreads)
                 if (row < rows)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) to[(c / 4 + j) ^ (row & 7)] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                __syncwarp();
             }
         }
     }
     tc::fence_before();
+    __syncwarp();
     if (S > 1) {
         tc::fence_proxy_async();
         cluster_wait();   // every CTA of the cluster has set its barrier up
@@ -384,6 +387,7 @@ __global__ void __launch_bounds__(kMaxThreads)
             lin::finish_column8<kF32>(p, bias[c], bias[p.gated ? bn + c : c], t0 + rank * share + r0, have, n0 + c, a, b);
         }
     }
+    __syncwarp();   // the lanes of a warp had different numbers of pieces
     if (kPair || S > 1) cluster_wait();
     if (kPair && warp == 2) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(pl.cols));
 }

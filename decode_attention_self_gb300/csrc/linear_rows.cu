@@ -95,6 +95,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) linear_rows_kernel(const __gri
             for (int i = 0; i < kBlocks; ++i) now[u][i] = wv[u][i];
         }
         if (s0 + kSteps * warps < steps) load_w(s0 + kSteps * warps);
+        __syncwarp();   // lanes past K or the last row loaded nothing; the products want all of them at once
         float part[kTiles][kBlocks][4] = {};
 #pragma unroll
         for (int u = 0; u < kSteps; ++u)

@@ -412,6 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::fence_before();
             __syncwarp();
             if (lane == 0) remote_arrive(tc::mapa(tc::smem_u32(&ctl.sums_free[chain & 1]), 0));
+            __syncwarp();
             chain += shared ? 1 : 2;
         };
         for (int i = share.first; share.active && ok && i < tiles; i += share.step) {
@@ -481,6 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (closes) {
                     __syncwarp();
                     if (lane == 0) tc::mbar_arrive(&ctl.boxes_full[set]);
+                    __syncwarp();   // whole again: tensor-memory instructions want all lanes at once
                 }
                 return true;
             };
