@@ -163,15 +163,65 @@ __device__ __forceinline__ void ld32(uint32_t taddr, T *r) {
         : DR_TC_R8(q, 0), DR_TC_R8(q, 8), DR_TC_R8(q, 16), DR_TC_R8(q, 24)
         : "r"(taddr));
 }
-// 16 columns
+// Loads that are waited for in the same statement.  To the compiler the outputs of a statement are there when it ends, so it may
+// copy or spill them at once, most of all where they cross a loop's edge: registers of a load that is waited for later hold
+// nothing yet.
+#define DR_TC_E8(r, o) "=&r"(r[o]), "=&r"(r[o + 1]), "=&r"(r[o + 2]), "=&r"(r[o + 3]), "=&r"(r[o + 4]), "=&r"(r[o + 5]), \
+                       "=&r"(r[o + 6]), "=&r"(r[o + 7])   // written before the statement's inputs were all read
 template <typename T>
-__device__ __forceinline__ void ld16(uint32_t taddr, T *r) {
+__device__ __forceinline__ void ld16_wait(uint32_t taddr, T *r) {
     uint32_t *q = reinterpret_cast<uint32_t *>(r);
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
-        "[%16];"
-        : DR_TC_R8(q, 0), DR_TC_R8(q, 8)
-        : "r"(taddr));
+        "{\n"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];\n"
+        " tcgen05.wait::ld.sync.aligned;\n}"
+        : DR_TC_E8(q, 0), DR_TC_E8(q, 8)
+        : "r"(taddr)
+        : "memory");
+}
+// The same of two places, one latency for both.
+template <typename T>
+__device__ __forceinline__ void ld16x2_wait(uint32_t at, T *r, uint32_t at2, T *r2) {
+    uint32_t *q = reinterpret_cast<uint32_t *>(r), *q2 = reinterpret_cast<uint32_t *>(r2);
+    asm volatile(
+        "{\n"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%32];\n"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, "
+        "%29, %30, %31}, [%33];\n"
+        " tcgen05.wait::ld.sync.aligned;\n}"
+        : DR_TC_E8(q, 0), DR_TC_E8(q, 8), DR_TC_E8(q2, 0), DR_TC_E8(q2, 8)
+        : "r"(at), "r"(at2)
+        : "memory");
+}
+template <typename T>
+__device__ __forceinline__ void ld32_wait(uint32_t taddr, T *r) {
+    uint32_t *q = reinterpret_cast<uint32_t *>(r);
+    asm volatile(
+        "{\n"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
+        " tcgen05.wait::ld.sync.aligned;\n}"
+        : DR_TC_E8(q, 0), DR_TC_E8(q, 8), DR_TC_E8(q, 16), DR_TC_E8(q, 24)
+        : "r"(taddr)
+        : "memory");
+}
+// The same of two places, one latency for both.
+template <typename T>
+__device__ __forceinline__ void ld32x2_wait(uint32_t at, T *r, uint32_t at2, T *r2) {
+    uint32_t *q = reinterpret_cast<uint32_t *>(r), *q2 = reinterpret_cast<uint32_t *>(r2);
+    asm volatile(
+        "{\n"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%64];\n"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, "
+        "%45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%65];\n"
+        " tcgen05.wait::ld.sync.aligned;\n}"
+        : DR_TC_E8(q, 0), DR_TC_E8(q, 8), DR_TC_E8(q, 16), DR_TC_E8(q, 24), DR_TC_E8(q2, 0), DR_TC_E8(q2, 8),
+          DR_TC_E8(q2, 16), DR_TC_E8(q2, 24)
+        : "r"(at), "r"(at2)
+        : "memory");
 }
 __device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 // Ties 32 registers to this point of the program: what reads them afterwards cannot move above a wait_ld before it.
@@ -182,11 +232,6 @@ __device__ __forceinline__ void pin32(T *r) {
     uint32_t *q = reinterpret_cast<uint32_t *>(r);
     asm volatile("" : DR_TC_P8(q, 0), DR_TC_P8(q, 8));
     asm volatile("" : DR_TC_P8(q, 16), DR_TC_P8(q, 24));
-}
-template <typename T>
-__device__ __forceinline__ void pin16(T *r) {
-    uint32_t *q = reinterpret_cast<uint32_t *>(r);
-    asm volatile("" : DR_TC_P8(q, 0), DR_TC_P8(q, 8));
 }
 template <typename T>
 __device__ __forceinline__ void st32(uint32_t taddr, const T *r) {

@@ -268,25 +268,17 @@ __global__ void __launch_bounds__(kMaxThreads)
     const int nb = pl.nb;
     const uint32_t from = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const auto sums = [&](int c, float (&v)[16]) {   // columns c .. c+15 of the row, all pieces of K
-        tc::ld16(from + c, v);
+        tc::ld16_wait(from + c, v);
 #pragma unroll 1
-        for (int i = 1; i < pieces; i += 2) {
+        for (int i = 1; i < pieces; i += 2) {   // two at a time
             float one[16], two[16];
-            tc::ld16(from + i * nb + c, one);
-            if (i + 1 < pieces) tc::ld16(from + (i + 1) * nb + c, two);
-            tc::wait_ld();
-            tc::pin16(v);
-            tc::pin16(one);
+            tc::ld16x2_wait(from + i * nb + c, one, from + min(i + 1, pieces - 1) * nb + c, two);
 #pragma unroll
             for (int j = 0; j < 16; ++j) v[j] += one[j];
-            if (i + 1 < pieces) {
-                tc::pin16(two);
+            if (i + 1 < pieces)
 #pragma unroll
                 for (int j = 0; j < 16; ++j) v[j] += two[j];
-            }
         }
-        tc::wait_ld();
-        tc::pin16(v);
     };
     if (ok && (warp & 3) * 32 < rows) {
         if (direct) {

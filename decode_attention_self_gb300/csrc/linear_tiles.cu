@@ -424,19 +424,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::fence_after();
                 from = tmem + lanes + (chain & 1) * kTileW + share.col0;
                 if (!kF32 || k == 0) {
-                    tc::ld32(from, acc);
-                    if (two) tc::ld32(from + apart, acc + 32);
-                    tc::wait_ld();
-                    tc::pin32(acc);
-                    tc::pin32(acc + 32);
+                    if (two) tc::ld32x2_wait(from, acc, from + apart, acc + 32);
+                    else tc::ld32_wait(from, acc);
                 } else {
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         if (q >= 2 && !two) break;
                         float more[16];
-                        tc::ld16(from + (q < 2 ? 0 : apart) + (q & 1) * 16, more);
-                        tc::wait_ld();
-                        tc::pin16(more);
+                        tc::ld16_wait(from + (q < 2 ? 0 : apart) + (q & 1) * 16, more);
 #pragma unroll
                         for (int j = 0; j < 16; ++j) acc[16 * q + j] += more[j];
                     }
@@ -486,36 +481,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 return true;
             };
-            // Blocks in turn in either half of the registers; while one is worked on the other's successor is read.
+            // Two blocks at a time, one in either half of the registers (gated: one, and what multiplies it).
 #pragma unroll 1
             for (int k = 0;;) {
                 ok = block(acc, acc + 32, k);
-                if (!ok || k + 1 == share.blocks) break;
-                if (p.gated) {   // (two blocks of its set's share)
-                    tc::ld32(from + 32, acc);
-                    tc::ld32(from + 32 + apart, acc + 32);
-                    tc::wait_ld();
-                    tc::pin32(acc);
-                    tc::pin32(acc + 32);
-                    release();
-                    ++k;
-                    continue;
-                }
-                if (!shared) {
-                    if (k == 0) {
-                        tc::ld32(from + 64, acc);
-                    } else {
-                        tc::wait_ld();
-                        tc::pin32(acc + 32);
-                        release();
-                    }
-                }
-                ok = block(acc + 32, acc, k + 1);
-                k += 2;
-                if (!ok || k == share.blocks) break;
-                tc::wait_ld();
-                tc::pin32(acc);
-                tc::ld32(from + 96, acc + 32);
+                if (ok && !p.gated && share.blocks > 1) ok = block(acc + 32, acc, k + 1);
+                k += p.gated ? 1 : 2;
+                if (!ok || shared || k >= share.blocks) break;   // (a shared tile's warps have their two at once)
+                from += p.gated ? 32 : 64;   // the rest of the set's share
+                tc::ld32x2_wait(from, acc, from + apart, acc + 32);
+                release();
             }
         }
     }
