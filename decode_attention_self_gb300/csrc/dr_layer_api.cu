@@ -6,9 +6,10 @@
 
 namespace {
 
-// The kernels look a tile past the last token and a group of steps past the last k in 32-bit numbers; tensor maps take
-// strides below 2^40 bytes.
-constexpr int kMaxTokens = 0x7FFFF000, kMaxK = 1 << 30;
+// The kernels look a tile past the last token in 32-bit numbers; tensor maps take strides below 2^40 bytes.  K: a bounded wait
+// (2^32 cycles) spans the products of up to two tiles, at 2^24 so 2^19 chunks of 64, of 300 to 520 cycles from L2 (1400 where
+// every operand comes from memory): a sixth of the limit.
+constexpr int kMaxTokens = 0x7FFFF000, kMaxK = 1 << 24;
 constexpr int64_t kMaxStride = 1LL << 37;
 
 bool aligned(const void *p, int bytes) { return reinterpret_cast<uintptr_t>(p) % (uintptr_t)bytes == 0; }

@@ -571,7 +571,7 @@ typedef struct dr_linear_out {
  *   x        : [T][K] bf16 (device, 16-byte aligned), tokens x_stride elements apart (a multiple of 8, >= K)
  *   W        : [N][K] bf16, [2N][K] when gated (device, 16-byte aligned)
  *   opts     : nullable (no bias, activation or residual)
- *   T        : 1 .. 2^31 - 4096;  K : a multiple of 8, at most 2^30;  N : the columns of all outputs together, any number
+ *   T        : 1 .. 2^31 - 4096;  K : a multiple of 8, at most 2^24;  N : the columns of all outputs together, any number
  *              below 2^30
  *   outs     : n_outs (1 .. DR_LINEAR_MAX_OUTS) outputs, read on the host during the call; a residual takes a single
  *              one.  16-byte aligned pointers and strides make them faster, and so for the residual.  Outputs overlap
