@@ -27,7 +27,7 @@ struct LinearParams {
     int32_t T, K, N;          // N: output columns
     int32_t act, gated;
     int32_t out_f32;
-    int32_t vec_out, vec_res; // rows of the outputs (the residual) start on 32 bytes (2), on 16 (1) or anywhere (0)
+    int32_t vec_out, vec_res; // 1: rows of all outputs (there is a residual, and its rows) start on 16 bytes
     int32_t *err;
     int32_t stall_tile = -1;  // test hook: the CTAs of this output tile never load their first K chunk
 };

@@ -14,10 +14,7 @@ constexpr int64_t kMaxStride = 1LL << 37;
 
 bool aligned(const void *p, int bytes) { return reinterpret_cast<uintptr_t>(p) % (uintptr_t)bytes == 0; }
 
-// Whether rows start on 32 bytes (2), on 16 (1) or anywhere (0).
-int row_alignment(const void *p, int64_t stride_bytes) {
-    return aligned(p, 32) && stride_bytes % 32 == 0 ? 2 : aligned(p, 16) && stride_bytes % 16 == 0 ? 1 : 0;
-}
+bool aligned_rows(const void *p, int64_t stride_bytes) { return aligned(p, 16) && stride_bytes % 16 == 0; }
 
 dr_status from_cuda(cudaError_t e) { return e == cudaSuccess ? DR_OK : DR_ERR_CUDA; }
 
@@ -52,7 +49,7 @@ dr_status linear_call(const void *x, int64_t x_stride, const void *W, const dr_l
             return DR_ERR_INVALID_ARG;
     }
     if (N > 0x3FFFFFFF) return DR_ERR_INVALID_ARG;   // weight rows are counted in 32 bits
-    p.vec_out = 2;
+    p.vec_out = 1;
     int64_t at = 0;
     for (int i = 0; i < n_outs; ++i) {
         const dr_linear_out &o = outs[i];
@@ -61,7 +58,7 @@ dr_status linear_call(const void *x, int64_t x_stride, const void *W, const dr_l
         for (int j = 0; j < i; ++j)
             if (outs[j].ptr == o.ptr) return DR_ERR_INVALID_ARG;
         if (i + 1 < n_outs && o.cols % 64 != 0) return DR_ERR_INVALID_ARG;
-        p.vec_out = min(p.vec_out, row_alignment(o.ptr, o.stride * e));
+        if (!aligned_rows(o.ptr, o.stride * e)) p.vec_out = 0;
         if (at + o.cols > N) return DR_ERR_INVALID_ARG;
         p.out[i].ptr = o.ptr;
         p.out[i].stride = o.stride;
@@ -71,7 +68,7 @@ dr_status linear_call(const void *x, int64_t x_stride, const void *W, const dr_l
     }
     if (at != N) return DR_ERR_INVALID_ARG;
     for (int i = n_outs; i < DR_LINEAR_MAX_OUTS; ++i) p.out[i] = p.out[0];
-    p.vec_res = p.residual ? row_alignment(p.residual, p.res_stride * e) : 0;
+    p.vec_res = p.residual && aligned_rows(p.residual, p.res_stride * e);
     p.x = static_cast<const uint16_t *>(x);
     p.x_stride = x_stride;
     p.W = static_cast<const uint16_t *>(W);
