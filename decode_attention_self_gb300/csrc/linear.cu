@@ -41,12 +41,16 @@ enum class Way { kRows, kCluster, kTiles };
 
 // Which kernel takes a call; measured on both sides of each border, us.
 // Rows or cluster: 16 tokens 8192 -> 8192 24.6 and 27.8, 4096 -> 1024 5.2 and 6.2; 32 tokens, where a CTA's tokens weigh more, 1024 ->
-// 1536 3.6 and 4.4, 1024 -> 4096 4.6 and 5.6, 4096 -> 1024 7.0 and 6.3, 1536 -> 6144 10.0 and 7.8, 8192 -> 8192 44 and 28.
+// 1536 3.6 and 4.4, 1024 -> 4096 4.6 and 5.6, 4096 -> 1024 7.0 and 6.3, 1536 -> 6144 10.0 and 7.8, 8192 -> 8192 44 and 28.  (The rule
+// looks at the weights' size alone and takes 4096 -> 1024 to the rows too.)
 // Cluster or tiles: the pairs that stay take what is more than one wave of tiles of 128 tokens by 64 weight rows and, with bf16
 // outputs, of pairs' tiles of 256 by 128.  1024 tokens 4096 -> 1024 (128 of 128 by 64) 12.6 and 18, 256 tokens 1024 -> 4096 (128) 6.7 and
 // 8.3; 512 tokens 1024 -> 4096 (64 of 256 by 128) 7.9 and 9.7, 2048 tokens 4096 -> 1024 (64) 14.9 and 19.3, 700 tokens 1024 -> 4096 (96)
 // 13.6 and 10.9; fp32 outputs, to pairs' tiles: 1024 tokens 1024 -> 1536 (48) with a residual 10.9 and 9.3, without one 9.5 and 9.1, 2048
-// tokens 1024 -> 1024 (64) 9.8 and 9.6, 8.0 and 9.1.  So do fp32 outputs of a K too long for the other kernel's short sums.
+// tokens 1024 -> 1024 (64) 9.8 and 9.6, 8.0 and 9.1.  (The rule does not look at the residual: what has none loses up to a tenth by it.)
+// So do fp32 outputs of a K too long for the other kernel's short sums, and 17 to 128 tokens of more weight rows than a wave of 64 each
+// takes (9728 on 152 SMs): tiles of 256 tokens are mostly empty there, and 9792 rows, 77 tiles of 128 for 76 pairs, go as 39 tiles of 256
+// (64 tokens 1024 -> 9728 6.7 on this side, -> 9792 10.4 on the other).
 Way way_of(const LinearParams &p, int sms) {
     const int64_t rows = (int64_t)p.N * (p.gated ? 2 : 1);
     if (p.T <= 16 || (p.T <= 32 && rows * p.K <= 6 << 20)) return Way::kRows;

@@ -16,8 +16,8 @@
 // (One warp takes some 400 cycles to issue a chunk's four products, wait and commit, and 310 to issue its copies, whatever
 // their size: with one of each, 128 tokens of 1024 -> 4096 took 8700 cycles for 16 chunks, with two 5300.)
 // The kernel runs once through its code, so there is little of it: 16 columns of a token at a time, from tensor memory to the
-// outputs.  (By way of shared memory, with a warp's stores side by side, 256 tokens 1024 -> 4096 took 7.7 us, now 6.8.)  A pass
-// costs some 1300 cycles, 2000 with gelu, of which little is arithmetic: two warps per scheduler cannot hide its latencies, so
+// outputs.  (By way of shared memory, with a warp's stores side by side, 256 tokens 1024 -> 4096 took 7.7 us, 6.8 at that step.)  A
+// pass costs some 1400 cycles, 2400 with gelu, of which little is arithmetic: two warps per scheduler cannot hide its latencies, so
 // tiles of 64 and 128 rows have 16 warps.
 // Tensor-core sums are cut off, not rounded: each addition may lose the last bit towards zero, so a chain over K drifts by about
 // 1e-9 K (measured: 1.0e-6 at K = 1024, 2.1e-6 at 2048).  fp32 outputs therefore break the chain every 512 of K into
@@ -384,9 +384,10 @@ __global__ void __launch_bounds__(kMaxThreads)
     if (kPair && warp == 2) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(pl.cols));
 }
 
-// Tiles and split of a call.  Measured with one wave of tiles of 32 against 64 rows of W, us: 128 tokens 1024 -> 4096 5.8
-// and 6.9, 4096 -> 1024 (4 CTAs per tile) 6.7 and 8.6; 256 tokens 1024 -> 4096, where tiles of 32 are two waves, 7.8 and 6.8.  Tiles of
-// 64 against pairs, where both are a wave: 512 tokens 1024 -> 2048 6.3 and 6.7, 1024 tokens 4096 -> 1024 12.5 and 13.4.
+// Tiles and split of a call.  Measured with one wave of tiles of 32 against 64 rows of W, us (both sides at the step that made the
+// choice): 128 tokens 1024 -> 4096 5.8 and 6.9, 4096 -> 1024 (4 CTAs per tile) 6.7 and 8.6; 256 tokens 1024 -> 4096, where tiles of 32 are
+// two waves, 7.8 and 6.8.  Tiles of 64 against pairs, where both are a wave: 512 tokens 1024 -> 2048 6.3 and 6.7, 1024 tokens 4096 -> 1024
+// 12.5 and 13.4.
 // A CTA of a split keeps 4 chunks (or 6, 8, 16, us): 128 tokens 1000 -> 500 5.0 (5.6, 5.6, 7.3), 1024 -> 1024 4.8 (5.0, 5.0, 5.1), 2048 ->
 // 1024 5.6 (5.6, 5.5, 6.0); 64 tokens 1536 -> 1024 4.4 (4.4, 5.0, 5.4).  Eight chunks are not split: 64 tokens 512 -> 512 3.7 whole, 3.9
 // halved.

@@ -19,6 +19,8 @@
 // Outputs or residuals whose rows are not 16-byte aligned are moved by the epilogue warps, a row of 32 columns at a time.
 // fp32 outputs: tensor-core chains drift by about 1e-9 K, so each 512 of K is a tile's sums of its own, added up in the
 // epilogue warps' registers.
+// An epilogue warp reads 64 of its sums at once and waits for them there and then: nothing it reads is in flight while it works
+// (reads that ran ahead of the work were slower, too: 16384 tokens 1024 -> 4096 with gelu, sustained, 101 us, now 95).
 // Every mbarrier wait is bounded; after one that runs out the pair's further tiles are not written, and copies and
 // products in flight are waited for before it exits.
 #include <type_traits>

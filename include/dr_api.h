@@ -566,7 +566,10 @@ typedef struct dr_linear_out {
  * per term of K): with fp32 outputs no such sum is longer than 512 terms, and
  * the sums are added in fp32.  A NaN or infinity in a token, weight row or
  * residual reaches that token's, column's or element's outputs and no others;
- * at a = -inf gelu, gelu_tanh and silu give their limit 0.
+ * at a = -inf gelu, gelu_tanh and silu give their limit 0.  With outputs of
+ * either type activations use the hardware's exponential and reciprocal (2 and
+ * 1 units in the last place), and gelu a fit that is within 1e-6 of the tail
+ * that it leaves of a: together within 5e-7 + 2^-21 |v|.
  *
  *   x        : [T][K] bf16 (device, 16-byte aligned), tokens x_stride elements apart (a multiple of 8, >= K)
  *   W        : [N][K] bf16, [2N][K] when gated (device, 16-byte aligned)
@@ -623,8 +626,9 @@ typedef struct dr_norm {
  * Each part may be left out: post or pre (null: nothing is normed), gate,
  * residual (h is then the rest), h or y (not written).  Statistics and all
  * arithmetic are fp32; layer norm takes its mean first and the squared
- * differences after.  y comes from h before h is rounded to its type.  A NaN
- * or infinity stays in its token.
+ * differences after.  A norm multiplies by its root's reciprocal, rounded: one
+ * rounding more than a division by the root.  y comes from h before h is
+ * rounded to its type.  A NaN or infinity stays in its token.
  *
  *   x        : [T][Dm] in x_dtype, tokens x_stride elements apart
  *   gate     : nullable bf16, [Dm] for all tokens (gate_stride 0) or [T][Dm] (gate_stride >= Dm)
